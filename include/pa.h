@@ -32,9 +32,14 @@
  * Memory layout (this library's choice; the pages fix none):
  *   k_cache, v_cache : [num_blocks][num_kv_heads][block_size][head_dim],
  *                      element type kv_dtype (F16, BF16 or INT8 codes).
- *                      Each (block, kv head) tile is contiguous.
- *   k_scale, v_scale : INT8 only, fp32 [num_blocks][num_kv_heads][block_size]
- *   k_zp, v_zp       : INT8 only, int8 [num_blocks][num_kv_heads][block_size]
+ *                      Each (block, kv head) tile is contiguous. INT4: rows of
+ *                      head_dim / 2 bytes, byte j holding elements 2j (low
+ *                      four bits) and 2j + 1 (high four bits).
+ *   k_scale, v_scale : INT8 only, fp32 [num_blocks][num_kv_heads][block_size];
+ *                      INT4: fp32 [num_blocks][num_kv_heads][block_size]
+ *                      [head_dim / PA_INT4_GROUP]
+ *   k_zp, v_zp       : INT8 only, int8 [num_blocks][num_kv_heads][block_size];
+ *                      INT4: int8, shaped as the scales
  *   slot             : phys_block * block_size + offset (int64); < 0 = skip
  *   block_tables     : int32 [num_seqs][max_blocks_per_seq]; entry b of row s
  *                      is the physical block holding tokens 16b .. 16b+15 of
@@ -69,10 +74,15 @@ typedef enum pa_status {
 /* PA_FP8_E4M3: 8-bit float codes (1 sign, 4 exponent bits with bias 7, 3
  * fraction bits, no infinities, largest finite 448) with one fp32 scale per
  * KV head ([p2] §5.2: FP8 KV cache with per-head scaling factors found on
- * calibration data); the value of a code is E4M3(code) * scale[head]. */
+ * calibration data); the value of a code is E4M3(code) * scale[head].
+ * PA_INT4: unsigned 4-bit codes, two to a byte, with one fp32 scale and one
+ * zero point (0 .. 15, held in an int8) per token, KV head and group of
+ * PA_INT4_GROUP elements; the value of a code is (code - zero_point) * scale.
+ * 74 bytes a row at head_dim 128, against 256 at 16 bits. */
 typedef enum pa_dtype {
-    PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2, PA_INT8 = 3, PA_FP8_E4M3 = 4
+    PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2, PA_INT8 = 3, PA_FP8_E4M3 = 4, PA_INT4 = 5
 } pa_dtype;
+#define PA_INT4_GROUP 64   /* elements of a cached row that share a scale */
 
 /* Message for the last failing call on this thread ("" if none). */
 const char* pa_last_error(void);
@@ -214,8 +224,8 @@ pa_status pa_pool_prefix_groups(pa_pool* pool, const int32_t* seqs, int32_t n,
 
 /* Copy-on-write block copies ([p2] §2.1: copy a shared block only when it
  * is modified). For each i < n_pairs, copies physical block d_pairs[2i] to
- * d_pairs[2i+1] in k_cache and v_cache and, for INT8, in k_scale, v_scale,
- * k_zp, v_zp (pass NULL for those otherwise). d_pairs: device int32
+ * d_pairs[2i+1] in k_cache and v_cache and, for INT8 and INT4, in k_scale,
+ * v_scale, k_zp, v_zp (pass NULL for those otherwise). d_pairs: device int32
  * [n_pairs][2]. Sources and destinations must be distinct blocks, and no
  * destination may also be a source. n_pairs == 0 is a no-op. */
 pa_status pa_copy_blocks(void* k_cache, void* v_cache, void* k_scale,
@@ -239,11 +249,37 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, void* k_scale,
  * fp32 [num_kv_heads] (read only; k_zp, v_zp unused): code =
  * E4M3(x / scale[head]) with the IEEE fp32 quotient rounded to the nearest
  * E4M3 value, ties to even, magnitudes past 448 saturating to +-448.
- * slot_mapping: device int64 [num_tokens]; a negative slot skips the token. */
+ * For kv_dtype INT4 each group of PA_INT4_GROUP elements of a (token, kv head)
+ * row is quantised by the INT8 formula with 16 codes: scale = (mx - mn)/15 (1
+ * if 0), zp = clamp(-rint(mn/scale), 0, 15), code = clamp(rint(x/scale) + zp,
+ * 0, 15), IEEE fp32 division and round-half-to-even. Rows hold finite values
+ * whose range mx - mn is finite in fp32; a group that does not gets codes of
+ * no meaning, other groups are not touched by it.
+ * slot_mapping: device int64 [num_tokens]; a negative slot skips the token.
+ * The slots of one call are distinct. */
 pa_status pa_append_kv(const void* key, const void* value, pa_dtype src_dtype,
                        void* k_cache, void* v_cache, pa_dtype kv_dtype,
                        float* k_scale, float* v_scale, int8_t* k_zp,
                        int8_t* v_zp, const int64_t* slot_mapping,
+                       int32_t num_tokens, int32_t num_blocks,
+                       int32_t num_kv_heads, int32_t head_dim,
+                       int32_t block_size, void* stream);
+
+/* Read cached rows back through a slot mapping, at the values the cache holds:
+ * key, value [num_tokens][num_kv_heads][head_dim] of out_dtype (F16, BF16 or
+ * F32) receive the K and V rows of slot_mapping[t] (any cache type; the value
+ * of a code, one fp32 product, is rounded once more to a 16-bit out_dtype; a
+ * 16-bit cache read as its own type is a bit copy). For attention computed outside the cache that
+ * must see what the cache holds (the queries of a prompt whose K/V were just
+ * quantised), for moving tokens between caches of different types, and for
+ * writing a sequence out. A negative slot leaves its row of key and value as
+ * it was; slots may repeat. key, value and the caches are 16-byte aligned;
+ * scales and zero points as for pa_append_kv. */
+pa_status pa_gather_kv(void* key, void* value, pa_dtype out_dtype,
+                       const void* k_cache, const void* v_cache,
+                       pa_dtype kv_dtype, const float* k_scale,
+                       const float* v_scale, const int8_t* k_zp,
+                       const int8_t* v_zp, const int64_t* slot_mapping,
                        int32_t num_tokens, int32_t num_blocks,
                        int32_t num_kv_heads, int32_t head_dim,
                        int32_t block_size, void* stream);
@@ -291,7 +327,8 @@ size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
  *                  num_seqs) with at most 1536 sequences runs on the tensor
  *                  cores with one share per SM, shares cut by cost; its
  *                  partial slots hold 96 rows, and it uses as many SMs as the
- *                  workspace size above has room for. A multiple
+ *                  workspace size above has room for. INT8, FP8 and INT4
+ *                  caches take this schedule only. A multiple
  *                  of 16 up to 4096 selects fixed split-KV partitions of that
  *                  many tokens (one CTA per partition, KV head and sequence).
  *   workspace      device memory of pa_decode_workspace_size() bytes,
@@ -322,6 +359,9 @@ size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
  *                  partition_size 0: partial slots, each int32 {sequence,
  *                  kv head, first token, end token} then fp32 m[R], l[R]
  *                  (base-2 units) and O[R][head_dim] (not normalised).
+ * INT4 caches: k_scale, v_scale, k_zp and v_zp are 16-byte aligned; at most
+ * 4080 query rows per KV head (num_heads / num_kv_heads x max_q_len). Codes,
+ * scales and zero points of slots past a context may hold anything.
  * Requirements: head_dim 64 or 128, block_size 16, num_heads a multiple of
  * num_kv_heads, context_lens[s] >= (query run length of s) >= 1, at most
  * 8192 sequences per call with partition_size 0. */
@@ -418,8 +458,8 @@ size_t pa_decode_shared_prefix_workspace_size(
  *                 pa_decode's rule: zero before the first call, left zero
  *                 by every call; the rest needs no initialisation.
  * Other arguments as pa_decode. Under PA_VALIDATE=1 the group arrays are
- * also checked against the block tables (PA_ERR_VALIDATION). INT8 caches
- * return PA_ERR_UNSUPPORTED. */
+ * also checked against the block tables (PA_ERR_VALIDATION). INT8, FP8 and
+ * INT4 caches return PA_ERR_UNSUPPORTED. */
 pa_status pa_decode_shared_prefix(
     void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
     const void* k_cache, const void* v_cache, pa_dtype kv_dtype,

@@ -18,7 +18,8 @@ import numpy as np
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpa.so")
 
-PA_F16, PA_BF16, PA_F32, PA_INT8, PA_FP8_E4M3 = 0, 1, 2, 3, 4
+PA_F16, PA_BF16, PA_F32, PA_INT8, PA_FP8_E4M3, PA_INT4 = 0, 1, 2, 3, 4, 5
+INT4_GROUP = 64    # elements of a cached row that share a 4-bit scale and zero point
 STATUS = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED",
           3: "PA_ERR_OUT_OF_BLOCKS", 4: "PA_ERR_BAD_REFCOUNT", 5: "PA_ERR_CUDA",
           6: "PA_ERR_VALIDATION", 7: "PA_ERR_DEVICE"}
@@ -51,6 +52,8 @@ _SIGS = {
     "pa_copy_blocks": ([_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32,
                         ctypes.c_int, _P], ctypes.c_int),
     "pa_append_kv": ([_P, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _P, _P,
+                      _I32, _I32, _I32, _I32, _I32, _P], ctypes.c_int),
+    "pa_gather_kv": ([_P, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _P, _P,
                       _I32, _I32, _I32, _I32, _I32, _P], ctypes.c_int),
     "pa_decode_workspace_size": ([_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32], _SZ),
     "pa_decode": ([_P, ctypes.c_int, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _P,
@@ -101,7 +104,13 @@ def version() -> str:
 def _dtype_code(t) -> int:
     import torch
     return {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32,
-            torch.int8: PA_INT8, torch.float8_e4m3fn: PA_FP8_E4M3}[t.dtype]
+            torch.int8: PA_INT8, torch.float8_e4m3fn: PA_FP8_E4M3,
+            torch.uint8: PA_INT4}[t.dtype]
+
+
+def _head_dim(cache) -> int:
+    """Elements of a cached row: an INT4 cache (uint8) holds two to a byte."""
+    return cache.shape[3] * 2 if _dtype_code(cache) == PA_INT4 else cache.shape[3]
 
 
 def _ptr(t) -> Optional[int]:
@@ -265,7 +274,7 @@ def copy_blocks(k_cache, v_cache, pairs, num_blocks: Optional[int] = None, k_sca
     nb = k_cache.shape[0] if num_blocks is None else num_blocks
     _check(lib().pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
                                 _ptr(k_zp), _ptr(v_zp), _ptr(pairs), n, nb,
-                                k_cache.shape[1], k_cache.shape[3], k_cache.shape[2],
+                                k_cache.shape[1], _head_dim(k_cache), k_cache.shape[2],
                                 _dtype_code(k_cache), _stream(stream)))
 
 
@@ -277,7 +286,20 @@ def append_kv(key, value, k_cache, v_cache, slot_mapping, num_blocks: Optional[i
     _check(lib().pa_append_kv(_ptr(key), _ptr(value), _dtype_code(key), _ptr(k_cache),
                               _ptr(v_cache), _dtype_code(k_cache), _ptr(k_scale),
                               _ptr(v_scale), _ptr(k_zp), _ptr(v_zp), _ptr(slot_mapping), T, nb,
-                              k_cache.shape[1], k_cache.shape[3], k_cache.shape[2],
+                              k_cache.shape[1], _head_dim(k_cache), k_cache.shape[2],
+                              _stream(stream)))
+
+
+def gather_kv(key, value, k_cache, v_cache, slot_mapping, num_blocks: Optional[int] = None,
+              k_scale=None, v_scale=None, k_zp=None, v_zp=None, stream=None) -> None:
+    """pa_gather_kv: the inverse of append_kv; key/value [T, H_kv, d] (F16,
+    BF16 or F32) receive the cached rows at the values the cache holds."""
+    T = int(key.shape[0])
+    nb = k_cache.shape[0] if num_blocks is None else num_blocks
+    _check(lib().pa_gather_kv(_ptr(key), _ptr(value), _dtype_code(key), _ptr(k_cache),
+                              _ptr(v_cache), _dtype_code(k_cache), _ptr(k_scale),
+                              _ptr(v_scale), _ptr(k_zp), _ptr(v_zp), _ptr(slot_mapping), T, nb,
+                              k_cache.shape[1], _head_dim(k_cache), k_cache.shape[2],
                               _stream(stream)))
 
 

@@ -62,8 +62,12 @@ using pa::fail;
 namespace {
 
 bool is_kv_dtype(pa_dtype t) {
-    return t == PA_F16 || t == PA_BF16 || t == PA_INT8 || t == PA_FP8_E4M3;
+    return t == PA_F16 || t == PA_BF16 || t == PA_INT8 || t == PA_FP8_E4M3 || t == PA_INT4;
 }
+
+// caches whose rows carry scales and zero points of their own
+bool has_zero_points(pa_dtype t) { return t == PA_INT8 || t == PA_INT4; }
+const char* cache_name(pa_dtype t) { return t == PA_INT4 ? "INT4" : "INT8"; }
 
 pa_status check_shape(int32_t num_kv_heads, int32_t head_dim, int32_t block_size) {
     if (block_size != 16)
@@ -83,6 +87,18 @@ pa_status to_host(std::vector<T>& h, const T* d, size_t n, cudaStream_t st) {
                            "validate: copy to host");
 }
 
+pa_status validate_slots(const int64_t* slots, int32_t num_tokens, int32_t num_blocks,
+                         cudaStream_t st) {
+    std::vector<int64_t> h;
+    if (pa_status s = to_host(h, slots, (size_t)num_tokens, st)) return s;
+    const int64_t lim = (int64_t)num_blocks * 16;
+    for (int32_t i = 0; i < num_tokens; ++i)
+        if (h[i] >= lim)
+            return fail(PA_ERR_VALIDATION, "slot %lld of token %d outside the pool (%lld slots)",
+                        (long long)h[i], i, (long long)lim);
+    return PA_OK;
+}
+
 }  // namespace
 
 extern "C" const char* pa_last_error(void) { return g_msg; }
@@ -99,9 +115,10 @@ extern "C" pa_status pa_copy_blocks(void* k_cache, void* v_cache, void* k_scale,
     if (!k_cache || !v_cache || !d_pairs) return fail(PA_ERR_INVALID_ARG, "NULL pointer");
     if (!is_kv_dtype(kv_dtype)) return fail(PA_ERR_INVALID_ARG, "kv_dtype %d", (int)kv_dtype);
     if (pa_status s = check_shape(num_kv_heads, head_dim, block_size)) return s;
-    const bool q8 = kv_dtype == PA_INT8;
-    if (q8 && (!k_scale || !v_scale || !k_zp || !v_zp))
-        return fail(PA_ERR_INVALID_ARG, "INT8 cache needs k_scale, v_scale, k_zp, v_zp");
+    const bool rows = has_zero_points(kv_dtype);
+    if (rows && (!k_scale || !v_scale || !k_zp || !v_zp))
+        return fail(PA_ERR_INVALID_ARG, "%s cache needs k_scale, v_scale, k_zp, v_zp",
+                    cache_name(kv_dtype));
     cudaStream_t st = (cudaStream_t)stream;
     if (pa::validate_enabled()) {
         std::vector<int32_t> h;
@@ -122,14 +139,15 @@ extern "C" pa_status pa_copy_blocks(void* k_cache, void* v_cache, void* k_scale,
     pa::CopyArgs a{};
     a.arrays[0] = k_cache;
     a.arrays[1] = v_cache;
-    a.bytes_per_block[0] = a.bytes_per_block[1] = tile * head_dim * pa::dtype_bytes(kv_dtype);
-    if (q8) {
+    a.bytes_per_block[0] = a.bytes_per_block[1] = tile * pa::cache_row_bytes(kv_dtype, head_dim);
+    if (rows) {
+        const int64_t groups = pa::row_groups(kv_dtype, head_dim);
         a.arrays[2] = k_scale;
         a.arrays[3] = v_scale;
         a.arrays[4] = k_zp;
         a.arrays[5] = v_zp;
-        a.bytes_per_block[2] = a.bytes_per_block[3] = tile * 4;
-        a.bytes_per_block[4] = a.bytes_per_block[5] = tile;
+        a.bytes_per_block[2] = a.bytes_per_block[3] = tile * groups * 4;
+        a.bytes_per_block[4] = a.bytes_per_block[5] = tile * groups;
     }
     for (int i = 0; i < 6; ++i)
         if (a.arrays[i] && ((uintptr_t)a.arrays[i] % 16 != 0))
@@ -162,25 +180,54 @@ extern "C" pa_status pa_append_kv(const void* key, const void* value, pa_dtype s
         return fail(PA_ERR_INVALID_ARG, "FP8 cache needs per-head k_scale and v_scale");
     if (pa_status s = check_shape(num_kv_heads, head_dim, block_size)) return s;
     if (num_blocks <= 0) return fail(PA_ERR_INVALID_ARG, "num_blocks %d", num_blocks);
-    if (kv_dtype == PA_INT8 && (!k_scale || !v_scale || !k_zp || !v_zp))
-        return fail(PA_ERR_INVALID_ARG, "INT8 cache needs k_scale, v_scale, k_zp, v_zp");
+    if (has_zero_points(kv_dtype) && (!k_scale || !v_scale || !k_zp || !v_zp))
+        return fail(PA_ERR_INVALID_ARG, "%s cache needs k_scale, v_scale, k_zp, v_zp",
+                    cache_name(kv_dtype));
     if (((uintptr_t)key | (uintptr_t)value | (uintptr_t)k_cache | (uintptr_t)v_cache) % 16)
         return fail(PA_ERR_INVALID_ARG, "key, value and caches must be 16-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
-    if (pa::validate_enabled()) {
-        std::vector<int64_t> h;
-        if (pa_status s = to_host(h, slot_mapping, (size_t)num_tokens, st)) return s;
-        const int64_t lim = (int64_t)num_blocks * block_size;
-        for (int32_t i = 0; i < num_tokens; ++i) {
-            if (h[i] >= lim)
-                return fail(PA_ERR_VALIDATION, "slot %lld of token %d outside the pool (%lld slots)",
-                            (long long)h[i], i, (long long)lim);
-        }
-    }
+    if (pa::validate_enabled())
+        if (pa_status s = validate_slots(slot_mapping, num_tokens, num_blocks, st)) return s;
+    if (kv_dtype == PA_INT4 && ((uintptr_t)k_scale | (uintptr_t)v_scale) % 4)
+        return fail(PA_ERR_INVALID_ARG, "k_scale / v_scale must be 4-byte aligned");
     pa::AppendArgs a{key, value, src_dtype, k_cache, v_cache, kv_dtype, k_scale, v_scale,
                      k_zp, v_zp, slot_mapping, num_tokens, num_blocks, num_kv_heads,
                      head_dim, block_size, st};
     return pa::launch_append_kv(a);
+}
+
+extern "C" pa_status pa_gather_kv(void* key, void* value, pa_dtype out_dtype,
+                                  const void* k_cache, const void* v_cache, pa_dtype kv_dtype,
+                                  const float* k_scale, const float* v_scale,
+                                  const int8_t* k_zp, const int8_t* v_zp,
+                                  const int64_t* slot_mapping, int32_t num_tokens,
+                                  int32_t num_blocks, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t block_size, void* stream) {
+    if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens < 0");
+    if (num_tokens == 0) return PA_OK;
+    if (!key || !value || !k_cache || !v_cache || !slot_mapping)
+        return fail(PA_ERR_INVALID_ARG, "NULL pointer");
+    if (out_dtype != PA_F16 && out_dtype != PA_BF16 && out_dtype != PA_F32)
+        return fail(PA_ERR_UNSUPPORTED, "out_dtype %d (F16, BF16 or F32)", (int)out_dtype);
+    if (!is_kv_dtype(kv_dtype)) return fail(PA_ERR_INVALID_ARG, "kv_dtype %d", (int)kv_dtype);
+    if (pa_status s = check_shape(num_kv_heads, head_dim, block_size)) return s;
+    if (num_blocks <= 0) return fail(PA_ERR_INVALID_ARG, "num_blocks %d", num_blocks);
+    if (kv_dtype == PA_FP8_E4M3 && (!k_scale || !v_scale))
+        return fail(PA_ERR_INVALID_ARG, "FP8 cache needs per-head k_scale and v_scale");
+    if (has_zero_points(kv_dtype) && (!k_scale || !v_scale || !k_zp || !v_zp))
+        return fail(PA_ERR_INVALID_ARG, "%s cache needs k_scale, v_scale, k_zp, v_zp",
+                    cache_name(kv_dtype));
+    if (((uintptr_t)key | (uintptr_t)value | (uintptr_t)k_cache | (uintptr_t)v_cache) % 16)
+        return fail(PA_ERR_INVALID_ARG, "key, value and caches must be 16-byte aligned");
+    if (((uintptr_t)k_scale | (uintptr_t)v_scale) % 4)
+        return fail(PA_ERR_INVALID_ARG, "k_scale / v_scale must be 4-byte aligned");
+    cudaStream_t st = (cudaStream_t)stream;
+    if (pa::validate_enabled())
+        if (pa_status s = validate_slots(slot_mapping, num_tokens, num_blocks, st)) return s;
+    return pa::launch_gather_kv(pa::GatherArgs{key, value, out_dtype, k_cache, v_cache, kv_dtype,
+                                               k_scale, v_scale, k_zp, v_zp, slot_mapping,
+                                               num_tokens, num_blocks, num_kv_heads, head_dim,
+                                               st});
 }
 
 namespace {
@@ -236,8 +283,9 @@ pa_status check_decode_args(void* out, pa_dtype out_dtype, const void* q, pa_dty
         return fail(PA_ERR_INVALID_ARG, "FP8 cache needs per-head k_scale and v_scale");
     if (out_dtype != PA_F32 && out_dtype != q_dtype)
         return fail(PA_ERR_UNSUPPORTED, "out_dtype must be F32 or the q dtype");
-    if (kv_dtype == PA_INT8 && (!k_scale || !v_scale || !k_zp || !v_zp))
-        return fail(PA_ERR_INVALID_ARG, "INT8 cache needs k_scale, v_scale, k_zp, v_zp");
+    if (has_zero_points(kv_dtype) && (!k_scale || !v_scale || !k_zp || !v_zp))
+        return fail(PA_ERR_INVALID_ARG, "%s cache needs k_scale, v_scale, k_zp, v_zp",
+                    cache_name(kv_dtype));
     if (!query_start_loc) {
         if (num_q_tokens != num_seqs)
             return fail(PA_ERR_INVALID_ARG, "without query_start_loc num_q_tokens must equal num_seqs");

@@ -1,5 +1,6 @@
-// KV-cache writes: append through a slot mapping (F16/BF16 copy, INT8 or
-// FP8 quantisation) and copy-on-write block copies.
+// KV-cache writes: append through a slot mapping (F16/BF16 copy, INT8, INT4
+// or FP8 quantisation) and copy-on-write block copies; the read side of the
+// same mapping, cached rows back as 16- or 32-bit rows.
 //
 // Append restates the decode workflow of "cs336 lecture 10" (KV Cache:
 // append the new K, V to the cache) and the block table of "KV Cache ...
@@ -182,6 +183,166 @@ __global__ void append_kv_fp8_kernel(const T* __restrict__ key, const T* __restr
     }
 }
 
+// INT4 append: the formula of the INT8 path with 16 unsigned codes and one
+// (scale, zero point) per 64 elements. A thread holds 8 consecutive elements
+// of a K row and of the same V row (16-byte loads, 4-byte code stores), 8
+// threads a group; the range is reduced over them with shuffles. Moves 2 bytes
+// in and 0.58 bytes out an element, so it is bound by memory at prefill sizes.
+template <typename T>
+__global__ void append_kv_int4_kernel(const T* __restrict__ key, const T* __restrict__ value,
+                                      uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
+                                      float* __restrict__ k_scale, float* __restrict__ v_scale,
+                                      int8_t* __restrict__ k_zp, int8_t* __restrict__ v_zp,
+                                      const int64_t* __restrict__ slots, int num_tokens,
+                                      int num_kv_heads, int head_dim, int64_t num_slots,
+                                      unsigned int* err) {
+    const int per_row = head_dim / 8, groups = head_dim / PA_INT4_GROUP;
+    const int64_t total = (int64_t)num_tokens * num_kv_heads * per_row;   // a multiple of 8
+    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    // the 8 threads of a group are all in range or all out of it, and hold one token
+    if (i >= total) return;
+    const unsigned int peers = 0xffu << (threadIdx.x & 24);
+    const int64_t tg = i / per_row;
+    const int c = (int)(i - tg * per_row);
+    const int64_t t = tg / num_kv_heads, g = tg - t * num_kv_heads;
+    const int64_t slot = __ldg(slots + t);
+    if (slot < 0) return;
+    if (slot >= num_slots) {
+        if (c == 0 && err) atomicOr(err, pa::ERR_BAD_SLOT);
+        return;
+    }
+    const int64_t row = ((slot / kBlock) * num_kv_heads + g) * kBlock + slot % kBlock;
+    const uint4 raw[2] = {__ldg(reinterpret_cast<const uint4*>(key) + i),
+                          __ldg(reinterpret_cast<const uint4*>(value) + i)};
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const T* h = reinterpret_cast<const T*>(&raw[which]);
+        float x[8], mn = 0.0f, mx = 0.0f;   // the range is widened to contain 0
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = to_f32<T>(h[e]);
+            mn = x[e] < mn ? x[e] : mn;
+            mx = x[e] > mx ? x[e] : mx;
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
+            const float a = __shfl_xor_sync(peers, mn, o);
+            const float b = __shfl_xor_sync(peers, mx, o);
+            mn = a < mn ? a : mn;
+            mx = b > mx ? b : mx;
+        }
+        float scale = __fdiv_rn(__fsub_rn(mx, mn), 15.0f);
+        if (scale == 0.0f) scale = 1.0f;
+        int zp = (int)-rintf(__fdiv_rn(mn, scale));
+        zp = zp < 0 ? 0 : (zp > 15 ? 15 : zp);
+        uint32_t word = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            int q = (int)rintf(__fdiv_rn(x[e], scale)) + zp;
+            q = q < 0 ? 0 : (q > 15 ? 15 : q);
+            word |= (uint32_t)q << (4 * e);
+        }
+        reinterpret_cast<uint32_t*>(which ? v_cache : k_cache)[row * per_row + c] = word;
+        if ((c & 7) == 0) {
+            (which ? v_scale : k_scale)[row * groups + c / 8] = scale;
+            (which ? v_zp : k_zp)[row * groups + c / 8] = (int8_t)zp;
+        }
+    }
+}
+
+// 8 consecutive cached elements (elements 8c .. 8c + 7 of cached row `row`,
+// KV head g) as fp32; a code's value is one fp32 product.
+template <int KV>
+__device__ __forceinline__ void load8(float (&x)[8], const void* cache, const float* scale,
+                                      const int8_t* zp, int64_t row, int64_t g, int c,
+                                      int head_dim) {
+    const int per_row = head_dim / 8;
+    if constexpr (KV == PA_F16 || KV == PA_BF16) {
+        const uint4 raw = __ldg(static_cast<const uint4*>(cache) + row * per_row + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (KV == PA_F16)
+                x[e] = __half2float(reinterpret_cast<const __half*>(&raw)[e]);
+            else
+                x[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(&raw)[e]);
+        }
+    } else if constexpr (KV == PA_INT4) {
+        const uint32_t w = __ldg(static_cast<const uint32_t*>(cache) + row * per_row + c);
+        const int64_t at = row * (head_dim / PA_INT4_GROUP) + c / 8;
+        const float s = __ldg(scale + at);
+        const int z = __ldg(zp + at);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __fmul_rn((float)((int)(w >> (4 * e) & 15u) - z), s);
+    } else {
+        const uint2 raw = __ldg(static_cast<const uint2*>(cache) + row * per_row + c);
+        if constexpr (KV == PA_INT8) {
+            const float s = __ldg(scale + row);
+            const int z = __ldg(zp + row);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = __fmul_rn((float)((int)reinterpret_cast<const int8_t*>(&raw)[e] - z), s);
+        } else {
+            const float s = __ldg(scale + g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const __half_raw v = __nv_cvt_fp8_to_halfraw(
+                    reinterpret_cast<const uint8_t*>(&raw)[e], __NV_E4M3);
+                x[e] = __fmul_rn(__half2float(__half(v)), s);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void store8(float* dst, const float (&x)[8]) {
+    reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* dst, const float (&x)[8]) {
+    uint4 raw;
+    T* h = reinterpret_cast<T*>(&raw);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (std::is_same<T, __half>::value) h[e] = __float2half_rn(x[e]);
+        else h[e] = __float2bfloat16_rn(x[e]);
+    }
+    *reinterpret_cast<uint4*>(dst) = raw;
+}
+
+// Cached rows read back through a slot mapping: the inverse of append, each
+// row at the values the cache holds. One thread per 8 elements of a K row and
+// of the same V row. Bound by memory: the cache's bytes in, the rows out.
+template <int KV, typename T>
+__global__ void gather_kv_kernel(T* __restrict__ key, T* __restrict__ value,
+                                 const void* __restrict__ k_cache,
+                                 const void* __restrict__ v_cache,
+                                 const float* __restrict__ k_scale,
+                                 const float* __restrict__ v_scale,
+                                 const int8_t* __restrict__ k_zp, const int8_t* __restrict__ v_zp,
+                                 const int64_t* __restrict__ slots, int num_tokens,
+                                 int num_kv_heads, int head_dim, int64_t num_slots,
+                                 unsigned int* err) {
+    const int per_row = head_dim / 8;
+    const int64_t total = (int64_t)num_tokens * num_kv_heads * per_row;
+    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const int64_t tg = i / per_row;
+    const int c = (int)(i - tg * per_row);
+    const int64_t t = tg / num_kv_heads, g = tg - t * num_kv_heads;
+    const int64_t slot = __ldg(slots + t);
+    if (slot < 0) return;
+    if (slot >= num_slots) {
+        if (c == 0 && err) atomicOr(err, pa::ERR_BAD_SLOT);
+        return;
+    }
+    const int64_t row = ((slot / kBlock) * num_kv_heads + g) * kBlock + slot % kBlock;
+    float a[8], b[8];
+    load8<KV>(a, k_cache, k_scale, k_zp, row, g, c, head_dim);
+    load8<KV>(b, v_cache, v_scale, v_zp, row, g, c, head_dim);
+    store8(key + i * 8, a);
+    store8(value + i * 8, b);
+}
+
 struct CopyParams {
     uint4* arrays[6];
     int64_t vecs_per_block[6];
@@ -211,7 +372,21 @@ namespace pa {
 pa_status launch_append_kv(const AppendArgs& a) {
     unsigned int* err = device_error_word();
     const int64_t num_slots = (int64_t)a.num_blocks * a.block_size;
-    if (a.kv_dtype == PA_FP8_E4M3) {
+    if (a.kv_dtype == PA_INT4) {
+        const int64_t total = (int64_t)a.num_tokens * a.num_kv_heads * (a.head_dim / 8);
+        const int threads = 256;
+        const int64_t grid = (total + threads - 1) / threads;
+        if (grid > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "too many tokens for one launch");
+#define PA_LAUNCH_Q4(T)                                                                        \
+    append_kv_int4_kernel<T><<<(unsigned)grid, threads, 0, a.stream>>>(                        \
+        static_cast<const T*>(a.key), static_cast<const T*>(a.value),                          \
+        static_cast<uint8_t*>(a.k_cache), static_cast<uint8_t*>(a.v_cache), a.k_scale,         \
+        a.v_scale, a.k_zp, a.v_zp, a.slots, a.num_tokens, a.num_kv_heads, a.head_dim,          \
+        num_slots, err)
+        if (a.src_dtype == PA_BF16) PA_LAUNCH_Q4(__nv_bfloat16);
+        else PA_LAUNCH_Q4(__half);
+#undef PA_LAUNCH_Q4
+    } else if (a.kv_dtype == PA_FP8_E4M3) {
         const int64_t total = (int64_t)a.num_tokens * a.num_kv_heads * (a.head_dim / 16);
         const int threads = 256;
         const int64_t blocks = (total + threads - 1) / threads;
@@ -259,6 +434,45 @@ pa_status launch_append_kv(const AppendArgs& a) {
 #undef PA_LAUNCH_Q8
     }
     return cuda_status(cudaGetLastError(), "append_kv launch");
+}
+
+namespace {
+
+template <int KV, typename T>
+void gather_as(const GatherArgs& a, unsigned grid, int threads, int64_t num_slots,
+               unsigned int* err) {
+    gather_kv_kernel<KV, T><<<grid, threads, 0, a.stream>>>(
+        static_cast<T*>(a.key), static_cast<T*>(a.value), a.k_cache, a.v_cache, a.k_scale,
+        a.v_scale, a.k_zp, a.v_zp, a.slots, a.num_tokens, a.num_kv_heads, a.head_dim, num_slots,
+        err);
+}
+
+template <int KV>
+void gather_from(const GatherArgs& a, unsigned grid, int threads, int64_t num_slots,
+                 unsigned int* err) {
+    if (a.out_dtype == PA_F32) gather_as<KV, float>(a, grid, threads, num_slots, err);
+    else if (a.out_dtype == PA_F16) gather_as<KV, __half>(a, grid, threads, num_slots, err);
+    else gather_as<KV, __nv_bfloat16>(a, grid, threads, num_slots, err);
+}
+
+}  // namespace
+
+pa_status launch_gather_kv(const GatherArgs& a) {
+    unsigned int* err = device_error_word();
+    const int64_t num_slots = (int64_t)a.num_blocks * kBlock;
+    const int threads = 256;
+    const int64_t total = (int64_t)a.num_tokens * a.num_kv_heads * (a.head_dim / 8);
+    const int64_t grid = (total + threads - 1) / threads;
+    if (grid > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "too many tokens for one launch");
+    const unsigned n = (unsigned)grid;
+    switch (a.kv_dtype) {
+        case PA_F16: gather_from<PA_F16>(a, n, threads, num_slots, err); break;
+        case PA_BF16: gather_from<PA_BF16>(a, n, threads, num_slots, err); break;
+        case PA_INT8: gather_from<PA_INT8>(a, n, threads, num_slots, err); break;
+        case PA_INT4: gather_from<PA_INT4>(a, n, threads, num_slots, err); break;
+        default: gather_from<PA_FP8_E4M3>(a, n, threads, num_slots, err); break;
+    }
+    return cuda_status(cudaGetLastError(), "gather_kv launch");
 }
 
 pa_status launch_copy_blocks(const CopyArgs& a) {

@@ -35,8 +35,19 @@ inline int dtype_bytes(pa_dtype t) {
         case PA_F16: case PA_BF16: return 2;
         case PA_F32: return 4;
         case PA_INT8: case PA_FP8_E4M3: return 1;
+        case PA_INT4: return 0;   // half a byte: see cache_row_bytes
     }
     return 0;
+}
+
+// Bytes of one cached row (head_dim elements of one token and KV head).
+inline int cache_row_bytes(pa_dtype t, int head_dim) {
+    return t == PA_INT4 ? head_dim / 2 : head_dim * dtype_bytes(t);
+}
+// Scales (and zero points) of one cached row: one for INT8, one per 64
+// elements for INT4, none for the others (FP8's are per KV head).
+inline int row_groups(pa_dtype t, int head_dim) {
+    return t == PA_INT4 ? head_dim / PA_INT4_GROUP : t == PA_INT8 ? 1 : 0;
 }
 
 bool validate_enabled();
@@ -80,6 +91,26 @@ struct AppendArgs {
     cudaStream_t stream;
 };
 pa_status launch_append_kv(const AppendArgs& a);
+
+struct GatherArgs {
+    void* key;
+    void* value;
+    pa_dtype out_dtype;
+    const void* k_cache;
+    const void* v_cache;
+    pa_dtype kv_dtype;
+    const float* k_scale;
+    const float* v_scale;
+    const int8_t* k_zp;
+    const int8_t* v_zp;
+    const int64_t* slots;
+    int32_t num_tokens;
+    int32_t num_blocks;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    cudaStream_t stream;
+};
+pa_status launch_gather_kv(const GatherArgs& a);
 
 struct CopyArgs {
     void* arrays[6];          // k, v, k_scale, v_scale, k_zp, v_zp (unused = null)
@@ -185,14 +216,14 @@ struct BalancedShape {
 };
 
 // Kernel families of the balanced schedule.
-enum TileKind { kTile16Bit = 0, kTileInt8 = 1, kTileFp8 = 2 };
+enum TileKind { kTile16Bit = 0, kTileInt8 = 1, kTileFp8 = 2, kTileInt4 = 3 };
 
 // Query rows per tile: 16 while a KV head has at most 16 rows (G q heads x
 // the longest query run), else 64 for the 16-bit kernels (four warps of 16
-// rows share each block); the INT8 and FP8 kernels always use 16 (one warp
-// per tile, further rows as further chunks).
+// rows share each block); the INT8, FP8 and INT4 kernels always use 16 (one
+// warp per tile, further rows as further chunks).
 inline int tile_rows(int64_t rows, int kind) {
-    if (rows <= 16 || kind == kTileFp8 || kind == kTileInt8) return 16;
+    if (rows <= 16 || kind != kTile16Bit) return 16;
     return 64;
 }
 
@@ -231,6 +262,7 @@ inline pa_status balanced_check(const DecodeArgs& a) {
                                            a.max_q_len, a.max_context_len,
                                            a.kv_dtype == PA_INT8       ? kTileInt8
                                            : a.kv_dtype == PA_FP8_E4M3 ? kTileFp8
+                                           : a.kv_dtype == PA_INT4     ? kTileInt4
                                                                        : kTile16Bit);
     if (b.max_chunks > 255 || b.virtual_blocks > 0x7fffffffll)
         return fail(PA_ERR_UNSUPPORTED, "decode call too large for one balanced launch");

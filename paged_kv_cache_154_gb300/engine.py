@@ -19,12 +19,12 @@ from typing import Dict, List, Optional, Sequence
 import numpy as np
 import torch
 
-from . import (BLOCK_SIZE, Pool, append_kv, copy_blocks, decode, decode_shared_prefix,
+from . import (BLOCK_SIZE, INT4_GROUP, Pool, append_kv, copy_blocks, decode, decode_shared_prefix,
                decode_shared_prefix_workspace_size, decode_workspace_size,
                zeroed_workspace)
 
 KV_TORCH = {"f16": torch.float16, "bf16": torch.bfloat16, "int8": torch.int8,
-            "fp8": torch.float8_e4m3fn}
+            "fp8": torch.float8_e4m3fn, "int4": torch.uint8}
 
 
 @dataclass
@@ -71,14 +71,17 @@ class PagedKVCache:
         self.pool = Pool(num_blocks, BLOCK_SIZE, free_order)
         nb = num_blocks + canary_blocks
         shp = (nb, num_kv_heads, BLOCK_SIZE, head_dim)
+        if kv_dtype == "int4":     # two elements to a byte
+            shp = shp[:3] + (head_dim // 2,)
         self.k = torch.zeros(shp, dtype=KV_TORCH[kv_dtype], device=self.device)
         self.v = torch.zeros(shp, dtype=KV_TORCH[kv_dtype], device=self.device)
         self.k_scale = self.v_scale = self.k_zp = self.v_zp = None
-        if kv_dtype == "int8":
-            self.k_scale = torch.zeros(shp[:3], dtype=torch.float32, device=self.device)
-            self.v_scale = torch.zeros(shp[:3], dtype=torch.float32, device=self.device)
-            self.k_zp = torch.zeros(shp[:3], dtype=torch.int8, device=self.device)
-            self.v_zp = torch.zeros(shp[:3], dtype=torch.int8, device=self.device)
+        if kv_dtype in ("int8", "int4"):
+            row = shp[:3] + ((head_dim // INT4_GROUP,) if kv_dtype == "int4" else ())
+            self.k_scale = torch.zeros(row, dtype=torch.float32, device=self.device)
+            self.v_scale = torch.zeros(row, dtype=torch.float32, device=self.device)
+            self.k_zp = torch.zeros(row, dtype=torch.int8, device=self.device)
+            self.v_zp = torch.zeros(row, dtype=torch.int8, device=self.device)
         if kv_dtype == "fp8":
             if head_scales is None:
                 raise ValueError("an FP8 cache needs per-head scales (k_scale, v_scale)")
@@ -91,7 +94,7 @@ class PagedKVCache:
 
     def arrays(self) -> List[torch.Tensor]:
         out = [self.k, self.v]
-        if self.kv_dtype == "int8":
+        if self.kv_dtype in ("int8", "int4"):
             out += [self.k_scale, self.v_scale, self.k_zp, self.v_zp]
         return out
 
