@@ -138,6 +138,22 @@ pa_status pa_seq_append_slots_batch(pa_pool* pool, const int32_t* seqs,
                                     int64_t* slots_out, int32_t* cow_pairs_out,
                                     int32_t* n_cow);
 
+/* Make the blocks under the first n_tokens tokens of a sequence its own, for a
+ * call that writes into them (pa_move_tokens): each that other sequences share
+ * is replaced by a fresh block, with the pair (old, fresh) appended to
+ * cow_pairs_out (int32 [max_pairs][2]; may be NULL if none is shared) and
+ * counted in *n_cow for pa_copy_blocks; each that the prefix cache holds is
+ * taken out of it. All or nothing: PA_ERR_OUT_OF_BLOCKS, or PA_ERR_INVALID_ARG
+ * when max_pairs is too small, changes nothing. */
+pa_status pa_seq_make_private(pa_pool* pool, int32_t seq, int32_t n_tokens,
+                              int32_t* cow_pairs_out, int32_t max_pairs, int32_t* n_cow);
+
+/* Give up the tokens past the first n_tokens (at most the tokens held): whole
+ * blocks behind them are released as by pa_seq_free. After an eviction, or to
+ * take back rejected draft tokens. The sequence registers nothing in the prefix
+ * cache from then on. */
+pa_status pa_seq_truncate(pa_pool* pool, int32_t seq, int32_t n_tokens);
+
 /* Release a sequence: refcount - 1 on each block; blocks reaching 0 go back
  * to the end of the free list in table order ([p3] release). */
 pa_status pa_seq_free(pa_pool* pool, int32_t seq);
@@ -472,6 +488,96 @@ pa_status pa_decode_shared_prefix(
     const int32_t* prefix_len, int32_t num_groups, int32_t max_group_q_len,
     int32_t max_prefix_len, void* workspace, size_t workspace_bytes,
     void* stream);
+
+/* ---- Eviction by accumulated attention weight. A cache of bounded size keeps
+ * the tokens that attention has looked at most. Per decode step (or once, from
+ * a prompt's last queries) pa_accumulate_weights adds up what every cached token
+ * received; when a sequence is over its budget, pa_evict_select chooses the kept
+ * tokens of every KV head and pa_move_tokens moves the rows, after
+ * pa_seq_make_private on the pool and before pa_seq_truncate. ---- */
+
+/* Bytes of workspace pa_accumulate_weights needs for these sizes (0 for invalid
+ * sizes); at least 256-byte aligned, needs no initialisation, and may be shared
+ * by calls of one stream. Host-only: needs no GPU. */
+size_t pa_accumulate_weights_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
+                                            int32_t num_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_q_len,
+                                            int32_t max_context_len);
+
+/* scores_out[s][g][t] = scores_in[s][g][t] + the attention weight that token t
+ * of sequence s receives from the sequence's query run, summed over its queries
+ * and over the query heads of KV head g: the softmax of pa_decode on the same
+ * arguments (every cache type; causal within the run), in fp32.
+ *   scores_out, scores_in  fp32 [num_seqs][num_kv_heads][score_stride]; rows are
+ *                  in the order of block_tables. scores_in may be scores_out, or
+ *                  NULL for zeros. Only t < context_lens[s] is read and written.
+ *                  scores_out is 16-byte aligned.
+ *   score_stride   elements from one KV head's scores to the next, at least
+ *                  max_context_len
+ *   query_start_loc  as in pa_decode; an empty run, a context of length 0, and a
+ *                  query that sees no token add nothing (num_q_tokens is still
+ *                  at least num_seqs)
+ *   context_lens   lengths above max_context_len are taken as max_context_len
+ * At most 4096 query rows per KV head (num_heads / num_kv_heads x max_q_len)
+ * and 65535 sequences. Results do not depend on the order in which the GPU
+ * runs the call. */
+pa_status pa_accumulate_weights(
+    float* scores_out, const float* scores_in, int64_t score_stride, const void* q,
+    pa_dtype q_dtype, const void* k_cache, pa_dtype kv_dtype, const float* k_scale,
+    const int8_t* k_zp, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+    int32_t num_q_tokens, int32_t max_q_len, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+    int32_t max_context_len, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Choose which tokens stay. For sequence s with L = context_lens[s] tokens and
+ * n = min(new_lens[s], L) to keep (a negative new_lens[s] keeps all), each KV
+ * head keeps first its protected tokens, in slot order, then those of the
+ * largest score, equal scores in slot order (-0 equals +0; NaN comes last).
+ * Slots 0 .. n - 1 remain: the i-th slot below n whose token goes takes the i-th
+ * kept token from above. So tokens do not stay in text order; the positions say
+ * where in the text a slot's token stands.
+ *   positions      int32, shaped as the scores, or NULL (all in text order): the
+ *                  token's position, or negative where the slot has its token in
+ *                  text order counted from the end, total_lens[s] - L + slot (as
+ *                  slots appended since the last eviction do)
+ *   total_lens     int32 [num_seqs]: tokens the sequence has ever had, or NULL
+ *                  for context_lens
+ *   num_sinks, num_recent   tokens at positions < num_sinks or >= total_lens[s] -
+ *                  num_recent are protected
+ *   moves          int32 [num_seqs][num_kv_heads][max_moves][2]: (source slot,
+ *                  destination slot), destinations ascending; max_moves is at
+ *                  least max_context_len / 2 (and 1). 8-byte aligned. Entries past
+ *                  the count are left as they were.
+ *   move_counts    int32 [num_seqs][num_kv_heads]
+ *   scores_out, positions_out   as scores and positions, which they may be (the
+ *                  same pointers; no other overlap): the entries of slots 0 ..
+ *                  n - 1 after the moves, every position explicit; entries n .. L
+ *                  - 1 become 0 and -1; entries from L on are left as they were
+ * score_stride as in pa_accumulate_weights. */
+pa_status pa_evict_select(int32_t* moves, int32_t max_moves, int32_t* move_counts,
+                          float* scores_out, int32_t* positions_out, const float* scores,
+                          const int32_t* positions, int64_t score_stride,
+                          const int32_t* context_lens, const int32_t* new_lens,
+                          const int32_t* total_lens, int32_t num_seqs, int32_t num_kv_heads,
+                          int32_t max_context_len, int32_t num_sinks, int32_t num_recent,
+                          void* stream);
+
+/* Carry out moves within sequences: for i < move_counts[s][g], the K and V row
+ * (with its scales and zero points, where rows have them) of KV head g at slot
+ * moves[s][g][i][0] of sequence s is copied to slot moves[s][g][i][1]. No
+ * destination may appear twice or as a source; the blocks written must belong to
+ * the sequence alone (pa_seq_make_private). A slot outside [0, context_lens[s])
+ * is skipped with PA_DEVERR_BAD_SLOT, a block outside the pool with
+ * PA_DEVERR_BAD_BLOCK. Any cache type; other arguments as in pa_copy_blocks and
+ * pa_decode. */
+pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype kv_dtype, float* k_scale,
+                         float* v_scale, int8_t* k_zp, int8_t* v_zp,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* moves, int32_t max_moves,
+                         const int32_t* move_counts, int32_t num_seqs, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                         int32_t max_context_len, void* stream);
 
 /* Device error word bits. */
 #define PA_DEVERR_WAIT_FULL  (1u << 0) /* a consumer gave up waiting for a staged tile */

@@ -62,6 +62,16 @@ _SIGS = {
     "pa_decode_no_alloc": ([_P, ctypes.c_int, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P,
                             _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
                             _I32, ctypes.c_float, _I32, _I32, _P], ctypes.c_int),
+    "pa_seq_make_private": ([_P, _I32, _I32, _P, _I32, _P], ctypes.c_int),
+    "pa_seq_truncate": ([_P, _I32, _I32], ctypes.c_int),
+    "pa_accumulate_weights_workspace_size": ([_I32] * 7, _SZ),
+    "pa_accumulate_weights": ([_P, _P, _I64, _P, ctypes.c_int, _P, ctypes.c_int, _P, _P, _P,
+                               _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                               ctypes.c_float, _I32, _P, _SZ, _P], ctypes.c_int),
+    "pa_evict_select": ([_P, _I32, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _I32, _I32, _I32, _I32,
+                         _I32, _P], ctypes.c_int),
+    "pa_move_tokens": ([_P, _P, ctypes.c_int, _P, _P, _P, _P, _P, _I32, _P, _P, _I32, _P, _I32,
+                        _I32, _I32, _I32, _I32, _I32, _P], ctypes.c_int),
     "pa_device_error": ([_P, _P], ctypes.c_int),
     "pa_pool_prefix_groups": ([_P, _P, _I32, _P, _P, _P, _P], ctypes.c_int),
     "pa_pool_enable_prefix_cache": ([_P, _I32], ctypes.c_int),
@@ -184,6 +194,19 @@ class Pool:
                                                slots.ctypes.data, pairs.ctypes.data,
                                                ctypes.addressof(ncow)))
         return slots[:total], pairs[:ncow.value]
+
+    def seq_make_private(self, seq: int, n_tokens: int) -> np.ndarray:
+        """pa_seq_make_private: the copy pairs, int32 [k][2], for copy_blocks."""
+        room = max(1, -(-int(n_tokens) // self.block_size))
+        pairs = np.zeros((room, 2), np.int32)
+        n = _I32()
+        _check(lib().pa_seq_make_private(self._h, seq, n_tokens, pairs.ctypes.data, room,
+                                         ctypes.addressof(n)))
+        return pairs[:n.value]
+
+    def seq_truncate(self, seq: int, n_tokens: int) -> None:
+        """pa_seq_truncate: give up the tokens past the first n_tokens."""
+        _check(lib().pa_seq_truncate(self._h, seq, n_tokens))
 
     def seq_free(self, seq: int) -> None:
         _check(lib().pa_seq_free(self._h, seq))
@@ -368,6 +391,86 @@ def decode_shared_prefix(out, q, k_cache, v_cache, block_tables, context_lens,
         q.shape[2], k_cache.shape[2], nb, float(scale), int(max_context_len), _ptr(group_start),
         _ptr(prefix_len), int(prefix_len.shape[0]), int(max_group_q_len), int(max_prefix_len),
         _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# eviction by accumulated attention weight
+# ---------------------------------------------------------------------------
+
+def _shaped(name: str, t, shape, dtype) -> None:
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
+
+
+def accumulate_weights_workspace_size(num_seqs: int, num_q_tokens: int, num_heads: int,
+                                      num_kv_heads: int, head_dim: int, max_q_len: int,
+                                      max_context_len: int) -> int:
+    return int(lib().pa_accumulate_weights_workspace_size(
+        num_seqs, num_q_tokens, num_heads, num_kv_heads, head_dim, max_q_len, max_context_len))
+
+
+def accumulate_weights(scores_out, scores_in, q, k_cache, block_tables, context_lens,
+                       max_context_len: int, scale: float, query_start_loc=None,
+                       max_q_len: int = 1, num_blocks=None, k_scale=None, k_zp=None,
+                       workspace=None, stream=None) -> None:
+    """pa_accumulate_weights; scores fp32 [num_seqs, H_kv, width >= max_context_len],
+    scores_in None for zeros, or scores_out itself; workspace: uint8 of
+    accumulate_weights_workspace_size() bytes; other arguments as decode()."""
+    import torch
+    num_seqs = int(context_lens.shape[0])
+    shape = (num_seqs, k_cache.shape[1], scores_out.shape[2])
+    _shaped("scores_out", scores_out, shape, torch.float32)
+    if scores_in is not None:
+        _shaped("scores_in", scores_in, shape, torch.float32)
+    nb = k_cache.shape[0] if num_blocks is None else num_blocks
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().pa_accumulate_weights(
+        _ptr(scores_out), _ptr(scores_in), shape[2], _ptr(q), _dtype_code(q), _ptr(k_cache),
+        _dtype_code(k_cache), _ptr(k_scale), _ptr(k_zp), _ptr(block_tables),
+        block_tables.shape[1], _ptr(context_lens), _ptr(query_start_loc), num_seqs,
+        int(q.shape[0]), max_q_len if query_start_loc is not None else 1, q.shape[1],
+        k_cache.shape[1], q.shape[2], k_cache.shape[2], nb, float(scale), int(max_context_len),
+        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def evict_select(moves, move_counts, scores_out, positions_out, scores, positions, context_lens,
+                 new_lens, total_lens, max_context_len: int, num_sinks: int = 0,
+                 num_recent: int = 0, stream=None) -> None:
+    """pa_evict_select; moves int32 [num_seqs, H_kv, max_moves, 2], move_counts
+    int32 [num_seqs, H_kv], scores fp32 and positions int32 (or None) [num_seqs,
+    H_kv, width], lengths int32 [num_seqs] (total_lens may be None)."""
+    import torch
+    num_seqs = int(context_lens.shape[0])
+    shape = (num_seqs, scores.shape[1], scores.shape[2])
+    _shaped("scores", scores, shape, torch.float32)
+    _shaped("scores_out", scores_out, shape, torch.float32)
+    _shaped("positions_out", positions_out, shape, torch.int32)
+    if positions is not None:
+        _shaped("positions", positions, shape, torch.int32)
+    _shaped("moves", moves, (*shape[:2], moves.shape[2], 2), torch.int32)
+    _shaped("move_counts", move_counts, shape[:2], torch.int32)
+    _check(lib().pa_evict_select(
+        _ptr(moves), moves.shape[2], _ptr(move_counts), _ptr(scores_out), _ptr(positions_out),
+        _ptr(scores), _ptr(positions), shape[2], _ptr(context_lens), _ptr(new_lens),
+        _ptr(total_lens), num_seqs, shape[1], int(max_context_len), int(num_sinks),
+        int(num_recent), _stream(stream)))
+
+
+def move_tokens(k_cache, v_cache, block_tables, context_lens, moves, move_counts,
+                max_context_len: int, num_blocks=None, k_scale=None, v_scale=None, k_zp=None,
+                v_zp=None, stream=None) -> None:
+    """pa_move_tokens; moves and move_counts as evict_select() writes them."""
+    import torch
+    num_seqs = int(context_lens.shape[0])
+    shape = (num_seqs, k_cache.shape[1])
+    _shaped("moves", moves, (*shape, moves.shape[2], 2), torch.int32)
+    _shaped("move_counts", move_counts, shape, torch.int32)
+    nb = k_cache.shape[0] if num_blocks is None else num_blocks
+    _check(lib().pa_move_tokens(
+        _ptr(k_cache), _ptr(v_cache), _dtype_code(k_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(k_zp), _ptr(v_zp), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+        _ptr(moves), moves.shape[2], _ptr(move_counts), num_seqs, k_cache.shape[1],
+        _head_dim(k_cache), k_cache.shape[2], nb, int(max_context_len), _stream(stream)))
 
 
 NO_ALLOC_WORKSPACE_BYTES = 40 << 20

@@ -209,18 +209,11 @@ extern "C" pa_status pa_gather_kv(void* key, void* value, pa_dtype out_dtype,
         return fail(PA_ERR_INVALID_ARG, "NULL pointer");
     if (out_dtype != PA_F16 && out_dtype != PA_BF16 && out_dtype != PA_F32)
         return fail(PA_ERR_UNSUPPORTED, "out_dtype %d (F16, BF16 or F32)", (int)out_dtype);
-    if (!is_kv_dtype(kv_dtype)) return fail(PA_ERR_INVALID_ARG, "kv_dtype %d", (int)kv_dtype);
-    if (pa_status s = check_shape(num_kv_heads, head_dim, block_size)) return s;
-    if (num_blocks <= 0) return fail(PA_ERR_INVALID_ARG, "num_blocks %d", num_blocks);
-    if (kv_dtype == PA_FP8_E4M3 && (!k_scale || !v_scale))
-        return fail(PA_ERR_INVALID_ARG, "FP8 cache needs per-head k_scale and v_scale");
-    if (has_zero_points(kv_dtype) && (!k_scale || !v_scale || !k_zp || !v_zp))
-        return fail(PA_ERR_INVALID_ARG, "%s cache needs k_scale, v_scale, k_zp, v_zp",
-                    cache_name(kv_dtype));
-    if (((uintptr_t)key | (uintptr_t)value | (uintptr_t)k_cache | (uintptr_t)v_cache) % 16)
-        return fail(PA_ERR_INVALID_ARG, "key, value and caches must be 16-byte aligned");
-    if (((uintptr_t)k_scale | (uintptr_t)v_scale) % 4)
-        return fail(PA_ERR_INVALID_ARG, "k_scale / v_scale must be 4-byte aligned");
+    if (pa_status s = pa::check_cache_args(k_cache, v_cache, kv_dtype, k_scale, v_scale, k_zp,
+                                           v_zp, num_kv_heads, head_dim, block_size, num_blocks))
+        return s;
+    if (((uintptr_t)key | (uintptr_t)value) % 16)
+        return fail(PA_ERR_INVALID_ARG, "key and value must be 16-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
     if (pa::validate_enabled())
         if (pa_status s = validate_slots(slot_mapping, num_tokens, num_blocks, st)) return s;
@@ -307,13 +300,13 @@ pa_status check_decode_args(void* out, pa_dtype out_dtype, const void* q, pa_dty
     return PA_OK;
 }
 
-// PA_VALIDATE=1: context lengths, query runs and block-table entries of every
-// sequence, read back from the device.
-pa_status validate_decode_arrays(const int32_t* block_tables, int32_t max_blocks_per_seq,
-                                 const int32_t* context_lens, const int32_t* query_start_loc,
-                                 int32_t num_seqs, int32_t num_q_tokens, int32_t max_q_len,
-                                 int32_t block_size, int32_t num_blocks, int32_t max_context_len,
-                                 cudaStream_t st) {
+// PA_VALIDATE=1: context lengths, query runs (of at least min_run tokens) and
+// block-table entries of every sequence, read back from the device.
+static pa_status validate_sequences(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t* context_lens, const int32_t* query_start_loc,
+                                    int32_t num_seqs, int32_t num_q_tokens, int32_t max_q_len,
+                                    int32_t min_run, int32_t block_size, int32_t num_blocks,
+                                    int32_t max_context_len, cudaStream_t st) {
     std::vector<int32_t> lens, bt, qsl;
     if (pa_status s = to_host(lens, context_lens, (size_t)num_seqs, st)) return s;
     if (pa_status s = to_host(bt, block_tables, (size_t)num_seqs * max_blocks_per_seq, st))
@@ -321,11 +314,11 @@ pa_status validate_decode_arrays(const int32_t* block_tables, int32_t max_blocks
     if (query_start_loc)
         if (pa_status s = to_host(qsl, query_start_loc, (size_t)num_seqs + 1, st)) return s;
     for (int32_t s = 0; s < num_seqs; ++s) {
-        int32_t r = query_start_loc ? qsl[s + 1] - qsl[s] : 1;
+        int32_t r = query_start_loc ? qsl[s + 1] - qsl[s] : min_run;
         int32_t L = lens[s];
         if (query_start_loc && (qsl[s] < 0 || qsl[s + 1] > num_q_tokens))
             return fail(PA_ERR_VALIDATION, "query_start_loc of sequence %d out of range", s);
-        if (r < 1 || r > max_q_len || L < r || L > max_context_len)
+        if (r < min_run || r > max_q_len || L < (min_run ? r : 0) || L > max_context_len)
             return fail(PA_ERR_VALIDATION, "sequence %d: context_len %d, query run %d", s, L, r);
         for (int32_t b = 0; b < (L + block_size - 1) / block_size; ++b) {
             int32_t e = bt[(size_t)s * max_blocks_per_seq + b];
@@ -335,6 +328,95 @@ pa_status validate_decode_arrays(const int32_t* block_tables, int32_t max_blocks
         }
     }
     return PA_OK;
+}
+
+pa_status check_cache_args(const void* k_cache, const void* v_cache, pa_dtype kv_dtype,
+                           const float* k_scale, const float* v_scale, const int8_t* k_zp,
+                           const int8_t* v_zp, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t block_size, int32_t num_blocks) {
+    if (!is_kv_dtype(kv_dtype)) return fail(PA_ERR_INVALID_ARG, "kv_dtype %d", (int)kv_dtype);
+    if (pa_status s = check_shape(num_kv_heads, head_dim, block_size)) return s;
+    if (num_blocks <= 0) return fail(PA_ERR_INVALID_ARG, "num_blocks %d", num_blocks);
+    if (kv_dtype == PA_FP8_E4M3 && (!k_scale || !v_scale))
+        return fail(PA_ERR_INVALID_ARG, "FP8 cache needs per-head k_scale and v_scale");
+    if (has_zero_points(kv_dtype) && (!k_scale || !v_scale || !k_zp || !v_zp))
+        return fail(PA_ERR_INVALID_ARG, "%s cache needs k_scale, v_scale, k_zp, v_zp",
+                    cache_name(kv_dtype));
+    if (((uintptr_t)k_cache | (uintptr_t)v_cache) % 16)
+        return fail(PA_ERR_INVALID_ARG, "k_cache and v_cache must be 16-byte aligned");
+    if (((uintptr_t)k_scale | (uintptr_t)v_scale) % 4)
+        return fail(PA_ERR_INVALID_ARG, "k_scale / v_scale must be 4-byte aligned");
+    return PA_OK;
+}
+
+pa_status validate_lengths(const int32_t* context_lens, const int32_t* new_lens,
+                           const int32_t* total_lens, int32_t num_seqs, int32_t max_context_len,
+                           cudaStream_t st) {
+    std::vector<int32_t> lens, total;
+    if (pa_status s = to_host(lens, context_lens, (size_t)num_seqs, st)) return s;
+    if (total_lens)
+        if (pa_status s = to_host(total, total_lens, (size_t)num_seqs, st)) return s;
+    for (int32_t s = 0; s < num_seqs; ++s) {
+        if (lens[s] < 0 || lens[s] > max_context_len)
+            return fail(PA_ERR_VALIDATION, "sequence %d: context_len %d", s, lens[s]);
+        if (total_lens && total[s] < lens[s])
+            return fail(PA_ERR_VALIDATION, "sequence %d: total_len %d < context_len %d", s,
+                        total[s], lens[s]);
+    }
+    return PA_OK;
+}
+
+pa_status validate_moves(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* moves, int32_t max_moves,
+                         const int32_t* move_counts, int32_t num_seqs, int32_t num_kv_heads,
+                         int32_t num_blocks, int32_t max_context_len, cudaStream_t st) {
+    if (pa_status s = validate_score_arrays(block_tables, max_blocks_per_seq, context_lens, nullptr,
+                                            num_seqs, num_seqs, 1, num_blocks, max_context_len, st))
+        return s;
+    std::vector<int32_t> lens, counts, mv;
+    const size_t rows = (size_t)num_seqs * num_kv_heads;
+    if (pa_status s = to_host(lens, context_lens, (size_t)num_seqs, st)) return s;
+    if (pa_status s = to_host(counts, move_counts, rows, st)) return s;
+    if (pa_status s = to_host(mv, moves, rows * max_moves * 2, st)) return s;
+    std::vector<uint8_t> role;
+    for (size_t r = 0; r < rows; ++r) {
+        const int32_t L = lens[r / num_kv_heads];
+        if (counts[r] < 0 || counts[r] > max_moves)
+            return fail(PA_ERR_VALIDATION, "row %zu has %d moves of at most %d", r, counts[r],
+                        max_moves);
+        role.assign((size_t)L, 0);   // 1 = source, 2 = destination
+        for (int32_t i = 0; i < 2 * counts[r]; ++i) {
+            const int32_t slot = mv[r * max_moves * 2 + i];
+            const uint8_t want = (i % 2) ? 2 : 1;
+            if (slot < 0 || slot >= L)
+                return fail(PA_ERR_VALIDATION, "row %zu, move %d: slot %d outside [0,%d)", r,
+                            i / 2, slot, L);
+            if (role[slot] && (role[slot] != want || want == 2))
+                return fail(PA_ERR_VALIDATION, "row %zu: slot %d is used twice in its moves", r,
+                            slot);
+            role[slot] = want;
+        }
+    }
+    return PA_OK;
+}
+
+pa_status validate_decode_arrays(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* context_lens, const int32_t* query_start_loc,
+                                 int32_t num_seqs, int32_t num_q_tokens, int32_t max_q_len,
+                                 int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                                 cudaStream_t st) {
+    return validate_sequences(block_tables, max_blocks_per_seq, context_lens, query_start_loc,
+                              num_seqs, num_q_tokens, max_q_len, 1, block_size, num_blocks,
+                              max_context_len, st);
+}
+
+pa_status validate_score_arrays(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                const int32_t* context_lens, const int32_t* query_start_loc,
+                                int32_t num_seqs, int32_t num_q_tokens, int32_t max_q_len,
+                                int32_t num_blocks, int32_t max_context_len, cudaStream_t st) {
+    return validate_sequences(block_tables, max_blocks_per_seq, context_lens, query_start_loc,
+                              num_seqs, num_q_tokens, max_q_len, 0, 16, num_blocks,
+                              max_context_len, st);
 }
 
 }  // namespace pa

@@ -194,6 +194,27 @@ pa_status validate_decode_arrays(const int32_t* block_tables, int32_t max_blocks
                                  int32_t num_seqs, int32_t num_q_tokens, int32_t max_q_len,
                                  int32_t block_size, int32_t num_blocks, int32_t max_context_len,
                                  cudaStream_t st);
+// The same for the calls that also take empty sequences and empty query runs.
+pa_status validate_score_arrays(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                const int32_t* context_lens, const int32_t* query_start_loc,
+                                int32_t num_seqs, int32_t num_q_tokens, int32_t max_q_len,
+                                int32_t num_blocks, int32_t max_context_len, cudaStream_t st);
+// A cache's pointers, type and shape, for the calls that take whole caches.
+pa_status check_cache_args(const void* k_cache, const void* v_cache, pa_dtype kv_dtype,
+                           const float* k_scale, const float* v_scale, const int8_t* k_zp,
+                           const int8_t* v_zp, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t block_size, int32_t num_blocks);
+// PA_VALIDATE=1: 0 <= context_lens[s] <= max_context_len, and total_lens[s] (if
+// given) at least context_lens[s].
+pa_status validate_lengths(const int32_t* context_lens, const int32_t* new_lens,
+                           const int32_t* total_lens, int32_t num_seqs, int32_t max_context_len,
+                           cudaStream_t st);
+// PA_VALIDATE=1: every move inside its sequence, no destination used twice or
+// as a source, all blocks inside the pool.
+pa_status validate_moves(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* moves, int32_t max_moves,
+                         const int32_t* move_counts, int32_t num_seqs, int32_t num_kv_heads,
+                         int32_t num_blocks, int32_t max_context_len, cudaStream_t st);
 
 // Balanced schedule (partition_size == 0): at most this many worker warps
 // (and partial-slot pairs), and at most this many sequences per call (their

@@ -388,6 +388,74 @@ extern "C" pa_status pa_seq_free(pa_pool* p, int32_t seq) {
     return PA_OK;
 }
 
+// The blocks under a sequence's first n tokens made its own: a shared one is
+// replaced by a fresh block (the pair is returned for the device copy), and none
+// stays registered in the prefix cache, since its contents are about to stop
+// being the tokens it is registered under.
+extern "C" pa_status pa_seq_make_private(pa_pool* p, int32_t seq, int32_t n_tokens,
+                                         int32_t* cow_pairs_out, int32_t max_pairs,
+                                         int32_t* n_cow) {
+    if (!p || !n_cow) return pa::fail(PA_ERR_INVALID_ARG, "NULL argument");
+    *n_cow = 0;
+    if (pa_status s = check_seq(p, seq)) return s;
+    if (n_tokens < 0 || n_tokens > p->lens[seq])
+        return pa::fail(PA_ERR_INVALID_ARG, "sequence %d holds %d tokens, not %d", seq,
+                        p->lens[seq], n_tokens);
+    std::vector<int32_t>& table = p->tables[seq];
+    const int64_t nb = ((int64_t)n_tokens + p->block_size - 1) / p->block_size;
+    int64_t need = 0;
+    for (int64_t i = 0; i < nb; ++i) need += p->ref[table[i]] > 1;
+    if (need > available(p))
+        return pa::fail(PA_ERR_OUT_OF_BLOCKS, "private copies of %lld blocks, %lld free",
+                        (long long)need, (long long)available(p));
+    if (need > 0 && (!cow_pairs_out || max_pairs < need))
+        return pa::fail(PA_ERR_INVALID_ARG, "%lld block copies, room for %d", (long long)need,
+                        cow_pairs_out ? max_pairs : 0);
+    for (int64_t i = 0; i < nb; ++i) {
+        const int32_t b = table[i];
+        if (p->ref[b] > 1) {
+            const int32_t fresh = take_block(p);
+            p->ref[b] -= 1;
+            p->ref[fresh] = 1;
+            table[i] = fresh;
+            cow_pairs_out[2 * *n_cow] = b;
+            cow_pairs_out[2 * *n_cow + 1] = fresh;
+            ++*n_cow;
+        } else if (p->pc_on) {
+            unregister_block(p, b);
+        }
+    }
+    if (n_tokens > 0) p->seq_known[seq] = 0;   // its blocks no longer hold a known prefix
+    return PA_OK;
+}
+
+// The tokens past n_tokens given up: their blocks lose this holder, in table
+// order, as pa_seq_free's do.
+extern "C" pa_status pa_seq_truncate(pa_pool* p, int32_t seq, int32_t n_tokens) {
+    if (!p) return pa::fail(PA_ERR_INVALID_ARG, "NULL pool");
+    if (pa_status s = check_seq(p, seq)) return s;
+    if (n_tokens < 0 || n_tokens > p->lens[seq])
+        return pa::fail(PA_ERR_INVALID_ARG, "sequence %d holds %d tokens, not %d", seq,
+                        p->lens[seq], n_tokens);
+    if (n_tokens == p->lens[seq]) return PA_OK;
+    std::vector<int32_t>& table = p->tables[seq];
+    const int64_t nb = ((int64_t)n_tokens + p->block_size - 1) / p->block_size;
+    for (int64_t i = nb; i < (int64_t)table.size(); ++i)
+        if (p->ref[table[i]] <= 0)
+            return pa::fail(PA_ERR_BAD_REFCOUNT, "refcount underflow on block %d", table[i]);
+    for (int64_t i = nb; i < (int64_t)table.size(); ++i) {
+        p->ref[table[i]] -= 1;
+        if (p->ref[table[i]] == 0) release_block(p, table[i]);
+    }
+    table.resize(nb);
+    p->lens[seq] = n_tokens;
+    // a block that is now partly filled will be written again by the next append: it
+    // must not be handed out for the prefix it was registered under
+    if (p->pc_on && n_tokens % p->block_size) unregister_block(p, table.back());
+    p->seq_known[seq] = 0;
+    return PA_OK;
+}
+
 extern "C" pa_status pa_pool_enable_prefix_cache(pa_pool* p, int32_t max_cached_blocks) {
     if (!p) return pa::fail(PA_ERR_INVALID_ARG, "NULL pool");
     if (max_cached_blocks < 0) return pa::fail(PA_ERR_INVALID_ARG, "max_cached_blocks < 0");

@@ -19,9 +19,10 @@ from typing import Dict, List, Optional, Sequence
 import numpy as np
 import torch
 
-from . import (BLOCK_SIZE, INT4_GROUP, Pool, append_kv, copy_blocks, decode, decode_shared_prefix,
-               decode_shared_prefix_workspace_size, decode_workspace_size,
-               zeroed_workspace)
+from . import (BLOCK_SIZE, INT4_GROUP, Pool, accumulate_weights,
+               accumulate_weights_workspace_size, append_kv, copy_blocks, decode,
+               decode_shared_prefix, decode_shared_prefix_workspace_size, decode_workspace_size,
+               evict_select, move_tokens, zeroed_workspace)
 
 KV_TORCH = {"f16": torch.float16, "bf16": torch.bfloat16, "int8": torch.int8,
             "fp8": torch.float8_e4m3fn, "int4": torch.uint8}
@@ -55,6 +56,17 @@ class SharedPrefix:
     max_group_q_len: int
     max_prefix_len: int
     workspace: torch.Tensor
+
+
+@dataclass
+class TokenWeights:
+    """What attention has given every cached token of a batch of sequences (one
+    row per sequence, in the order of `seqs`), by which tokens are evicted."""
+    seqs: List
+    scores: torch.Tensor              # fp32 [S, H_kv, width]
+    positions: torch.Tensor           # int32 [S, H_kv, width], -1: in text order
+    evicted: np.ndarray               # int64 [S]: tokens evicted so far
+    workspace: Optional[torch.Tensor] = None
 
 
 class PagedKVCache:
@@ -208,6 +220,65 @@ class PagedKVCache:
         if write:
             self.write_step(si)
         return self.attend_step(si, scale, partition_size)
+
+    # -- eviction by accumulated attention weight ---------------------------------
+    def track_weights(self, seqs: Sequence, width: int) -> TokenWeights:
+        """Empty weights for `seqs` (caller-chosen names), up to `width` tokens each."""
+        shape = (len(seqs), self.num_kv_heads, width)
+        return TokenWeights(list(seqs), torch.zeros(shape, device=self.device),
+                            torch.full(shape, -1, dtype=torch.int32, device=self.device),
+                            np.zeros(len(seqs), np.int64))
+
+    def accumulate_step(self, si: StepInputs, tw: TokenWeights, scale: float) -> None:
+        """Add the weights of the step's queries (rows of si and tw alike)."""
+        n = accumulate_weights_workspace_size(si.context_lens.shape[0], si.q.shape[0],
+                                              si.q.shape[1], self.num_kv_heads, self.head_dim,
+                                              si.max_q_len, si.max_context_len)
+        if tw.workspace is None or tw.workspace.numel() < n:
+            tw.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+        accumulate_weights(tw.scores, tw.scores, si.q, self.k, si.block_tables, si.context_lens,
+                           si.max_context_len, scale, si.query_start_loc, si.max_q_len,
+                           self.num_blocks, self.k_scale, self.k_zp, tw.workspace)
+
+    def evict(self, tw: TokenWeights, names: Dict, keep, num_sinks: int = 0,
+              num_recent: int = 0) -> None:
+        """Bring every sequence of tw down to `keep` tokens (an int, or one per
+        sequence; a shorter sequence stays as it is): blocks that will be
+        written become its own (copied where shared), the kept tokens are chosen
+        per KV head, their rows moved, and the freed blocks given back. Where the
+        pool cannot cover the copies it raises, and no token has gone."""
+        ids = [names[s] for s in tw.seqs]
+        lens = np.array([self.pool.seq_len(i) for i in ids], np.int64)
+        kept = np.minimum(np.broadcast_to(np.asarray(keep, np.int64), lens.shape), lens)
+        if (kept < 0).any():
+            raise ValueError("keep is negative")
+        if not (kept < lens).any():
+            return
+        for i, n, L in zip(ids, kept, lens):
+            if n < L:
+                # copied at once: a later sequence's error leaves a consistent cache
+                pairs = self.pool.seq_make_private(i, int(n))
+                if len(pairs):
+                    copy_blocks(self.k, self.v, torch.from_numpy(pairs).to(self.device),
+                                self.num_blocks, self.k_scale, self.v_scale, self.k_zp, self.v_zp)
+        width = int(lens.max())
+        bt, cl = self.pool.block_tables(ids, -(-width // BLOCK_SIZE))
+        dev = self.device
+
+        def to(a):
+            return torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(dev)
+
+        shape = tw.scores.shape[:2]
+        moves = torch.empty((*shape, max(1, width // 2), 2), dtype=torch.int32, device=dev)
+        counts = torch.empty(shape, dtype=torch.int32, device=dev)
+        lens_d = to(cl)
+        evict_select(moves, counts, tw.scores, tw.positions, tw.scores, tw.positions, lens_d,
+                     to(kept), to(lens + tw.evicted), width, num_sinks, num_recent)
+        move_tokens(self.k, self.v, to(bt), lens_d, moves, counts, width, self.num_blocks,
+                    self.k_scale, self.v_scale, self.k_zp, self.v_zp)
+        for i, n in zip(ids, kept):
+            self.pool.seq_truncate(i, int(n))
+        tw.evicted += lens - kept
 
     def capture(self, fn, *args) -> "torch.cuda.CUDAGraph":
         """Record fn(*args) (e.g. write_step or attend_step) in a CUDA graph;
