@@ -61,22 +61,74 @@ struct Row {
     }
     __device__ __forceinline__ uint32_t key(int j) const {
         const int q = position(j);
-        return q < sinks || q >= first_recent ? kProtected : score_key(w[j]);
+        const float x = w[j];   // loaded beside the position, not after it
+        return q < sinks || q >= first_recent ? kProtected : score_key(x);
     }
 };
 
+// Radix digits of a key, highest first: 11, 11 and 10 bits.
+constexpr int kDigits = 3;
+constexpr int kBins = 2048;
+__device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : d == 1 ? 10 : 0; }
+__device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
+
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kMaxCluster = 8;
+// shared memory of a CTA: one histogram a digit, then the keys of its slots
+constexpr int kHistBytes = kDigits * kBins * 4;
+constexpr int kMaxKeys = (200 * 1024 - kHistBytes) / 4;
 
-// A CTA a (KV head, sequence). The n-th largest key by four 8-bit radix steps,
-// then one walk that counts and one that emits, each warp over a contiguous
-// range of slots with ballots, so that lists come out in slot order.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of the cluster has arrived, and what each wrote before (shared or
+// global memory) is visible to all.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// the address of this CTA's shared variable in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(pa::smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ uint4 load_remote(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// A cluster of CTAs a (KV head, sequence), each CTA a contiguous part of the row
+// (CL CTAs; 1: no cluster). The n-th largest key by three radix steps over keys
+// held in shared memory (KEYS; computed again from the scores when a part is too
+// long for that), then one walk that counts and one that emits, every warp over
+// a contiguous range of slots with ballots, so that the lists come out in slot
+// order. Bound by latency: barriers, one read of scores and positions, and the
+// histogram's shared-memory atomics, which is why digits are 11 bits (the first
+// holds the exponent and two more bits, so that like-sized scores spread) and
+// why every warp finds the digit for itself from the chunks' sums.
+template <int CL, bool KEYS>
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const SelectParams p) {
-    __shared__ uint32_t hist[kSelectWarps][256];
-    __shared__ uint32_t digit_s, left_s;
-    __shared__ int gt[kSelectWarps], eq[kSelectWarps], gt_low[kSelectWarps], eq_low[kSelectWarps];
-    const int s = blockIdx.y, g = blockIdx.x;
+    extern __shared__ __align__(16) uint32_t smem[];
+    uint32_t* const hist = smem;                       // [kDigits][kBins]
+    uint32_t* const keys = smem + kDigits * kBins;
+    __shared__ __align__(16) int warp_counts[kSelectWarps][4];   // gt, eq, gt below n, eq below n
+    __shared__ __align__(16) int cta_counts[4];
+    __shared__ uint32_t chunk_sums[kDigits][kBins / 128];
+    static_assert(kBins / 128 <= kSelectWarps, "a warp a chunk");
+    const int s = blockIdx.z, g = blockIdx.y, part = CL == 1 ? 0 : (int)cluster_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pa::grid_dependents_launch();
+    for (int i = tid; i < kDigits * kBins / 4; i += kSelectThreads)
+        reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    pa::grid_dependency_wait();
     const int64_t sg = (int64_t)s * p.num_kv_heads + g;
     const int L = max(0, min(__ldg(p.context_lens + s), p.max_len));
     const int asked = __ldg(p.new_lens + s);
@@ -87,77 +139,149 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
     float* const w_out = p.scores_out + sg * p.stride;
     int32_t* const pos_out = p.positions_out + sg * p.stride;
     int2* const moves = p.moves + sg * p.max_moves;
+    // this CTA's slots, and this warp's of them
+    const int per = ((L + CL - 1) / CL + 31) / 32 * 32;
+    const int a0 = min(L, part * per), a1 = min(L, a0 + per);
+    const int seg = ((a1 - a0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int j0 = min(a1, a0 + warp * seg), j1 = min(a1, j0 + seg);
+    auto key_at = [&](int j) { return KEYS ? keys[j - a0] : row.key(j); };
+    auto sync = [&]() {
+        if constexpr (CL == 1) __syncthreads();
+        else cluster_sync();
+    };
 
     // key of the n-th token in the order, and how many tokens with that key stay
     uint32_t cut = 0, left = (uint32_t)n;
-    if (n > 0 && n < L) {
-#pragma unroll 1
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < kSelectWarps * 256; i += kSelectThreads) hist[0][i] = 0;
-            __syncthreads();
-            const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-            for (int j = tid; j < L; j += kSelectThreads) {
-                const uint32_t k = row.key(j);
-                if ((k & mask) == (cut & mask)) atomicAdd(&hist[warp][k >> shift & 255], 1u);
-            }
-            __syncthreads();
-            if (tid < 256) {
-                uint32_t t = 0;
-#pragma unroll
-                for (int i = 0; i < kSelectWarps; ++i) t += hist[i][tid];
-                hist[0][tid] = t;
-            }
-            __syncthreads();
-            if (warp == 0) {   // lane i: digits 255 - 8 i and the seven below
-                uint32_t mine = 0;
-                for (int d = 0; d < 8; ++d) mine += hist[0][255 - 8 * lane - d];
-                uint32_t upto = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += y;
-                }
-                uint32_t above = upto - mine;
-                if (above < left && left <= upto)
-                    for (int d = 0; d < 8; ++d) {
-                        const uint32_t h = hist[0][255 - 8 * lane - d];
-                        if (above + h >= left) {
-                            digit_s = 255 - 8 * lane - d;
-                            left_s = left - above;
-                            break;
-                        }
-                        above += h;
-                    }
-            }
-            __syncthreads();
-            cut |= digit_s << shift;
-            left = left_s;
+    const bool search = n > 0 && n < L;
+    __syncthreads();                                   // the histograms are zero
+    if (search || KEYS) {
+#pragma unroll 4
+        for (int b = j0; b < j1; b += 32) {            // warp-uniform
+            const int j = b + lane;
+            const uint32_t k = j < j1 ? row.key(j) : 0u;
+            if (KEYS && j < j1) keys[j - a0] = k;
+            // protected tokens come in long runs: one addition for a warp's
+            const uint32_t safe = __ballot_sync(0xffffffffu, j < j1 && k == kProtected);
+            if (j < j1 && (k != kProtected || lane == __ffs(safe) - 1))
+                atomicAdd(hist + (k >> 21), k == kProtected ? (uint32_t)__popc(safe) : 1u);
         }
     }
-    // n == L: all stay (every key is above no cut); n == 0: none does
+    if (search) {
+#pragma unroll 1
+        for (int d = 0; d < kDigits; ++d) {
+            uint32_t* const h = hist + d * kBins;
+            const int shift = digit_shift(d), bins = 1 << digit_bits(d);
+            if (d > 0) {
+                const uint32_t mask = 0xffffffffu << (shift + digit_bits(d));
+                for (int b = j0; b < j1; b += 32) {
+                    const int j = b + lane;
+                    const uint32_t k = j < j1 ? key_at(j) : 0u;
+                    const uint32_t safe = __ballot_sync(0xffffffffu, j < j1 && k == kProtected);
+                    if (j < j1 && (k & mask) == cut &&
+                        (k != kProtected || lane == __ffs(safe) - 1))
+                        atomicAdd(h + (k >> shift & (bins - 1)),
+                                  k == kProtected ? (uint32_t)__popc(safe) : 1u);
+                }
+            }
+            sync();
+            if constexpr (CL > 1) {
+                // the cluster's sum, in registers until every CTA has read the parts
+                const int vecs = bins / 4;
+                uint4 t = make_uint4(0u, 0u, 0u, 0u);
+                if (tid < vecs)
+#pragma unroll
+                    for (int c = 0; c < CL; ++c) {
+                        const uint4 v = load_remote(remote(h + 4 * tid, c));
+                        t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+                    }
+                cluster_sync();
+                if (tid < vecs) reinterpret_cast<uint4*>(h)[tid] = t;
+                __syncthreads();
+            }
+            // a warp sums a chunk of 128 bins (chunk 0 the highest), then every warp finds the
+            // chunk of the n-th key and the bin in it
+            const int chunks = bins / 128;
+            if (warp < chunks) {
+                const uint4 v = *reinterpret_cast<const uint4*>(h + bins - 128 * (warp + 1) + 4 * lane);
+                const uint32_t sum = __reduce_add_sync(0xffffffffu, v.x + v.y + v.z + v.w);
+                if (lane == 0) chunk_sums[d][warp] = sum;
+            }
+            __syncthreads();
+            uint32_t upto = lane < chunks ? chunk_sums[d][lane] : 0u;
+            const uint32_t own = upto;
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            const int chunk = __ffs(__ballot_sync(0xffffffffu, lane < chunks && upto >= left)) - 1;
+            const uint32_t above = __shfl_sync(0xffffffffu, upto - own, chunk);
+            const int top = bins - 128 * chunk - 4 * lane;   // the lane's bins: top - 1 .. top - 4
+            const uint4 v = *reinterpret_cast<const uint4*>(h + top - 4);
+            uint32_t run = v.x + v.y + v.z + v.w;
+            const uint32_t mine = run;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += y;
+            }
+            run += above;                              // keys in the lane's bins and higher ones
+            const int owner = __ffs(__ballot_sync(0xffffffffu, run >= left)) - 1;
+            uint32_t before = run - mine;
+            int bin = top - 1;
+            if (before + v.w < left) {
+                before += v.w, --bin;
+                if (before + v.z < left) {
+                    before += v.z, --bin;
+                    if (before + v.y < left) before += v.y, --bin;
+                }
+            }
+            left -= __shfl_sync(0xffffffffu, before, owner);
+            cut |= (uint32_t)__shfl_sync(0xffffffffu, bin, owner) << shift;
+        }
+    } else {
+        __syncthreads();
+    }
+    // n == L: all stay; n == 0: none does
     const bool all = n == L, none = n == 0;
     auto larger = [&](uint32_t k) { return all || (!none && k > cut); };
     auto equal = [&](uint32_t k) { return !all && !none && k == cut; };
 
-    const int seg = ((L + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-    const int j0 = min(L, warp * seg), j1 = min(L, j0 + seg);
     int c_gt = 0, c_eq = 0, c_gt_low = 0, c_eq_low = 0;
     for (int b = j0; b < j1; b += 32) {
         const int j = b + lane;
-        const uint32_t k = j < j1 ? row.key(j) : 0u;
+        const uint32_t k = j < j1 ? key_at(j) : 0u;
         const bool is_gt = j < j1 && larger(k), is_eq = j < j1 && equal(k);
-        c_gt += __popc(__ballot_sync(0xffffffffu, is_gt));
-        c_eq += __popc(__ballot_sync(0xffffffffu, is_eq));
-        c_gt_low += __popc(__ballot_sync(0xffffffffu, is_gt && j < n));
-        c_eq_low += __popc(__ballot_sync(0xffffffffu, is_eq && j < n));
+        const uint32_t gts = __ballot_sync(0xffffffffu, is_gt);
+        const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
+        const uint32_t low = n <= b ? 0u : n - b >= 32 ? 0xffffffffu : (1u << (n - b)) - 1u;
+        c_gt += __popc(gts);
+        c_eq += __popc(eqs);
+        c_gt_low += __popc(gts & low);
+        c_eq_low += __popc(eqs & low);
     }
-    if (lane == 0) gt[warp] = c_gt, eq[warp] = c_eq, gt_low[warp] = c_gt_low, eq_low[warp] = c_eq_low;
+    if (lane == 0)
+        *reinterpret_cast<int4*>(warp_counts[warp]) = make_int4(c_gt, c_eq, c_gt_low, c_eq_low);
     __syncthreads();
-    int eq_before = 0, gt_before = 0, low = 0, ties_low = 0;
+    int gt_before = 0, eq_before = 0, low = 0, ties_low = 0, gt_all = 0, eq_all = 0;
+#pragma unroll
     for (int i = 0; i < kSelectWarps; ++i) {
-        if (i < warp) gt_before += gt[i], eq_before += eq[i];
-        low += gt_low[i];
-        ties_low += eq_low[i];
+        const int4 c = *reinterpret_cast<const int4*>(warp_counts[i]);
+        if (i < warp) gt_before += c.x, eq_before += c.y;
+        gt_all += c.x, eq_all += c.y;
+        low += c.z, ties_low += c.w;
+    }
+    if constexpr (CL > 1) {
+        if (tid == 0)
+            *reinterpret_cast<int4*>(cta_counts) = make_int4(gt_all, eq_all, low, ties_low);
+        cluster_sync();
+        low = ties_low = 0;
+#pragma unroll
+        for (int c = 0; c < CL; ++c) {
+            const uint4 v = load_remote(remote(cta_counts, c));
+            if (c < part) gt_before += (int)v.x, eq_before += (int)v.y;
+            low += (int)v.z, ties_low += (int)v.w;
+        }
     }
     const int ties = (int)left;                       // tokens of key `cut` that stay
     const int kept_low = low + min(ties, ties_low);   // kept tokens below n
@@ -165,7 +289,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
     int kept = gt_before + min(ties, eq_before);      // kept tokens before the warp's next slot
     for (int b = j0; b < j1; b += 32) {
         const int j = b + lane;
-        const uint32_t k = j < j1 ? row.key(j) : 0u;
+        const uint32_t k = j < j1 ? key_at(j) : 0u;
         const bool is_eq = j < j1 && equal(k);
         const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
         const uint32_t below = (1u << lane) - 1u;
@@ -185,15 +309,15 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
         eq_before += __popc(eqs);
         kept += __popc(keeps);
     }
-    __syncthreads();
-    for (int i = tid; i < count; i += kSelectThreads) {
-        const int2 m = moves[i];
+    sync();                                            // the list is whole
+    for (int i = part * kSelectThreads + tid; i < count; i += CL * kSelectThreads) {
+        const int2 m = __ldcg(moves + i);              // written by other CTAs of the cluster
         w_out[m.y] = row.w[m.x];
         pos_out[m.y] = row.position(m.x);
     }
-    if (tid == 0) p.move_counts[sg] = count;
-    __syncthreads();
-    for (int j = n + tid; j < L; j += kSelectThreads) {
+    if (part == 0 && tid == 0) p.move_counts[sg] = count;
+    sync();                                            // entries from n on are read no more
+    for (int j = max(n, a0) + tid; j < a1; j += kSelectThreads) {
         w_out[j] = 0.f;
         pos_out[j] = -1;
     }
@@ -209,46 +333,144 @@ struct MoveParams {
     const int32_t* move_counts;
     unsigned int* err;
     int max_moves, num_kv_heads, max_len, num_blocks, max_blocks;
-    int row_vecs;             // 16-byte vectors of a row
-    int groups;               // scales of a row
 };
 
 constexpr int kMoveThreads = 256;
+constexpr int kMoveBatch = 4;
 
 // Grid: (parts, KV head, sequence); the parts stride over the row's moves. A
-// thread copies one 16-byte vector of a K or V row, or one scale and zero point.
+// thread copies one 16-byte vector of a K or V row, or one scale and zero point,
+// of kMoveBatch moves at a time: all their loads are on the way before the first
+// store (no destination is a source, so the order is free). The lists, the table
+// entries and the rows are three dependent reads: with one copy a thread the
+// kernel waited on them (16 prompts to 1024 of up to 8192 tokens: 23.7 us).
+template <int VECS, int GROUPS>   // 16-byte vectors and scales of a row
 __global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const MoveParams p) {
+    constexpr int kPieces = 2 * VECS + 2 * GROUPS;
+    pa::grid_dependency_wait();
     const int s = blockIdx.z, g = blockIdx.y;
     const int64_t sg = (int64_t)s * p.num_kv_heads + g;
     const int L = max(0, min(__ldg(p.context_lens + s), p.max_len));
     const int count = min(__ldg(p.move_counts + sg), p.max_moves);
-    const int vecs = 2 * p.row_vecs, pieces = vecs + 2 * p.groups;
     const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
-    const int64_t items = (int64_t)count * pieces;
-    for (int64_t i = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; i < items;
-         i += (int64_t)gridDim.x * kMoveThreads) {
-        const int m = (int)(i / pieces), piece = (int)(i - (int64_t)m * pieces);
-        const int2 mv = __ldg(p.moves + sg * p.max_moves + m);
-        if (mv.x < 0 || mv.x >= L || mv.y < 0 || mv.y >= L) {
-            if (p.err) atomicOr(p.err, pa::ERR_BAD_SLOT);
-            continue;
+    const int64_t items = (int64_t)count * kPieces;
+    const int64_t step = (int64_t)gridDim.x * kMoveThreads;
+    for (int64_t i0 = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; i0 < items;
+         i0 += kMoveBatch * step) {
+        int2 mv[kMoveBatch];
+        int bs[kMoveBatch], bd[kMoveBatch];
+#pragma unroll
+        for (int k = 0; k < kMoveBatch; ++k) {
+            const int64_t i = i0 + k * step;
+            mv[k] = make_int2(0, 0);
+            if (i < items) mv[k] = __ldg(p.moves + sg * p.max_moves + i / kPieces);
         }
-        const int bs = __ldg(table + mv.x / kBS), bd = __ldg(table + mv.y / kBS);
-        if (bs < 0 || bs >= p.num_blocks || bd < 0 || bd >= p.num_blocks) {
-            if (p.err) atomicOr(p.err, pa::ERR_BAD_BLOCK);
-            continue;
+#pragma unroll
+        for (int k = 0; k < kMoveBatch; ++k) {
+            const bool in = mv[k].x >= 0 && mv[k].x < L && mv[k].y >= 0 && mv[k].y < L;
+            bs[k] = bd[k] = -1;
+            if (i0 + k * step >= items) continue;
+            if (!in) {
+                if (p.err) atomicOr(p.err, pa::ERR_BAD_SLOT);
+                continue;
+            }
+            bs[k] = __ldg(table + mv[k].x / kBS);
+            bd[k] = __ldg(table + mv[k].y / kBS);
+            if (bs[k] < 0 || bs[k] >= p.num_blocks || bd[k] < 0 || bd[k] >= p.num_blocks) {
+                if (p.err) atomicOr(p.err, pa::ERR_BAD_BLOCK);
+                bs[k] = -1;
+            }
         }
-        const int64_t src = ((int64_t)bs * p.num_kv_heads + g) * kBS + mv.x % kBS;
-        const int64_t dst = ((int64_t)bd * p.num_kv_heads + g) * kBS + mv.y % kBS;
-        if (piece < vecs) {
-            const int v = piece >= p.row_vecs, c = piece - v * p.row_vecs;
-            uint4* code = p.code[v];
-            code[dst * p.row_vecs + c] = code[src * p.row_vecs + c];
-        } else {
-            const int v = piece - vecs >= p.groups, c = piece - vecs - v * p.groups;
-            p.scale[v][dst * p.groups + c] = p.scale[v][src * p.groups + c];
-            p.zp[v][dst * p.groups + c] = p.zp[v][src * p.groups + c];
+        uint4 data[kMoveBatch];
+#pragma unroll
+        for (int k = 0; k < kMoveBatch; ++k) {
+            if (bs[k] < 0) continue;
+            const int piece = (int)((i0 + k * step) % kPieces);
+            const int64_t src = ((int64_t)bs[k] * p.num_kv_heads + g) * kBS + mv[k].x % kBS;
+            if (GROUPS == 0 || piece < 2 * VECS) {
+                const int v = piece >= VECS;
+                data[k] = __ldcs(p.code[v] + src * VECS + (piece - v * VECS));
+            } else if constexpr (GROUPS > 0) {
+                const int c = piece - 2 * VECS, v = c >= GROUPS;
+                data[k].x = __float_as_uint(p.scale[v][src * GROUPS + (c - v * GROUPS)]);
+                data[k].y = (uint8_t)p.zp[v][src * GROUPS + (c - v * GROUPS)];
+            }
         }
+#pragma unroll
+        for (int k = 0; k < kMoveBatch; ++k) {
+            if (bs[k] < 0) continue;
+            const int piece = (int)((i0 + k * step) % kPieces);
+            const int64_t dst = ((int64_t)bd[k] * p.num_kv_heads + g) * kBS + mv[k].y % kBS;
+            if (GROUPS == 0 || piece < 2 * VECS) {
+                const int v = piece >= VECS;
+                p.code[v][dst * VECS + (piece - v * VECS)] = data[k];
+            } else if constexpr (GROUPS > 0) {
+                const int c = piece - 2 * VECS, v = c >= GROUPS;
+                p.scale[v][dst * GROUPS + (c - v * GROUPS)] = __uint_as_float(data[k].x);
+                p.zp[v][dst * GROUPS + (c - v * GROUPS)] = (int8_t)data[k].y;
+            }
+        }
+    }
+}
+
+template <int VECS, int GROUPS>
+pa_status launch_move(const MoveParams& p, int num_seqs, cudaStream_t st) {
+    // about 8 CTAs a SM over the whole call, but no more than the moves could use
+    const int64_t rows = (int64_t)num_seqs * p.num_kv_heads;
+    const int64_t could = ((int64_t)p.max_moves * (2 * VECS + 2 * GROUPS) +
+                           kMoveBatch * kMoveThreads - 1) / (kMoveBatch * kMoveThreads);
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(could, (152 * 8 + rows - 1) / rows));
+    return pa::cuda_status(pa::launch_pdl(move_tokens_kernel<VECS, GROUPS>,
+                                          dim3((unsigned)parts, p.num_kv_heads, num_seqs),
+                                          dim3(kMoveThreads), 0, st, p),
+                           "move_tokens launch");
+}
+
+template <int CL, bool KEYS>
+pa_status launch_select_as(const SelectParams& p, int num_seqs, int keys, cudaStream_t st) {
+    auto kern = evict_select_kernel<CL, KEYS>;
+    static bool attr_set = false;   // per instantiation; benign race (idempotent)
+    if (!attr_set) {
+        if (pa_status s = pa::cuda_status(
+                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kHistBytes + 4 * kMaxKeys),
+                "evict_select: set shared memory size"))
+            return s;
+        attr_set = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CL, p.num_kv_heads, num_seqs);
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = kHistBytes + (KEYS ? 4 * keys : 0);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CL;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CL == 1 ? 1 : 2;
+    return pa::cuda_status(cudaLaunchKernelEx(&cfg, kern, p), "evict_select launch");
+}
+
+// How many CTAs share a row: more while the rows alone leave SMs idle and a part
+// stays worth its barriers (2048 slots, 4 a thread), or while a part's keys do not
+// fit shared memory.
+pa_status launch_select(const SelectParams& p, int num_seqs, cudaStream_t st) {
+    const int64_t rows = (int64_t)num_seqs * p.num_kv_heads;
+    int cl = 1;
+    while (cl < kMaxCluster && ((rows * cl < 152 && p.max_len / cl > 2048) ||
+                                p.max_len / cl + 32 > kMaxKeys))
+        cl *= 2;
+    const int keys = ((p.max_len + cl - 1) / cl + 31) / 32 * 32;
+    if (keys > kMaxKeys) return launch_select_as<kMaxCluster, false>(p, num_seqs, keys, st);
+    switch (cl) {
+        case 1: return launch_select_as<1, true>(p, num_seqs, keys, st);
+        case 2: return launch_select_as<2, true>(p, num_seqs, keys, st);
+        case 4: return launch_select_as<4, true>(p, num_seqs, keys, st);
+        default: return launch_select_as<8, true>(p, num_seqs, keys, st);
     }
 }
 
@@ -279,8 +501,8 @@ extern "C" pa_status pa_evict_select(int32_t* moves, int32_t max_moves, int32_t*
                     std::max(1, max_context_len / 2));
     if (num_sinks < 0 || num_recent < 0)
         return fail(PA_ERR_INVALID_ARG, "num_sinks %d, num_recent %d", num_sinks, num_recent);
-    if (num_seqs > 65535)
-        return fail(PA_ERR_UNSUPPORTED, "more than 65535 sequences in one call");
+    if (num_seqs > 65535 || num_kv_heads > 65535)
+        return fail(PA_ERR_UNSUPPORTED, "more than 65535 sequences or KV heads in one call");
     if ((uintptr_t)moves % 8)
         return fail(PA_ERR_INVALID_ARG, "moves must be 8-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
@@ -304,8 +526,7 @@ extern "C" pa_status pa_evict_select(int32_t* moves, int32_t max_moves, int32_t*
     p.max_len = max_context_len;
     p.sinks = num_sinks;
     p.recent = num_recent;
-    evict_select_kernel<<<dim3(num_kv_heads, num_seqs), kSelectThreads, 0, st>>>(p);
-    return pa::cuda_status(cudaGetLastError(), "evict_select launch");
+    return launch_select(p, num_seqs, st);
 }
 
 extern "C" pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype kv_dtype,
@@ -340,8 +561,8 @@ extern "C" pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype kv_dt
     MoveParams p{};
     p.code[0] = static_cast<uint4*>(k_cache);
     p.code[1] = static_cast<uint4*>(v_cache);
-    p.groups = pa::row_groups(kv_dtype, head_dim);
-    if (p.groups) {
+    const int groups = pa::row_groups(kv_dtype, head_dim);
+    if (groups) {
         p.scale[0] = k_scale, p.scale[1] = v_scale;
         p.zp[0] = k_zp, p.zp[1] = v_zp;
     }
@@ -355,12 +576,15 @@ extern "C" pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype kv_dt
     p.max_len = max_context_len;
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks_per_seq;
-    p.row_vecs = pa::cache_row_bytes(kv_dtype, head_dim) / 16;
-    // about 16 CTAs a SM over the whole call, but no more than the moves could use
-    const int64_t rows = (int64_t)num_seqs * num_kv_heads;
-    const int64_t could = ((int64_t)max_moves * (2 * p.row_vecs + 2 * p.groups) + kMoveThreads - 1) /
-                          kMoveThreads;
-    const int64_t parts = std::max<int64_t>(1, std::min(could, 152 * 16 / rows));
-    move_tokens_kernel<<<dim3((unsigned)parts, num_kv_heads, num_seqs), kMoveThreads, 0, st>>>(p);
-    return pa::cuda_status(cudaGetLastError(), "move_tokens launch");
+    const bool wide = head_dim == 128;
+    switch (kv_dtype) {
+        case PA_INT8:
+            return wide ? launch_move<8, 1>(p, num_seqs, st) : launch_move<4, 1>(p, num_seqs, st);
+        case PA_INT4:
+            return wide ? launch_move<4, 2>(p, num_seqs, st) : launch_move<2, 1>(p, num_seqs, st);
+        case PA_FP8_E4M3:
+            return wide ? launch_move<8, 0>(p, num_seqs, st) : launch_move<4, 0>(p, num_seqs, st);
+        default:
+            return wide ? launch_move<16, 0>(p, num_seqs, st) : launch_move<8, 0>(p, num_seqs, st);
+    }
 }

@@ -14,6 +14,7 @@
 #include <cuda_fp8.h>
 
 #include "pa_internal.h"
+#include "ptx.cuh"
 
 namespace {
 
@@ -184,27 +185,29 @@ __global__ void append_kv_fp8_kernel(const T* __restrict__ key, const T* __restr
 }
 
 // INT4 append: the formula of the INT8 path with 16 unsigned codes and one
-// (scale, zero point) per 64 elements. A thread holds 8 consecutive elements
-// of a K row and of the same V row (16-byte loads, 4-byte code stores), 8
-// threads a group; the range is reduced over them with shuffles. Moves 2 bytes
-// in and 0.58 bytes out an element, so it is bound by memory at prefill sizes.
-template <typename T>
-__global__ void append_kv_int4_kernel(const T* __restrict__ key, const T* __restrict__ value,
-                                      uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
-                                      float* __restrict__ k_scale, float* __restrict__ v_scale,
-                                      int8_t* __restrict__ k_zp, int8_t* __restrict__ v_zp,
-                                      const int64_t* __restrict__ slots, int num_tokens,
-                                      int num_kv_heads, int head_dim, int64_t num_slots,
-                                      unsigned int* err) {
-    const int per_row = head_dim / 8, groups = head_dim / PA_INT4_GROUP;
-    const int64_t total = (int64_t)num_tokens * num_kv_heads * per_row;   // a multiple of 8
-    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-    // the 8 threads of a group are all in range or all out of it, and hold one token
+// (scale, zero point) per 64 elements. A thread holds 8 consecutive elements of
+// a K row and of the same V row (16-byte loads, 4-byte code stores), 8 threads a
+// group; the range is reduced over them with shuffles. 2 bytes in and 0.58 out
+// an element: bound by memory once nothing else is in the way, so the rows are
+// asked for before the slot is known, indexes are 32 bits wide (their 64-bit
+// divisions alone cost a third of the kernel) and codes come without divisions.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) append_kv_int4_kernel(
+    const T* __restrict__ key, const T* __restrict__ value, uint8_t* __restrict__ k_cache,
+    uint8_t* __restrict__ v_cache, float* __restrict__ k_scale, float* __restrict__ v_scale,
+    int8_t* __restrict__ k_zp, int8_t* __restrict__ v_zp, const int64_t* __restrict__ slots,
+    uint32_t total, uint32_t num_kv_heads, int64_t num_slots, unsigned int* err) {
+    constexpr int kPerRow = D / 8, kGroups = D / PA_INT4_GROUP;
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+    // total is a multiple of 8: the 8 threads of a group are all in range or all out of it,
+    // and hold one token
+    pa::grid_dependency_wait();
     if (i >= total) return;
     const unsigned int peers = 0xffu << (threadIdx.x & 24);
-    const int64_t tg = i / per_row;
-    const int c = (int)(i - tg * per_row);
-    const int64_t t = tg / num_kv_heads, g = tg - t * num_kv_heads;
+    const uint4 raw[2] = {__ldcs(reinterpret_cast<const uint4*>(key) + i),
+                          __ldcs(reinterpret_cast<const uint4*>(value) + i)};
+    const uint32_t tg = i / kPerRow, c = i % kPerRow;
+    const uint32_t t = tg / num_kv_heads, g = tg - t * num_kv_heads;
     const int64_t slot = __ldg(slots + t);
     if (slot < 0) return;
     if (slot >= num_slots) {
@@ -212,8 +215,6 @@ __global__ void append_kv_int4_kernel(const T* __restrict__ key, const T* __rest
         return;
     }
     const int64_t row = ((slot / kBlock) * num_kv_heads + g) * kBlock + slot % kBlock;
-    const uint4 raw[2] = {__ldg(reinterpret_cast<const uint4*>(key) + i),
-                          __ldg(reinterpret_cast<const uint4*>(value) + i)};
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const T* h = reinterpret_cast<const T*>(&raw[which]);
@@ -233,102 +234,118 @@ __global__ void append_kv_int4_kernel(const T* __restrict__ key, const T* __rest
         }
         float scale = __fdiv_rn(__fsub_rn(mx, mn), 15.0f);
         if (scale == 0.0f) scale = 1.0f;
-        int zp = (int)-rintf(__fdiv_rn(mn, scale));
-        zp = zp < 0 ? 0 : (zp > 15 ? 15 : zp);
+        // rint(x / scale) by a product with the reciprocal: |x / scale| <= 15, so the product is
+        // within 15 * 2^-22 < 4e-6 of the fp32 quotient, and rounds to the same integer unless
+        // it is that near a tie (or the reciprocal is not a normal number). Then divide.
+        constexpr float kRound = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer
+        const float inv = __frcp_rn(scale);
+        int q[9];                               // the last: the zero point's quotient
+        float far = 0.0f;                       // the largest distance from an integer
+#pragma unroll
+        for (int e = 0; e < 9; ++e) {
+            const float v = e < 8 ? x[e & 7] : mn;
+            const float y = __fmaf_rn(v, inv, kRound);
+            q[e] = __float_as_int(y) - __float_as_int(kRound);
+            far = fmaxf(far, fabsf(__fmaf_rn(v, inv, __fsub_rn(kRound, y))));
+        }
+        if (!(far < 0.49999f) || !(scale > 1e-30f && scale < 1e30f)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = (int)rintf(__fdiv_rn(x[e], scale));
+            q[8] = (int)rintf(__fdiv_rn(mn, scale));
+        }
+        const int zp = q[8] > 0 ? 0 : (q[8] < -15 ? 15 : -q[8]);
         uint32_t word = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            int q = (int)rintf(__fdiv_rn(x[e], scale)) + zp;
-            q = q < 0 ? 0 : (q > 15 ? 15 : q);
-            word |= (uint32_t)q << (4 * e);
+            const int code = q[e] + zp;
+            word |= (uint32_t)(code < 0 ? 0 : (code > 15 ? 15 : code)) << (4 * e);
         }
-        reinterpret_cast<uint32_t*>(which ? v_cache : k_cache)[row * per_row + c] = word;
+        reinterpret_cast<uint32_t*>(which ? v_cache : k_cache)[row * kPerRow + c] = word;
         if ((c & 7) == 0) {
-            (which ? v_scale : k_scale)[row * groups + c / 8] = scale;
-            (which ? v_zp : k_zp)[row * groups + c / 8] = (int8_t)zp;
+            (which ? v_scale : k_scale)[row * kGroups + c / 8] = scale;
+            (which ? v_zp : k_zp)[row * kGroups + c / 8] = (int8_t)zp;
         }
     }
 }
 
-// 8 consecutive cached elements (elements 8c .. 8c + 7 of cached row `row`,
-// KV head g) as fp32; a code's value is one fp32 product.
-template <int KV>
-__device__ __forceinline__ void load8(float (&x)[8], const void* cache, const float* scale,
-                                      const int8_t* zp, int64_t row, int64_t g, int c,
-                                      int head_dim) {
-    const int per_row = head_dim / 8;
-    if constexpr (KV == PA_F16 || KV == PA_BF16) {
-        const uint4 raw = __ldg(static_cast<const uint4*>(cache) + row * per_row + c);
+// 8 consecutive cached elements (elements 8c .. 8c + 7 of cached row `row`) as
+// stored, with what their codes are scaled by.
+template <int KV, int D>
+struct Cached8 {
+    uint4 raw;
+    float scale;
+    int zp;
+    __device__ __forceinline__ void load(const void* cache, const float* scales,
+                                         const int8_t* zps, int64_t row, uint32_t g, uint32_t c) {
+        constexpr int kPerRow = D / 8;
+        if constexpr (KV == PA_F16 || KV == PA_BF16) {
+            raw = __ldg(static_cast<const uint4*>(cache) + row * kPerRow + c);
+        } else if constexpr (KV == PA_INT4) {
+            raw.x = __ldg(static_cast<const uint32_t*>(cache) + row * kPerRow + c);
+            scale = __ldg(scales + row * (D / PA_INT4_GROUP) + c / 8);
+            zp = __ldg(zps + row * (D / PA_INT4_GROUP) + c / 8);
+        } else {
+            const uint2 u = __ldg(static_cast<const uint2*>(cache) + row * kPerRow + c);
+            raw.x = u.x, raw.y = u.y;
+            scale = __ldg(scales + (KV == PA_INT8 ? row : (int64_t)g));
+            if constexpr (KV == PA_INT8) zp = __ldg(zps + row);
+        }
+    }
+    // a code's value is one fp32 product
+    __device__ __forceinline__ float value(int e) const {
+        if constexpr (KV == PA_F16)
+            return __half2float(reinterpret_cast<const __half*>(&raw)[e]);
+        else if constexpr (KV == PA_BF16)
+            return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(&raw)[e]);
+        else if constexpr (KV == PA_INT4)
+            return __fmul_rn((float)((int)(raw.x >> (4 * e) & 15u) - zp), scale);
+        else if constexpr (KV == PA_INT8)
+            return __fmul_rn((float)((int)reinterpret_cast<const int8_t*>(&raw)[e] - zp), scale);
+        else
+            return __fmul_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(
+                                 reinterpret_cast<const uint8_t*>(&raw)[e], __NV_E4M3))),
+                             scale);
+    }
+};
+
+template <int KV, int D>
+__device__ __forceinline__ void store8(float* dst, const Cached8<KV, D>& x) {
+    __stcs(reinterpret_cast<float4*>(dst),
+           make_float4(x.value(0), x.value(1), x.value(2), x.value(3)));
+    __stcs(reinterpret_cast<float4*>(dst) + 1,
+           make_float4(x.value(4), x.value(5), x.value(6), x.value(7)));
+}
+template <int KV, int D, typename T>
+__device__ __forceinline__ void store8(T* dst, const Cached8<KV, D>& x) {
+    constexpr bool half = std::is_same<T, __half>::value;
+    uint4 out = x.raw;   // a 16-bit cache read as its own type
+    if constexpr (KV != (half ? PA_F16 : PA_BF16)) {
+        T* h = reinterpret_cast<T*>(&out);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if constexpr (KV == PA_F16)
-                x[e] = __half2float(reinterpret_cast<const __half*>(&raw)[e]);
-            else
-                x[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(&raw)[e]);
-        }
-    } else if constexpr (KV == PA_INT4) {
-        const uint32_t w = __ldg(static_cast<const uint32_t*>(cache) + row * per_row + c);
-        const int64_t at = row * (head_dim / PA_INT4_GROUP) + c / 8;
-        const float s = __ldg(scale + at);
-        const int z = __ldg(zp + at);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __fmul_rn((float)((int)(w >> (4 * e) & 15u) - z), s);
-    } else {
-        const uint2 raw = __ldg(static_cast<const uint2*>(cache) + row * per_row + c);
-        if constexpr (KV == PA_INT8) {
-            const float s = __ldg(scale + row);
-            const int z = __ldg(zp + row);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] = __fmul_rn((float)((int)reinterpret_cast<const int8_t*>(&raw)[e] - z), s);
-        } else {
-            const float s = __ldg(scale + g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const __half_raw v = __nv_cvt_fp8_to_halfraw(
-                    reinterpret_cast<const uint8_t*>(&raw)[e], __NV_E4M3);
-                x[e] = __fmul_rn(__half2float(__half(v)), s);
-            }
+            if constexpr (half) h[e] = __float2half_rn(x.value(e));
+            else h[e] = __float2bfloat16_rn(x.value(e));
         }
     }
-}
-
-__device__ __forceinline__ void store8(float* dst, const float (&x)[8]) {
-    reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float (&x)[8]) {
-    uint4 raw;
-    T* h = reinterpret_cast<T*>(&raw);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if constexpr (std::is_same<T, __half>::value) h[e] = __float2half_rn(x[e]);
-        else h[e] = __float2bfloat16_rn(x[e]);
-    }
-    *reinterpret_cast<uint4*>(dst) = raw;
+    __stcs(reinterpret_cast<uint4*>(dst), out);
 }
 
 // Cached rows read back through a slot mapping: the inverse of append, each
 // row at the values the cache holds. One thread per 8 elements of a K row and
 // of the same V row. Bound by memory: the cache's bytes in, the rows out.
-template <int KV, typename T>
-__global__ void gather_kv_kernel(T* __restrict__ key, T* __restrict__ value,
-                                 const void* __restrict__ k_cache,
-                                 const void* __restrict__ v_cache,
-                                 const float* __restrict__ k_scale,
-                                 const float* __restrict__ v_scale,
-                                 const int8_t* __restrict__ k_zp, const int8_t* __restrict__ v_zp,
-                                 const int64_t* __restrict__ slots, int num_tokens,
-                                 int num_kv_heads, int head_dim, int64_t num_slots,
-                                 unsigned int* err) {
-    const int per_row = head_dim / 8;
-    const int64_t total = (int64_t)num_tokens * num_kv_heads * per_row;
-    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+template <int KV, int D, typename T>
+__global__ void __launch_bounds__(256) gather_kv_kernel(
+    T* __restrict__ key, T* __restrict__ value, const void* __restrict__ k_cache,
+    const void* __restrict__ v_cache, const float* __restrict__ k_scale,
+    const float* __restrict__ v_scale, const int8_t* __restrict__ k_zp,
+    const int8_t* __restrict__ v_zp, const int64_t* __restrict__ slots, uint32_t total,
+    uint32_t num_kv_heads, int64_t num_slots, unsigned int* err) {
+    constexpr int kPerRow = D / 8;
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+    pa::grid_dependency_wait();
     if (i >= total) return;
-    const int64_t tg = i / per_row;
-    const int c = (int)(i - tg * per_row);
-    const int64_t t = tg / num_kv_heads, g = tg - t * num_kv_heads;
+    const uint32_t tg = i / kPerRow, c = i % kPerRow;
+    const uint32_t t = tg / num_kv_heads, g = tg - t * num_kv_heads;
     const int64_t slot = __ldg(slots + t);
     if (slot < 0) return;
     if (slot >= num_slots) {
@@ -336,11 +353,11 @@ __global__ void gather_kv_kernel(T* __restrict__ key, T* __restrict__ value,
         return;
     }
     const int64_t row = ((slot / kBlock) * num_kv_heads + g) * kBlock + slot % kBlock;
-    float a[8], b[8];
-    load8<KV>(a, k_cache, k_scale, k_zp, row, g, c, head_dim);
-    load8<KV>(b, v_cache, v_scale, v_zp, row, g, c, head_dim);
-    store8(key + i * 8, a);
-    store8(value + i * 8, b);
+    Cached8<KV, D> a, b;
+    a.load(k_cache, k_scale, k_zp, row, g, c);
+    b.load(v_cache, v_scale, v_zp, row, g, c);
+    store8(key + (int64_t)i * 8, a);
+    store8(value + (int64_t)i * 8, b);
 }
 
 struct CopyParams {
@@ -374,17 +391,21 @@ pa_status launch_append_kv(const AppendArgs& a) {
     const int64_t num_slots = (int64_t)a.num_blocks * a.block_size;
     if (a.kv_dtype == PA_INT4) {
         const int64_t total = (int64_t)a.num_tokens * a.num_kv_heads * (a.head_dim / 8);
-        const int threads = 256;
-        const int64_t grid = (total + threads - 1) / threads;
-        if (grid > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "too many tokens for one launch");
-#define PA_LAUNCH_Q4(T)                                                                        \
-    append_kv_int4_kernel<T><<<(unsigned)grid, threads, 0, a.stream>>>(                        \
-        static_cast<const T*>(a.key), static_cast<const T*>(a.value),                          \
-        static_cast<uint8_t*>(a.k_cache), static_cast<uint8_t*>(a.v_cache), a.k_scale,         \
-        a.v_scale, a.k_zp, a.v_zp, a.slots, a.num_tokens, a.num_kv_heads, a.head_dim,          \
-        num_slots, err)
-        if (a.src_dtype == PA_BF16) PA_LAUNCH_Q4(__nv_bfloat16);
-        else PA_LAUNCH_Q4(__half);
+        if (total > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "too many tokens for one launch");
+#define PA_LAUNCH_Q4(T, D)                                                                     \
+    return cuda_status(                                                                        \
+        launch_pdl(append_kv_int4_kernel<T, D>, dim3((unsigned)((total + 255) / 256)),         \
+                   dim3(256), 0, a.stream, static_cast<const T*>(a.key),                       \
+                   static_cast<const T*>(a.value), static_cast<uint8_t*>(a.k_cache),           \
+                   static_cast<uint8_t*>(a.v_cache), a.k_scale, a.v_scale, a.k_zp, a.v_zp,     \
+                   a.slots, (uint32_t)total, (uint32_t)a.num_kv_heads, num_slots, err),        \
+        "append_kv launch")
+        if (a.src_dtype == PA_BF16) {
+            if (a.head_dim == 128) PA_LAUNCH_Q4(__nv_bfloat16, 128);
+            PA_LAUNCH_Q4(__nv_bfloat16, 64);
+        }
+        if (a.head_dim == 128) PA_LAUNCH_Q4(__half, 128);
+        PA_LAUNCH_Q4(__half, 64);
 #undef PA_LAUNCH_Q4
     } else if (a.kv_dtype == PA_FP8_E4M3) {
         const int64_t total = (int64_t)a.num_tokens * a.num_kv_heads * (a.head_dim / 16);
@@ -438,41 +459,41 @@ pa_status launch_append_kv(const AppendArgs& a) {
 
 namespace {
 
-template <int KV, typename T>
-void gather_as(const GatherArgs& a, unsigned grid, int threads, int64_t num_slots,
-               unsigned int* err) {
-    gather_kv_kernel<KV, T><<<grid, threads, 0, a.stream>>>(
-        static_cast<T*>(a.key), static_cast<T*>(a.value), a.k_cache, a.v_cache, a.k_scale,
-        a.v_scale, a.k_zp, a.v_zp, a.slots, a.num_tokens, a.num_kv_heads, a.head_dim, num_slots,
-        err);
+template <int KV, int D, typename T>
+pa_status gather_as(const GatherArgs& a, uint32_t total) {
+    return cuda_status(
+        launch_pdl(gather_kv_kernel<KV, D, T>, dim3((total + 255u) / 256u), dim3(256), 0, a.stream,
+                   static_cast<T*>(a.key), static_cast<T*>(a.value), a.k_cache, a.v_cache,
+                   a.k_scale, a.v_scale, a.k_zp, a.v_zp, a.slots, total, (uint32_t)a.num_kv_heads,
+                   (int64_t)a.num_blocks * kBlock, device_error_word()),
+        "gather_kv launch");
+}
+
+template <int KV, int D>
+pa_status gather_from(const GatherArgs& a, uint32_t total) {
+    if (a.out_dtype == PA_F32) return gather_as<KV, D, float>(a, total);
+    if (a.out_dtype == PA_F16) return gather_as<KV, D, __half>(a, total);
+    return gather_as<KV, D, __nv_bfloat16>(a, total);
 }
 
 template <int KV>
-void gather_from(const GatherArgs& a, unsigned grid, int threads, int64_t num_slots,
-                 unsigned int* err) {
-    if (a.out_dtype == PA_F32) gather_as<KV, float>(a, grid, threads, num_slots, err);
-    else if (a.out_dtype == PA_F16) gather_as<KV, __half>(a, grid, threads, num_slots, err);
-    else gather_as<KV, __nv_bfloat16>(a, grid, threads, num_slots, err);
+pa_status gather_dim(const GatherArgs& a, uint32_t total) {
+    return a.head_dim == 128 ? gather_from<KV, 128>(a, total) : gather_from<KV, 64>(a, total);
 }
 
 }  // namespace
 
 pa_status launch_gather_kv(const GatherArgs& a) {
-    unsigned int* err = device_error_word();
-    const int64_t num_slots = (int64_t)a.num_blocks * kBlock;
-    const int threads = 256;
     const int64_t total = (int64_t)a.num_tokens * a.num_kv_heads * (a.head_dim / 8);
-    const int64_t grid = (total + threads - 1) / threads;
-    if (grid > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "too many tokens for one launch");
-    const unsigned n = (unsigned)grid;
+    if (total > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "too many tokens for one launch");
+    const uint32_t n = (uint32_t)total;
     switch (a.kv_dtype) {
-        case PA_F16: gather_from<PA_F16>(a, n, threads, num_slots, err); break;
-        case PA_BF16: gather_from<PA_BF16>(a, n, threads, num_slots, err); break;
-        case PA_INT8: gather_from<PA_INT8>(a, n, threads, num_slots, err); break;
-        case PA_INT4: gather_from<PA_INT4>(a, n, threads, num_slots, err); break;
-        default: gather_from<PA_FP8_E4M3>(a, n, threads, num_slots, err); break;
+        case PA_F16: return gather_dim<PA_F16>(a, n);
+        case PA_BF16: return gather_dim<PA_BF16>(a, n);
+        case PA_INT8: return gather_dim<PA_INT8>(a, n);
+        case PA_INT4: return gather_dim<PA_INT4>(a, n);
+        default: return gather_dim<PA_FP8_E4M3>(a, n);
     }
-    return cuda_status(cudaGetLastError(), "gather_kv launch");
 }
 
 pa_status launch_copy_blocks(const CopyArgs& a) {

@@ -9,14 +9,17 @@
 //   S[i][t] = sum_g ks[t][g] * sum_{j in g} q_ij (c[t][j] - kz[t][g])
 //   O[i][j] = sum_t P[i][t] vs[t][g(j)] * (c[t][j] - vz[t][g(j)])
 //
-// c - z is an integer in [-15, 15], exact in fp16. Two codes become an fp16
-// pair with one three-input logic operation: a code in mantissa bits 0-3 of
-// 1024.0 is 1024 + c, in bits 4-7 of 64.0 it is 64 + c; subtracting 1024 + z
-// or 64 + z is exact. q goes to fp16 after an exact power-of-two scaling per
-// row, the V scale is folded into P against a running power-of-two reference
-// per group, so the fp16 P never exceeds the softmax weight (at most 2^8 under
-// the lazily moved maximum) and a new reference rescales O exactly. Products
-// accumulate in fp32; the softmax maximum, sum and the scales are fp32.
+// (the zero-point terms are taken out of the sums: z * sum_j q_ij of S, and of
+// O the sum over tokens of P vs vz, one product more). A masked pair of codes IS
+// an fp16 pair: a code in bits 0-3 of a half is the subnormal c * 2^-24, in bits
+// 4-7 c * 2^-20, both exact, and the tensor cores multiply subnormals like any
+// number; so a word of 8 codes costs one shift and four masks, and no
+// conversion. The powers of two go into q, the output and the row's scale. q
+// goes to fp16 after an exact power-of-two scaling per row, the V scale is
+// folded into P against a running power-of-two reference per group, so the fp16
+// P never exceeds the softmax weight (at most 2^8 under the lazily moved
+// maximum) and a new reference rescales O exactly. Products accumulate in fp32;
+// the softmax maximum, sum and the scales are fp32.
 //
 // What bounds it: a (token, kv head) costs 148 bytes at d = 128, so the
 // memory system delivers one every 7 cycles of an SM, in which its 256 codes
@@ -52,10 +55,9 @@ using pa::sched::kBS;
 using pa::sched::kWorkerWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyMax = 8.f;    // base-2 headroom before the running max is moved
-constexpr int kStages = 4;
-// 16 warps a SM at 128 registers a thread; the accumulators of 16 rows at d =
-// 128 need more, and get 12 warps at 168
-constexpr int ctas_per_sm(int d, int nr) { return d == 128 && nr == 2 ? 3 : 4; }
+// 12 warps a SM: the 2048 shares that the schedule knows at most would leave
+// some SMs with 16 warps and some with 12, and the kernel waiting for the former
+constexpr int ctas_per_sm(int d, int nr) { return d == 128 && nr == 2 ? 2 : 3; }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -73,6 +75,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// the same on a zero accumulator
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t d;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
@@ -86,35 +97,20 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     return d;
 }
 
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-    __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-    return *reinterpret_cast<uint32_t*>(&r);
-}
-
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
-constexpr uint32_t kBase1024 = 0x64006400u, kBase64 = 0x54005400u;
-
-// The zero points of two tokens (or of one, twice), as what the biased codes
-// are reduced by: fp16 pairs 1024 + z and 64 + z.
-struct ZeroPair {
-    uint32_t z1024, z64;
-    // zz: the two zero points in the low bytes of the two halves
-    __device__ __forceinline__ explicit ZeroPair(uint32_t zz)
-        : z1024(zz | kBase1024), z64(zz * 16u + kBase64) {}
-};
-
-// (code - z) of the nibble pairs of a word: nibbles 0 and 4 -> n[0], 1 and 5 ->
-// n[1], 2 and 6 -> n[2], 3 and 7 -> n[3]
-__device__ __forceinline__ void unpack(uint32_t w, const ZeroPair& z, uint32_t (&n)[4]) {
+// The codes of a word as fp16 pairs: nibbles 0 and 4 -> n[0], 2 and 6 -> n[2] in
+// units of 2^-24; 1 and 5 -> n[1], 3 and 7 -> n[3] in units of 2^-20.
+constexpr float kUnit = 16777216.f;      // 2^24
+__device__ __forceinline__ void unpack(uint32_t w, uint32_t (&n)[4]) {
     const uint32_t h = w >> 8;
-    n[0] = hsub2((w & 0x000f000fu) | kBase1024, z.z1024);
-    n[1] = hsub2((w & 0x00f000f0u) | kBase64, z.z64);
-    n[2] = hsub2((h & 0x000f000fu) | kBase1024, z.z1024);
-    n[3] = hsub2((h & 0x00f000f0u) | kBase64, z.z64);
+    n[0] = w & 0x000f000fu;
+    n[1] = w & 0x00f000f0u;
+    n[2] = h & 0x000f000fu;
+    n[3] = h & 0x00f000f0u;
 }
 
 // smallest e with 2^e >= x, for a positive finite x (x = 0 gives -126)
@@ -139,20 +135,23 @@ __device__ __forceinline__ uint32_t tile4_offset(int row, int chunk) {
     else return row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4);
 }
 
-// Per warp: kStages stages of (K codes, V codes), then the stages' scale
-// areas (k scale, v scale [16][groups] fp32, k zero point, v zero point
-// [16][groups]), padded so the next warp's ring starts on a 1024-byte boundary.
+// Per warp: kStages stages of two blocks' (K codes, V codes), then the stages'
+// scale areas, two blocks' (k scale, v scale [16][groups] fp32, k zero point, v
+// zero point [16][groups]), padded so the next warp's ring starts on a 1024-byte
+// boundary. Two blocks a stage: half the waits and issues of one.
 template <int D>
 struct Q4Layout {
+    static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kGroups = D / PA_INT4_GROUP;
     static constexpr int kTile = kBS * D / 2;             // one K (or V) code tile
-    static constexpr int kStage = 2 * kTile;
+    static constexpr int kBlockCodes = 2 * kTile;
+    static constexpr int kStage = 2 * kBlockCodes;
     static constexpr int kScaleArea = kBS * kGroups * 4;
     static constexpr int kZpArea = kBS * kGroups;
-    static constexpr int kMeta = 2 * (kScaleArea + kZpArea);
+    static constexpr int kMeta = 2 * (kScaleArea + kZpArea);   // of one block
     static constexpr int kMetaAt = kStages * kStage;
-    static constexpr int kWarp = (kMetaAt + kStages * kMeta + 1023) / 1024 * 1024;
-    static_assert(kStage % 512 == 0 && kMeta % 16 == 0, "swizzle and bulk copy alignment");
+    static constexpr int kWarp = (kMetaAt + kStages * 2 * kMeta + 1023) / 1024 * 1024;
+    static_assert(kTile % 512 == 0 && kMeta % 16 == 0, "swizzle and bulk copy alignment");
     __host__ __device__ static int smem_bytes(int num_seqs) {
         return pa::sched::header_bytes(num_seqs, kStages) + kWorkerWarps * kWarp + 1024;
     }
@@ -173,7 +172,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                              const pa::sched::Params p, const Q4Extra x) {
     using namespace pa::sched;
     using Lay = Q4Layout<D>;
-    constexpr int S = kStages;
+    constexpr int S = Lay::kStages;
     constexpr int GR = Lay::kGroups;
     constexpr int CH = D / 32;           // 16-byte chunks of a row: 32 dims each
 
@@ -204,25 +203,23 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     if (lane == 0) write_merge_record(p, wid, 0, 0, 0);   // none unless set at the end
     if (wid >= W || n <= 0) return;   // the grid's last CTA may have spare warps
 
-    uint64_t pol_once = 0, pol_again = 0;
+    const uint64_t pol_once = pa::policy_evict_first(), pol_again = pa::policy_evict_normal();
     if (lane == 0) {
         for (int i = 0; i < S; ++i) pa::mbar_init(bars + 8 * i, 1);
         pa::fence_barrier_init();
         pa::prefetch_tensormap(&tmap_k);
         pa::prefetch_tensormap(&tmap_v);
-        pol_once = pa::policy_evict_first();
-        pol_again = pa::policy_evict_normal();
     }
     __syncwarp();
 
     // each lane keeps the (block x H_kv + kv head) tile of virtual block
-    // win + lane and whether later row chunks read that block again
-    int win = -32, my_tile = 0, my_once = 1;
+    // win + lane; the top bit: later row chunks read that block again
+    int win = -32;
+    uint32_t my_tile = 0;
     auto refresh = [&](int wbase) {
         win = wbase;
         const int64_t f = f0 + wbase + lane;
         my_tile = 0;
-        my_once = 1;
         if (f < f1) {
             const Pos q = locate(p, cum, chunks, f);
             int blk = __ldg(p.block_tables + (int64_t)q.s * p.max_blocks + q.b);
@@ -230,44 +227,62 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                 if (p.err) atomicOr(p.err, pa::ERR_BAD_BLOCK);
                 blk = 0;
             }
-            my_tile = blk * hkv + q.g;
-            my_once = q.C == 1;
+            my_tile = (uint32_t)(blk * hkv + q.g) | (q.C == 1 ? 0u : 0x80000000u);
         }
     };
-    auto issue = [&](int k) {   // warp-uniform
-        if (k >= win + 32) refresh(k & ~31);
-        const int tile = __shfl_sync(0xffffffffu, my_tile, k - win);
-        const int once = __shfl_sync(0xffffffffu, my_once, k - win);
-        if (lane == 0) {
-            const uint32_t bar = bars + 8 * (k % S);
-            const uint32_t dst = ring + (k % S) * Lay::kStage;
-            const uint32_t sd = ring + Lay::kMetaAt + (k % S) * Lay::kMeta;
-            const uint64_t pol = once ? pol_once : pol_again;
-            const int64_t row = (int64_t)tile * (kBS * GR);
-            pa::mbar_arrive_expect_tx(bar, 2 * Lay::kTile + Lay::kMeta);
-            pa::tma_load_2d(dst, &tmap_k, 0, tile * kBS, bar, pol);
-            pa::tma_load_2d(dst + Lay::kTile, &tmap_v, 0, tile * kBS, bar, pol);
-            bulk_load(sd, x.k_scale + row, Lay::kScaleArea, bar);
-            bulk_load(sd + Lay::kScaleArea, x.v_scale + row, Lay::kScaleArea, bar);
-            bulk_load(sd + 2 * Lay::kScaleArea, x.k_zp + row, Lay::kZpArea, bar);
-            bulk_load(sd + 2 * Lay::kScaleArea + Lay::kZpArea, x.v_zp + row, Lay::kZpArea, bar);
+    // A stage's copies are issued by several lanes at once, one each: lanes 0 .. 3 the
+    // K and V codes of its two blocks, lanes 0 .. 7 their scales and zero points.
+    const int which = lane & 3;          // k scale, v scale, k zero point, v zero point
+    const uint8_t* const meta_src =
+        which == 0   ? reinterpret_cast<const uint8_t*>(x.k_scale)
+        : which == 1 ? reinterpret_cast<const uint8_t*>(x.v_scale)
+        : which == 2 ? reinterpret_cast<const uint8_t*>(x.k_zp)
+                     : reinterpret_cast<const uint8_t*>(x.v_zp);
+    const uint32_t meta_bytes = which < 2 ? Lay::kScaleArea : Lay::kZpArea;
+    const uint32_t meta_dst = ring + Lay::kMetaAt + (lane >> 2 & 1) * Lay::kMeta +
+                              (which < 2 ? which * Lay::kScaleArea
+                                         : 2 * Lay::kScaleArea + (which - 2) * Lay::kZpArea);
+    const CUtensorMap* const map = (lane & 1) == 0 ? &tmap_k : &tmap_v;
+    int issued = 0, ist = 0;             // pairs of blocks asked for, and the next one's stage
+    auto issue = [&]() {                 // warp-uniform
+        const int b0 = 2 * issued, have = min(2, n - b0);
+        if (b0 >= win + 32) refresh(b0 & ~31);
+        const uint32_t code_tile = __shfl_sync(0xffffffffu, my_tile, b0 - win + (lane >> 1 & 1));
+        const uint32_t meta_tile = __shfl_sync(0xffffffffu, my_tile, b0 - win + (lane >> 2 & 1));
+        if (lane < 4 * have) {
+            const uint32_t bar = bars + 8 * ist;
+            if (lane == 0)
+                pa::mbar_arrive_expect_tx(bar, have * (Lay::kBlockCodes + Lay::kMeta));
+            if (lane < 2 * have)
+                pa::tma_load_2d(ring + ist * Lay::kStage + lane * Lay::kTile, map, 0,
+                                (int)(code_tile & 0x7fffffffu) * kBS, bar,
+                                code_tile >> 31 ? pol_again : pol_once);
+            bulk_load(meta_dst + ist * 2 * Lay::kMeta,
+                      meta_src + (uint64_t)(meta_tile & 0x7fffffffu) * meta_bytes, meta_bytes,
+                      bar);
         }
+        ++issued;
+        ist = ist + 1 == S ? 0 : ist + 1;
     };
-    int issued = 0;
-    for (; issued < S && issued < n; ++issued) issue(issued);
+    const int pairs = (n + 1) / 2;
+    while (issued < S && issued < pairs) issue();
 
     Pos cur = locate(p, cum, chunks, f0);
     // S^T / O^T fragments: the lane holds query rows 8 nr + 2 qc and + 1
     float o[NR][CH][2][4];               // [.][chunk][dims 4 quad + 2 j, + 1][(dim, row)]
+    float oz[NR][GR][4];                 // sum of P vz: row 2 qc + e in [e], of lanes quad == 0
     float m_run[NR][2], l_run[NR][2], rowmul[NR][2];
+    float qsum[NR][GR][2];               // sum of the row's q over a group, as K products count it
+    float m_ref[NR][2];                  // m_run, or 0 while no key was seen
     int bound[NR][2];                    // last key each row sees
     uint32_t qb[NR][CH][4];              // row 8 nr + quad, dims 32 c + 8 qc .. + 7
-    int ev[GR];                          // log2 of the running V-scale reference
+    float vref[GR], vinv[GR];            // running V-scale reference, a power of two; its inverse
     int L = 0, r = 1, q0 = 0, rows = 0, row_off = 0, seg_b0 = cur.b, last_q = 0;
     bool seg_first = true;
 
     // Segment start: this warp's q rows as fp16 B fragments, each row scaled
-    // by 2^(14 - e_row), its dims paired as the nibbles of a K word are.
+    // by 2^(14 - e_row), its dims paired as the nibbles of a K word are and the
+    // odd ones, whose codes count 2^-20, by 2^-4 more.
     auto start_segment = [&]() {
         L = __ldg(p.context_lens + cur.s);
         r = query_run(p.qsl, cur.s, &q0);
@@ -308,18 +323,35 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                 ex = (int)((__float_as_uint(mx) >> 23) & 0xff) - 127;   // floor(log2 max|q|)
                 ex = max(-100, min(100, ex));
             }
-            const float up = exp2i(14 - ex);
+            const float up[2] = {exp2i(14 - ex), exp2i(10 - ex)};
+            float qs[GR];
+#pragma unroll
+            for (int g = 0; g < GR; ++g) qs[g] = 0.f;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    qb[nr][c][e] = pack_half2(v[c][e] * up, v[c][e + 4] * up);
-            const float mul = row < rows ? p.scale_log2 * exp2i(ex - 14) : 0.f;
+                for (int e = 0; e < 4; ++e) {
+                    qb[nr][c][e] = pack_half2(v[c][e] * up[e & 1], v[c][e + 4] * up[e & 1]);
+                    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&qb[nr][c][e]));
+                    qs[c * GR / CH] += (f.x + f.y) * (e & 1 ? 16.f / kUnit : 1.f / kUnit);
+                }
+            const float mul = row < rows ? p.scale_log2 * exp2i(ex - 14) * kUnit : 0.f;
+#pragma unroll
+            for (int g = 0; g < GR; ++g) {
+                qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], 1);
+                qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], 2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    qsum[nr][g][e] = __shfl_sync(0xffffffffu, qs[g], 4 * (2 * qc + e));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) oz[nr][g][e] = 0.f;
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 rowmul[nr][e] = __shfl_sync(0xffffffffu, mul, 4 * (2 * qc + e));
                 bound[nr][e] = min(last_q + (row_off + 8 * nr + 2 * qc + e) / G, L - 1);
                 m_run[nr][e] = -INFINITY;
+                m_ref[nr][e] = 0.f;
                 l_run[nr][e] = 0.f;
             }
 #pragma unroll
@@ -330,11 +362,11 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                     for (int e = 0; e < 4; ++e) o[nr][c][j][e] = 0.f;
         }
 #pragma unroll
-        for (int g = 0; g < GR; ++g) ev[g] = -126;
+        for (int g = 0; g < GR; ++g) vref[g] = exp2i(-126), vinv[g] = exp2i(126);
     };
 
     // Segment end: the output rows (segment held whole) or the partial slot;
-    // O of group g is in units of the V-scale reference 2^ev[g].
+    // O of group g is in units of the V-scale reference vref[g].
     auto finish_segment = [&](bool complete, int slot_idx, int tok_end) {
         Slot sl(p.slots + (2 * wid + slot_idx) * (int64_t)p.slot_bytes, p.rows_per_tile);
         if (!complete && lane == 0) {
@@ -352,8 +384,15 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                 l += __shfl_xor_sync(0xffffffffu, l, 4);
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
+                float z[GR];
+#pragma unroll
+                for (int g = 0; g < GR; ++g) z[g] = __shfl_sync(0xffffffffu, oz[nr][g][e], qc);
                 const int row = 8 * nr + 2 * qc + e;
                 if (row >= rows) continue;
+                float mulg[GR];
+                const float inv = complete ? kUnit / l : kUnit;
+#pragma unroll
+                for (int g = 0; g < GR; ++g) mulg[g] = vref[g] * inv;
                 int64_t obase = 0;
                 if (complete) {
                     const int gr = row_off + row;
@@ -364,10 +403,11 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                 }
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    const float vref = exp2i(ev[c * GR / CH]);
-                    const float mul = complete ? vref / l : vref;
-                    const float4 v = make_float4(o[nr][c][0][e] * mul, o[nr][c][0][2 + e] * mul,
-                                                 o[nr][c][1][e] * mul, o[nr][c][1][2 + e] * mul);
+                    // dims 4 quad, + 2 count 2^-24, dims 4 quad + 1, + 3 count 2^-20
+                    const float zc = z[c * GR / CH], mul = mulg[c * GR / CH];
+                    const float4 v = make_float4(
+                        (o[nr][c][0][e] - zc) * mul, fmaf(o[nr][c][0][2 + e], 0.0625f, -zc) * mul,
+                        (o[nr][c][1][e] - zc) * mul, fmaf(o[nr][c][1][2 + e], 0.0625f, -zc) * mul);
                     const int col = 32 * c + 4 * quad;
                     if (!complete) {
                         *reinterpret_cast<float4*>(sl.o + (int64_t)row * D + col) = v;
@@ -389,92 +429,103 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             }
     };
 
+    // lane constants of the operand loads: a chunk further is 32 bytes in the swizzled row
+    const uint32_t ld0 = tile4_offset<D>(ld_tok, ld_chk);
     start_segment();
-    int consumed = 0;
-    for (int k = 0; k < n; ++k) {
-        const int st = k % S;
-        if (!pa::mbar_wait(bars + 8 * st, (k / S) & 1, p.err, pa::ERR_WAIT_FULL)) break;
-        consumed = k + 1;
-        const uint32_t kb = ring + st * Lay::kStage, vb = kb + Lay::kTile;
-        const float* ksc = reinterpret_cast<const float*>(meta + st * Lay::kMeta);
+    int consumed = 0, st = 0;
+    uint32_t phase = 0;
+    for (int k = 0; k < n; ++k) {        // blocks; two in a stage
+        const int half = k & 1;
+        if (half == 0 && !pa::mbar_wait(bars + 8 * st, phase, p.err, pa::ERR_WAIT_FULL)) break;
+        consumed = (k >> 1) + 1;
+        const uint32_t kb = ring + st * Lay::kStage + half * Lay::kBlockCodes + ld0;
+        const uint32_t vb = kb + Lay::kTile;
+        const uint8_t* const mt = meta + (2 * st + half) * Lay::kMeta;
+        const float* ksc = reinterpret_cast<const float*>(mt) + quad * GR;
         const float* vsc = ksc + kBS * GR;
-        const uint8_t* kzp = meta + st * Lay::kMeta + 2 * Lay::kScaleArea;
-        const uint8_t* vzp = kzp + Lay::kZpArea;
+        const uint8_t* kzp = mt + 2 * Lay::kScaleArea + quad * GR;
+        const uint8_t* vzp = mt + 2 * Lay::kScaleArea + Lay::kZpArea;
         const int tok0 = cur.b * kBS;
 
         // scales of the lane's tokens quad and quad + 8
         float ks[2][GR], vs[2][GR];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int t = quad + 8 * h;
             if constexpr (GR == 2) {
-                const float2 a = *reinterpret_cast<const float2*>(ksc + 2 * t);
-                const float2 b = *reinterpret_cast<const float2*>(vsc + 2 * t);
+                const float2 a = *reinterpret_cast<const float2*>(ksc + 16 * h);
+                const float2 b = *reinterpret_cast<const float2*>(vsc + 16 * h);
                 ks[h][0] = a.x, ks[h][1] = a.y, vs[h][0] = b.x, vs[h][1] = b.y;
             } else {
-                ks[h][0] = ksc[t], vs[h][0] = vsc[t];
+                ks[h][0] = ksc[8 * h], vs[h][0] = vsc[8 * h];
             }
-            // scales past the context may hold anything: their weights must be 0
-            if (tok0 + t >= L)
-#pragma unroll
-                for (int g = 0; g < GR; ++g) vs[h][g] = 0.f;
         }
 
-        // ---- S^T = (K codes - z) Q^T: 16 tokens x 8 NR rows, one sum per group ----
+        // ---- S^T = K codes Q^T: 16 tokens x 8 NR rows, one sum per group ----
         float s[NR][GR][4];
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int g = 0; g < GR; ++g)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nr][g][e] = 0.f;
 #pragma unroll
         for (int pp = 0; pp < CH / 2; ++pp) {
             uint32_t rr[4];
-            pa::ldmatrix_x4(kb + tile4_offset<D>(ld_tok, 2 * pp + ld_chk), rr[0], rr[1], rr[2],
-                            rr[3]);
+            pa::ldmatrix_x4(kb ^ (32 * pp), rr[0], rr[1], rr[2], rr[3]);
             const int g = pp * 2 * GR / CH;
-            const ZeroPair z0(kzp[quad * GR + g] * 0x00010001u);
-            const ZeroPair z1(kzp[(quad + 8) * GR + g] * 0x00010001u);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 uint32_t lo[4], hi[4];
-                unpack(rr[2 * j], z0, lo);
-                unpack(rr[2 * j + 1], z1, hi);
+                unpack(rr[2 * j], lo);
+                unpack(rr[2 * j + 1], hi);
                 const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
                 const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr) {
                     const uint32_t(&q)[4] = qb[nr][2 * pp + j];
-                    mma_f16(s[nr][g], a0, q[0], q[1]);
+                    if (j == 0 && (GR == CH / 2 || pp == 0))
+                        mma_f16_first(s[nr][g], a0, q[0], q[1]);
+                    else
+                        mma_f16(s[nr][g], a0, q[0], q[1]);
                     mma_f16(s[nr][g], a1, q[2], q[3]);
                 }
             }
         }
 
-        // ---- scales, mask, online softmax (lazy max) ----
-        const bool need_mask = tok0 + kBS - 1 > last_q;
+        // ---- zero points, scales, mask, online softmax (lazy max) ----
         float a[NR][4];                  // [.][2 h + e]: token quad + 8 h, row 2 qc + e
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float z[GR];
+#pragma unroll
+            for (int g = 0; g < GR; ++g) z[g] = (float)kzp[8 * GR * h + g];
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = fmaf(-z[0], qsum[nr][0][e], s[nr][0][2 * h + e]) * ks[h][0];
+                    if constexpr (GR == 2)
+                        v = fmaf(fmaf(-z[1], qsum[nr][1][e], s[nr][1][2 * h + e]), ks[h][1], v);
+                    a[nr][2 * h + e] = v * rowmul[nr][e];
+                }
+        }
+        if (tok0 + kBS - 1 > last_q) {   // the last block or two of a context
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int t = tok0 + quad + 8 * h;
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (t > bound[nr][e]) a[nr][2 * h + e] = -INFINITY;
+                // scales past the context may hold anything: their weights must be 0
+                if (t >= L)
+#pragma unroll
+                    for (int g = 0; g < GR; ++g) vs[h][g] = 0.f;
+            }
+        }
         bool raise = false;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int e = 0; e < 2; ++e)
+                raise |= fmaxf(a[nr][e], a[nr][2 + e]) > m_run[nr][e] + kLazyMax;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float v = s[nr][0][2 * h + e] * ks[h][0];
-                    if constexpr (GR == 2) v = fmaf(s[nr][1][2 * h + e], ks[h][1], v);
-                    v *= rowmul[nr][e];
-                    if (need_mask && tok0 + quad + 8 * h > bound[nr][e]) v = -INFINITY;
-                    a[nr][2 * h + e] = v;
-                    raise |= v > m_run[nr][e] + kLazyMax;
-                }
-        int evn[GR];
-#pragma unroll
-        for (int g = 0; g < GR; ++g) {
-            evn[g] = ev[g];
-            raise |= fmaxf(vs[0][g], vs[1][g]) > exp2i(ev[g]);
-        }
+        for (int g = 0; g < GR; ++g) raise |= fmaxf(vs[0][g], vs[1][g]) > vref[g];
         if (__any_sync(0xffffffffu, raise)) {   // rare: a row's maximum or a V reference moves
             float vfix[GR];
 #pragma unroll
@@ -483,9 +534,10 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                evn[g] = max(ev[g], ceil_log2(mx));
-                vfix[g] = exp2i(ev[g] - evn[g]);
-                ev[g] = evn[g];
+                const float next = fmaxf(vref[g], exp2i(ceil_log2(mx)));
+                vfix[g] = vref[g] / next;                  // powers of two: exact
+                vref[g] = next;
+                vinv[g] = 1.f / next;
             }
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
@@ -498,9 +550,11 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                     float al = 1.f;
                     if (mx > m_run[nr][e] + kLazyMax) {
                         al = pa::ex2(m_run[nr][e] - mx);   // 0 while m_run is -inf
-                        m_run[nr][e] = mx;
+                        m_run[nr][e] = m_ref[nr][e] = mx;
                     }
                     l_run[nr][e] *= al;
+#pragma unroll
+                    for (int g = 0; g < GR; ++g) oz[nr][g][e] *= al * vfix[g];
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
                         const float f = al * vfix[c * GR / CH];
@@ -515,9 +569,8 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
         float vmul[2][GR];
 #pragma unroll
         for (int g = 0; g < GR; ++g) {
-            const float inv = exp2i(-ev[g]);
-            vmul[0][g] = vs[0][g] * inv;
-            vmul[1][g] = vs[1][g] * inv;
+            vmul[0][g] = vs[0][g] * vinv[g];
+            vmul[1][g] = vs[1][g] * vinv[g];
         }
         uint32_t pb[NR][GR][2];          // P^T operand: tokens 2 qc, + 1 / 2 qc + 8, + 9 of row quad
 #pragma unroll
@@ -525,9 +578,8 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             float w[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float m_use = m_run[nr][e] == -INFINITY ? 0.f : m_run[nr][e];
-                w[e] = pa::ex2(a[nr][e] - m_use);
-                w[2 + e] = pa::ex2(a[nr][2 + e] - m_use);
+                w[e] = pa::ex2(a[nr][e] - m_ref[nr][e]);
+                w[2 + e] = pa::ex2(a[nr][2 + e] - m_ref[nr][e]);
                 l_run[nr][e] += w[e] + w[2 + e];
             }
 #pragma unroll
@@ -538,29 +590,17 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                         pack_half2(w[2 * h] * vmul[h][g], w[2 * h + 1] * vmul[h][g]));
         }
 
-        // ---- O^T += (V codes - z)^T P^T ----
+        // ---- O^T += V codes^T P^T, and the zero points' sums ----
 #pragma unroll
         for (int pp = 0; pp < CH / 2; ++pp) {
             uint32_t rr[4];
-            pa::ldmatrix_x4_trans(vb + tile4_offset<D>(ld_tok, 2 * pp + ld_chk), rr[0], rr[1],
-                                  rr[2], rr[3]);
+            pa::ldmatrix_x4_trans(vb ^ (32 * pp), rr[0], rr[1], rr[2], rr[3]);
             const int g = pp * 2 * GR / CH;
-            // zero points of tokens 2 qc, 2 qc + 1 and 2 qc + 8, 2 qc + 9
-            uint32_t y0, y1;
-            if constexpr (GR == 2) {
-                y0 = reinterpret_cast<const uint32_t*>(vzp)[qc];
-                y1 = reinterpret_cast<const uint32_t*>(vzp)[qc + 4];
-            } else {
-                y0 = reinterpret_cast<const uint16_t*>(vzp)[qc];
-                y1 = reinterpret_cast<const uint16_t*>(vzp)[qc + 4];
-            }
-            const uint32_t sel = GR == 2 ? (g == 0 ? 0x4240u : 0x4341u) : 0x4140u;
-            const ZeroPair z0(prmt(y0, 0u, sel)), z1(prmt(y1, 0u, sel));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 uint32_t lo[4], hi[4];
-                unpack(rr[2 * j], z0, lo);
-                unpack(rr[2 * j + 1], z1, hi);
+                unpack(rr[2 * j], lo);
+                unpack(rr[2 * j + 1], hi);
                 const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]};
                 const uint32_t a1[4] = {lo[2], lo[3], hi[2], hi[3]};
 #pragma unroll
@@ -570,11 +610,34 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                 }
             }
         }
-        __syncwarp();
-        if (issued < n) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            issue(issued);
-            ++issued;
+        {
+            // row 0 of a tile of its own: the zero points of tokens 2 qc, + 1 and 2 qc + 8, + 9
+            uint32_t y0 = 0, y1 = 0;
+            if (quad == 0) {
+                if constexpr (GR == 2) {
+                    y0 = reinterpret_cast<const uint32_t*>(vzp)[qc];
+                    y1 = reinterpret_cast<const uint32_t*>(vzp)[qc + 4];
+                } else {
+                    y0 = reinterpret_cast<const uint16_t*>(vzp)[qc];
+                    y1 = reinterpret_cast<const uint16_t*>(vzp)[qc + 4];
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < GR; ++g) {
+                const uint32_t sel = GR == 2 ? (g == 0 ? 0x4240u : 0x4341u) : 0x4140u;
+                const uint32_t az[4] = {prmt(y0, 0u, sel), 0u, prmt(y1, 0u, sel), 0u};
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+                    mma_f16(oz[nr][g], az, pb[nr][g][0], pb[nr][g][1]);
+            }
+        }
+        if (half || k == n - 1) {
+            __syncwarp();
+            if (issued < pairs) {        // into the stage just read
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                issue();
+            }
+            if (++st == S) st = 0, phase ^= 1;
         }
         ++cur.b;
         const bool seg_done = cur.b == cur.nbs;
