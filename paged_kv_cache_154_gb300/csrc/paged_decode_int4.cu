@@ -33,10 +33,8 @@
 // register, with no byte shuffles. P^T gets its operand layout from movmatrix.
 //
 // Work split: the balanced schedule (balanced.cuh) with the per-warp layout of
-// the FP8 kernel: every warp streams its own share through its own ring (code
-// tiles by TMA, scales and zero points by bulk copies on the same barrier);
-// 8 or 16 query rows per tile, further rows as further chunks.
-#include <cuda.h>
+// the FP8 kernel: every warp streams its own share through its own ring; 8 or 16
+// query rows per tile, further rows as further chunks.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -55,16 +53,12 @@ using pa::sched::kBS;
 using pa::sched::kWorkerWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyMax = 8.f;    // base-2 headroom before the running max is moved
-// 12 warps a SM: the 2048 shares that the schedule knows at most would leave
-// some SMs with 16 warps and some with 12, and the kernel waiting for the former
 constexpr int ctas_per_sm(int d, int nr) { return d == 128 && nr == 2 ? 2 : 3; }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-        : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "l"(policy)
+                 : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -126,9 +120,9 @@ __device__ __forceinline__ float exp2i(int e) {   // 2^e for e in [-126, 127]
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// byte offset of 16-byte chunk `chunk` (32 codes) of token row `row` in a code
-// tile as the tensor map writes it: rows of 64 bytes under the 64-byte
-// swizzle (d = 128), rows of 32 bytes under the 32-byte swizzle (d = 64)
+// byte offset of 16-byte chunk `chunk` (32 codes) of token row `row` in a staged
+// code tile: rows of 64 (d = 128) or 32 bytes, the chunks of a row exchanged so
+// that the eight rows of an operand load fall into different banks
 template <int D>
 __device__ __forceinline__ uint32_t tile4_offset(int row, int chunk) {
     if constexpr (D == 128) return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
@@ -137,8 +131,7 @@ __device__ __forceinline__ uint32_t tile4_offset(int row, int chunk) {
 
 // Per warp: kStages stages of two blocks' (K codes, V codes), then the stages'
 // scale areas, two blocks' (k scale, v scale [16][groups] fp32, k zero point, v
-// zero point [16][groups]), padded so the next warp's ring starts on a 1024-byte
-// boundary. Two blocks a stage: half the waits and issues of one.
+// zero point [16][groups]). Two blocks a stage: half the waits and issues of one.
 template <int D>
 struct Q4Layout {
     static constexpr int kStages = D == 128 ? 3 : 6;
@@ -150,14 +143,31 @@ struct Q4Layout {
     static constexpr int kZpArea = kBS * kGroups;
     static constexpr int kMeta = 2 * (kScaleArea + kZpArea);   // of one block
     static constexpr int kMetaAt = kStages * kStage;
-    static constexpr int kWarp = (kMetaAt + kStages * 2 * kMeta + 1023) / 1024 * 1024;
-    static_assert(kTile % 512 == 0 && kMeta % 16 == 0, "swizzle and bulk copy alignment");
+    static constexpr int kWarp = kMetaAt + kStages * 2 * kMeta;
+    static_assert(kTile % 512 == 0 && kMeta % 16 == 0, "alignment");
+    __host__ __device__ static int header(int num_seqs) {   // cum, then chunks
+        return ((num_seqs + 1) * 4 + num_seqs + 127) / 128 * 128;
+    }
     __host__ __device__ static int smem_bytes(int num_seqs) {
-        return pa::sched::header_bytes(num_seqs, kStages) + kWorkerWarps * kWarp + 1024;
+        return header(num_seqs) + kWorkerWarps * kWarp;
+    }
+};
+
+// share_start() in 32-bit arithmetic (B < 2^31, w <= W < 2^16): w B / W =
+// w (B / W) + w (B mod W) / W; the 64-bit divisions are a quarter of a share's
+// fixed cost.
+struct Shares {
+    uint32_t each, rest, W;
+    __device__ __forceinline__ Shares(int64_t B, int64_t W_)
+        : each((uint32_t)B / (uint32_t)W_), rest((uint32_t)B % (uint32_t)W_), W((uint32_t)W_) {}
+    __device__ __forceinline__ int64_t start(int64_t w) const {
+        return (int64_t)((uint32_t)w * each + (uint32_t)w * rest / W);
     }
 };
 
 struct Q4Extra {
+    const uint8_t* k;       // [num_blocks][num_kv_heads][16][D / 2]
+    const uint8_t* v;
     const float* k_scale;   // [num_blocks][num_kv_heads][16][D / 64]
     const float* v_scale;
     const int8_t* k_zp;
@@ -167,50 +177,39 @@ struct Q4Extra {
 // NR: tiles of 8 query rows (1: at most 8 rows per KV head; 2: chunks of 16)
 template <typename TQ, int D, int NR>
 __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
-    paged_decode_int4_kernel(const __grid_constant__ CUtensorMap tmap_k,
-                             const __grid_constant__ CUtensorMap tmap_v,
-                             const pa::sched::Params p, const Q4Extra x) {
+    paged_decode_int4_kernel(const pa::sched::Params p, const Q4Extra x) {
     using namespace pa::sched;
     using Lay = Q4Layout<D>;
     constexpr int S = Lay::kStages;
     constexpr int GR = Lay::kGroups;
+    constexpr int kRows = 8 * NR;
     constexpr int CH = D / 32;           // 16-byte chunks of a row: 32 dims each
 
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = pa::smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t* const smem = smem_raw + (base - raw);
+    extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = lane >> 2, qc = lane & 3;
     const int mat = lane >> 3, mrow = lane & 7;
     const int ld_tok = (mat & 1) * 8 + mrow;   // m0, m2: tokens 0-7; m1, m3: tokens 8-15
     const int ld_chk = mat >> 1;               // m0, m1: chunk 2pp; m2, m3: chunk 2pp + 1
     const int hkv = p.num_kv_heads, G = p.group, n_seqs = p.num_seqs;
-    int32_t* const cum = reinterpret_cast<int32_t*>(smem + kWorkerWarps * S * 8);
+    int32_t* const cum = reinterpret_cast<int32_t*>(smem);
     uint8_t* const chunks = reinterpret_cast<uint8_t*>(cum + n_seqs + 1);
-    const uint32_t bars = base + warp * S * 8;
-    const int hdr = header_bytes(n_seqs, S);
-    const uint32_t ring = base + hdr + warp * Lay::kWarp;
-    const uint8_t* const meta = smem + hdr + warp * Lay::kWarp + Lay::kMetaAt;
+    uint8_t* const mine = smem + Lay::header(n_seqs) + warp * Lay::kWarp;
+    const uint32_t ring = pa::smem_addr(mine);
+    const uint8_t* const meta = mine + Lay::kMetaAt;
 
     build_prefix(cum, chunks, p);
     const int64_t B = cum[n_seqs];
     const int64_t wid = (int64_t)blockIdx.x * kWorkerWarps + warp;
     const int64_t W = share_count(p, B);
-    const int64_t f0 = share_start(wid, B, W);
-    const int64_t f1 = share_start(wid + 1, B, W);
-    const int n = (int)(f1 - f0);
     if (lane == 0) write_merge_record(p, wid, 0, 0, 0);   // none unless set at the end
-    if (wid >= W || n <= 0) return;   // the grid's last CTA may have spare warps
+    if (wid >= W) return;             // the grid's last CTA may have spare warps
+    const Shares shares(B, W);
+    const int64_t f0 = shares.start(wid), f1 = shares.start(wid + 1);
+    const int n = (int)(f1 - f0);
+    if (n <= 0) return;
 
     const uint64_t pol_once = pa::policy_evict_first(), pol_again = pa::policy_evict_normal();
-    if (lane == 0) {
-        for (int i = 0; i < S; ++i) pa::mbar_init(bars + 8 * i, 1);
-        pa::fence_barrier_init();
-        pa::prefetch_tensormap(&tmap_k);
-        pa::prefetch_tensormap(&tmap_v);
-    }
-    __syncwarp();
 
     // each lane keeps the (block x H_kv + kv head) tile of virtual block
     // win + lane; the top bit: later row chunks read that block again
@@ -230,42 +229,58 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             my_tile = (uint32_t)(blk * hkv + q.g) | (q.C == 1 ? 0u : 0x80000000u);
         }
     };
-    // A stage's copies are issued by several lanes at once, one each: lanes 0 .. 3 the
-    // K and V codes of its two blocks, lanes 0 .. 7 their scales and zero points.
-    const int which = lane & 3;          // k scale, v scale, k zero point, v zero point
-    const uint8_t* const meta_src =
-        which == 0   ? reinterpret_cast<const uint8_t*>(x.k_scale)
-        : which == 1 ? reinterpret_cast<const uint8_t*>(x.v_scale)
-        : which == 2 ? reinterpret_cast<const uint8_t*>(x.k_zp)
-                     : reinterpret_cast<const uint8_t*>(x.v_zp);
-    const uint32_t meta_bytes = which < 2 ? Lay::kScaleArea : Lay::kZpArea;
-    const uint32_t meta_dst = ring + Lay::kMetaAt + (lane >> 2 & 1) * Lay::kMeta +
-                              (which < 2 ? which * Lay::kScaleArea
-                                         : 2 * Lay::kScaleArea + (which - 2) * Lay::kZpArea);
-    const CUtensorMap* const map = (lane & 1) == 0 ? &tmap_k : &tmap_v;
-    int issued = 0, ist = 0;             // pairs of blocks asked for, and the next one's stage
-    auto issue = [&]() {                 // warp-uniform
-        const int b0 = 2 * issued, have = min(2, n - b0);
-        if (b0 >= win + 32) refresh(b0 & ~31);
-        const uint32_t code_tile = __shfl_sync(0xffffffffu, my_tile, b0 - win + (lane >> 1 & 1));
-        const uint32_t meta_tile = __shfl_sync(0xffffffffu, my_tile, b0 - win + (lane >> 2 & 1));
-        if (lane < 4 * have) {
-            const uint32_t bar = bars + 8 * ist;
-            if (lane == 0)
-                pa::mbar_arrive_expect_tx(bar, have * (Lay::kBlockCodes + Lay::kMeta));
-            if (lane < 2 * have)
-                pa::tma_load_2d(ring + ist * Lay::kStage + lane * Lay::kTile, map, 0,
-                                (int)(code_tile & 0x7fffffffu) * kBS, bar,
-                                code_tile >> 31 ? pol_again : pol_once);
-            bulk_load(meta_dst + ist * 2 * Lay::kMeta,
-                      meta_src + (uint64_t)(meta_tile & 0x7fffffffu) * meta_bytes, meta_bytes,
-                      bar);
-        }
-        ++issued;
-        ist = ist + 1 == S ? 0 : ist + 1;
-    };
+    // A block is staged by 16-byte asynchronous copies, a lane each: one or two of
+    // its K codes, as many of V, and one of its scales and zero points. (Bulk and
+    // tensor copies take their operands from uniform registers, so six of them a
+    // block cost 100 instructions where these cost 15, and issue slots are what
+    // this kernel is short of.)
+    const int row0 = lane / CH, chk0 = lane % CH;      // the lane's chunk of a code tile
+    const uint32_t code_dst = ring + tile4_offset<D>(row0, chk0);
+    constexpr int kS16 = Lay::kScaleArea / 16, kZ16 = Lay::kZpArea / 16;
+    const uint8_t* meta_src = nullptr;
+    uint32_t meta_bytes = 0;                           // of a block, in the lane's array
+    const uint32_t meta_dst = ring + Lay::kMetaAt + 16 * lane;
+    if (lane < 2 * kS16) {
+        meta_src = reinterpret_cast<const uint8_t*>(lane < kS16 ? x.k_scale : x.v_scale) +
+                   16 * (lane % kS16);
+        meta_bytes = Lay::kScaleArea;
+    } else if (lane < 2 * (kS16 + kZ16)) {
+        const int z = lane - 2 * kS16;
+        meta_src = reinterpret_cast<const uint8_t*>(z < kZ16 ? x.k_zp : x.v_zp) + 16 * (z % kZ16);
+        meta_bytes = Lay::kZpArea;
+    }
     const int pairs = (n + 1) / 2;
-    while (issued < S && issued < pairs) issue();
+    int issued = 0;                      // pairs of blocks asked for, every one a copy group
+    uint32_t code_at = code_dst, meta_at = meta_dst;   // in the next pair's stage
+    auto issue = [&]() {                 // warp-uniform
+        if (issued < pairs) {
+            const int b0 = 2 * issued;
+            if (b0 >= win + 32) refresh(b0 & ~31);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (b0 + u >= n) break;
+                const uint32_t tagged = __shfl_sync(0xffffffffu, my_tile, b0 + u - win);
+                const uint32_t tile = tagged & 0x7fffffffu;
+                const uint64_t pol = tagged >> 31 ? pol_again : pol_once;
+                const uint64_t at = (uint64_t)tile * Lay::kTile + 16 * lane;
+#pragma unroll
+                for (int j = 0; j < Lay::kTile / 512; ++j) {
+                    const uint32_t dst = code_at + u * Lay::kBlockCodes + 512 * j;
+                    copy16(dst, x.k + at + 512 * j, pol);
+                    copy16(dst + Lay::kTile, x.v + at + 512 * j, pol);
+                }
+                if (meta_bytes)
+                    copy16(meta_at + u * Lay::kMeta, meta_src + (uint64_t)tile * meta_bytes, pol);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++issued;
+        const bool wrap = code_at == code_dst + (S - 1) * Lay::kStage;
+        code_at = wrap ? code_dst : code_at + Lay::kStage;
+        meta_at = wrap ? meta_dst : meta_at + 2 * Lay::kMeta;
+    };
+#pragma unroll 1
+    for (int i = 0; i < S; ++i) issue();
 
     Pos cur = locate(p, cum, chunks, f0);
     // S^T / O^T fragments: the lane holds query rows 8 nr + 2 qc and + 1
@@ -279,6 +294,9 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     float vref[GR], vinv[GR];            // running V-scale reference, a power of two; its inverse
     int L = 0, r = 1, q0 = 0, rows = 0, row_off = 0, seg_b0 = cur.b, last_q = 0;
     bool seg_first = true;
+    // i / G for row numbers (i, G < 2^13): exact, as i times the rounding is under 2^32
+    const uint32_t inv_g = 0xffffffffu / (uint32_t)G + 1u;
+    auto query_of = [&](int i) { return G == 1 ? i : (int)__umulhi((uint32_t)i, inv_g); };
 
     // Segment start: this warp's q rows as fp16 B fragments, each row scaled
     // by 2^(14 - e_row), its dims paired as the nibbles of a K word are and the
@@ -287,16 +305,16 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
         L = __ldg(p.context_lens + cur.s);
         r = query_run(p.qsl, cur.s, &q0);
         last_q = L - r;
-        row_off = cur.c * kBS;
-        rows = min(kBS, G * r - row_off);
+        row_off = cur.c * kRows;
+        rows = min(kRows, G * r - row_off);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             const int row = 8 * nr + quad;
             float v[CH][8];
             if (row < rows) {
-                const int gr = row_off + row;
+                const int gr = row_off + row, qi = query_of(gr);
                 const TQ* src = static_cast<const TQ*>(p.q) +
-                                ((int64_t)(q0 + gr / G) * p.num_heads + cur.g * G + gr % G) * D +
+                                ((int64_t)(q0 + qi) * p.num_heads + cur.g * G + gr - qi * G) * D +
                                 8 * qc;
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
@@ -349,7 +367,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 rowmul[nr][e] = __shfl_sync(0xffffffffu, mul, 4 * (2 * qc + e));
-                bound[nr][e] = min(last_q + (row_off + 8 * nr + 2 * qc + e) / G, L - 1);
+                bound[nr][e] = min(last_q + query_of(row_off + 8 * nr + 2 * qc + e), L - 1);
                 m_run[nr][e] = -INFINITY;
                 m_ref[nr][e] = 0.f;
                 l_run[nr][e] = 0.f;
@@ -395,8 +413,8 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                 for (int g = 0; g < GR; ++g) mulg[g] = vref[g] * inv;
                 int64_t obase = 0;
                 if (complete) {
-                    const int gr = row_off + row;
-                    obase = ((int64_t)(q0 + gr / G) * p.num_heads + cur.g * G + gr % G) * D;
+                    const int gr = row_off + row, qi = query_of(gr);
+                    obase = ((int64_t)(q0 + qi) * p.num_heads + cur.g * G + gr - qi * G) * D;
                 } else if (quad == 0) {
                     sl.m[row] = m_run[nr][e];
                     sl.l[row] = l;
@@ -432,105 +450,120 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     // lane constants of the operand loads: a chunk further is 32 bytes in the swizzled row
     const uint32_t ld0 = tile4_offset<D>(ld_tok, ld_chk);
     start_segment();
-    int consumed = 0, st = 0;
-    uint32_t phase = 0;
-    for (int k = 0; k < n; ++k) {        // blocks; two in a stage
-        const int half = k & 1;
-        if (half == 0 && !pa::mbar_wait(bars + 8 * st, phase, p.err, pa::ERR_WAIT_FULL)) break;
-        consumed = (k >> 1) + 1;
-        const uint32_t kb = ring + st * Lay::kStage + half * Lay::kBlockCodes + ld0;
-        const uint32_t vb = kb + Lay::kTile;
-        const uint8_t* const mt = meta + (2 * st + half) * Lay::kMeta;
-        const float* ksc = reinterpret_cast<const float*>(mt) + quad * GR;
-        const float* vsc = ksc + kBS * GR;
-        const uint8_t* kzp = mt + 2 * Lay::kScaleArea + quad * GR;
-        const uint8_t* vzp = mt + 2 * Lay::kScaleArea + Lay::kZpArea;
-        const int tok0 = cur.b * kBS;
-
-        // scales of the lane's tokens quad and quad + 8
-        float ks[2][GR], vs[2][GR];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if constexpr (GR == 2) {
-                const float2 a = *reinterpret_cast<const float2*>(ksc + 16 * h);
-                const float2 b = *reinterpret_cast<const float2*>(vsc + 16 * h);
-                ks[h][0] = a.x, ks[h][1] = a.y, vs[h][0] = b.x, vs[h][1] = b.y;
-            } else {
-                ks[h][0] = ksc[8 * h], vs[h][0] = vsc[8 * h];
-            }
+    int st = 0, half = 0;                // half: the stage's first block not yet done
+    for (int k = 0; k < n;) {
+        if (half == 0) {                 // S groups are on their way: the oldest is here
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+            __syncwarp();
         }
+        // Both blocks of the stage at once; a block of another segment (or none) is masked
+        // here and its segment comes back for it.
+        const int take = min(2 - half, min(cur.nbs - cur.b, n - k));
+        const uint32_t kb = ring + st * Lay::kStage + ld0;
+        const uint8_t* const mt = meta + 2 * st * Lay::kMeta;
+        const int tok0 = (cur.b - half) * kBS;   // of the stage's first block
 
-        // ---- S^T = K codes Q^T: 16 tokens x 8 NR rows, one sum per group ----
-        float s[NR][GR][4];
+        // scales of the lane's tokens quad and quad + 8 of each block
+        float ks[2][2][GR], vs[2][2][GR];
 #pragma unroll
-        for (int pp = 0; pp < CH / 2; ++pp) {
-            uint32_t rr[4];
-            pa::ldmatrix_x4(kb ^ (32 * pp), rr[0], rr[1], rr[2], rr[3]);
-            const int g = pp * 2 * GR / CH;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t lo[4], hi[4];
-                unpack(rr[2 * j], lo);
-                unpack(rr[2 * j + 1], hi);
-                const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
-                const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    const uint32_t(&q)[4] = qb[nr][2 * pp + j];
-                    if (j == 0 && (GR == CH / 2 || pp == 0))
-                        mma_f16_first(s[nr][g], a0, q[0], q[1]);
-                    else
-                        mma_f16(s[nr][g], a0, q[0], q[1]);
-                    mma_f16(s[nr][g], a1, q[2], q[3]);
-                }
-            }
-        }
-
-        // ---- zero points, scales, mask, online softmax (lazy max) ----
-        float a[NR][4];                  // [.][2 h + e]: token quad + 8 h, row 2 qc + e
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float z[GR];
-#pragma unroll
-            for (int g = 0; g < GR; ++g) z[g] = (float)kzp[8 * GR * h + g];
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float v = fmaf(-z[0], qsum[nr][0][e], s[nr][0][2 * h + e]) * ks[h][0];
-                    if constexpr (GR == 2)
-                        v = fmaf(fmaf(-z[1], qsum[nr][1][e], s[nr][1][2 * h + e]), ks[h][1], v);
-                    a[nr][2 * h + e] = v * rowmul[nr][e];
-                }
-        }
-        if (tok0 + kBS - 1 > last_q) {   // the last block or two of a context
+        for (int u = 0; u < 2; ++u) {
+            const float* ksc = reinterpret_cast<const float*>(mt + u * Lay::kMeta) + quad * GR;
+            const float* vsc = ksc + kBS * GR;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int t = tok0 + quad + 8 * h;
+                if constexpr (GR == 2) {
+                    const float2 a = *reinterpret_cast<const float2*>(ksc + 16 * h);
+                    const float2 b = *reinterpret_cast<const float2*>(vsc + 16 * h);
+                    ks[u][h][0] = a.x, ks[u][h][1] = a.y, vs[u][h][0] = b.x, vs[u][h][1] = b.y;
+                } else {
+                    ks[u][h][0] = ksc[8 * h], vs[u][h][0] = vsc[8 * h];
+                }
+            }
+        }
+
+        // ---- S^T = K codes Q^T: 2 x 16 tokens x 8 NR rows, one sum per group; then
+        // zero points and scales ----
+        float a[2][NR][4];               // [.][.][2 h + e]: token quad + 8 h, row 2 qc + e
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float s[NR][GR][4];
+#pragma unroll
+            for (int pp = 0; pp < CH / 2; ++pp) {
+                uint32_t rr[4];
+                pa::ldmatrix_x4((kb + u * Lay::kBlockCodes) ^ (32 * pp), rr[0], rr[1], rr[2], rr[3]);
+                const int g = pp * 2 * GR / CH;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t lo[4], hi[4];
+                    unpack(rr[2 * j], lo);
+                    unpack(rr[2 * j + 1], hi);
+                    const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
+                    const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) {
+                        const uint32_t(&q)[4] = qb[nr][2 * pp + j];
+                        if (j == 0 && (GR == CH / 2 || pp == 0))
+                            mma_f16_first(s[nr][g], a0, q[0], q[1]);
+                        else
+                            mma_f16(s[nr][g], a0, q[0], q[1]);
+                        mma_f16(s[nr][g], a1, q[2], q[3]);
+                    }
+                }
+            }
+            const uint8_t* kzp = mt + u * Lay::kMeta + 2 * Lay::kScaleArea + quad * GR;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float z[GR];
+#pragma unroll
+                for (int g = 0; g < GR; ++g) z[g] = (float)kzp[8 * GR * h + g];
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (t > bound[nr][e]) a[nr][2 * h + e] = -INFINITY;
-                // scales past the context may hold anything: their weights must be 0
-                if (t >= L)
-#pragma unroll
-                    for (int g = 0; g < GR; ++g) vs[h][g] = 0.f;
+                    for (int e = 0; e < 2; ++e) {
+                        float v = fmaf(-z[0], qsum[nr][0][e], s[nr][0][2 * h + e]) * ks[u][h][0];
+                        if constexpr (GR == 2)
+                            v = fmaf(fmaf(-z[1], qsum[nr][1][e], s[nr][1][2 * h + e]), ks[u][h][1],
+                                     v);
+                        a[u][nr][2 * h + e] = v * rowmul[nr][e];
+                    }
             }
+        }
+
+        // ---- mask, online softmax (lazy max) ----
+        if (take < 2 || tok0 + 2 * kBS - 1 > last_q) {   // the ends of a share or a context
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = tok0 + 16 * u + quad + 8 * h;
+                    const bool here = u >= half && u < half + take;
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (!here || t > bound[nr][e]) a[u][nr][2 * h + e] = -INFINITY;
+                    // scales past the context may hold anything: their weights must be 0
+                    if (!here || t >= L)
+#pragma unroll
+                        for (int g = 0; g < GR; ++g) vs[u][h][g] = 0.f;
+                }
         }
         bool raise = false;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                raise |= fmaxf(a[nr][e], a[nr][2 + e]) > m_run[nr][e] + kLazyMax;
+                raise |= fmaxf(fmaxf(a[0][nr][e], a[0][nr][2 + e]),
+                               fmaxf(a[1][nr][e], a[1][nr][2 + e])) > m_run[nr][e] + kLazyMax;
 #pragma unroll
-        for (int g = 0; g < GR; ++g) raise |= fmaxf(vs[0][g], vs[1][g]) > vref[g];
+        for (int g = 0; g < GR; ++g)
+            raise |= fmaxf(fmaxf(vs[0][0][g], vs[0][1][g]), fmaxf(vs[1][0][g], vs[1][1][g])) >
+                     vref[g];
         if (__any_sync(0xffffffffu, raise)) {   // rare: a row's maximum or a V reference moves
             float vfix[GR];
 #pragma unroll
             for (int g = 0; g < GR; ++g) {
-                float mx = fmaxf(vs[0][g], vs[1][g]);
+                float mx = fmaxf(fmaxf(vs[0][0][g], vs[0][1][g]), fmaxf(vs[1][0][g], vs[1][1][g]));
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -543,7 +576,8 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(a[nr][e], a[nr][2 + e]);
+                    float mx = fmaxf(fmaxf(a[0][nr][e], a[0][nr][2 + e]),
+                                     fmaxf(a[1][nr][e], a[1][nr][2 + e]));
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1)
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -566,52 +600,49 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                     }
                 }
         }
-        float vmul[2][GR];
 #pragma unroll
-        for (int g = 0; g < GR; ++g) {
-            vmul[0][g] = vs[0][g] * vinv[g];
-            vmul[1][g] = vs[1][g] * vinv[g];
-        }
-        uint32_t pb[NR][GR][2];          // P^T operand: tokens 2 qc, + 1 / 2 qc + 8, + 9 of row quad
+        for (int u = 0; u < 2; ++u) {
+            uint32_t pb[NR][GR][2];      // P^T operand: tokens 2 qc, + 1 / 2 qc + 8, + 9 of row quad
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            float w[4];
+            for (int nr = 0; nr < NR; ++nr) {
+                float w[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                w[e] = pa::ex2(a[nr][e] - m_ref[nr][e]);
-                w[2 + e] = pa::ex2(a[nr][2 + e] - m_ref[nr][e]);
-                l_run[nr][e] += w[e] + w[2 + e];
+                for (int e = 0; e < 2; ++e) {
+                    w[e] = pa::ex2(a[u][nr][e] - m_ref[nr][e]);
+                    w[2 + e] = pa::ex2(a[u][nr][2 + e] - m_ref[nr][e]);
+                    l_run[nr][e] += w[e] + w[2 + e];
+                }
+#pragma unroll
+                for (int g = 0; g < GR; ++g)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float m = vs[u][h][g] * vinv[g];
+                        pb[nr][g][h] = movmatrix(pack_half2(w[2 * h] * m, w[2 * h + 1] * m));
+                    }
             }
+            // ---- O^T += V codes^T P^T, and the zero points' sums ----
+            const uint32_t vb = kb + u * Lay::kBlockCodes + Lay::kTile;
 #pragma unroll
-            for (int g = 0; g < GR; ++g)
+            for (int pp = 0; pp < CH / 2; ++pp) {
+                uint32_t rr[4];
+                pa::ldmatrix_x4_trans(vb ^ (32 * pp), rr[0], rr[1], rr[2], rr[3]);
+                const int g = pp * 2 * GR / CH;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    pb[nr][g][h] = movmatrix(
-                        pack_half2(w[2 * h] * vmul[h][g], w[2 * h + 1] * vmul[h][g]));
-        }
-
-        // ---- O^T += V codes^T P^T, and the zero points' sums ----
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t lo[4], hi[4];
+                    unpack(rr[2 * j], lo);
+                    unpack(rr[2 * j + 1], hi);
+                    const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]};
+                    const uint32_t a1[4] = {lo[2], lo[3], hi[2], hi[3]};
 #pragma unroll
-        for (int pp = 0; pp < CH / 2; ++pp) {
-            uint32_t rr[4];
-            pa::ldmatrix_x4_trans(vb ^ (32 * pp), rr[0], rr[1], rr[2], rr[3]);
-            const int g = pp * 2 * GR / CH;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t lo[4], hi[4];
-                unpack(rr[2 * j], lo);
-                unpack(rr[2 * j + 1], hi);
-                const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]};
-                const uint32_t a1[4] = {lo[2], lo[3], hi[2], hi[3]};
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    mma_f16(o[nr][2 * pp + j][0], a0, pb[nr][g][0], pb[nr][g][1]);
-                    mma_f16(o[nr][2 * pp + j][1], a1, pb[nr][g][0], pb[nr][g][1]);
+                    for (int nr = 0; nr < NR; ++nr) {
+                        mma_f16(o[nr][2 * pp + j][0], a0, pb[nr][g][0], pb[nr][g][1]);
+                        mma_f16(o[nr][2 * pp + j][1], a1, pb[nr][g][0], pb[nr][g][1]);
+                    }
                 }
             }
-        }
-        {
             // row 0 of a tile of its own: the zero points of tokens 2 qc, + 1 and 2 qc + 8, + 9
+            const uint8_t* vzp = mt + u * Lay::kMeta + 2 * Lay::kScaleArea + Lay::kZpArea;
             uint32_t y0 = 0, y1 = 0;
             if (quad == 0) {
                 if constexpr (GR == 2) {
@@ -631,19 +662,19 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                     mma_f16(oz[nr][g], az, pb[nr][g][0], pb[nr][g][1]);
             }
         }
-        if (half || k == n - 1) {
+        k += take;
+        half += take;
+        if (half == 2) {
             __syncwarp();
-            if (issued < pairs) {        // into the stage just read
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                issue();
-            }
-            if (++st == S) st = 0, phase ^= 1;
+            issue();                     // into the stage just read
+            half = 0;
+            if (++st == S) st = 0;
         }
-        ++cur.b;
+        cur.b += take;
         const bool seg_done = cur.b == cur.nbs;
-        if (seg_done || k == n - 1) {
+        if (seg_done || k == n) {
             finish_segment(seg_b0 == 0 && seg_done, seg_first ? 0 : 1, min(cur.b * kBS, L));
-            if (k == n - 1) {
+            if (k == n) {
                 if (lane == 0)
                     record_last_segment(p, wid, f1, B, seg_done, seg_b0, cur.nbs - cur.b,
                                         seg_first, q0, rows);
@@ -655,14 +686,11 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             start_segment();
         }
     }
-    // drain: no copy of this warp may still be in flight when it exits
-    for (int k = consumed; k < issued; ++k)
-        if (!pa::mbar_wait(bars + 8 * (k % S), (k / S) & 1, p.err, pa::ERR_WAIT_DRAIN)) break;
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <typename TQ, int D, int NR>
-pa_status launch_int4(const pa::DecodeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
-                      pa::sched::Params prm, const Q4Extra& x) {
+pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, const Q4Extra& x) {
     using Lay = Q4Layout<D>;
     auto kern = paged_decode_int4_kernel<TQ, D, NR>;
     static bool attr_set = false;   // per instantiation; benign race (idempotent)
@@ -688,13 +716,17 @@ pa_status launch_int4(const pa::DecodeArgs& a, const CUtensorMap& mk, const CUte
     const pa::BalancedShape shape = pa::balanced_shape(a.num_seqs, a.num_heads, a.num_kv_heads,
                                                        a.head_dim, a.max_q_len, a.max_context_len,
                                                        pa::kTileInt4);
+    // Slots of 8 NR rows: with 8 the workspace, sized for 2048 workers' slots of 16 and
+    // more rows, holds those of 16 warps on every SM.
+    prm.rows_per_tile = 8 * NR;
+    prm.slot_bytes = (int)pa::sched::slot_bytes(8 * NR, D);
+    const int64_t room = (shape.workspace_bytes - shape.cum_bytes) / (2 * prm.slot_bytes);
     const int64_t workers =
-        std::min<int64_t>((int64_t)ctas * sms * kWorkerWarps, shape.workers);
+        std::min({(int64_t)ctas * sms * kWorkerWarps, shape.virtual_blocks, room});
     prm.workers = (int)workers;
     const int grid = (int)((workers + kWorkerWarps - 1) / kWorkerWarps);
     if (pa_status s = pa::cuda_status(
-            pa::launch_pdl(kern, dim3(grid), dim3(kWorkerWarps * 32), smem, a.stream, mk, mv, prm,
-                           x),
+            pa::launch_pdl(kern, dim3(grid), dim3(kWorkerWarps * 32), smem, a.stream, prm, x),
             "int4 decode launch"))
         return s;
     const int row_slots = (int)std::min<int64_t>(kBS, (int64_t)(a.num_heads / a.num_kv_heads) *
@@ -705,14 +737,13 @@ pa_status launch_int4(const pa::DecodeArgs& a, const CUtensorMap& mk, const CUte
 }
 
 template <typename TQ>
-pa_status dispatch(const pa::DecodeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
-                   const pa::sched::Params& b, const Q4Extra& x) {
+pa_status dispatch(const pa::DecodeArgs& a, const pa::sched::Params& b, const Q4Extra& x) {
     const bool one = (int64_t)b.group * a.max_q_len <= 8;
     if (a.head_dim == 128)
-        return one ? launch_int4<TQ, 128, 1>(a, mk, mv, b, x)
-                   : launch_int4<TQ, 128, 2>(a, mk, mv, b, x);
-    return one ? launch_int4<TQ, 64, 1>(a, mk, mv, b, x)
-               : launch_int4<TQ, 64, 2>(a, mk, mv, b, x);
+        return one ? launch_int4<TQ, 128, 1>(a, b, x)
+                   : launch_int4<TQ, 128, 2>(a, b, x);
+    return one ? launch_int4<TQ, 64, 1>(a, b, x)
+               : launch_int4<TQ, 64, 2>(a, b, x);
 }
 
 }  // namespace
@@ -728,13 +759,6 @@ pa_status launch_decode_int4(const DecodeArgs& a) {
     const BalancedShape shape = balanced_shape(a.num_seqs, a.num_heads, a.num_kv_heads,
                                                a.head_dim, a.max_q_len, a.max_context_len,
                                                kTileInt4);
-    CUtensorMap mk, mv;   // rows of head_dim / 2 bytes
-    if (pa_status s =
-            cache_tensor_map(&mk, a.k_cache, a.num_blocks, a.num_kv_heads, a.head_dim / 2, 1))
-        return s;
-    if (pa_status s =
-            cache_tensor_map(&mv, a.v_cache, a.num_blocks, a.num_kv_heads, a.head_dim / 2, 1))
-        return s;
     pa::sched::Params b{};
     b.out = a.out;
     b.q = a.q;
@@ -754,9 +778,10 @@ pa_status launch_decode_int4(const DecodeArgs& a) {
     b.slot_bytes = (int)shape.slot_bytes;
     b.scale_log2 = a.scale * kLog2e;
     b.out_f32 = a.out_dtype == PA_F32;
-    const Q4Extra x{a.k_scale, a.v_scale, a.k_zp, a.v_zp};
-    return a.q_dtype == PA_BF16 ? dispatch<__nv_bfloat16>(a, mk, mv, b, x)
-                                : dispatch<__half>(a, mk, mv, b, x);
+    const Q4Extra x{static_cast<const uint8_t*>(a.k_cache),
+                    static_cast<const uint8_t*>(a.v_cache), a.k_scale, a.v_scale, a.k_zp, a.v_zp};
+    return a.q_dtype == PA_BF16 ? dispatch<__nv_bfloat16>(a, b, x)
+                                : dispatch<__half>(a, b, x);
 }
 
 }  // namespace pa

@@ -30,9 +30,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // 16-bit elements: box 16 rows x 64 columns with 128-byte swizzle (head_dim
 // 128 takes two boxes). 8-bit codes: box 16 rows x head_dim, 128-byte swizzle
 // for head_dim 128 and 64-byte swizzle for head_dim 64 (one swizzle span per
-// row either way). 4-bit codes are mapped as their bytes, d = head_dim / 2 of
-// them a row: rows of 64 bytes as above, rows of 32 bytes with the 32-byte
-// swizzle.
+// row either way).
 pa_status make_map(CUtensorMap* m, const void* cache, int num_blocks, int hkv, int d,
                    int elem_bytes) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
@@ -45,9 +43,8 @@ pa_status make_map(CUtensorMap* m, const void* cache, int num_blocks, int hkv, i
     cuuint32_t estr[2] = {1, 1};
     const CUtensorMapDataType type =
         elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    const CUtensorMapSwizzle swz = (elem_bytes == 1 && d == 64)   ? CU_TENSOR_MAP_SWIZZLE_64B
-                                   : (elem_bytes == 1 && d == 32) ? CU_TENSOR_MAP_SWIZZLE_32B
-                                                                  : CU_TENSOR_MAP_SWIZZLE_128B;
+    const CUtensorMapSwizzle swz = (elem_bytes == 1 && d == 64) ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                                : CU_TENSOR_MAP_SWIZZLE_128B;
     CUresult r = fn(m, type, 2, const_cast<void*>(cache), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
