@@ -157,11 +157,18 @@ struct Q4Layout {
 // w (B / W) + w (B mod W) / W; the 64-bit divisions are a quarter of a share's
 // fixed cost.
 struct Shares {
-    uint32_t each, rest, W;
-    __device__ __forceinline__ Shares(int64_t B, int64_t W_)
-        : each((uint32_t)B / (uint32_t)W_), rest((uint32_t)B % (uint32_t)W_), W((uint32_t)W_) {}
-    __device__ __forceinline__ int64_t start(int64_t w) const {
-        return (int64_t)((uint32_t)w * each + (uint32_t)w * rest / W);
+    uint32_t B, each, rest, W;
+    __device__ __forceinline__ Shares(int64_t B_, int64_t W_)
+        : B((uint32_t)B_), each(B / (uint32_t)W_), rest(B % (uint32_t)W_), W((uint32_t)W_) {}
+    __device__ __forceinline__ uint32_t start(uint32_t w) const {
+        return w * each + w * rest / W;
+    }
+    // the share that holds block f: an estimate in floating point, then exact steps
+    __device__ __forceinline__ uint32_t of(uint32_t f) const {
+        uint32_t w = min(W - 1, (uint32_t)(((float)f + 0.5f) * (float)W / (float)B));
+        while (start(w) > f) --w;
+        while (start(w + 1) <= f) ++w;
+        return w;
     }
 };
 
@@ -202,10 +209,9 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     const int64_t B = cum[n_seqs];
     const int64_t wid = (int64_t)blockIdx.x * kWorkerWarps + warp;
     const int64_t W = share_count(p, B);
-    if (lane == 0) write_merge_record(p, wid, 0, 0, 0);   // none unless set at the end
     if (wid >= W) return;             // the grid's last CTA may have spare warps
     const Shares shares(B, W);
-    const int64_t f0 = shares.start(wid), f1 = shares.start(wid + 1);
+    const int64_t f0 = shares.start((uint32_t)wid), f1 = shares.start((uint32_t)wid + 1);
     const int n = (int)(f1 - f0);
     if (n <= 0) return;
 
@@ -674,12 +680,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
         const bool seg_done = cur.b == cur.nbs;
         if (seg_done || k == n) {
             finish_segment(seg_b0 == 0 && seg_done, seg_first ? 0 : 1, min(cur.b * kBS, L));
-            if (k == n) {
-                if (lane == 0)
-                    record_last_segment(p, wid, f1, B, seg_done, seg_b0, cur.nbs - cur.b,
-                                        seg_first, q0, rows);
-                break;
-            }
+            if (k == n) break;
             next_segment(p, cur, cum, chunks);
             seg_b0 = 0;
             seg_first = false;
@@ -687,6 +688,134 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Merges the pieces of the segments that share boundaries cut (log-sum-exp rule):
+// an item is a (sequence, KV head, row chunk, query row), served by `wpr` of a
+// CTA's warps, which take its pieces in turn and meet in shared memory. A warp
+// asks for its first eight pieces' columns beside all of the row's (m, l), from
+// which it gets the weights and the denominator. Few long sequences are cut into
+// a hundred pieces each: one warp a row waited for its loads 14 times over (14 us
+// behind the long-context step), eight do twice. Merging in the decode kernel, by
+// the last piece to finish, was slower (55.5 us against 48.8 for the Llama-3-8B
+// step): equal shares end together, so nothing hides it, and a warp that folds
+// all of a segment's rows waits longer than a grid of warps that fold one each.
+constexpr int kMergeWarps = 8;
+template <typename TQ, int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::sched::Params p,
+                                                                      int max_chunks,
+                                                                      int row_slots, int wpr) {
+    using namespace pa::sched;
+    constexpr int EPL = D / 32, kUnroll = 8;
+    __shared__ __align__(16) float part[kMergeWarps][D];
+    pa::grid_dependents_launch();
+    pa::grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp & (wpr - 1);
+    uint32_t item = blockIdx.x * (kMergeWarps / wpr) + warp / wpr;
+    const int row = item % row_slots;
+    item /= row_slots;
+    const int c = item % max_chunks;
+    item /= max_chunks;
+    const int g = item % p.num_kv_heads, s = item / p.num_kv_heads;
+    const int RT = p.rows_per_tile, G = p.group;
+    int q0 = 0, np = 0, first_slot = 0;
+    uint32_t wa = 0;
+    if (s < p.num_seqs) {                // warp-uniform
+        const int base = __ldcg(p.cum_out + s), next = __ldcg(p.cum_out + s + 1);
+        const int64_t B = __ldcg(p.cum_out + p.num_seqs);
+        const int r = query_run(p.qsl, s, &q0);
+        const int rows = min(RT, G * r - c * RT);
+        uint32_t fa = base + g * ((next - base) / p.num_kv_heads), nb = (next - base) / p.num_kv_heads;
+        if (G * r > RT) {                // several chunks: blocks of the ones before this
+            const int L = __ldg(p.context_lens + s);
+            for (int i = 0; i < c; ++i) fa += chunk_blocks(p, L, r, 0, i);
+            nb = rows > 0 ? chunk_blocks(p, L, r, 0, c) : 0;
+        }
+        if (row < rows && nb > 0) {
+            const Shares shares(B, share_count(p, B));
+            wa = shares.of(fa);
+            const uint32_t wb = shares.of(fa + nb - 1);
+            first_slot = shares.start(wa) < fa ? 1 : 0;
+            np = wb > wa ? (int)(wb - wa) + 1 : 0;   // one share: already written
+        }
+    }
+    auto piece = [&](int i) {
+        return Slot(p.slots + (2 * ((int64_t)wa + i) + (i == 0 ? first_slot : 0)) * p.slot_bytes, RT);
+    };
+    float w[kUnroll], v[kUnroll][EPL];   // a batch of this warp's pieces: m (or -inf) and columns
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+            const int i = i0 + j * wpr;
+            w[j] = -INFINITY;
+            if (i >= np) continue;       // warp-uniform
+            const Slot sl = piece(i);
+            const float* src = sl.o + (int64_t)row * D + lane * EPL;
+            if constexpr (EPL == 4) {
+                const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+                v[j][0] = t.x, v[j][1] = t.y, v[j][2] = t.z, v[j][3] = t.w;
+            } else {
+                const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+                v[j][0] = t.x, v[j][1] = t.y;
+            }
+            w[j] = __ldcg(sl.m + row);   // -inf where the piece has no visible key
+        }
+    };
+    load(sub);                           // on the way beside the weights
+    float M = -INFINITY, den = 0.f, acc[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+    for (int i = lane; i < np; i += 32) {
+        const Slot sl = piece(i);
+        const float l = __ldcg(sl.l + row), m = __ldcg(sl.m + row);
+        if (m == -INFINITY && l == 0.f) continue;
+        const float top = fmaxf(M, m);
+        den = den * exp2f(M - top) + l * exp2f(m - top);
+        M = top;
+    }
+    {
+        float top = M;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        den *= M == -INFINITY ? 1.f : exp2f(M - top);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+        M = top;
+    }
+    for (int i0 = sub; i0 < np; i0 += kUnroll * wpr) {
+        if (i0 != sub) load(i0);
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+            if (i0 + j * wpr >= np || w[j] == -INFINITY) continue;
+            const float f = exp2f(w[j] - M);
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) acc[e] = fmaf(f, v[j][e], acc[e]);
+        }
+    }
+    if (wpr > 1) {                       // the same for the whole grid
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) part[warp][lane * EPL + e] = acc[e];
+        __syncthreads();
+        if (sub != 0 || np == 0) return;
+        for (int i = 1; i < wpr; ++i)
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) acc[e] += part[warp + i][lane * EPL + e];
+    }
+    if (np == 0) return;
+    const int gr = c * RT + row;
+    const int64_t out = ((int64_t)(q0 + gr / G) * p.num_heads + g * G + gr % G) * D + lane * EPL;
+    const float inv = 1.f / den;
+    if (p.out_f32) {
+        float* dst = static_cast<float*>(p.out) + out;
+        if constexpr (EPL == 4)
+            *reinterpret_cast<float4*>(dst) =
+                make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+        else
+            *reinterpret_cast<float2*>(dst) = make_float2(acc[0] * inv, acc[1] * inv);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) store_out<TQ>(p.out, out + e, acc[e] * inv, 0);
 }
 
 template <typename TQ, int D, int NR>
@@ -721,19 +850,26 @@ pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, const Q4Ex
     prm.rows_per_tile = 8 * NR;
     prm.slot_bytes = (int)pa::sched::slot_bytes(8 * NR, D);
     const int64_t room = (shape.workspace_bytes - shape.cum_bytes) / (2 * prm.slot_bytes);
-    const int64_t workers =
-        std::min({(int64_t)ctas * sms * kWorkerWarps, shape.virtual_blocks, room});
+    const int64_t workers = std::min({(int64_t)ctas * sms * kWorkerWarps, shape.virtual_blocks, room});
     prm.workers = (int)workers;
     const int grid = (int)((workers + kWorkerWarps - 1) / kWorkerWarps);
     if (pa_status s = pa::cuda_status(
             pa::launch_pdl(kern, dim3(grid), dim3(kWorkerWarps * 32), smem, a.stream, prm, x),
             "int4 decode launch"))
         return s;
-    const int row_slots = (int)std::min<int64_t>(kBS, (int64_t)(a.num_heads / a.num_kv_heads) *
-                                                          a.max_q_len);
-    return pa::cuda_status(pa::sched::launch_segment_reduce<TQ, D>(prm, (int)shape.max_chunks,
-                                                                    row_slots, a.stream),
-                           "segment reduce launch");
+    // rows of the fullest chunk, and chunks, of the longest query run; the workers of a
+    // segment on average decide how many warps share a row
+    const int64_t rows = (int64_t)prm.group * a.max_q_len;
+    const int row_slots = (int)std::min<int64_t>(8 * NR, rows);
+    const int chunks = (int)((rows + 8 * NR - 1) / (8 * NR));
+    const int64_t segments = (int64_t)a.num_seqs * a.num_kv_heads * chunks;
+    int wpr = 1;
+    while (wpr < kMergeWarps && workers > 8 * wpr * segments) wpr *= 2;
+    const int64_t items = segments * row_slots, per = kMergeWarps / wpr;
+    return pa::cuda_status(
+        pa::launch_pdl(int4_merge_kernel<TQ, D>, dim3((unsigned)((items + per - 1) / per)),
+                       dim3(32 * kMergeWarps), 0, a.stream, prm, chunks, row_slots, wpr),
+        "int4 merge launch");
 }
 
 template <typename TQ>
