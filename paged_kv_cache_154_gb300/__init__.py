@@ -111,11 +111,16 @@ def version() -> str:
     return lib().pa_version().decode()
 
 
+_CODES: dict = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    return {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32,
-            torch.int8: PA_INT8, torch.float8_e4m3fn: PA_FP8_E4M3,
-            torch.uint8: PA_INT4}[t.dtype]
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32,
+                       torch.int8: PA_INT8, torch.float8_e4m3fn: PA_FP8_E4M3,
+                       torch.uint8: PA_INT4})
+    return _CODES[t.dtype]
 
 
 def _head_dim(cache) -> int:
@@ -130,11 +135,22 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream=None) -> Optional[int]:
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    """The handle of `stream`, or of the current device's current stream (asked
+    for directly: building torch's Stream object takes 3 us a call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = torch.cuda.current_device
+        _raw_stream = ((lambda: raw(device())) if raw is not None else
+                       (lambda: torch.cuda.current_stream().cuda_stream))
+    return _raw_stream()
 
 
 # ---------------------------------------------------------------------------
@@ -398,7 +414,7 @@ def decode_shared_prefix(out, q, k_cache, v_cache, block_tables, context_lens,
 # ---------------------------------------------------------------------------
 
 def _shaped(name: str, t, shape, dtype) -> None:
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
 
 

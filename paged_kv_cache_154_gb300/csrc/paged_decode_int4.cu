@@ -832,15 +832,23 @@ pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, const Q4Ex
         attr_set = true;
     }
     const int smem = Lay::smem_bytes(a.num_seqs);
-    int dev = 0, sms = 0, ctas = 0;
+    // the answers of the last call's queries, which cost as much as a launch
+    thread_local int last_dev = -1, last_smem = -1, sms = 0, ctas = 0;
+    int dev = 0;
     if (pa_status s = pa::cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return s;
-    if (pa_status s = pa::cuda_status(
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "SM count"))
-        return s;
-    if (pa_status s = pa::cuda_status(
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kern, kWorkerWarps * 32, smem),
-            "occupancy query"))
-        return s;
+    if (dev != last_dev || smem != last_smem) {
+        last_dev = -1;
+        if (pa_status s = pa::cuda_status(
+                cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "SM count"))
+            return s;
+        if (pa_status s =
+                pa::cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                                    &ctas, kern, kWorkerWarps * 32, smem),
+                                "occupancy query"))
+            return s;
+        last_dev = dev;
+        last_smem = smem;
+    }
     if (ctas < 1) return pa::fail(PA_ERR_UNSUPPORTED, "int4 decode kernel does not fit on an SM");
     const pa::BalancedShape shape = pa::balanced_shape(a.num_seqs, a.num_heads, a.num_kv_heads,
                                                        a.head_dim, a.max_q_len, a.max_context_len,
