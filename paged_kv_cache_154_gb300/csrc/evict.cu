@@ -59,9 +59,7 @@ struct Row {
         const int q = pos ? pos[j] : -1;
         return q >= 0 ? q : shift + j;
     }
-    __device__ __forceinline__ uint32_t key(int j) const {
-        const int q = position(j);
-        const float x = w[j];   // loaded beside the position, not after it
+    __device__ __forceinline__ uint32_t key(int q, float x) const {
         return q < sinks || q >= first_recent ? kProtected : score_key(x);
     }
 };
@@ -72,8 +70,6 @@ constexpr int kBins = 2048;
 __device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : d == 1 ? 10 : 0; }
 __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kMaxCluster = 8;
 // shared memory of a CTA: one histogram a digit, then the keys of its slots
 constexpr int kHistBytes = kDigits * kBins * 4;
@@ -106,27 +102,30 @@ __device__ __forceinline__ uint4 load_remote(uint32_t addr) {
 }
 
 // A cluster of CTAs a (KV head, sequence), each CTA a contiguous part of the row
-// (CL CTAs; 1: no cluster). The n-th largest key by three radix steps over keys
-// held in shared memory (KEYS; computed again from the scores when a part is too
-// long for that), then one walk that counts and one that emits, every warp over
-// a contiguous range of slots with ballots, so that the lists come out in slot
-// order. Bound by latency: barriers, one read of scores and positions, and the
-// histogram's shared-memory atomics, which is why digits are 11 bits (the first
-// holds the exponent and two more bits, so that like-sized scores spread) and
-// why every warp finds the digit for itself from the chunks' sums.
-template <int CL, bool KEYS>
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const SelectParams p) {
+// (CL CTAs; 1: no cluster). One pass over scores and positions copies the slots
+// below n to the output (those of evicted tokens are written again later) and
+// leaves keys in shared memory (KEYS; computed again from the scores when a part
+// is too long for that). Then the n-th largest key by three radix steps, one walk
+// over the keys that counts and one that emits, every warp over a contiguous
+// range of slots with ballots, so that the lists come out in slot order. Bound by
+// latency: barriers, the one read, and the histogram's shared-memory atomics,
+// which is why digits are 11 bits (the first holds the exponent and two more
+// bits, so that like-sized scores spread) and why every warp finds the digit for
+// itself from the chunks' sums. Copying inside the emitting walk cost a memory
+// round trip for every 32 slots of a warp (131072 tokens: 83 us).
+template <int CL, int T, bool KEYS>   // CTAs a row, threads a CTA
+__global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
+    constexpr int kWarps = T / 32;
     extern __shared__ __align__(16) uint32_t smem[];
     uint32_t* const hist = smem;                       // [kDigits][kBins]
     uint32_t* const keys = smem + kDigits * kBins;
-    __shared__ __align__(16) int warp_counts[kSelectWarps][4];   // gt, eq, gt below n, eq below n
+    __shared__ __align__(16) int warp_counts[kWarps][4];   // gt, eq, gt below n, eq below n
     __shared__ __align__(16) int cta_counts[4];
     __shared__ uint32_t chunk_sums[kDigits][kBins / 128];
-    static_assert(kBins / 128 <= kSelectWarps, "a warp a chunk");
     const int s = blockIdx.z, g = blockIdx.y, part = CL == 1 ? 0 : (int)cluster_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pa::grid_dependents_launch();
-    for (int i = tid; i < kDigits * kBins / 4; i += kSelectThreads)
+    for (int i = tid; i < kDigits * kBins / 4; i += T)
         reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     pa::grid_dependency_wait();
     const int64_t sg = (int64_t)s * p.num_kv_heads + g;
@@ -142,9 +141,9 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
     // this CTA's slots, and this warp's of them
     const int per = ((L + CL - 1) / CL + 31) / 32 * 32;
     const int a0 = min(L, part * per), a1 = min(L, a0 + per);
-    const int seg = ((a1 - a0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int seg = ((a1 - a0 + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int j0 = min(a1, a0 + warp * seg), j1 = min(a1, j0 + seg);
-    auto key_at = [&](int j) { return KEYS ? keys[j - a0] : row.key(j); };
+    auto key_at = [&](int j) { return KEYS ? keys[j - a0] : row.key(row.position(j), row.w[j]); };
     auto sync = [&]() {
         if constexpr (CL == 1) __syncthreads();
         else cluster_sync();
@@ -154,11 +153,22 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
     uint32_t cut = 0, left = (uint32_t)n;
     const bool search = n > 0 && n < L;
     __syncthreads();                                   // the histograms are zero
-    if (search || KEYS) {
-#pragma unroll 4
-        for (int b = j0; b < j1; b += 32) {            // warp-uniform
-            const int j = b + lane;
-            const uint32_t k = j < j1 ? row.key(j) : 0u;
+    constexpr int kAhead = 4;                          // reads on the way together
+    for (int b0 = j0; b0 < j1; b0 += 32 * kAhead) {    // warp-uniform
+        float w[kAhead];
+        int pos[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int j = b0 + 32 * i + lane;
+            w[i] = 0.f, pos[i] = 0;
+            if (j < j1) w[i] = row.w[j], pos[i] = row.position(j);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int j = b0 + 32 * i + lane;
+            if (b0 + 32 * i >= j1) break;              // warp-uniform
+            const uint32_t k = row.key(pos[i], w[i]);
+            if (j < n && j < j1) w_out[j] = w[i], pos_out[j] = pos[i];
             if (KEYS && j < j1) keys[j - a0] = k;
             // protected tokens come in long runs: one addition for a warp's
             const uint32_t safe = __ballot_sync(0xffffffffu, j < j1 && k == kProtected);
@@ -187,24 +197,31 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
             if constexpr (CL > 1) {
                 // the cluster's sum, in registers until every CTA has read the parts
                 const int vecs = bins / 4;
-                uint4 t = make_uint4(0u, 0u, 0u, 0u);
-                if (tid < vecs)
+                constexpr int kMine = (kBins / 4 + T - 1) / T;
+                uint4 t[kMine];
 #pragma unroll
-                    for (int c = 0; c < CL; ++c) {
-                        const uint4 v = load_remote(remote(h + 4 * tid, c));
-                        t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
-                    }
+                for (int i = 0; i < kMine; ++i) {
+                    t[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (tid + i * T < vecs)
+#pragma unroll
+                        for (int c = 0; c < CL; ++c) {
+                            const uint4 v = load_remote(remote(h + 4 * (tid + i * T), c));
+                            t[i].x += v.x, t[i].y += v.y, t[i].z += v.z, t[i].w += v.w;
+                        }
+                }
                 cluster_sync();
-                if (tid < vecs) reinterpret_cast<uint4*>(h)[tid] = t;
+#pragma unroll
+                for (int i = 0; i < kMine; ++i)
+                    if (tid + i * T < vecs) reinterpret_cast<uint4*>(h)[tid + i * T] = t[i];
                 __syncthreads();
             }
             // a warp sums a chunk of 128 bins (chunk 0 the highest), then every warp finds the
             // chunk of the n-th key and the bin in it
             const int chunks = bins / 128;
-            if (warp < chunks) {
-                const uint4 v = *reinterpret_cast<const uint4*>(h + bins - 128 * (warp + 1) + 4 * lane);
+            for (int i = warp; i < chunks; i += kWarps) {
+                const uint4 v = *reinterpret_cast<const uint4*>(h + bins - 128 * (i + 1) + 4 * lane);
                 const uint32_t sum = __reduce_add_sync(0xffffffffu, v.x + v.y + v.z + v.w);
-                if (lane == 0) chunk_sums[d][warp] = sum;
+                if (lane == 0) chunk_sums[d][i] = sum;
             }
             __syncthreads();
             uint32_t upto = lane < chunks ? chunk_sums[d][lane] : 0u;
@@ -239,8 +256,6 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
             left -= __shfl_sync(0xffffffffu, before, owner);
             cut |= (uint32_t)__shfl_sync(0xffffffffu, bin, owner) << shift;
         }
-    } else {
-        __syncthreads();
     }
     // n == L: all stay; n == 0: none does
     const bool all = n == L, none = n == 0;
@@ -265,7 +280,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
     __syncthreads();
     int gt_before = 0, eq_before = 0, low = 0, ties_low = 0, gt_all = 0, eq_all = 0;
 #pragma unroll
-    for (int i = 0; i < kSelectWarps; ++i) {
+    for (int i = 0; i < kWarps; ++i) {
         const int4 c = *reinterpret_cast<const int4*>(warp_counts[i]);
         if (i < warp) gt_before += c.x, eq_before += c.y;
         gt_all += c.x, eq_all += c.y;
@@ -297,27 +312,30 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
         const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
         const int rank = kept + __popc(keeps & below);   // kept tokens before slot j
         if (j < j1) {
-            if (keep && j >= n) {
-                moves[rank - kept_low].x = j;
-            } else if (keep) {
-                w_out[j] = row.w[j];
-                pos_out[j] = row.position(j);
-            } else if (j < n) {
-                moves[j - rank].y = j;
-            }
+            if (keep && j >= n) moves[rank - kept_low].x = j;
+            if (!keep && j < n) moves[j - rank].y = j;
         }
         eq_before += __popc(eqs);
         kept += __popc(keeps);
     }
     sync();                                            // the list is whole
-    for (int i = part * kSelectThreads + tid; i < count; i += CL * kSelectThreads) {
-        const int2 m = __ldcg(moves + i);              // written by other CTAs of the cluster
-        w_out[m.y] = row.w[m.x];
-        pos_out[m.y] = row.position(m.x);
+    for (int i0 = part * T + tid; i0 < count; i0 += kAhead * CL * T) {
+        int2 m[kAhead];                                // written by other CTAs of the cluster
+        float w[kAhead];
+        int pos[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i * CL * T < count) m[i] = __ldcg(moves + i0 + i * CL * T);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i * CL * T < count) w[i] = row.w[m[i].x], pos[i] = row.position(m[i].x);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i * CL * T < count) w_out[m[i].y] = w[i], pos_out[m[i].y] = pos[i];
     }
     if (part == 0 && tid == 0) p.move_counts[sg] = count;
     sync();                                            // entries from n on are read no more
-    for (int j = max(n, a0) + tid; j < a1; j += kSelectThreads) {
+    for (int j = max(n, a0) + tid; j < a1; j += T) {
         w_out[j] = 0.f;
         pos_out[j] = -1;
     }
@@ -426,9 +444,9 @@ pa_status launch_move(const MoveParams& p, int num_seqs, cudaStream_t st) {
                            "move_tokens launch");
 }
 
-template <int CL, bool KEYS>
+template <int CL, int T, bool KEYS>
 pa_status launch_select_as(const SelectParams& p, int num_seqs, int keys, cudaStream_t st) {
-    auto kern = evict_select_kernel<CL, KEYS>;
+    auto kern = evict_select_kernel<CL, T, KEYS>;
     static bool attr_set = false;   // per instantiation; benign race (idempotent)
     if (!attr_set) {
         if (pa_status s = pa::cuda_status(
@@ -440,7 +458,7 @@ pa_status launch_select_as(const SelectParams& p, int num_seqs, int keys, cudaSt
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CL, p.num_kv_heads, num_seqs);
-    cfg.blockDim = dim3(kSelectThreads);
+    cfg.blockDim = dim3(T);
     cfg.dynamicSmemBytes = kHistBytes + (KEYS ? 4 * keys : 0);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -455,9 +473,17 @@ pa_status launch_select_as(const SelectParams& p, int num_seqs, int keys, cudaSt
     return pa::cuda_status(cudaLaunchKernelEx(&cfg, kern, p), "evict_select launch");
 }
 
+template <int CL>
+pa_status launch_select_cl(const SelectParams& p, int num_seqs, int keys, cudaStream_t st) {
+    // four to five slots a thread where an SM then holds several CTAs, more in long parts
+    if (keys <= 1280) return launch_select_as<CL, 256, true>(p, num_seqs, keys, st);
+    if (keys <= 4096) return launch_select_as<CL, 512, true>(p, num_seqs, keys, st);
+    return launch_select_as<CL, 1024, true>(p, num_seqs, keys, st);
+}
+
 // How many CTAs share a row: more while the rows alone leave SMs idle and a part
-// stays worth its barriers (2048 slots, 4 a thread), or while a part's keys do not
-// fit shared memory.
+// stays worth its barriers (2048 slots), or while a part's keys do not fit shared
+// memory.
 pa_status launch_select(const SelectParams& p, int num_seqs, cudaStream_t st) {
     const int64_t rows = (int64_t)num_seqs * p.num_kv_heads;
     int cl = 1;
@@ -465,12 +491,12 @@ pa_status launch_select(const SelectParams& p, int num_seqs, cudaStream_t st) {
                                 p.max_len / cl + 32 > kMaxKeys))
         cl *= 2;
     const int keys = ((p.max_len + cl - 1) / cl + 31) / 32 * 32;
-    if (keys > kMaxKeys) return launch_select_as<kMaxCluster, false>(p, num_seqs, keys, st);
+    if (keys > kMaxKeys) return launch_select_as<kMaxCluster, 1024, false>(p, num_seqs, keys, st);
     switch (cl) {
-        case 1: return launch_select_as<1, true>(p, num_seqs, keys, st);
-        case 2: return launch_select_as<2, true>(p, num_seqs, keys, st);
-        case 4: return launch_select_as<4, true>(p, num_seqs, keys, st);
-        default: return launch_select_as<8, true>(p, num_seqs, keys, st);
+        case 1: return launch_select_cl<1>(p, num_seqs, keys, st);
+        case 2: return launch_select_cl<2>(p, num_seqs, keys, st);
+        case 4: return launch_select_cl<4>(p, num_seqs, keys, st);
+        default: return launch_select_cl<8>(p, num_seqs, keys, st);
     }
 }
 

@@ -218,48 +218,57 @@ __global__ void __launch_bounds__(256) append_kv_int4_kernel(
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const T* h = reinterpret_cast<const T*>(&raw[which]);
-        float x[8], mn = 0.0f, mx = 0.0f;   // the range is widened to contain 0
+        float x[9], mn = 0.0f, mx = 0.0f;   // the range is widened to contain 0
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x[e] = to_f32<T>(h[e]);
-            mn = x[e] < mn ? x[e] : mn;
-            mx = x[e] > mx ? x[e] : mx;
+            mn = fminf(mn, x[e]);
+            mx = fmaxf(mx, x[e]);
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) {
-            const float a = __shfl_xor_sync(peers, mn, o);
-            const float b = __shfl_xor_sync(peers, mx, o);
-            mn = a < mn ? a : mn;
-            mx = b > mx ? b : mx;
+            mn = fminf(mn, __shfl_xor_sync(peers, mn, o));
+            mx = fmaxf(mx, __shfl_xor_sync(peers, mx, o));
         }
         float scale = __fdiv_rn(__fsub_rn(mx, mn), 15.0f);
         if (scale == 0.0f) scale = 1.0f;
+        x[8] = mn;                          // its quotient gives the zero point
         // rint(x / scale) by a product with the reciprocal: |x / scale| <= 15, so the product is
-        // within 15 * 2^-22 < 4e-6 of the fp32 quotient, and rounds to the same integer unless
-        // it is that near a tie (or the reciprocal is not a normal number). Then divide.
+        // within 15 * 2^-22 < 4e-6 of the fp32 quotient and rounds to the same integer unless
+        // it is that near a tie, which 16-bit inputs often are.
         constexpr float kRound = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer
         const float inv = __frcp_rn(scale);
-        int q[9];                               // the last: the zero point's quotient
+        int q[9];
         float far = 0.0f;                       // the largest distance from an integer
 #pragma unroll
         for (int e = 0; e < 9; ++e) {
-            const float v = e < 8 ? x[e & 7] : mn;
-            const float y = __fmaf_rn(v, inv, kRound);
+            const float y = __fmaf_rn(x[e], inv, kRound);
             q[e] = __float_as_int(y) - __float_as_int(kRound);
-            far = fmaxf(far, fabsf(__fmaf_rn(v, inv, __fsub_rn(kRound, y))));
+            far = fmaxf(far, fabsf(__fmaf_rn(x[e], inv, __fsub_rn(kRound, y))));
         }
-        if (!(far < 0.49999f) || !(scale > 1e-30f && scale < 1e30f)) {
+        if (!(scale > 1e-30f && scale < 1e30f)) {   // the reciprocal is no normal number
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = (int)rintf(__fdiv_rn(x[e], scale));
-            q[8] = (int)rintf(__fdiv_rn(mn, scale));
+            for (int e = 0; e < 9; ++e) q[e] = (int)rintf(__fdiv_rn(x[e], scale));
+        } else if (!(far < 0.49999f)) {
+            // Near the tie h = k + 1/2: r = x - h scale has the exact sign of x / scale - h (one
+            // rounding, of a difference that fits), and the quotient rounds to h itself, an
+            // even tie, iff |r| < scale * ulp(h) / 2 (half of that below h = 1/2, a power of
+            // two; x / scale is never a midpoint, that would take 25 bits of x).
+#pragma unroll
+            for (int e = 0; e < 9; ++e) {
+                const float k = (float)q[e], d = __fmaf_rn(x[e], inv, -k);
+                if (fabsf(d) < 0.49999f) continue;
+                const float t = k + copysignf(0.5f, d), r = __fmaf_rn(-t, scale, x[e]);
+                float ulp = __uint_as_float(__float_as_uint(t) & 0x7f800000u) * 0x1p-24f;
+                if (fabsf(t) == 0.5f && (r < 0.0f) == (t > 0.0f)) ulp *= 0.5f;
+                q[e] = (int)(fabsf(r) < scale * ulp ? rintf(t) : t + copysignf(0.5f, r));
+            }
         }
-        const int zp = q[8] > 0 ? 0 : (q[8] < -15 ? 15 : -q[8]);
+        const int zp = min(15, -q[8]);
+        // q >= q[8], as rounding keeps the order: only the top can leave 0 .. 15
         uint32_t word = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int code = q[e] + zp;
-            word |= (uint32_t)(code < 0 ? 0 : (code > 15 ? 15 : code)) << (4 * e);
-        }
+        for (int e = 0; e < 8; ++e) word |= (uint32_t)min(15, q[e] + zp) << (4 * e);
         reinterpret_cast<uint32_t*>(which ? v_cache : k_cache)[row * kPerRow + c] = word;
         if ((c & 7) == 0) {
             (which ? v_scale : k_scale)[row * kGroups + c / 8] = scale;
