@@ -102,17 +102,20 @@ __device__ __forceinline__ uint4 load_remote(uint32_t addr) {
 }
 
 // A cluster of CTAs a (KV head, sequence), each CTA a contiguous part of the row
-// (CL CTAs; 1: no cluster). One pass over scores and positions copies the slots
-// below n to the output (those of evicted tokens are written again later) and
-// leaves keys in shared memory (KEYS; computed again from the scores when a part
-// is too long for that). Then the n-th largest key by three radix steps, one walk
+// (CL CTAs; 1: no cluster). One pass over scores and positions leaves keys in
+// shared memory (KEYS; computed again from the scores when a part is too long for
+// that). Then the n-th largest key by three radix steps, one walk
 // over the keys that counts and one that emits, every warp over a contiguous
 // range of slots with ballots, so that the lists come out in slot order. Bound by
 // latency: barriers, the one read, and the histogram's shared-memory atomics,
 // which is why digits are 11 bits (the first holds the exponent and two more
 // bits, so that like-sized scores spread) and why every warp finds the digit for
-// itself from the chunks' sums. Copying inside the emitting walk cost a memory
-// round trip for every 32 slots of a warp (131072 tokens: 83 us).
+// itself from the chunks' sums. Nothing is written to global memory before the
+// emitting walk: a cluster barrier waits for stores on their way. Copying inside
+// that walk cost a memory round trip for every 32 slots of a warp, so it has a
+// loop of its own (131072 tokens: 83 us so, 41 us with the copy beside the first
+// read; clusters of 16 took 85 us, their barriers and remote reads outweigh the
+// halved parts).
 template <int CL, int T, bool KEYS>   // CTAs a row, threads a CTA
 __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
     constexpr int kWarps = T / 32;
@@ -168,7 +171,6 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
             const int j = b0 + 32 * i + lane;
             if (b0 + 32 * i >= j1) break;              // warp-uniform
             const uint32_t k = row.key(pos[i], w[i]);
-            if (j < n && j < j1) w_out[j] = w[i], pos_out[j] = pos[i];
             if (KEYS && j < j1) keys[j - a0] = k;
             // protected tokens come in long runs: one addition for a warp's
             const uint32_t safe = __ballot_sync(0xffffffffu, j < j1 && k == kProtected);
@@ -317,6 +319,21 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
         }
         eq_before += __popc(eqs);
         kept += __popc(keeps);
+    }
+    // The slots below n as they are; those of evicted tokens are written again below.
+    for (int b0 = j0; b0 < min(j1, n); b0 += 32 * kAhead) {
+        float w[kAhead];
+        int pos[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int j = b0 + 32 * i + lane;
+            if (j < min(j1, n)) w[i] = row.w[j], pos[i] = row.position(j);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int j = b0 + 32 * i + lane;
+            if (j < min(j1, n)) w_out[j] = w[i], pos_out[j] = pos[i];
+        }
     }
     sync();                                            // the list is whole
     for (int i0 = part * T + tid; i0 < count; i0 += kAhead * CL * T) {

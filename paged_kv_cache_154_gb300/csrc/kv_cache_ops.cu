@@ -184,13 +184,49 @@ __global__ void append_kv_fp8_kernel(const T* __restrict__ key, const T* __restr
     }
 }
 
+// Two fp32 numbers and the two-wide arithmetic on them (each operation rounds
+// as its scalar form does).
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float lo, float hi) {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    }
+    __device__ __forceinline__ float lo() const {
+        float a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+        return a;
+    }
+    __device__ __forceinline__ float hi() const {
+        float a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+        return b;
+    }
+};
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+
 // INT4 append: the formula of the INT8 path with 16 unsigned codes and one
 // (scale, zero point) per 64 elements. A thread holds 8 consecutive elements of
 // a K row and of the same V row (16-byte loads, 4-byte code stores), 8 threads a
 // group; the range is reduced over them with shuffles. 2 bytes in and 0.58 out
 // an element: bound by memory once nothing else is in the way, so the rows are
 // asked for before the slot is known, indexes are 32 bits wide (their 64-bit
-// divisions alone cost a third of the kernel) and codes come without divisions.
+// divisions alone cost a third of the kernel) and quotients come from one
+// reciprocal a group.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) append_kv_int4_kernel(
     const T* __restrict__ key, const T* __restrict__ value, uint8_t* __restrict__ k_cache,
@@ -218,7 +254,7 @@ __global__ void __launch_bounds__(256) append_kv_int4_kernel(
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const T* h = reinterpret_cast<const T*>(&raw[which]);
-        float x[9], mn = 0.0f, mx = 0.0f;   // the range is widened to contain 0
+        float x[8], mn = 0.0f, mx = 0.0f;   // the range is widened to contain 0
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x[e] = to_f32<T>(h[e]);
@@ -230,45 +266,48 @@ __global__ void __launch_bounds__(256) append_kv_int4_kernel(
             mn = fminf(mn, __shfl_xor_sync(peers, mn, o));
             mx = fmaxf(mx, __shfl_xor_sync(peers, mx, o));
         }
-        float scale = __fdiv_rn(__fsub_rn(mx, mn), 15.0f);
-        if (scale == 0.0f) scale = 1.0f;
-        x[8] = mn;                          // its quotient gives the zero point
-        // rint(x / scale) by a product with the reciprocal: |x / scale| <= 15, so the product is
-        // within 15 * 2^-22 < 4e-6 of the fp32 quotient and rounds to the same integer unless
-        // it is that near a tie, which 16-bit inputs often are.
-        constexpr float kRound = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer
-        const float inv = __frcp_rn(scale);
-        int q[9];
-        float far = 0.0f;                       // the largest distance from an integer
+        const float range = __fsub_rn(mx, mn);
+        float scale;
+        uint32_t word;
+        int zp;
+        if (range > 1e-28f && range < 1e30f) {
+            // Correctly rounded quotients by Markstein's theorem: with the correctly rounded
+            // reciprocal y of b, q = a y and r = a - b q (exact in one fused operation),
+            // q + r y is the rounded a / b. Then, adding 1.5 * 2^23 rounds to an integer in
+            // the low bits, and the codes are put together from those bits as they are: the
+            // excess of each over its code is the same number.
+            constexpr float kFifteenth = 1.0f / 15.0f, kRound = 12582912.0f;
+            const float s0 = __fmul_rn(range, kFifteenth);
+            scale = __fmaf_rn(__fmaf_rn(-s0, 15.0f, range), kFifteenth, s0);
+            const float inv = __frcp_rn(scale);
+            const float z0 = __fmul_rn(mn, inv);
+            const float z1 = __fmaf_rn(__fmaf_rn(-z0, scale, mn), inv, z0);
+            const float zr = __fadd_rn(z1, kRound);
+            zp = min(15, __float_as_int(kRound) - __float_as_int(zr));
+            const float top = __int_as_float(__float_as_int(kRound) + 15 - zp);
+            // no code is below 0: rounding keeps the order, and the zero point is -rint(mn / scale)
+            word = 0;
 #pragma unroll
-        for (int e = 0; e < 9; ++e) {
-            const float y = __fmaf_rn(x[e], inv, kRound);
-            q[e] = __float_as_int(y) - __float_as_int(kRound);
-            far = fmaxf(far, fabsf(__fmaf_rn(x[e], inv, __fsub_rn(kRound, y))));
-        }
-        if (!(scale > 1e-30f && scale < 1e30f)) {   // the reciprocal is no normal number
+            for (int e = 6; e >= 0; e -= 2) {
+                const F2 v(x[e], x[e + 1]), q = v * F2(inv, inv);
+                const F2 r = fma(q, F2(-scale, -scale), v);
+                const F2 y = fma(r, F2(inv, inv), q) + F2(kRound, kRound);
+                word = word * 16u + __float_as_uint(fminf(y.hi(), top));
+                word = word * 16u + __float_as_uint(fminf(y.lo(), top));
+            }
+            word -= (uint32_t)(__float_as_int(kRound) - zp) * 0x11111111u;
+        } else {                            // range 0, or too near the ends of fp32
+            scale = __fdiv_rn(range, 15.0f);
+            if (scale == 0.0f) scale = 1.0f;
+            zp = (int)-rintf(__fdiv_rn(mn, scale));
+            zp = zp < 0 ? 0 : min(15, zp);
+            word = 0;
 #pragma unroll
-            for (int e = 0; e < 9; ++e) q[e] = (int)rintf(__fdiv_rn(x[e], scale));
-        } else if (!(far < 0.49999f)) {
-            // Near the tie h = k + 1/2: r = x - h scale has the exact sign of x / scale - h (one
-            // rounding, of a difference that fits), and the quotient rounds to h itself, an
-            // even tie, iff |r| < scale * ulp(h) / 2 (half of that below h = 1/2, a power of
-            // two; x / scale is never a midpoint, that would take 25 bits of x).
-#pragma unroll
-            for (int e = 0; e < 9; ++e) {
-                const float k = (float)q[e], d = __fmaf_rn(x[e], inv, -k);
-                if (fabsf(d) < 0.49999f) continue;
-                const float t = k + copysignf(0.5f, d), r = __fmaf_rn(-t, scale, x[e]);
-                float ulp = __uint_as_float(__float_as_uint(t) & 0x7f800000u) * 0x1p-24f;
-                if (fabsf(t) == 0.5f && (r < 0.0f) == (t > 0.0f)) ulp *= 0.5f;
-                q[e] = (int)(fabsf(r) < scale * ulp ? rintf(t) : t + copysignf(0.5f, r));
+            for (int e = 0; e < 8; ++e) {
+                const int q = (int)rintf(__fdiv_rn(x[e], scale)) + zp;
+                word |= (uint32_t)(q < 0 ? 0 : min(15, q)) << (4 * e);
             }
         }
-        const int zp = min(15, -q[8]);
-        // q >= q[8], as rounding keeps the order: only the top can leave 0 .. 15
-        uint32_t word = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) word |= (uint32_t)min(15, q[e] + zp) << (4 * e);
         reinterpret_cast<uint32_t*>(which ? v_cache : k_cache)[row * kPerRow + c] = word;
         if ((c & 7) == 0) {
             (which ? v_scale : k_scale)[row * kGroups + c / 8] = scale;
@@ -306,8 +345,10 @@ struct Cached8 {
             return __half2float(reinterpret_cast<const __half*>(&raw)[e]);
         else if constexpr (KV == PA_BF16)
             return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(&raw)[e]);
-        else if constexpr (KV == PA_INT4)
-            return __fmul_rn((float)((int)(raw.x >> (4 * e) & 15u) - zp), scale);
+        else if constexpr (KV == PA_INT4)   // 2^23 + code as its bits, less 2^23 + zero point
+            return __fmul_rn(__fsub_rn(__uint_as_float((raw.x >> (4 * e) & 15u) | 0x4b000000u),
+                                       8388608.0f + (float)zp),
+                             scale);
         else if constexpr (KV == PA_INT8)
             return __fmul_rn((float)((int)reinterpret_cast<const int8_t*>(&raw)[e] - zp), scale);
         else

@@ -53,6 +53,7 @@ using pa::sched::kBS;
 using pa::sched::kWorkerWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyMax = 8.f;    // base-2 headroom before the running max is moved
+constexpr int kWholeTokens = 256;
 constexpr int ctas_per_sm(int d, int nr) { return d == 128 && nr == 2 ? 2 : 3; }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
@@ -179,6 +180,8 @@ struct Q4Extra {
     const float* v_scale;
     const int8_t* k_zp;
     const int8_t* v_zp;
+    int whole;              // a worker takes a whole segment instead of a share
+    int max_chunks;
 };
 
 // NR: tiles of 8 query rows (1: at most 8 rows per KV head; 2: chunks of 16)
@@ -206,12 +209,25 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     const uint8_t* const meta = mine + Lay::kMetaAt;
 
     build_prefix(cum, chunks, p);
-    const int64_t B = cum[n_seqs];
     const int64_t wid = (int64_t)blockIdx.x * kWorkerWarps + warp;
-    const int64_t W = share_count(p, B);
-    if (wid >= W) return;             // the grid's last CTA may have spare warps
-    const Shares shares(B, W);
-    const int64_t f0 = shares.start((uint32_t)wid), f1 = shares.start((uint32_t)wid + 1);
+    if (wid >= p.workers) return;     // the grid's last CTA may have spare warps
+    int64_t f0, f1;
+    if (x.whole) {                    // worker (s, g, c): its segment's blocks
+        const int c = (uint32_t)wid % x.max_chunks, sg = (uint32_t)wid / x.max_chunks;
+        const int s = sg / hkv, g = sg - s * hkv;
+        if (c >= chunks[s]) return;
+        int q0;
+        const int r = query_run(p.qsl, s, &q0);
+        const int L = __ldg(p.context_lens + s);
+        f0 = cum[s] + (int64_t)g * ((cum[s + 1] - cum[s]) / hkv);
+        for (int i = 0; i < c; ++i) f0 += chunk_blocks(p, L, r, 0, i);
+        f1 = f0 + chunk_blocks(p, L, r, 0, c);
+    } else {
+        const int64_t B = cum[n_seqs], W = share_count(p, B);
+        if (wid >= W) return;
+        const Shares shares(B, W);
+        f0 = shares.start((uint32_t)wid), f1 = shares.start((uint32_t)wid + 1);
+    }
     const int n = (int)(f1 - f0);
     if (n <= 0) return;
 
@@ -819,7 +835,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::
 }
 
 template <typename TQ, int D, int NR>
-pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, const Q4Extra& x) {
+pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, Q4Extra x) {
     using Lay = Q4Layout<D>;
     auto kern = paged_decode_int4_kernel<TQ, D, NR>;
     static bool attr_set = false;   // per instantiation; benign race (idempotent)
@@ -858,19 +874,25 @@ pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, const Q4Ex
     prm.rows_per_tile = 8 * NR;
     prm.slot_bytes = (int)pa::sched::slot_bytes(8 * NR, D);
     const int64_t room = (shape.workspace_bytes - shape.cum_bytes) / (2 * prm.slot_bytes);
-    const int64_t workers = std::min({(int64_t)ctas * sms * kWorkerWarps, shape.virtual_blocks, room});
+    const int64_t rows = (int64_t)prm.group * a.max_q_len;
+    const int chunks = (int)((rows + 8 * NR - 1) / (8 * NR));
+    const int64_t segments = (int64_t)a.num_seqs * a.num_kv_heads * chunks;
+    // Short contexts are not cut: a warp walks a segment of kWholeTokens in less than the
+    // merge's launch takes.
+    x.whole = a.max_context_len <= kWholeTokens;
+    x.max_chunks = chunks;
+    const int64_t workers =
+        x.whole ? segments
+                : std::min({(int64_t)ctas * sms * kWorkerWarps, shape.virtual_blocks, room});
     prm.workers = (int)workers;
     const int grid = (int)((workers + kWorkerWarps - 1) / kWorkerWarps);
     if (pa_status s = pa::cuda_status(
             pa::launch_pdl(kern, dim3(grid), dim3(kWorkerWarps * 32), smem, a.stream, prm, x),
             "int4 decode launch"))
         return s;
-    // rows of the fullest chunk, and chunks, of the longest query run; the workers of a
-    // segment on average decide how many warps share a row
-    const int64_t rows = (int64_t)prm.group * a.max_q_len;
+    if (x.whole) return PA_OK;
+    // the workers of a segment, on average, decide how many warps share a row's merge
     const int row_slots = (int)std::min<int64_t>(8 * NR, rows);
-    const int chunks = (int)((rows + 8 * NR - 1) / (8 * NR));
-    const int64_t segments = (int64_t)a.num_seqs * a.num_kv_heads * chunks;
     int wpr = 1;
     while (wpr < kMergeWarps && workers > 8 * wpr * segments) wpr *= 2;
     const int64_t items = segments * row_slots, per = kMergeWarps / wpr;
@@ -923,7 +945,8 @@ pa_status launch_decode_int4(const DecodeArgs& a) {
     b.scale_log2 = a.scale * kLog2e;
     b.out_f32 = a.out_dtype == PA_F32;
     const Q4Extra x{static_cast<const uint8_t*>(a.k_cache),
-                    static_cast<const uint8_t*>(a.v_cache), a.k_scale, a.v_scale, a.k_zp, a.v_zp};
+                    static_cast<const uint8_t*>(a.v_cache), a.k_scale, a.v_scale, a.k_zp, a.v_zp,
+                    0, 1};
     return a.q_dtype == PA_BF16 ? dispatch<__nv_bfloat16>(a, b, x)
                                 : dispatch<__half>(a, b, x);
 }
