@@ -92,6 +92,11 @@ __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(pa::smem_addr(p)), "r"(rank));
     return a;
 }
+__device__ __forceinline__ uint32_t load_remote1(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint4 load_remote(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -101,30 +106,51 @@ __device__ __forceinline__ uint4 load_remote(uint32_t addr) {
     return v;
 }
 
+// Four consecutive slots of a lane: `slots` of them are inside the row.
+__device__ __forceinline__ void load4(const float* w, float (&v)[4], int j, int slots, bool aligned) {
+    if (aligned && slots >= 4) {
+        const float4 t = *reinterpret_cast<const float4*>(w + j);
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < slots ? w[j + i] : 0.f;
+    }
+}
+__device__ __forceinline__ void load4(const int32_t* p, int (&v)[4], int j, int slots, bool aligned) {
+    if (aligned && slots >= 4) {
+        const int4 t = *reinterpret_cast<const int4*>(p + j);
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < slots ? p[j + i] : 0;
+    }
+}
+
 // A cluster of CTAs a (KV head, sequence), each CTA a contiguous part of the row
-// (CL CTAs; 1: no cluster). One pass over scores and positions leaves keys in
-// shared memory (KEYS; computed again from the scores when a part is too long for
-// that). Then the n-th largest key by three radix steps, one walk
-// over the keys that counts and one that emits, every warp over a contiguous
-// range of slots with ballots, so that the lists come out in slot order. Bound by
-// latency: barriers, the one read, and the histogram's shared-memory atomics,
-// which is why digits are 11 bits (the first holds the exponent and two more
-// bits, so that like-sized scores spread) and why every warp finds the digit for
-// itself from the chunks' sums. Nothing is written to global memory before the
-// emitting walk: a cluster barrier waits for stores on their way. Copying inside
-// that walk cost a memory round trip for every 32 slots of a warp, so it has a
-// loop of its own (131072 tokens: 83 us so, 41 us with the copy beside the first
-// read; clusters of 16 took 85 us, their barriers and remote reads outweigh the
-// halved parts).
+// (CL CTAs; 1: no cluster), each warp a contiguous range of that in pieces of 128
+// slots, four a lane. One pass over scores and positions leaves keys in shared
+// memory (KEYS; computed again from the scores when a part is too long for that).
+// Then the n-th largest key by three radix steps, a walk that counts and one that
+// emits the moves, ranks by a scan over the lanes, so that the lists come out in
+// slot order. Bound by latency for short rows (barriers, the one read) and by
+// issue slots for long ones: keys are read four at a time, the counting walk
+// counts in registers, and the scan is one for 128 slots. A walk of 32 slots at a
+// time with ballots took 43 us for 131072 tokens of 8 heads on 64 SMs, 274
+// instructions for 32 slots; clusters of 16 took 85 us, their barriers and remote
+// reads outweigh the halved parts. Digits are 11 bits: the first holds the
+// exponent and two more bits, so that like-sized scores spread over the
+// histogram. Protected keys are above every score, so a first digit that falls on
+// theirs ends the search.
 template <int CL, int T, bool KEYS>   // CTAs a row, threads a CTA
 __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
-    constexpr int kWarps = T / 32;
+    constexpr int kWarps = T / 32, kPiece = 128;
     extern __shared__ __align__(16) uint32_t smem[];
     uint32_t* const hist = smem;                       // [kDigits][kBins]
     uint32_t* const keys = smem + kDigits * kBins;
     __shared__ __align__(16) int warp_counts[kWarps][4];   // gt, eq, gt below n, eq below n
     __shared__ __align__(16) int cta_counts[4];
     __shared__ uint32_t chunk_sums[kDigits][kBins / 128];
+    __shared__ uint4 search_s[kDigits];
     const int s = blockIdx.z, g = blockIdx.y, part = CL == 1 ? 0 : (int)cluster_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pa::grid_dependents_launch();
@@ -141,12 +167,34 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
     float* const w_out = p.scores_out + sg * p.stride;
     int32_t* const pos_out = p.positions_out + sg * p.stride;
     int2* const moves = p.moves + sg * p.max_moves;
-    // this CTA's slots, and this warp's of them
-    const int per = ((L + CL - 1) / CL + 31) / 32 * 32;
+    const bool aligned =
+        (((uintptr_t)row.w | (uintptr_t)row.pos | (uintptr_t)w_out | (uintptr_t)pos_out) & 15) == 0;
+    // this CTA's slots, and this warp's of them: whole pieces, but for the row's last
+    const int per = ((L + CL - 1) / CL + kPiece - 1) / kPiece * kPiece;
     const int a0 = min(L, part * per), a1 = min(L, a0 + per);
-    const int seg = ((a1 - a0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int seg = ((a1 - a0 + kWarps - 1) / kWarps + kPiece - 1) / kPiece * kPiece;
     const int j0 = min(a1, a0 + warp * seg), j1 = min(a1, j0 + seg);
-    auto key_at = [&](int j) { return KEYS ? keys[j - a0] : row.key(row.position(j), row.w[j]); };
+    // scores and positions of slots j .. j + 3
+    auto read4 = [&](int j, float (&w)[4], int (&pos)[4]) {
+        load4(row.w, w, j, j1 - j, aligned);
+        if (row.pos) load4(row.pos, pos, j, j1 - j, aligned);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            pos[i] = row.pos && pos[i] >= 0 ? pos[i] : row.shift + j + i;
+    };
+    // their keys; 0 past the row
+    auto keys4 = [&](int j, uint32_t (&k)[4]) {
+        if constexpr (KEYS) {
+            const uint4 t = *reinterpret_cast<const uint4*>(keys + (j - a0));
+            k[0] = t.x, k[1] = t.y, k[2] = t.z, k[3] = t.w;
+        } else {
+            float w[4];
+            int pos[4];
+            read4(j, w, pos);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = j + i < j1 ? row.key(pos[i], w[i]) : 0u;
+        }
+    };
     auto sync = [&]() {
         if constexpr (CL == 1) __syncthreads();
         else cluster_sync();
@@ -156,27 +204,22 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
     uint32_t cut = 0, left = (uint32_t)n;
     const bool search = n > 0 && n < L;
     __syncthreads();                                   // the histograms are zero
-    constexpr int kAhead = 4;                          // reads on the way together
-    for (int b0 = j0; b0 < j1; b0 += 32 * kAhead) {    // warp-uniform
-        float w[kAhead];
-        int pos[kAhead];
+#pragma unroll 4
+    for (int b = j0; b < j1; b += kPiece) {            // warp-uniform
+        const int j = b + 4 * lane;
+        float w[4];
+        int pos[4];
+        read4(j, w, pos);
+        uint32_t k[4];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int j = b0 + 32 * i + lane;
-            w[i] = 0.f, pos[i] = 0;
-            if (j < j1) w[i] = row.w[j], pos[i] = row.position(j);
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int j = b0 + 32 * i + lane;
-            if (b0 + 32 * i >= j1) break;              // warp-uniform
-            const uint32_t k = row.key(pos[i], w[i]);
-            if (KEYS && j < j1) keys[j - a0] = k;
+        for (int i = 0; i < 4; ++i) {
+            k[i] = j + i < j1 ? row.key(pos[i], w[i]) : 0u;
             // protected tokens come in long runs: one addition for a warp's
-            const uint32_t safe = __ballot_sync(0xffffffffu, j < j1 && k == kProtected);
-            if (j < j1 && (k != kProtected || lane == __ffs(safe) - 1))
-                atomicAdd(hist + (k >> 21), k == kProtected ? (uint32_t)__popc(safe) : 1u);
+            const uint32_t safe = __ballot_sync(0xffffffffu, k[i] == kProtected);
+            if (j + i < j1 && (k[i] != kProtected || lane == __ffs(safe) - 1))
+                atomicAdd(hist + (k[i] >> 21), k[i] == kProtected ? (uint32_t)__popc(safe) : 1u);
         }
+        if (KEYS) *reinterpret_cast<uint4*>(keys + (j - a0)) = make_uint4(k[0], k[1], k[2], k[3]);
     }
     if (search) {
 #pragma unroll 1
@@ -185,157 +228,214 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
             const int shift = digit_shift(d), bins = 1 << digit_bits(d);
             if (d > 0) {
                 const uint32_t mask = 0xffffffffu << (shift + digit_bits(d));
-                for (int b = j0; b < j1; b += 32) {
-                    const int j = b + lane;
-                    const uint32_t k = j < j1 ? key_at(j) : 0u;
-                    const uint32_t safe = __ballot_sync(0xffffffffu, j < j1 && k == kProtected);
-                    if (j < j1 && (k & mask) == cut &&
-                        (k != kProtected || lane == __ffs(safe) - 1))
-                        atomicAdd(h + (k >> shift & (bins - 1)),
-                                  k == kProtected ? (uint32_t)__popc(safe) : 1u);
+                for (int b = j0; b < j1; b += kPiece) {
+                    const int j = b + 4 * lane;
+                    uint32_t k[4];
+                    keys4(j, k);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if ((k[i] & mask) == cut && j + i < j1)
+                            atomicAdd(h + (k[i] >> shift & (bins - 1)), 1u);
                 }
             }
-            sync();
-            if constexpr (CL > 1) {
-                // the cluster's sum, in registers until every CTA has read the parts
-                const int vecs = bins / 4;
-                constexpr int kMine = (kBins / 4 + T - 1) / T;
-                uint4 t[kMine];
-#pragma unroll
-                for (int i = 0; i < kMine; ++i) {
-                    t[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (tid + i * T < vecs)
-#pragma unroll
-                        for (int c = 0; c < CL; ++c) {
-                            const uint4 v = load_remote(remote(h + 4 * (tid + i * T), c));
-                            t[i].x += v.x, t[i].y += v.y, t[i].z += v.z, t[i].w += v.w;
-                        }
-                }
-                cluster_sync();
-#pragma unroll
-                for (int i = 0; i < kMine; ++i)
-                    if (tid + i * T < vecs) reinterpret_cast<uint4*>(h)[tid + i * T] = t[i];
-                __syncthreads();
-            }
-            // a warp sums a chunk of 128 bins (chunk 0 the highest), then every warp finds the
-            // chunk of the n-th key and the bin in it
+            __syncthreads();
+            // a warp sums a chunk of 128 bins (chunk 0 the highest); then the n-th key's chunk is
+            // found from the chunks' sums, and its bin from that chunk's bins, in a cluster by
+            // one warp that reads both from all its CTAs (the whole histograms would be 16
+            // times as much), else by every warp for itself
             const int chunks = bins / 128;
             for (int i = warp; i < chunks; i += kWarps) {
                 const uint4 v = *reinterpret_cast<const uint4*>(h + bins - 128 * (i + 1) + 4 * lane);
                 const uint32_t sum = __reduce_add_sync(0xffffffffu, v.x + v.y + v.z + v.w);
                 if (lane == 0) chunk_sums[d][i] = sum;
             }
-            __syncthreads();
-            uint32_t upto = lane < chunks ? chunk_sums[d][lane] : 0u;
-            const uint32_t own = upto;
+            sync();
+            uint32_t bin = 0, above = 0, in_bin = 0;   // the bin, keys in higher ones, and in it
+            if (CL == 1 || warp == 0) {
+                uint32_t upto = 0;
+                if (lane < chunks) {
+                    if constexpr (CL == 1) {
+                        upto = chunk_sums[d][lane];
+                    } else {
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
-            }
-            const int chunk = __ffs(__ballot_sync(0xffffffffu, lane < chunks && upto >= left)) - 1;
-            const uint32_t above = __shfl_sync(0xffffffffu, upto - own, chunk);
-            const int top = bins - 128 * chunk - 4 * lane;   // the lane's bins: top - 1 .. top - 4
-            const uint4 v = *reinterpret_cast<const uint4*>(h + top - 4);
-            uint32_t run = v.x + v.y + v.z + v.w;
-            const uint32_t mine = run;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += y;
-            }
-            run += above;                              // keys in the lane's bins and higher ones
-            const int owner = __ffs(__ballot_sync(0xffffffffu, run >= left)) - 1;
-            uint32_t before = run - mine;
-            int bin = top - 1;
-            if (before + v.w < left) {
-                before += v.w, --bin;
-                if (before + v.z < left) {
-                    before += v.z, --bin;
-                    if (before + v.y < left) before += v.y, --bin;
+                        for (int c = 0; c < CL; ++c)
+                            upto += load_remote1(remote(&chunk_sums[d][lane], c));
+                    }
                 }
+                const uint32_t own = upto;
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                const int chunk =
+                    __ffs(__ballot_sync(0xffffffffu, lane < chunks && upto >= left)) - 1;
+                above = __shfl_sync(0xffffffffu, upto - own, chunk);
+                const int top = bins - 128 * chunk - 4 * lane;   // the lane's bins: top - 1 .. - 4
+                uint4 v;
+                if constexpr (CL == 1) {
+                    v = *reinterpret_cast<const uint4*>(h + top - 4);
+                } else {
+                    v = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int c = 0; c < CL; ++c) {
+                        const uint4 t = load_remote(remote(h + top - 4, c));
+                        v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+                    }
+                }
+                const uint32_t mine = v.x + v.y + v.z + v.w;
+                uint32_t run = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
+                    if (lane >= o) run += y;
+                }
+                run += above;                          // keys in the lane's bins and higher ones
+                const int owner = __ffs(__ballot_sync(0xffffffffu, run >= left)) - 1;
+                uint32_t before = run - mine, found = v.w;
+                int at = top - 1;
+                if (before + found < left) {
+                    before += found, found = v.z, --at;
+                    if (before + found < left) {
+                        before += found, found = v.y, --at;
+                        if (before + found < left) before += found, found = v.x, --at;
+                    }
+                }
+                above = __shfl_sync(0xffffffffu, before, owner);
+                bin = __shfl_sync(0xffffffffu, (uint32_t)at, owner);
+                in_bin = __shfl_sync(0xffffffffu, found, owner);
             }
-            left -= __shfl_sync(0xffffffffu, before, owner);
-            cut |= (uint32_t)__shfl_sync(0xffffffffu, bin, owner) << shift;
+            if constexpr (CL > 1) {
+                if (tid == 0) search_s[d] = make_uint4(bin, above, in_bin, 0u);
+                __syncthreads();
+                bin = search_s[d].x, above = search_s[d].y, in_bin = search_s[d].z;
+            }
+            left -= above;
+            cut |= bin << shift;
+            if (in_bin == left) {                      // all of the bin stays: no need to split it
+                --cut;                                 // (bin 0 whole would be the whole row)
+                left = 0;
+                break;
+            }
+            if (cut >> 21 == kProtected >> 21) {       // only protected keys are that high
+                cut = kProtected;
+                break;
+            }
         }
     }
-    // n == L: all stay; n == 0: none does
-    const bool all = n == L, none = n == 0;
-    auto larger = [&](uint32_t k) { return all || (!none && k > cut); };
-    auto equal = [&](uint32_t k) { return !all && !none && k == cut; };
+    // n == L: all stay (keys are at least 0, so all are above or at the cut 0, as many ties as
+    // there are); n == 0: none does
+    if (n == L) cut = 0, left = (uint32_t)L;
+    if (n == 0) cut = kProtected, left = 0;
 
+    // this warp's keys above and at the cut, all and those below n
     int c_gt = 0, c_eq = 0, c_gt_low = 0, c_eq_low = 0;
-    for (int b = j0; b < j1; b += 32) {
-        const int j = b + lane;
-        const uint32_t k = j < j1 ? key_at(j) : 0u;
-        const bool is_gt = j < j1 && larger(k), is_eq = j < j1 && equal(k);
-        const uint32_t gts = __ballot_sync(0xffffffffu, is_gt);
-        const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
-        const uint32_t low = n <= b ? 0u : n - b >= 32 ? 0xffffffffu : (1u << (n - b)) - 1u;
-        c_gt += __popc(gts);
-        c_eq += __popc(eqs);
-        c_gt_low += __popc(gts & low);
-        c_eq_low += __popc(eqs & low);
+    const bool mixed = j0 < n && j1 > n;
+    for (int b = j0; b < j1; b += kPiece) {
+        const int j = b + 4 * lane;
+        uint32_t k[4];
+        keys4(j, k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool is_eq = k[i] == cut && j + i < j1;
+            c_gt += k[i] > cut;
+            c_eq += is_eq;
+            if (mixed) {
+                c_gt_low += k[i] > cut && j + i < n;
+                c_eq_low += is_eq && j + i < n;
+            }
+        }
     }
+    if (j1 <= n) c_gt_low = c_gt, c_eq_low = c_eq;
+    c_gt = __reduce_add_sync(0xffffffffu, c_gt), c_eq = __reduce_add_sync(0xffffffffu, c_eq);
+    c_gt_low = __reduce_add_sync(0xffffffffu, c_gt_low);
+    c_eq_low = __reduce_add_sync(0xffffffffu, c_eq_low);
     if (lane == 0)
         *reinterpret_cast<int4*>(warp_counts[warp]) = make_int4(c_gt, c_eq, c_gt_low, c_eq_low);
     __syncthreads();
-    int gt_before = 0, eq_before = 0, low = 0, ties_low = 0, gt_all = 0, eq_all = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        const int4 c = *reinterpret_cast<const int4*>(warp_counts[i]);
-        if (i < warp) gt_before += c.x, eq_before += c.y;
-        gt_all += c.x, eq_all += c.y;
-        low += c.z, ties_low += c.w;
-    }
+    int4 c = make_int4(0, 0, 0, 0);
+    if (lane < kWarps) c = *reinterpret_cast<const int4*>(warp_counts[lane]);
+    int gt_before = __reduce_add_sync(0xffffffffu, lane < warp ? c.x : 0);
+    int eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? c.y : 0);
+    int low = __reduce_add_sync(0xffffffffu, c.z), ties_low = __reduce_add_sync(0xffffffffu, c.w);
     if constexpr (CL > 1) {
-        if (tid == 0)
-            *reinterpret_cast<int4*>(cta_counts) = make_int4(gt_all, eq_all, low, ties_low);
-        cluster_sync();
-        low = ties_low = 0;
-#pragma unroll
-        for (int c = 0; c < CL; ++c) {
-            const uint4 v = load_remote(remote(cta_counts, c));
-            if (c < part) gt_before += (int)v.x, eq_before += (int)v.y;
-            low += (int)v.z, ties_low += (int)v.w;
+        if (warp == 0) {
+            const int gt = __reduce_add_sync(0xffffffffu, c.x);
+            const int eq = __reduce_add_sync(0xffffffffu, c.y);
+            if (lane == 0) *reinterpret_cast<int4*>(cta_counts) = make_int4(gt, eq, low, ties_low);
         }
+        cluster_sync();
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);          // lane i: CTA i of the cluster
+        if (lane < CL) v = load_remote(remote(cta_counts, lane));
+        gt_before += __reduce_add_sync(0xffffffffu, lane < part ? (int)v.x : 0);
+        eq_before += __reduce_add_sync(0xffffffffu, lane < part ? (int)v.y : 0);
+        low = __reduce_add_sync(0xffffffffu, (int)v.z);
+        ties_low = __reduce_add_sync(0xffffffffu, (int)v.w);
     }
     const int ties = (int)left;                       // tokens of key `cut` that stay
     const int kept_low = low + min(ties, ties_low);   // kept tokens below n
     const int count = n - kept_low;                   // holes, and tokens to fill them
-    int kept = gt_before + min(ties, eq_before);      // kept tokens before the warp's next slot
-    for (int b = j0; b < j1; b += 32) {
-        const int j = b + lane;
-        const uint32_t k = j < j1 ? key_at(j) : 0u;
-        const bool is_eq = j < j1 && equal(k);
-        const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
-        const uint32_t below = (1u << lane) - 1u;
-        const bool keep = j < j1 && (larger(k) || (is_eq && eq_before + __popc(eqs & below) < ties));
-        const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
-        const int rank = kept + __popc(keeps & below);   // kept tokens before slot j
-        if (j < j1) {
-            if (keep && j >= n) moves[rank - kept_low].x = j;
-            if (!keep && j < n) moves[j - rank].y = j;
+    int kept = gt_before + min(ties, eq_before);      // kept tokens before the warp's next piece
+    for (int b = j0; b < j1; b += kPiece) {
+        const int j = b + 4 * lane;
+        uint32_t k[4];
+        keys4(j, k);
+        uint32_t keep = 0, eq = 0;                     // a bit a slot
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            keep |= (uint32_t)(k[i] > cut) << i;
+            eq |= (uint32_t)(k[i] == cut && j + i < j1) << i;
         }
-        eq_before += __popc(eqs);
-        kept += __popc(keeps);
+        if (__any_sync(0xffffffffu, eq)) {             // ties: the first `ties` of the row stay
+            int run = __popc(eq);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += y;
+            }
+            int mine = eq_before + run - __popc(eq);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (eq >> i & 1u) {
+                    keep |= (uint32_t)(mine < ties) << i;
+                    ++mine;
+                }
+            eq_before += __shfl_sync(0xffffffffu, run, 31);
+        }
+        int run = __popc(keep);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += y;
+        }
+        int rank = kept + run - __popc(keep);          // kept tokens before the lane's slots
+        kept += __shfl_sync(0xffffffffu, run, 31);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool stays = keep >> i & 1u;
+            if (stays && j + i >= n) moves[rank - kept_low].x = j + i;
+            if (!stays && j + i < n && j + i < j1) moves[j + i - rank].y = j + i;
+            rank += stays;
+        }
     }
     // The slots below n as they are; those of evicted tokens are written again below.
-    for (int b0 = j0; b0 < min(j1, n); b0 += 32 * kAhead) {
-        float w[kAhead];
-        int pos[kAhead];
+    const int jn = min(j1, n);
+    for (int b = j0; b < jn; b += kPiece) {
+        const int j = b + 4 * lane;
+        float w[4];
+        int pos[4];
+        read4(j, w, pos);
+        if (aligned && j + 4 <= jn) {
+            *reinterpret_cast<float4*>(w_out + j) = make_float4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<int4*>(pos_out + j) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int j = b0 + 32 * i + lane;
-            if (j < min(j1, n)) w[i] = row.w[j], pos[i] = row.position(j);
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int j = b0 + 32 * i + lane;
-            if (j < min(j1, n)) w_out[j] = w[i], pos_out[j] = pos[i];
+            for (int i = 0; i < 4; ++i)
+                if (j + i < jn) w_out[j + i] = w[i], pos_out[j + i] = pos[i];
         }
     }
     sync();                                            // the list is whole
+    constexpr int kAhead = 4;                          // moves on the way together
     for (int i0 = part * T + tid; i0 < count; i0 += kAhead * CL * T) {
         int2 m[kAhead];                                // written by other CTAs of the cluster
         float w[kAhead];
@@ -505,9 +605,9 @@ pa_status launch_select(const SelectParams& p, int num_seqs, cudaStream_t st) {
     const int64_t rows = (int64_t)num_seqs * p.num_kv_heads;
     int cl = 1;
     while (cl < kMaxCluster && ((rows * cl < 152 && p.max_len / cl > 2048) ||
-                                p.max_len / cl + 32 > kMaxKeys))
+                                p.max_len / cl + 128 > kMaxKeys))
         cl *= 2;
-    const int keys = ((p.max_len + cl - 1) / cl + 31) / 32 * 32;
+    const int keys = ((p.max_len + cl - 1) / cl + 127) / 128 * 128;   // whole pieces
     if (keys > kMaxKeys) return launch_select_as<kMaxCluster, 1024, false>(p, num_seqs, keys, st);
     switch (cl) {
         case 1: return launch_select_cl<1>(p, num_seqs, keys, st);
