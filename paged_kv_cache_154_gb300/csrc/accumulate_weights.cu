@@ -14,20 +14,23 @@
 //      (m = largest logit in base-2 units, l = sum 2^(a - m));
 //   2. the tiles' (m, l) merged into a row's, and out = in + sum over rows
 //      2^(a - m) / l: from the logits that kernel 1 stored (stored_kernel, which
-//      merges for itself), or from logits computed again (rows_kernel merges,
-//      then again_kernel).
+//      merges for itself), or from logits computed again (many_kernel for both
+//      passes, rows_kernel between them).
 //
 // Storing costs 8 bytes a row and token, mostly within L2; computing again costs
 // a second read of K and its products. So few rows are stored (up to 16 rows
 // per KV head, while the buffer stays under 256 MB), many are computed again.
 //
-// What bounds it: the read of K, once for few rows. K goes from global memory
-// to operand registers directly: tokens stand in the M dimension of the
-// warp-level product, and as the order of the dims is free (q is loaded in the
-// same order), a lane's 16-byte load of its token is four operand registers
-// with no staging in shared memory. Codes are made exact in fp16 as in the
-// decode kernels: code - zero point (INT8, INT4), E4M3 to fp16; q goes to fp16
-// after an exact power-of-two scaling per row. Sums and softmax are fp32.
+// What bounds it: for few rows the read of K, which goes from global memory to
+// operand registers directly: tokens stand in the M dimension of the warp-level
+// product, and as the order of the dims is free (q is loaded in the same order), a
+// lane's 16-byte load of its token is four operand registers with no staging in
+// shared memory. For many rows it is the products and exponentials: a tile of K is
+// staged in shared memory once, for warps that hold 16 rows of q each.
+// Codes are made exact in fp16: code - zero point (INT8), E4M3 to fp16, masked
+// nibbles as subnormals with the zero points taken out of the sums (INT4, as in
+// the decode kernel); q goes to fp16 after an exact power-of-two scaling per row.
+// Sums and softmax are fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -41,13 +44,14 @@
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kUnit = 16777216.f;       // 2^24: masked nibbles are subnormals in units of 2^-24
 constexpr int kBS = 16;                  // tokens per block
 constexpr int kWarps = 4;                // warps per CTA
 constexpr int kTileTokens = 512;         // tokens of a logits CTA: 8 blocks a warp
 static_assert(kTileTokens / kBS / kWarps <= 32, "a lane holds a block id");
 constexpr int kOutTokens = 1024;         // tokens of a stored CTA
-constexpr int kAgainBlocks = 2;          // blocks of a warp of an again CTA
-constexpr int kMaxRows = 4096;           // query rows per KV head: their sums fit shared memory
+constexpr int kManyWarps = 8;            // warps of a many_kernel CTA
+constexpr int kMaxRows = 4096;           // query rows per KV head
 constexpr int64_t kMaxStored = (int64_t)256 << 20;
 
 struct Params {
@@ -63,10 +67,12 @@ struct Params {
     float* logits;            // [num_seqs x H_kv][max tokens, a multiple of 16][row_pad], or null
     float2* stats;            // [num_seqs x H_kv][row_slots][tiles]: (m, l)
     float2* sums;             // [num_seqs x H_kv][row_slots]: see row_sum; computed again only
+    int row_warps;            // many_kernel: warps over chunks of 16 rows; the others split tokens
+    int tile_tokens;          // of stats
     unsigned int* err;
     int64_t stride;           // of in and out, per KV head
     int num_seqs, num_q_tokens, max_q_len, num_heads, num_kv_heads, group, num_blocks, max_blocks;
-    int max_len, tokens_pad, tiles, row_slots, row_pad, chunks;
+    int max_len, tokens_pad, tiles, row_slots, row_pad;
     int q_bf16;
     float scale_log2;
 };
@@ -110,10 +116,17 @@ __device__ __forceinline__ float exp2i(int e) {   // 2^e for e in [-126, 127]
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// (m, l) of a pair of partial sums
+__device__ __forceinline__ void merge(float& m, float& l, float m2, float l2) {
+    const float top = fmaxf(m, m2);
+    const float ref = top == -INFINITY ? 0.f : top;
+    l = l * pa::ex2(m - ref) + l2 * pa::ex2(m2 - ref);
+    m = top;
+}
+
 // The K operand. Per lane (quad = lane / 4, qc = lane % 4) and token half h
 // (token quad + 8 h of a block): kWords 32-bit words of the token's row, loaded
-// kVec words at a time; frag() makes the A registers of k-step kk, whose columns
-// 2 qc, 2 qc + 1 and 2 qc + 8, 2 qc + 9 are the dims dim(kk, qc, 0 .. 3).
+// kVec words at a time; frag() makes the A registers of k-step kk.
 template <int KV, int D>
 struct KRows {
     static constexpr bool k16 = KV == PA_F16 || KV == PA_BF16;
@@ -122,45 +135,65 @@ struct KRows {
     static constexpr int kVec = KV == PA_INT4 ? 2 : 4;    // a 4-bit load stays in one group
     static constexpr int kGroups = KV == PA_INT4 ? D / PA_INT4_GROUP : 1;
     static constexpr int kSteps = D / 16;
+    static constexpr bool kScaled = KV == PA_INT8 || KV == PA_INT4;
     uint32_t w[2][kWords];
     float scale[2][kGroups];
     int zp[2][kGroups];
 
-    __device__ __forceinline__ static int dim(int kk, int qc, int e) {
-        if constexpr (k16) return 32 * (kk / 2) + 8 * qc + 4 * (kk & 1) + e;
-        else if constexpr (KV == PA_INT4)      // nibble pairs (0,4), (1,5) | (2,6), (3,7)
-            return 64 * (kk / 4) + 16 * qc + 8 * (kk / 2 & 1) + 2 * (kk & 1) + (e >> 1) +
-                   4 * (e & 1);
-        else return 64 * (kk / 4) + 16 * qc + 4 * (kk & 3) + e;
-    }
-
-    // rows `row` (token 0 of the block) + quad, + quad + 8 of the cache
-    __device__ __forceinline__ void load(const Params& p, int64_t row, int quad, int qc) {
+    __device__ __forceinline__ void load_scales(const Params& p, int64_t row, int quad) {
+        if constexpr (kScaled) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t t = row + quad + 8 * h;
-            const uint8_t* src = static_cast<const uint8_t*>(p.k) + t * kRowBytes;
-#pragma unroll
-            for (int j = 0; j < kWords / kVec; ++j) {
-                if constexpr (kVec == 4) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + 64 * j + 16 * qc));
-                    w[h][4 * j] = u.x, w[h][4 * j + 1] = u.y;
-                    w[h][4 * j + 2] = u.z, w[h][4 * j + 3] = u.w;
-                } else {
-                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(src + 32 * j + 8 * qc));
-                    w[h][2 * j] = u.x, w[h][2 * j + 1] = u.y;
-                }
-            }
-            if constexpr (KV == PA_INT8 || KV == PA_INT4)
+            for (int h = 0; h < 2; ++h) {
+                const int64_t t = row + quad + 8 * h;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     scale[h][g] = __ldg(p.k_scale + t * kGroups + g);
                     zp[h][g] = __ldg(p.k_zp + t * kGroups + g);
                 }
+            }
+        }
+    }
+    template <typename V, typename Load>
+    __device__ __forceinline__ void put(int h, int j, Load load) {
+        const V u = load();
+        w[h][kVec * j] = u.x, w[h][kVec * j + 1] = u.y;
+        if constexpr (kVec == 4) w[h][4 * j + 2] = u.z, w[h][4 * j + 3] = u.w;
+    }
+    using Vec = typename std::conditional<kVec == 4, uint4, uint2>::type;
+    // from global memory: rows `row` (token 0 of the block) + quad, + quad + 8 of the cache
+    __device__ __forceinline__ void load(const Params& p, int64_t row, int quad, int qc) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t* src =
+                static_cast<const uint8_t*>(p.k) + (row + quad + 8 * h) * kRowBytes + 4 * kVec * qc;
+#pragma unroll
+            for (int j = 0; j < kWords / kVec; ++j)
+                put<Vec>(h, j, [&] { return __ldg(reinterpret_cast<const Vec*>(src + 16 * kVec * j)); });
+        }
+        load_scales(p, row, quad);
+    }
+    // A staged row: its 16-byte chunks are exchanged so that the rows of one load fall into
+    // different banks (rows of 32 bytes, and of 64 loaded 16 at a time, need none).
+    __device__ __forceinline__ static int staged_chunk(int row, int chunk) {
+        if constexpr (KV == PA_INT4) return kRowBytes == 64 ? chunk ^ (row & 2) : chunk;
+        else return kRowBytes >= 128 ? chunk ^ ((row & 1) << 2) : chunk;
+    }
+    // from a staged tile, at tile rows `row` + quad, + quad + 8
+    __device__ __forceinline__ void load_staged(const uint8_t* tile, int row, int quad, int qc) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = row + quad + 8 * h;
+#pragma unroll
+            for (int j = 0; j < kWords / kVec; ++j) {
+                const int at = 16 * kVec * j + 4 * kVec * qc;
+                const uint8_t* src = tile + t * kRowBytes + 16 * staged_chunk(t, at / 16) + at % 16;
+                put<Vec>(h, j, [&] { return *reinterpret_cast<const Vec*>(src); });
+            }
         }
     }
 
-    // the pair (dims 0, 1 or 2, 3 of the step) of one token
+    // a pair of dims of one token, in the low (hi = 0) or high columns of k-step kk; INT4: in
+    // units of 2^-24 (hi = 0) and 2^-20
     __device__ __forceinline__ uint32_t pair(int h, int kk, int hi) const {
         if constexpr (k16) {
             return w[h][2 * kk + hi];
@@ -169,10 +202,8 @@ struct KRows {
             const uint32_t z = prmt((uint32_t)zp[h][0] ^ 0x80u, 0x64646464u, 0x4040u);
             return hsub2(prmt(w[h][kk] ^ 0x80808080u, 0x64646464u, hi ? 0x4342u : 0x4140u), z);
         } else if constexpr (KV == PA_INT4) {
-            const uint32_t z = (uint32_t)(zp[h][kk / 4] & 255) * 0x00010001u;
             const uint32_t u = kk & 1 ? w[h][kk / 2] >> 8 : w[h][kk / 2];
-            return hi ? hsub2((u & 0x00f000f0u) | 0x54005400u, z * 16u + 0x54005400u)
-                      : hsub2((u & 0x000f000fu) | 0x64006400u, z | 0x64006400u);
+            return u & (hi ? 0x00f000f0u : 0x000f000fu);
         } else {
             return e4m3x2_to_f16x2(hi ? w[h][kk] >> 16 : w[h][kk]);
         }
@@ -186,13 +217,15 @@ struct KRows {
 // 8 NR query rows of one (sequence, KV head) as B operands, in K's order of
 // dims: row 8 nr + quad of the chunk that starts at row `first`. mul: what a
 // product of rows 8 nr + 2 qc + e is multiplied by; bound: the last token that
-// row sees (-1: none).
+// row sees (-1: none); qsum: INT4, the sum of a group's q in the products' units.
 template <int KV, int D, int NR>
 struct QRows {
     using K = KRows<KV, D>;
+    static constexpr int kSums = KV == PA_INT4 ? K::kGroups : 1;
     uint32_t b[NR][K::kSteps][2];
     float mul[NR][2];
     int bound[NR][2];
+    float qsum[NR][kSums][2];
 
     __device__ __forceinline__ void load(const Params& p, const Seq& sq, int g, int first,
                                          int quad, int qc) {
@@ -203,12 +236,12 @@ struct QRows {
         for (int nr = 0; nr < NR; ++nr) {
             const int row = first + 8 * nr + quad;
             const bool on = row < rows;
-            const int64_t at = on ? ((int64_t)(sq.q0 + row / p.group) * p.num_heads +
-                                     g * p.group + row % p.group) * D
-                                  : 0;
-            float m = on ? head : 0.f;
+            const int qi = on ? row / p.group : 0;
+            const uint16_t* src =
+                static_cast<const uint16_t*>(p.q) +
+                ((int64_t)(sq.q0 + qi) * p.num_heads + g * p.group + (on ? row - qi * p.group : 0)) * D;
+            float m = on ? head : 0.f, qs[kSums] = {};
             if constexpr (K::k16) {
-                const uint16_t* src = static_cast<const uint16_t*>(p.q) + at;
 #pragma unroll
                 for (int j = 0; j < K::kSteps / 2; ++j) {
                     uint4 u = make_uint4(0u, 0u, 0u, 0u);
@@ -217,19 +250,25 @@ struct QRows {
                     b[nr][2 * j + 1][0] = u.z, b[nr][2 * j + 1][1] = u.w;
                 }
             } else {
-                // two rounds over the row: its largest element, then fp16 after scaling
-                // that into [2^14, 2^15)
-                const uint16_t* src = static_cast<const uint16_t*>(p.q) + at;
-                auto element = [&](int kk, int e) {
-                    const uint16_t u = on ? __ldg(src + K::dim(kk, qc, e)) : (uint16_t)0;
-                    return p.q_bf16 ? __uint_as_float((uint32_t)u << 16)
-                                    : __half2float(__ushort_as_half(u));
-                };
-                float mx = 0.f;
+                // the lane's dims 64 j + 16 qc .. + 15, then fp16 after scaling the row's largest
+                // element into [2^14, 2^15)
+                float v[D / 64][16], mx = 0.f;
 #pragma unroll
-                for (int kk = 0; kk < K::kSteps; ++kk)
+                for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(element(kk, e)));
+                    for (int i = 0; i < 2; ++i) {
+                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                        if (on)
+                            u = __ldg(reinterpret_cast<const uint4*>(src + 64 * j + 16 * qc + 8 * i));
+                        const uint16_t* x = reinterpret_cast<const uint16_t*>(&u);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float f = p.q_bf16 ? __uint_as_float((uint32_t)x[e] << 16)
+                                                     : __half2float(__ushort_as_half(x[e]));
+                            v[j][8 * i + e] = f;
+                            mx = fmaxf(mx, fabsf(f));
+                        }
+                    }
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 int ex = 0;
@@ -239,18 +278,40 @@ struct QRows {
                 }
                 const float up = exp2i(14 - ex);
                 m *= exp2i(ex - 14);
+                if constexpr (KV == PA_INT4) m *= kUnit;
 #pragma unroll
                 for (int kk = 0; kk < K::kSteps; ++kk)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const __half2 v = __floats2half2_rn(element(kk, 2 * e) * up,
-                                                            element(kk, 2 * e + 1) * up);
-                        b[nr][kk][e] = *reinterpret_cast<const uint32_t*>(&v);
+                        const float* x = v[kk / 4];
+                        __half2 h;
+                        if constexpr (KV == PA_INT4) {
+                            // nibbles 0 and 4, 1 and 5 | 2 and 6, 3 and 7 of word kk / 2
+                            const int i = 8 * (kk / 2 & 1) + 2 * (kk & 1) + e;
+                            const float f = e ? up * 0.0625f : up;
+                            h = __floats2half2_rn(x[i] * f, x[i + 4] * f);
+                            const float2 r = __half22float2(h);
+                            qs[kk / 4] += (r.x + r.y) * (e ? 16.f / kUnit : 1.f / kUnit);
+                        } else {
+                            const int i = 4 * (kk & 3) + 2 * e;
+                            h = __floats2half2_rn(x[i] * up, x[i + 1] * up);
+                        }
+                        b[nr][kk][e] = *reinterpret_cast<const uint32_t*>(&h);
                     }
+            }
+            if constexpr (KV == PA_INT4) {
+#pragma unroll
+                for (int i = 0; i < kSums; ++i) {
+                    qs[i] += __shfl_xor_sync(0xffffffffu, qs[i], 1);
+                    qs[i] += __shfl_xor_sync(0xffffffffu, qs[i], 2);
+                }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 mul[nr][e] = __shfl_sync(0xffffffffu, m, 4 * (2 * qc + e));
+#pragma unroll
+                for (int i = 0; i < kSums; ++i)
+                    qsum[nr][i][e] = __shfl_sync(0xffffffffu, qs[i], 4 * (2 * qc + e));
                 const int mine = first + 8 * nr + 2 * qc + e;
                 bound[nr][e] = mine < rows ? min(sq.L - sq.r + mine / p.group, sq.L - 1) : -1;
             }
@@ -284,12 +345,54 @@ struct QRows {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float v = s[nr][0][2 * h + e];
-                    if constexpr (KV == PA_INT8 || KV == PA_INT4) v *= k.scale[h][0];
-                    if constexpr (K::kGroups == 2) v = fmaf(s[nr][1][2 * h + e], k.scale[h][1], v);
+                    if constexpr (KV == PA_INT4) v = fmaf(-(float)k.zp[h][0], qsum[nr][0][e], v);
+                    if constexpr (K::kScaled) v *= k.scale[h][0];
+                    if constexpr (K::kGroups == 2)
+                        v = fmaf(fmaf(-(float)k.zp[h][1], qsum[nr][1][e], s[nr][1][2 * h + e]),
+                                 k.scale[h][1], v);
                     v *= mul[nr][e];
                     if (tok0 + quad + 8 * h > bound[nr][e]) v = -INFINITY;
                     a[nr][2 * h + e] = v;
                 }
+    }
+};
+
+// The running (m, l) of a lane's rows, over the tokens it sees.
+template <int NR>
+struct RowSums {
+    float m[NR][2], l[NR][2];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) m[nr][e] = -INFINITY, l[nr][e] = 0.f;
+    }
+    __device__ __forceinline__ void add(const float (&a)[NR][4]) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float mx = fmaxf(a[nr][e], a[nr][2 + e]);
+                if (mx > m[nr][e]) {
+                    l[nr][e] *= pa::ex2(m[nr][e] - mx);
+                    m[nr][e] = mx;
+                }
+                const float ref = m[nr][e] == -INFINITY ? 0.f : m[nr][e];
+                l[nr][e] += pa::ex2(a[nr][e] - ref) + pa::ex2(a[nr][2 + e] - ref);
+            }
+    }
+    // over the warp's tokens: rows 8 nr + 2 qc + e to part[], by the lanes of quad 0
+    __device__ __forceinline__ void finish(float2* part, int quad, int qc) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    merge(m[nr][e], l[nr][e], __shfl_xor_sync(0xffffffffu, m[nr][e], off),
+                          __shfl_xor_sync(0xffffffffu, l[nr][e], off));
+                if (quad == 0) part[8 * nr + 2 * qc + e] = make_float2(m[nr][e], l[nr][e]);
+            }
     }
 };
 
@@ -300,25 +403,18 @@ __device__ __forceinline__ int block_of(const Params& p, int s, int i) {
     return 0;
 }
 
-// (m, l) of a pair of partial sums
-__device__ __forceinline__ void merge(float& m, float& l, float m2, float l2) {
-    const float top = fmaxf(m, m2);
-    const float ref = top == -INFINITY ? 0.f : top;
-    l = l * pa::ex2(m - ref) + l2 * pa::ex2(m2 - ref);
-    m = top;
-}
-
-// Grid: (tiles of kTileTokens tokens, KV head x chunk of 8 NR rows, sequence).
+// Grid: (tiles of kTileTokens tokens, KV head, sequence): few rows, stored logits.
 template <int KV, int D, int NR>
 __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
+    // blocks of K in registers, on their way while one is multiplied
+    constexpr int kDepth = KRows<KV, D>::kWords >= 16 ? 2 : 4;
     __shared__ float2 part[kWarps][8 * NR];
     pa::grid_dependents_launch();
     pa::grid_dependency_wait();
-    const int s = blockIdx.z, g = blockIdx.y / p.chunks, c = blockIdx.y % p.chunks;
-    const int tile = blockIdx.x, first = 8 * NR * c;
+    const int s = blockIdx.z, g = blockIdx.y, tile = blockIdx.x;
     const Seq sq(p, s);
     const int rows = p.group * sq.r;
-    if (tile * kTileTokens >= sq.L || first >= rows) return;
+    if (tile * kTileTokens >= sq.L || rows == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, qc = lane & 3;
     // this warp's blocks: b0 + warp, + kWarps, ...
     const int b0 = tile * (kTileTokens / kBS) + warp;
@@ -326,24 +422,30 @@ __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
     const int n = b0 < nb ? (nb - b0 + kWarps - 1) / kWarps : 0;
     int my_block = 0;
     if (lane < n) my_block = block_of(p, s, b0 + lane * kWarps);
-    QRows<KV, D, NR> q;
-    q.load(p, sq, g, first, quad, qc);
-    float m[NR][2], l[NR][2];
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) m[nr][e] = -INFINITY, l[nr][e] = 0.f;
     auto fetch = [&](KRows<KV, D>& k, int i) {
         const int64_t blk = __shfl_sync(0xffffffffu, my_block, i);
         k.load(p, (blk * p.num_kv_heads + g) * kBS, quad, qc);
     };
-    auto consume = [&](const KRows<KV, D>& k, int i) {
-        const int tok0 = (b0 + i * kWarps) * kBS;
-        float a[NR][4];
-        q.logits(k, tok0, quad, a);
+    KRows<KV, D> k[kDepth];
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            if (p.logits) {   // stored calls have one chunk
+    for (int i = 0; i < kDepth - 1; ++i)
+        if (i < n) fetch(k[i], i);
+    QRows<KV, D, NR> q;
+    q.load(p, sq, g, 0, quad, qc);
+    RowSums<NR> sums;
+    sums.clear();
+    for (int i0 = 0; i0 < n; i0 += kDepth) {
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u) {
+            const int i = i0 + u;
+            if (i >= n) break;
+            if (i + kDepth - 1 < n) fetch(k[(u + kDepth - 1) % kDepth], i + kDepth - 1);
+            const int tok0 = (b0 + i * kWarps) * kBS;
+            float a[NR][4];
+            q.logits(k[u], tok0, quad, a);
+            sums.add(a);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int row = 8 * nr + 2 * qc;
@@ -355,46 +457,16 @@ __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
                     else if (row < p.row_pad)
                         *dst = a[nr][2 * h];
                 }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {   // the lane's own running sum: merged at the end
-                const float mx = fmaxf(a[nr][e], a[nr][2 + e]);
-                if (mx > m[nr][e]) {
-                    l[nr][e] *= pa::ex2(m[nr][e] - mx);
-                    m[nr][e] = mx;
-                }
-                const float ref = m[nr][e] == -INFINITY ? 0.f : m[nr][e];
-                l[nr][e] += pa::ex2(a[nr][e] - ref) + pa::ex2(a[nr][2 + e] - ref);
-            }
         }
-    };
-    KRows<KV, D> k0, k1;   // the next block's rows are on their way while one is multiplied
-    if (n > 0) fetch(k0, 0);
-    for (int i = 0; i < n; i += 2) {
-        if (i + 1 < n) fetch(k1, i + 1);
-        consume(k0, i);
-        if (i + 1 == n) break;
-        if (i + 2 < n) fetch(k0, i + 2);
-        consume(k1, i + 1);
     }
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1)
-                merge(m[nr][e], l[nr][e], __shfl_xor_sync(0xffffffffu, m[nr][e], off),
-                      __shfl_xor_sync(0xffffffffu, l[nr][e], off));
-            if (quad == 0) part[warp][8 * nr + 2 * qc + e] = make_float2(m[nr][e], l[nr][e]);
-        }
+    sums.finish(part[warp], quad, qc);
     __syncthreads();
     const int row = threadIdx.x;
-    if (row < min(8 * NR, rows - first)) {
+    if (row < min(8 * NR, rows)) {
         float2 t = part[0][row];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) merge(t.x, t.y, part[w][row].x, part[w][row].y);
-        p.stats[((int64_t)(s * p.num_kv_heads + g) * p.row_slots + first + row) * p.tiles + tile] =
-            t;
+        p.stats[((int64_t)(s * p.num_kv_heads + g) * p.row_slots + row) * p.tiles + tile] = t;
     }
 }
 
@@ -403,7 +475,7 @@ __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
 // saw nothing.
 __device__ __forceinline__ float2 row_sum(const Params& p, const Seq& sq, int64_t sg, int row,
                                           int lane) {
-    const int tiles = (sq.L + kTileTokens - 1) / kTileTokens;
+    const int tiles = (sq.L + p.tile_tokens - 1) / p.tile_tokens;
     const float2* src = p.stats + (sg * p.row_slots + row) * p.tiles;
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i < tiles; i += 32) {
@@ -416,7 +488,7 @@ __device__ __forceinline__ float2 row_sum(const Params& p, const Seq& sq, int64_
     return make_float2(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l);
 }
 
-// Grid: (rows / kWarps, KV head, sequence): a warp a row, for again_kernel.
+// Grid: (rows / kWarps, KV head, sequence): a warp a row, between many_kernel's passes.
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const Params p) {
     pa::grid_dependents_launch();
     pa::grid_dependency_wait();
@@ -441,126 +513,190 @@ __global__ void __launch_bounds__(256) stored_kernel(const Params p) {
     if (t0 >= sq.L) return;
     const int64_t sg = (int64_t)s * p.num_kv_heads + g;
     const int rows = p.group * sq.r;
+    const int64_t base = sg * p.stride;
+    constexpr int kEach = kOutTokens / 256;   // tokens of a thread, all asked for together
+    float a[kEach][RP], before[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int t = t0 + i * 256 + threadIdx.x;
+        before[i] = 0.f;
+        if (t >= sq.L) continue;
+        if (p.in) before[i] = p.in[base + t];
+        if (rows > 0) {
+            const float* src = p.logits + (sg * p.tokens_pad + t) * RP;
+            if constexpr (RP >= 4) {
+#pragma unroll
+                for (int j = 0; j < RP / 4; ++j)
+                    *reinterpret_cast<float4*>(a[i] + 4 * j) =
+                        __ldcs(reinterpret_cast<const float4*>(src) + j);
+            } else {
+#pragma unroll
+                for (int j = 0; j < RP; ++j) a[i][j] = __ldcs(src + j);
+            }
+        }
+    }
     for (int row = threadIdx.x >> 5; row < min(rows, RP); row += 8) {
         const float2 t = row_sum(p, sq, sg, row, threadIdx.x & 31);
         if ((threadIdx.x & 31) == 0) sum[row] = t;
     }
     __syncthreads();
-    const int64_t base = sg * p.stride;
-    for (int t = t0 + threadIdx.x; t < min(sq.L, t0 + kOutTokens); t += 256) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int t = t0 + i * 256 + threadIdx.x;
+        if (t >= sq.L) continue;
         float w = 0.f;
-        if (rows > 0) {
-            const float* src = p.logits + (sg * p.tokens_pad + t) * RP;
-            float a[RP];
-            if constexpr (RP >= 4) {
 #pragma unroll
-                for (int i = 0; i < RP / 4; ++i)
-                    *reinterpret_cast<float4*>(a + 4 * i) =
-                        __ldg(reinterpret_cast<const float4*>(src) + i);
-            } else {
-#pragma unroll
-                for (int i = 0; i < RP; ++i) a[i] = __ldg(src + i);
-            }
-#pragma unroll
-            for (int i = 0; i < RP; ++i)
-                if (i < rows) w = fmaf(pa::ex2(a[i] - sum[i].x), sum[i].y, w);
-        }
-        p.out[base + t] = (p.in ? p.in[base + t] : 0.f) + w;
+        for (int j = 0; j < RP; ++j)
+            if (j < rows) w = fmaf(pa::ex2(a[i][j] - sum[j].x), sum[j].y, w);
+        p.out[base + t] = before[i] + w;
     }
 }
 
-// Grid: (tiles of kWarps x kAgainBlocks blocks, KV head, sequence); shared
-// memory: the rows' sums.
+// Tokens of a many_kernel tile: 32 KB of K, at most 512.
 template <int KV, int D>
-__global__ void __launch_bounds__(kWarps * 32) again_kernel(const Params p) {
-    constexpr int NR = 2;
-    extern __shared__ float2 sum[];
+constexpr int many_tokens() {
+    return 32768 / KRows<KV, D>::kRowBytes < 512 ? 32768 / KRows<KV, D>::kRowBytes : 512;
+}
+
+// Many rows. Grid: (tiles of many_tokens(), KV head, sequence). The tile's K is
+// staged in shared memory once; warp (rc, tg) takes the row chunks rc, rc +
+// row_warps, .. of 16 rows and the tile's blocks tg, tg + token_warps, ... SUM
+// false: the rows' (m, l) over the tile; SUM true: the weights of the tile's
+// tokens, summed over the rows (each warp keeps sums of its own, which are added
+// up in a fixed order). A warp with its own K loads for every chunk of rows
+// instead took 22 + 21 us where this takes 8 + 8 (8 prompts of up to 4001 tokens,
+// 128 rows, d = 64).
+template <int KV, int D, bool SUM>
+__global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
+    constexpr int NR = 2, kTokens = many_tokens<KV, D>(), kBlocks = kTokens / kBS;
+    constexpr int kRowBytes = KRows<KV, D>::kRowBytes, kChunks = kRowBytes / 16;
+    extern __shared__ __align__(128) uint8_t tile_s[];   // K, then SUM: float [row_warps][kTokens]
+    __shared__ int blocks_s[kBlocks];
+    __shared__ float2 part_s[kManyWarps][8 * NR];
+    pa::grid_dependents_launch();
     pa::grid_dependency_wait();
-    const int s = blockIdx.z, g = blockIdx.y;
+    const int s = blockIdx.z, g = blockIdx.y, tile = blockIdx.x, t0 = tile * kTokens;
     const Seq sq(p, s);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, qc = lane & 3;
-    const int t0 = blockIdx.x * kWarps * kAgainBlocks * kBS;
-    if (t0 >= sq.L) return;
-    const int64_t sg = (int64_t)s * p.num_kv_heads + g;
     const int rows = p.group * sq.r;
-    for (int i = threadIdx.x; i < (rows + 15) / 16 * 16; i += kWarps * 32)
-        sum[i] = i < rows ? __ldg(p.sums + sg * p.row_slots + i) : make_float2(0.f, 0.f);
-    __syncthreads();
-    KRows<KV, D> k[kAgainBlocks];
-    float w[kAgainBlocks][2];
-    int tok0[kAgainBlocks];
-#pragma unroll
-    for (int i = 0; i < kAgainBlocks; ++i) {
-        w[i][0] = w[i][1] = 0.f;
-        tok0[i] = t0 + (warp * kAgainBlocks + i) * kBS;
-        if (tok0[i] < sq.L)
-            k[i].load(p, ((int64_t)block_of(p, s, tok0[i] / kBS) * p.num_kv_heads + g) * kBS, quad,
-                      qc);
+    if (t0 >= sq.L || (!SUM && rows == 0)) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, qc = lane & 3;
+    const int64_t sg = (int64_t)s * p.num_kv_heads + g;
+    const int nb = min(kBlocks, (sq.L - t0 + kBS - 1) / kBS);
+    float* const sums = reinterpret_cast<float*>(tile_s + kTokens * kRowBytes);
+    if (rows > 0) {
+        if (tid < nb) blocks_s[tid] = block_of(p, s, t0 / kBS + tid);
+        if (SUM)
+            for (int i = tid; i < p.row_warps * kTokens; i += 32 * kManyWarps) sums[i] = 0.f;
+        __syncthreads();
+        for (int i = tid; i < nb * kBS * kChunks; i += 32 * kManyWarps) {
+            const int t = i / kChunks, c = i % kChunks;
+            const int64_t row = ((int64_t)blocks_s[t / kBS] * p.num_kv_heads + g) * kBS + t % kBS;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(pa::smem_addr(
+                             tile_s + t * kRowBytes + 16 * KRows<KV, D>::staged_chunk(t, c))),
+                         "l"(static_cast<const uint8_t*>(p.k) + row * kRowBytes + 16 * c)
+                         : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
     }
-    for (int first = 0; first < rows; first += 8 * NR) {
+    const int row_warps = p.row_warps, token_warps = kManyWarps / row_warps;
+    const int rc = warp % row_warps, tg = warp / row_warps;
+    const int rounds = (rows + 8 * NR * row_warps - 1) / (8 * NR * row_warps);
+    for (int it = 0; it < rounds; ++it) {
+        const int first = (it * row_warps + rc) * 8 * NR;
         QRows<KV, D, NR> q;
-        q.load(p, sq, g, first, quad, qc);
+        RowSums<NR> own;
+        float2 total[NR][2];
+        own.clear();
+        if (first < rows) {              // warp-uniform
+            q.load(p, sq, g, first, quad, qc);
+            if constexpr (SUM) {
 #pragma unroll
-        for (int i = 0; i < kAgainBlocks; ++i) {
-            if (tok0[i] >= sq.L) continue;   // warp-uniform
-            float a[NR][4];
-            q.logits(k[i], tok0[i], quad, a);
+                for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = first + 8 * nr + 2 * qc + e;
+                        total[nr][e] = row < rows ? __ldg(p.sums + sg * p.row_slots + row)
+                                                  : make_float2(0.f, 0.f);
+                    }
+            }
+            for (int b = tg; b < nb; b += token_warps) {
+                KRows<KV, D> k;
+                k.load_scales(p, ((int64_t)blocks_s[b] * p.num_kv_heads + g) * kBS, quad);
+                k.load_staged(tile_s, b * kBS, quad, qc);
+                float a[NR][4];
+                q.logits(k, t0 + b * kBS, quad, a);
+                if constexpr (!SUM) {
+                    own.add(a);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float2 x = sum[first + 8 * nr + 2 * qc + e];
-                    w[i][0] = fmaf(pa::ex2(a[nr][e] - x.x), x.y, w[i][0]);
-                    w[i][1] = fmaf(pa::ex2(a[nr][2 + e] - x.x), x.y, w[i][1]);
+                    for (int h = 0; h < 2; ++h) {
+                        float w = 0.f;
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                w = fmaf(pa::ex2(a[nr][2 * h + e] - total[nr][e].x),
+                                         total[nr][e].y, w);
+                        w += __shfl_xor_sync(0xffffffffu, w, 1);
+                        w += __shfl_xor_sync(0xffffffffu, w, 2);
+                        if (qc == 0) sums[rc * kTokens + b * kBS + quad + 8 * h] += w;
+                    }
                 }
+            }
+        }
+        if constexpr (!SUM) {
+            own.finish(part_s[warp], quad, qc);
+            __syncthreads();
+            const int c = tid / (8 * NR), i = tid % (8 * NR);
+            const int row = (it * row_warps + c) * 8 * NR + i;
+            if (c < row_warps && row < rows) {
+                float2 t = part_s[c][i];
+                for (int w = 1; w < token_warps; ++w)
+                    merge(t.x, t.y, part_s[c + w * row_warps][i].x, part_s[c + w * row_warps][i].y);
+                p.stats[(sg * p.row_slots + row) * p.tiles + tile] = t;
+            }
+            __syncthreads();
         }
     }
-    const int64_t base = sg * p.stride;
-#pragma unroll
-    for (int i = 0; i < kAgainBlocks; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float x = w[i][h];
-            x += __shfl_xor_sync(0xffffffffu, x, 1);
-            x += __shfl_xor_sync(0xffffffffu, x, 2);
-            const int t = tok0[i] + quad + 8 * h;
-            if (qc == 0 && t < sq.L) p.out[base + t] = (p.in ? p.in[base + t] : 0.f) + x;
+    if constexpr (SUM) {
+        __syncthreads();
+        const int64_t base = sg * p.stride + t0;
+        for (int t = tid; t < min(kTokens, sq.L - t0); t += 32 * kManyWarps) {
+            float w = 0.f;
+            if (rows > 0)
+                for (int c = 0; c < row_warps; ++c) w += sums[c * kTokens + t];
+            p.out[base + t] = (p.in ? p.in[base + t] : 0.f) + w;
         }
+    }
 }
 
 struct Shape {
     int64_t rows;         // most query rows per KV head
-    int nr, chunks, row_slots, row_pad, tiles, tokens_pad;
-    int64_t stats_bytes, sums_bytes, logits_bytes;   // logits 0: computed again
+    int row_pad, tiles, tile_tokens, tokens_pad;
+    bool stored;
+    int64_t stats_bytes, sums_bytes, logits_bytes;
 };
 
-Shape shape_of(int num_seqs, int num_heads, int num_kv_heads, int max_q_len, int max_len) {
+// tile_tokens: of many_kernel, whose tiles depend on the cache type; 128 at least
+Shape shape_of(int num_seqs, int num_heads, int num_kv_heads, int max_q_len, int max_len,
+               int many_tile = 128) {
     Shape h{};
     h.rows = (int64_t)(num_heads / num_kv_heads) * max_q_len;
-    h.nr = h.rows <= 8 ? 1 : 2;
-    h.chunks = (int)((h.rows + 8 * h.nr - 1) / (8 * h.nr));
-    h.row_slots = (int)h.rows;
-    h.tiles = (max_len + kTileTokens - 1) / kTileTokens;
     h.tokens_pad = (max_len + kBS - 1) / kBS * kBS;
     const int64_t sg = (int64_t)num_seqs * num_kv_heads;
-    h.stats_bytes = (sg * h.rows * h.tiles * 8 + 255) / 256 * 256;
-    if (h.rows <= 16) {
-        h.row_pad = 1;
-        while (h.row_pad < h.rows) h.row_pad *= 2;
-        h.logits_bytes = sg * h.tokens_pad * h.row_pad * 4;
-        if (h.logits_bytes > kMaxStored) h.logits_bytes = 0;
+    h.row_pad = 1;
+    while (h.row_pad < h.rows) h.row_pad *= 2;
+    h.logits_bytes = sg * h.tokens_pad * h.row_pad * 4;
+    h.stored = h.rows <= 16 && h.logits_bytes <= kMaxStored;
+    if (!h.stored) {
+        h.logits_bytes = 0;
+        h.sums_bytes = (sg * h.rows * 8 + 255) / 256 * 256;
     }
-    if (!h.logits_bytes) h.sums_bytes = (sg * h.rows * 8 + 255) / 256 * 256;
+    h.tile_tokens = h.stored ? kTileTokens : many_tile;
+    h.tiles = (max_len + h.tile_tokens - 1) / h.tile_tokens;
+    h.stats_bytes = (sg * h.rows * h.tiles * 8 + 255) / 256 * 256;
     return h;
-}
-
-template <int KV, int D, int NR>
-pa_status launch_logits(const Params& p, cudaStream_t st) {
-    return pa::cuda_status(
-        pa::launch_pdl(logits_kernel<KV, D, NR>,
-                       dim3(p.tiles, p.num_kv_heads * p.chunks, p.num_seqs), dim3(kWarps * 32), 0,
-                       st, p),
-        "accumulate_weights logits launch");
 }
 
 template <int RP>
@@ -573,10 +709,21 @@ pa_status launch_stored(const Params& p, cudaStream_t st) {
 }
 
 template <int KV, int D>
-pa_status launch_typed(const Params& p, int nr, int64_t rows, cudaStream_t st) {
-    if (pa_status s = nr == 1 ? launch_logits<KV, D, 1>(p, st) : launch_logits<KV, D, 2>(p, st))
-        return s;
-    if (p.logits) {
+pa_status launch_typed(Params& p, const Shape& small, void* workspace, cudaStream_t st) {
+    char* const ws = static_cast<char*>(workspace);
+    p.stats = reinterpret_cast<float2*>(ws);
+    if (small.stored) {
+        p.logits = reinterpret_cast<float*>(ws + small.stats_bytes);
+        p.tiles = small.tiles;
+        p.tile_tokens = small.tile_tokens;
+        p.row_pad = small.row_pad;
+        const dim3 grid(p.tiles, p.num_kv_heads, p.num_seqs);
+        if (pa_status s = pa::cuda_status(
+                small.rows <= 8
+                    ? pa::launch_pdl(logits_kernel<KV, D, 1>, grid, dim3(kWarps * 32), 0, st, p)
+                    : pa::launch_pdl(logits_kernel<KV, D, 2>, grid, dim3(kWarps * 32), 0, st, p),
+                "accumulate_weights logits launch"))
+            return s;
         switch (p.row_pad) {
             case 1: return launch_stored<1>(p, st);
             case 2: return launch_stored<2>(p, st);
@@ -585,29 +732,50 @@ pa_status launch_typed(const Params& p, int nr, int64_t rows, cudaStream_t st) {
             default: return launch_stored<16>(p, st);
         }
     }
+    constexpr int kTokens = many_tokens<KV, D>();
+    const Shape h = shape_of(p.num_seqs, p.num_heads, p.num_kv_heads, p.max_q_len, p.max_len,
+                             kTokens);
+    p.tiles = h.tiles;
+    p.tile_tokens = kTokens;
+    p.sums = reinterpret_cast<float2*>(ws + h.stats_bytes);
+    p.row_warps = 1;
+    while (p.row_warps < kManyWarps && 16 * p.row_warps < h.rows) p.row_warps *= 2;
+    const int tile = kTokens * KRows<KV, D>::kRowBytes, sums = 4 * p.row_warps * kTokens;
+    static bool attr_set = false;   // per instantiation; benign race (idempotent)
+    if (!attr_set) {
+        if (pa_status s = pa::cuda_status(
+                cudaFuncSetAttribute(many_kernel<KV, D, true>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     tile + 4 * kManyWarps * kTokens),
+                "accumulate_weights: set shared memory size"))
+            return s;
+        attr_set = true;
+    }
+    const dim3 grid(p.tiles, p.num_kv_heads, p.num_seqs), block(32 * kManyWarps);
+    if (pa_status s = pa::cuda_status(
+            pa::launch_pdl(many_kernel<KV, D, false>, grid, block, (size_t)tile, st, p),
+            "accumulate_weights logits launch"))
+        return s;
     if (pa_status s = pa::cuda_status(
             pa::launch_pdl(rows_kernel,
-                           dim3((unsigned)((rows + kWarps - 1) / kWarps), p.num_kv_heads,
+                           dim3((unsigned)((h.rows + kWarps - 1) / kWarps), p.num_kv_heads,
                                 p.num_seqs),
                            dim3(kWarps * 32), 0, st, p),
             "accumulate_weights row sums launch"))
         return s;
-    const int tokens = kWarps * kAgainBlocks * kBS;
     return pa::cuda_status(
-        pa::launch_pdl(again_kernel<KV, D>,
-                       dim3((p.max_len + tokens - 1) / tokens, p.num_kv_heads, p.num_seqs),
-                       dim3(kWarps * 32), (size_t)((rows + 15) / 16 * 16 * 8), st, p),
+        pa::launch_pdl(many_kernel<KV, D, true>, grid, block, (size_t)(tile + sums), st, p),
         "accumulate_weights sum launch");
 }
 
 template <int D>
-pa_status launch_kv(pa_dtype kv, const Params& p, int nr, int64_t rows, cudaStream_t st) {
+pa_status launch_kv(pa_dtype kv, Params& p, const Shape& h, void* workspace, cudaStream_t st) {
     switch (kv) {
-        case PA_F16: return launch_typed<PA_F16, D>(p, nr, rows, st);
-        case PA_BF16: return launch_typed<PA_BF16, D>(p, nr, rows, st);
-        case PA_INT8: return launch_typed<PA_INT8, D>(p, nr, rows, st);
-        case PA_INT4: return launch_typed<PA_INT4, D>(p, nr, rows, st);
-        default: return launch_typed<PA_FP8_E4M3, D>(p, nr, rows, st);
+        case PA_F16: return launch_typed<PA_F16, D>(p, h, workspace, st);
+        case PA_BF16: return launch_typed<PA_BF16, D>(p, h, workspace, st);
+        case PA_INT8: return launch_typed<PA_INT8, D>(p, h, workspace, st);
+        case PA_INT4: return launch_typed<PA_INT4, D>(p, h, workspace, st);
+        default: return launch_typed<PA_FP8_E4M3, D>(p, h, workspace, st);
     }
 }
 
@@ -649,10 +817,10 @@ extern "C" pa_status pa_accumulate_weights(
     if (((uintptr_t)scores_in | (uintptr_t)k_scale) % 4)
         return fail(PA_ERR_INVALID_ARG, "scores and k_scale must be 4-byte aligned");
     const Shape h = shape_of(num_seqs, num_heads, num_kv_heads, max_q_len, max_context_len);
-    if (num_seqs > 65535 || (int64_t)num_kv_heads * h.chunks > 65535 || h.rows > kMaxRows)
+    if (num_seqs > 65535 || num_kv_heads > 65535 || h.rows > kMaxRows)
         return fail(PA_ERR_UNSUPPORTED,
                     "accumulate_weights call too large (%d sequences, %d KV heads, %lld query rows "
-                    "per KV head; at most 65535, and %d rows)",
+                    "per KV head; at most 65535, 65535 and %d)",
                     num_seqs, num_kv_heads, (long long)h.rows, kMaxRows);
     const size_t need = (size_t)(h.stats_bytes + h.sums_bytes + h.logits_bytes);
     if (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256)
@@ -674,10 +842,6 @@ extern "C" pa_status pa_accumulate_weights(
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.qsl = query_start_loc;
-    p.stats = static_cast<float2*>(workspace);
-    char* const after = static_cast<char*>(workspace) + h.stats_bytes;
-    if (h.logits_bytes) p.logits = reinterpret_cast<float*>(after);
-    else p.sums = reinterpret_cast<float2*>(after);
     p.err = pa::device_error_word();
     p.stride = score_stride;
     p.num_seqs = num_seqs;
@@ -690,12 +854,9 @@ extern "C" pa_status pa_accumulate_weights(
     p.max_blocks = max_blocks_per_seq;
     p.max_len = max_context_len;
     p.tokens_pad = h.tokens_pad;
-    p.tiles = h.tiles;
-    p.row_slots = h.row_slots;
-    p.row_pad = h.row_pad;
-    p.chunks = h.chunks;
+    p.row_slots = (int)h.rows;
     p.q_bf16 = q_dtype == PA_BF16;
     p.scale_log2 = scale * kLog2e;
-    return head_dim == 128 ? launch_kv<128>(kv_dtype, p, h.nr, h.rows, st)
-                           : launch_kv<64>(kv_dtype, p, h.nr, h.rows, st);
+    return head_dim == 128 ? launch_kv<128>(kv_dtype, p, h, workspace, st)
+                           : launch_kv<64>(kv_dtype, p, h, workspace, st);
 }

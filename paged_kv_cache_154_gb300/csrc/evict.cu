@@ -240,9 +240,9 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
             }
             __syncthreads();
             // a warp sums a chunk of 128 bins (chunk 0 the highest); then the n-th key's chunk is
-            // found from the chunks' sums, and its bin from that chunk's bins, in a cluster by
-            // one warp that reads both from all its CTAs (the whole histograms would be 16
-            // times as much), else by every warp for itself
+            // found from the chunks' sums, and its bin from that chunk's bins, by one warp, which
+            // in a cluster reads both from all CTAs (the whole histograms would be 16 times as
+            // much)
             const int chunks = bins / 128;
             for (int i = warp; i < chunks; i += kWarps) {
                 const uint4 v = *reinterpret_cast<const uint4*>(h + bins - 128 * (i + 1) + 4 * lane);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
             }
             sync();
             uint32_t bin = 0, above = 0, in_bin = 0;   // the bin, keys in higher ones, and in it
-            if (CL == 1 || warp == 0) {
+            if (warp == 0) {
                 uint32_t upto = 0;
                 if (lane < chunks) {
                     if constexpr (CL == 1) {
@@ -305,11 +305,9 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
                 bin = __shfl_sync(0xffffffffu, (uint32_t)at, owner);
                 in_bin = __shfl_sync(0xffffffffu, found, owner);
             }
-            if constexpr (CL > 1) {
-                if (tid == 0) search_s[d] = make_uint4(bin, above, in_bin, 0u);
-                __syncthreads();
-                bin = search_s[d].x, above = search_s[d].y, in_bin = search_s[d].z;
-            }
+            if (tid == 0) search_s[d] = make_uint4(bin, above, in_bin, 0u);
+            __syncthreads();
+            bin = search_s[d].x, above = search_s[d].y, in_bin = search_s[d].z;
             left -= above;
             cut |= bin << shift;
             if (in_bin == left) {                      // all of the bin stays: no need to split it
@@ -470,94 +468,94 @@ struct MoveParams {
     int max_moves, num_kv_heads, max_len, num_blocks, max_blocks;
 };
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveBatch = 4;
+constexpr int kMoveWarps = 4;
+constexpr int kMoveAhead = 4;   // copies on the way together, per warp: 8 were slower (80 us
+                                // against 70 with the selection of 131072 tokens), 2 too (74)
 
-// Grid: (parts, KV head, sequence); the parts stride over the row's moves. A
-// thread copies one 16-byte vector of a K or V row, or one scale and zero point,
-// of kMoveBatch moves at a time: all their loads are on the way before the first
-// store (no destination is a source, so the order is free). The lists, the table
-// entries and the rows are three dependent reads: with one copy a thread the
-// kernel waited on them (16 prompts to 1024 of up to 8192 tokens: 23.7 us).
+// Grid: (parts, KV head, sequence); the warps of all parts share the row's moves.
+// A lane looks up one move (its slots, their blocks) and copies its scales and
+// zero points; then the warp copies the moves' K and V rows in 16-byte vectors,
+// 32 / (2 VECS) moves at a time and kMoveAhead such loads on the way before the
+// first store (no destination is a source, so the order is free). Bound by
+// memory: each row in and out, in pieces of 256 bytes and less that lie apart.
 template <int VECS, int GROUPS>   // 16-byte vectors and scales of a row
-__global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const MoveParams p) {
-    constexpr int kPieces = 2 * VECS + 2 * GROUPS;
+__global__ void __launch_bounds__(32 * kMoveWarps) move_tokens_kernel(const MoveParams p) {
+    constexpr int kPieces = 2 * VECS, kMoves = 32 / kPieces;   // moves of one warp-wide copy
+    static_assert(kPieces <= 32, "a move fits a warp");
+    pa::grid_dependents_launch();
     pa::grid_dependency_wait();
-    const int s = blockIdx.z, g = blockIdx.y;
+    const int s = blockIdx.z, g = blockIdx.y, lane = threadIdx.x & 31;
     const int64_t sg = (int64_t)s * p.num_kv_heads + g;
     const int L = max(0, min(__ldg(p.context_lens + s), p.max_len));
     const int count = min(__ldg(p.move_counts + sg), p.max_moves);
     const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
-    const int64_t items = (int64_t)count * kPieces;
-    const int64_t step = (int64_t)gridDim.x * kMoveThreads;
-    for (int64_t i0 = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; i0 < items;
-         i0 += kMoveBatch * step) {
-        int2 mv[kMoveBatch];
-        int bs[kMoveBatch], bd[kMoveBatch];
-#pragma unroll
-        for (int k = 0; k < kMoveBatch; ++k) {
-            const int64_t i = i0 + k * step;
-            mv[k] = make_int2(0, 0);
-            if (i < items) mv[k] = __ldg(p.moves + sg * p.max_moves + i / kPieces);
-        }
-#pragma unroll
-        for (int k = 0; k < kMoveBatch; ++k) {
-            const bool in = mv[k].x >= 0 && mv[k].x < L && mv[k].y >= 0 && mv[k].y < L;
-            bs[k] = bd[k] = -1;
-            if (i0 + k * step >= items) continue;
-            if (!in) {
+    const int warps = gridDim.x * kMoveWarps;
+    // moves of a warp's turn: at most one a lane, and as many turns for every warp
+    const int turns = max(1, (count + 32 * warps - 1) / (32 * warps));
+    const int per = max(1, (count + turns * warps - 1) / (turns * warps));
+    const int v = lane % kPieces >= VECS, c = lane % kPieces - v * VECS;
+    uint4* const code = p.code[v];
+    for (int64_t m0 = (int64_t)(blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * per; m0 < count;
+         m0 += (int64_t)warps * per) {
+        const int here = (int)min((int64_t)per, count - m0);
+        int bs = -1, bd = -1, at = 0;    // blocks, and the offsets in them: source | destination << 4
+        if (lane < here) {
+            const int2 mv = __ldg(p.moves + sg * p.max_moves + m0 + lane);
+            if (mv.x < 0 || mv.x >= L || mv.y < 0 || mv.y >= L) {
                 if (p.err) atomicOr(p.err, pa::ERR_BAD_SLOT);
-                continue;
-            }
-            bs[k] = __ldg(table + mv[k].x / kBS);
-            bd[k] = __ldg(table + mv[k].y / kBS);
-            if (bs[k] < 0 || bs[k] >= p.num_blocks || bd[k] < 0 || bd[k] >= p.num_blocks) {
-                if (p.err) atomicOr(p.err, pa::ERR_BAD_BLOCK);
-                bs[k] = -1;
-            }
-        }
-        uint4 data[kMoveBatch];
-#pragma unroll
-        for (int k = 0; k < kMoveBatch; ++k) {
-            if (bs[k] < 0) continue;
-            const int piece = (int)((i0 + k * step) % kPieces);
-            const int64_t src = ((int64_t)bs[k] * p.num_kv_heads + g) * kBS + mv[k].x % kBS;
-            if (GROUPS == 0 || piece < 2 * VECS) {
-                const int v = piece >= VECS;
-                data[k] = __ldcs(p.code[v] + src * VECS + (piece - v * VECS));
-            } else if constexpr (GROUPS > 0) {
-                const int c = piece - 2 * VECS, v = c >= GROUPS;
-                data[k].x = __float_as_uint(p.scale[v][src * GROUPS + (c - v * GROUPS)]);
-                data[k].y = (uint8_t)p.zp[v][src * GROUPS + (c - v * GROUPS)];
+            } else {
+                bs = __ldg(table + mv.x / kBS), bd = __ldg(table + mv.y / kBS);
+                at = mv.x % kBS | mv.y % kBS << 4;
+                if (bs < 0 || bs >= p.num_blocks || bd < 0 || bd >= p.num_blocks) {
+                    if (p.err) atomicOr(p.err, pa::ERR_BAD_BLOCK);
+                    bs = -1;
+                }
             }
         }
+        auto row_of = [&](int blk, int off) {
+            return ((int64_t)blk * p.num_kv_heads + g) * kBS + off;
+        };
+        if (GROUPS > 0 && bs >= 0) {
+            const int64_t src = row_of(bs, at & 15) * GROUPS, dst = row_of(bd, at >> 4) * GROUPS;
+            float sc[2][GROUPS > 0 ? GROUPS : 1];
+            int8_t zp[2][GROUPS > 0 ? GROUPS : 1];
 #pragma unroll
-        for (int k = 0; k < kMoveBatch; ++k) {
-            if (bs[k] < 0) continue;
-            const int piece = (int)((i0 + k * step) % kPieces);
-            const int64_t dst = ((int64_t)bd[k] * p.num_kv_heads + g) * kBS + mv[k].y % kBS;
-            if (GROUPS == 0 || piece < 2 * VECS) {
-                const int v = piece >= VECS;
-                p.code[v][dst * VECS + (piece - v * VECS)] = data[k];
-            } else if constexpr (GROUPS > 0) {
-                const int c = piece - 2 * VECS, v = c >= GROUPS;
-                p.scale[v][dst * GROUPS + (c - v * GROUPS)] = __uint_as_float(data[k].x);
-                p.zp[v][dst * GROUPS + (c - v * GROUPS)] = (int8_t)data[k].y;
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < GROUPS; ++j) sc[i][j] = p.scale[i][src + j], zp[i][j] = p.zp[i][src + j];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < GROUPS; ++j) p.scale[i][dst + j] = sc[i][j], p.zp[i][dst + j] = zp[i][j];
+        }
+        for (int i0 = 0; i0 < here; i0 += kMoves * kMoveAhead) {
+            uint4 data[kMoveAhead];
+            int to[kMoveAhead], off[kMoveAhead];
+#pragma unroll
+            for (int k = 0; k < kMoveAhead; ++k) {
+                const int m = i0 + k * kMoves + lane / kPieces;   // past the last: lanes with bs = -1
+                const int from = __shfl_sync(0xffffffffu, bs, m & 31);
+                to[k] = __shfl_sync(0xffffffffu, bd, m & 31);
+                off[k] = __shfl_sync(0xffffffffu, at, m & 31);
+                if (m >= here || from < 0) to[k] = -1;
+                if (to[k] >= 0) data[k] = __ldcs(code + row_of(from, off[k] & 15) * VECS + c);
             }
+#pragma unroll
+            for (int k = 0; k < kMoveAhead; ++k)
+                if (to[k] >= 0) code[row_of(to[k], off[k] >> 4) * VECS + c] = data[k];
         }
     }
 }
 
 template <int VECS, int GROUPS>
 pa_status launch_move(const MoveParams& p, int num_seqs, cudaStream_t st) {
-    // about 8 CTAs a SM over the whole call, but no more than the moves could use
+    // 8 CTAs a SM over the whole call, but no more than the moves could use
     const int64_t rows = (int64_t)num_seqs * p.num_kv_heads;
-    const int64_t could = ((int64_t)p.max_moves * (2 * VECS + 2 * GROUPS) +
-                           kMoveBatch * kMoveThreads - 1) / (kMoveBatch * kMoveThreads);
+    const int64_t could = (p.max_moves + kMoveWarps - 1) / kMoveWarps;
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(could, (152 * 8 + rows - 1) / rows));
     return pa::cuda_status(pa::launch_pdl(move_tokens_kernel<VECS, GROUPS>,
                                           dim3((unsigned)parts, p.num_kv_heads, num_seqs),
-                                          dim3(kMoveThreads), 0, st, p),
+                                          dim3(32 * kMoveWarps), 0, st, p),
                            "move_tokens launch");
 }
 
