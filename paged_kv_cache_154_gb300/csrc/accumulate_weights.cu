@@ -47,8 +47,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kUnit = 16777216.f;       // 2^24: masked nibbles are subnormals in units of 2^-24
 constexpr int kBS = 16;                  // tokens per block
 constexpr int kWarps = 4;                // warps per CTA
-constexpr int kTileTokens = 512;         // tokens of a logits CTA: 8 blocks a warp
-static_assert(kTileTokens / kBS / kWarps <= 32, "a lane holds a block id");
+constexpr int kMaxTile = 2048;            // tokens of a logits CTA: a lane holds a block id
+static_assert(kMaxTile / kBS / kWarps <= 32, "a lane holds a block id");
 constexpr int kOutTokens = 1024;         // tokens of a stored CTA
 constexpr int kManyWarps = 8;            // warps of a many_kernel CTA
 constexpr int kMaxRows = 4096;           // query rows per KV head
@@ -116,6 +116,22 @@ __device__ __forceinline__ float exp2i(int e) {   // 2^e for e in [-126, 127]
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// the product of mma_16816 on a zero accumulator
+template <bool BF16>
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // (m, l) of a pair of partial sums
 __device__ __forceinline__ void merge(float& m, float& l, float m2, float l2) {
     const float top = fmaxf(m, m2);
@@ -145,10 +161,14 @@ struct KRows {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int64_t t = row + quad + 8 * h;
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    scale[h][g] = __ldg(p.k_scale + t * kGroups + g);
-                    zp[h][g] = __ldg(p.k_zp + t * kGroups + g);
+                if constexpr (kGroups == 2) {
+                    const float2 f = __ldg(reinterpret_cast<const float2*>(p.k_scale) + t);
+                    const uint16_t z = __ldg(reinterpret_cast<const uint16_t*>(p.k_zp) + t);
+                    scale[h][0] = f.x, scale[h][1] = f.y;
+                    zp[h][0] = z & 255, zp[h][1] = z >> 8;   // 0 .. 15
+                } else {
+                    scale[h][0] = __ldg(p.k_scale + t);
+                    zp[h][0] = __ldg(p.k_zp + t);
                 }
             }
         }
@@ -178,18 +198,27 @@ struct KRows {
         if constexpr (KV == PA_INT4) return kRowBytes == 64 ? chunk ^ (row & 2) : chunk;
         else return kRowBytes >= 128 ? chunk ^ ((row & 1) << 2) : chunk;
     }
-    // from a staged tile, at tile rows `row` + quad, + quad + 8
-    __device__ __forceinline__ void load_staged(const uint8_t* tile, int row, int quad, int qc) {
+    // A lane's place in a staged block (of 16 rows); a load further is an exclusive-or away.
+    __device__ __forceinline__ static uint32_t staged_at(int quad, int qc) {
+        const int at = 4 * kVec * qc;
+        return quad * kRowBytes + 16 * staged_chunk(quad, at / 16) + at % 16;
+    }
+    __device__ __forceinline__ void load_staged(uint32_t at) {   // staged block + staged_at
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int t = row + quad + 8 * h;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < kWords / kVec; ++j) {
-                const int at = 16 * kVec * j + 4 * kVec * qc;
-                const uint8_t* src = tile + t * kRowBytes + 16 * staged_chunk(t, at / 16) + at % 16;
-                put<Vec>(h, j, [&] { return *reinterpret_cast<const Vec*>(src); });
+                const uint32_t src = (at + 8 * h * kRowBytes) ^ (16 * kVec * j);
+                if constexpr (kVec == 4)
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[h][4 * j]), "=r"(w[h][4 * j + 1]), "=r"(w[h][4 * j + 2]),
+                                   "=r"(w[h][4 * j + 3])
+                                 : "r"(src));
+                else
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                 : "=r"(w[h][2 * j]), "=r"(w[h][2 * j + 1])
+                                 : "r"(src));
             }
-        }
     }
 
     // a pair of dims of one token, in the low (hi = 0) or high columns of k-step kk; INT4: in
@@ -320,23 +349,21 @@ struct QRows {
 
     // logits (base-2 units) of the block whose first token is tok0: a[nr][2 h + e] of
     // token quad + 8 h and row 8 nr + 2 qc + e; -inf where the row does not see it
-    __device__ __forceinline__ void logits(const K& k, int tok0, int quad,
+    // (masked: some row may not see all of it)
+    __device__ __forceinline__ void logits(const K& k, int tok0, int quad, bool masked,
                                            float (&a)[NR][4]) const {
         float s[NR][K::kGroups][4];
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int g = 0; g < K::kGroups; ++g)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nr][g][e] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < K::kSteps; ++kk) {
             uint32_t f[4];
             k.frag(kk, f);
+            const int grp = kk * K::kGroups / K::kSteps;
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
-                pa::mma_16816<KV == PA_BF16>(s[nr][kk * K::kGroups / K::kSteps], f, b[nr][kk][0],
-                                             b[nr][kk][1]);
+                if (kk % (K::kSteps / K::kGroups) == 0)
+                    mma_first<KV == PA_BF16>(s[nr][grp], f, b[nr][kk][0], b[nr][kk][1]);
+                else
+                    pa::mma_16816<KV == PA_BF16>(s[nr][grp], f, b[nr][kk][0], b[nr][kk][1]);
         }
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
@@ -350,48 +377,80 @@ struct QRows {
                     if constexpr (K::kGroups == 2)
                         v = fmaf(fmaf(-(float)k.zp[h][1], qsum[nr][1][e], s[nr][1][2 * h + e]),
                                  k.scale[h][1], v);
-                    v *= mul[nr][e];
-                    if (tok0 + quad + 8 * h > bound[nr][e]) v = -INFINITY;
-                    a[nr][2 * h + e] = v;
+                    a[nr][2 * h + e] = v * mul[nr][e];
                 }
+        if (masked) {
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (tok0 + quad + 8 * (i >> 1) > bound[nr][i & 1]) a[nr][i] = -INFINITY;
+        }
     }
 };
 
-// The running (m, l) of a lane's rows, over the tokens it sees.
+// The running sums of a warp's rows: l = sum 2^(a - ref) over the tokens that the
+// lane sees. The reference is the warp's (lanes of a row agree) and moves only when
+// a logit passes it by 2^8; -inf: no token seen yet.
 template <int NR>
 struct RowSums {
-    float m[NR][2], l[NR][2];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) m[nr][e] = -INFINITY, l[nr][e] = 0.f;
-    }
-    __device__ __forceinline__ void add(const float (&a)[NR][4]) {
+    float ref[NR][2], l[NR][2];
+    __device__ __forceinline__ void clear(const int (&bound)[NR][2]) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float mx = fmaxf(a[nr][e], a[nr][2 + e]);
-                if (mx > m[nr][e]) {
-                    l[nr][e] *= pa::ex2(m[nr][e] - mx);
-                    m[nr][e] = mx;
-                }
-                const float ref = m[nr][e] == -INFINITY ? 0.f : m[nr][e];
-                l[nr][e] += pa::ex2(a[nr][e] - ref) + pa::ex2(a[nr][2 + e] - ref);
+                ref[nr][e] = bound[nr][e] < 0 ? 0.f : -INFINITY;   // rows that see nothing at all
+                l[nr][e] = 0.f;
             }
     }
-    // over the warp's tokens: rows 8 nr + 2 qc + e to part[], by the lanes of quad 0
+    __device__ __forceinline__ void add(const float (&a)[NR][4]) {
+        float t[NR][4];
+        bool raise = false;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[nr][i] = a[nr][i] - ref[nr][i & 1];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) raise |= !(fmaxf(t[nr][e], t[nr][2 + e]) <= 8.f);
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(a[nr][e], a[nr][2 + e]);
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    if (mx > ref[nr][e] + 8.f) {
+                        l[nr][e] *= pa::ex2(ref[nr][e] - mx);   // 0 while ref is -inf
+                        ref[nr][e] = mx;
+                    }
+                    // still no token: nothing but -inf and NaN, which stays
+                    const bool none = ref[nr][e] == -INFINITY;
+#pragma unroll
+                    for (int i = e; i < 4; i += 2)
+                        t[nr][i] = none && a[nr][i] == -INFINITY ? -INFINITY
+                                                                 : a[nr][i] - ref[nr][e];
+                }
+        }
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) l[nr][e] += pa::ex2(t[nr][e]) + pa::ex2(t[nr][2 + e]);
+    }
+    // over the warp's tokens: (reference, sum) of rows 8 nr + 2 qc + e to part[]
     __device__ __forceinline__ void finish(float2* part, int quad, int qc) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                float sum = l[nr][e];
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
-                    merge(m[nr][e], l[nr][e], __shfl_xor_sync(0xffffffffu, m[nr][e], off),
-                          __shfl_xor_sync(0xffffffffu, l[nr][e], off));
-                if (quad == 0) part[8 * nr + 2 * qc + e] = make_float2(m[nr][e], l[nr][e]);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                if (quad == 0) part[8 * nr + 2 * qc + e] = make_float2(ref[nr][e], sum);
             }
     }
 };
@@ -403,7 +462,7 @@ __device__ __forceinline__ int block_of(const Params& p, int s, int i) {
     return 0;
 }
 
-// Grid: (tiles of kTileTokens tokens, KV head, sequence): few rows, stored logits.
+// Grid: (tiles of p.tile_tokens tokens, KV head, sequence): few rows, stored logits.
 template <int KV, int D, int NR>
 __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
     // blocks of K in registers, on their way while one is multiplied
@@ -414,11 +473,11 @@ __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
     const int s = blockIdx.z, g = blockIdx.y, tile = blockIdx.x;
     const Seq sq(p, s);
     const int rows = p.group * sq.r;
-    if (tile * kTileTokens >= sq.L || rows == 0) return;
+    if (tile * p.tile_tokens >= sq.L || rows == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, qc = lane & 3;
     // this warp's blocks: b0 + warp, + kWarps, ...
-    const int b0 = tile * (kTileTokens / kBS) + warp;
-    const int nb = min((sq.L + kBS - 1) / kBS, (tile + 1) * (kTileTokens / kBS));
+    const int b0 = tile * (p.tile_tokens / kBS) + warp;
+    const int nb = min((sq.L + kBS - 1) / kBS, (tile + 1) * (p.tile_tokens / kBS));
     const int n = b0 < nb ? (nb - b0 + kWarps - 1) / kWarps : 0;
     int my_block = 0;
     if (lane < n) my_block = block_of(p, s, b0 + lane * kWarps);
@@ -433,7 +492,10 @@ __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
     QRows<KV, D, NR> q;
     q.load(p, sq, g, 0, quad, qc);
     RowSums<NR> sums;
-    sums.clear();
+    sums.clear(q.bound);
+    // the lane's logits: rows 8 nr + 2 qc and + 1 of token quad, those that are kept
+    float* const keep = p.logits +
+                        ((int64_t)(s * p.num_kv_heads + g) * p.tokens_pad + quad) * p.row_pad + 2 * qc;
     for (int i0 = 0; i0 < n; i0 += kDepth) {
 #pragma unroll
         for (int u = 0; u < kDepth; ++u) {
@@ -442,20 +504,18 @@ __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
             if (i + kDepth - 1 < n) fetch(k[(u + kDepth - 1) % kDepth], i + kDepth - 1);
             const int tok0 = (b0 + i * kWarps) * kBS;
             float a[NR][4];
-            q.logits(k[u], tok0, quad, a);
+            q.logits(k[u], tok0, quad, tok0 + kBS - 1 > sq.L - sq.r, a);
             sums.add(a);
+            float* const dst = keep + (int64_t)tok0 * p.row_pad;
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int row = 8 * nr + 2 * qc;
-                    float* dst = p.logits + ((int64_t)(s * p.num_kv_heads + g) * p.tokens_pad +
-                                             tok0 + quad + 8 * h) * p.row_pad + row;
-                    if (row + 1 < p.row_pad)
-                        *reinterpret_cast<float2*>(dst) = make_float2(a[nr][2 * h],
-                                                                      a[nr][2 * h + 1]);
-                    else if (row < p.row_pad)
-                        *dst = a[nr][2 * h];
+                    float* const at = dst + 8 * h * p.row_pad + 8 * nr;
+                    if (8 * nr + 2 * qc + 1 < p.row_pad)
+                        *reinterpret_cast<float2*>(at) = make_float2(a[nr][2 * h], a[nr][2 * h + 1]);
+                    else if (8 * nr + 2 * qc < p.row_pad)
+                        *at = a[nr][2 * h];
                 }
         }
     }
@@ -552,13 +612,11 @@ __global__ void __launch_bounds__(256) stored_kernel(const Params p) {
     }
 }
 
-// Tokens of a many_kernel tile: 32 KB of K, at most 512.
-template <int KV, int D>
-constexpr int many_tokens() {
-    return 32768 / KRows<KV, D>::kRowBytes < 512 ? 32768 / KRows<KV, D>::kRowBytes : 512;
-}
+// Tokens of a many_kernel tile: 32 KB of K at most, and few enough that a ragged
+// batch spreads evenly (with 256 and more, SMs were idle for 38 % of the call).
+constexpr int kManyTokens = 128;
 
-// Many rows. Grid: (tiles of many_tokens(), KV head, sequence). The tile's K is
+// Many rows. Grid: (tiles of kManyTokens, KV head, sequence). The tile's K is
 // staged in shared memory once; warp (rc, tg) takes the row chunks rc, rc +
 // row_warps, .. of 16 rows and the tile's blocks tg, tg + token_warps, ... SUM
 // false: the rows' (m, l) over the tile; SUM true: the weights of the tile's
@@ -568,9 +626,10 @@ constexpr int many_tokens() {
 // 128 rows, d = 64).
 template <int KV, int D, bool SUM>
 __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
-    constexpr int NR = 2, kTokens = many_tokens<KV, D>(), kBlocks = kTokens / kBS;
+    constexpr int NR = 2, kTokens = kManyTokens, kBlocks = kTokens / kBS;
     constexpr int kRowBytes = KRows<KV, D>::kRowBytes, kChunks = kRowBytes / 16;
-    extern __shared__ __align__(128) uint8_t tile_s[];   // K, then SUM: float [row_warps][kTokens]
+    // K, then SUM: float [row_warps][kTokens]; aligned to the span that staged rows exchange in
+    extern __shared__ __align__(256) uint8_t tile_s[];
     __shared__ int blocks_s[kBlocks];
     __shared__ float2 part_s[kManyWarps][8 * NR];
     pa::grid_dependents_launch();
@@ -599,17 +658,20 @@ __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
     }
+    const uint32_t staged = pa::smem_addr(tile_s) + KRows<KV, D>::staged_at(quad, qc);
     const int row_warps = p.row_warps, token_warps = kManyWarps / row_warps;
     const int rc = warp % row_warps, tg = warp / row_warps;
     const int rounds = (rows + 8 * NR * row_warps - 1) / (8 * NR * row_warps);
     for (int it = 0; it < rounds; ++it) {
         const int first = (it * row_warps + rc) * 8 * NR;
+        // the last token that every row of the chunk sees (rows past the last see none)
+        const int last_seen = first + 8 * NR <= rows ? sq.L - sq.r + first / p.group : -1;
         QRows<KV, D, NR> q;
         RowSums<NR> own;
         float2 total[NR][2];
-        own.clear();
         if (first < rows) {              // warp-uniform
             q.load(p, sq, g, first, quad, qc);
+            own.clear(q.bound);
             if constexpr (SUM) {
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr)
@@ -623,9 +685,9 @@ __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
             for (int b = tg; b < nb; b += token_warps) {
                 KRows<KV, D> k;
                 k.load_scales(p, ((int64_t)blocks_s[b] * p.num_kv_heads + g) * kBS, quad);
-                k.load_staged(tile_s, b * kBS, quad, qc);
+                k.load_staged(staged + b * kBS * kRowBytes);
                 float a[NR][4];
-                q.logits(k, t0 + b * kBS, quad, a);
+                q.logits(k, t0 + b * kBS, quad, t0 + (b + 1) * kBS - 1 > last_seen, a);
                 if constexpr (!SUM) {
                     own.add(a);
                 } else {
@@ -646,7 +708,7 @@ __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
             }
         }
         if constexpr (!SUM) {
-            own.finish(part_s[warp], quad, qc);
+            if (first < rows) own.finish(part_s[warp], quad, qc);
             __syncthreads();
             const int c = tid / (8 * NR), i = tid % (8 * NR);
             const int row = (it * row_warps + c) * 8 * NR + i;
@@ -671,6 +733,15 @@ __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
     }
 }
 
+// Tokens of a logits CTA: one wave of four CTAs a SM where a tile of up to
+// kMaxTile does that (fewer starts: 100001 tokens of 8 heads 30.6 us against 32.6
+// with 512), else 512, whose many waves even out a ragged batch (Llama-3-8B step:
+// 64.7 us, 70.9 with 2048).
+int stored_tile(int64_t tokens) {
+    const int64_t t = (tokens + 4 * 152 - 1) / (4 * 152);
+    return t > kMaxTile ? 512 : (int)std::max<int64_t>(128, (t + 63) / 64 * 64);
+}
+
 struct Shape {
     int64_t rows;         // most query rows per KV head
     int row_pad, tiles, tile_tokens, tokens_pad;
@@ -678,9 +749,7 @@ struct Shape {
     int64_t stats_bytes, sums_bytes, logits_bytes;
 };
 
-// tile_tokens: of many_kernel, whose tiles depend on the cache type; 128 at least
-Shape shape_of(int num_seqs, int num_heads, int num_kv_heads, int max_q_len, int max_len,
-               int many_tile = 128) {
+Shape shape_of(int num_seqs, int num_heads, int num_kv_heads, int max_q_len, int max_len) {
     Shape h{};
     h.rows = (int64_t)(num_heads / num_kv_heads) * max_q_len;
     h.tokens_pad = (max_len + kBS - 1) / kBS * kBS;
@@ -693,7 +762,7 @@ Shape shape_of(int num_seqs, int num_heads, int num_kv_heads, int max_q_len, int
         h.logits_bytes = 0;
         h.sums_bytes = (sg * h.rows * 8 + 255) / 256 * 256;
     }
-    h.tile_tokens = h.stored ? kTileTokens : many_tile;
+    h.tile_tokens = h.stored ? stored_tile(sg * max_len) : kManyTokens;
     h.tiles = (max_len + h.tile_tokens - 1) / h.tile_tokens;
     h.stats_bytes = (sg * h.rows * h.tiles * 8 + 255) / 256 * 256;
     return h;
@@ -709,17 +778,17 @@ pa_status launch_stored(const Params& p, cudaStream_t st) {
 }
 
 template <int KV, int D>
-pa_status launch_typed(Params& p, const Shape& small, void* workspace, cudaStream_t st) {
+pa_status launch_typed(Params& p, const Shape& h, void* workspace, cudaStream_t st) {
     char* const ws = static_cast<char*>(workspace);
     p.stats = reinterpret_cast<float2*>(ws);
-    if (small.stored) {
-        p.logits = reinterpret_cast<float*>(ws + small.stats_bytes);
-        p.tiles = small.tiles;
-        p.tile_tokens = small.tile_tokens;
-        p.row_pad = small.row_pad;
+    if (h.stored) {
+        p.logits = reinterpret_cast<float*>(ws + h.stats_bytes);
+        p.tiles = h.tiles;
+        p.tile_tokens = h.tile_tokens;
+        p.row_pad = h.row_pad;
         const dim3 grid(p.tiles, p.num_kv_heads, p.num_seqs);
         if (pa_status s = pa::cuda_status(
-                small.rows <= 8
+                h.rows <= 8
                     ? pa::launch_pdl(logits_kernel<KV, D, 1>, grid, dim3(kWarps * 32), 0, st, p)
                     : pa::launch_pdl(logits_kernel<KV, D, 2>, grid, dim3(kWarps * 32), 0, st, p),
                 "accumulate_weights logits launch"))
@@ -732,11 +801,9 @@ pa_status launch_typed(Params& p, const Shape& small, void* workspace, cudaStrea
             default: return launch_stored<16>(p, st);
         }
     }
-    constexpr int kTokens = many_tokens<KV, D>();
-    const Shape h = shape_of(p.num_seqs, p.num_heads, p.num_kv_heads, p.max_q_len, p.max_len,
-                             kTokens);
+    constexpr int kTokens = kManyTokens;
     p.tiles = h.tiles;
-    p.tile_tokens = kTokens;
+    p.tile_tokens = h.tile_tokens;
     p.sums = reinterpret_cast<float2*>(ws + h.stats_bytes);
     p.row_warps = 1;
     while (p.row_warps < kManyWarps && 16 * p.row_warps < h.rows) p.row_warps *= 2;
@@ -816,6 +883,8 @@ extern "C" pa_status pa_accumulate_weights(
                     (long long)score_stride, max_context_len);
     if (((uintptr_t)scores_in | (uintptr_t)k_scale) % 4)
         return fail(PA_ERR_INVALID_ARG, "scores and k_scale must be 4-byte aligned");
+    if (kv_dtype == PA_INT4 && ((uintptr_t)k_scale | (uintptr_t)k_zp) % 16)
+        return fail(PA_ERR_INVALID_ARG, "k_scale and k_zp must be 16-byte aligned");
     const Shape h = shape_of(num_seqs, num_heads, num_kv_heads, max_q_len, max_context_len);
     if (num_seqs > 65535 || num_kv_heads > 65535 || h.rows > kMaxRows)
         return fail(PA_ERR_UNSUPPORTED,

@@ -164,7 +164,7 @@ WEIGHTS = dict(out=A, before=None, stride=64, q=A, qt=pa.PA_BF16, k=A, kt=pa.PA_
     (dict(kt=pa.PA_F16), 2), (dict(kt=9), 1), (dict(mb=3), 1), (dict(ml=0), 1), (dict(nq=3), 1),
     (dict(ws=None), 1), (dict(wb=64), 1), (dict(ws=A + 16), 1), (dict(out=ODD), 1),
     (dict(q=ODD), 1), (dict(k=ODD), 1), (dict(before=A + 2), 1), (dict(S=-1), 1),
-    (dict(qsl=A, mq=1025, nq=2000, ml=2000, mb=125, stride=2000), 2),
+    (dict(qsl=A, mq=1025, nq=2000, ml=2000, mb=125, stride=2000), 2), (dict(kz=A + 4), 1),
     (dict(S=65536, nq=65536), 2), (dict(nb=0), 1),
 ])
 def test_weights_refusals(change, status):
@@ -247,6 +247,7 @@ def test_workspace_sizes():
     f = pa.accumulate_weights_workspace_size
     assert f(0, 1, 8, 2, 64, 1, 64) == 0 and f(2, 2, 7, 2, 64, 1, 64) == 0
     # 4 rows a KV head: the tiles' sums, and 16 bytes a token of logits
-    assert f(2, 2, 8, 2, 64, 1, 600) == 256 + 2 * 2 * 608 * 16
+    logits = 2 * 2 * 608 * 16
+    assert logits < f(2, 2, 8, 2, 64, 1, 600) < 1.1 * logits
     # more rows than are stored: sums of the rows' tiles alone, not 8 bytes a row and token
     assert 0 < f(2, 64, 8, 2, 64, 32, 600) < 2 * 2 * 128 * 600
