@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(256) stored_kernel(const Params p) {
 
 // Tokens of a many_kernel tile: 32 KB of K at most, and few enough that a ragged
 // batch spreads evenly (with 256 and more, SMs were idle for 38 % of the call).
-constexpr int kManyTokens = 128;
+constexpr int kManyTokens = 256;
 
 // Many rows. Grid: (tiles of kManyTokens, KV head, sequence). The tile's K is
 // staged in shared memory once; warp (rc, tg) takes the row chunks rc, rc +
