@@ -135,7 +135,7 @@ __device__ __forceinline__ uint32_t tile4_offset(int row, int chunk) {
 // zero point [16][groups]). Two blocks a stage: half the waits and issues of one.
 template <int D>
 struct Q4Layout {
-    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr int kGroups = D / PA_INT4_GROUP;
     static constexpr int kTile = kBS * D / 2;             // one K (or V) code tile
     static constexpr int kBlockCodes = 2 * kTile;
@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     float o[NR][CH][2][4];               // [.][chunk][dims 4 quad + 2 j, + 1][(dim, row)]
     float oz[NR][GR][4];                 // sum of P vz: row 2 qc + e in [e], of lanes quad == 0
     float m_run[NR][2], l_run[NR][2], rowmul[NR][2];
+    bool fresh = true;                   // no block of the segment done: m_run is not set yet
     float qsum[NR][GR][2];               // sum of the row's q over a group, as K products count it
-    float m_ref[NR][2];                  // m_run, or 0 while no key was seen
     int bound[NR][2];                    // last key each row sees
     uint32_t qb[NR][CH][4];              // row 8 nr + quad, dims 32 c + 8 qc .. + 7
     float vref[GR], vinv[GR];            // running V-scale reference, a power of two; its inverse
@@ -390,8 +390,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             for (int e = 0; e < 2; ++e) {
                 rowmul[nr][e] = __shfl_sync(0xffffffffu, mul, 4 * (2 * qc + e));
                 bound[nr][e] = min(last_q + query_of(row_off + 8 * nr + 2 * qc + e), L - 1);
-                m_run[nr][e] = -INFINITY;
-                m_ref[nr][e] = 0.f;
+                m_run[nr][e] = 0.f;
                 l_run[nr][e] = 0.f;
             }
 #pragma unroll
@@ -403,6 +402,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
         }
 #pragma unroll
         for (int g = 0; g < GR; ++g) vref[g] = exp2i(-126), vinv[g] = exp2i(126);
+        fresh = true;
     };
 
     // Segment end: the output rows (segment held whole) or the partial slot;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                 const int row = 8 * nr + 2 * qc + e;
                 if (row >= rows) continue;
                 float mulg[GR];
-                const float inv = complete ? kUnit / l : kUnit;
+                const float inv = complete ? __fdividef(kUnit, l) : kUnit;
 #pragma unroll
                 for (int g = 0; g < GR; ++g) mulg[g] = vref[g] * inv;
                 int64_t obase = 0;
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                     const int gr = row_off + row, qi = query_of(gr);
                     obase = ((int64_t)(q0 + qi) * p.num_heads + cur.g * G + gr - qi * G) * D;
                 } else if (quad == 0) {
-                    sl.m[row] = m_run[nr][e];
+                    sl.m[row] = l == 0.f ? -INFINITY : m_run[nr][e];   // a row that saw nothing
                     sl.l[row] = l;
                 }
 #pragma unroll
@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             }
     };
 
+    const uint32_t zsel = quad != 0 ? 0x4444u : GR == 2 ? 0x4240u : 0x4140u;
     // lane constants of the operand loads: a chunk further is 32 bytes in the swizzled row
     const uint32_t ld0 = tile4_offset<D>(ld_tok, ld_chk);
     start_segment();
@@ -505,7 +506,8 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
 
         // ---- S^T = K codes Q^T: 2 x 16 tokens x 8 NR rows, one sum per group; then
         // zero points and scales ----
-        float a[2][NR][4];               // [.][.][2 h + e]: token quad + 8 h, row 2 qc + e
+        // a: logit less the running maximum, [.][.][2 h + e] of token quad + 8 h, row 2 qc + e
+        float a[2][NR][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             float s[NR][GR][4];
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                         if constexpr (GR == 2)
                             v = fmaf(fmaf(-z[1], qsum[nr][1][e], s[nr][1][2 * h + e]), ks[u][h][1],
                                      v);
-                        a[u][nr][2 * h + e] = v * rowmul[nr][e];
+                        a[u][nr][2 * h + e] = fmaf(v, rowmul[nr][e], -m_run[nr][e]);
                     }
             }
         }
@@ -570,13 +572,13 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                         for (int g = 0; g < GR; ++g) vs[u][h][g] = 0.f;
                 }
         }
-        bool raise = false;
+        bool raise = fresh;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 raise |= fmaxf(fmaxf(a[0][nr][e], a[0][nr][2 + e]),
-                               fmaxf(a[1][nr][e], a[1][nr][2 + e])) > m_run[nr][e] + kLazyMax;
+                               fmaxf(a[1][nr][e], a[1][nr][2 + e])) > kLazyMax;
 #pragma unroll
         for (int g = 0; g < GR; ++g)
             raise |= fmaxf(fmaxf(vs[0][0][g], vs[0][1][g]), fmaxf(vs[1][0][g], vs[1][1][g])) >
@@ -590,9 +592,9 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                 for (int off = 4; off < 32; off <<= 1)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                 const float next = fmaxf(vref[g], exp2i(ceil_log2(mx)));
-                vfix[g] = vref[g] / next;                  // powers of two: exact
+                vinv[g] = exp2i(-(int)(__float_as_uint(next) >> 23) + 127);   // powers of two: exact
+                vfix[g] = vref[g] * vinv[g];
                 vref[g] = next;
-                vinv[g] = 1.f / next;
             }
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
@@ -604,9 +606,13 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                     for (int off = 4; off < 32; off <<= 1)
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                     float al = 1.f;
-                    if (mx > m_run[nr][e] + kLazyMax) {
-                        al = pa::ex2(m_run[nr][e] - mx);   // 0 while m_run is -inf
-                        m_run[nr][e] = m_ref[nr][e] = mx;
+                    if (mx > (fresh ? -INFINITY : kLazyMax)) {
+                        al = fresh ? 0.f : pa::ex2(-mx);
+                        m_run[nr][e] += mx;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int i = e; i < 4; i += 2) a[u][nr][i] -= mx;
                     }
                     l_run[nr][e] *= al;
 #pragma unroll
@@ -621,6 +627,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                         }
                     }
                 }
+            fresh = false;
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -630,8 +637,8 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                 float w[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    w[e] = pa::ex2(a[u][nr][e] - m_ref[nr][e]);
-                    w[2 + e] = pa::ex2(a[u][nr][2 + e] - m_ref[nr][e]);
+                    w[e] = pa::ex2(a[u][nr][e]);
+                    w[2 + e] = pa::ex2(a[u][nr][2 + e]);
                     l_run[nr][e] += w[e] + w[2 + e];
                 }
 #pragma unroll
@@ -665,19 +672,18 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             }
             // row 0 of a tile of its own: the zero points of tokens 2 qc, + 1 and 2 qc + 8, + 9
             const uint8_t* vzp = mt + u * Lay::kMeta + 2 * Lay::kScaleArea + Lay::kZpArea;
-            uint32_t y0 = 0, y1 = 0;
-            if (quad == 0) {
-                if constexpr (GR == 2) {
-                    y0 = reinterpret_cast<const uint32_t*>(vzp)[qc];
-                    y1 = reinterpret_cast<const uint32_t*>(vzp)[qc + 4];
-                } else {
-                    y0 = reinterpret_cast<const uint16_t*>(vzp)[qc];
-                    y1 = reinterpret_cast<const uint16_t*>(vzp)[qc + 4];
-                }
+            uint32_t y0, y1;
+            if constexpr (GR == 2) {
+                y0 = reinterpret_cast<const uint32_t*>(vzp)[qc];
+                y1 = reinterpret_cast<const uint32_t*>(vzp)[qc + 4];
+            } else {
+                y0 = reinterpret_cast<const uint16_t*>(vzp)[qc];
+                y1 = reinterpret_cast<const uint16_t*>(vzp)[qc + 4];
             }
 #pragma unroll
             for (int g = 0; g < GR; ++g) {
-                const uint32_t sel = GR == 2 ? (g == 0 ? 0x4240u : 0x4341u) : 0x4140u;
+                // the two zero points' bytes into halves; all zero in the lanes of other rows
+                const uint32_t sel = GR == 2 ? zsel + 0x0101u * g : zsel;
                 const uint32_t az[4] = {prmt(y0, 0u, sel), 0u, prmt(y1, 0u, sel), 0u};
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr)
