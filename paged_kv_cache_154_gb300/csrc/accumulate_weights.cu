@@ -612,8 +612,8 @@ __global__ void __launch_bounds__(256) stored_kernel(const Params p) {
     }
 }
 
-// Tokens of a many_kernel tile: 32 KB of K at most, and few enough that a ragged
-// batch spreads evenly (with 256 and more, SMs were idle for 38 % of the call).
+// Tokens of a many_kernel tile: enough for the starts of its warps to be worth it
+// (28.6 us for the 8 prompts below, 30.2 with 128), 64 KB of K at most.
 constexpr int kManyTokens = 256;
 
 // Many rows. Grid: (tiles of kManyTokens, KV head, sequence). The tile's K is
@@ -621,9 +621,10 @@ constexpr int kManyTokens = 256;
 // row_warps, .. of 16 rows and the tile's blocks tg, tg + token_warps, ... SUM
 // false: the rows' (m, l) over the tile; SUM true: the weights of the tile's
 // tokens, summed over the rows (each warp keeps sums of its own, which are added
-// up in a fixed order). A warp with its own K loads for every chunk of rows
-// instead took 22 + 21 us where this takes 8 + 8 (8 prompts of up to 4001 tokens,
-// 128 rows, d = 64).
+// up in a fixed order). 8 prompts of up to 4001 tokens, 128 rows, d = 64: 28.6 us
+// a call; 40 us with K loaded from global memory for every chunk of rows; 32 us
+// with ldmatrix in place of 16-byte loads, although that saves four register
+// moves a product.
 template <int KV, int D, bool SUM>
 __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
     constexpr int NR = 2, kTokens = kManyTokens, kBlocks = kTokens / kBS;
@@ -810,6 +811,11 @@ pa_status launch_typed(Params& p, const Shape& h, void* workspace, cudaStream_t 
     const int tile = kTokens * KRows<KV, D>::kRowBytes, sums = 4 * p.row_warps * kTokens;
     static bool attr_set = false;   // per instantiation; benign race (idempotent)
     if (!attr_set) {
+        if (pa_status s = pa::cuda_status(
+                cudaFuncSetAttribute(many_kernel<KV, D, false>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, tile),
+                "accumulate_weights: set shared memory size"))
+            return s;
         if (pa_status s = pa::cuda_status(
                 cudaFuncSetAttribute(many_kernel<KV, D, true>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
