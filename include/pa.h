@@ -377,7 +377,10 @@ size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
  *                  (base-2 units) and O[R][head_dim] (not normalised).
  * INT4 caches: k_scale, v_scale, k_zp and v_zp are 16-byte aligned; at most
  * 4080 query rows per KV head (num_heads / num_kv_heads x max_q_len). Codes,
- * scales and zero points of slots past a context may hold anything.
+ * scales and zero points of slots past a context may hold anything. Softmax
+ * weight times V scale is rounded to fp16 relative to the largest V scale of the
+ * (sequence, KV head, group), so tokens whose V scale is 2^14 or more below that
+ * lose bits, of the order of 2^-25 of that scale.
  * Requirements: head_dim 64 or 128, block_size 16, num_heads a multiple of
  * num_kv_heads, context_lens[s] >= (query run length of s) >= 1, at most
  * 8192 sequences per call with partition_size 0. */
@@ -497,7 +500,7 @@ pa_status pa_decode_shared_prefix(
  * pa_seq_make_private on the pool and before pa_seq_truncate. ---- */
 
 /* Bytes of workspace pa_accumulate_weights needs for these sizes (0 for invalid
- * sizes); at least 256-byte aligned, needs no initialisation, and may be shared
+ * sizes and for more than a call may have); at least 256-byte aligned, needs no initialisation, and may be shared
  * by calls of one stream. Host-only: needs no GPU. */
 size_t pa_accumulate_weights_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
                                             int32_t num_heads, int32_t num_kv_heads,
@@ -518,9 +521,9 @@ size_t pa_accumulate_weights_workspace_size(int32_t num_seqs, int32_t num_q_toke
  *                  query that sees no token add nothing (num_q_tokens is still
  *                  at least num_seqs)
  *   context_lens   lengths above max_context_len are taken as max_context_len
- * At most 4096 query rows per KV head (num_heads / num_kv_heads x max_q_len)
- * and 65535 sequences. Results do not depend on the order in which the GPU
- * runs the call. */
+ * INT4 caches: k_scale and k_zp are 16-byte aligned. At most 4096 query rows
+ * per KV head (num_heads / num_kv_heads x max_q_len), 65535 sequences and 2^30
+ * tokens. Results do not depend on the order in which the GPU runs the call. */
 pa_status pa_accumulate_weights(
     float* scores_out, const float* scores_in, int64_t score_stride, const void* q,
     pa_dtype q_dtype, const void* k_cache, pa_dtype kv_dtype, const float* k_scale,
@@ -554,7 +557,7 @@ pa_status pa_accumulate_weights(
  *                  same pointers; no other overlap): the entries of slots 0 ..
  *                  n - 1 after the moves, every position explicit; entries n .. L
  *                  - 1 become 0 and -1; entries from L on are left as they were
- * score_stride as in pa_accumulate_weights. */
+ * score_stride as in pa_accumulate_weights. At most 65535 sequences and 2^30 tokens. */
 pa_status pa_evict_select(int32_t* moves, int32_t max_moves, int32_t* move_counts,
                           float* scores_out, int32_t* positions_out, const float* scores,
                           const int32_t* positions, int64_t score_stride,
@@ -569,8 +572,8 @@ pa_status pa_evict_select(int32_t* moves, int32_t max_moves, int32_t* move_count
  * destination may appear twice or as a source; the blocks written must belong to
  * the sequence alone (pa_seq_make_private). A slot outside [0, context_lens[s])
  * is skipped with PA_DEVERR_BAD_SLOT, a block outside the pool with
- * PA_DEVERR_BAD_BLOCK. Any cache type; other arguments as in pa_copy_blocks and
- * pa_decode. */
+ * PA_DEVERR_BAD_BLOCK. Any cache type; at most 65535 sequences and 2^30 tokens;
+ * other arguments as in pa_copy_blocks and pa_decode. */
 pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype kv_dtype, float* k_scale,
                          float* v_scale, int8_t* k_zp, int8_t* v_zp,
                          const int32_t* block_tables, int32_t max_blocks_per_seq,

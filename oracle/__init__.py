@@ -10,6 +10,8 @@ Contents (each function cites the passage it restates):
                      quantiser (fp32), block copies; built with gcc.
   * allocator.py  -- block pool with refcounts and copy-on-write.
   * formulas.py   -- the KV-cache memory formula.
+  * compressed.py -- plain 64-bit forms of the 4-bit cache, of accumulated
+                     attention weights and of the eviction's choice.
   * lse_merge()   -- the split-KV log-sum-exp merge (below).
   * run()         -- executes a workload script sequentially on the host.
 

@@ -34,8 +34,9 @@ def values_int4(packed: np.ndarray, scale: np.ndarray, zp: np.ndarray) -> np.nda
     code = np.empty((*packed.shape[:-1], packed.shape[-1] * 2))
     code[..., 0::2], code[..., 1::2] = packed & 15, packed >> 4
     rep = GROUP
-    return (code - np.repeat(zp.astype(np.float64), rep, -1)) * np.repeat(
-        scale.astype(np.float64), rep, -1)
+    with np.errstate(invalid="ignore"):      # slots of no token may hold infinite scales
+        return (code - np.repeat(zp.astype(np.float64), rep, -1)) * np.repeat(
+            scale.astype(np.float64), rep, -1)
 
 
 def cache_values(cache) -> tuple:

@@ -438,6 +438,10 @@ def accumulate_weights(scores_out, scores_in, q, k_cache, block_tables, context_
     _shaped("scores_out", scores_out, shape, torch.float32)
     if scores_in is not None:
         _shaped("scores_in", scores_in, shape, torch.float32)
+    _shaped("block_tables", block_tables, (num_seqs, block_tables.shape[1]), torch.int32)
+    _shaped("context_lens", context_lens, (num_seqs,), torch.int32)
+    if query_start_loc is not None:
+        _shaped("query_start_loc", query_start_loc, (num_seqs + 1,), torch.int32)
     nb = k_cache.shape[0] if num_blocks is None else num_blocks
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().pa_accumulate_weights(
@@ -465,6 +469,10 @@ def evict_select(moves, move_counts, scores_out, positions_out, scores, position
         _shaped("positions", positions, shape, torch.int32)
     _shaped("moves", moves, (*shape[:2], moves.shape[2], 2), torch.int32)
     _shaped("move_counts", move_counts, shape[:2], torch.int32)
+    _shaped("context_lens", context_lens, shape[:1], torch.int32)
+    _shaped("new_lens", new_lens, shape[:1], torch.int32)
+    if total_lens is not None:
+        _shaped("total_lens", total_lens, shape[:1], torch.int32)
     _check(lib().pa_evict_select(
         _ptr(moves), moves.shape[2], _ptr(move_counts), _ptr(scores_out), _ptr(positions_out),
         _ptr(scores), _ptr(positions), shape[2], _ptr(context_lens), _ptr(new_lens),
@@ -481,6 +489,8 @@ def move_tokens(k_cache, v_cache, block_tables, context_lens, moves, move_counts
     shape = (num_seqs, k_cache.shape[1])
     _shaped("moves", moves, (*shape, moves.shape[2], 2), torch.int32)
     _shaped("move_counts", move_counts, shape, torch.int32)
+    _shaped("context_lens", context_lens, shape[:1], torch.int32)
+    _shaped("block_tables", block_tables, (num_seqs, block_tables.shape[1]), torch.int32)
     nb = k_cache.shape[0] if num_blocks is None else num_blocks
     _check(lib().pa_move_tokens(
         _ptr(k_cache), _ptr(v_cache), _dtype_code(k_cache), _ptr(k_scale), _ptr(v_scale),

@@ -53,6 +53,7 @@ constexpr int kOutTokens = 1024;         // tokens of a stored CTA
 constexpr int kManyWarps = 8;            // warps of a many_kernel CTA
 constexpr int kMaxRows = 4096;           // query rows per KV head
 constexpr int64_t kMaxStored = (int64_t)256 << 20;
+constexpr int64_t kMaxWorkspace = (int64_t)1 << 40;
 
 struct Params {
     float* out;
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
     sums.clear(q.bound);
     // the lane's logits: rows 8 nr + 2 qc and + 1 of token quad, those that are kept
     float* const keep = p.logits +
-                        ((int64_t)(s * p.num_kv_heads + g) * p.tokens_pad + quad) * p.row_pad + 2 * qc;
+                        (((int64_t)s * p.num_kv_heads + g) * p.tokens_pad + quad) * p.row_pad + 2 * qc;
     for (int i0 = 0; i0 < n; i0 += kDepth) {
 #pragma unroll
         for (int u = 0; u < kDepth; ++u) {
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
         float2 t = part[0][row];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) merge(t.x, t.y, part[w][row].x, part[w][row].y);
-        p.stats[((int64_t)(s * p.num_kv_heads + g) * p.row_slots + row) * p.tiles + tile] = t;
+        p.stats[(((int64_t)s * p.num_kv_heads + g) * p.row_slots + row) * p.tiles + tile] = t;
     }
 }
 
@@ -539,7 +540,7 @@ __device__ __forceinline__ float2 row_sum(const Params& p, const Seq& sq, int64_
     const float2* src = p.stats + (sg * p.row_slots + row) * p.tiles;
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i < tiles; i += 32) {
-        const float2 t = __ldg(src + i);
+        const float2 t = __ldcg(src + i);   // the kernel before may have ended under this one
         merge(m, l, t.x, t.y);
     }
 #pragma unroll
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int row = first + 8 * nr + 2 * qc + e;
-                        total[nr][e] = row < rows ? __ldg(p.sums + sg * p.row_slots + row)
+                        total[nr][e] = row < rows ? __ldcg(p.sums + sg * p.row_slots + row)
                                                   : make_float2(0.f, 0.f);
                     }
             }
@@ -748,24 +749,27 @@ struct Shape {
     int row_pad, tiles, tile_tokens, tokens_pad;
     bool stored;
     int64_t stats_bytes, sums_bytes, logits_bytes;
+    bool fits;            // false: larger than a call may be, the rest is not set
 };
 
 Shape shape_of(int num_seqs, int num_heads, int num_kv_heads, int max_q_len, int max_len) {
     Shape h{};
     h.rows = (int64_t)(num_heads / num_kv_heads) * max_q_len;
+    // bounds that keep every product below in 64 bits
+    if (num_seqs > 65535 || num_kv_heads > 65535 || h.rows > kMaxRows || max_len > pa::kMaxTokens)
+        return h;
     h.tokens_pad = (max_len + kBS - 1) / kBS * kBS;
     const int64_t sg = (int64_t)num_seqs * num_kv_heads;
     h.row_pad = 1;
     while (h.row_pad < h.rows) h.row_pad *= 2;
-    h.logits_bytes = sg * h.tokens_pad * h.row_pad * 4;
-    h.stored = h.rows <= 16 && h.logits_bytes <= kMaxStored;
-    if (!h.stored) {
-        h.logits_bytes = 0;
-        h.sums_bytes = (sg * h.rows * 8 + 255) / 256 * 256;
-    }
+    h.stored = h.rows <= 16 && sg * h.tokens_pad <= kMaxStored / (4 * h.row_pad);
+    if (h.stored) h.logits_bytes = sg * h.tokens_pad * h.row_pad * 4;
+    else h.sums_bytes = (sg * h.rows * 8 + 255) / 256 * 256;
     h.tile_tokens = h.stored ? stored_tile(sg * max_len) : kManyTokens;
     h.tiles = (max_len + h.tile_tokens - 1) / h.tile_tokens;
+    if (sg * h.rows > kMaxWorkspace / 8 / h.tiles) return h;
     h.stats_bytes = (sg * h.rows * h.tiles * 8 + 255) / 256 * 256;
+    h.fits = true;
     return h;
 }
 
@@ -809,21 +813,13 @@ pa_status launch_typed(Params& p, const Shape& h, void* workspace, cudaStream_t 
     p.row_warps = 1;
     while (p.row_warps < kManyWarps && 16 * p.row_warps < h.rows) p.row_warps *= 2;
     const int tile = kTokens * KRows<KV, D>::kRowBytes, sums = 4 * p.row_warps * kTokens;
-    static bool attr_set = false;   // per instantiation; benign race (idempotent)
-    if (!attr_set) {
-        if (pa_status s = pa::cuda_status(
-                cudaFuncSetAttribute(many_kernel<KV, D, false>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, tile),
-                "accumulate_weights: set shared memory size"))
-            return s;
-        if (pa_status s = pa::cuda_status(
-                cudaFuncSetAttribute(many_kernel<KV, D, true>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     tile + 4 * kManyWarps * kTokens),
-                "accumulate_weights: set shared memory size"))
-            return s;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> allowed[2]{};
+    if (pa_status s = pa::allow_smem(many_kernel<KV, D, false>, tile, allowed[0],
+                                     "accumulate_weights: set shared memory size"))
+        return s;
+    if (pa_status s = pa::allow_smem(many_kernel<KV, D, true>, tile + 4 * kManyWarps * kTokens,
+                                     allowed[1], "accumulate_weights: set shared memory size"))
+        return s;
     const dim3 grid(p.tiles, p.num_kv_heads, p.num_seqs), block(32 * kManyWarps);
     if (pa_status s = pa::cuda_status(
             pa::launch_pdl(many_kernel<KV, D, false>, grid, block, (size_t)tile, st, p),
@@ -862,7 +858,7 @@ extern "C" size_t pa_accumulate_weights_workspace_size(int32_t num_seqs, int32_t
         head_dim <= 0 || max_q_len <= 0 || max_context_len <= 0 || num_heads % num_kv_heads != 0)
         return 0;
     const Shape h = shape_of(num_seqs, num_heads, num_kv_heads, max_q_len, max_context_len);
-    return (size_t)(h.stats_bytes + h.sums_bytes + h.logits_bytes);
+    return h.fits ? (size_t)(h.stats_bytes + h.sums_bytes + h.logits_bytes) : 0;
 }
 
 extern "C" pa_status pa_accumulate_weights(
@@ -892,11 +888,12 @@ extern "C" pa_status pa_accumulate_weights(
     if (kv_dtype == PA_INT4 && ((uintptr_t)k_scale | (uintptr_t)k_zp) % 16)
         return fail(PA_ERR_INVALID_ARG, "k_scale and k_zp must be 16-byte aligned");
     const Shape h = shape_of(num_seqs, num_heads, num_kv_heads, max_q_len, max_context_len);
-    if (num_seqs > 65535 || num_kv_heads > 65535 || h.rows > kMaxRows)
+    if (!h.fits)
         return fail(PA_ERR_UNSUPPORTED,
                     "accumulate_weights call too large (%d sequences, %d KV heads, %lld query rows "
-                    "per KV head; at most 65535, 65535 and %d)",
-                    num_seqs, num_kv_heads, (long long)h.rows, kMaxRows);
+                    "per KV head, %d tokens; at most 65535, 65535, %d and %d)",
+                    num_seqs, num_kv_heads, (long long)h.rows, max_context_len, kMaxRows,
+                    pa::kMaxTokens);
     const size_t need = (size_t)(h.stats_bytes + h.sums_bytes + h.logits_bytes);
     if (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256)
         return fail(PA_ERR_INVALID_ARG, "workspace needs %zu bytes, 256-byte aligned (got %zu)",

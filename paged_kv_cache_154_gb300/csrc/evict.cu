@@ -482,12 +482,14 @@ template <int VECS, int GROUPS>   // 16-byte vectors and scales of a row
 __global__ void __launch_bounds__(32 * kMoveWarps) move_tokens_kernel(const MoveParams p) {
     constexpr int kPieces = 2 * VECS, kMoves = 32 / kPieces;   // moves of one warp-wide copy
     static_assert(kPieces <= 32, "a move fits a warp");
-    pa::grid_dependents_launch();
+    // Kernels that read the cache may do so by loads that are not ordered after this one
+    // until it has ended, so they are not let in early; nor is the list, which the kernel
+    // before may have finished under this one, read that way.
     pa::grid_dependency_wait();
     const int s = blockIdx.z, g = blockIdx.y, lane = threadIdx.x & 31;
     const int64_t sg = (int64_t)s * p.num_kv_heads + g;
     const int L = max(0, min(__ldg(p.context_lens + s), p.max_len));
-    const int count = min(__ldg(p.move_counts + sg), p.max_moves);
+    const int count = min(__ldcg(p.move_counts + sg), p.max_moves);
     const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
     const int warps = gridDim.x * kMoveWarps;
     // moves of a warp's turn: at most one a lane, and as many turns for every warp
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_tokens_kernel(const Move
         const int here = (int)min((int64_t)per, count - m0);
         int bs = -1, bd = -1, at = 0;    // blocks, and the offsets in them: source | destination << 4
         if (lane < here) {
-            const int2 mv = __ldg(p.moves + sg * p.max_moves + m0 + lane);
+            const int2 mv = __ldcg(p.moves + sg * p.max_moves + m0 + lane);
             if (mv.x < 0 || mv.x >= L || mv.y < 0 || mv.y >= L) {
                 if (p.err) atomicOr(p.err, pa::ERR_BAD_SLOT);
             } else {
@@ -562,15 +564,10 @@ pa_status launch_move(const MoveParams& p, int num_seqs, cudaStream_t st) {
 template <int CL, int T, bool KEYS>
 pa_status launch_select_as(const SelectParams& p, int num_seqs, int keys, cudaStream_t st) {
     auto kern = evict_select_kernel<CL, T, KEYS>;
-    static bool attr_set = false;   // per instantiation; benign race (idempotent)
-    if (!attr_set) {
-        if (pa_status s = pa::cuda_status(
-                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kHistBytes + 4 * kMaxKeys),
-                "evict_select: set shared memory size"))
-            return s;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> allowed{0};
+    if (pa_status s = pa::allow_smem(kern, kHistBytes + 4 * kMaxKeys, allowed,
+                                     "evict_select: set shared memory size"))
+        return s;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CL, p.num_kv_heads, num_seqs);
     cfg.blockDim = dim3(T);
@@ -642,8 +639,10 @@ extern "C" pa_status pa_evict_select(int32_t* moves, int32_t max_moves, int32_t*
                     std::max(1, max_context_len / 2));
     if (num_sinks < 0 || num_recent < 0)
         return fail(PA_ERR_INVALID_ARG, "num_sinks %d, num_recent %d", num_sinks, num_recent);
-    if (num_seqs > 65535 || num_kv_heads > 65535)
-        return fail(PA_ERR_UNSUPPORTED, "more than 65535 sequences or KV heads in one call");
+    if (num_seqs > 65535 || num_kv_heads > 65535 || max_context_len > pa::kMaxTokens)
+        return fail(PA_ERR_UNSUPPORTED,
+                    "more than 65535 sequences or KV heads, or %d tokens, in one call",
+                    pa::kMaxTokens);
     if ((uintptr_t)moves % 8)
         return fail(PA_ERR_INVALID_ARG, "moves must be 8-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
@@ -690,8 +689,10 @@ extern "C" pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype kv_dt
     if (max_context_len <= 0 || (int64_t)max_blocks_per_seq * block_size < max_context_len)
         return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq %d, max_context_len %d",
                     max_blocks_per_seq, max_context_len);
-    if (num_seqs > 65535 || num_kv_heads > 65535)
-        return fail(PA_ERR_UNSUPPORTED, "more than 65535 sequences or KV heads in one call");
+    if (num_seqs > 65535 || num_kv_heads > 65535 || max_context_len > pa::kMaxTokens)
+        return fail(PA_ERR_UNSUPPORTED,
+                    "more than 65535 sequences or KV heads, or %d tokens, in one call",
+                    pa::kMaxTokens);
     if ((uintptr_t)moves % 8) return fail(PA_ERR_INVALID_ARG, "moves must be 8-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
     if (pa::validate_enabled())

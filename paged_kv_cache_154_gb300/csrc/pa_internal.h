@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pa.h"
 
 namespace pa {
@@ -69,6 +71,24 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+constexpr int kMaxTokens = 1 << 30;   // of a sequence, where slots are counted in 32 bits
+
+// Raises a kernel's limit of dynamic shared memory to `bytes`, once per kernel
+// and device: `done` is the kernel's own, a bit a device (devices past 63 every
+// time).
+template <typename Kernel>
+pa_status allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& done, const char* what) {
+    int dev = 0;
+    if (pa_status s = cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return s;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return PA_OK;
+    if (pa_status s = cuda_status(
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), what))
+        return s;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return PA_OK;
 }
 
 struct AppendArgs {

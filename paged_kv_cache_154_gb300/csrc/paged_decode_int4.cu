@@ -844,15 +844,10 @@ template <typename TQ, int D, int NR>
 pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, Q4Extra x) {
     using Lay = Q4Layout<D>;
     auto kern = paged_decode_int4_kernel<TQ, D, NR>;
-    static bool attr_set = false;   // per instantiation; benign race (idempotent)
-    if (!attr_set) {
-        if (pa_status s = pa::cuda_status(
-                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     Lay::smem_bytes(pa::kBalancedMaxSeqs)),
-                "int4 decode: set shared memory size"))
-            return s;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> allowed{0};
+    if (pa_status s = pa::allow_smem(kern, Lay::smem_bytes(pa::kBalancedMaxSeqs), allowed,
+                                     "int4 decode: set shared memory size"))
+        return s;
     const int smem = Lay::smem_bytes(a.num_seqs);
     // the answers of the last call's queries, which cost as much as a launch
     thread_local int last_dev = -1, last_smem = -1, sms = 0, ctas = 0;
@@ -925,6 +920,15 @@ namespace pa {
 pa_status launch_decode_int4(const DecodeArgs& a) {
     if (a.partition_size != 0)
         return fail(PA_ERR_UNSUPPORTED, "INT4 caches use the balanced schedule (partition_size 0)");
+    // tile numbers have 31 bits; row chunks round the rows of the merge's grid up to twice
+    // as many
+    const int64_t segments = (int64_t)a.num_seqs * a.num_kv_heads;
+    if ((int64_t)a.num_blocks * a.num_kv_heads > INT32_MAX ||
+        segments * (a.num_heads / a.num_kv_heads) * a.max_q_len > 1 << 30)
+        return fail(PA_ERR_UNSUPPORTED,
+                    "int4 decode call too large (%d blocks x %d KV heads, %d sequences x %d heads x "
+                    "%d queries; at most 2^31 - 1 and 2^30)",
+                    a.num_blocks, a.num_kv_heads, a.num_seqs, a.num_heads, a.max_q_len);
     if (pa_status s = balanced_check(a)) return s;
     if (((uintptr_t)a.k_scale | (uintptr_t)a.v_scale | (uintptr_t)a.k_zp | (uintptr_t)a.v_zp) % 16)
         return fail(PA_ERR_INVALID_ARG, "scales and zero points must be 16-byte aligned");

@@ -248,10 +248,14 @@ class PagedKVCache:
         per KV head, their rows moved, and the freed blocks given back. Where the
         pool cannot cover the copies it raises, and no token has gone."""
         ids = [names[s] for s in tw.seqs]
+        if len(set(ids)) != len(ids):
+            raise ValueError("a sequence appears twice")
         lens = np.array([self.pool.seq_len(i) for i in ids], np.int64)
         kept = np.minimum(np.broadcast_to(np.asarray(keep, np.int64), lens.shape), lens)
         if (kept < 0).any():
             raise ValueError("keep is negative")
+        if lens.size and lens.max() > tw.scores.shape[2]:
+            raise ValueError(f"a sequence holds {lens.max()} tokens, its weights {tw.scores.shape[2]}")
         if not (kept < lens).any():
             return
         for i, n, L in zip(ids, kept, lens):

@@ -166,6 +166,9 @@ WEIGHTS = dict(out=A, before=None, stride=64, q=A, qt=pa.PA_BF16, k=A, kt=pa.PA_
     (dict(q=ODD), 1), (dict(k=ODD), 1), (dict(before=A + 2), 1), (dict(S=-1), 1),
     (dict(qsl=A, mq=1025, nq=2000, ml=2000, mb=125, stride=2000), 2), (dict(kz=A + 4), 1),
     (dict(S=65536, nq=65536), 2), (dict(nb=0), 1),
+    (dict(ml=(1 << 30) + 1, mb=1 << 27, stride=1 << 31), 2),
+    (dict(qsl=A, S=65535, nq=65535, H=32768, Hkv=32768, mq=64, ml=1 << 30, mb=1 << 27,
+          stride=1 << 31), 2),
 ])
 def test_weights_refusals(change, status):
     assert refused("pa_accumulate_weights", WEIGHTS, **change) == status
@@ -181,7 +184,7 @@ SELECT = dict(moves=A, mm=32, counts=A, wo=A, po=A, w=A, pos=A, stride=64, cl=A,
     (dict(w=None), 1), (dict(cl=None), 1), (dict(nl=None), 1), (dict(mm=31), 1),
     (dict(mm=0, ml=1), 1), (dict(stride=63), 1), (dict(ml=0), 1), (dict(sinks=-1), 1),
     (dict(recent=-1), 1), (dict(Hkv=0), 1), (dict(moves=A + 4), 1), (dict(S=65536), 2),
-    (dict(S=-1), 1),
+    (dict(S=-1), 1), (dict(ml=(1 << 30) + 1, mm=1 << 30, stride=1 << 31), 2),
 ])
 def test_select_refusals(change, status):
     assert refused("pa_evict_select", SELECT, **change) == status
@@ -197,7 +200,7 @@ MOVE = dict(k=A, v=A, kt=pa.PA_INT4, ks=A, vs=A, kz=A, vz=A, bt=A, mb=4, cl=A, m
     (dict(kt=pa.PA_FP8_E4M3, ks=None), 1), (dict(kt=pa.PA_F32), 1), (dict(d=32), 2),
     (dict(bs=8), 2), (dict(nb=0), 1), (dict(mb=3), 1), (dict(ml=0), 1), (dict(mm=0), 1),
     (dict(k=ODD), 1), (dict(v=ODD), 1), (dict(ks=A + 2), 1), (dict(moves=A + 4), 1),
-    (dict(S=65536), 2), (dict(S=-1), 1),
+    (dict(S=65536), 2), (dict(S=-1), 1), (dict(ml=(1 << 30) + 1, mb=1 << 27), 2),
 ])
 def test_move_refusals(change, status):
     assert refused("pa_move_tokens", MOVE, **change) == status
@@ -233,6 +236,9 @@ def test_int4_refusals_of_the_calls_that_were_there():
     assert refused("pa_decode", dec, kz=None) == 1
     assert refused("pa_decode", dec, vs=A + 4) == 1
     assert refused("pa_decode", dec, P=32, wb=1 << 30) == 2
+    assert refused("pa_decode", dec, nb=1 << 30) == 2            # 2^31 tiles
+    assert refused("pa_decode", dec, qsl=A, H=4096, Hkv=4096, S=8192, nq=1 << 20, mq=64,
+                   ml=64, wb=1 << 40) == 2                       # 2^31 rows of queries
 
 
 def test_empty_calls_are_accepted():
@@ -246,6 +252,10 @@ def test_empty_calls_are_accepted():
 def test_workspace_sizes():
     f = pa.accumulate_weights_workspace_size
     assert f(0, 1, 8, 2, 64, 1, 64) == 0 and f(2, 2, 7, 2, 64, 1, 64) == 0
+    # larger than a call may be, whatever the products of the sizes come to
+    assert f(1, 1, 1 << 20, 1, 64, 1 << 20, 16) == 0 and f(1, 1, 8, 8, 64, 4097, 4097) == 0
+    assert f(65535, 65535, 65535, 65535, 64, 16, 1 << 30) == 0
+    assert f(1 << 30, 1 << 30, 8, 8, 64, 1, 64) == 0
     # 4 rows a KV head: the tiles' sums, and 16 bytes a token of logits
     logits = 2 * 2 * 608 * 16
     assert logits < f(2, 2, 8, 2, 64, 1, 600) < 1.1 * logits
