@@ -164,13 +164,23 @@ struct Shares {
     __device__ __forceinline__ uint32_t start(uint32_t w) const {
         return w * each + w * rest / W;
     }
-    // the share that holds block f: an estimate in floating point, then exact steps
-    __device__ __forceinline__ uint32_t of(uint32_t f) const {
-        uint32_t w = min(W - 1, (uint32_t)(((float)f + 0.5f) * (float)W / (float)B));
-        while (start(w) > f) --w;
-        while (start(w + 1) <= f) ++w;
-        return w;
-    }
+};
+
+// The share that holds block f: the largest w with w B / W <= f, which is w B < (f + 1) W;
+// an estimate in floating point, then exact steps.
+__device__ __forceinline__ uint32_t share_with(uint32_t f, uint32_t B, uint32_t W) {
+    const uint64_t end = ((uint64_t)f + 1) * W;
+    uint32_t w = min(W - 1, (uint32_t)__fdividef(((float)f + 0.5f) * (float)W, (float)B));
+    while ((uint64_t)w * B >= end) --w;
+    while ((uint64_t)(w + 1) * B < end) ++w;
+    return w;
+}
+
+struct __align__(32) MergeRecord {
+    int np;                 // pieces, in shares wid, wid + 1, ..; 0: nothing to merge
+    int wid, first_slot;    // the first piece's worker and slot
+    int q0, g, row0, rows;  // first query token, KV head, first query row and rows of the chunk
+    int pad;
 };
 
 struct Q4Extra {
@@ -182,6 +192,10 @@ struct Q4Extra {
     const int8_t* v_zp;
     int whole;              // a worker takes a whole segment instead of a share
     int max_chunks;
+    // What the merge has to know of a cut segment, left by the worker of its first piece:
+    // one per segment where there are no more segments than workers, else one per worker.
+    MergeRecord* records;   // null with `whole`
+    int by_segment;
 };
 
 // NR: tiles of 8 query rows (1: at most 8 rows per KV head; 2: chunks of 16)
@@ -211,6 +225,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     build_prefix(cum, chunks, p);
     const int64_t wid = (int64_t)blockIdx.x * kWorkerWarps + warp;
     if (wid >= p.workers) return;     // the grid's last CTA may have spare warps
+    if (x.records && !x.by_segment && lane == 0) x.records[wid].np = 0;
     int64_t f0, f1;
     if (x.whole) {                    // worker (s, g, c): its segment's blocks
         const int c = (uint32_t)wid % x.max_chunks, sg = (uint32_t)wid / x.max_chunks;
@@ -323,7 +338,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     // Segment start: this warp's q rows as fp16 B fragments, each row scaled
     // by 2^(14 - e_row), its dims paired as the nibbles of a K word are and the
     // odd ones, whose codes count 2^-20, by 2^-4 more.
-    auto start_segment = [&]() {
+    auto start_segment = [&](int left) {   // left: blocks of the share that are not done
         L = __ldg(p.context_lens + cur.s);
         r = query_run(p.qsl, cur.s, &q0);
         last_q = L - r;
@@ -403,6 +418,21 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
 #pragma unroll
         for (int g = 0; g < GR; ++g) vref[g] = exp2i(-126), vinv[g] = exp2i(126);
         fresh = true;
+        // the segment's merge record, by the worker that holds its first block
+        if (lane == 0 && x.records && seg_b0 == 0 && cur.c < x.max_chunks) {
+            const bool cut = cur.nbs > left;
+            const int seg = (cur.s * hkv + cur.g) * x.max_chunks + cur.c;
+            MergeRecord* const m = x.records + (x.by_segment ? seg : wid);
+            if (cut) {                   // pieces up to the share of the segment's last block
+                const uint32_t B = (uint32_t)cum[n_seqs], W = (uint32_t)share_count(p, B);
+                const uint32_t wb = share_with((uint32_t)f1 + cur.nbs - left - 1, B, W);
+                reinterpret_cast<int4*>(m)[0] =
+                    make_int4((int)(wb - wid) + 1, (int)wid, seg_first ? 0 : 1, q0);
+                reinterpret_cast<int4*>(m)[1] = make_int4(cur.g, row_off, rows, 0);
+            } else if (x.by_segment) {
+                m->np = 0;
+            }
+        }
     };
 
     // Segment end: the output rows (segment held whole) or the partial slot;
@@ -472,7 +502,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     const uint32_t zsel = quad != 0 ? 0x4444u : GR == 2 ? 0x4240u : 0x4140u;
     // lane constants of the operand loads: a chunk further is 32 bytes in the swizzled row
     const uint32_t ld0 = tile4_offset<D>(ld_tok, ld_chk);
-    start_segment();
+    start_segment(n);
     int st = 0, half = 0;                // half: the stage's first block not yet done
     for (int k = 0; k < n;) {
         if (half == 0) {                 // S groups are on their way: the oldest is here
@@ -706,61 +736,48 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             next_segment(p, cur, cum, chunks);
             seg_b0 = 0;
             seg_first = false;
-            start_segment();
+            start_segment(n - k);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Merges the pieces of the segments that share boundaries cut (log-sum-exp rule):
-// an item is a (sequence, KV head, row chunk, query row), served by `wpr` of a
-// CTA's warps, which take its pieces in turn and meet in shared memory. A warp
-// asks for its first eight pieces' columns beside all of the row's (m, l), from
-// which it gets the weights and the denominator. Few long sequences are cut into
-// a hundred pieces each: one warp a row waited for its loads 14 times over (14 us
-// behind the long-context step), eight do twice. Merging in the decode kernel, by
-// the last piece to finish, was slower (55.5 us against 48.8 for the Llama-3-8B
-// step): equal shares end together, so nothing hides it, and a warp that folds
-// all of a segment's rows waits longer than a grid of warps that fold one each.
+// Merges the pieces of the segments that share boundaries cut (log-sum-exp rule).
+// Grid: (query rows, merge records); a row is served by `wpr` of a CTA's warps,
+// which take its pieces in turn and meet in shared memory. A warp asks for its
+// first eight pieces' columns beside all of the row's (m, l), from which it gets
+// the weights and the denominator. Bound by the latency of record, pieces and
+// output in turn: the record saves every warp the arithmetic that finds a
+// segment's shares (2.5, 5.1 and 1.9 us of the Llama-3-8B, verify and long-context
+// steps, behind a launch of 1 us). Few long sequences are cut into a hundred pieces
+// each: one warp a row waited for its loads 14 times over (14 us behind the
+// long-context step), eight do twice. Merging in the decode kernel, by the last
+// piece to finish, was slower (55.5 us against 48.8 for the Llama-3-8B step): equal
+// shares end together, so nothing hides it, and a warp that folds all of a
+// segment's rows waits longer than a grid of warps that fold one each.
 constexpr int kMergeWarps = 8;
 template <typename TQ, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::sched::Params p,
-                                                                      int max_chunks,
-                                                                      int row_slots, int wpr) {
+                                                                      const Q4Extra x, int wpr) {
     using namespace pa::sched;
     constexpr int EPL = D / 32, kUnroll = 8;
     __shared__ __align__(16) float part[kMergeWarps][D];
     pa::grid_dependents_launch();
     pa::grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp & (wpr - 1);
-    uint32_t item = blockIdx.x * (kMergeWarps / wpr) + warp / wpr;
-    const int row = item % row_slots;
-    item /= row_slots;
-    const int c = item % max_chunks;
-    item /= max_chunks;
-    const int g = item % p.num_kv_heads, s = item / p.num_kv_heads;
-    const int RT = p.rows_per_tile, G = p.group;
-    int q0 = 0, np = 0, first_slot = 0;
-    uint32_t wa = 0;
-    if (s < p.num_seqs) {                // warp-uniform
-        const int base = __ldcg(p.cum_out + s), next = __ldcg(p.cum_out + s + 1);
-        const int64_t B = __ldcg(p.cum_out + p.num_seqs);
-        const int r = query_run(p.qsl, s, &q0);
-        const int rows = min(RT, G * r - c * RT);
-        uint32_t fa = base + g * ((next - base) / p.num_kv_heads), nb = (next - base) / p.num_kv_heads;
-        if (G * r > RT) {                // several chunks: blocks of the ones before this
-            const int L = __ldg(p.context_lens + s);
-            for (int i = 0; i < c; ++i) fa += chunk_blocks(p, L, r, 0, i);
-            nb = rows > 0 ? chunk_blocks(p, L, r, 0, c) : 0;
-        }
-        if (row < rows && nb > 0) {
-            const Shares shares(B, share_count(p, B));
-            wa = shares.of(fa);
-            const uint32_t wb = shares.of(fa + nb - 1);
-            first_slot = shares.start(wa) < fa ? 1 : 0;
-            np = wb > wa ? (int)(wb - wa) + 1 : 0;   // one share: already written
-        }
+    const int row = (blockIdx.x * (blockDim.x >> 5) + warp) / wpr;
+    const int G = p.group, RT = p.rows_per_tile;
+    const int4* const rec = reinterpret_cast<const int4*>(x.records + blockIdx.y);
+    const int4 r0 = __ldcg(rec), r1 = __ldcg(rec + 1);
+    bool live = true;
+    if (x.by_segment) {                  // a segment without blocks leaves its record unset
+        const int c = blockIdx.y % x.max_chunks, s = blockIdx.y / x.max_chunks / p.num_kv_heads;
+        int q0;
+        const int r = query_run(p.qsl, s, &q0), L = __ldg(p.context_lens + s);
+        live = c * RT < G * r && chunk_blocks(p, L, r, 0, c) > 0;
     }
+    const int np = live && row < r1.z ? r0.x : 0, wa = r0.y, first_slot = r0.z;
+    if (wpr == 1 && np == 0) return;
     auto piece = [&](int i) {
         return Slot(p.slots + (2 * ((int64_t)wa + i) + (i == 0 ? first_slot : 0)) * p.slot_bytes, RT);
     };
@@ -824,8 +841,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::
             for (int e = 0; e < EPL; ++e) acc[e] += part[warp + i][lane * EPL + e];
     }
     if (np == 0) return;
-    const int gr = c * RT + row;
-    const int64_t out = ((int64_t)(q0 + gr / G) * p.num_heads + g * G + gr % G) * D + lane * EPL;
+    const int gr = r1.y + row;
+    const int64_t out = ((int64_t)(r0.w + gr / G) * p.num_heads + r1.x * G + gr % G) * D + lane * EPL;
     const float inv = 1.f / den;
     if (p.out_f32) {
         float* dst = static_cast<float*>(p.out) + out;
@@ -874,7 +891,6 @@ pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, Q4Extra x)
     // more rows, holds those of 16 warps on every SM.
     prm.rows_per_tile = 8 * NR;
     prm.slot_bytes = (int)pa::sched::slot_bytes(8 * NR, D);
-    const int64_t room = (shape.workspace_bytes - shape.cum_bytes) / (2 * prm.slot_bytes);
     const int64_t rows = (int64_t)prm.group * a.max_q_len;
     const int chunks = (int)((rows + 8 * NR - 1) / (8 * NR));
     const int64_t segments = (int64_t)a.num_seqs * a.num_kv_heads * chunks;
@@ -882,9 +898,16 @@ pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, Q4Extra x)
     // merge's launch takes.
     x.whole = a.max_context_len <= kWholeTokens;
     x.max_chunks = chunks;
-    const int64_t workers =
-        x.whole ? segments
-                : std::min({(int64_t)ctas * sms * kWorkerWarps, shape.virtual_blocks, room});
+    int64_t workers = segments;
+    if (!x.whole) {
+        workers = std::min((int64_t)ctas * sms * kWorkerWarps, shape.virtual_blocks);
+        const int64_t record_bytes = (std::min(segments, workers) * (int64_t)sizeof(MergeRecord) + 255) / 256 * 256;
+        x.records = reinterpret_cast<MergeRecord*>(prm.slots);
+        prm.slots += record_bytes;
+        const int64_t room = shape.workspace_bytes - shape.cum_bytes - record_bytes;
+        workers = std::min(workers, room / (2 * prm.slot_bytes));
+        x.by_segment = segments <= workers;
+    }
     prm.workers = (int)workers;
     const int grid = (int)((workers + kWorkerWarps - 1) / kWorkerWarps);
     if (pa_status s = pa::cuda_status(
@@ -896,10 +919,11 @@ pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, Q4Extra x)
     const int row_slots = (int)std::min<int64_t>(8 * NR, rows);
     int wpr = 1;
     while (wpr < kMergeWarps && workers > 8 * wpr * segments) wpr *= 2;
-    const int64_t items = segments * row_slots, per = kMergeWarps / wpr;
+    const int per = std::min(row_slots, kMergeWarps / wpr);   // rows of a CTA
     return pa::cuda_status(
-        pa::launch_pdl(int4_merge_kernel<TQ, D>, dim3((unsigned)((items + per - 1) / per)),
-                       dim3(32 * kMergeWarps), 0, a.stream, prm, chunks, row_slots, wpr),
+        pa::launch_pdl(int4_merge_kernel<TQ, D>,
+                       dim3((row_slots + per - 1) / per, (unsigned)std::min(segments, workers)),
+                       dim3(32 * per * wpr), 0, a.stream, prm, x, wpr),
         "int4 merge launch");
 }
 
@@ -941,7 +965,6 @@ pa_status launch_decode_int4(const DecodeArgs& a) {
     b.block_tables = a.block_tables;
     b.context_lens = a.context_lens;
     b.qsl = a.query_start_loc;
-    b.cum_out = static_cast<int32_t*>(a.slots);
     b.slots = static_cast<uint8_t*>(a.slots) + shape.cum_bytes;
     b.err = device_error_word();
     b.max_blocks = a.max_blocks_per_seq;
@@ -956,7 +979,7 @@ pa_status launch_decode_int4(const DecodeArgs& a) {
     b.out_f32 = a.out_dtype == PA_F32;
     const Q4Extra x{static_cast<const uint8_t*>(a.k_cache),
                     static_cast<const uint8_t*>(a.v_cache), a.k_scale, a.v_scale, a.k_zp, a.v_zp,
-                    0, 1};
+                    0, 1, nullptr, 0};
     return a.q_dtype == PA_BF16 ? dispatch<__nv_bfloat16>(a, b, x)
                                 : dispatch<__half>(a, b, x);
 }
