@@ -50,11 +50,16 @@
 namespace {
 
 using pa::sched::kBS;
-using pa::sched::kWorkerWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyMax = 8.f;    // base-2 headroom before the running max is moved
 constexpr int kWholeTokens = 256;
-constexpr int ctas_per_sm(int d, int nr) { return d == 128 && nr == 2 ? 2 : 3; }
+// Warps of a CTA and CTAs of an SM, as many as the registers allow. One CTA of 12
+// warps: its warps run at one pace, where of three CTAs of 4 the older ones ran ahead
+// (a loop of 85, 98 and 113 thousand cycles for the same number of blocks) and left the
+// SM to the last (68.3 us against 70.5 for the long-context step). Two CTAs with 16 query
+// rows, where it made no such difference (55.0 us for the verify step, 55.8 in one).
+constexpr int ctas_per_sm(int d, int nr) { return d == 128 && nr == 2 ? 2 : 1; }
+constexpr int worker_warps(int d, int nr) { return d == 128 && nr == 2 ? 4 : 12; }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -149,22 +154,17 @@ struct Q4Layout {
     __host__ __device__ static int header(int num_seqs) {   // cum, then chunks
         return ((num_seqs + 1) * 4 + num_seqs + 127) / 128 * 128;
     }
-    __host__ __device__ static int smem_bytes(int num_seqs) {
-        return header(num_seqs) + kWorkerWarps * kWarp;
+    __host__ __device__ static int smem_bytes(int num_seqs, int warps) {
+        return header(num_seqs) + warps * kWarp;
     }
 };
 
 // share_start() in 32-bit arithmetic (B < 2^31, w <= W < 2^16): w B / W =
 // w (B / W) + w (B mod W) / W; the 64-bit divisions are a quarter of a share's
 // fixed cost.
-struct Shares {
-    uint32_t B, each, rest, W;
-    __device__ __forceinline__ Shares(int64_t B_, int64_t W_)
-        : B((uint32_t)B_), each(B / (uint32_t)W_), rest(B % (uint32_t)W_), W((uint32_t)W_) {}
-    __device__ __forceinline__ uint32_t start(uint32_t w) const {
-        return w * each + w * rest / W;
-    }
-};
+__device__ __forceinline__ uint32_t share_begin(uint32_t w, uint32_t B, uint32_t W) {
+    return w * (B / W) + w * (B % W) / W;
+}
 
 // The share that holds block f: the largest w with w B / W <= f, which is w B < (f + 1) W;
 // an estimate in floating point, then exact steps.
@@ -174,6 +174,51 @@ __device__ __forceinline__ uint32_t share_with(uint32_t f, uint32_t B, uint32_t 
     while ((uint64_t)w * B >= end) --w;
     while ((uint64_t)(w + 1) * B < end) ++w;
     return w;
+}
+
+// build_prefix() for tiles of RT rows: cum[s] = num_kv_heads * (blocks of all row chunks
+// of the sequences before s), chunks[s] = row chunks of s.
+template <int RT, int WARPS>
+__device__ __forceinline__ void prefix_sums(int32_t* cum, uint8_t* chunks,
+                                            const pa::sched::Params& p) {
+    using namespace pa::sched;
+    __shared__ int32_t totals[WARPS];
+    pa::grid_dependents_launch();   // the merge may be scheduled early
+    pa::grid_dependency_wait();     // inputs written by the previous kernel are visible
+    const int n = p.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (n + 32 * WARPS - 1) / (32 * WARPS);
+    const int a = min(n, tid * per), b = min(n, a + per);
+    int32_t own = 0;
+    for (int i = a; i < b; ++i) {
+        int q0;
+        const int L = __ldg(p.context_lens + i), r = query_run(p.qsl, i, &q0);
+        const int C = (p.group * r + RT - 1) / RT;
+        int blocks = max(0, L + kBS - 1) / kBS;   // what one chunk sees: the run's last row sees all
+        if (C != 1) {
+            blocks = 0;
+            for (int c = 0; c < C; ++c) blocks += chunk_blocks(p, L, r, 0, c);
+        }
+        chunks[i] = (uint8_t)C;
+        cum[i] = p.num_kv_heads * blocks;
+        own += p.num_kv_heads * blocks;
+    }
+    int32_t x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) totals[warp] = x;
+    __syncthreads();
+    const int32_t t = lane < WARPS ? totals[lane] : 0;
+    int32_t run = x - own + __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
+    for (int i = a; i < b; ++i) {
+        const int32_t v = cum[i];
+        cum[i] = run;
+        run += v;
+    }
+    if (tid == 32 * WARPS - 1) cum[n] = run;
+    __syncthreads();
 }
 
 struct __align__(32) MergeRecord {
@@ -200,7 +245,7 @@ struct Q4Extra {
 
 // NR: tiles of 8 query rows (1: at most 8 rows per KV head; 2: chunks of 16)
 template <typename TQ, int D, int NR>
-__global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
+__global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
     paged_decode_int4_kernel(const pa::sched::Params p, const Q4Extra x) {
     using namespace pa::sched;
     using Lay = Q4Layout<D>;
@@ -222,8 +267,8 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     const uint32_t ring = pa::smem_addr(mine);
     const uint8_t* const meta = mine + Lay::kMetaAt;
 
-    build_prefix(cum, chunks, p);
-    const int64_t wid = (int64_t)blockIdx.x * kWorkerWarps + warp;
+    prefix_sums<kRows, worker_warps(D, NR)>(cum, chunks, p);
+    const int64_t wid = (int64_t)blockIdx.x * worker_warps(D, NR) + warp;
     if (wid >= p.workers) return;     // the grid's last CTA may have spare warps
     if (x.records && !x.by_segment && lane == 0) x.records[wid].np = 0;
     int64_t f0, f1;
@@ -240,8 +285,8 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     } else {
         const int64_t B = cum[n_seqs], W = share_count(p, B);
         if (wid >= W) return;
-        const Shares shares(B, W);
-        f0 = shares.start((uint32_t)wid), f1 = shares.start((uint32_t)wid + 1);
+        f0 = share_begin((uint32_t)wid, (uint32_t)B, (uint32_t)W);
+        f1 = share_begin((uint32_t)wid + 1, (uint32_t)B, (uint32_t)W);
     }
     const int n = (int)(f1 - f0);
     if (n <= 0) return;
@@ -256,8 +301,9 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
         win = wbase;
         const int64_t f = f0 + wbase + lane;
         my_tile = 0;
+        Pos q{};
         if (f < f1) {
-            const Pos q = locate(p, cum, chunks, f);
+            q = locate(p, cum, chunks, f);
             int blk = __ldg(p.block_tables + (int64_t)q.s * p.max_blocks + q.b);
             if (blk < 0 || blk >= p.num_blocks) {
                 if (p.err) atomicOr(p.err, pa::ERR_BAD_BLOCK);
@@ -265,7 +311,15 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             }
             my_tile = (uint32_t)(blk * hkv + q.g) | (q.C == 1 ? 0u : 0x80000000u);
         }
+        return q;
     };
+    Pos cur = refresh(0);                // of block f0: lane 0's
+    cur.s = __shfl_sync(0xffffffffu, cur.s, 0);
+    cur.g = __shfl_sync(0xffffffffu, cur.g, 0);
+    cur.c = __shfl_sync(0xffffffffu, cur.c, 0);
+    cur.b = __shfl_sync(0xffffffffu, cur.b, 0);
+    cur.nbs = __shfl_sync(0xffffffffu, cur.nbs, 0);
+    cur.C = __shfl_sync(0xffffffffu, cur.C, 0);
     // A block is staged by 16-byte asynchronous copies, a lane each: one or two of
     // its K codes, as many of V, and one of its scales and zero points. (Bulk and
     // tensor copies take their operands from uniform registers, so six of them a
@@ -289,10 +343,10 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     const int pairs = (n + 1) / 2;
     int issued = 0;                      // pairs of blocks asked for, every one a copy group
     uint32_t code_at = code_dst, meta_at = meta_dst;   // in the next pair's stage
-    auto issue = [&]() {                 // warp-uniform
+    auto issue = [&](bool starting) {    // warp-uniform
         if (issued < pairs) {
             const int b0 = 2 * issued;
-            if (b0 >= win + 32) refresh(b0 & ~31);
+            if (!starting && b0 >= win + 32) refresh(b0 & ~31);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 if (b0 + u >= n) break;
@@ -317,9 +371,8 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
         meta_at = wrap ? meta_dst : meta_at + 2 * Lay::kMeta;
     };
 #pragma unroll 1
-    for (int i = 0; i < S; ++i) issue();
+    for (int i = 0; i < S; ++i) issue(true);
 
-    Pos cur = locate(p, cum, chunks, f0);
     // S^T / O^T fragments: the lane holds query rows 8 nr + 2 qc and + 1
     float o[NR][CH][2][4];               // [.][chunk][dims 4 quad + 2 j, + 1][(dim, row)]
     float oz[NR][GR][4];                 // sum of P vz: row 2 qc + e in [e], of lanes quad == 0
@@ -379,25 +432,28 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
                 ex = max(-100, min(100, ex));
             }
             const float up[2] = {exp2i(14 - ex), exp2i(10 - ex)};
-            float qs[GR];
-#pragma unroll
-            for (int g = 0; g < GR; ++g) qs[g] = 0.f;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 4; ++e)
                     qb[nr][c][e] = pack_half2(v[c][e] * up[e & 1], v[c][e + 4] * up[e & 1]);
-                    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&qb[nr][c][e]));
-                    qs[c * GR / CH] += (f.x + f.y) * (e & 1 ? 16.f / kUnit : 1.f / kUnit);
+            // the sums over a group: the product with a K of codes 1
+            float ones[GR][4];
+            const uint32_t one[4] = {0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u};
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    float(&sum)[4] = ones[c * GR / CH];
+                    if (e == 0 && c % (CH / GR) == 0)
+                        mma_f16_first(sum, one, qb[nr][c][e], qb[nr][c][e + 1]);
+                    else
+                        mma_f16(sum, one, qb[nr][c][e], qb[nr][c][e + 1]);
                 }
             const float mul = row < rows ? p.scale_log2 * exp2i(ex - 14) * kUnit : 0.f;
 #pragma unroll
             for (int g = 0; g < GR; ++g) {
-                qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], 1);
-                qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], 2);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    qsum[nr][g][e] = __shfl_sync(0xffffffffu, qs[g], 4 * (2 * qc + e));
+                qsum[nr][g][0] = ones[g][0], qsum[nr][g][1] = ones[g][1];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) oz[nr][g][e] = 0.f;
             }
@@ -502,9 +558,11 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
     const uint32_t zsel = quad != 0 ? 0x4444u : GR == 2 ? 0x4240u : 0x4140u;
     // lane constants of the operand loads: a chunk further is 32 bytes in the swizzled row
     const uint32_t ld0 = tile4_offset<D>(ld_tok, ld_chk);
-    start_segment(n);
     int st = 0, half = 0;                // half: the stage's first block not yet done
+    bool start = true;                   // (one copy of the start: it is long, and cold code)
     for (int k = 0; k < n;) {
+        if (start) start_segment(n - k);
+        start = false;
         if (half == 0) {                 // S groups are on their way: the oldest is here
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
             __syncwarp();
@@ -724,7 +782,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
         half += take;
         if (half == 2) {
             __syncwarp();
-            issue();                     // into the stage just read
+            issue(false);                // into the stage just read
             half = 0;
             if (++st == S) st = 0;
         }
@@ -736,7 +794,7 @@ __global__ void __launch_bounds__(kWorkerWarps * 32, ctas_per_sm(D, NR))
             next_segment(p, cur, cum, chunks);
             seg_b0 = 0;
             seg_first = false;
-            start_segment(n - k);
+            start = true;
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -860,12 +918,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::
 template <typename TQ, int D, int NR>
 pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, Q4Extra x) {
     using Lay = Q4Layout<D>;
+    constexpr int kWorkerWarps = worker_warps(D, NR);
     auto kern = paged_decode_int4_kernel<TQ, D, NR>;
     static std::atomic<uint64_t> allowed{0};
-    if (pa_status s = pa::allow_smem(kern, Lay::smem_bytes(pa::kBalancedMaxSeqs), allowed,
+    if (pa_status s = pa::allow_smem(kern, Lay::smem_bytes(pa::kBalancedMaxSeqs, kWorkerWarps), allowed,
                                      "int4 decode: set shared memory size"))
         return s;
-    const int smem = Lay::smem_bytes(a.num_seqs);
+    const int smem = Lay::smem_bytes(a.num_seqs, kWorkerWarps);
     // the answers of the last call's queries, which cost as much as a launch
     thread_local int last_dev = -1, last_smem = -1, sms = 0, ctas = 0;
     int dev = 0;
