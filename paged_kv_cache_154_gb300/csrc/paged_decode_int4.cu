@@ -67,6 +67,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t p
                  : "memory");
 }
 
+// the same if `on` is not 0
+__device__ __forceinline__ void copy16_if(uint32_t on, uint32_t dst, const void* src,
+                                          uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+        "@p cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;\n\t}" ::"r"(dst),
+        "l"(src), "l"(policy), "r"(on)
+        : "memory");
+}
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -288,13 +298,15 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
         f0 = share_begin((uint32_t)wid, (uint32_t)B, (uint32_t)W);
         f1 = share_begin((uint32_t)wid + 1, (uint32_t)B, (uint32_t)W);
     }
-    const int n = (int)(f1 - f0);
+    // the same in all lanes, which a reduction tells the compiler too
+    const int n = __reduce_max_sync(0xffffffffu, (int)(f1 - f0));
     if (n <= 0) return;
 
-    const uint64_t pol_once = pa::policy_evict_first(), pol_again = pa::policy_evict_normal();
+    // read once, where no sequence has several row chunks; one policy a call, as its choice
+    // by block took 14 of 285 instructions a block
+    const uint64_t pol = x.max_chunks == 1 ? pa::policy_evict_first() : pa::policy_evict_normal();
 
-    // each lane keeps the (block x H_kv + kv head) tile of virtual block
-    // win + lane; the top bit: later row chunks read that block again
+    // each lane keeps the (block x H_kv + kv head) tile of virtual block win + lane
     int win = -32;
     uint32_t my_tile = 0;
     auto refresh = [&](int wbase) {
@@ -309,7 +321,7 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
                 if (p.err) atomicOr(p.err, pa::ERR_BAD_BLOCK);
                 blk = 0;
             }
-            my_tile = (uint32_t)(blk * hkv + q.g) | (q.C == 1 ? 0u : 0x80000000u);
+            my_tile = (uint32_t)(blk * hkv + q.g);
         }
         return q;
     };
@@ -328,7 +340,9 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
     const int row0 = lane / CH, chk0 = lane % CH;      // the lane's chunk of a code tile
     const uint32_t code_dst = ring + tile4_offset<D>(row0, chk0);
     constexpr int kS16 = Lay::kScaleArea / 16, kZ16 = Lay::kZpArea / 16;
-    const uint8_t* meta_src = nullptr;
+    const uint8_t* const k_src = x.k + 16 * lane;
+    const uint8_t* const v_src = x.v + 16 * lane;
+    const uint8_t* meta_src = k_src;
     uint32_t meta_bytes = 0;                           // of a block, in the lane's array
     const uint32_t meta_dst = ring + Lay::kMetaAt + 16 * lane;
     if (lane < 2 * kS16) {
@@ -348,20 +362,18 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
             const int b0 = 2 * issued;
             if (!starting && b0 >= win + 32) refresh(b0 & ~31);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (b0 + u >= n) break;
-                const uint32_t tagged = __shfl_sync(0xffffffffu, my_tile, b0 + u - win);
-                const uint32_t tile = tagged & 0x7fffffffu;
-                const uint64_t pol = tagged >> 31 ? pol_again : pol_once;
-                const uint64_t at = (uint64_t)tile * Lay::kTile + 16 * lane;
+            for (int u = 0; u < 2; ++u) {   // a last block alone is staged twice
+                const uint32_t tile = __shfl_sync(0xffffffffu, my_tile, min(b0 + u, n - 1) - win);
+                const uint8_t* const k = k_src + (uint64_t)tile * Lay::kTile;
+                const uint8_t* const v = v_src + (uint64_t)tile * Lay::kTile;
 #pragma unroll
                 for (int j = 0; j < Lay::kTile / 512; ++j) {
                     const uint32_t dst = code_at + u * Lay::kBlockCodes + 512 * j;
-                    copy16(dst, x.k + at + 512 * j, pol);
-                    copy16(dst + Lay::kTile, x.v + at + 512 * j, pol);
+                    copy16(dst, k + 512 * j, pol);
+                    copy16(dst + Lay::kTile, v + 512 * j, pol);
                 }
-                if (meta_bytes)
-                    copy16(meta_at + u * Lay::kMeta, meta_src + (uint64_t)tile * meta_bytes, pol);
+                copy16_if(meta_bytes, meta_at + u * Lay::kMeta,
+                          meta_src + (uint64_t)tile * meta_bytes, pol);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
