@@ -479,45 +479,43 @@ __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
     // this warp's blocks: b0 + warp, + kWarps, ...
     const int b0 = tile * (p.tile_tokens / kBS) + warp;
     const int nb = min((sq.L + kBS - 1) / kBS, (tile + 1) * (p.tile_tokens / kBS));
-    const int n = b0 < nb ? (nb - b0 + kWarps - 1) / kWarps : 0;
+    // the same in all lanes, which a reduction tells the compiler too
+    const int n = __reduce_max_sync(0xffffffffu, b0 < nb ? (nb - b0 + kWarps - 1) / kWarps : 0);
     int my_block = 0;
     if (lane < n) my_block = block_of(p, s, b0 + lane * kWarps);
-    auto fetch = [&](KRows<KV, D>& k, int i) {
-        const int64_t blk = __shfl_sync(0xffffffffu, my_block, i);
+    auto fetch = [&](KRows<KV, D>& k, int i) {   // past the last: the last again, not used
+        const int64_t blk = __shfl_sync(0xffffffffu, my_block, min(i, n - 1));
         k.load(p, (blk * p.num_kv_heads + g) * kBS, quad, qc);
     };
     KRows<KV, D> k[kDepth];
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i)
-        if (i < n) fetch(k[i], i);
+    for (int i = 0; i < kDepth - 1; ++i) fetch(k[i], i);
     QRows<KV, D, NR> q;
     q.load(p, sq, g, 0, quad, qc);
     RowSums<NR> sums;
     sums.clear(q.bound);
     // the lane's logits: rows 8 nr + 2 qc and + 1 of token quad, those that are kept
-    float* const keep = p.logits +
-                        (((int64_t)s * p.num_kv_heads + g) * p.tokens_pad + quad) * p.row_pad + 2 * qc;
+    float* keep = p.logits +
+                  (((int64_t)s * p.num_kv_heads + g) * p.tokens_pad + b0 * kBS + quad) * p.row_pad +
+                  2 * qc;
+    const int half = 8 * p.row_pad, step = kWarps * kBS * p.row_pad;
     for (int i0 = 0; i0 < n; i0 += kDepth) {
 #pragma unroll
         for (int u = 0; u < kDepth; ++u) {
             const int i = i0 + u;
             if (i >= n) break;
-            if (i + kDepth - 1 < n) fetch(k[(u + kDepth - 1) % kDepth], i + kDepth - 1);
+            fetch(k[(u + kDepth - 1) % kDepth], i + kDepth - 1);
             const int tok0 = (b0 + i * kWarps) * kBS;
             float a[NR][4];
             q.logits(k[u], tok0, quad, tok0 + kBS - 1 > sq.L - sq.r, a);
             sums.add(a);
-            float* const dst = keep + (int64_t)tok0 * p.row_pad;
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float* const at = dst + 8 * h * p.row_pad + 8 * nr;
-                    if (8 * nr + 2 * qc + 1 < p.row_pad)
-                        *reinterpret_cast<float2*>(at) = make_float2(a[nr][2 * h], a[nr][2 * h + 1]);
-                    else if (8 * nr + 2 * qc < p.row_pad)
-                        *at = a[nr][2 * h];
+                if (8 * nr + 2 * qc < p.row_pad) {
+                    *reinterpret_cast<float2*>(keep + 8 * nr) = make_float2(a[nr][0], a[nr][1]);
+                    *reinterpret_cast<float2*>(keep + half + 8 * nr) = make_float2(a[nr][2], a[nr][3]);
                 }
+            keep += step;
         }
     }
     sums.finish(part[warp], quad, qc);
@@ -760,7 +758,7 @@ Shape shape_of(int num_seqs, int num_heads, int num_kv_heads, int max_q_len, int
         return h;
     h.tokens_pad = (max_len + kBS - 1) / kBS * kBS;
     const int64_t sg = (int64_t)num_seqs * num_kv_heads;
-    h.row_pad = 1;
+    h.row_pad = 2;            // two rows a store
     while (h.row_pad < h.rows) h.row_pad *= 2;
     h.stored = h.rows <= 16 && sg * h.tokens_pad <= kMaxStored / (4 * h.row_pad);
     if (h.stored) h.logits_bytes = sg * h.tokens_pad * h.row_pad * 4;
@@ -799,7 +797,6 @@ pa_status launch_typed(Params& p, const Shape& h, void* workspace, cudaStream_t 
                 "accumulate_weights logits launch"))
             return s;
         switch (p.row_pad) {
-            case 1: return launch_stored<1>(p, st);
             case 2: return launch_stored<2>(p, st);
             case 4: return launch_stored<4>(p, st);
             case 8: return launch_stored<8>(p, st);
