@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -257,6 +258,8 @@ struct QRows {
     int bound[NR][2];
     float qsum[NR][kSums][2];
 
+    // OWN: mul, bound and qsum are those of rows 8 nr + quad instead, in [..][0]
+    template <bool OWN = false>
     __device__ __forceinline__ void load(const Params& p, const Seq& sq, int g, int first,
                                          int quad, int qc) {
         const int rows = p.group * sq.r;
@@ -335,6 +338,13 @@ struct QRows {
                     qs[i] += __shfl_xor_sync(0xffffffffu, qs[i], 1);
                     qs[i] += __shfl_xor_sync(0xffffffffu, qs[i], 2);
                 }
+            }
+            if constexpr (OWN) {
+                mul[nr][0] = m;
+#pragma unroll
+                for (int i = 0; i < kSums; ++i) qsum[nr][i][0] = qs[i];
+                bound[nr][0] = on ? min(sq.L - sq.r + qi, sq.L - 1) : -1;
+                continue;
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -612,18 +622,170 @@ __global__ void __launch_bounds__(256) stored_kernel(const Params p) {
 }
 
 // Tokens of a many_kernel tile: enough for the starts of its warps to be worth it
-// (28.6 us for the 8 prompts below, 30.2 with 128), 64 KB of K at most.
+// (1.6 us less for the 8 prompts below than 128), 64 KB of K at most.
 constexpr int kManyTokens = 256;
+
+// 16 rows against the 16 tokens of two blocks, rows in the M dimension: the 16 bytes
+// that a lane loads of a token are B operands as they come (with tokens in M an A operand
+// mixes two tokens' words, which cost a move each), and the rows' A operands come from
+// shared memory, one load for both blocks (kept in registers, they were copied for every
+// product). Two blocks, since the chain of a block's load, products and vote is what a warp
+// waits for. v[u][nr][h][e]: product of row 8 nr + quad and token 8 h + 2 qc + e of block u,
+// without the row's factor.
+template <int KV, int D>
+struct ManyBlocks {
+    using K = KRows<KV, D>;
+    float v[2][2][2][2];
+    __device__ __forceinline__ void run(const Params& p, const QRows<KV, D, 2>& q, uint32_t qa,
+                                        const uint32_t (&staged)[2], const int64_t (&row)[2],
+                                        int quad, int qc) {
+        constexpr int G = K::kGroups;
+        K k[2];
+        float scale[2][2][2][G], zp[2][2][2][G];    // of tokens 8 h + 2 qc + e
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            k[u].load_staged(staged[u]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t t = row[u] + 8 * h + 2 * qc;
+                float(&sc)[2][G] = scale[u][h];
+                float(&z0)[2][G] = zp[u][h];
+                if constexpr (KV == PA_INT8) {
+                    sc[0][0] = __ldg(p.k_scale + t), sc[1][0] = __ldg(p.k_scale + t + 1);
+                    k[u].zp[h][0] = __ldg(p.k_zp + row[u] + 8 * h + quad);
+                } else if constexpr (G == 2) {
+                    const float4 f = __ldg(reinterpret_cast<const float4*>(p.k_scale + 2 * t));
+                    const uint32_t z = __ldg(reinterpret_cast<const uint32_t*>(p.k_zp + 2 * t));
+                    sc[0][0] = f.x, sc[0][1] = f.y, sc[1][0] = f.z, sc[1][1] = f.w;
+                    z0[0][0] = (float)(z & 255), z0[0][1] = (float)(z >> 8 & 255);
+                    z0[1][0] = (float)(z >> 16 & 255), z0[1][1] = (float)(z >> 24);
+                } else if constexpr (KV == PA_INT4) {
+                    const float2 f = __ldg(reinterpret_cast<const float2*>(p.k_scale + t));
+                    const uint16_t z = __ldg(reinterpret_cast<const uint16_t*>(p.k_zp + t));
+                    sc[0][0] = f.x, sc[1][0] = f.y;
+                    z0[0][0] = (float)(z & 255), z0[1][0] = (float)(z >> 8);
+                }
+            }
+        }
+        float s[2][2][G][4];
+#pragma unroll
+        for (int kk = 0; kk < K::kSteps; ++kk) {
+            uint32_t a[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                         : "r"(qa + 512 * kk));
+            const int g = kk * G / K::kSteps;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (kk % (K::kSteps / G) == 0)
+                        mma_first<KV == PA_BF16>(s[u][h][g], a, k[u].pair(h, kk, 0),
+                                                 k[u].pair(h, kk, 1));
+                    else
+                        pa::mma_16816<KV == PA_BF16>(s[u][h][g], a, k[u].pair(h, kk, 0),
+                                                     k[u].pair(h, kk, 1));
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int u = i / 8, nr = i / 4 % 2, h = i / 2 % 2, e = i % 2;
+            float x = s[u][h][0][2 * nr + e];
+            if constexpr (KV == PA_INT4) x = fmaf(-zp[u][h][e][0], q.qsum[nr][0][0], x);
+            if constexpr (K::kScaled) x *= scale[u][h][e][0];
+            if constexpr (G == 2)
+                x = fmaf(fmaf(-zp[u][h][e][1], q.qsum[nr][1][0], s[u][h][1][2 * nr + e]),
+                         scale[u][h][e][1], x);
+            v[u][nr][h][e] = x;
+        }
+    }
+    // logits (base-2 units) less ref, -inf where the row does not see the token
+    __device__ __forceinline__ void relative(const QRows<KV, D, 2>& q, const float (&ref)[2],
+                                             const int (&tok0)[2], int qc, bool masked,
+                                             float (&t)[2][2][2][2]) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int u = i / 8, nr = i / 4 % 2, h = i / 2 % 2, e = i % 2;
+            t[u][nr][h][e] = fmaf(v[u][nr][h][e], q.mul[nr][0], -ref[nr]);
+        }
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int u = i / 8, nr = i / 4 % 2, h = i / 2 % 2, e = i % 2;
+                if (tok0[u] + 8 * h + 2 * qc + e > q.bound[nr][0]) t[u][nr][h][e] = -INFINITY;
+            }
+        }
+    }
+};
+
+// The running sums of the lane's rows quad and quad + 8, as RowSums.
+struct ManySums {
+    float ref[2], l[2];
+    template <int KV, int D>
+    __device__ __forceinline__ void clear(const QRows<KV, D, 2>& q) {
+#pragma unroll
+        for (int nr = 0; nr < 2; ++nr) {
+            ref[nr] = q.bound[nr][0] < 0 ? 0.f : -INFINITY;
+            l[nr] = 0.f;
+        }
+    }
+    __device__ __forceinline__ static float largest(const float (&t)[2][2][2][2], int nr) {
+        return fmaxf(fmaxf(fmaxf(t[0][nr][0][0], t[0][nr][0][1]), fmaxf(t[0][nr][1][0], t[0][nr][1][1])),
+                     fmaxf(fmaxf(t[1][nr][0][0], t[1][nr][0][1]), fmaxf(t[1][nr][1][0], t[1][nr][1][1])));
+    }
+    template <int KV, int D>
+    __device__ __forceinline__ void add(const ManyBlocks<KV, D>& b, const QRows<KV, D, 2>& q,
+                                        const int (&tok0)[2], int qc, bool masked) {
+        float t[2][2][2][2];
+        b.relative(q, ref, tok0, qc, masked, t);
+        const bool raise = !(largest(t, 0) <= 8.f) || !(largest(t, 1) <= 8.f);
+        if (__any_sync(0xffffffffu, raise)) {
+            const float zero[2] = {0.f, 0.f};
+            float a[2][2][2][2];
+            b.relative(q, zero, tok0, qc, masked, a);
+#pragma unroll
+            for (int nr = 0; nr < 2; ++nr) {
+                float mx = largest(a, nr);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                if (mx > ref[nr] + 8.f) {
+                    l[nr] *= pa::ex2(ref[nr] - mx);   // 0 while ref is -inf
+                    ref[nr] = mx;
+                }
+                // still no token: nothing but -inf and NaN, which stays
+                const bool none = ref[nr] == -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float x = a[i / 4][nr][i / 2 % 2][i % 2];
+                    t[i / 4][nr][i / 2 % 2][i % 2] = none && x == -INFINITY ? -INFINITY : x - ref[nr];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nr = 0; nr < 2; ++nr)
+                l[nr] += (pa::ex2(t[u][nr][0][0]) + pa::ex2(t[u][nr][0][1])) +
+                         (pa::ex2(t[u][nr][1][0]) + pa::ex2(t[u][nr][1][1]));
+    }
+    __device__ __forceinline__ void finish(float2* part, int quad, int qc) {
+#pragma unroll
+        for (int nr = 0; nr < 2; ++nr) {
+            float sum = l[nr];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (qc == 0) part[8 * nr + quad] = make_float2(ref[nr], sum);
+        }
+    }
+};
 
 // Many rows. Grid: (tiles of kManyTokens, KV head, sequence). The tile's K is
 // staged in shared memory once; warp (rc, tg) takes the row chunks rc, rc +
 // row_warps, .. of 16 rows and the tile's blocks tg, tg + token_warps, ... SUM
 // false: the rows' (m, l) over the tile; SUM true: the weights of the tile's
 // tokens, summed over the rows (each warp keeps sums of its own, which are added
-// up in a fixed order). 8 prompts of up to 4001 tokens, 128 rows, d = 64: 28.6 us
-// a call; 40 us with K loaded from global memory for every chunk of rows; 32 us
-// with ldmatrix in place of 16-byte loads, although that saves four register
-// moves a product.
+// up in a fixed order). Bound by the latency of a warp's pairs of blocks. 8 prompts
+// of up to 4001 tokens, 128 rows, d = 64: 25.2 us a call; 28.6 us with tokens in M,
+// a block at a time; 40 us with K loaded from global memory for every chunk of rows.
 template <int KV, int D, bool SUM>
 __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
     constexpr int NR = 2, kTokens = kManyTokens, kBlocks = kTokens / kBS;
@@ -631,6 +793,7 @@ __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
     // K, then SUM: float [row_warps][kTokens]; aligned to the span that staged rows exchange in
     extern __shared__ __align__(256) uint8_t tile_s[];
     __shared__ int blocks_s[kBlocks];
+    __shared__ uint4 turn_s[kManyWarps][KRows<KV, D>::kSteps][32];
     __shared__ float2 part_s[kManyWarps][8 * NR];
     pa::grid_dependents_launch();
     pa::grid_dependency_wait();
@@ -667,43 +830,71 @@ __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
         // the last token that every row of the chunk sees (rows past the last see none)
         const int last_seen = first + 8 * NR <= rows ? sq.L - sq.r + first / p.group : -1;
         QRows<KV, D, NR> q;
-        RowSums<NR> own;
-        float2 total[NR][2];
+        ManySums own;
+        float ref[2], inv[2];
         if (first < rows) {              // warp-uniform
-            q.load(p, sq, g, first, quad, qc);
-            own.clear(q.bound);
+            q.template load<true>(p, sq, g, first, quad, qc);
+#pragma unroll
+            for (int kk = 0; kk < KRows<KV, D>::kSteps; ++kk)
+                turn_s[warp][kk][lane] =
+                    make_uint4(q.b[0][kk][0], q.b[1][kk][0], q.b[0][kk][1], q.b[1][kk][1]);
+            __syncwarp();
+            const uint32_t qa = pa::smem_addr(&turn_s[warp][0][lane]);
+            own.clear(q);
             if constexpr (SUM) {
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = first + 8 * nr + 2 * qc + e;
-                        total[nr][e] = row < rows ? __ldcg(p.sums + sg * p.row_slots + row)
-                                                  : make_float2(0.f, 0.f);
-                    }
+                for (int nr = 0; nr < NR; ++nr) {
+                    const int row = first + 8 * nr + quad;
+                    const float2 t = row < rows ? __ldcg(p.sums + sg * p.row_slots + row)
+                                                : make_float2(0.f, 0.f);
+                    ref[nr] = t.x, inv[nr] = t.y;
+                }
             }
-            for (int b = tg; b < nb; b += token_warps) {
-                KRows<KV, D> k;
-                k.load_scales(p, ((int64_t)blocks_s[b] * p.num_kv_heads + g) * kBS, quad);
-                k.load_staged(staged + b * kBS * kRowBytes);
-                float a[NR][4];
-                q.logits(k, t0 + b * kBS, quad, t0 + (b + 1) * kBS - 1 > last_seen, a);
+            for (int b = tg; b < nb; b += 2 * token_warps) {
+                const int second = b + token_warps;
+                const bool both = second < nb;      // else the first again, masked
+                const int at[2] = {b, both ? second : b};
+                uint32_t from[2];
+                int64_t row[2];
+                int tok0[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    from[u] = staged + at[u] * kBS * kRowBytes;
+                    row[u] = KRows<KV, D>::kScaled
+                                 ? ((int64_t)blocks_s[at[u]] * p.num_kv_heads + g) * kBS
+                                 : 0;
+                    tok0[u] = t0 + at[u] * kBS;
+                }
+                const bool masked = !both || tok0[1] + kBS - 1 > last_seen;
+                if (!both) tok0[1] = INT_MAX / 2;
+                ManyBlocks<KV, D> blocks;
+                blocks.run(p, q, qa, from, row, quad, qc);
                 if constexpr (!SUM) {
-                    own.add(a);
+                    own.add(blocks, q, tok0, qc, masked);
                 } else {
+                    float t[2][2][2][2];
+                    blocks.relative(q, ref, tok0, qc, masked, t);
+                    // over the 8 lanes of a token, which split the eight tokens between them
+                    const bool up = lane & 16, odd = lane & 8, far = lane & 4;
+                    float w[2][4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float w = 0.f;
+                    for (int i = 0; i < 8; ++i)
+                        w[i / 4][i % 4] = fmaf(pa::ex2(t[i / 4][0][i / 2 % 2][i % 2]), inv[0],
+                                               pa::ex2(t[i / 4][1][i / 2 % 2][i % 2]) * inv[1]);
+                    float x[4], y[2];
 #pragma unroll
-                        for (int nr = 0; nr < NR; ++nr)
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = (up ? w[1][i] : w[0][i]) +
+                               __shfl_xor_sync(0xffffffffu, up ? w[0][i] : w[1][i], 16);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                w = fmaf(pa::ex2(a[nr][2 * h + e] - total[nr][e].x),
-                                         total[nr][e].y, w);
-                        w += __shfl_xor_sync(0xffffffffu, w, 1);
-                        w += __shfl_xor_sync(0xffffffffu, w, 2);
-                        if (qc == 0) sums[rc * kTokens + b * kBS + quad + 8 * h] += w;
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        y[i] = (odd ? x[2 + i] : x[i]) +
+                               __shfl_xor_sync(0xffffffffu, odd ? x[i] : x[2 + i], 8);
+                    const float sum = (far ? y[1] : y[0]) +
+                                      __shfl_xor_sync(0xffffffffu, far ? y[0] : y[1], 4);
+                    if (both || !up)
+                        sums[rc * kTokens + (up ? at[1] : at[0]) * kBS + (odd ? 8 : 0) + 2 * qc +
+                             (far ? 1 : 0)] += sum;
                 }
             }
         }
