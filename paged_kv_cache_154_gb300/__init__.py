@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import Optional, Sequence, Tuple
 
 import numpy as np
@@ -322,10 +323,11 @@ def append_kv(key, value, k_cache, v_cache, slot_mapping, num_blocks: Optional[i
     """pa_append_kv; key/value [T, H_kv, d]; slot_mapping device int64 [T]."""
     T = int(key.shape[0])
     nb = k_cache.shape[0] if num_blocks is None else num_blocks
+    shape, code = k_cache.shape, _dtype_code(k_cache)
     _check(lib().pa_append_kv(_ptr(key), _ptr(value), _dtype_code(key), _ptr(k_cache),
-                              _ptr(v_cache), _dtype_code(k_cache), _ptr(k_scale),
-                              _ptr(v_scale), _ptr(k_zp), _ptr(v_zp), _ptr(slot_mapping), T, nb,
-                              k_cache.shape[1], _head_dim(k_cache), k_cache.shape[2],
+                              _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale), _ptr(k_zp),
+                              _ptr(v_zp), _ptr(slot_mapping), T, nb, shape[1],
+                              shape[3] * 2 if code == PA_INT4 else shape[3], shape[2],
                               _stream(stream)))
 
 
@@ -335,10 +337,11 @@ def gather_kv(key, value, k_cache, v_cache, slot_mapping, num_blocks: Optional[i
     BF16 or F32) receive the cached rows at the values the cache holds."""
     T = int(key.shape[0])
     nb = k_cache.shape[0] if num_blocks is None else num_blocks
+    shape, code = k_cache.shape, _dtype_code(k_cache)
     _check(lib().pa_gather_kv(_ptr(key), _ptr(value), _dtype_code(key), _ptr(k_cache),
-                              _ptr(v_cache), _dtype_code(k_cache), _ptr(k_scale),
-                              _ptr(v_scale), _ptr(k_zp), _ptr(v_zp), _ptr(slot_mapping), T, nb,
-                              k_cache.shape[1], _head_dim(k_cache), k_cache.shape[2],
+                              _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale), _ptr(k_zp),
+                              _ptr(v_zp), _ptr(slot_mapping), T, nb, shape[1],
+                              shape[3] * 2 if code == PA_INT4 else shape[3], shape[2],
                               _stream(stream)))
 
 
@@ -413,9 +416,11 @@ def decode_shared_prefix(out, q, k_cache, v_cache, block_tables, context_lens,
 # eviction by accumulated attention weight
 # ---------------------------------------------------------------------------
 
-def _shaped(name: str, t, shape, dtype) -> None:
-    if t.shape != shape or t.dtype is not dtype:
-        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
+def _shaped(shape, dtype, *named) -> None:
+    """Every (name, tensor) has this shape and type (tensors that are None may)."""
+    for name, t in named:
+        if t is not None and (t.shape != shape or t.dtype is not dtype):
+            raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
 
 
 def accumulate_weights_workspace_size(num_seqs: int, num_q_tokens: int, num_heads: int,
@@ -432,16 +437,13 @@ def accumulate_weights(scores_out, scores_in, q, k_cache, block_tables, context_
     """pa_accumulate_weights; scores fp32 [num_seqs, H_kv, width >= max_context_len],
     scores_in None for zeros, or scores_out itself; workspace: uint8 of
     accumulate_weights_workspace_size() bytes; other arguments as decode()."""
-    import torch
-    num_seqs = int(context_lens.shape[0])
+    torch = sys.modules["torch"]
+    num_seqs = context_lens.shape[0]
     shape = (num_seqs, k_cache.shape[1], scores_out.shape[2])
-    _shaped("scores_out", scores_out, shape, torch.float32)
-    if scores_in is not None:
-        _shaped("scores_in", scores_in, shape, torch.float32)
-    _shaped("block_tables", block_tables, (num_seqs, block_tables.shape[1]), torch.int32)
-    _shaped("context_lens", context_lens, (num_seqs,), torch.int32)
-    if query_start_loc is not None:
-        _shaped("query_start_loc", query_start_loc, (num_seqs + 1,), torch.int32)
+    _shaped(shape, torch.float32, ("scores_out", scores_out), ("scores_in", scores_in))
+    _shaped((num_seqs,), torch.int32, ("context_lens", context_lens))
+    _shaped((num_seqs, block_tables.shape[1]), torch.int32, ("block_tables", block_tables))
+    _shaped((num_seqs + 1,), torch.int32, ("query_start_loc", query_start_loc))
     nb = k_cache.shape[0] if num_blocks is None else num_blocks
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().pa_accumulate_weights(
@@ -459,24 +461,20 @@ def evict_select(moves, move_counts, scores_out, positions_out, scores, position
     """pa_evict_select; moves int32 [num_seqs, H_kv, max_moves, 2], move_counts
     int32 [num_seqs, H_kv], scores fp32 and positions int32 (or None) [num_seqs,
     H_kv, width], lengths int32 [num_seqs] (total_lens may be None)."""
-    import torch
-    num_seqs = int(context_lens.shape[0])
-    shape = (num_seqs, scores.shape[1], scores.shape[2])
-    _shaped("scores", scores, shape, torch.float32)
-    _shaped("scores_out", scores_out, shape, torch.float32)
-    _shaped("positions_out", positions_out, shape, torch.int32)
-    if positions is not None:
-        _shaped("positions", positions, shape, torch.int32)
-    _shaped("moves", moves, (*shape[:2], moves.shape[2], 2), torch.int32)
-    _shaped("move_counts", move_counts, shape[:2], torch.int32)
-    _shaped("context_lens", context_lens, shape[:1], torch.int32)
-    _shaped("new_lens", new_lens, shape[:1], torch.int32)
-    if total_lens is not None:
-        _shaped("total_lens", total_lens, shape[:1], torch.int32)
+    torch = sys.modules["torch"]
+    num_seqs, shape = context_lens.shape[0], scores.shape
+    heads, width, max_moves = shape[1], shape[2], moves.shape[2]
+    _shaped((num_seqs, heads, width), torch.float32, ("scores", scores),
+            ("scores_out", scores_out))
+    _shaped(shape, torch.int32, ("positions_out", positions_out), ("positions", positions))
+    _shaped((num_seqs, heads, max_moves, 2), torch.int32, ("moves", moves))
+    _shaped((num_seqs, heads), torch.int32, ("move_counts", move_counts))
+    _shaped((num_seqs,), torch.int32, ("context_lens", context_lens), ("new_lens", new_lens),
+            ("total_lens", total_lens))
     _check(lib().pa_evict_select(
-        _ptr(moves), moves.shape[2], _ptr(move_counts), _ptr(scores_out), _ptr(positions_out),
-        _ptr(scores), _ptr(positions), shape[2], _ptr(context_lens), _ptr(new_lens),
-        _ptr(total_lens), num_seqs, shape[1], int(max_context_len), int(num_sinks),
+        _ptr(moves), max_moves, _ptr(move_counts), _ptr(scores_out), _ptr(positions_out),
+        _ptr(scores), _ptr(positions), width, _ptr(context_lens), _ptr(new_lens),
+        _ptr(total_lens), num_seqs, heads, int(max_context_len), int(num_sinks),
         int(num_recent), _stream(stream)))
 
 
@@ -484,19 +482,19 @@ def move_tokens(k_cache, v_cache, block_tables, context_lens, moves, move_counts
                 max_context_len: int, num_blocks=None, k_scale=None, v_scale=None, k_zp=None,
                 v_zp=None, stream=None) -> None:
     """pa_move_tokens; moves and move_counts as evict_select() writes them."""
-    import torch
-    num_seqs = int(context_lens.shape[0])
-    shape = (num_seqs, k_cache.shape[1])
-    _shaped("moves", moves, (*shape, moves.shape[2], 2), torch.int32)
-    _shaped("move_counts", move_counts, shape, torch.int32)
-    _shaped("context_lens", context_lens, shape[:1], torch.int32)
-    _shaped("block_tables", block_tables, (num_seqs, block_tables.shape[1]), torch.int32)
-    nb = k_cache.shape[0] if num_blocks is None else num_blocks
+    torch = sys.modules["torch"]
+    num_seqs, cache = context_lens.shape[0], k_cache.shape
+    heads, max_moves, blocks = cache[1], moves.shape[2], block_tables.shape[1]
+    _shaped((num_seqs, heads, max_moves, 2), torch.int32, ("moves", moves))
+    _shaped((num_seqs, heads), torch.int32, ("move_counts", move_counts))
+    _shaped((num_seqs,), torch.int32, ("context_lens", context_lens))
+    _shaped((num_seqs, blocks), torch.int32, ("block_tables", block_tables))
+    nb = cache[0] if num_blocks is None else num_blocks
     _check(lib().pa_move_tokens(
         _ptr(k_cache), _ptr(v_cache), _dtype_code(k_cache), _ptr(k_scale), _ptr(v_scale),
-        _ptr(k_zp), _ptr(v_zp), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-        _ptr(moves), moves.shape[2], _ptr(move_counts), num_seqs, k_cache.shape[1],
-        _head_dim(k_cache), k_cache.shape[2], nb, int(max_context_len), _stream(stream)))
+        _ptr(k_zp), _ptr(v_zp), _ptr(block_tables), blocks, _ptr(context_lens), _ptr(moves),
+        max_moves, _ptr(move_counts), num_seqs, heads, _head_dim(k_cache), cache[2], nb,
+        int(max_context_len), _stream(stream)))
 
 
 NO_ALLOC_WORKSPACE_BYTES = 40 << 20
