@@ -15,7 +15,7 @@
 //   2. the tiles' (m, l) merged into a row's, and out = in + sum over rows
 //      2^(a - m) / l: from the logits that kernel 1 stored (stored_kernel, which
 //      merges for itself), or from logits computed again (many_kernel for both
-//      passes, rows_kernel between them).
+//      passes, rows_kernel between them where contexts are long).
 //
 // Storing costs 8 bytes a row and token, mostly within L2; computing again costs
 // a second read of K and its products. So few rows are stored (up to 16 rows
@@ -25,8 +25,11 @@
 // operand registers directly: tokens stand in the M dimension of the warp-level
 // product, and as the order of the dims is free (q is loaded in the same order), a
 // lane's 16-byte load of its token is four operand registers with no staging in
-// shared memory. For many rows it is the products and exponentials: a tile of K is
-// staged in shared memory once, for warps that hold 16 rows of q each.
+// shared memory. The Llama-3-8B-shaped step (64 sequences of 512-4096 tokens, bf16,
+// 325 MB) takes 64.4 us: 54 us at 82 % of the copy rate, and the sum; one 4-bit sequence
+// of 100001 tokens (66 MB) 26.7 us, where the chain of a block counts as much as its
+// bytes. For many rows it is the latency of load, product and exponential: a tile of
+// K is staged in shared memory once, for warps of 16 rows of q each.
 // Codes are made exact in fp16: code - zero point (INT8), E4M3 to fp16, masked
 // nibbles as subnormals with the zero points taken out of the sums (INT4, as in
 // the decode kernel); q goes to fp16 after an exact power-of-two scaling per row.
@@ -68,7 +71,8 @@ struct Params {
     const int32_t* qsl;       // may be null: one query token per sequence
     float* logits;            // [num_seqs x H_kv][max tokens, a multiple of 16][row_pad], or null
     float2* stats;            // [num_seqs x H_kv][row_slots][tiles]: (m, l)
-    float2* sums;             // [num_seqs x H_kv][row_slots]: see row_sum; computed again only
+    float2* sums;             // [num_seqs x H_kv][row_slots]: see row_sum; computed again only,
+                              // null: every warp makes its rows' from stats
     int row_warps;            // many_kernel: warps over chunks of 16 rows; the others split tokens
     int tile_tokens;          // of stats
     unsigned int* err;
@@ -540,19 +544,21 @@ __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
 }
 
 // What turns a row's logit a into its weight 2^(a - ref) * inv, from the (m, l)
-// of its tiles, by one warp: ref = m and inv = 1 / l, or 0 and 0 for a row that
+// of its tiles, by LANES lanes: ref = m and inv = 1 / l, or 0 and 0 for a row that
 // saw nothing.
+template <int LANES>
 __device__ __forceinline__ float2 row_sum(const Params& p, const Seq& sq, int64_t sg, int row,
                                           int lane) {
     const int tiles = (sq.L + p.tile_tokens - 1) / p.tile_tokens;
     const float2* src = p.stats + (sg * p.row_slots + row) * p.tiles;
     float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < tiles; i += 32) {
+#pragma unroll 4
+    for (int i = lane; i < tiles; i += LANES) {
         const float2 t = __ldcg(src + i);   // the kernel before may have ended under this one
         merge(m, l, t.x, t.y);
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
+    for (int off = LANES / 2; off > 0; off >>= 1)
         merge(m, l, __shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, l, off));
     return make_float2(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l);
 }
@@ -566,7 +572,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const Params p) {
     const Seq sq(p, s);
     if (row >= p.group * sq.r) return;
     const int64_t sg = (int64_t)s * p.num_kv_heads + g;
-    const float2 t = row_sum(p, sq, sg, row, lane);
+    const float2 t = row_sum<32>(p, sq, sg, row, lane);
     if (lane == 0) p.sums[sg * p.row_slots + row] = t;
 }
 
@@ -605,7 +611,7 @@ __global__ void __launch_bounds__(256) stored_kernel(const Params p) {
         }
     }
     for (int row = threadIdx.x >> 5; row < min(rows, RP); row += 8) {
-        const float2 t = row_sum(p, sq, sg, row, threadIdx.x & 31);
+        const float2 t = row_sum<32>(p, sq, sg, row, threadIdx.x & 31);
         if ((threadIdx.x & 31) == 0) sum[row] = t;
     }
     __syncthreads();
@@ -784,8 +790,9 @@ struct ManySums {
 // false: the rows' (m, l) over the tile; SUM true: the weights of the tile's
 // tokens, summed over the rows (each warp keeps sums of its own, which are added
 // up in a fixed order). Bound by the latency of a warp's pairs of blocks. 8 prompts
-// of up to 4001 tokens, 128 rows, d = 64: 25.2 us a call; 28.6 us with tokens in M,
-// a block at a time; 40 us with K loaded from global memory for every chunk of rows.
+// of up to 4001 tokens, 128 rows, d = 64: 23.5 us a call; 3.5 us more with tokens in
+// M, a block at a time, and 11 more again with K loaded from global memory for every
+// chunk of rows.
 template <int KV, int D, bool SUM>
 __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
     constexpr int NR = 2, kTokens = kManyTokens, kBlocks = kTokens / kBS;
@@ -845,8 +852,12 @@ __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr) {
                     const int row = first + 8 * nr + quad;
-                    const float2 t = row < rows ? __ldcg(p.sums + sg * p.row_slots + row)
-                                                : make_float2(0.f, 0.f);
+                    float2 t = make_float2(0.f, 0.f);
+                    if (p.sums) {
+                        if (row < rows) t = __ldcg(p.sums + sg * p.row_slots + row);
+                    } else {
+                        t = row_sum<4>(p, sq, sg, min(row, rows - 1), qc);
+                    }
                     ref[nr] = t.x, inv[nr] = t.y;
                 }
             }
@@ -933,6 +944,11 @@ int stored_tile(int64_t tokens) {
     return t > kMaxTile ? 512 : (int)std::max<int64_t>(128, (t + 63) / 64 * 64);
 }
 
+// Up to as many tiles the warps of the last pass merge their rows' (m, l) themselves, by
+// one batch of loads; beyond, a kernel between the passes does it once (8 prompts of 4001
+// tokens, 16 tiles: 34.9 us, 35.7 with that kernel; of 8192, 32 tiles: 56.7 and 53.9).
+constexpr int kFoldTiles = 16;
+
 struct Shape {
     int64_t rows;         // most query rows per KV head
     int row_pad, tiles, tile_tokens, tokens_pad;
@@ -953,11 +969,11 @@ Shape shape_of(int num_seqs, int num_heads, int num_kv_heads, int max_q_len, int
     while (h.row_pad < h.rows) h.row_pad *= 2;
     h.stored = h.rows <= 16 && sg * h.tokens_pad <= kMaxStored / (4 * h.row_pad);
     if (h.stored) h.logits_bytes = sg * h.tokens_pad * h.row_pad * 4;
-    else h.sums_bytes = (sg * h.rows * 8 + 255) / 256 * 256;
     h.tile_tokens = h.stored ? stored_tile(sg * max_len) : kManyTokens;
     h.tiles = (max_len + h.tile_tokens - 1) / h.tile_tokens;
     if (sg * h.rows > kMaxWorkspace / 8 / h.tiles) return h;
     h.stats_bytes = (sg * h.rows * h.tiles * 8 + 255) / 256 * 256;
+    if (!h.stored && h.tiles > kFoldTiles) h.sums_bytes = (sg * h.rows * 8 + 255) / 256 * 256;
     h.fits = true;
     return h;
 }
@@ -997,7 +1013,7 @@ pa_status launch_typed(Params& p, const Shape& h, void* workspace, cudaStream_t 
     constexpr int kTokens = kManyTokens;
     p.tiles = h.tiles;
     p.tile_tokens = h.tile_tokens;
-    p.sums = reinterpret_cast<float2*>(ws + h.stats_bytes);
+    if (h.sums_bytes) p.sums = reinterpret_cast<float2*>(ws + h.stats_bytes);
     p.row_warps = 1;
     while (p.row_warps < kManyWarps && 16 * p.row_warps < h.rows) p.row_warps *= 2;
     const int tile = kTokens * KRows<KV, D>::kRowBytes, sums = 4 * p.row_warps * kTokens;
@@ -1013,13 +1029,14 @@ pa_status launch_typed(Params& p, const Shape& h, void* workspace, cudaStream_t 
             pa::launch_pdl(many_kernel<KV, D, false>, grid, block, (size_t)tile, st, p),
             "accumulate_weights logits launch"))
         return s;
-    if (pa_status s = pa::cuda_status(
-            pa::launch_pdl(rows_kernel,
-                           dim3((unsigned)((h.rows + kWarps - 1) / kWarps), p.num_kv_heads,
-                                p.num_seqs),
-                           dim3(kWarps * 32), 0, st, p),
-            "accumulate_weights row sums launch"))
-        return s;
+    if (p.sums)
+        if (pa_status s = pa::cuda_status(
+                pa::launch_pdl(rows_kernel,
+                               dim3((unsigned)((h.rows + kWarps - 1) / kWarps), p.num_kv_heads,
+                                    p.num_seqs),
+                               dim3(kWarps * 32), 0, st, p),
+                "accumulate_weights row sums launch"))
+            return s;
     return pa::cuda_status(
         pa::launch_pdl(many_kernel<KV, D, true>, grid, block, (size_t)(tile + sums), st, p),
         "accumulate_weights sum launch");

@@ -10,7 +10,8 @@ import torch
 import paged_kv_cache_154_gb300 as pa
 from oracle import compressed as ref
 from paged_kv_cache_154_gb300.engine import PagedKVCache
-from test_gpu_eviction import accumulate, check_select, filled, run_select
+from test_gpu_eviction import accumulate, check as check_weights
+from test_gpu_eviction import check_select, filled, run_select
 from test_gpu_int4 import check, decode, sequences
 
 pytestmark = pytest.mark.gpu
@@ -49,6 +50,19 @@ def test_rows_of_empty_sequences_are_left_as_they_were(long):
     live = [1, 3]
     assert (out[[0, 2, 4]] == 5.5).all()
     check(out[live], q[live], cache, tables[live], [long, 33], np.arange(3), 0.09, torch.float32)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8", "fp8", "int4"])
+@pytest.mark.parametrize("longest", [4096, 4097])     # 16 tiles of many rows, and one more
+def test_weights_of_many_rows_and_tiles(kv, longest):
+    lens, runs, H, Hkv, d = [longest, 300, 0, 31], [21, 40, 0, 1], 8, 2, 64 if kv == "fp8" else 128
+    cache, tables, src = filled(longest, kv, lens, Hkv, d)
+    q = torch.randn((sum(runs), H, d), generator=torch.Generator().manual_seed(3)).to(src)
+    before = torch.rand((4, Hkv, longest), device="cuda")
+    out, qsl = accumulate(cache, tables, lens, runs, q, d ** -0.5, before, longest)
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
+    check_weights(out, cache, tables, lens, qsl, q, d ** -0.5, before, longest)
 
 
 # num_blocks whose K alone passes 4 GB: 16 tokens x 8 heads x 128 elements a block
