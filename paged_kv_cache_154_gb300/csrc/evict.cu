@@ -136,8 +136,8 @@ __device__ __forceinline__ void load4(const int32_t* p, int (&v)[4], int j, int 
 // issue slots for long ones: keys are read four at a time, the counting walk
 // counts in registers, and the scan is one for 128 slots. A walk of 32 slots at a
 // time with ballots took 43 us for 131072 tokens of 8 heads on 64 SMs, 274
-// instructions for 32 slots; clusters of 16 took 85 us, their barriers and remote
-// reads outweigh the halved parts. Digits are 11 bits: the first holds the
+// instructions for 32 slots, where pieces of 128 take 30 us; clusters of 16 took 85
+// us, their barriers and remote reads outweigh the halved parts. Digits are 11 bits: the first holds the
 // exponent and two more bits, so that like-sized scores spread over the
 // histogram. Protected keys are above every score, so a first digit that falls on
 // theirs ends the search.
@@ -477,7 +477,8 @@ constexpr int kMoveAhead = 4;   // copies on the way together, per warp: 8 were 
 // zero points; then the warp copies the moves' K and V rows in 16-byte vectors,
 // 32 / (2 VECS) moves at a time and kMoveAhead such loads on the way before the
 // first store (no destination is a source, so the order is free). Bound by
-// memory: each row in and out, in pieces of 256 bytes and less that lie apart.
+// memory: each row in and out, in pieces of 256 bytes and less that lie apart; 24
+// thousand moves of 8 heads (bf16, d = 128) run at 84 % of the copy rate.
 template <int VECS, int GROUPS>   // 16-byte vectors and scales of a row
 __global__ void __launch_bounds__(32 * kMoveWarps) move_tokens_kernel(const MoveParams p) {
     constexpr int kPieces = 2 * VECS, kMoves = 32 / kPieces;   // moves of one warp-wide copy

@@ -32,9 +32,15 @@
 // fragment is 4 dims of 2 tokens: every masked nibble pair is an operand
 // register, with no byte shuffles. P^T gets its operand layout from movmatrix.
 //
-// Work split: the balanced schedule (balanced.cuh) with the per-warp layout of
-// the FP8 kernel: every warp streams its own share through its own ring; 8 or 16
-// query rows per tile, further rows as further chunks.
+// Work split: the balanced schedule (balanced.cuh): every warp streams its own
+// share through its own stages; 8 or 16 query rows per tile, further rows as
+// further chunks. Contexts of at most kWholeTokens are not cut.
+//
+// Measured, whole calls: 64 sequences of 512-4096 tokens, 32 query heads over 8
+// (157 MB) 37.4 us, 4.2 TB/s; 4 sequences of 32768-131072 (324 MB) 63.2 us, 5.1
+// TB/s, 75 % of the copy rate; a verify step of 16 to 40 rows per KV head (74 MB)
+// 50.2 us. A block of 16 tokens takes 245 instructions, of which 70 mask, and the
+// schedulers issue 0.57 a cycle.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -52,7 +58,7 @@ namespace {
 using pa::sched::kBS;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyMax = 8.f;    // base-2 headroom before the running max is moved
-constexpr int kWholeTokens = 256;
+constexpr int kWholeTokens = 256;  // a warp walks them in the time of the merge's launch
 // Warps of a CTA and CTAs of an SM, as many as the registers allow. One CTA of 12
 // warps: its warps run at one pace, where of three CTAs of 4 the older ones ran ahead
 // (a loop of 85, 98 and 113 thousand cycles for the same number of blocks) and left the
