@@ -126,6 +126,18 @@ __device__ __forceinline__ void load4(const int32_t* p, int (&v)[4], int j, int 
     }
 }
 
+// Of four bits a lane: how many are set in the lanes below, and in all of them.
+__device__ __forceinline__ int before_lane(uint32_t bits, int lane, int& total) {
+    int below = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t m = __ballot_sync(0xffffffffu, bits >> i & 1u);
+        below += __popc(m & ((1u << lane) - 1u));
+        total += __popc(m);
+    }
+    return below;
+}
+
 // A cluster of CTAs a (KV head, sequence), each CTA a contiguous part of the row
 // (CL CTAs; 1: no cluster), each warp a contiguous range of that in pieces of 128
 // slots, four a lane. One pass over scores and positions leaves keys in shared
@@ -136,7 +148,7 @@ __device__ __forceinline__ void load4(const int32_t* p, int (&v)[4], int j, int 
 // issue slots for long ones: keys are read four at a time, the counting walk
 // counts in registers, and the scan is one for 128 slots. A walk of 32 slots at a
 // time with ballots took 43 us for 131072 tokens of 8 heads on 64 SMs, 274
-// instructions for 32 slots, where pieces of 128 take 30 us; clusters of 16 took 85
+// instructions for 32 slots, where pieces of 128 take 28 us; clusters of 16 took 85
 // us, their barriers and remote reads outweigh the halved parts. Digits are 11 bits: the first holds the
 // exponent and two more bits, so that like-sized scores spread over the
 // histogram. Protected keys are above every score, so a first digit that falls on
@@ -210,14 +222,22 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
         float w[4];
         int pos[4];
         read4(j, w, pos);
-        uint32_t k[4];
+        uint32_t k[4], top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             k[i] = j + i < j1 ? row.key(pos[i], w[i]) : 0u;
-            // protected tokens come in long runs: one addition for a warp's
-            const uint32_t safe = __ballot_sync(0xffffffffu, k[i] == kProtected);
-            if (j + i < j1 && (k[i] != kProtected || lane == __ffs(safe) - 1))
-                atomicAdd(hist + (k[i] >> 21), k[i] == kProtected ? (uint32_t)__popc(safe) : 1u);
+            top = max(top, k[i]);
+        }
+        if (b + kPiece <= j1 && !__any_sync(0xffffffffu, top == kProtected)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) atomicAdd(hist + (k[i] >> 21), 1u);
+        } else {                         // protected tokens come in long runs: one addition for a warp's
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t safe = __ballot_sync(0xffffffffu, k[i] == kProtected);
+                if (j + i < j1 && (k[i] != kProtected || lane == __ffs(safe) - 1))
+                    atomicAdd(hist + (k[i] >> 21), k[i] == kProtected ? (uint32_t)__popc(safe) : 1u);
+            }
         }
         if (KEYS) *reinterpret_cast<uint4*>(keys + (j - a0)) = make_uint4(k[0], k[1], k[2], k[3]);
     }
@@ -385,29 +405,19 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
             eq |= (uint32_t)(k[i] == cut && j + i < j1) << i;
         }
         if (__any_sync(0xffffffffu, eq)) {             // ties: the first `ties` of the row stay
-            int run = __popc(eq);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += y;
-            }
-            int mine = eq_before + run - __popc(eq);
+            int total = 0;
+            int mine = eq_before + before_lane(eq, lane, total);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (eq >> i & 1u) {
                     keep |= (uint32_t)(mine < ties) << i;
                     ++mine;
                 }
-            eq_before += __shfl_sync(0xffffffffu, run, 31);
+            eq_before += total;
         }
-        int run = __popc(keep);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += y;
-        }
-        int rank = kept + run - __popc(keep);          // kept tokens before the lane's slots
-        kept += __shfl_sync(0xffffffffu, run, 31);
+        int total = 0;
+        int rank = kept + before_lane(keep, lane, total);   // kept tokens before the lane's slots
+        kept += total;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool stays = keep >> i & 1u;
@@ -416,20 +426,27 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
             rank += stays;
         }
     }
-    // The slots below n as they are; those of evicted tokens are written again below.
-    const int jn = min(j1, n);
-    for (int b = j0; b < jn; b += kPiece) {
-        const int j = b + 4 * lane;
+    // The slots below n as they are, shared by the row's CTAs; those of evicted tokens are
+    // written again below. Keys come from shared memory by now, so that nobody reads what
+    // this writes (a part whose keys are computed again copies its own slots).
+    const int share = KEYS ? ((n + CL - 1) / CL + 3) / 4 * 4 : 0;
+    const int c0 = KEYS ? min(n, part * share) + 4 * tid : min(j0, n) + 4 * lane;
+    const int c1 = KEYS ? min(n, (part + 1) * share) : min(j1, n);
+#pragma unroll 2
+    for (int j = c0; j < c1; j += KEYS ? 4 * T : kPiece) {
         float w[4];
         int pos[4];
-        read4(j, w, pos);
-        if (aligned && j + 4 <= jn) {
+        load4(row.w, w, j, c1 - j, aligned);
+        if (row.pos) load4(row.pos, pos, j, c1 - j, aligned);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pos[i] = row.pos && pos[i] >= 0 ? pos[i] : row.shift + j + i;
+        if (aligned && j + 4 <= c1) {
             *reinterpret_cast<float4*>(w_out + j) = make_float4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<int4*>(pos_out + j) = make_int4(pos[0], pos[1], pos[2], pos[3]);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (j + i < jn) w_out[j + i] = w[i], pos_out[j + i] = pos[i];
+                if (j + i < c1) w_out[j + i] = w[i], pos_out[j + i] = pos[i];
         }
     }
     sync();                                            // the list is whole
