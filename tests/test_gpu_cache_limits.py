@@ -39,6 +39,31 @@ def test_lengths_around_the_uncut_limit(lens, runs, H, Hkv, d):
     check(got, q, cache, tables, lens, qsl, d ** -0.5, torch.float32)
 
 
+@pytest.mark.parametrize("lens,runs,H,Hkv,d", [
+    ([257 + 7 * i % 90 for i in range(250)], [1] * 250, 16, 8, 64),      # more segments than workers
+    ([260 + 11 * i % 60 for i in range(70)], [5, 1] * 35, 64, 8, 128),   # and of two row chunks
+    ([300, 40000, 1], [1, 1, 1], 8, 2, 128),                             # hundreds of pieces
+    ([3000, 25, 17], [40, 2, 3], 8, 2, 64),
+])
+def test_cut_segments_merge_inside_their_workspace(lens, runs, H, Hkv, d):
+    """However a call is cut: right answers, and nothing written past the workspace
+    and the output, whatever the workspace held before."""
+    cache, tables, qsl, q = sequences(len(lens), lens, runs, H, Hkv, d, torch.bfloat16, junk=False)
+    size = pa.decode_workspace_size(len(lens), q.shape[0], H, Hkv, d, max(runs), max(lens))
+    ws = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws[:pa.ARRIVAL_BYTES] = 0
+    out = torch.full((q.shape[0] + 8, H, d), 7.0, device="cuda")
+    pa.decode(out[:q.shape[0]], q.cuda(), cache.k, cache.v, torch.from_numpy(tables).cuda(),
+              torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens), d ** -0.5,
+              torch.from_numpy(qsl).cuda() if max(runs) > 1 else None, max(runs),
+              cache.num_blocks, cache.k_scale, cache.v_scale, cache.k_zp, cache.v_zp, 0, ws[:size])
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
+    assert (ws[size:] == 0xA5).all() and (out[q.shape[0]:] == 7).all()
+    assert (ws[:pa.ARRIVAL_BYTES] == 0).all()
+    check(out[:q.shape[0]], q, cache, tables, lens, qsl, d ** -0.5, torch.float32)
+
+
 @pytest.mark.parametrize("long", [100, 900])
 def test_rows_of_empty_sequences_are_left_as_they_were(long):
     lens, runs = [0, long, 0, 33, 0], [1] * 5
