@@ -261,3 +261,25 @@ def test_workspace_sizes():
     assert logits < f(2, 2, 8, 2, 64, 1, 600) < 1.1 * logits
     # more rows than are stored: sums of the rows' tiles alone, not 8 bytes a row and token
     assert 0 < f(2, 64, 8, 2, 64, 32, 600) < 2 * 2 * 128 * 600
+
+
+def test_engine_refuses_evictions_before_anything_moves():
+    from paged_kv_cache_154_gb300.engine import PagedKVCache
+    cache = PagedKVCache(8, 2, 64, "bf16", device="cpu")     # nothing below reaches a GPU
+    names = {}
+    for name, n in (("a", 40), ("b", 20)):
+        names[name] = cache.pool.seq_create()
+        cache.pool.seq_append_slots(names[name], n)
+    before = cache.pool.stats()
+    tw = cache.track_weights(["a", "b"], 40)
+    with pytest.raises(ValueError, match="negative"):
+        cache.evict(tw, names, [10, -1])
+    with pytest.raises(ValueError, match="twice"):
+        cache.evict(cache.track_weights(["a", "a"], 40), names, 10)
+    with pytest.raises(ValueError, match="holds 40 tokens"):
+        cache.evict(cache.track_weights(["a", "b"], 39), names, 10)
+    with pytest.raises(KeyError):
+        cache.evict(cache.track_weights(["c"], 40), names, 10)
+    cache.evict(tw, names, 40)                               # nothing is over its budget
+    assert [cache.pool.seq_len(i) for i in names.values()] == [40, 20]
+    assert cache.pool.stats() == before and not tw.evicted.any()
