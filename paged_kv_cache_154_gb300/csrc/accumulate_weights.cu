@@ -26,8 +26,8 @@
 // product, and as the order of the dims is free (q is loaded in the same order), a
 // lane's 16-byte load of its token is four operand registers with no staging in
 // shared memory. The Llama-3-8B-shaped step (64 sequences of 512-4096 tokens, bf16,
-// 325 MB) takes 64.4 us: 54 us at 82 % of the copy rate, and the sum; one 4-bit sequence
-// of 100001 tokens (66 MB) 26.7 us, where the chain of a block counts as much as its
+// 325 MB) takes 63.2 us: 54 us at 82 % of the copy rate, and the sum; one 4-bit sequence
+// of 100001 tokens (66 MB) 24.5 us, where the chain of a block counts as much as its
 // bytes. For many rows it is the latency of load, product and exponential: a tile of
 // K is staged in shared memory once, for warps of 16 rows of q each.
 // Codes are made exact in fp16: code - zero point (INT8), E4M3 to fp16, masked
@@ -480,11 +480,14 @@ __device__ __forceinline__ int block_of(const Params& p, int s, int i) {
 // Grid: (tiles of p.tile_tokens tokens, KV head, sequence): few rows, stored logits.
 template <int KV, int D, int NR>
 __global__ void __launch_bounds__(kWarps * 32) logits_kernel(const Params p) {
-    // blocks of K in registers, on their way while one is multiplied
-    constexpr int kDepth = KRows<KV, D>::kWords >= 16 ? 2 : 4;
+    // blocks of K in registers, on their way while one is multiplied (of 16-bit rows of 128,
+    // 2: 64.1 us for the Llama-3-8B-shaped step, 3: 63.2; of smaller rows 5 are no better)
+    constexpr int kDepth = KRows<KV, D>::kWords >= 16 ? 3 : 4;
     __shared__ float2 part[kWarps][8 * NR];
-    pa::grid_dependents_launch();
+    // let the sum's kernel in only now: what ran before this one has ended, and that kernel
+    // reads its inputs before it waits
     pa::grid_dependency_wait();
+    pa::grid_dependents_launch();
     const int s = blockIdx.z, g = blockIdx.y, tile = blockIdx.x;
     const Seq sq(p, s);
     const int rows = p.group * sq.r;
@@ -577,15 +580,20 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const Params p) {
 }
 
 // Grid: (tiles of kOutTokens tokens, KV head, sequence). RP: the rows a token
-// has in the stored logits.
+// has in the stored logits. Bound by latency (lengths, logits and row sums, output):
+// the lengths and the weights so far are read before the logits are complete, and up to
+// 6 CTAs share an SM (one 4-bit sequence of 100001 tokens: 24.5 us a call, 26.0 with 4
+// CTAs, 26.5 without the early reads either).
 template <int RP>
-__global__ void __launch_bounds__(256) stored_kernel(const Params p) {
+__global__ void __launch_bounds__(256, RP <= 4 ? 6 : RP == 8 ? 3 : 2) stored_kernel(const Params p) {
     __shared__ float2 sum[RP];
-    pa::grid_dependency_wait();
     const int s = blockIdx.z, g = blockIdx.y;
     const Seq sq(p, s);
     const int t0 = blockIdx.x * kOutTokens;
-    if (t0 >= sq.L) return;
+    if (t0 >= sq.L) {
+        pa::grid_dependency_wait();
+        return;
+    }
     const int64_t sg = (int64_t)s * p.num_kv_heads + g;
     const int rows = p.group * sq.r;
     const int64_t base = sg * p.stride;
@@ -595,8 +603,13 @@ __global__ void __launch_bounds__(256) stored_kernel(const Params p) {
     for (int i = 0; i < kEach; ++i) {
         const int t = t0 + i * 256 + threadIdx.x;
         before[i] = 0.f;
+        if (t < sq.L && p.in) before[i] = __ldcg(p.in + base + t);
+    }
+    pa::grid_dependency_wait();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int t = t0 + i * 256 + threadIdx.x;
         if (t >= sq.L) continue;
-        if (p.in) before[i] = p.in[base + t];
         if (rows > 0) {
             const float* src = p.logits + (sg * p.tokens_pad + t) * RP;
             if constexpr (RP >= 4) {
