@@ -499,7 +499,7 @@ extern "C" pa_status pa_decode(void* out, pa_dtype out_dtype, const void* q, pa_
                                             align256(rows * sizeof(float)));
     }
     a.stream = st;
-    return pa::launch_decode(a);
+    return kv_dtype == PA_INT4 ? pa::launch_decode_int4(a) : pa::launch_decode(a);
 }
 
 static_assert(PA_DEVERR_WAIT_FULL == pa::ERR_WAIT_FULL && PA_DEVERR_WAIT_EMPTY == pa::ERR_WAIT_EMPTY &&

@@ -184,7 +184,8 @@ struct DecodeArgs {
     int max_workers;           // balanced 16-bit decode: at most this many worker warps (0: none)
     cudaStream_t stream;
 };
-pa_status launch_decode(const DecodeArgs& a);
+pa_status launch_decode(const DecodeArgs& a);        // every cache type but INT4
+pa_status launch_decode_int4(const DecodeArgs& a);   // INT4 caches
 
 // TMA tensor map of a cache ([num_blocks][num_kv_heads][16][head_dim] of
 // elem_bytes-byte elements), cached per (pointer, shape, device)

@@ -1281,7 +1281,6 @@ namespace pa {
 
 pa_status launch_decode_int8(const DecodeArgs& a);
 pa_status launch_decode_fp8(const DecodeArgs& a);
-pa_status launch_decode_int4(const DecodeArgs& a);
 bool prefill_tc_applies(const DecodeArgs& a);
 pa_status launch_prefill_tc(const DecodeArgs& a);
 bool prefix_tc_applies(const DecodeArgs& a);
@@ -1289,14 +1288,12 @@ pa_status launch_prefix_tc(const DecodeArgs& a);
 
 pa_status launch_decode(const DecodeArgs& a) {
     if ((a.ctx_start || a.lse_out || a.unmasked) &&
-        (a.kv_dtype == PA_INT8 || a.kv_dtype == PA_FP8_E4M3 || a.kv_dtype == PA_INT4 ||
-         a.partition_size))
+        (a.kv_dtype == PA_INT8 || a.kv_dtype == PA_FP8_E4M3 || a.partition_size))
         return fail(PA_ERR_UNSUPPORTED,
                     "token offsets, log-sum-exp output and unmasked rows need a 16-bit cache and "
                     "the balanced schedule");
     if (a.kv_dtype == PA_INT8) return launch_decode_int8(a);
     if (a.kv_dtype == PA_FP8_E4M3) return launch_decode_fp8(a);
-    if (a.kv_dtype == PA_INT4) return launch_decode_int4(a);
     if (prefill_tc_applies(a)) return launch_prefill_tc(a);
     if (prefix_tc_applies(a)) return launch_prefix_tc(a);
     if (a.partition_size > kMaxPartBlocks * kBS)
