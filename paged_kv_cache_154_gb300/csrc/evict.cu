@@ -486,16 +486,19 @@ struct MoveParams {
 };
 
 constexpr int kMoveWarps = 4;
-constexpr int kMoveAhead = 4;   // copies on the way together, per warp: 8 were slower (80 us
-                                // against 70 with the selection of 131072 tokens), 2 too (74)
+constexpr int kMoveAhead = 4;   // copies on the way together, per warp: 8 were slower (67.5 us
+                                // against 64.5 with the selection of 131072 tokens), 2 too
+                                // (68.0), and so were loads ahead of the last stores (69)
 
 // Grid: (parts, KV head, sequence); the warps of all parts share the row's moves.
 // A lane looks up one move (its slots, their blocks) and copies its scales and
 // zero points; then the warp copies the moves' K and V rows in 16-byte vectors,
 // 32 / (2 VECS) moves at a time and kMoveAhead such loads on the way before the
 // first store (no destination is a source, so the order is free). Bound by
-// memory: each row in and out, in pieces of 256 bytes and less that lie apart; 24
-// thousand moves of 8 heads (bf16, d = 128) run at 84 % of the copy rate.
+// memory: each row in and out, in pieces of 256 bytes and less that lie apart; 25
+// thousand moves of each of 8 heads (bf16, d = 128, 206 MB in and out) take 35 us
+// alone. Caching loads rather than streaming ones: 63.3 us against 64.5 with the
+// selection of 131072 tokens; a row's address from one base a lane: 64.5 against 68.6.
 template <int VECS, int GROUPS>   // 16-byte vectors and scales of a row
 __global__ void __launch_bounds__(32 * kMoveWarps) move_tokens_kernel(const MoveParams p) {
     constexpr int kPieces = 2 * VECS, kMoves = 32 / kPieces;   // moves of one warp-wide copy
@@ -514,7 +517,12 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_tokens_kernel(const Move
     const int turns = max(1, (count + 32 * warps - 1) / (32 * warps));
     const int per = max(1, (count + turns * warps - 1) / (turns * warps));
     const int v = lane % kPieces >= VECS, c = lane % kPieces - v * VECS;
-    uint4* const code = p.code[v];
+    // the lane's vector of row 0 of the KV head's tile in block 0
+    uint4* const code = (v ? p.code[1] : p.code[0]) + (int64_t)g * kBS * VECS + c;
+    const uint32_t block_vecs = (uint32_t)p.num_kv_heads * kBS * VECS;
+    auto vec_at = [&](int blk, int off) {
+        return code + ((uint64_t)(uint32_t)blk * block_vecs + off * VECS);
+    };
     for (int64_t m0 = (int64_t)(blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * per; m0 < count;
          m0 += (int64_t)warps * per) {
         const int here = (int)min((int64_t)per, count - m0);
@@ -550,19 +558,20 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_tokens_kernel(const Move
         }
         for (int i0 = 0; i0 < here; i0 += kMoves * kMoveAhead) {
             uint4 data[kMoveAhead];
-            int to[kMoveAhead], off[kMoveAhead];
+            uint4* to[kMoveAhead];
 #pragma unroll
             for (int k = 0; k < kMoveAhead; ++k) {
                 const int m = i0 + k * kMoves + lane / kPieces;   // past the last: lanes with bs = -1
                 const int from = __shfl_sync(0xffffffffu, bs, m & 31);
-                to[k] = __shfl_sync(0xffffffffu, bd, m & 31);
-                off[k] = __shfl_sync(0xffffffffu, at, m & 31);
-                if (m >= here || from < 0) to[k] = -1;
-                if (to[k] >= 0) data[k] = __ldcs(code + row_of(from, off[k] & 15) * VECS + c);
+                const int dst = __shfl_sync(0xffffffffu, bd, m & 31);
+                const int off = __shfl_sync(0xffffffffu, at, m & 31);
+                const bool on = m < here && from >= 0;
+                to[k] = on ? vec_at(dst, off >> 4) : nullptr;
+                if (on) data[k] = *vec_at(from, off & 15);
             }
 #pragma unroll
             for (int k = 0; k < kMoveAhead; ++k)
-                if (to[k] >= 0) code[row_of(to[k], off[k] >> 4) * VECS + c] = data[k];
+                if (to[k]) *to[k] = data[k];
         }
     }
 }
