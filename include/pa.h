@@ -285,12 +285,12 @@ pa_status pa_append_kv(const void* key, const void* value, pa_dtype src_dtype,
  * key, value [num_tokens][num_kv_heads][head_dim] of out_dtype (F16, BF16 or
  * F32) receive the K and V rows of slot_mapping[t] (any cache type; the value
  * of a code, one fp32 product, is rounded once more to a 16-bit out_dtype; a
- * 16-bit cache read as its own type is a bit copy). For attention computed outside the cache that
- * must see what the cache holds (the queries of a prompt whose K/V were just
- * quantised), for moving tokens between caches of different types, and for
- * writing a sequence out. A negative slot leaves its row of key and value as
- * it was; slots may repeat. key, value and the caches are 16-byte aligned;
- * scales and zero points as for pa_append_kv. */
+ * 16-bit cache read as its own type is a bit copy). For attention computed
+ * outside the cache that must see what the cache holds (the queries of a prompt
+ * whose K/V were just quantised), for moving tokens between caches of different
+ * types, and for writing a sequence out. A negative slot leaves its row of key
+ * and value as it was; slots may repeat. key, value and the caches are 16-byte
+ * aligned; scales and zero points as for pa_append_kv. */
 pa_status pa_gather_kv(void* key, void* value, pa_dtype out_dtype,
                        const void* k_cache, const void* v_cache,
                        pa_dtype kv_dtype, const float* k_scale,
@@ -500,8 +500,9 @@ pa_status pa_decode_shared_prefix(
  * pa_seq_make_private on the pool and before pa_seq_truncate. ---- */
 
 /* Bytes of workspace pa_accumulate_weights needs for these sizes (0 for invalid
- * sizes and for more than a call may have); at least 256-byte aligned, needs no initialisation, and may be shared
- * by calls of one stream. Host-only: needs no GPU. */
+ * sizes and for more than a call may have); at least 256-byte aligned, needs no
+ * initialisation, and may be shared by calls of one stream. Host-only: needs no
+ * GPU. */
 size_t pa_accumulate_weights_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
                                             int32_t num_heads, int32_t num_kv_heads,
                                             int32_t head_dim, int32_t max_q_len,

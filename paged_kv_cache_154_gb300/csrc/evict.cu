@@ -149,8 +149,8 @@ __device__ __forceinline__ int before_lane(uint32_t bits, int lane, int& total) 
 // counts in registers, and the scan is one for 128 slots. A walk of 32 slots at a
 // time with ballots took 43 us for 131072 tokens of 8 heads on 64 SMs, 274
 // instructions for 32 slots, where pieces of 128 take 28 us; clusters of 16 took 85
-// us, their barriers and remote reads outweigh the halved parts. Digits are 11 bits: the first holds the
-// exponent and two more bits, so that like-sized scores spread over the
+// us, their barriers and remote reads outweigh the halved parts. Digits are 11 bits:
+// the first holds the exponent and two more bits, so that like-sized scores spread over the
 // histogram. Protected keys are above every score, so a first digit that falls on
 // theirs ends the search.
 template <int CL, int T, bool KEYS>   // CTAs a row, threads a CTA
@@ -231,12 +231,13 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const SelectParams p) {
         if (b + kPiece <= j1 && !__any_sync(0xffffffffu, top == kProtected)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) atomicAdd(hist + (k[i] >> 21), 1u);
-        } else {                         // protected tokens come in long runs: one addition for a warp's
+        } else {                         // protected tokens come in runs: one addition a warp
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t safe = __ballot_sync(0xffffffffu, k[i] == kProtected);
                 if (j + i < j1 && (k[i] != kProtected || lane == __ffs(safe) - 1))
-                    atomicAdd(hist + (k[i] >> 21), k[i] == kProtected ? (uint32_t)__popc(safe) : 1u);
+                    atomicAdd(hist + (k[i] >> 21),
+                              k[i] == kProtected ? (uint32_t)__popc(safe) : 1u);
             }
         }
         if (KEYS) *reinterpret_cast<uint4*>(keys + (j - a0)) = make_uint4(k[0], k[1], k[2], k[3]);
@@ -550,11 +551,13 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_tokens_kernel(const Move
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < GROUPS; ++j) sc[i][j] = p.scale[i][src + j], zp[i][j] = p.zp[i][src + j];
+                for (int j = 0; j < GROUPS; ++j)
+                    sc[i][j] = p.scale[i][src + j], zp[i][j] = p.zp[i][src + j];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < GROUPS; ++j) p.scale[i][dst + j] = sc[i][j], p.zp[i][dst + j] = zp[i][j];
+                for (int j = 0; j < GROUPS; ++j)
+                    p.scale[i][dst + j] = sc[i][j], p.zp[i][dst + j] = zp[i][j];
         }
         for (int i0 = 0; i0 < here; i0 += kMoves * kMoveAhead) {
             uint4 data[kMoveAhead];

@@ -222,12 +222,12 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
 // INT4 append: the formula of the INT8 path with 16 unsigned codes and one
 // (scale, zero point) per 64 elements. 8 threads a row; a thread holds 8
 // consecutive elements of every group of the K row and of the same V row (16-byte
-// loads, 4-byte code stores), and a group's range is reduced over the 8 with shuffles. 2 bytes in and 0.58 out
-// an element: bound by instruction issue before memory, so indexes are 32 bits wide
+// loads, 4-byte code stores), and a group's range is reduced over the 8 with
+// shuffles. 2 bytes in and 0.58 out an element: bound by instruction issue before memory, so indexes are 32 bits wide
 // (their 64-bit divisions alone cost a third of the kernel), a thread's index
 // arithmetic serves every group of a row, and quotients come from one reciprocal a
 // group; the rows are asked for before the slot is known. 16384 tokens of 8 heads of
-// 128 elements, with the gather that reads them back: 33.5 us, 37.3 us with a thread a
+// 128 elements, with the gather that reads them back: 32.8 us, 37.3 us with a thread a
 // group, 59 us with a division an element.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) append_kv_int4_kernel(
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(256) append_kv_int4_kernel(
                 word |= (uint32_t)(q < 0 ? 0 : min(15, q)) << (4 * e);
             }
         }
-        reinterpret_cast<uint32_t*>(which ? v_cache : k_cache)[row * (8 * kGroups) + 8 * j + c] = word;
+        reinterpret_cast<uint32_t*>(which ? v_cache : k_cache)[(row * kGroups + j) * 8 + c] = word;
         if (c == 0) {
             (which ? v_scale : k_scale)[row * kGroups + j] = scale;
             (which ? v_zp : k_zp)[row * kGroups + j] = (int8_t)zp;
@@ -378,10 +378,24 @@ __device__ __forceinline__ void store8(T* dst, const Cached8<KV, D>& x) {
     uint4 out = x.raw;   // a 16-bit cache read as its own type
     if constexpr (KV != (half ? PA_F16 : PA_BF16)) {
         T* h = reinterpret_cast<T*>(&out);
+        if constexpr (KV == PA_INT4) {   // value(), two at a time
+            const float zero = -(8388608.0f + (float)x.zp);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (half) h[e] = __float2half_rn(x.value(e));
-            else h[e] = __float2bfloat16_rn(x.value(e));
+            for (int e = 0; e < 8; e += 2) {
+                const F2 code(__uint_as_float((x.raw.x >> (4 * e) & 15u) | 0x4b000000u),
+                              __uint_as_float((x.raw.x >> (4 * e + 4) & 15u) | 0x4b000000u));
+                const F2 v = (code + F2(zero, zero)) * F2(x.scale, x.scale);
+                if constexpr (half)
+                    *reinterpret_cast<__half2*>(h + e) = __floats2half2_rn(v.lo(), v.hi());
+                else
+                    *reinterpret_cast<__nv_bfloat162*>(h + e) = __floats2bfloat162_rn(v.lo(), v.hi());
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if constexpr (half) h[e] = __float2half_rn(x.value(e));
+                else h[e] = __float2bfloat16_rn(x.value(e));
+            }
         }
     }
     __stcs(reinterpret_cast<uint4*>(dst), out);
@@ -389,7 +403,8 @@ __device__ __forceinline__ void store8(T* dst, const Cached8<KV, D>& x) {
 
 // Cached rows read back through a slot mapping: the inverse of append, each
 // row at the values the cache holds. 8 threads a row; a thread has 8 elements of
-// every 64 of the K row and of the same V row. Bound by memory: the cache's bytes in, the rows out.
+// every 64 of the K row and of the same V row. The streaming loads and stores here
+// and in the append are worth 3 us of 36. Bound by memory: the cache's bytes in, the rows out.
 template <int KV, int D, typename T>
 __global__ void __launch_bounds__(256) gather_kv_kernel(
     T* __restrict__ key, T* __restrict__ value, const void* __restrict__ k_cache,

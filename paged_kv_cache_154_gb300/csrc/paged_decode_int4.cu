@@ -939,7 +939,8 @@ pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, Q4Extra x)
     constexpr int kWorkerWarps = worker_warps(D, NR);
     auto kern = paged_decode_int4_kernel<TQ, D, NR>;
     static std::atomic<uint64_t> allowed{0};
-    if (pa_status s = pa::allow_smem(kern, Lay::smem_bytes(pa::kBalancedMaxSeqs, kWorkerWarps), allowed,
+    if (pa_status s = pa::allow_smem(kern, Lay::smem_bytes(pa::kBalancedMaxSeqs, kWorkerWarps),
+                                     allowed,
                                      "int4 decode: set shared memory size"))
         return s;
     const int smem = Lay::smem_bytes(a.num_seqs, kWorkerWarps);
@@ -978,7 +979,8 @@ pa_status launch_int4(const pa::DecodeArgs& a, pa::sched::Params prm, Q4Extra x)
     int64_t workers = segments;
     if (!x.whole) {
         workers = std::min((int64_t)ctas * sms * kWorkerWarps, shape.virtual_blocks);
-        const int64_t record_bytes = (std::min(segments, workers) * (int64_t)sizeof(MergeRecord) + 255) / 256 * 256;
+        const int64_t record_bytes =
+            (std::min(segments, workers) * (int64_t)sizeof(MergeRecord) + 255) / 256 * 256;
         x.records = reinterpret_cast<MergeRecord*>(prm.slots);
         prm.slots += record_bytes;
         const int64_t room = shape.workspace_bytes - shape.cum_bytes - record_bytes;
