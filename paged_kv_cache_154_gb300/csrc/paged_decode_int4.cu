@@ -885,14 +885,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::
         const float l = __ldcg(sl.l + row), m = __ldcg(sl.m + row);
         if (m == -INFINITY && l == 0.f) continue;
         const float top = fmaxf(M, m);
-        den = den * exp2f(M - top) + l * exp2f(m - top);
+        den = den * pa::ex2(M - top) + l * pa::ex2(m - top);
         M = top;
     }
     {
         float top = M;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        den *= M == -INFINITY ? 1.f : exp2f(M - top);
+        den *= M == -INFINITY ? 1.f : pa::ex2(M - top);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
         M = top;
@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
             if (i0 + j * wpr >= np || w[j] == -INFINITY) continue;
-            const float f = exp2f(w[j] - M);
+            const float f = pa::ex2(w[j] - M);
 #pragma unroll
             for (int e = 0; e < EPL; ++e) acc[e] = fmaf(f, v[j][e], acc[e]);
         }
