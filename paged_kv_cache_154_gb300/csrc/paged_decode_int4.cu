@@ -13,8 +13,8 @@
 // O the sum over tokens of P vs vz, one product more). A masked pair of codes IS
 // an fp16 pair: a code in bits 0-3 of a half is the subnormal c * 2^-24, in bits
 // 4-7 c * 2^-20, both exact, and the tensor cores multiply subnormals like any
-// number; so a word of 8 codes costs one shift and four masks (four instructions
-// for V), and no conversion. The powers of two go into q, the output and the row's scale. q
+// number; so a word of 8 codes costs one shift and four masks, and no
+// conversion. The powers of two go into q, the output and the row's scale. q
 // goes to fp16 after an exact power-of-two scaling per row, the V scale is
 // folded into P against a running power-of-two reference per group, so the fp16
 // P never exceeds the softmax weight (at most 2^8 under the lazily moved
@@ -127,16 +127,6 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&n)[4]) {
     n[1] = w & 0x00f000f0u;
     n[2] = h & 0x000f000fu;
     n[3] = h & 0x00f000f0u;
-}
-
-// The same words for V, whose pairs are different outputs: n[1] and n[3] hold both codes of
-// a byte, low + 16 high in units of 2^-24 (at most 255: exact), and the low ones' sums come
-// off at the end. An instruction less a word.
-__device__ __forceinline__ void unpack_v(uint32_t w, uint32_t (&n)[4]) {
-    n[0] = w & 0x000f000fu;
-    n[1] = w & 0x00ff00ffu;
-    n[3] = prmt(w, 0u, 0x4341u);
-    n[2] = n[3] & 0x000f000fu;
 }
 
 // smallest e with 2^e >= x, for a positive finite x (x = 0 gives -126)
@@ -557,12 +547,11 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
                 }
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    // dims 4 quad, + 2; and 16 times dims 4 quad + 1, + 3 above them
+                    // dims 4 quad, + 2 count 2^-24, dims 4 quad + 1, + 3 count 2^-20
                     const float zc = z[c * GR / CH], mul = mulg[c * GR / CH];
-                    const float(&lo)[4] = o[nr][c][0], (&hi)[4] = o[nr][c][1];
                     const float4 v = make_float4(
-                        (lo[e] - zc) * mul, fmaf(lo[2 + e] - lo[e], 0.0625f, -zc) * mul,
-                        (hi[e] - zc) * mul, fmaf(hi[2 + e] - hi[e], 0.0625f, -zc) * mul);
+                        (o[nr][c][0][e] - zc) * mul, fmaf(o[nr][c][0][2 + e], 0.0625f, -zc) * mul,
+                        (o[nr][c][1][e] - zc) * mul, fmaf(o[nr][c][1][2 + e], 0.0625f, -zc) * mul);
                     const int col = 32 * c + 4 * quad;
                     if (!complete) {
                         *reinterpret_cast<float4*>(sl.o + (int64_t)row * D + col) = v;
@@ -776,8 +765,8 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     uint32_t lo[4], hi[4];
-                    unpack_v(rr[2 * j], lo);
-                    unpack_v(rr[2 * j + 1], hi);
+                    unpack(rr[2 * j], lo);
+                    unpack(rr[2 * j + 1], hi);
                     const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]};
                     const uint32_t a1[4] = {lo[2], lo[3], hi[2], hi[3]};
 #pragma unroll
