@@ -64,6 +64,25 @@ def test_cut_segments_merge_inside_their_workspace(lens, runs, H, Hkv, d):
     check(out[:q.shape[0]], q, cache, tables, lens, qsl, d ** -0.5, torch.float32)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_averages_of_long_contexts(d):
+    """Nearly even weights over a long context average values of either sign to
+    a hundredth of them, where errors of the accumulation would show. Weights are
+    rounded to fp16, off by at most 2^-11 and 2^-11 / sqrt(3) in the mean square;
+    the same weights make the output, so its error is that share of its norm,
+    for the elements of the low halves of bytes and for those of the high ones.
+    The rest of 2^-11 is left to the accumulation."""
+    lens, runs = [60_000], [1]
+    cache, tables, qsl, q = sequences(d, lens, runs, 16, 2, d, torch.bfloat16)
+    got = decode(cache, tables, lens, runs, qsl, q, torch.float32, 0.25 * d ** -0.5)
+    k, v = ref.cache_values(cache)
+    want = ref.attend(q.double().numpy(), k, v, tables, lens, qsl, 0.25 * d ** -0.5)
+    err = got.double().cpu().numpy() - want
+    for half in (0, 1):
+        e, w = err[..., half::2], want[..., half::2]
+        assert np.linalg.norm(e) <= 2.0 ** -11 * np.linalg.norm(w)
+
+
 @pytest.mark.parametrize("long", [100, 900])
 def test_rows_of_empty_sequences_are_left_as_they_were(long):
     lens, runs = [0, long, 0, 33, 0], [1] * 5
