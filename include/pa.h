@@ -374,7 +374,8 @@ size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
  *                  each region starting on a 256-byte boundary. With
  *                  partition_size 0: partial slots, each int32 {sequence,
  *                  kv head, first token, end token} then fp32 m[R], l[R]
- *                  (base-2 units) and O[R][head_dim] (not normalised).
+ *                  (base-2 units) and O[R][head_dim] (not normalised; INT4
+ *                  caches: divided by l, R and their number the kernel's own).
  * INT4 caches: k_scale, v_scale, k_zp and v_zp are 16-byte aligned; at most
  * 4080 query rows per KV head (num_heads / num_kv_heads x max_q_len). Codes,
  * scales and zero points of slots past a context may hold anything. Softmax

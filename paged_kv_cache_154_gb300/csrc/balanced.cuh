@@ -68,8 +68,8 @@ __device__ __forceinline__ int first_block(const Params& p, int s) {
 
 
 // A partial slot: int32 {seq, kv head, chunk, first token, end token, 0, 0, 0},
-// then fp32 m[RT] (base-2 units), l[RT], O[RT][D] (not normalised). Row j of a
-// slot is query row chunk*RT + j of the (sequence, kv head).
+// then fp32 m[RT] (base-2 units), l[RT], O[RT][D] (not normalised; INT4: divided
+// by l). Row j of a slot is query row chunk*RT + j of the (sequence, kv head).
 struct Slot {
     int32_t* hdr;
     float* m;

@@ -509,8 +509,10 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
         }
     };
 
-    // Segment end: the output rows (segment held whole) or the partial slot;
-    // O of group g is in units of the V-scale reference vref[g].
+    // Segment end: the output rows (segment held whole) or the partial slot, whose O is the
+    // average over the piece: a sum of values near the largest fp32 number would not be
+    // finite. O of group g is in units of the V-scale reference vref[g]; that comes last, as
+    // neither 2^24 vref nor vref / l need be a normal number.
     auto finish_segment = [&](bool complete, int slot_idx, int tok_end) {
         Slot sl(p.slots + (2 * wid + slot_idx) * (int64_t)p.slot_bytes, p.rows_per_tile);
         if (!complete && lane == 0) {
@@ -533,10 +535,8 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
                 for (int g = 0; g < GR; ++g) z[g] = __shfl_sync(0xffffffffu, oz[nr][g][e], qc);
                 const int row = 8 * nr + 2 * qc + e;
                 if (row >= rows) continue;
-                float mulg[GR];
-                const float inv = complete ? __fdividef(kUnit, l) : kUnit;
-#pragma unroll
-                for (int g = 0; g < GR; ++g) mulg[g] = vref[g] * inv;
+                // a piece that the row sees nothing of (l = 0) is marked by its m, its O not read
+                const float inv = __fdividef(kUnit, l);
                 int64_t obase = 0;
                 if (complete) {
                     const int gr = row_off + row, qi = query_of(gr);
@@ -548,10 +548,11 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     // dims 4 quad, + 2 count 2^-24, dims 4 quad + 1, + 3 count 2^-20
-                    const float zc = z[c * GR / CH], mul = mulg[c * GR / CH];
-                    const float4 v = make_float4(
-                        (o[nr][c][0][e] - zc) * mul, fmaf(o[nr][c][0][2 + e], 0.0625f, -zc) * mul,
-                        (o[nr][c][1][e] - zc) * mul, fmaf(o[nr][c][1][2 + e], 0.0625f, -zc) * mul);
+                    const float zc = z[c * GR / CH], ref = vref[c * GR / CH];
+                    const float4 v = make_float4((o[nr][c][0][e] - zc) * inv * ref,
+                                                 fmaf(o[nr][c][0][2 + e], 0.0625f, -zc) * inv * ref,
+                                                 (o[nr][c][1][e] - zc) * inv * ref,
+                                                 fmaf(o[nr][c][1][2 + e], 0.0625f, -zc) * inv * ref);
                     const int col = 32 * c + 4 * quad;
                     if (!complete) {
                         *reinterpret_cast<float4*>(sl.o + (int64_t)row * D + col) = v;
@@ -818,7 +819,8 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Merges the pieces of the segments that share boundaries cut (log-sum-exp rule).
+// Merges the pieces of the segments that share boundaries cut (log-sum-exp rule): the
+// average of the pieces' averages O by their sums, 2^(m - M) l / den each.
 // Grid: (query rows, merge records); a row is served by `wpr` of a CTA's warps,
 // which take its pieces in turn and meet in shared memory. A warp asks for its
 // first eight pieces' columns beside all of the row's (m, l), from which it gets
@@ -857,7 +859,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::
     auto piece = [&](int i) {
         return Slot(p.slots + (2 * ((int64_t)wa + i) + (i == 0 ? first_slot : 0)) * p.slot_bytes, RT);
     };
-    float w[kUnroll], v[kUnroll][EPL];   // a batch of this warp's pieces: m (or -inf) and columns
+    // a batch of this warp's pieces: m (or -inf), l and columns
+    float w[kUnroll], ls[kUnroll], v[kUnroll][EPL];
     auto load = [&](int i0) {
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
@@ -874,6 +877,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::
                 v[j][0] = t.x, v[j][1] = t.y;
             }
             w[j] = __ldcg(sl.m + row);   // -inf where the piece has no visible key
+            ls[j] = __ldcg(sl.l + row);
         }
     };
     load(sub);                           // on the way beside the weights
@@ -897,12 +901,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::
         for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
         M = top;
     }
+    const float inv = 1.f / den;
     for (int i0 = sub; i0 < np; i0 += kUnroll * wpr) {
         if (i0 != sub) load(i0);
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
             if (i0 + j * wpr >= np || w[j] == -INFINITY) continue;
-            const float f = pa::ex2(w[j] - M);
+            const float f = pa::ex2(w[j] - M) * ls[j] * inv;
 #pragma unroll
             for (int e = 0; e < EPL; ++e) acc[e] = fmaf(f, v[j][e], acc[e]);
         }
@@ -919,18 +924,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) int4_merge_kernel(const pa::
     if (np == 0) return;
     const int gr = r1.y + row;
     const int64_t out = ((int64_t)(r0.w + gr / G) * p.num_heads + r1.x * G + gr % G) * D + lane * EPL;
-    const float inv = 1.f / den;
     if (p.out_f32) {
         float* dst = static_cast<float*>(p.out) + out;
         if constexpr (EPL == 4)
-            *reinterpret_cast<float4*>(dst) =
-                make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+            *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         else
-            *reinterpret_cast<float2*>(dst) = make_float2(acc[0] * inv, acc[1] * inv);
+            *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
         return;
     }
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) store_out<TQ>(p.out, out + e, acc[e] * inv, 0);
+    for (int e = 0; e < EPL; ++e) store_out<TQ>(p.out, out + e, acc[e], 0);
 }
 
 template <typename TQ, int D, int NR>
