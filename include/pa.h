@@ -378,10 +378,12 @@ size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
  *                  caches: divided by l, R and their number the kernel's own).
  * INT4 caches: k_scale, v_scale, k_zp and v_zp are 16-byte aligned; at most
  * 4080 query rows per KV head (num_heads / num_kv_heads x max_q_len). Codes,
- * scales and zero points of slots past a context may hold anything. Softmax
- * weight times V scale is rounded to fp16 relative to the largest V scale of the
- * (sequence, KV head, group), so tokens whose V scale is 2^14 or more below that
- * lose bits, of the order of 2^-25 of that scale.
+ * scales and zero points of slots past a context may hold anything. A
+ * token's softmax weight times its V scale is rounded to fp16: to 11 bits, or to
+ * a multiple of 2^-31 of the row's largest weight times the power of two above the
+ * largest V scale of the (sequence, KV head, group), whichever is coarser, so
+ * tokens 2^21 and more below those lose bits. q is rounded to fp16 as a multiple of
+ * a power of two: exact but for elements 2^24 and more below the row's largest.
  * Requirements: head_dim 64 or 128, block_size 16, num_heads a multiple of
  * num_kv_heads, context_lens[s] >= (query run length of s) >= 1, at most
  * 8192 sequences per call with partition_size 0. */

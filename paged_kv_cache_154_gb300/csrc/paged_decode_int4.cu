@@ -16,9 +16,11 @@
 // number; so a word of 8 codes costs one shift and four masks, and no
 // conversion. The powers of two go into q, the output and the row's scale. q
 // goes to fp16 after an exact power-of-two scaling per row, the V scale is
-// folded into P against a running power-of-two reference per group, so the fp16
-// P never exceeds the softmax weight (at most 2^8 under the lazily moved
-// maximum) and a new reference rescales O exactly. Products accumulate in fp32;
+// folded into P against a running power of two per group that is no smaller
+// than any V scale so far, in units of 2^-7 of it: the fp16 P is at most 2^7 times
+// the softmax weight (2^8 under the lazily moved maximum), the largest power that
+// stays finite, so that weights 2^-21 of the largest keep 11 bits and those of
+// 2^-32 count; a new reference rescales O exactly. Products accumulate in fp32;
 // the softmax maximum, sum and the scales are fp32.
 //
 // What bounds it: a (token, kv head) costs 148 bytes at d = 128, so the
@@ -58,6 +60,7 @@ namespace {
 using pa::sched::kBS;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyMax = 8.f;    // base-2 headroom before the running max is moved
+constexpr int kPBits = 7;          // P is 2^kPBits weights: 2^(kLazyMax + kPBits) is finite in fp16
 constexpr int kWholeTokens = 256;  // a warp walks them in the time of the merge's launch
 // Warps of a CTA and CTAs of an SM, as many as the registers allow. One CTA of 12
 // warps: its warps run at one pace, where of three CTAs of 4 the older ones ran ahead
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
     float qsum[NR][GR][2];               // sum of the row's q over a group, as K products count it
     int bound[NR][2];                    // last key each row sees
     uint32_t qb[NR][CH][4];              // row 8 nr + quad, dims 32 c + 8 qc .. + 7
-    float vref[GR], vinv[GR];            // running V-scale reference, a power of two; its inverse
+    float vtop[GR], vinv[GR];            // running top of the V scales, a power of two; 2^kPBits / it
     int L = 0, r = 1, q0 = 0, rows = 0, row_off = 0, seg_b0 = cur.b, last_q = 0;
     bool seg_first = true;
     // i / G for row numbers (i, G < 2^13): exact, as i times the rounding is under 2^32
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
                     for (int e = 0; e < 4; ++e) o[nr][c][j][e] = 0.f;
         }
 #pragma unroll
-        for (int g = 0; g < GR; ++g) vref[g] = exp2i(-126), vinv[g] = exp2i(126);
+        for (int g = 0; g < GR; ++g) vtop[g] = exp2i(kPBits - 126), vinv[g] = exp2i(126);
         fresh = true;
         // the segment's merge record, by the worker that holds its first block
         if (lane == 0 && x.records && seg_b0 == 0 && cur.c < x.max_chunks) {
@@ -511,8 +514,8 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
 
     // Segment end: the output rows (segment held whole) or the partial slot, whose O is the
     // average over the piece: a sum of values near the largest fp32 number would not be
-    // finite. O of group g is in units of the V-scale reference vref[g]; that comes last, as
-    // neither 2^24 vref nor vref / l need be a normal number.
+    // finite. O of group g is in units of vtop[g] / 2^kPBits; vtop comes last, as neither
+    // 2^24 vtop nor vtop / l need be a normal number.
     auto finish_segment = [&](bool complete, int slot_idx, int tok_end) {
         Slot sl(p.slots + (2 * wid + slot_idx) * (int64_t)p.slot_bytes, p.rows_per_tile);
         if (!complete && lane == 0) {
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
                 const int row = 8 * nr + 2 * qc + e;
                 if (row >= rows) continue;
                 // a piece that the row sees nothing of (l = 0) is marked by its m, its O not read
-                const float inv = __fdividef(kUnit, l);
+                const float inv = __fdividef(kUnit / (1 << kPBits), l);
                 int64_t obase = 0;
                 if (complete) {
                     const int gr = row_off + row, qi = query_of(gr);
@@ -548,11 +551,11 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     // dims 4 quad, + 2 count 2^-24, dims 4 quad + 1, + 3 count 2^-20
-                    const float zc = z[c * GR / CH], ref = vref[c * GR / CH];
-                    const float4 v = make_float4((o[nr][c][0][e] - zc) * inv * ref,
-                                                 fmaf(o[nr][c][0][2 + e], 0.0625f, -zc) * inv * ref,
-                                                 (o[nr][c][1][e] - zc) * inv * ref,
-                                                 fmaf(o[nr][c][1][2 + e], 0.0625f, -zc) * inv * ref);
+                    const float zc = z[c * GR / CH], top = vtop[c * GR / CH];
+                    const float4 v = make_float4((o[nr][c][0][e] - zc) * inv * top,
+                                                 fmaf(o[nr][c][0][2 + e], 0.0625f, -zc) * inv * top,
+                                                 (o[nr][c][1][e] - zc) * inv * top,
+                                                 fmaf(o[nr][c][1][2 + e], 0.0625f, -zc) * inv * top);
                     const int col = 32 * c + 4 * quad;
                     if (!complete) {
                         *reinterpret_cast<float4*>(sl.o + (int64_t)row * D + col) = v;
@@ -689,8 +692,8 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
 #pragma unroll
         for (int g = 0; g < GR; ++g)
             raise |= fmaxf(fmaxf(vs[0][0][g], vs[0][1][g]), fmaxf(vs[1][0][g], vs[1][1][g])) >
-                     vref[g];
-        if (__any_sync(0xffffffffu, raise)) {   // rare: a row's maximum or a V reference moves
+                     vtop[g];
+        if (__any_sync(0xffffffffu, raise)) {   // rare: a row's maximum or a V scale's top moves
             float vfix[GR];
 #pragma unroll
             for (int g = 0; g < GR; ++g) {
@@ -698,10 +701,11 @@ __global__ void __launch_bounds__(worker_warps(D, NR) * 32, ctas_per_sm(D, NR))
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float next = fmaxf(vref[g], exp2i(ceil_log2(mx)));
-                vinv[g] = exp2i(-(int)(__float_as_uint(next) >> 23) + 127);   // powers of two: exact
-                vfix[g] = vref[g] * vinv[g];
-                vref[g] = next;
+                const float next = fmaxf(vtop[g], exp2i(ceil_log2(mx)));
+                const int e = (int)(__float_as_uint(next) >> 23) - 127;   // powers of two: exact
+                vinv[g] = exp2i(kPBits - e);
+                vfix[g] = vtop[g] * exp2i(-e);
+                vtop[g] = next;
             }
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)

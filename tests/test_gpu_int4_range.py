@@ -101,3 +101,71 @@ def test_pieces_of_rows_that_see_nothing_of_them():
     top = max(np.abs(ref.tokens_of(v, tables[s], L, 0)).max() for s, L in enumerate(lens))
     out = got.double().cpu().numpy()
     assert np.isfinite(out).all() and np.abs(out - want).max() <= REL * top
+
+
+def one_table(S, L, Hkv, d, k, v):
+    """A cache that holds one context of L tokens (rows k, v [L, H_kv, d]), and the block
+    tables of S sequences that all share it."""
+    nb = (L + 15) // 16
+    cache = new_cache(nb + 3, Hkv, d)
+    table = np.random.default_rng(5).permutation(nb + 3)[:nb].astype(np.int32)
+    t = np.arange(L)
+    slots = torch.from_numpy(table[t // 16].astype(np.int64) * 16 + t % 16).cuda()
+    pa.append_kv(k.cuda(), v.cuda(), cache.k, cache.v, slots, cache.num_blocks, cache.k_scale,
+                 cache.v_scale, cache.k_zp, cache.v_zp)
+    return cache, np.tile(table, (S, 1))
+
+
+def attend_one_table(cache, table, L, q, scale):
+    """64-bit attention of q [S, H, d] over the context that all of them share: outputs,
+    sums of weight times |value|, and the largest weights [S, H]."""
+    S, H, d = q.shape
+    out, mag, top = (torch.empty((S, H, n), dtype=torch.float64, device="cuda")
+                     for n in (d, d, 1))
+    G = H // cache.num_kv_heads
+    for g, (k, v) in enumerate(zip(*[[torch.from_numpy(ref.tokens_of(x, table, L, g)).cuda()
+                                      for g in range(cache.num_kv_heads)]
+                                     for x in ref.cache_values(cache)])):
+        h = slice(g * G, g * G + G)
+        p = torch.softmax(q[:, h].double().cuda().reshape(S * G, d) @ k.T * scale, -1)
+        out[:, h] = (p @ v).reshape(S, G, d)
+        mag[:, h] = (p @ v.abs()).reshape(S, G, d)
+        top[:, h] = p.amax(-1).reshape(S, G, 1)
+    return out, mag, top[..., 0]
+
+
+@pytest.mark.parametrize("S,H,Hkv,d", [(1, 8, 2, 64), (200, 8, 1, 128), (130, 16, 1, 128),
+                                       (200, 8, 1, 64)])
+def test_weights_far_below_a_dominant_one(S, H, Hkv, d):
+    """The first token takes nearly all of the weight and has the value 0, so that the
+    others, each 2^-26 of it, make the output. A weight times its V scale is rounded to
+    fp16: by 2^-11 of itself, or by 2^-32 of the largest weight times the power of two
+    above the largest V scale, which the up to 15 steps of a value multiply. Logits are
+    off by 2^-16 of sum |q k| scale, that is 18 of the first token: 2.8e-4 of a weight
+    (the other tokens' sums are small)."""
+    L = 20_000
+    gen = torch.Generator().manual_seed(7)
+    k = torch.randn((L, Hkv, d), generator=gen) * 0.25
+    k[..., 0] = 0
+    k[0] = 0
+    k[0, :, 0] = 16
+    v = torch.randn((L, Hkv, d), generator=gen) + 1
+    v[0] = 0
+    q = torch.randn((S, H, d), generator=gen) * 0.25
+    scale = d ** -0.5
+    q[..., 0] = 26 * float(np.log(2)) / (16 * scale)
+    q = q.bfloat16()
+    cache, tables = one_table(S, L, Hkv, d, k.bfloat16(), v.bfloat16())
+    got = decode(cache, tables, [L] * S, [1] * S, np.arange(S + 1, dtype=np.int32), q,
+                 torch.float32, scale)
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
+    want, mag, top = attend_one_table(cache, tables[0], L, q, scale)
+    assert (top > 0.99).all()
+    # the tokens of the first one's piece alone are rounded against it; a call has at least
+    # 1216 workers' shares, or as many as 1250 blocks make
+    n = min(L, 16 * (-(-S * Hkv * 1250 // 1216) + 1))
+    s_top = 2.0 ** np.ceil(np.log2(float(cache.v_scale[tables[0].tolist()].max())))
+    tol = mag * (2.0 ** -11 + 5.6e-4) + n * 15 * s_top * 2.0 ** -32
+    err = (got.double() - want).abs()
+    assert (err <= tol).all(), ((err - tol).max(), want.abs().max())
