@@ -169,3 +169,28 @@ def test_weights_far_below_a_dominant_one(S, H, Hkv, d):
     tol = mag * (2.0 ** -11 + 5.6e-4) + n * 15 * s_top * 2.0 ** -32
     err = (got.double() - want).abs()
     assert (err <= tol).all(), ((err - tol).max(), want.abs().max())
+
+
+@pytest.mark.parametrize("H,d", [(16, 128), (32, 128), (8, 64), (32, 64)])
+def test_small_averages_over_long_shares(H, d):
+    """Nearly even weights over shares of several hundred blocks: values of either sign
+    average to a hundredth of them, where what the accumulation loses would show. The
+    bound is that of test_small_averages_of_long_contexts: 2^-11 / sqrt(3) of the norm in
+    the mean square for the fp16 weights, up to 2^-11 with the accumulation, for the
+    elements of the low and of the high halves of bytes."""
+    S, L, Hkv = 256, 32768, 2          # 1048576 blocks over at most 1824 workers
+    gen = torch.Generator().manual_seed(d + H)
+    k, v = (torch.randn((L, Hkv, d), generator=gen).bfloat16() for _ in range(2))
+    q = torch.randn((S, H, d), generator=gen).bfloat16()
+    scale = 0.25 * d ** -0.5
+    cache, tables = one_table(S, L, Hkv, d, k, v)
+    got = decode(cache, tables, [L] * S, [1] * S, np.arange(S + 1, dtype=np.int32), q,
+                 torch.float32, scale)
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
+    want, mag, _ = attend_one_table(cache, tables[0], L, q, scale)
+    err = got.double() - want
+    for half in (0, 1):
+        e, w = err[..., half::2].norm(), want[..., half::2].norm()
+        print(f"half {half}: {e / w:.2e} of the norm, which is {w / mag[..., half::2].norm():.1e}")
+        assert e <= 2.0 ** -11 * w
