@@ -502,10 +502,14 @@ pa_status pa_decode_shared_prefix(
  * tokens of every KV head and pa_move_tokens moves the rows, after
  * pa_seq_make_private on the pool and before pa_seq_truncate. ---- */
 
-/* Bytes of workspace pa_accumulate_weights needs for these sizes (0 for invalid
- * sizes and for more than a call may have); at least 256-byte aligned, needs no
- * initialisation, and may be shared by calls of one stream. Host-only: needs no
- * GPU. */
+/* Bytes of workspace with which pa_accumulate_weights is fastest for these sizes
+ * (0 for invalid sizes and for more than a call may have); at least 256-byte
+ * aligned, needs no initialisation, and may be shared by calls of one stream. A
+ * buffer of this size for the largest num_seqs, query rows per KV head and
+ * max_context_len at some num_kv_heads serves every smaller call too. It may be smaller than what a
+ * smaller call asks for: few query rows store their logits while those stay under
+ * 256 MB; without room for them they are computed twice, with the same results but
+ * for rounding. Host-only: needs no GPU. */
 size_t pa_accumulate_weights_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
                                             int32_t num_heads, int32_t num_kv_heads,
                                             int32_t head_dim, int32_t max_q_len,

@@ -19,7 +19,8 @@
 //
 // Storing costs 8 bytes a row and token, mostly within L2; computing again costs
 // a second read of K and its products. So few rows are stored (up to 16 rows
-// per KV head, while the buffer stays under 256 MB), many are computed again.
+// per KV head, while the buffer stays under 256 MB and the workspace has room for
+// it), many are computed again.
 //
 // What bounds it: for few rows the read of K, which goes from global memory to
 // operand registers directly: tokens stand in the M dimension of the warp-level
@@ -952,9 +953,11 @@ __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
 // kMaxTile does that (fewer starts: 100001 tokens of 8 heads 30.6 us against 32.6
 // with 512), else 512, whose many waves even out a ragged batch (Llama-3-8B step:
 // 64.7 us, 70.9 with 2048).
+constexpr int kMinTile = 128;
+static_assert(kManyTokens >= kMinTile, "stats are sized for tiles of kMinTile");
 int stored_tile(int64_t tokens) {
     const int64_t t = (tokens + 4 * 152 - 1) / (4 * 152);
-    return t > kMaxTile ? 512 : (int)std::max<int64_t>(128, (t + 63) / 64 * 64);
+    return t > kMaxTile ? 512 : (int)std::max<int64_t>(kMinTile, (t + 63) / 64 * 64);
 }
 
 // Up to as many tiles the warps of the last pass merge their rows' (m, l) themselves, by
@@ -962,12 +965,22 @@ int stored_tile(int64_t tokens) {
 // tokens, 16 tiles: 34.9 us, 35.7 with that kernel; of 8192, 32 tiles: 56.7 and 53.9).
 constexpr int kFoldTiles = 16;
 
+// A call computes its logits twice in a workspace of stats and sums, whose sizes grow
+// with every argument, so that a buffer sized for the largest call serves them all;
+// where the logits are worth storing and find room behind the stats it stores them.
 struct Shape {
     int64_t rows;         // most query rows per KV head
-    int row_pad, tiles, tile_tokens, tokens_pad;
-    bool stored;
-    int64_t stats_bytes, sums_bytes, logits_bytes;
+    int row_pad, tokens_pad;
+    int64_t stats_bytes;  // (m, l) of tiles of kMinTile tokens, the smallest
+    int64_t sums_bytes;   // computed again
+    int64_t logits_bytes; // stored; 0: not worth it
     bool fits;            // false: larger than a call may be, the rest is not set
+
+    int64_t least_bytes() const { return stats_bytes + sums_bytes; }
+    int64_t stored_bytes() const { return logits_bytes ? stats_bytes + logits_bytes : INT64_MAX; }
+    int64_t bytes() const {
+        return logits_bytes ? std::max(least_bytes(), stored_bytes()) : least_bytes();
+    }
 };
 
 Shape shape_of(int num_seqs, int num_heads, int num_kv_heads, int max_q_len, int max_len) {
@@ -980,13 +993,12 @@ Shape shape_of(int num_seqs, int num_heads, int num_kv_heads, int max_q_len, int
     const int64_t sg = (int64_t)num_seqs * num_kv_heads;
     h.row_pad = 2;            // two rows a store
     while (h.row_pad < h.rows) h.row_pad *= 2;
-    h.stored = h.rows <= 16 && sg * h.tokens_pad <= kMaxStored / (4 * h.row_pad);
-    if (h.stored) h.logits_bytes = sg * h.tokens_pad * h.row_pad * 4;
-    h.tile_tokens = h.stored ? stored_tile(sg * max_len) : kManyTokens;
-    h.tiles = (max_len + h.tile_tokens - 1) / h.tile_tokens;
-    if (sg * h.rows > kMaxWorkspace / 8 / h.tiles) return h;
-    h.stats_bytes = (sg * h.rows * h.tiles * 8 + 255) / 256 * 256;
-    if (!h.stored && h.tiles > kFoldTiles) h.sums_bytes = (sg * h.rows * 8 + 255) / 256 * 256;
+    if (h.rows <= 16 && sg * h.tokens_pad <= kMaxStored / (4 * h.row_pad))
+        h.logits_bytes = sg * h.tokens_pad * h.row_pad * 4;
+    const int64_t tiles = (max_len + kMinTile - 1) / kMinTile;
+    if (sg * h.rows > kMaxWorkspace / 8 / tiles) return h;
+    h.stats_bytes = (sg * h.rows * tiles * 8 + 255) / 256 * 256;
+    if (max_len > kFoldTiles * kManyTokens) h.sums_bytes = (sg * h.rows * 8 + 255) / 256 * 256;
     h.fits = true;
     return h;
 }
@@ -1001,13 +1013,14 @@ pa_status launch_stored(const Params& p, cudaStream_t st) {
 }
 
 template <int KV, int D>
-pa_status launch_typed(Params& p, const Shape& h, void* workspace, cudaStream_t st) {
+pa_status launch_typed(Params& p, const Shape& h, void* workspace, bool stored, cudaStream_t st) {
     char* const ws = static_cast<char*>(workspace);
     p.stats = reinterpret_cast<float2*>(ws);
-    if (h.stored) {
+    p.tile_tokens =
+        stored ? stored_tile((int64_t)p.num_seqs * p.num_kv_heads * p.max_len) : kManyTokens;
+    p.tiles = (p.max_len + p.tile_tokens - 1) / p.tile_tokens;
+    if (stored) {
         p.logits = reinterpret_cast<float*>(ws + h.stats_bytes);
-        p.tiles = h.tiles;
-        p.tile_tokens = h.tile_tokens;
         p.row_pad = h.row_pad;
         const dim3 grid(p.tiles, p.num_kv_heads, p.num_seqs);
         if (pa_status s = pa::cuda_status(
@@ -1024,8 +1037,6 @@ pa_status launch_typed(Params& p, const Shape& h, void* workspace, cudaStream_t 
         }
     }
     constexpr int kTokens = kManyTokens;
-    p.tiles = h.tiles;
-    p.tile_tokens = h.tile_tokens;
     if (h.sums_bytes) p.sums = reinterpret_cast<float2*>(ws + h.stats_bytes);
     p.row_warps = 1;
     while (p.row_warps < kManyWarps && 16 * p.row_warps < h.rows) p.row_warps *= 2;
@@ -1056,13 +1067,14 @@ pa_status launch_typed(Params& p, const Shape& h, void* workspace, cudaStream_t 
 }
 
 template <int D>
-pa_status launch_kv(pa_dtype kv, Params& p, const Shape& h, void* workspace, cudaStream_t st) {
+pa_status launch_kv(pa_dtype kv, Params& p, const Shape& h, void* workspace, bool stored,
+                    cudaStream_t st) {
     switch (kv) {
-        case PA_F16: return launch_typed<PA_F16, D>(p, h, workspace, st);
-        case PA_BF16: return launch_typed<PA_BF16, D>(p, h, workspace, st);
-        case PA_INT8: return launch_typed<PA_INT8, D>(p, h, workspace, st);
-        case PA_INT4: return launch_typed<PA_INT4, D>(p, h, workspace, st);
-        default: return launch_typed<PA_FP8_E4M3, D>(p, h, workspace, st);
+        case PA_F16: return launch_typed<PA_F16, D>(p, h, workspace, stored, st);
+        case PA_BF16: return launch_typed<PA_BF16, D>(p, h, workspace, stored, st);
+        case PA_INT8: return launch_typed<PA_INT8, D>(p, h, workspace, stored, st);
+        case PA_INT4: return launch_typed<PA_INT4, D>(p, h, workspace, stored, st);
+        default: return launch_typed<PA_FP8_E4M3, D>(p, h, workspace, stored, st);
     }
 }
 
@@ -1076,7 +1088,7 @@ extern "C" size_t pa_accumulate_weights_workspace_size(int32_t num_seqs, int32_t
         head_dim <= 0 || max_q_len <= 0 || max_context_len <= 0 || num_heads % num_kv_heads != 0)
         return 0;
     const Shape h = shape_of(num_seqs, num_heads, num_kv_heads, max_q_len, max_context_len);
-    return h.fits ? (size_t)(h.stats_bytes + h.sums_bytes + h.logits_bytes) : 0;
+    return h.fits ? (size_t)h.bytes() : 0;
 }
 
 extern "C" pa_status pa_accumulate_weights(
@@ -1112,7 +1124,7 @@ extern "C" pa_status pa_accumulate_weights(
                     "per KV head, %d tokens; at most 65535, 65535, %d and %d)",
                     num_seqs, num_kv_heads, (long long)h.rows, max_context_len, kMaxRows,
                     pa::kMaxTokens);
-    const size_t need = (size_t)(h.stats_bytes + h.sums_bytes + h.logits_bytes);
+    const size_t need = (size_t)h.least_bytes();
     if (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256)
         return fail(PA_ERR_INVALID_ARG, "workspace needs %zu bytes, 256-byte aligned (got %zu)",
                     need, workspace_bytes);
@@ -1147,6 +1159,7 @@ extern "C" pa_status pa_accumulate_weights(
     p.row_slots = (int)h.rows;
     p.q_bf16 = q_dtype == PA_BF16;
     p.scale_log2 = scale * kLog2e;
-    return head_dim == 128 ? launch_kv<128>(kv_dtype, p, h, workspace, st)
-                           : launch_kv<64>(kv_dtype, p, h, workspace, st);
+    const bool stored = (int64_t)std::min<size_t>(workspace_bytes, INT64_MAX - 1) >= h.stored_bytes();
+    return head_dim == 128 ? launch_kv<128>(kv_dtype, p, h, workspace, stored, st)
+                           : launch_kv<64>(kv_dtype, p, h, workspace, stored, st);
 }
