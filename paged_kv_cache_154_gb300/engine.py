@@ -44,6 +44,7 @@ class StepInputs:
     out: torch.Tensor
     workspace: Optional[torch.Tensor]
     shared: Optional["SharedPrefix"] = None
+    weights_workspace: Optional[torch.Tensor] = None   # accumulate_step's, from its first call on
 
 
 @dataclass
@@ -66,7 +67,6 @@ class TokenWeights:
     scores: torch.Tensor              # fp32 [S, H_kv, width]
     positions: torch.Tensor           # int32 [S, H_kv, width], -1: in text order
     evicted: np.ndarray               # int64 [S]: tokens evicted so far
-    workspace: Optional[torch.Tensor] = None
 
 
 class PagedKVCache:
@@ -230,15 +230,16 @@ class PagedKVCache:
                             np.zeros(len(seqs), np.int64))
 
     def accumulate_step(self, si: StepInputs, tw: TokenWeights, scale: float) -> None:
-        """Add the weights of the step's queries (rows of si and tw alike)."""
+        """Add the weights of the step's queries (rows of si and tw alike). The workspace
+        is the step's own, so that a captured step keeps the one it was captured with."""
         n = accumulate_weights_workspace_size(si.context_lens.shape[0], si.q.shape[0],
                                               si.q.shape[1], self.num_kv_heads, self.head_dim,
                                               si.max_q_len, si.max_context_len)
-        if tw.workspace is None or tw.workspace.numel() < n:
-            tw.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+        if si.weights_workspace is None or si.weights_workspace.numel() < n:
+            si.weights_workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
         accumulate_weights(tw.scores, tw.scores, si.q, self.k, si.block_tables, si.context_lens,
                            si.max_context_len, scale, si.query_start_loc, si.max_q_len,
-                           self.num_blocks, self.k_scale, self.k_zp, tw.workspace)
+                           self.num_blocks, self.k_scale, self.k_zp, si.weights_workspace)
 
     def evict(self, tw: TokenWeights, names: Dict, keep, num_sinks: int = 0,
               num_recent: int = 0) -> None:

@@ -1,11 +1,14 @@
 """Workspaces of the weight sums: one buffer, sized for a server's largest call, under
-every smaller one. Tolerances are those of test_gpu_eviction."""
+every smaller one, and the buffers of captured steps. Tolerances are those of
+test_gpu_eviction."""
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_cache_154_gb300 as pa
-from test_gpu_eviction import check, filled
+from oracle import compressed as ref
+from paged_kv_cache_154_gb300.engine import PagedKVCache
+from test_gpu_eviction import REL, Op, check, filled
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +70,45 @@ def test_a_buffer_too_small_for_the_call_is_refused():
                               torch.empty(least - 1, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     check(out, cache, tables, lens, np.arange(2), q.cpu(), 0.125, None, 700)
+
+
+def test_captured_steps_keep_their_workspaces():
+    """Two captured steps of one batch's weights, the later and larger one in between: each
+    replays into the buffer it was captured with, and the sums are those of eager steps."""
+    H, Hkv, d = 8, 2, 64
+    gen = torch.Generator().manual_seed(3)
+
+    def rows(n):
+        return torch.randn((n, Hkv, d), generator=gen).to(torch.bfloat16)
+
+    cache, names = PagedKVCache(200, Hkv, d, "int4"), {}
+    cache.run_phase([Op(seq="a"), Op(seq="a", k=rows(900), v=rows(900)), Op(seq="b"),
+                     Op(seq="b", k=rows(33), v=rows(33))], names)
+    tw = cache.track_weights(["a", "b"], 1000)
+    steps, graphs, held = [], [], []
+    for n in (1, 20):
+        q = torch.randn((2 * n, H, d), generator=gen).to(torch.bfloat16)
+        si = cache.prepare_step([Op(seq=s, k=rows(n), v=rows(n)) for s in ("a", "b")], names, q)
+        cache.write_step(si)
+        graphs.append(cache.capture(cache.accumulate_step, si, tw, 0.125))
+        steps.append(si)
+        held.append(si.weights_workspace.data_ptr())
+    other = [torch.full((w.numel(),), 0x5A, dtype=torch.uint8, device="cuda")
+             for w in (si.weights_workspace for si in steps) for _ in range(3)]
+    tw.scores.zero_()
+    for g in (graphs[0], graphs[1], graphs[0]):
+        g.replay()
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
+    assert [si.weights_workspace.data_ptr() for si in steps] == held and held[0] != held[1]
+    assert all((x == 0x5A).all() for x in other)
+    k, _ = ref.cache_values(cache)
+    want = 0
+    for si, times in zip(steps, (2, 1)):
+        lens, nq = si.context_lens.tolist(), si.q.shape[0]
+        w = ref.weights(si.q.double().cpu().numpy(), k, si.block_tables.cpu().numpy(), lens,
+                        np.arange(3) * (nq // 2), 0.125, 1000)
+        want = want + times * w
+    got = tw.scores.double().cpu().numpy()
+    # three additions to a sum, each rounded by 2^-24
+    assert (np.abs(got - want) <= (REL + 3 * 2.0 ** -24) * want + 1e-30).all()
