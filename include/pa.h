@@ -150,8 +150,12 @@ pa_status pa_seq_make_private(pa_pool* pool, int32_t seq, int32_t n_tokens,
 
 /* Give up the tokens past the first n_tokens (at most the tokens held): whole
  * blocks behind them are released as by pa_seq_free. After an eviction, or to
- * take back rejected draft tokens. The sequence registers nothing in the prefix
- * cache from then on. */
+ * take back rejected draft tokens: the caller then clears the accumulated weights
+ * of the slots given up (scores 0, positions -1), which pa_accumulate_weights
+ * would add the next tokens' to, and gives that call the accepted queries only.
+ * Tokens that pa_evict_select left stand in no order, so slots do not say which
+ * of them are the last. The sequence registers nothing in the prefix cache from
+ * then on. */
 pa_status pa_seq_truncate(pa_pool* pool, int32_t seq, int32_t n_tokens);
 
 /* Release a sequence: refcount - 1 on each block; blocks reaching 0 go back
@@ -521,7 +525,9 @@ size_t pa_accumulate_weights_workspace_size(int32_t num_seqs, int32_t num_q_toke
  * arguments (every cache type; causal within the run), in fp32.
  *   scores_out, scores_in  fp32 [num_seqs][num_kv_heads][score_stride]; rows are
  *                  in the order of block_tables. scores_in may be scores_out, or
- *                  NULL for zeros. Only t < context_lens[s] is read and written.
+ *                  NULL for zeros. Only t < context_lens[s] is read and written;
+ *                  a slot that another token held before starts from that
+ *                  token's sum unless it was cleared.
  *                  scores_out is 16-byte aligned.
  *   score_stride   elements from one KV head's scores to the next, at least
  *                  max_context_len

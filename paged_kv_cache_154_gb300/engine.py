@@ -45,6 +45,7 @@ class StepInputs:
     workspace: Optional[torch.Tensor]
     shared: Optional["SharedPrefix"] = None
     weights_workspace: Optional[torch.Tensor] = None   # accumulate_step's, from its first call on
+    q_lens: Optional[Sequence[int]] = None   # query run of every sequence
 
 
 @dataclass
@@ -67,6 +68,11 @@ class TokenWeights:
     scores: torch.Tensor              # fp32 [S, H_kv, width]
     positions: torch.Tensor           # int32 [S, H_kv, width], -1: in text order
     evicted: np.ndarray               # int64 [S]: tokens evicted so far
+    settled: Optional[np.ndarray] = None   # int64 [S]: tokens the last eviction left, in no order
+
+    def __post_init__(self):
+        if self.settled is None:
+            self.settled = np.zeros(len(self.seqs), np.int64)
 
 
 class PagedKVCache:
@@ -189,7 +195,7 @@ class PagedKVCache:
             max_q_len=max(q_lens), max_context_len=max(lens),
             out=torch.empty((nq, q.shape[1], q.shape[2]), dtype=out_dtype, device=dev),
             workspace=zeroed_workspace(ws_bytes, dev),
-            shared=shared)
+            shared=shared, q_lens=q_lens)
 
     def write_step(self, si: StepInputs) -> None:
         """The step's cache writes: copy-on-write block copies, then the append."""
@@ -229,17 +235,63 @@ class PagedKVCache:
                             torch.full(shape, -1, dtype=torch.int32, device=self.device),
                             np.zeros(len(seqs), np.int64))
 
-    def accumulate_step(self, si: StepInputs, tw: TokenWeights, scale: float) -> None:
+    def accumulate_step(self, si: StepInputs, tw: TokenWeights, scale: float,
+                        accepted: Optional[Sequence[int]] = None) -> None:
         """Add the weights of the step's queries (rows of si and tw alike). The workspace
-        is the step's own, so that a captured step keeps the one it was captured with."""
+        is the step's own, so that a captured step keeps the one it was captured with.
+
+        accepted: of a verify step, how many of every sequence's queries count, from the
+        first on; the tokens of the others are those that truncate() takes back, before
+        or after this call. Host numbers, so such a call is not captured. Without it
+        every query counts, and what rejected ones gave stays in the sums."""
+        q, lens, start = si.q, si.context_lens, si.query_start_loc
+        if accepted is not None:
+            runs = np.asarray(si.q_lens, np.int64)
+            acc = np.asarray(accepted, np.int64)
+            if acc.shape != runs.shape or (acc < 0).any() or (acc > runs).any():
+                raise ValueError(f"accepted {acc.tolist()} of query runs {runs.tolist()}")
+            first = np.cumsum(runs) - runs
+            rows = np.concatenate([f + np.arange(a) for f, a in zip(first, acc)])
+            # a call has at least as many queries as sequences: those behind the last run add nothing
+            rows = np.append(rows, np.zeros(max(0, len(runs) - len(rows)), np.int64))
+
+            def to(a, dtype):
+                return torch.from_numpy(np.ascontiguousarray(a, dtype)).to(self.device)
+
+            q = q[to(rows, np.int64)]
+            lens = lens - to(runs - acc, np.int32)
+            start = to(np.append(0, np.cumsum(acc)), np.int32)
         n = accumulate_weights_workspace_size(si.context_lens.shape[0], si.q.shape[0],
                                               si.q.shape[1], self.num_kv_heads, self.head_dim,
                                               si.max_q_len, si.max_context_len)
         if si.weights_workspace is None or si.weights_workspace.numel() < n:
             si.weights_workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
-        accumulate_weights(tw.scores, tw.scores, si.q, self.k, si.block_tables, si.context_lens,
-                           si.max_context_len, scale, si.query_start_loc, si.max_q_len,
+        accumulate_weights(tw.scores, tw.scores, q, self.k, si.block_tables, lens,
+                           si.max_context_len, scale, start, si.max_q_len,
                            self.num_blocks, self.k_scale, self.k_zp, si.weights_workspace)
+
+    def truncate(self, tw: TokenWeights, names: Dict, lens) -> None:
+        """Take back the tokens of tw's sequences past the first `lens` (an int, or one per
+        sequence; a shorter sequence stays as it is), as rejected draft tokens, and the
+        weights they received: the next tokens in their slots start from none. Tokens that
+        an eviction left stand in no order and cannot be cut by their slots."""
+        ids = [names[s] for s in tw.seqs]
+        now = np.array([self.pool.seq_len(i) for i in ids], np.int64)
+        new = np.minimum(np.broadcast_to(np.asarray(lens, np.int64), now.shape), now)
+        if (new < 0).any():
+            raise ValueError("a length is negative")
+        for s, n, old, kept in zip(tw.seqs, new, now, tw.settled):
+            if n < old and n < kept:
+                raise ValueError(f"sequence {s!r}: its first {kept} tokens are what an eviction "
+                                 f"left, which {n} would cut")
+        if not (new < now).any():
+            return
+        for i, n in zip(ids, new):
+            self.pool.seq_truncate(i, int(n))
+        past = (torch.arange(tw.scores.shape[2], device=tw.scores.device) >=
+                torch.from_numpy(new).to(tw.scores.device)[:, None, None])
+        tw.scores.masked_fill_(past, 0)
+        tw.positions.masked_fill_(past, -1)
 
     def evict(self, tw: TokenWeights, names: Dict, keep, num_sinks: int = 0,
               num_recent: int = 0) -> None:
@@ -284,6 +336,7 @@ class PagedKVCache:
         for i, n in zip(ids, kept):
             self.pool.seq_truncate(i, int(n))
         tw.evicted += lens - kept
+        tw.settled = np.where(kept < lens, kept, tw.settled)
 
     def capture(self, fn, *args) -> "torch.cuda.CUDAGraph":
         """Record fn(*args) (e.g. write_step or attend_step) in a CUDA graph;

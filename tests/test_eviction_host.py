@@ -283,3 +283,55 @@ def test_engine_refuses_evictions_before_anything_moves():
     cache.evict(tw, names, 40)                               # nothing is over its budget
     assert [cache.pool.seq_len(i) for i in names.values()] == [40, 20]
     assert cache.pool.stats() == before and not tw.evicted.any()
+
+
+def cpu_engine(**lens):
+    """An engine whose tensors are the host's (nothing reaches a GPU) with sequences of these
+    lengths, and weights of 128 tokens each in which slot t has t + 1."""
+    import torch
+    from paged_kv_cache_154_gb300.engine import PagedKVCache
+    cache, names = PagedKVCache(40, 2, 64, "bf16", device="cpu"), {}
+    for name, n in lens.items():
+        names[name] = cache.pool.seq_create()
+        cache.pool.seq_append_slots(names[name], n)
+    tw = cache.track_weights(list(lens), 128)
+    for row, n in enumerate(lens.values()):
+        tw.scores[row, :, :n] = torch.arange(1.0, n + 1)
+    return cache, names, tw
+
+
+def test_truncated_tokens_leave_no_weight():
+    import torch
+    cache, names, tw = cpu_engine(a=60, b=40, c=33)
+    tw.positions[2, :, :33] = torch.arange(33)
+    cache.truncate(tw, names, [57, 40, 20])
+    assert [cache.pool.seq_len(i) for i in names.values()] == [57, 40, 20]
+    for row, n in enumerate((57, 40, 20)):
+        assert torch.equal(tw.scores[row, :, :n], torch.arange(1.0, n + 1).expand(2, n))
+        assert not tw.scores[row, :, n:].any()
+    assert torch.equal(tw.positions[2, :, :20], torch.arange(20).int().expand(2, 20))
+    assert (tw.positions[2, :, 20:] == -1).all() and (tw.positions[:2] == -1).all()
+    cache.truncate(tw, names, 50)
+    assert [cache.pool.seq_len(i) for i in names.values()] == [50, 40, 20]
+    assert not tw.scores[0, :, 50:].any() and tw.scores[0, 0, 49] == 50
+
+
+def test_truncation_refusals():
+    cache, names, tw = cpu_engine(a=60, b=40)
+    tw.settled[:] = 32, 0                # as after an eviction that left 32 of a's tokens
+    for lens, text in (([31, 40], "cut"), ([60, -1], "negative"), (0, "cut")):
+        with pytest.raises(ValueError, match=text):
+            cache.truncate(tw, names, lens)
+        assert [cache.pool.seq_len(i) for i in names.values()] == [60, 40]
+        assert tw.scores[0, 0, 59] == 60
+    cache.truncate(tw, names, [32, 0])
+    assert [cache.pool.seq_len(i) for i in names.values()] == [32, 0]
+
+
+def test_accepted_queries_are_within_their_runs():
+    from types import SimpleNamespace
+    cache, names, tw = cpu_engine(a=60, b=40)
+    si = SimpleNamespace(q=None, context_lens=None, query_start_loc=None, q_lens=[3, 1], seqs=None)
+    for bad in ([4, 0], [3], [-1, 1], [2, 2]):
+        with pytest.raises(ValueError, match="accepted"):
+            cache.accumulate_step(si, tw, 0.125, bad)
