@@ -171,6 +171,7 @@ class Pool:
         _check(lib().pa_pool_create(num_blocks, block_size, fo, ctypes.byref(self._h)))
         self.num_blocks = num_blocks
         self.block_size = block_size
+        self.evicted: dict = {}   # sequence id: tokens that evictions took out of it (its forks too)
 
     def __del__(self):
         if getattr(self, "_h", None) and _lib is not None:
@@ -185,6 +186,8 @@ class Pool:
     def seq_fork(self, parent: int) -> int:
         out = _I32()
         _check(lib().pa_seq_fork(self._h, parent, ctypes.addressof(out)))
+        if parent in self.evicted:
+            self.evicted[out.value] = self.evicted[parent]
         return out.value
 
     def seq_append_slots(self, seq: int, n: int) -> Tuple[np.ndarray, Optional[Tuple[int, int]]]:
@@ -227,6 +230,7 @@ class Pool:
 
     def seq_free(self, seq: int) -> None:
         _check(lib().pa_seq_free(self._h, seq))
+        self.evicted.pop(seq, None)
 
     def seq_len(self, seq: int) -> int:
         out = _I32()

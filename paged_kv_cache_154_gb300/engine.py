@@ -46,6 +46,7 @@ class StepInputs:
     shared: Optional["SharedPrefix"] = None
     weights_workspace: Optional[torch.Tensor] = None   # accumulate_step's, from its first call on
     q_lens: Optional[Sequence[int]] = None   # query run of every sequence
+    seqs: Optional[Sequence] = None          # their names
 
 
 @dataclass
@@ -195,7 +196,7 @@ class PagedKVCache:
             max_q_len=max(q_lens), max_context_len=max(lens),
             out=torch.empty((nq, q.shape[1], q.shape[2]), dtype=out_dtype, device=dev),
             workspace=zeroed_workspace(ws_bytes, dev),
-            shared=shared, q_lens=q_lens)
+            shared=shared, q_lens=q_lens, seqs=[op.seq for op in step_ops])
 
     def write_step(self, si: StepInputs) -> None:
         """The step's cache writes: copy-on-write block copies, then the append."""
@@ -228,12 +229,40 @@ class PagedKVCache:
         return self.attend_step(si, scale, partition_size)
 
     # -- eviction by accumulated attention weight ---------------------------------
-    def track_weights(self, seqs: Sequence, width: int) -> TokenWeights:
-        """Empty weights for `seqs` (caller-chosen names), up to `width` tokens each."""
+    def track_weights(self, seqs: Sequence, width: int, carry: Sequence[TokenWeights] = (),
+                      parents: Optional[Dict] = None) -> TokenWeights:
+        """Weights for `seqs` (caller-chosen names), up to `width` tokens each: of a batch
+        whose sequences come and go, a new one when it changes. A sequence that one of
+        `carry` tracks, or whose parent there (`parents`: a fork's name to its parent's)
+        does, comes over with its weights and positions; the others start from none. A
+        sequence that has lost tokens to an eviction has to come over."""
         shape = (len(seqs), self.num_kv_heads, width)
-        return TokenWeights(list(seqs), torch.zeros(shape, device=self.device),
-                            torch.full(shape, -1, dtype=torch.int32, device=self.device),
-                            np.zeros(len(seqs), np.int64))
+        tw = TokenWeights(list(seqs), torch.zeros(shape, device=self.device),
+                          torch.full(shape, -1, dtype=torch.int32, device=self.device),
+                          np.zeros(len(seqs), np.int64))
+        for i, name in enumerate(seqs):
+            source = (parents or {}).get(name, name)
+            old = next((t for t in carry if source in t.seqs), None)
+            if old is None:
+                continue
+            j, n = old.seqs.index(source), min(width, old.scores.shape[2])
+            tw.scores[i, :, :n] = old.scores[j, :, :n]
+            tw.positions[i, :, :n] = old.positions[j, :, :n]
+            tw.evicted[i], tw.settled[i] = old.evicted[j], old.settled[j]
+        return tw
+
+    def _tracked(self, tw: TokenWeights, names: Dict) -> List[int]:
+        """The pool's ids of tw's sequences, whose evictions tw has to know of: a row that
+        does not takes kept tokens for the first ones of the text."""
+        ids = [names[s] for s in tw.seqs]
+        if len(set(ids)) != len(ids):
+            raise ValueError("a sequence appears twice")
+        for s, i, n in zip(tw.seqs, ids, tw.evicted):
+            if self.pool.evicted.get(i, 0) != n:
+                raise ValueError(f"sequence {s!r} has lost {self.pool.evicted.get(i, 0)} tokens to "
+                                 f"evictions, {n} in these weights: carry its row over "
+                                 "(track_weights)")
+        return ids
 
     def accumulate_step(self, si: StepInputs, tw: TokenWeights, scale: float,
                         accepted: Optional[Sequence[int]] = None) -> None:
@@ -244,6 +273,8 @@ class PagedKVCache:
         first on; the tokens of the others are those that truncate() takes back, before
         or after this call. Host numbers, so such a call is not captured. Without it
         every query counts, and what rejected ones gave stays in the sums."""
+        if si.seqs is not None and list(si.seqs) != tw.seqs:
+            raise ValueError(f"the step is of {list(si.seqs)}, the weights of {tw.seqs}")
         q, lens, start = si.q, si.context_lens, si.query_start_loc
         if accepted is not None:
             runs = np.asarray(si.q_lens, np.int64)
@@ -275,7 +306,7 @@ class PagedKVCache:
         sequence; a shorter sequence stays as it is), as rejected draft tokens, and the
         weights they received: the next tokens in their slots start from none. Tokens that
         an eviction left stand in no order and cannot be cut by their slots."""
-        ids = [names[s] for s in tw.seqs]
+        ids = self._tracked(tw, names)
         now = np.array([self.pool.seq_len(i) for i in ids], np.int64)
         new = np.minimum(np.broadcast_to(np.asarray(lens, np.int64), now.shape), now)
         if (new < 0).any():
@@ -300,9 +331,7 @@ class PagedKVCache:
         written become its own (copied where shared), the kept tokens are chosen
         per KV head, their rows moved, and the freed blocks given back. Where the
         pool cannot cover the copies it raises, and no token has gone."""
-        ids = [names[s] for s in tw.seqs]
-        if len(set(ids)) != len(ids):
-            raise ValueError("a sequence appears twice")
+        ids = self._tracked(tw, names)
         lens = np.array([self.pool.seq_len(i) for i in ids], np.int64)
         kept = np.minimum(np.broadcast_to(np.asarray(keep, np.int64), lens.shape), lens)
         if (kept < 0).any():
@@ -336,6 +365,7 @@ class PagedKVCache:
         for i, n in zip(ids, kept):
             self.pool.seq_truncate(i, int(n))
         tw.evicted += lens - kept
+        self.pool.evicted.update((i, int(n)) for i, n in zip(ids, tw.evicted) if n)
         tw.settled = np.where(kept < lens, kept, tw.settled)
 
     def capture(self, fn, *args) -> "torch.cuda.CUDAGraph":

@@ -335,3 +335,38 @@ def test_accepted_queries_are_within_their_runs():
     for bad in ([4, 0], [3], [-1, 1], [2, 2]):
         with pytest.raises(ValueError, match="accepted"):
             cache.accumulate_step(si, tw, 0.125, bad)
+
+
+def test_weights_come_over_when_the_batch_changes():
+    import torch
+    cache, names, tw = cpu_engine(a=60, b=40)
+    tw.positions[0, :, :32] = torch.randperm(32).int()
+    tw.evicted[0] = cache.pool.evicted[names["a"]] = 28     # as after an eviction of a
+    tw.settled[0] = 32
+    names["f"] = cache.pool.seq_fork(names["a"])
+    names["n"] = cache.pool.seq_create()
+    for seqs in (["a"], ["f"], ["n", "a"]):     # a fork has its parent's tokens
+        for call in (lambda t: cache.evict(t, names, 8), lambda t: cache.truncate(t, names, 50)):
+            with pytest.raises(ValueError, match="lost 28 tokens to evictions, 0 in these"):
+                call(cache.track_weights(seqs, 128))
+    assert cache.pool.seq_len(names["a"]) == 60
+    new = cache.track_weights(["n", "f", "b", "a"], 100, carry=[tw], parents={"f": "a"})
+    assert new.evicted.tolist() == [0, 28, 0, 28] and new.settled.tolist() == [0, 32, 0, 32]
+    for i, j in ((1, 0), (2, 1), (3, 0)):
+        assert torch.equal(new.scores[i], tw.scores[j, :, :100])
+        assert torch.equal(new.positions[i], tw.positions[j, :, :100])
+    assert not new.scores[0].any() and (new.positions[0] == -1).all()
+    cache.truncate(new, names, 50)              # known to all of them
+    new.scores[3] = 9
+    assert tw.scores[0, 0, 5] == 6              # rows of its own
+    cache.pool.seq_free(names["f"])
+    assert names["f"] not in cache.pool.evicted and names["a"] in cache.pool.evicted
+
+
+def test_a_step_of_other_sequences_is_refused():
+    from types import SimpleNamespace
+    cache, names, tw = cpu_engine(a=60, b=40)
+    si = SimpleNamespace(q=None, context_lens=None, query_start_loc=None, q_lens=[1, 1],
+                         seqs=["b", "a"])
+    with pytest.raises(ValueError, match="weights of"):
+        cache.accumulate_step(si, tw, 0.125)

@@ -116,3 +116,67 @@ def test_rejected_drafts_leave_nothing_behind(kv, first):
     assert (tw.evicted > 0).any()
     with pytest.raises(ValueError, match="eviction"):
         cache.truncate(tw, names, 1)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int4"])
+def test_a_batch_that_changes_keeps_its_weights(kv):
+    """A sequence ends, another joins and one that was evicted from is forked; the rest
+    come over into new weights. Sinks and recent tokens stay those of the text."""
+    H, Hkv, d, budget, sinks, recent, scale = 8, 2, 64, 48, 4, 12, 0.125
+    gen = torch.Generator().manual_seed(6)
+
+    def rows(n, heads=Hkv):
+        return torch.randn((n, heads, d), generator=gen).to(torch.bfloat16)
+
+    cache, names, model = PagedKVCache(64, Hkv, d, kv), {}, {}
+
+    def join(s, n):
+        k, v = rows(n), rows(n)
+        cache.run_phase([Op(seq=s), Op(seq=s, k=k, v=v)], names)
+        model[s] = Model(kv, Hkv)
+        model[s].append(k, v)
+
+    def steps(seqs, tw, count):
+        for _ in range(count):
+            new = [(rows(1), rows(1)) for _ in seqs]
+            q = rows(len(seqs), H)
+            si = cache.prepare_step([Op(seq=s, k=k, v=v) for s, (k, v) in zip(seqs, new)], names,
+                                    q)
+            cache.write_step(si)
+            cache.accumulate_step(si, tw, scale)
+            for b, (s, (k, v)) in enumerate(zip(seqs, new)):
+                model[s].append(k, v)
+                for g, m in enumerate(model[s].heads):
+                    p = ref.probabilities(q[b:b + 1, g * 4:g * 4 + 4].double().numpy(), m[0], scale)
+                    m[2] = m[2] + p.sum((0, 1))
+                    w = tw.scores[b, g].double().cpu().numpy()
+                    assert np.allclose(w[:len(m[2])], m[2], rtol=REL, atol=1e-7)
+                    m[2] = w[:len(m[2])]
+            cache.evict(tw, names, budget, sinks, recent)
+            for b, s in enumerate(seqs):
+                L, n = len(model[s]), min(budget, len(model[s]))
+                for g, m in enumerate(model[s].heads):
+                    mv, _, _ = ref.select(m[2], m[3], L, n, model[s].seen, sinks, recent)
+                    for x in m:
+                        x[mv[:, 1]] = x[mv[:, 0]]
+                    model[s].heads[g] = [x[:n] for x in m]
+                    pos = tw.positions[b, g, :n].cpu().numpy()
+                    real = np.where(pos < 0, model[s].seen - n + np.arange(n), pos)
+                    assert np.array_equal(real, model[s].heads[g][3])
+                    assert set(range(min(sinks, n))) <= set(real) and model[s].seen - 1 in real
+        return tw
+
+    for s, n in (("a", 70), ("b", 30), ("c", 45)):
+        join(s, n)
+    tw = steps(["a", "b", "c"], cache.track_weights(["a", "b", "c"], 96), 6)
+    cache.pool.seq_free(names.pop("b"))
+    join("d", 60)
+    cache.run_phase([Op(parent="a", child="f")], names)
+    twin = Model(kv, Hkv)
+    twin.seen, twin.heads = model["a"].seen, [[x.copy() for x in m] for m in model["a"].heads]
+    model["f"] = twin
+    seqs = ["d", "c", "f", "a"]
+    tw = cache.track_weights(seqs, 80, carry=[tw], parents={"f": "a"})
+    steps(seqs, tw, 8)
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
