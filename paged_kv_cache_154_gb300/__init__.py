@@ -309,25 +309,88 @@ class Pool:
 # device operations (torch tensors in, nothing allocated)
 # ---------------------------------------------------------------------------
 
+def _shaped(shape, dtype, *named) -> None:
+    """Every (name, tensor) has this shape and type (tensors that are None may)."""
+    for name, t in named:
+        if t is not None and (t.shape != shape or t.dtype is not dtype):
+            raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
+
+
+# What the library reads and writes through a pointer is sized by other tensors, so these
+# checks compare bytes: 0.8 us an append or read-back, where shapes and types took 2.4.
+def _sized(*named) -> None:
+    """Every (name, tensor, count, dtype) has so many elements of that type (tensors that
+    are None may: the library's own checks name what is missing)."""
+    for name, t, count, dtype in named:
+        if t is not None and (t.numel() != count or t.dtype is not dtype):
+            raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {count} of {dtype}")
+
+
+def _cache_sized(code, num_blocks, shape, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp) -> None:
+    """The arrays of a cache (k_cache of this shape) belong to one another: scales and zero
+    points per row (INT8), per INT4_GROUP elements of a row (INT4), scales per KV head (FP8)."""
+    if num_blocks > shape[0]:
+        raise ValueError(f"num_blocks {num_blocks}, k_cache has {shape[0]}")
+    size = k_cache.nbytes
+    n = (size * 2 // INT4_GROUP if code == PA_INT4 else size // shape[3] if code == PA_INT8 else
+         shape[1] if code == PA_FP8_E4M3 else 0)    # scales
+    if ((v_cache is None or v_cache.nbytes == size)
+            and (k_scale is None or k_scale.nbytes == 4 * n)
+            and (v_scale is None or v_scale.nbytes == 4 * n)
+            and (k_zp is None or k_zp.nbytes == n) and (v_zp is None or v_zp.nbytes == n)):
+        return
+    if n == 0 or code == PA_FP8_E4M3:               # not read
+        k_zp = v_zp = None
+    if n == 0:
+        k_scale = v_scale = None
+    torch = sys.modules["torch"]
+    _sized(("v_cache", v_cache, k_cache.numel(), k_cache.dtype),
+           ("k_scale", k_scale, n, torch.float32), ("v_scale", v_scale, n, torch.float32),
+           ("k_zp", k_zp, n, torch.int8), ("v_zp", v_zp, n, torch.int8))
+
+
+def _rows_sized(code, shape, T, key, value, slot_mapping) -> None:
+    """T rows of keys and of values as a cache of this shape holds them, and their slots."""
+    n = T * shape[1] * shape[3] * (2 if code == PA_INT4 else 1)
+    if (key.numel() != n or value.nbytes != key.nbytes or value.dtype is not key.dtype
+            or slot_mapping.nbytes != 8 * T):
+        _sized(("key", key, n, key.dtype), ("value", value, n, key.dtype),
+               ("slot_mapping", slot_mapping, T, sys.modules["torch"].int64))
+
+
+def _queries_sized(code, shape, q_shape, out) -> None:
+    """Queries are as wide as the rows of a cache of this shape, outputs as the queries."""
+    if q_shape[2] != (shape[3] * 2 if code == PA_INT4 else shape[3]):
+        raise ValueError(f"q is {tuple(q_shape)}, the cache {tuple(shape)}: not one head_dim")
+    if out is not None and out.numel() != q_shape[0] * q_shape[1] * q_shape[2]:
+        raise ValueError(f"out is {tuple(out.shape)}, q {tuple(q_shape)}")
+
+
 def copy_blocks(k_cache, v_cache, pairs, num_blocks: Optional[int] = None, k_scale=None,
                 v_scale=None, k_zp=None, v_zp=None, stream=None) -> None:
     """pa_copy_blocks; pairs: device int32 [n, 2] (src, dst)."""
     n = 0 if pairs is None else int(pairs.shape[0])
     if n == 0:
         return
-    nb = k_cache.shape[0] if num_blocks is None else num_blocks
+    shape, code = k_cache.shape, _dtype_code(k_cache)
+    nb = shape[0] if num_blocks is None else num_blocks
+    if code == PA_INT4:
+        _cache_sized(code, nb, shape, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp)
     _check(lib().pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                _ptr(k_zp), _ptr(v_zp), _ptr(pairs), n, nb,
-                                k_cache.shape[1], _head_dim(k_cache), k_cache.shape[2],
-                                _dtype_code(k_cache), _stream(stream)))
+                                _ptr(k_zp), _ptr(v_zp), _ptr(pairs), n, nb, shape[1],
+                                shape[3] * 2 if code == PA_INT4 else shape[3], shape[2], code,
+                                _stream(stream)))
 
 
 def append_kv(key, value, k_cache, v_cache, slot_mapping, num_blocks: Optional[int] = None,
               k_scale=None, v_scale=None, k_zp=None, v_zp=None, stream=None) -> None:
     """pa_append_kv; key/value [T, H_kv, d]; slot_mapping device int64 [T]."""
     T = int(key.shape[0])
-    nb = k_cache.shape[0] if num_blocks is None else num_blocks
     shape, code = k_cache.shape, _dtype_code(k_cache)
+    nb = shape[0] if num_blocks is None else num_blocks
+    if code == PA_INT4:
+        _cache_sized(code, nb, shape, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp)
+        _rows_sized(code, shape, T, key, value, slot_mapping)
     _check(lib().pa_append_kv(_ptr(key), _ptr(value), _dtype_code(key), _ptr(k_cache),
                               _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale), _ptr(k_zp),
                               _ptr(v_zp), _ptr(slot_mapping), T, nb, shape[1],
@@ -338,10 +401,13 @@ def append_kv(key, value, k_cache, v_cache, slot_mapping, num_blocks: Optional[i
 def gather_kv(key, value, k_cache, v_cache, slot_mapping, num_blocks: Optional[int] = None,
               k_scale=None, v_scale=None, k_zp=None, v_zp=None, stream=None) -> None:
     """pa_gather_kv: the inverse of append_kv; key/value [T, H_kv, d] (F16,
-    BF16 or F32) receive the cached rows at the values the cache holds."""
+    BF16 or F32) receive the cached rows at the values the cache holds;
+    slot_mapping device int64 [T]."""
     T = int(key.shape[0])
-    nb = k_cache.shape[0] if num_blocks is None else num_blocks
     shape, code = k_cache.shape, _dtype_code(k_cache)
+    nb = shape[0] if num_blocks is None else num_blocks
+    _cache_sized(code, nb, shape, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp)
+    _rows_sized(code, shape, T, key, value, slot_mapping)
     _check(lib().pa_gather_kv(_ptr(key), _ptr(value), _dtype_code(key), _ptr(k_cache),
                               _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale), _ptr(k_zp),
                               _ptr(v_zp), _ptr(slot_mapping), T, nb, shape[1],
@@ -373,15 +439,18 @@ def decode(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len
            workspace=None, stream=None) -> None:
     """pa_decode; out/q [num_q_tokens, H, d]; caches [num_blocks, H_kv, 16, d]."""
     num_seqs = int(context_lens.shape[0])
-    nq = int(q.shape[0])
-    nb = k_cache.shape[0] if num_blocks is None else num_blocks
+    q_shape, shape, code = q.shape, k_cache.shape, _dtype_code(k_cache)
+    nb = shape[0] if num_blocks is None else num_blocks
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if code == PA_INT4:
+        _cache_sized(code, nb, shape, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp)
+        _queries_sized(code, shape, q_shape, out)
     _check(lib().pa_decode(_ptr(out), _dtype_code(out), _ptr(q), _dtype_code(q), _ptr(k_cache),
-                           _ptr(v_cache), _dtype_code(k_cache), _ptr(k_scale), _ptr(v_scale),
+                           _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale),
                            _ptr(k_zp), _ptr(v_zp), _ptr(block_tables), block_tables.shape[1],
-                           _ptr(context_lens), _ptr(query_start_loc), num_seqs, nq,
-                           max_q_len if query_start_loc is not None else 1, q.shape[1],
-                           k_cache.shape[1], q.shape[2], k_cache.shape[2], nb, float(scale),
+                           _ptr(context_lens), _ptr(query_start_loc), num_seqs, q_shape[0],
+                           max_q_len if query_start_loc is not None else 1, q_shape[1],
+                           shape[1], q_shape[2], shape[2], nb, float(scale),
                            int(max_context_len), int(partition_size), _ptr(workspace), ws_bytes,
                            _stream(stream)))
 
@@ -420,13 +489,6 @@ def decode_shared_prefix(out, q, k_cache, v_cache, block_tables, context_lens,
 # eviction by accumulated attention weight
 # ---------------------------------------------------------------------------
 
-def _shaped(shape, dtype, *named) -> None:
-    """Every (name, tensor) has this shape and type (tensors that are None may)."""
-    for name, t in named:
-        if t is not None and (t.shape != shape or t.dtype is not dtype):
-            raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
-
-
 def accumulate_weights_workspace_size(num_seqs: int, num_q_tokens: int, num_heads: int,
                                       num_kv_heads: int, head_dim: int, max_q_len: int,
                                       max_context_len: int) -> int:
@@ -443,20 +505,24 @@ def accumulate_weights(scores_out, scores_in, q, k_cache, block_tables, context_
     accumulate_weights_workspace_size() bytes; other arguments as decode()."""
     torch = sys.modules["torch"]
     num_seqs = context_lens.shape[0]
-    shape = (num_seqs, k_cache.shape[1], scores_out.shape[2])
+    cache, q_shape = k_cache.shape, q.shape
+    shape = (num_seqs, cache[1], scores_out.shape[2])
     _shaped(shape, torch.float32, ("scores_out", scores_out), ("scores_in", scores_in))
     _shaped((num_seqs,), torch.int32, ("context_lens", context_lens))
     _shaped((num_seqs, block_tables.shape[1]), torch.int32, ("block_tables", block_tables))
     _shaped((num_seqs + 1,), torch.int32, ("query_start_loc", query_start_loc))
-    nb = k_cache.shape[0] if num_blocks is None else num_blocks
+    code = _dtype_code(k_cache)
+    nb = cache[0] if num_blocks is None else num_blocks
+    _cache_sized(code, nb, cache, k_cache, None, k_scale, None, k_zp, None)
+    _queries_sized(code, cache, q_shape, None)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().pa_accumulate_weights(
         _ptr(scores_out), _ptr(scores_in), shape[2], _ptr(q), _dtype_code(q), _ptr(k_cache),
-        _dtype_code(k_cache), _ptr(k_scale), _ptr(k_zp), _ptr(block_tables),
+        code, _ptr(k_scale), _ptr(k_zp), _ptr(block_tables),
         block_tables.shape[1], _ptr(context_lens), _ptr(query_start_loc), num_seqs,
-        int(q.shape[0]), max_q_len if query_start_loc is not None else 1, q.shape[1],
-        k_cache.shape[1], q.shape[2], k_cache.shape[2], nb, float(scale), int(max_context_len),
-        _ptr(workspace), ws_bytes, _stream(stream)))
+        q_shape[0], max_q_len if query_start_loc is not None else 1, q_shape[1], cache[1],
+        q_shape[2], cache[2], nb, float(scale), int(max_context_len), _ptr(workspace), ws_bytes,
+        _stream(stream)))
 
 
 def evict_select(moves, move_counts, scores_out, positions_out, scores, positions, context_lens,
@@ -494,8 +560,10 @@ def move_tokens(k_cache, v_cache, block_tables, context_lens, moves, move_counts
     _shaped((num_seqs,), torch.int32, ("context_lens", context_lens))
     _shaped((num_seqs, blocks), torch.int32, ("block_tables", block_tables))
     nb = cache[0] if num_blocks is None else num_blocks
+    code = _dtype_code(k_cache)
+    _cache_sized(code, nb, cache, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp)
     _check(lib().pa_move_tokens(
-        _ptr(k_cache), _ptr(v_cache), _dtype_code(k_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale),
         _ptr(k_zp), _ptr(v_zp), _ptr(block_tables), blocks, _ptr(context_lens), _ptr(moves),
         max_moves, _ptr(move_counts), num_seqs, heads, _head_dim(k_cache), cache[2], nb,
         int(max_context_len), _stream(stream)))
@@ -516,10 +584,14 @@ def decode_no_alloc(out, q, k_cache, v_cache, block_tables, context_lens, max_co
     (for callers that cannot allocate device memory); same arguments as
     decode() minus the workspace."""
     num_seqs = int(context_lens.shape[0])
-    nb = k_cache.shape[0] if num_blocks is None else num_blocks
+    shape, code = k_cache.shape, _dtype_code(k_cache)
+    nb = shape[0] if num_blocks is None else num_blocks
+    if code == PA_INT4:
+        _cache_sized(code, nb, shape, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp)
+        _queries_sized(code, shape, q.shape, out)
     _check(lib().pa_decode_no_alloc(
         _ptr(out), _dtype_code(out), _ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache),
-        _dtype_code(k_cache), _ptr(k_scale), _ptr(v_scale), _ptr(k_zp), _ptr(v_zp),
+        code, _ptr(k_scale), _ptr(v_scale), _ptr(k_zp), _ptr(v_zp),
         _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), _ptr(query_start_loc),
         num_seqs, int(q.shape[0]), max_q_len if query_start_loc is not None else 1, q.shape[1],
         k_cache.shape[1], q.shape[2], k_cache.shape[2], nb, float(scale), int(max_context_len),
