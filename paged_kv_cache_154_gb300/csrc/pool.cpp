@@ -305,6 +305,10 @@ pa_status append(pa_pool* p, int32_t seq, int32_t n_tokens, int64_t* slots_out,
         cow_pair_out[0] = src;
         cow_pair_out[1] = dst;
         *n_cow = 1;
+    } else if (p->pc_on && L % bs != 0) {
+        // a tail that was cut out of a registered block: about to be written in place, it
+        // must not be handed out for its old prefix any more
+        unregister_block(p, table.back());
     }
     for (int64_t i = 0; i < n_tokens; ++i) {
         int64_t pos = L + i;
@@ -449,10 +453,7 @@ extern "C" pa_status pa_seq_truncate(pa_pool* p, int32_t seq, int32_t n_tokens) 
     }
     table.resize(nb);
     p->lens[seq] = n_tokens;
-    // a block that is now partly filled will be written again by the next append: it
-    // must not be handed out for the prefix it was registered under
-    if (p->pc_on && n_tokens % p->block_size) unregister_block(p, table.back());
-    p->seq_known[seq] = 0;
+    p->seq_known[seq] = 0;   // a cut block stays registered until it is written (append)
     return PA_OK;
 }
 

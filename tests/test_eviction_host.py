@@ -127,6 +127,32 @@ def test_a_truncated_block_is_not_handed_out_for_its_old_prefix(cut):
     assert not set(table(p, c)) & set(table(p, a)[cut // 16:])
 
 
+@pytest.mark.parametrize("release", ["never", "before", "after"])
+def test_a_cut_block_that_others_hold_keeps_serving(release):
+    p = pa.Pool(16)
+    p.enable_prefix_cache(16)
+    toks = list(range(48))
+    a, _ = p.create_with_prefix(toks)
+    p.append_tokens(a, toks)
+    b, hit = p.create_with_prefix(toks + [1])
+    blocks = table(p, a)
+    assert hit == 48 and table(p, b) == blocks
+    p.seq_truncate(a, 23)                     # the second block is cut, but b has it whole
+    c, hit = p.create_with_prefix(toks + [9])
+    assert hit == 48 and table(p, c) == blocks
+    p.seq_free(c)
+    if release == "before":
+        p.seq_free(b)                         # now a is its only holder
+    _, pair = p.seq_append_slots(a, 3)        # into a copy while b has it, else in place
+    assert (pair is None) == (release == "before")
+    if release == "after":
+        p.seq_free(b)
+    d, hit = p.create_with_prefix(toks + [9])
+    assert hit == (16 if release == "before" else 48)
+    assert table(p, d)[1:] == ([] if release == "before" else blocks[1:])
+    assert table(p, a)[0] == blocks[0] and (table(p, a)[1] == blocks[1]) == (release == "before")
+
+
 def test_plain_selection_keeps_the_budget():
     """The plain form itself: the kept tokens by hand."""
     w = np.array([5, 1, 4, 4, 0, 9, 4], np.float32)
