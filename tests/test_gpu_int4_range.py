@@ -9,7 +9,7 @@ import torch
 import paged_kv_cache_154_gb300 as pa
 from gpu_harness import half_ulp
 from oracle import compressed as ref
-from test_gpu_int4 import REL, decode, new_cache, sequences
+from test_gpu_int4 import REL, bits, decode, host_append, new_cache, sequences
 
 pytestmark = pytest.mark.gpu
 
@@ -194,3 +194,73 @@ def test_small_averages_over_long_shares(H, d):
         e, w = err[..., half::2].norm(), want[..., half::2].norm()
         print(f"half {half}: {e / w:.2e} of the norm, which is {w / mag[..., half::2].norm():.1e}")
         assert e <= 2.0 ** -11 * w
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sign", ["mixed", "positive", "negative"])
+def test_append_at_the_ends_of_fp32_is_the_quantiser(d, sign):
+    """Groups whose range is subnormal, next to 1e-28 and 1e30 (where the append changes
+    its way of dividing) or near the largest that is finite: codes, scales and zero points
+    bit for bit, and read back at their values."""
+    factors = torch.tensor([1e-40, 1e-39, 1e-38, 1e-37, 1e-31, 1e-29, 1.7e-29, 2e-29, 2.3e-29,
+                            2.7e-29, 3e-29, 1e-28, 1e-20, 1e29, 1.7e29, 2e29, 2.3e29, 2.7e29,
+                            3e29, 1e30, 1e31, 1e33, 1e36, 3e37], dtype=torch.float64)
+    T, H = 40 * len(factors), 3
+    gen = torch.Generator().manual_seed(d)
+    rows = []
+    for _ in range(2):
+        x = torch.randn((T, H, d), generator=gen, dtype=torch.float64).clamp(-4.5, 4.5)
+        x = {"mixed": x, "positive": x.abs(), "negative": -x.abs()}[sign]
+        x[::7, :, ::5] = 0
+        rows.append((x * factors[torch.randint(len(factors), (T, 1, 1), generator=gen)]).bfloat16())
+    nb = T // 16 + 4
+    slots = torch.randperm(nb * 16, generator=gen)[:T]
+    cache = new_cache(nb, H, d)
+    on = (cache.k, cache.v, slots.cuda(), nb, cache.k_scale, cache.v_scale, cache.k_zp, cache.v_zp)
+    pa.append_kv(rows[0].cuda(), rows[1].cuda(), *on)
+    back = {t: [torch.empty((T, H, d), dtype=t, device="cuda") for _ in range(2)]
+            for t in (torch.float32, torch.bfloat16)}
+    for out in back.values():
+        pa.gather_kv(*out, *on)
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
+    both = []
+    for i, (x, got) in enumerate(((rows[0], (cache.k, cache.k_scale, cache.k_zp)),
+                                  (rows[1], (cache.v, cache.v_scale, cache.v_zp)))):
+        f = x.float().numpy()
+        assert np.isfinite(f).all()
+        span = (np.maximum(f.reshape(T, H, -1, 64).max(-1), 0) -
+                np.minimum(f.reshape(T, H, -1, 64).min(-1), 0))
+        assert np.isfinite(span).all()
+        both += [((span > lo) & (span < hi)).any() for lo, hi in
+                 ((0, 1e-37), (5e-29, 1e-28), (1e-28, 2e-28), (5e29, 1e30), (1e30, 2e30), (1e37, 3e38))]
+        want = host_append((nb, H, 16, d // 2), f, slots.numpy())
+        for a, b in zip(got, want):
+            assert np.array_equal(bits(a), np.ascontiguousarray(b).view(np.uint8).reshape(-1))
+        held = ref.values_int4(*ref.quantise_int4(f))
+        assert np.array_equal(back[torch.float32][i].cpu().numpy(), held.astype(np.float32))
+        assert torch.equal(back[torch.bfloat16][i].cpu(),
+                           torch.from_numpy(held.astype(np.float32)).bfloat16())
+    assert all(both)                          # every side of both thresholds is met
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_group_that_is_not_finite_touches_no_other(bad):
+    T, H, d, nb = 50, 3, 128, 8
+    gen = torch.Generator().manual_seed(2)
+    x = torch.randn((T, H, d), generator=gen).bfloat16()
+    y = x.clone()
+    y[7, 1, 70] = bad
+    y[9, 2, 3] = bad
+    slots = torch.randperm(nb * 16, generator=gen)[:T]
+    caches = []
+    for rows in (x, y):
+        c = new_cache(nb, H, d)
+        pa.append_kv(rows.cuda(), rows.cuda(), c.k, c.v, slots.cuda(), nb, c.k_scale, c.v_scale,
+                     c.k_zp, c.v_zp)
+        caches.append([a.reshape(nb, H, 16, 2, -1)[slots.cuda() // 16, :, slots.cuda() % 16]
+                       .cpu().contiguous().view(torch.uint8) for a in c.arrays()])
+    keep = torch.ones((T, H, 2), dtype=torch.bool)
+    keep[7, 1, 1] = keep[9, 2, 0] = False
+    for a, b in zip(*caches):
+        assert torch.equal(a[keep], b[keep])
