@@ -223,12 +223,12 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
 // (scale, zero point) per 64 elements. 8 threads a row; a thread holds 8
 // consecutive elements of every group of the K row and of the same V row (16-byte
 // loads, 4-byte code stores), and a group's range is reduced over the 8 with
-// shuffles. 2 bytes in and 0.58 out an element: bound by instruction issue before memory, so indexes are 32 bits wide
-// (their 64-bit divisions alone cost a third of the kernel), a thread's index
-// arithmetic serves every group of a row, and quotients come from one reciprocal a
-// group; the rows are asked for before the slot is known. 16384 tokens of 8 heads of
-// 128 elements, with the gather that reads them back: 32.8 us, 37.3 us with a thread a
-// group, 59 us with a division an element.
+// shuffles. 2 bytes in and 0.58 out an element: bound by instruction issue before
+// memory, so indexes are 32 bits wide (their 64-bit divisions alone cost a third of
+// the kernel), a thread's index arithmetic serves every group of a row, and
+// quotients come from one reciprocal a group; the rows are asked for before the
+// slot is known. 16384 tokens of 8 heads of 128 elements, with the gather that reads
+// them back: 32.8 us, 37.3 us with a thread a group, 59 us with a division an element.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) append_kv_int4_kernel(
     const T* __restrict__ key, const T* __restrict__ value, uint8_t* __restrict__ k_cache,
