@@ -6,6 +6,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <exception>
 #include <mutex>
 #include <vector>
 
@@ -78,9 +79,20 @@ pa_status check_shape(int32_t num_kv_heads, int32_t head_dim, int32_t block_size
     return PA_OK;
 }
 
+// n zeros; an exception must not leave a C entry
+template <typename T>
+pa_status zeros(std::vector<T>& h, size_t n) {
+    try {
+        h.assign(n, T());
+    } catch (const std::exception&) {
+        return fail(PA_ERR_INVALID_ARG, "validate: no host memory for %zu elements", n);
+    }
+    return PA_OK;
+}
+
 template <typename T>
 pa_status to_host(std::vector<T>& h, const T* d, size_t n, cudaStream_t st) {
-    h.resize(n);
+    if (pa_status s = zeros(h, n)) return s;
     if (n == 0) return PA_OK;
     if (pa_status s = pa::cuda_status(cudaStreamSynchronize(st), "validate: sync")) return s;
     return pa::cuda_status(cudaMemcpy(h.data(), d, n * sizeof(T), cudaMemcpyDeviceToHost),
@@ -123,7 +135,8 @@ extern "C" pa_status pa_copy_blocks(void* k_cache, void* v_cache, void* k_scale,
     if (pa::validate_enabled()) {
         std::vector<int32_t> h;
         if (pa_status s = to_host(h, d_pairs, 2 * (size_t)n_pairs, st)) return s;
-        std::vector<uint8_t> role(num_blocks, 0);   // 1 = source, 2 = destination
+        std::vector<uint8_t> role;   // 1 = source, 2 = destination
+        if (pa_status s = zeros(role, (size_t)num_blocks)) return s;
         for (int32_t i = 0; i < 2 * n_pairs; ++i) {
             int32_t b = h[i];
             if (b < 0 || b >= num_blocks)
@@ -384,7 +397,7 @@ pa_status validate_moves(const int32_t* block_tables, int32_t max_blocks_per_seq
         if (counts[r] < 0 || counts[r] > max_moves)
             return fail(PA_ERR_VALIDATION, "row %zu has %d moves of at most %d", r, counts[r],
                         max_moves);
-        role.assign((size_t)L, 0);   // 1 = source, 2 = destination
+        if (pa_status s = zeros(role, (size_t)L)) return s;   // 1 = source, 2 = destination
         for (int32_t i = 0; i < 2 * counts[r]; ++i) {
             const int32_t slot = mv[r * max_moves * 2 + i];
             const uint8_t want = (i % 2) ? 2 : 1;

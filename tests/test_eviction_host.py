@@ -396,3 +396,22 @@ def test_a_step_of_other_sequences_is_refused():
                          seqs=["b", "a"])
     with pytest.raises(ValueError, match="weights of"):
         cache.accumulate_step(si, tw, 0.125)
+
+
+def test_validation_without_host_memory_is_an_error():
+    """PA_VALIDATE copies a call's slots to the host: where they do not fit, the call
+    returns. In a process of its own that sees no GPU."""
+    import os
+    import subprocess
+    import sys
+    code = ("import resource, paged_kv_cache_154_gb300 as pa\n"
+            "lib = pa.lib()\n"
+            "now = int(open('/proc/self/statm').read().split()[0]) * resource.getpagesize()\n"
+            "resource.setrlimit(resource.RLIMIT_AS, (now + (1 << 30),) * 2)\n"
+            f"s = lib.pa_gather_kv(*{list(dict(GATHER, T=(1 << 31) - 1).values())!r})\n"
+            "print(s, lib.pa_last_error().decode())\n")
+    env = dict(os.environ, PA_VALIDATE="1", CUDA_VISIBLE_DEVICES="")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.startswith("1 ") and "host memory" in r.stdout, r.stdout
