@@ -950,9 +950,11 @@ __global__ void __launch_bounds__(32 * kManyWarps) many_kernel(const Params p) {
 }
 
 // Tokens of a logits CTA: one wave of four CTAs a SM where a tile of up to
-// kMaxTile does that (fewer starts: 100001 tokens of 8 heads 30.6 us against 32.6
-// with 512), else 512, whose many waves even out a ragged batch (Llama-3-8B step:
-// 64.7 us, 70.9 with 2048).
+// kMaxTile does that (fewer starts: 100001 tokens of 8 heads 41.7 us against 44.5
+// with 512 in bf16, 24.6 against 29.8 in 4 bits), else 512, whose many waves even out
+// a ragged batch (Llama-3-8B step: 63.4 us, 68.2 with 2048; 45.8 and 46.9 in 4 bits).
+// Few long contexts or even ones would rather have 2048 there too (2 of 131072 tokens:
+// 108.1 us, 103.1; 69.4 and 64.9 in 4 bits), but the host does not see the lengths.
 constexpr int kMinTile = 128;
 static_assert(kManyTokens >= kMinTile, "stats are sized for tiles of kMinTile");
 int stored_tile(int64_t tokens) {
@@ -961,8 +963,11 @@ int stored_tile(int64_t tokens) {
 }
 
 // Up to as many tiles the warps of the last pass merge their rows' (m, l) themselves, by
-// one batch of loads; beyond, a kernel between the passes does it once (8 prompts of 4001
-// tokens, 16 tiles: 34.9 us, 35.7 with that kernel; of 8192, 32 tiles: 56.7 and 53.9).
+// one batch of loads; beyond, a kernel between the passes does it once. 8 prompts, 4 heads
+// of 128 rows, d = 64: of 3900 tokens (16 tiles) 36.4 us, 37.0 with that kernel; of 5000
+// (20) 40.3 and 40.0; of 6000 (24) 42.2 and 41.4; of 8192 (32) 58.1 and 54.6. 2 prompts, 8
+// heads of 64 rows, d = 128: of 3900 19.0 and 20.3, of 4300 (17) 19.8 and 20.5, of 5000 31.6
+// and 31.1, of 6000 34.8 and 32.9.
 constexpr int kFoldTiles = 16;
 
 // A call computes its logits twice in a workspace of stats and sums, whose sizes grow

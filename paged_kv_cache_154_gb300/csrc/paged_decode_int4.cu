@@ -66,8 +66,11 @@ constexpr int kWholeTokens = 256;  // a warp walks them in the time of the merge
 // Warps of a CTA and CTAs of an SM, as many as the registers allow. One CTA of 12
 // warps: its warps run at one pace, where of three CTAs of 4 the older ones ran ahead
 // (a loop of 85, 98 and 113 thousand cycles for the same number of blocks) and left the
-// SM to the last (68.3 us against 70.5 for the long-context step). Two CTAs with 16 query
-// rows, where it made no such difference (55.0 us for the verify step, 55.8 in one).
+// SM to the last (68.3 us against 70.5 for the long-context step; with d = 64 28.2
+// against 31.4 for a batch step, 55.2 and 56.4 for a long-context one). With 16 query rows
+// two CTAs of 4 at d = 128, all that fits, where it made no such difference (55.0 us for
+// the verify step, 55.8 in one CTA of 8); at d = 64 12 warps fit again (40.2 us in one CTA,
+// 40.5 in three).
 constexpr int ctas_per_sm(int d, int nr) { return d == 128 && nr == 2 ? 2 : 1; }
 constexpr int worker_warps(int d, int nr) { return d == 128 && nr == 2 ? 4 : 12; }
 
