@@ -39,9 +39,9 @@
 // further chunks. Contexts of at most kWholeTokens are not cut.
 //
 // Measured, whole calls: 64 sequences of 512-4096 tokens, 32 query heads over 8
-// (157 MB) 37.4 us, 4.2 TB/s; 4 sequences of 32768-131072 (324 MB) 63.2 us, 5.1
+// (157 MB) 37.4 us, 4.2 TB/s; 4 sequences of 32768-131072 (324 MB) 64.0 us, 5.1
 // TB/s, 75 % of the copy rate; a verify step of 16 to 40 rows per KV head (74 MB)
-// 50.2 us. A block of 16 tokens takes 245 instructions, of which 70 mask, and the
+// 50.1 us. A block of 16 tokens takes 245 instructions, of which 70 mask, and the
 // schedulers issue 0.57 a cycle.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
