@@ -235,7 +235,8 @@ class PagedKVCache:
         whose sequences come and go, a new one when it changes. A sequence that one of
         `carry` tracks, or whose parent there (`parents`: a fork's name to its parent's)
         does, comes over with its weights and positions; the others start from none. A
-        sequence that has lost tokens to an eviction has to come over."""
+        sequence that has lost tokens to an eviction has to come over; rows go by name,
+        so a name given to a new sequence is not to be found in `carry`."""
         shape = (len(seqs), self.num_kv_heads, width)
         tw = TokenWeights(list(seqs), torch.zeros(shape, device=self.device),
                           torch.full(shape, -1, dtype=torch.int32, device=self.device),
