@@ -285,6 +285,62 @@ pa_status pa_append_kv(const void* key, const void* value, pa_dtype src_dtype,
                        int32_t num_kv_heads, int32_t head_dim,
                        int32_t block_size, void* stream);
 
+/* Rotary positions: the rows of every head turned by their token's position. A
+ * row's first rotary_dim elements are pairs, and pair f turns by the angle whose
+ * cosine and sine the table holds at the token's position: a' = a cos - b sin,
+ * b' = b cos + a sin, products and sums each rounded to fp32, the result once more
+ * to dtype. Elements from rotary_dim on are copied bit for bit.
+ *   q, k           rows [num_tokens][num_heads][head_dim] (k: num_kv_heads) of
+ *                  dtype (F16 or BF16); token t's heads start at t * q_stride
+ *                  (elements; so they may be parts of a wider row, such as a fused
+ *                  projection's), each head's rows follow one another. Either may
+ *                  be absent (its heads 0, NULL).
+ *   q_out, k_out   as q and k, each with a stride of its own; q_out may be q, and
+ *                  k_out k (the same pointer and stride); no other overlap
+ *   cos_sin        fp32 [max_positions][rotary_dim]: cosines of the rotary_dim / 2
+ *                  frequencies, then their sines (any factor of theirs included)
+ *   rotary_dim     a multiple of 16 up to head_dim
+ *   interleaved    0: pair f is elements f and rotary_dim / 2 + f; else 2f and 2f + 1
+ *   positions      int32 [num_axes][num_tokens], each in [0, max_positions). A token
+ *                  with a position outside is left out (none of its rows written)
+ *                  with PA_DEVERR_BAD_SLOT.
+ *   num_axes       1 (text) to 4
+ *   freq_axis      uint8 [rotary_dim / 2]: the axis whose position frequency f takes
+ *                  (images and video: time, height, width); not read with one axis,
+ *                  when it may be NULL. A value of num_axes or more leaves every
+ *                  token out, as above.
+ *   inverse        not 0: turned the other way (sin negated), which takes a rotation
+ *                  back and is its gradient
+ * Strides are multiples of 8 of at least a token's rows; rows and cos_sin are 16-byte
+ * aligned. head_dim 64 or 128. */
+pa_status pa_rope(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                  int32_t num_heads, void* k_out, int64_t k_out_stride, const void* k,
+                  int64_t k_stride, int32_t num_kv_heads, pa_dtype dtype, const float* cos_sin,
+                  int32_t max_positions, int32_t rotary_dim, int32_t interleaved,
+                  const int32_t* positions, int32_t num_axes, const uint8_t* freq_axis,
+                  int32_t inverse, int32_t num_tokens, int32_t head_dim, void* stream);
+
+/* pa_rope and pa_append_kv in one pass: q rotated into q_out, key rotated and
+ * appended to the cache through slot_mapping, value appended as it is. Where the
+ * cache is 16-bit it receives what pa_rope gives; an INT8, FP8 or INT4 cache
+ * receives the codes of the rotated fp32 values (pa_append_kv's formulas, without a
+ * rounding to 16 bits in between).
+ *   q, q_out       as in pa_rope (absent: num_heads 0)
+ *   key_out        the rotated keys as rows, for attention outside the cache
+ *                  (pa_prompt_attention), or NULL; may be key (the same stride)
+ *   slot_mapping   as in pa_append_kv: a token with a negative slot leaves the cache
+ *                  as it was; its rows of q_out and key_out are written
+ * Other arguments as in pa_rope and pa_append_kv. A token with a position outside
+ * cos_sin is left out whole (PA_DEVERR_BAD_SLOT). */
+pa_status pa_rope_append_kv(
+    void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, int32_t num_heads,
+    void* key_out, int64_t key_out_stride, const void* key, int64_t key_stride, const void* value,
+    int64_t value_stride, pa_dtype src_dtype, void* k_cache, void* v_cache, pa_dtype kv_dtype,
+    float* k_scale, float* v_scale, int8_t* k_zp, int8_t* v_zp, const int64_t* slot_mapping,
+    const float* cos_sin, int32_t max_positions, int32_t rotary_dim, int32_t interleaved,
+    const int32_t* positions, int32_t num_axes, const uint8_t* freq_axis, int32_t num_tokens,
+    int32_t num_blocks, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, void* stream);
+
 /* Read cached rows back through a slot mapping, at the values the cache holds:
  * key, value [num_tokens][num_kv_heads][head_dim] of out_dtype (F16, BF16 or
  * F32) receive the K and V rows of slot_mapping[t] (any cache type; the value
@@ -601,7 +657,7 @@ pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype kv_dtype, float*
 #define PA_DEVERR_WAIT_EMPTY (1u << 1) /* a producer gave up waiting for a free stage */
 #define PA_DEVERR_WAIT_DRAIN (1u << 2) /* the exit drain gave up on an in-flight copy */
 #define PA_DEVERR_BAD_BLOCK  (1u << 3) /* a block-table entry outside the pool */
-#define PA_DEVERR_BAD_SLOT   (1u << 4) /* a slot_mapping entry outside the pool */
+#define PA_DEVERR_BAD_SLOT   (1u << 4) /* a slot_mapping entry outside the pool, or a position outside cos_sin */
 #define PA_DEVERR_BAD_GROUP  (1u << 5) /* a shared-prefix group range or prefix length */
 #define PA_DEVERR_WORKSPACE  (1u << 6) /* a workspace arrival counter was not zero */
 

@@ -56,6 +56,11 @@ _SIGS = {
                       _I32, _I32, _I32, _I32, _I32, _P], ctypes.c_int),
     "pa_gather_kv": ([_P, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _P, _P,
                       _I32, _I32, _I32, _I32, _I32, _P], ctypes.c_int),
+    "pa_rope": ([_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _I32, ctypes.c_int, _P, _I32, _I32,
+                 _I32, _P, _I32, _P, _I32, _I32, _I32, _P], ctypes.c_int),
+    "pa_rope_append_kv": ([_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, ctypes.c_int,
+                           _P, _P, ctypes.c_int, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _P,
+                           _I32, _P, _I32, _I32, _I32, _I32, _I32, _P], ctypes.c_int),
     "pa_decode_workspace_size": ([_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32], _SZ),
     "pa_decode": ([_P, ctypes.c_int, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _P,
                    _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
@@ -415,6 +420,115 @@ def gather_kv(key, value, k_cache, v_cache, slot_mapping, num_blocks: Optional[i
                               _stream(stream)))
 
 
+# ---------------------------------------------------------------------------
+# rows of a projection: rotary positions, prompts
+# ---------------------------------------------------------------------------
+
+def _heads(name, t, T: int, d: int, dtype) -> Tuple[int, int]:
+    """Rows [T, heads, d] of this type, heads one after another (tokens may lie further
+    apart: parts of a fused projection): their number and the elements from token to token."""
+    s = t.shape
+    if len(s) != 3 or s[0] != T or s[2] != d or t.dtype is not dtype:
+        raise ValueError(f"{name} is {tuple(s)} {t.dtype}, not ({T}, heads, {d}) {dtype}")
+    if T == 0 or s[1] == 0:
+        return s[1], s[1] * d
+    a, b, c = t.stride()
+    if c != 1 or (b != d and s[1] > 1):
+        raise ValueError(f"{name} has strides {(a, b, c)}: a token's heads must be contiguous")
+    return s[1], (a if T > 1 else s[1] * d)
+
+
+def _on_current_device(*named) -> None:
+    """Every (name, tensor) is on the current CUDA device, whose stream the call goes to."""
+    torch = sys.modules["torch"]
+    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t in named:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _rotation(cos_sin, positions, freq_axis, T: int) -> Tuple[int, int, int]:
+    """(positions of the table, rotary_dim, axes) of a rotation of T tokens."""
+    torch = sys.modules["torch"]
+    shape = cos_sin.shape
+    if len(shape) != 2 or cos_sin.dtype is not torch.float32:
+        raise ValueError(f"cos_sin is {tuple(shape)} {cos_sin.dtype}, not (positions, rotary_dim) "
+                         "torch.float32")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.numel() != axes * T or positions.shape[-1] != T or (
+            positions.dtype is not torch.int32):
+        raise ValueError(f"positions is {tuple(positions.shape)} {positions.dtype}, not "
+                         f"({T},) or (axes, {T}) torch.int32")
+    if freq_axis is not None and axes > 1:
+        _sized(("freq_axis", freq_axis, shape[1] // 2, torch.uint8))
+    return shape[0], shape[1], axes
+
+
+def rope(q_out, q, k_out, k, cos_sin, positions, interleaved: bool = False, freq_axis=None,
+         inverse: bool = False, stream=None) -> None:
+    """pa_rope; q and q_out [T, H, d], k and k_out [T, H_kv, d] (or None both), of which
+    tokens may lie further apart than their rows (parts of a fused projection); cos_sin
+    fp32 [positions, rotary_dim]; positions int32 [T] or [axes, T]; freq_axis uint8
+    [rotary_dim / 2] with several axes."""
+    T, d = q.shape[0], q.shape[-1]
+    most, rd, axes = _rotation(cos_sin, positions, freq_axis, T)
+    H, qs = _heads("q", q, T, d, q.dtype)
+    Ho, qos = _heads("q_out", q_out, T, d, q.dtype)
+    G = ks = kos = Go = 0
+    if k is not None or k_out is not None:
+        G, ks = _heads("k", k, T, d, q.dtype)
+        Go, kos = _heads("k_out", k_out, T, d, q.dtype)
+    if H != Ho or G != Go:
+        raise ValueError(f"{H} and {G} heads of q and k, {Ho} and {Go} of q_out and k_out")
+    _on_current_device(("q", q), ("q_out", q_out), ("k", k), ("k_out", k_out),
+                       ("cos_sin", cos_sin), ("positions", positions), ("freq_axis", freq_axis))
+    _check(lib().pa_rope(q_out.data_ptr(), qos, q.data_ptr(), qs, H,
+                         k_out.data_ptr() if G else None, kos, k.data_ptr() if G else None, ks, G,
+                         _dtype_code(q), _ptr(cos_sin), most, rd, int(interleaved),
+                         _ptr(positions), axes, _ptr(freq_axis), int(inverse), T, d,
+                         _stream(stream)))
+
+
+def rope_append_kv(q_out, q, key, value, k_cache, v_cache, slot_mapping, cos_sin, positions,
+                   num_blocks: Optional[int] = None, k_scale=None, v_scale=None, k_zp=None,
+                   v_zp=None, key_out=None, interleaved: bool = False, freq_axis=None,
+                   stream=None) -> None:
+    """pa_rope_append_kv; rows and rotation as rope() takes them (q and q_out may be None
+    both; key_out, the rotated keys, may be key), cache and slots as append_kv()."""
+    T, d = key.shape[0], key.shape[-1]
+    shape, code = k_cache.shape, _dtype_code(k_cache)
+    nb = shape[0] if num_blocks is None else num_blocks
+    most, rd, axes = _rotation(cos_sin, positions, freq_axis, T)
+    G, ks = _heads("key", key, T, d, key.dtype)
+    Gv, vs = _heads("value", value, T, d, key.dtype)
+    kos, Go = 0, G
+    if key_out is not None:
+        Go, kos = _heads("key_out", key_out, T, d, key.dtype)
+    H = qs = Ho = qos = 0
+    if q is not None or q_out is not None:
+        H, qs = _heads("q", q, T, d, key.dtype)
+        Ho, qos = _heads("q_out", q_out, T, d, key.dtype)
+    if H != Ho or Gv != G or Go != G:
+        raise ValueError(f"{H} heads of q, {Ho} of q_out; {G} of key, {Gv} of value, {Go} of "
+                         "key_out")
+    if G != shape[1] or d != (shape[3] * 2 if code == PA_INT4 else shape[3]):
+        raise ValueError(f"key is {tuple(key.shape)}, the cache {tuple(shape)}")
+    _cache_sized(code, nb, shape, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp)
+    _sized(("slot_mapping", slot_mapping, T, sys.modules["torch"].int64))
+    _on_current_device(("q", q), ("q_out", q_out), ("key", key), ("value", value),
+                       ("k_cache", k_cache), ("v_cache", v_cache), ("slot_mapping", slot_mapping),
+                       ("cos_sin", cos_sin), ("positions", positions), ("k_scale", k_scale),
+                       ("v_scale", v_scale), ("k_zp", k_zp), ("v_zp", v_zp), ("key_out", key_out),
+                       ("freq_axis", freq_axis))
+    _check(lib().pa_rope_append_kv(
+        q_out.data_ptr() if H else None, qos, q.data_ptr() if H else None, qs, H,
+        None if key_out is None else key_out.data_ptr(), kos, key.data_ptr(), ks,
+        value.data_ptr(), vs, _dtype_code(key), _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale),
+        _ptr(v_scale), _ptr(k_zp), _ptr(v_zp), _ptr(slot_mapping), _ptr(cos_sin), most, rd,
+        int(interleaved), _ptr(positions), axes, _ptr(freq_axis), T, nb, G, d, shape[2],
+        _stream(stream)))
+
+
 def decode_workspace_size(num_seqs: int, num_q_tokens: int, num_heads: int, num_kv_heads: int,
                           head_dim: int, max_q_len: int, max_context_len: int,
                           partition_size: int = 0) -> int:
@@ -603,7 +717,7 @@ DEVERR_WAIT_FULL = 1 << 0      # a consumer gave up waiting for a staged tile
 DEVERR_WAIT_EMPTY = 1 << 1     # a producer gave up waiting for a free stage
 DEVERR_WAIT_DRAIN = 1 << 2     # the exit drain gave up on an in-flight copy
 DEVERR_BAD_BLOCK = 1 << 3      # a block-table entry outside the pool
-DEVERR_BAD_SLOT = 1 << 4       # a slot_mapping entry outside the pool
+DEVERR_BAD_SLOT = 1 << 4       # a slot_mapping entry outside the pool, or a position outside cos_sin
 DEVERR_BAD_GROUP = 1 << 5      # a shared-prefix group range or prefix length
 DEVERR_WORKSPACE = 1 << 6      # a workspace arrival counter was not zero
 

@@ -99,6 +99,10 @@ pa_status to_host(std::vector<T>& h, const T* d, size_t n, cudaStream_t st) {
                            "validate: copy to host");
 }
 
+}  // namespace
+
+namespace pa {
+
 pa_status validate_slots(const int64_t* slots, int32_t num_tokens, int32_t num_blocks,
                          cudaStream_t st) {
     std::vector<int64_t> h;
@@ -111,7 +115,26 @@ pa_status validate_slots(const int64_t* slots, int32_t num_tokens, int32_t num_b
     return PA_OK;
 }
 
-}  // namespace
+pa_status validate_positions(const int32_t* positions, int32_t num_axes, int32_t num_tokens,
+                             int32_t max_positions, const uint8_t* freq_axis, int32_t rotary_dim,
+                             cudaStream_t st) {
+    std::vector<int32_t> h;
+    if (pa_status s = to_host(h, positions, (size_t)num_axes * num_tokens, st)) return s;
+    for (size_t i = 0; i < h.size(); ++i)
+        if (h[i] < 0 || h[i] >= max_positions)
+            return fail(PA_ERR_VALIDATION, "position %d of token %d, axis %d outside [0,%d)", h[i],
+                        (int)(i % num_tokens), (int)(i / num_tokens), max_positions);
+    if (num_axes == 1) return PA_OK;
+    std::vector<uint8_t> axis;
+    if (pa_status s = to_host(axis, freq_axis, (size_t)rotary_dim / 2, st)) return s;
+    for (size_t f = 0; f < axis.size(); ++f)
+        if (axis[f] >= num_axes)
+            return fail(PA_ERR_VALIDATION, "frequency %d has axis %d of %d", (int)f, (int)axis[f],
+                        num_axes);
+    return PA_OK;
+}
+
+}  // namespace pa
 
 extern "C" const char* pa_last_error(void) { return g_msg; }
 extern "C" const char* pa_version(void) { return "paged-kv-gb300 0.1 (sm_103a)"; }
@@ -200,7 +223,7 @@ extern "C" pa_status pa_append_kv(const void* key, const void* value, pa_dtype s
         return fail(PA_ERR_INVALID_ARG, "key, value and caches must be 16-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
     if (pa::validate_enabled())
-        if (pa_status s = validate_slots(slot_mapping, num_tokens, num_blocks, st)) return s;
+        if (pa_status s = pa::validate_slots(slot_mapping, num_tokens, num_blocks, st)) return s;
     if (kv_dtype == PA_INT4 && ((uintptr_t)k_scale | (uintptr_t)v_scale) % 4)
         return fail(PA_ERR_INVALID_ARG, "k_scale / v_scale must be 4-byte aligned");
     pa::AppendArgs a{key, value, src_dtype, k_cache, v_cache, kv_dtype, k_scale, v_scale,
@@ -229,7 +252,7 @@ extern "C" pa_status pa_gather_kv(void* key, void* value, pa_dtype out_dtype,
         return fail(PA_ERR_INVALID_ARG, "key and value must be 16-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
     if (pa::validate_enabled())
-        if (pa_status s = validate_slots(slot_mapping, num_tokens, num_blocks, st)) return s;
+        if (pa_status s = pa::validate_slots(slot_mapping, num_tokens, num_blocks, st)) return s;
     return pa::launch_gather_kv(pa::GatherArgs{key, value, out_dtype, k_cache, v_cache, kv_dtype,
                                                k_scale, v_scale, k_zp, v_zp, slot_mapping,
                                                num_tokens, num_blocks, num_kv_heads, head_dim,

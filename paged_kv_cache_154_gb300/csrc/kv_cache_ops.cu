@@ -15,6 +15,7 @@
 
 #include "pa_internal.h"
 #include "ptx.cuh"
+#include "quantise.cuh"
 
 namespace {
 
@@ -46,14 +47,8 @@ __global__ void append_kv16_kernel(const uint4* __restrict__ key, const uint4* _
     }
 }
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x);
-template <>
-__device__ __forceinline__ float to_f32<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) {
-    return __bfloat162float(x);
-}
+using pa::F2;
+using pa::to_f32;
 
 // One warp per (token, kv head, K-or-V) row. EPL elements per lane
 // (head_dim = 32 * EPL). Arithmetic is IEEE fp32: correctly rounded
@@ -184,41 +179,6 @@ __global__ void append_kv_fp8_kernel(const T* __restrict__ key, const T* __restr
     }
 }
 
-// Two fp32 numbers and the two-wide arithmetic on them (each operation rounds
-// as its scalar form does).
-struct F2 {
-    uint64_t v;
-    __device__ __forceinline__ F2() {}
-    __device__ __forceinline__ F2(float lo, float hi) {
-        asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-    }
-    __device__ __forceinline__ float lo() const {
-        float a, b;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-        return a;
-    }
-    __device__ __forceinline__ float hi() const {
-        float a, b;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-        return b;
-    }
-};
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-    F2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-    F2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return d;
-}
-
 // INT4 append: the formula of the INT8 path with 16 unsigned codes and one
 // (scale, zero point) per 64 elements. 8 threads a row; a thread holds 8
 // consecutive elements of every group of the K row and of the same V row (16-byte
@@ -273,52 +233,12 @@ __global__ void __launch_bounds__(256) append_kv_int4_kernel(
             mn = fminf(mn, __shfl_xor_sync(peers, mn, o));
             mx = fmaxf(mx, __shfl_xor_sync(peers, mx, o));
         }
-        const float range = __fsub_rn(mx, mn);
-        float scale;
-        uint32_t word;
-        int zp;
-        if (range > 1e-28f && range < 1e30f) {
-            // Correctly rounded quotients by Markstein's theorem: with the correctly rounded
-            // reciprocal y of b, q = a y and r = a - b q (exact in one fused operation),
-            // q + r y is the rounded a / b. Then, adding 1.5 * 2^23 rounds to an integer in
-            // the low bits, and the codes are put together from those bits as they are: the
-            // excess of each over its code is the same number.
-            constexpr float kFifteenth = 1.0f / 15.0f, kRound = 12582912.0f;
-            const float s0 = __fmul_rn(range, kFifteenth);
-            scale = __fmaf_rn(__fmaf_rn(-s0, 15.0f, range), kFifteenth, s0);
-            const float inv = __frcp_rn(scale);
-            const float z0 = __fmul_rn(mn, inv);
-            const float z1 = __fmaf_rn(__fmaf_rn(-z0, scale, mn), inv, z0);
-            const float zr = __fadd_rn(z1, kRound);
-            zp = min(15, __float_as_int(kRound) - __float_as_int(zr));
-            const float top = __int_as_float(__float_as_int(kRound) + 15 - zp);
-            // no code is below 0: rounding keeps the order, and the zero point is -rint(mn / scale)
-            word = 0;
-#pragma unroll
-            for (int e = 6; e >= 0; e -= 2) {
-                const F2 v(x[e], x[e + 1]), q = v * F2(inv, inv);
-                const F2 r = fma(q, F2(-scale, -scale), v);
-                const F2 y = fma(r, F2(inv, inv), q) + F2(kRound, kRound);
-                word = word * 16u + __float_as_uint(fminf(y.hi(), top));
-                word = word * 16u + __float_as_uint(fminf(y.lo(), top));
-            }
-            word -= (uint32_t)(__float_as_int(kRound) - zp) * 0x11111111u;
-        } else {                            // range 0, or too near the ends of fp32
-            scale = __fdiv_rn(range, 15.0f);
-            if (scale == 0.0f) scale = 1.0f;
-            zp = (int)-rintf(__fdiv_rn(mn, scale));
-            zp = zp < 0 ? 0 : min(15, zp);
-            word = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int q = (int)rintf(__fdiv_rn(x[e], scale)) + zp;
-                word |= (uint32_t)(q < 0 ? 0 : min(15, q)) << (4 * e);
-            }
-        }
-        reinterpret_cast<uint32_t*>(which ? v_cache : k_cache)[(row * kGroups + j) * 8 + c] = word;
+        const pa::Quantiser<15, 0> quant(mn, mx);
+        reinterpret_cast<uint32_t*>(which ? v_cache : k_cache)[(row * kGroups + j) * 8 + c] =
+            quant.pack4(x);
         if (c == 0) {
-            (which ? v_scale : k_scale)[row * kGroups + j] = scale;
-            (which ? v_zp : k_zp)[row * kGroups + j] = (int8_t)zp;
+            (which ? v_scale : k_scale)[row * kGroups + j] = quant.scale;
+            (which ? v_zp : k_zp)[row * kGroups + j] = (int8_t)quant.zp;
         }
     }
 }

@@ -27,7 +27,7 @@ enum : unsigned int {
     ERR_WAIT_EMPTY = 1u << 1,   // producer gave up waiting for a free stage
     ERR_WAIT_DRAIN = 1u << 2,   // exit drain gave up on an in-flight copy
     ERR_BAD_BLOCK = 1u << 3,    // a block-table entry outside the pool
-    ERR_BAD_SLOT = 1u << 4,     // a slot outside the pool
+    ERR_BAD_SLOT = 1u << 4,     // a slot outside the pool, or a position outside the table of angles
     ERR_BAD_GROUP = 1u << 5,    // a shared-prefix group range or prefix length out of bounds
     ERR_WORKSPACE = 1u << 6,    // a split-segment arrival counter was not zero at the start
 };
@@ -225,6 +225,13 @@ pa_status check_cache_args(const void* k_cache, const void* v_cache, pa_dtype kv
                            const float* k_scale, const float* v_scale, const int8_t* k_zp,
                            const int8_t* v_zp, int32_t num_kv_heads, int32_t head_dim,
                            int32_t block_size, int32_t num_blocks);
+// PA_VALIDATE=1: slots below the pool's end; positions within the table of angles
+// and, with several axes, every frequency's axis one of them.
+pa_status validate_slots(const int64_t* slots, int32_t num_tokens, int32_t num_blocks,
+                         cudaStream_t st);
+pa_status validate_positions(const int32_t* positions, int32_t num_axes, int32_t num_tokens,
+                             int32_t max_positions, const uint8_t* freq_axis, int32_t rotary_dim,
+                             cudaStream_t st);
 // PA_VALIDATE=1: 0 <= context_lens[s] <= max_context_len, and total_lens[s] (if
 // given) at least context_lens[s].
 pa_status validate_lengths(const int32_t* context_lens, const int32_t* new_lens,
