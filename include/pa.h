@@ -555,6 +555,33 @@ pa_status pa_decode_shared_prefix(
     int32_t max_prefix_len, void* workspace, size_t workspace_bytes,
     void* stream);
 
+/* Causal attention over whole prompts, packed one after another, straight from the
+ * rows of a projection ([p3] §二 softmax(Q K^T / sqrt(d)) V; [p4] GQA): what a fresh
+ * prompt needs besides its append, whatever type its cache has. Query i of a prompt
+ * sees keys 0 .. i of the same prompt.
+ *   q, out         [num_tokens][num_heads][head_dim] of dtype (F16 or BF16); token t's
+ *                  heads start at t * q_stride and t * out_stride (elements)
+ *   key, value     [num_tokens][num_kv_heads][head_dim], likewise. Strides are
+ *                  multiples of 8 of at least a token's rows (so rows may be parts of
+ *                  a wider one), rows 16-byte aligned; out overlaps no input.
+ *   seq_start      int32 [num_seqs + 1]: prompt s is tokens seq_start[s] ..
+ *                  seq_start[s + 1] - 1 (none, where they are equal). Rows of out of
+ *                  tokens of no prompt are left as they were; starts outside
+ *                  [0, num_tokens] and lengths past max_seq_len are cut to them.
+ *   max_seq_len    the longest prompt (host value), at most 2^22
+ *   scale          softmax scale, 0 or more, finite
+ * Needs no workspace. Scores, softmax and sums are fp32, softmax weights are rounded
+ * once to dtype for the product with the values. Nothing of one prompt reaches
+ * another's rows, whatever values it holds; within a prompt a value that is not finite
+ * may reach queries up to 15 tokens before its own. At most 128 query heads per KV
+ * head, head_dim 64 or 128. */
+pa_status pa_prompt_attention(void* out, int64_t out_stride, const void* q, int64_t q_stride,
+                              const void* key, int64_t key_stride, const void* value,
+                              int64_t value_stride, pa_dtype dtype, const int32_t* seq_start,
+                              int32_t num_seqs, int32_t num_tokens, int32_t max_seq_len,
+                              int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                              float scale, void* stream);
+
 /* ---- Eviction by accumulated attention weight. A cache of bounded size keeps
  * the tokens that attention has looked at most. Per decode step (or once, from
  * a prompt's last queries) pa_accumulate_weights adds up what every cached token

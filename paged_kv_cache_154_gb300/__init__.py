@@ -61,6 +61,8 @@ _SIGS = {
     "pa_rope_append_kv": ([_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, ctypes.c_int,
                            _P, _P, ctypes.c_int, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _P,
                            _I32, _P, _I32, _I32, _I32, _I32, _I32, _P], ctypes.c_int),
+    "pa_prompt_attention": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, ctypes.c_int, _P, _I32, _I32,
+                             _I32, _I32, _I32, _I32, ctypes.c_float, _P], ctypes.c_int),
     "pa_decode_workspace_size": ([_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32], _SZ),
     "pa_decode": ([_P, ctypes.c_int, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _P,
                    _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
@@ -527,6 +529,28 @@ def rope_append_kv(q_out, q, key, value, k_cache, v_cache, slot_mapping, cos_sin
         _ptr(v_scale), _ptr(k_zp), _ptr(v_zp), _ptr(slot_mapping), _ptr(cos_sin), most, rd,
         int(interleaved), _ptr(positions), axes, _ptr(freq_axis), T, nb, G, d, shape[2],
         _stream(stream)))
+
+
+def prompt_attention(out, q, key, value, seq_start, max_seq_len: int, scale: float,
+                     stream=None) -> None:
+    """pa_prompt_attention; q and out [T, H, d], key and value [T, H_kv, d], of which tokens
+    may lie further apart than their rows; seq_start int32 [num_seqs + 1] on the device."""
+    T, d = q.shape[0], q.shape[-1]
+    H, qs = _heads("q", q, T, d, q.dtype)
+    Ho, os_ = _heads("out", out, T, d, q.dtype)
+    G, ks = _heads("key", key, T, d, q.dtype)
+    Gv, vs = _heads("value", value, T, d, q.dtype)
+    if H != Ho or G != Gv:
+        raise ValueError(f"{H} heads of q, {Ho} of out; {G} of key, {Gv} of value")
+    if seq_start.dim() != 1 or seq_start.dtype is not sys.modules["torch"].int32:
+        raise ValueError(f"seq_start is {tuple(seq_start.shape)} {seq_start.dtype}, not "
+                         "(num_seqs + 1,) torch.int32")
+    _on_current_device(("q", q), ("out", out), ("key", key), ("value", value),
+                       ("seq_start", seq_start))
+    _check(lib().pa_prompt_attention(
+        out.data_ptr(), os_, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs,
+        _dtype_code(q), _ptr(seq_start), seq_start.shape[0] - 1, T, int(max_seq_len), H, G, d,
+        float(scale), _stream(stream)))
 
 
 def decode_workspace_size(num_seqs: int, num_q_tokens: int, num_heads: int, num_kv_heads: int,

@@ -115,6 +115,17 @@ pa_status validate_slots(const int64_t* slots, int32_t num_tokens, int32_t num_b
     return PA_OK;
 }
 
+pa_status validate_starts(const int32_t* seq_start, int32_t num_seqs, int32_t num_tokens,
+                          int32_t max_seq_len, cudaStream_t st) {
+    std::vector<int32_t> h;
+    if (pa_status s = to_host(h, seq_start, (size_t)num_seqs + 1, st)) return s;
+    for (int32_t s = 0; s < num_seqs; ++s)
+        if (h[s] < 0 || h[s + 1] < h[s] || h[s + 1] > num_tokens || h[s + 1] - h[s] > max_seq_len)
+            return fail(PA_ERR_VALIDATION, "prompt %d has tokens %d to %d (of %d, at most %d each)",
+                        s, h[s], h[s + 1], num_tokens, max_seq_len);
+    return PA_OK;
+}
+
 pa_status validate_positions(const int32_t* positions, int32_t num_axes, int32_t num_tokens,
                              int32_t max_positions, const uint8_t* freq_axis, int32_t rotary_dim,
                              cudaStream_t st) {

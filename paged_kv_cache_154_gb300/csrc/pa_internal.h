@@ -200,6 +200,16 @@ pa_status cache_tensor_map(CUtensorMap* out, const void* ptr, int num_blocks, in
 pa_status cache_tensor_map_tile(CUtensorMap* out, const void* ptr, int num_blocks,
                                 int num_kv_heads);
 
+// 16-bit rows of a projection, [num_tokens][heads][head_dim] with `stride` elements from one
+// token's to the next's, 128-byte swizzled (not kept: they go with the call's pointers).
+// heads: a box is 64 columns of box_heads heads of box_tokens tokens, a row a (token, head)
+// pair; coordinates (column, head, token). tokens: a box is whole rows of one head of
+// box_tokens tokens, laid out as [64-column part][token][128 B]; coordinates (0, token, 0, head).
+pa_status rows_tensor_map_heads(CUtensorMap* out, const void* rows, int num_tokens, int64_t stride,
+                                int heads, int head_dim, int box_heads, int box_tokens);
+pa_status rows_tensor_map_tokens(CUtensorMap* out, const void* rows, int num_tokens,
+                                 int64_t stride, int heads, int head_dim, int box_tokens);
+
 // Host-side argument checks of the decode entry points (capi.cu).
 pa_status check_decode_args(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
                             const void* k_cache, const void* v_cache, pa_dtype kv_dtype,
@@ -232,6 +242,9 @@ pa_status validate_slots(const int64_t* slots, int32_t num_tokens, int32_t num_b
 pa_status validate_positions(const int32_t* positions, int32_t num_axes, int32_t num_tokens,
                              int32_t max_positions, const uint8_t* freq_axis, int32_t rotary_dim,
                              cudaStream_t st);
+// PA_VALIDATE=1: starts in order, within the tokens, no prompt longer than max_seq_len.
+pa_status validate_starts(const int32_t* seq_start, int32_t num_seqs, int32_t num_tokens,
+                          int32_t max_seq_len, cudaStream_t st);
 // PA_VALIDATE=1: 0 <= context_lens[s] <= max_context_len, and total_lens[s] (if
 // given) at least context_lens[s].
 pa_status validate_lengths(const int32_t* context_lens, const int32_t* new_lens,

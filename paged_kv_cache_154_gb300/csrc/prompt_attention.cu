@@ -1,0 +1,762 @@
+// Causal attention over whole prompts, packed one after another, on the
+// 5th-generation tensor cores (tcgen05, TMEM): q, k and v as a projection gives
+// them, before anything is cached. out_i = sum over j <= i of softmax_j(scale
+// q_i k_j) v_j within each prompt ("KV Cache ... PagedAttention" §二), query heads
+// in contiguous groups per KV head ("cs336 lecture 10", GQA).
+//
+// A task is a run of a prompt's tokens and one KV head: two Q tiles of 128 rows,
+// a row a (token, head of the group) pair, tokens_per_tile = 128 / group tokens a
+// tile, against the prompt's keys up to its last token in tiles of 128. Per tile:
+//   S = Q K^T      M128 N128, both K-major in shared memory, S in TMEM
+//   P = 2^(S - m)  one thread a row, P as 16 bits over the columns of S
+//   O += P V       M128 N = head_dim, P from TMEM, V MN-major in shared memory
+// The running maximum m moves only when a tile raises it by more than 2^8 (the
+// weights then stay below 2^8, and O is scaled in TMEM, which is rare); sums and O
+// are fp32. P is rounded to the 16-bit type once (half a step: 2^-9 bf16, 2^-12
+// fp16 of a weight), as the tensor cores take it: the same size as the rounding
+// of the output.
+//
+// A CTA a SM stays and works off its tasks: the longest first (a task's keys grow
+// with its place in the prompt), dealt out to and fro over the CTAs. Its roles:
+//   warps 0-3, 4-7   softmax of Q tile 0 and 1
+//   warps 8-11       epilogue: O / l to global memory while the next task runs
+//   warp 12          issues all products: P_0 V, Q_0 K'^T, P_1 V, Q_1 K'^T, so that
+//                    the softmax of either tile has the other's products to run in
+//   warp 13          TMA: Q tiles, K and V tiles into a ring
+//   warp 14          finds the tasks
+// Every wait is bounded; one that gives up ends every role's loop.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <float.h>
+#include <math.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "pa_internal.h"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace {
+
+constexpr int kRows = 128;               // rows of a Q tile
+constexpr int kKeys = 128;               // keys of a K or V tile
+constexpr int kThreads = 512;
+constexpr int kLaunchSeqs = 512;         // prompts a launch: their chunk counts stay in registers
+constexpr int kMaxLen = 1 << 22;         // a task's products end well before a wait gives up
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazyMax = 8.f;
+
+template <int D>
+struct Layout {
+    static constexpr int kHalves = D / 64;                     // 128-byte wide parts of a row
+    static constexpr int kTile = kKeys * D * 2;                // bytes of a K, V or Q tile
+    static constexpr int kHalf = kKeys * 128;                  // bytes of one part
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kKVOff = 2 * kTile;
+    static constexpr int kSumOff = kKVOff + kStages * kTile;   // l of both Q tiles' rows
+    static constexpr int kBarOff = kSumOff + 2 * kRows * 4;
+    // barriers
+    static constexpr int kKVFull = 0, kKVEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + 2,
+                         kSFull = kQEmpty + 2, kPFull = kSFull + 2 /* [tile][half] */,
+                         kOFull = kPFull + 4, kOFree = kOFull + 2, kLFull = kOFree + 2,
+                         kTaskFull = kLFull + 2, kTaskEmpty = kTaskFull + 2, kFin = kTaskEmpty + 2,
+                         kNumBars = kFin + 1;
+    static constexpr int kTaskOff = kBarOff + 8 * kNumBars + 8;   // two task records
+    static constexpr int kFlagOff = kTaskOff + 2 * 32;            // TMEM address, abort flag
+    static constexpr int kSmem = kFlagOff + 16 + 1024;            // + alignment slack
+    static_assert(kTaskOff % 16 == 0 && kSmem <= 227 * 1024, "shared memory per CTA");
+};
+// TMEM columns: S of Q tile x at 128 x (P over its first 64), O at 256 + D x
+constexpr uint32_t kTmemCols = 512, kOCol = 256;
+
+struct PromptParams {
+    void* out;
+    const int32_t* start;       // [num_seqs + 1] of this launch's prompts
+    unsigned int* err;
+    int64_t out_stride;
+    int num_seqs;
+    int num_tokens;
+    int max_len;
+    int num_kv_heads;
+    int group;
+    int tokens;                 // of a Q tile
+    int max_chunks;             // tasks of the longest prompt and one KV head
+    float scale_log2;
+};
+
+struct alignas(16) Task {
+    int start, len;             // of the prompt
+    int off;                    // first token of the task, in the prompt
+    int head;                   // KV head, or -1: no more tasks
+};
+
+// What a task's Q tile x sees: the prompt's tokens [0, keys), in `tiles` tiles.
+struct Span {
+    int first, keys, tiles;
+    __device__ __forceinline__ Span(const Task& t, int tokens, int x) {
+        first = t.off + x * tokens;
+        keys = min(first + tokens, t.len);
+        tiles = (keys + kKeys - 1) / kKeys;
+    }
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+    asm("{\n\t.reg .b64 ra, rd;\n\t"
+        "mov.b64 rd, {%0, %1};\n\tmov.b64 ra, {%2, %3};\n\t"
+        "add.rn.f32x2 rd, rd, ra;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Length of prompt s, cut to what the tensors hold.
+__device__ __forceinline__ int length_of(const PromptParams& p, int s, int& start) {
+    start = min(max(__ldg(p.start + s), 0), p.num_tokens);
+    const int len = __ldg(p.start + s + 1) - start;
+    return min(max(len, 0), min(p.max_len, p.num_tokens - start));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q,
+                            const __grid_constant__ CUtensorMap map_k,
+                            const __grid_constant__ CUtensorMap map_v,
+                            const __grid_constant__ PromptParams p) {
+    using LY = Layout<D>;
+    constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int kStages = LY::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = pa::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const smem = smem_raw + (base - raw);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t bars = base + LY::kBarOff;
+    float* const sums = reinterpret_cast<float*>(smem + LY::kSumOff);
+    volatile Task* const tasks = reinterpret_cast<volatile Task*>(smem + LY::kTaskOff);
+    uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(smem + LY::kFlagOff);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + LY::kFlagOff + 8);
+    auto bar = [&](int i) { return bars + 8u * i; };
+
+    pa::grid_dependents_launch();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < LY::kNumBars; ++i) {
+            // arrivals: P, l and a free O from the four warps of a group; a task record from
+            // every warp that reads it
+            const int n = (i >= LY::kPFull && i < LY::kOFull) || (i >= LY::kOFree && i < LY::kTaskFull)
+                              ? 4
+                          : i >= LY::kTaskEmpty && i < LY::kFin ? 14
+                                                               : 1;
+            pa::mbar_init(bar(i), n);
+        }
+        *abort_flag = 0;
+        pa::fence_barrier_init();
+        pa::prefetch_tensormap(&map_q);
+        pa::prefetch_tensormap(&map_k);
+        pa::prefetch_tensormap(&map_v);
+    }
+    if (warp == 12) {
+        pa::tc::tmem_alloc(pa::smem_addr(tmem_holder), kTmemCols);
+        pa::tc::tmem_relinquish();
+    }
+    pa::tc::fence_before_sync();
+    __syncthreads();
+    pa::tc::fence_after_sync();
+    const uint32_t tmem = *tmem_holder;
+    pa::grid_dependency_wait();
+
+    // a wait by the whole warp, or by one lane; false ends the role
+    auto wait = [&](int b, uint32_t parity, unsigned int code) -> bool {
+        if (__all_sync(0xffffffffu, pa::mbar_try_wait(bar(b), parity))) return true;
+        const bool ok = __all_sync(0xffffffffu, pa::mbar_wait(bar(b), parity, p.err, code)) &&
+                        __shfl_sync(0xffffffffu, *abort_flag, 0) == 0;
+        if (!ok && lane == 0) *abort_flag = 1;
+        return ok;
+    };
+    auto wait_one = [&](int b, uint32_t parity, unsigned int code) -> bool {
+        const bool ok = pa::mbar_wait(bar(b), parity, p.err, code) && !*abort_flag;
+        if (!ok) *abort_flag = 1;
+        return ok;
+    };
+    // the i-th task of this CTA
+    auto read_task = [&](int i, Task& t) -> bool {
+        if (!wait(LY::kTaskFull + (i & 1), (i >> 1) & 1, pa::ERR_WAIT_FULL)) return false;
+        volatile Task& r = tasks[i & 1];
+        t.start = r.start, t.len = r.len, t.off = r.off, t.head = r.head;
+        __syncwarp();
+        if (lane == 0) pa::mbar_arrive(bar(LY::kTaskEmpty + (i & 1)));
+        return t.head >= 0;
+    };
+    const int G = p.group, tokens = p.tokens;
+
+    if (warp < 8) {
+        // ---------------- softmax of Q tile x: one thread a row ----------------
+        more_registers<176>();
+        const int x = warp >> 2;
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t s_tm = tmem + lane_at + 128 * x, o_tm = tmem + lane_at + kOCol + D * x;
+        const int token = row / G;                           // of the tile
+        const float sl2 = p.scale_log2;
+        uint32_t it = 0, n_s = 0, n_o = 0;                   // K/V tiles, S tiles, tasks so far
+        Task task;
+        for (int i = 0; read_task(i, task); ++i) {
+            const bool two = task.len - task.off > tokens;
+            const Span all(task, tokens, two ? 1 : 0), span(task, tokens, x);
+            const uint32_t it0 = it;
+            it += 2 * all.tiles;
+            if (x == 1 && !two) continue;
+            // rows past the tile's tokens or the prompt hold anything; they are not written
+            const int bound = span.first + token;
+            float m_run = -INFINITY, l_run = 0.f;
+            bool ok = true;
+            for (int t = 0; t < span.tiles; ++t, ++n_s) {
+                ok = wait(LY::kSFull + x, n_s & 1, pa::ERR_WAIT_FULL);
+                if (!ok) break;
+                pa::tc::fence_after_sync();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) pa::tc::ld_32cols_nowait(s_tm + 32 * c, s[c]);
+                pa::tc::wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) pa::tc::loaded(s[c]);
+                auto sv = [&](int j) -> float& { return reinterpret_cast<float&>(s[j >> 5][j & 31]); };
+                const int key0 = t * kKeys;
+                if (key0 + kKeys - 1 > span.first) {         // a tile that some row must not see all of
+#pragma unroll
+                    for (int j = 0; j < kKeys; ++j)
+                        if (key0 + j > bound) sv(j) = -INFINITY;
+                }
+                float m4[4] = {sv(0), sv(1), sv(2), sv(3)};
+#pragma unroll
+                for (int j = 4; j < kKeys - 4; j += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], sv(j + 2 * q), sv(j + 2 * q + 1));
+                m4[0] = max3(m4[0], sv(kKeys - 4), sv(kKeys - 3));
+                m4[1] = max3(m4[1], sv(kKeys - 2), sv(kKeys - 1));
+                float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+                mx = mx == -INFINITY ? mx : mx * sl2;        // the scale is not negative
+                float alpha = 1.f;
+                const bool moved = mx > m_run + kLazyMax;
+                if (moved) {
+                    alpha = pa::ex2(m_run - mx);             // 0 while m_run is -inf
+                    m_run = mx;
+                }
+                // O may be scaled now: S of this tile was issued behind the last P V, and the
+                // barrier says that both are done; the next P V waits for this P
+                if (t > 0 && __any_sync(0xffffffffu, moved)) {
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t ov[16];
+                        pa::tc::ld_16cols(o_tm + 16 * q, ov);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        pa::tc::st_16cols(o_tm + 16 * q, ov);
+                    }
+                }
+                const float nm = m_run == -INFINITY ? 0.f : -m_run;
+                // V rows behind the prompt that a product reaches may hold anything: zeroed, so
+                // that a weight of 0 never meets a NaN. The first Q tile to reach them does it.
+                const int in_tile = span.keys - key0;        // visible keys of this tile
+                if (t == span.tiles - 1) {
+                    const int end = (span.keys + 15) & ~15;
+                    const bool first_has = x == 1 && [&] {
+                        const Span f(task, tokens, 0);
+                        return f.tiles == span.tiles && ((f.keys + 15) & ~15) > task.len;
+                    }();
+                    if (end > task.len && !first_has) {
+                        const uint32_t v = it0 + 2 * t + 1;
+                        ok = wait(LY::kKVFull + v % kStages, (v / kStages) & 1, pa::ERR_WAIT_FULL);
+                        if (!ok) break;
+                        const int z0 = task.len - key0, n = (end - task.len) * (D / 8);
+                        for (int e = row; e < n; e += kRows) {
+                            const int r = z0 + e / (D / 8), ch = e % (D / 8);
+                            const uint32_t dst = base + LY::kKVOff + (v % kStages) * LY::kTile +
+                                                 (ch >> 3) * LY::kHalf + r * 128 + ((ch & 7) << 4);
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0u)
+                                         : "memory");
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                }
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (32 * c < in_tile) {                  // else no product reads it
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            float e[4];
+#pragma unroll
+                            for (int q = 0; q < 4; q += 2) {
+                                fma2(e[q], e[q + 1], sv(32 * c + j + q), sv(32 * c + j + q + 1), sl2,
+                                     nm);
+                                e[q] = pa::ex2(e[q]);
+                                e[q + 1] = pa::ex2(e[q + 1]);
+                                pk[(j + q) / 2] = pack2<T>(e[q], e[q + 1]);
+                            }
+                            add2(l4[0], l4[1], e[0], e[1]);
+                            add2(l4[2], l4[3], e[2], e[3]);
+                        }
+                        pa::tc::st_16cols_nowait(s_tm + 16 * c, pk);
+                    }
+                    if (c & 1) {
+                        pa::tc::wait_st();
+                        pa::tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) pa::mbar_arrive(bar(LY::kPFull + 2 * x + (c >> 1)));
+                    }
+                }
+                l_run = l_run * alpha + ((l4[0] + l4[1]) + (l4[2] + l4[3]));
+            }
+            if (!ok) break;
+            // the sums of the last task have been read
+            if (n_o > 0 && !wait(LY::kOFree + x, (n_o - 1) & 1, pa::ERR_WAIT_EMPTY)) break;
+            ++n_o;
+            sums[x * kRows + row] = l_run;
+            __syncwarp();
+            if (lane == 0) pa::mbar_arrive(bar(LY::kLFull + x));
+        }
+    } else if (warp < 12) {
+        // ---------------- epilogue: O / l of each Q tile ----------------
+        fewer_registers<96>();
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
+        const int token = row / G, head = row % G;
+        uint32_t n_o[2] = {0, 0};
+        Task task;
+        for (int i = 0; read_task(i, task); ++i) {
+            bool ok = true;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (!ok || (x == 1 && task.len - task.off <= tokens)) continue;
+                const int at = task.off + x * tokens + token;
+                const bool valid = token < tokens && at < task.len;
+                T* const dst = static_cast<T*>(p.out) + (int64_t)(task.start + at) * p.out_stride +
+                               (int64_t)(task.head * G + head) * D;
+                ok = wait(LY::kLFull + x, n_o[x] & 1, pa::ERR_WAIT_FULL) &&
+                     wait(LY::kOFull + x, n_o[x] & 1, pa::ERR_WAIT_FULL);
+                if (!ok) continue;
+                pa::tc::fence_after_sync();
+                const float l = sums[x * kRows + row];
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const uint32_t o_tm = tmem + lane_at + kOCol + D * x;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    pa::tc::ld_32cols_nowait(o_tm + 32 * c, o);
+                    pa::tc::wait_ld();
+                    pa::tc::loaded(o);
+                    if (c == D / 32 - 1) {                   // all of O and l has been read
+                        pa::tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) pa::mbar_arrive(bar(LY::kOFree + x));
+                    }
+                    if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 w;
+                            w.x = pack2<T>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                            w.y = pack2<T>(__uint_as_float(o[e + 2]) * inv,
+                                           __uint_as_float(o[e + 3]) * inv);
+                            w.z = pack2<T>(__uint_as_float(o[e + 4]) * inv,
+                                           __uint_as_float(o[e + 5]) * inv);
+                            w.w = pack2<T>(__uint_as_float(o[e + 6]) * inv,
+                                           __uint_as_float(o[e + 7]) * inv);
+                            *reinterpret_cast<uint4*>(dst + 32 * c + e) = w;
+                        }
+                    }
+                }
+                ++n_o[x];
+            }
+            if (!ok) break;
+        }
+    } else {
+        fewer_registers<64>();
+        if (warp == 12) {
+            // ---------------- all products, issued by one elected lane ----------------
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t sb = __shfl_sync(0xffffffffu, base, 0);
+            constexpr uint32_t idesc_qk = pa::tc::idesc_f16(kBF16, false, false, kRows, kKeys);
+            constexpr uint32_t idesc_pv = pa::tc::idesc_f16(kBF16, false, true, kRows, D);
+            // the descriptor of address a + o is the one of a plus o >> 4
+            const uint64_t dq = pa::tc::smem_desc_sw128(sb, 16, 1024);
+            const uint64_t dk = pa::tc::smem_desc_sw128(sb + LY::kKVOff, 16, 1024);
+            const uint64_t dv = pa::tc::smem_desc_sw128(sb + LY::kKVOff, LY::kHalf, 1024);
+            uint32_t it = 0, n_s[2] = {0, 0}, n_q[2] = {0, 0};
+            auto kv_ready = [&](uint32_t i) {
+                return wait(LY::kKVFull + i % kStages, (i / kStages) & 1, pa::ERR_WAIT_FULL);
+            };
+            auto kv_done = [&](uint32_t i) {
+                pa::tc::commit_warp(bar(LY::kKVEmpty + i % kStages));
+            };
+            auto issue_qk = [&](int x, uint32_t i) {         // S_x = Q_x K^T
+                pa::tc::fence_after_sync();
+                const uint64_t a = dq + (uint64_t)((x * LY::kTile) >> 4);
+                const uint64_t b = dk + (uint64_t)(((i % kStages) * LY::kTile) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = ((kk >> 2) * LY::kHalf + (kk & 3) * 32) >> 4;
+                    pa::tc::mma_f16_ss_warp(tm + 128 * x, a + o, b + o, idesc_qk, kk > 0 ? 1u : 0u);
+                }
+                pa::tc::commit_warp(bar(LY::kSFull + x));
+            };
+            auto issue_pv = [&](int x, uint32_t i, int half, int steps, bool more) {   // O_x += P_x V
+                pa::tc::fence_after_sync();
+                const uint64_t b = dv + (uint64_t)(((i % kStages) * LY::kTile) >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int kb = 4 * half + k;
+                    if (kb < steps)
+                        pa::tc::mma_f16_ts_warp(tm + kOCol + D * x, tm + 128 * x + 8 * kb,
+                                                b + (uint64_t)((kb * 16 * 128) >> 4), idesc_pv,
+                                                more || kb > 0 ? 1u : 0u);
+                }
+            };
+            Task task;
+            for (int i = 0; read_task(i, task); ++i) {
+                const int nq = task.len - task.off > tokens ? 2 : 1;
+                const Span s0(task, tokens, 0), s1(task, tokens, nq - 1);
+                const int tiles = s1.tiles;
+                bool ok = kv_ready(it);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (ok && x < nq) {
+                        ok = wait(LY::kQFull + x, n_q[x] & 1, pa::ERR_WAIT_FULL);
+                        if (!ok) break;
+                        issue_qk(x, it);
+                        if ((x ? s1 : s0).tiles == 1) pa::tc::commit_warp(bar(LY::kQEmpty + x));
+                    }
+                if (ok) kv_done(it);
+                for (int t = 0; ok && t < tiles; ++t) {
+                    const uint32_t iv = it + 2 * t + 1, ik = iv + 1;
+                    ok = kv_ready(iv);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (!ok || x >= nq) continue;
+                        const Span& s = x ? s1 : s0;
+                        if (t < s.tiles) {
+                            // O of the last task has been read
+                            if (t == 0 && n_q[x] > 0)
+                                ok = wait(LY::kOFree + x, (n_q[x] - 1) & 1, pa::ERR_WAIT_EMPTY);
+                            const int steps = min(8, (s.keys - t * kKeys + 15) >> 4);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                ok = ok && wait(LY::kPFull + 2 * x + h, n_s[x] & 1, pa::ERR_WAIT_FULL);
+                                if (ok) issue_pv(x, iv, h, steps, t > 0);
+                            }
+                            if (!ok) continue;
+                            ++n_s[x];
+                            if (t == s.tiles - 1) pa::tc::commit_warp(bar(LY::kOFull + x));
+                        }
+                        if (x == nq - 1) kv_done(iv);
+                        if (t + 1 < s.tiles) {
+                            // the products run in the order of their issue: P V of this tile has
+                            // read P before S takes its columns
+                            ok = kv_ready(ik);
+                            if (!ok) continue;
+                            issue_qk(x, ik);
+                            if (t + 2 == s.tiles) pa::tc::commit_warp(bar(LY::kQEmpty + x));
+                            if (x == nq - 1) kv_done(ik);
+                        }
+                    }
+                }
+                if (!ok) break;
+                it += 2 * tiles;
+                ++n_q[0];
+                if (nq == 2) ++n_q[1];
+            }
+            // every product and commit of this warp is done before TMEM and the CTA go
+            pa::tc::commit_warp(bar(LY::kFin));
+            if (!__all_sync(0xffffffffu, pa::mbar_wait(bar(LY::kFin), 0, nullptr, 0)) && lane == 0 &&
+                p.err)
+                atomicOr(p.err, pa::ERR_WAIT_DRAIN);
+        } else if (warp == 13) {
+            // ---------------- TMA: Q tiles, then K and V tiles in turn ----------------
+            uint32_t it = 0, n_q[2] = {0, 0};
+            const uint32_t q_bytes = tokens * G * 128;
+            Task task;
+            for (int i = 0; read_task(i, task); ++i) {
+                bool ok = true;
+                if (lane == 0) {
+                    const int nq = task.len - task.off > tokens ? 2 : 1;
+                    const int tiles = Span(task, tokens, nq - 1).tiles;
+                    auto load = [&](int k) -> bool {         // the task's k-th K (even) or V tile
+                        const uint32_t at = it + k;
+                        if (at >= kStages && !wait_one(LY::kKVEmpty + at % kStages,
+                                                       ((at / kStages) - 1) & 1, pa::ERR_WAIT_EMPTY))
+                            return false;
+                        const uint32_t b = bar(LY::kKVFull + at % kStages);
+                        pa::mbar_arrive_expect_tx(b, LY::kTile);
+                        tma_load_4d(base + LY::kKVOff + (at % kStages) * LY::kTile,
+                                    k & 1 ? &map_v : &map_k, 0, task.start + (k >> 1) * kKeys, 0,
+                                    task.head, b);
+                        return true;
+                    };
+                    int done = 0;
+                    ok = load(0);
+                    if (ok) done = 1;
+                    for (int x = 0; ok && x < nq; ++x) {
+                        // Q of the last task has been read
+                        if (n_q[x] > 0)
+                            ok = wait_one(LY::kQEmpty + x, (n_q[x] - 1) & 1, pa::ERR_WAIT_EMPTY);
+                        if (!ok) break;
+                        const uint32_t b = bar(LY::kQFull + x);
+                        pa::mbar_arrive_expect_tx(b, q_bytes * LY::kHalves);
+                        for (int h = 0; h < LY::kHalves; ++h)
+                            tma_load_3d(base + x * LY::kTile + h * LY::kHalf, &map_q, 64 * h,
+                                        task.head * G, task.start + task.off + x * tokens, b);
+                        ++n_q[x];
+                    }
+                    for (int k = 1; ok && k < 2 * tiles; ++k) {
+                        ok = load(k);
+                        if (ok) done = k + 1;
+                    }
+                    it += done;
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+            }
+            // no copy may be in flight when the CTA ends (those whose tiles were consumed are
+            // not; after a wait gave up, the last of the ring and of Q may be)
+            if (lane == 0 && *abort_flag) {
+                bool ok = true;
+                for (uint32_t u = it > kStages ? it - kStages : 0; u < it; ++u)
+                    ok &= pa::mbar_wait(bar(LY::kKVFull + u % kStages), (u / kStages) & 1, nullptr, 0);
+                for (int x = 0; x < 2; ++x)
+                    if (n_q[x] > 0)
+                        ok &= pa::mbar_wait(bar(LY::kQFull + x), (n_q[x] - 1) & 1, nullptr, 0);
+                if (!ok && p.err) atomicOr(p.err, pa::ERR_WAIT_DRAIN);
+            }
+            __syncwarp();
+        } else if (warp == 14) {
+            // ---------------- tasks ----------------
+            // The tasks of all prompts in the order of their chunk's place, last first; among
+            // equals by prompt, then by KV head. With n_s chunks of prompt s, F(c) = sum of
+            // max(0, n_s - c) of them have a place of c or more: the chunk of task v is the
+            // c with F(c + 1) <= v < F(c), its prompt the (v - F(c + 1))-th with n_s > c.
+            int n[kLaunchSeqs / 32];
+            const int per_task = 2 * tokens;
+#pragma unroll
+            for (int j = 0; j < kLaunchSeqs / 32; ++j) {
+                const int s = 32 * j + lane;
+                int start;
+                n[j] = s < p.num_seqs ? (length_of(p, s, start) + per_task - 1) / per_task : 0;
+            }
+            auto at_least = [&](int c) -> unsigned {
+                unsigned sum = 0;
+#pragma unroll
+                for (int j = 0; j < kLaunchSeqs / 32; ++j) sum += (unsigned)max(0, n[j] - c);
+                return __reduce_add_sync(0xffffffffu, sum);
+            };
+            const unsigned all = at_least(0);
+            const unsigned P = gridDim.x;
+            for (unsigned i = 0;; ++i) {
+                const unsigned v = i * P + (i & 1 ? P - 1 - blockIdx.x : blockIdx.x);
+                const unsigned chunk = v / (unsigned)p.num_kv_heads;
+                Task t;
+                t.start = t.len = t.off = 0, t.head = -1;
+                if (chunk < all) {
+                    int lo = 0, hi = p.max_chunks;           // F(lo) > chunk >= F(hi)
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) >> 1;
+                        if (at_least(mid) > chunk) lo = mid;
+                        else hi = mid;
+                    }
+                    unsigned left = chunk - at_least(lo + 1);
+                    int s = 0;
+                    bool found = false;
+#pragma unroll
+                    for (int j = 0; j < kLaunchSeqs / 32; ++j) {
+                        const unsigned has = __ballot_sync(0xffffffffu, n[j] > lo);
+                        const unsigned cnt = __popc(has);
+                        if (!found) {
+                            if (left < cnt) {
+                                s = 32 * j + __fns(has, 0, left + 1);
+                                found = true;
+                            } else {
+                                left -= cnt;
+                            }
+                        }
+                    }
+                    t.len = length_of(p, s, t.start);
+                    t.off = lo * per_task;
+                    t.head = (int)(v % (unsigned)p.num_kv_heads);
+                }
+                if (i >= 2 &&
+                    !wait(LY::kTaskEmpty + (i & 1), ((i >> 1) - 1) & 1, pa::ERR_WAIT_EMPTY))
+                    break;
+                if (lane == 0) {
+                    volatile Task& r = tasks[i & 1];
+                    r.start = t.start, r.len = t.len, r.off = t.off, r.head = t.head;
+                    pa::mbar_arrive(bar(LY::kTaskFull + (i & 1)));
+                }
+                __syncwarp();
+                if (t.head < 0) break;
+            }
+        }
+    }
+    pa::tc::fence_before_sync();
+    __syncthreads();
+    pa::tc::fence_after_sync();
+    if (warp == 12) pa::tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <typename T, int D>
+pa_status launch(const CUtensorMap* maps, PromptParams p, int64_t grid, cudaStream_t st) {
+    auto kern = prompt_attention_kernel<T, D>;
+    static std::atomic<uint64_t> done{0};
+    if (pa_status s = pa::allow_smem(kern, Layout<D>::kSmem, done, "prompt: shared memory size"))
+        return s;
+    return pa::cuda_status(pa::launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads),
+                                          Layout<D>::kSmem, st, maps[0], maps[1], maps[2], p),
+                           "prompt attention launch");
+}
+
+pa_status check_rows(const char* name, const void* rows, int64_t stride, int32_t heads,
+                     int32_t head_dim) {
+    if ((uintptr_t)rows % 16) return pa::fail(PA_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+    if (stride < (int64_t)heads * head_dim || stride % 8)
+        return pa::fail(PA_ERR_INVALID_ARG,
+                        "%s_stride %lld is not a multiple of 8 of at least %lld elements", name,
+                        (long long)stride, (long long)heads * head_dim);
+    if (stride >= 1ll << 38)
+        return pa::fail(PA_ERR_UNSUPPORTED, "%s_stride %lld", name, (long long)stride);
+    return PA_OK;
+}
+
+}  // namespace
+
+extern "C" pa_status pa_prompt_attention(void* out, int64_t out_stride, const void* q,
+                                         int64_t q_stride, const void* key, int64_t key_stride,
+                                         const void* value, int64_t value_stride, pa_dtype dtype,
+                                         const int32_t* seq_start, int32_t num_seqs,
+                                         int32_t num_tokens, int32_t max_seq_len,
+                                         int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                         float scale, void* stream) {
+    using pa::fail;
+    if (num_seqs < 0 || num_tokens < 0)
+        return fail(PA_ERR_INVALID_ARG, "num_seqs %d, num_tokens %d", num_seqs, num_tokens);
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !key || !value || !seq_start) return fail(PA_ERR_INVALID_ARG, "NULL pointer");
+    if (dtype != PA_F16 && dtype != PA_BF16)
+        return fail(PA_ERR_UNSUPPORTED, "dtype %d (F16 or BF16)", (int)dtype);
+    if (head_dim != 64 && head_dim != 128)
+        return fail(PA_ERR_UNSUPPORTED, "head_dim %d (64 or 128 supported)", head_dim);
+    if (num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads)
+        return fail(PA_ERR_INVALID_ARG, "num_heads %d is not a multiple of num_kv_heads %d",
+                    num_heads, num_kv_heads);
+    const int group = num_heads / num_kv_heads;
+    if (group > kRows)
+        return fail(PA_ERR_UNSUPPORTED, "%d query heads per KV head (at most %d)", group, kRows);
+    if (max_seq_len < 1) return fail(PA_ERR_INVALID_ARG, "max_seq_len %d", max_seq_len);
+    if (max_seq_len > kMaxLen)
+        return fail(PA_ERR_UNSUPPORTED, "prompts of more than %d tokens", kMaxLen);
+    if (!(scale >= 0.f) || isinf(scale)) return fail(PA_ERR_INVALID_ARG, "scale %g", (double)scale);
+    if (pa_status s = check_rows("q", q, q_stride, num_heads, head_dim)) return s;
+    if (pa_status s = check_rows("key", key, key_stride, num_kv_heads, head_dim)) return s;
+    if (pa_status s = check_rows("value", value, value_stride, num_kv_heads, head_dim)) return s;
+    if (pa_status s = check_rows("out", out, out_stride, num_heads, head_dim)) return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (pa::validate_enabled())
+        if (pa_status s = pa::validate_starts(seq_start, num_seqs, num_tokens, max_seq_len, st))
+            return s;
+    int dev = 0, sms = 0;
+    if (pa_status s = pa::cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) return s;
+    if (pa_status s = pa::cuda_status(
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "SM count"))
+        return s;
+    PromptParams p{};
+    p.out = out;
+    p.err = pa::device_error_word();
+    p.out_stride = out_stride;
+    p.num_tokens = num_tokens;
+    p.max_len = max_seq_len;
+    p.num_kv_heads = num_kv_heads;
+    p.group = group;
+    p.tokens = kRows / group;
+    const int per_task = 2 * p.tokens;
+    p.max_chunks = (max_seq_len + per_task - 1) / per_task;
+    // not 0: a masked score of -inf stays one (a score of 2^100 still has a weight of 1)
+    p.scale_log2 = fmaxf(scale * kLog2e, FLT_MIN);
+    CUtensorMap maps[3];
+    if (pa_status s = pa::rows_tensor_map_heads(&maps[0], q, num_tokens, q_stride, num_heads,
+                                                head_dim, group, p.tokens))
+        return s;
+    if (pa_status s = pa::rows_tensor_map_tokens(&maps[1], key, num_tokens, key_stride,
+                                                 num_kv_heads, head_dim, kKeys))
+        return s;
+    if (pa_status s = pa::rows_tensor_map_tokens(&maps[2], value, num_tokens, value_stride,
+                                                 num_kv_heads, head_dim, kKeys))
+        return s;
+    for (int s0 = 0; s0 < num_seqs; s0 += kLaunchSeqs) {
+        p.start = seq_start + s0;
+        p.num_seqs = std::min(kLaunchSeqs, num_seqs - s0);
+        // at most so many tasks
+        const int64_t chunks = std::min((int64_t)p.num_seqs * p.max_chunks,
+                                        (int64_t)num_tokens / per_task + p.num_seqs);
+        if (chunks * num_kv_heads > 0x7fffffff)
+            return fail(PA_ERR_UNSUPPORTED, "too many rows for one launch");
+        const int64_t grid = std::min<int64_t>(sms, chunks * num_kv_heads);
+        pa_status s;
+        if (dtype == PA_BF16)
+            s = head_dim == 128 ? launch<__nv_bfloat16, 128>(maps, p, grid, st)
+                                : launch<__nv_bfloat16, 64>(maps, p, grid, st);
+        else
+            s = head_dim == 128 ? launch<__half, 128>(maps, p, grid, st)
+                                : launch<__half, 64>(maps, p, grid, st);
+        if (s) return s;
+    }
+    return PA_OK;
+}

@@ -70,6 +70,20 @@ pa_status make_map_tile(CUtensorMap* m, const void* cache, int num_blocks, int h
     return PA_OK;
 }
 
+pa_status encode_rows(CUtensorMap* m, const void* rows, int rank, const cuuint64_t* dims,
+                      const cuuint64_t* strides, const cuuint32_t* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return pa::fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(rows), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return pa::fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled (rows) failed (%d)", (int)r);
+    return PA_OK;
+}
+
 struct Entry {
     const void* ptr;
     int num_blocks, num_kv_heads, head_dim, elem_bytes, device;
@@ -82,6 +96,23 @@ int g_n = 0, g_next = 0;
 }  // namespace
 
 namespace pa {
+
+pa_status rows_tensor_map_heads(CUtensorMap* out, const void* rows, int num_tokens, int64_t stride,
+                                int heads, int head_dim, int box_heads, int box_tokens) {
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)num_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    return encode_rows(out, rows, 3, dims, strides, box);
+}
+
+pa_status rows_tensor_map_tokens(CUtensorMap* out, const void* rows, int num_tokens,
+                                 int64_t stride, int heads, int head_dim, int box_tokens) {
+    const cuuint64_t dims[4] = {64, (cuuint64_t)num_tokens, (cuuint64_t)head_dim / 64,
+                                (cuuint64_t)heads};
+    const cuuint64_t strides[3] = {(cuuint64_t)stride * 2, 128, (cuuint64_t)head_dim * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, (cuuint32_t)head_dim / 64, 1};
+    return encode_rows(out, rows, 4, dims, strides, box);
+}
 
 pa_status cache_tensor_map_tile(CUtensorMap* out, const void* ptr, int num_blocks,
                                 int num_kv_heads) {
