@@ -20,8 +20,8 @@
 // with its place in the prompt), dealt out to and fro over the CTAs. Its roles:
 //   warps 0-3, 4-7   softmax of Q tile 0 and 1
 //   warps 8-11       epilogue: O / l to global memory while the next task runs
-//   warp 12          issues all products: P_0 V, Q_0 K'^T, P_1 V, Q_1 K'^T, so that
-//                    the softmax of either tile has the other's products to run in
+//   warps 12, 15     issue the products of Q tile 0 and 1: the softmax of either tile
+//                    has the other's products to run in
 //   warp 13          TMA: Q tiles, K and V tiles into a ring
 //   warp 14          finds the tasks
 // Every wait is bounded; one that gives up ends every role's loop.
@@ -62,14 +62,14 @@ struct Layout {
     static constexpr int kKVFull = 0, kKVEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + 2,
                          kSFull = kQEmpty + 2, kPFull = kSFull + 2 /* [tile][half] */,
                          kOFull = kPFull + 4, kOFree = kOFull + 2, kLFull = kOFree + 2,
-                         kTaskFull = kLFull + 2, kTaskEmpty = kTaskFull + 2, kFin = kTaskEmpty + 2,
-                         kNumBars = kFin + 1;
-    static constexpr int kTaskOff = kBarOff + 8 * kNumBars + 8;   // two task records
+                         kClean = kLFull + 2, kTaskFull = kClean + kStages, kTaskEmpty = kTaskFull + 2,
+                         kFin = kTaskEmpty + 2, kTurn = kFin + 2, kNumBars = kTurn + 2;
+    static constexpr int kTaskOff = (kBarOff + 8 * kNumBars + 15) / 16 * 16;   // two task records
     static constexpr int kFlagOff = kTaskOff + 2 * 32;            // TMEM address, abort flag
     static constexpr int kSmem = kFlagOff + 16 + 1024;            // + alignment slack
     static_assert(kTaskOff % 16 == 0 && kSmem <= 227 * 1024, "shared memory per CTA");
 };
-// TMEM columns: S of Q tile x at 128 x (P over its first 64), O at 256 + D x
+// TMEM columns: S of Q tile x at 128 x (P over its last 64), O at 256 + D x
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 
 struct PromptParams {
@@ -108,19 +108,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
-    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
-        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d0), "=f"(d1)
-        : "f"(a0), "f"(a1), "f"(b), "f"(c));
-}
-__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+// a * b + c of two neighbours, b and c the same for both
+__device__ __forceinline__ void fma2(float& d0, float& d1, uint32_t a0, uint32_t a1, uint64_t b,
+                                     uint64_t c) {
     asm("{\n\t.reg .b64 ra, rd;\n\t"
-        "mov.b64 rd, {%0, %1};\n\tmov.b64 ra, {%2, %3};\n\t"
-        "add.rn.f32x2 rd, rd, ra;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "+f"(d0), "+f"(d1)
-        : "f"(a0), "f"(a1));
+        "mov.b64 ra, {%2, %3};\n\t"
+        "fma.rn.f32x2 rd, ra, %4, %5;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "r"(a0), "r"(a1), "l"(b), "l"(c));
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void add2(uint64_t& d, float a0, float a1) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(pair(a0, a1)));
+}
+__device__ __forceinline__ float sum_of(uint64_t d) {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+    return a + b;
 }
 
 template <typename T>
@@ -160,6 +168,31 @@ __device__ __forceinline__ void fewer_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(e));
+    return e != 0;
+}
+
+// A place in the ring of K and V tiles, and the parity of its use.
+template <int kStages>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ Ring next() const {
+        Ring r;
+        r.slot = slot + 1 == kStages ? 0 : slot + 1;
+        r.phase = slot + 1 == kStages ? phase ^ 1 : phase;
+        return r;
+    }
+    __device__ __forceinline__ void advance(uint32_t n) {
+        const uint32_t at = slot + n;
+        phase ^= (at / kStages) & 1;
+        slot = at % kStages;
+    }
+};
+
 // Length of prompt s, cut to what the tensors hold.
 __device__ __forceinline__ int length_of(const PromptParams& p, int s, int& start) {
     start = min(max(__ldg(p.start + s), 0), p.num_tokens);
@@ -191,11 +224,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     pa::grid_dependents_launch();
     if (threadIdx.x == 0) {
         for (int i = 0; i < LY::kNumBars; ++i) {
-            // arrivals: P, l and a free O from the four warps of a group; a task record from
-            // every warp that reads it
+            // arrivals: P, l, zeroed V rows and a free O from the four warps of a group; a free
+            // K or V tile from both issuing warps; a task record from every warp that reads it
             const int n = (i >= LY::kPFull && i < LY::kOFull) || (i >= LY::kOFree && i < LY::kTaskFull)
                               ? 4
-                          : i >= LY::kTaskEmpty && i < LY::kFin ? 14
+                          : i >= LY::kKVEmpty && i < LY::kQFull ? 2
+                          : i >= LY::kTaskEmpty && i < LY::kFin ? 15
                                                                : 1;
             pa::mbar_init(bar(i), n);
         }
@@ -224,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
     };
     auto wait_one = [&](int b, uint32_t parity, unsigned int code) -> bool {
+        if (pa::mbar_try_wait(bar(b), parity)) return true;
         const bool ok = pa::mbar_wait(bar(b), parity, p.err, code) && !*abort_flag;
         if (!ok) *abort_flag = 1;
         return ok;
@@ -237,25 +272,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) pa::mbar_arrive(bar(LY::kTaskEmpty + (i & 1)));
         return t.head >= 0;
     };
+    auto read_task_one = [&](int i, Task& t) -> bool {
+        if (!wait_one(LY::kTaskFull + (i & 1), (i >> 1) & 1, pa::ERR_WAIT_FULL)) return false;
+        volatile Task& r = tasks[i & 1];
+        t.start = r.start, t.len = r.len, t.off = r.off, t.head = r.head;
+        pa::mbar_arrive(bar(LY::kTaskEmpty + (i & 1)));
+        return t.head >= 0;
+    };
     const int G = p.group, tokens = p.tokens;
+    // whether the last products of both Q tiles reach V rows behind the prompt, in one tile:
+    // then Q tile 0's softmax zeroes them, and Q tile 1's products wait for that
+    auto first_cleans = [&](const Task& t) {
+        const Span a(t, tokens, 0), b(t, tokens, 1);
+        return b.keys > a.keys && a.tiles == b.tiles && ((a.keys + 15) & ~15) > t.len;
+    };
 
     if (warp < 8) {
         // ---------------- softmax of Q tile x: one thread a row ----------------
         more_registers<176>();
+        // 176 + 176 + 80 + 80: the 4 x 128 registers a thread of the launch
         const int x = warp >> 2;
         const int row = 32 * (warp & 3) + lane;
         const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t s_tm = tmem + lane_at + 128 * x, o_tm = tmem + lane_at + kOCol + D * x;
         const int token = row / G;                           // of the tile
-        const float sl2 = p.scale_log2;
-        uint32_t it = 0, n_s = 0, n_o = 0;                   // K/V tiles, S tiles, tasks so far
+        const uint64_t sl2 = pair(p.scale_log2, p.scale_log2);
+        Ring<kStages> kv;                                    // the task's first K tile
+        uint32_t n_s = 0, n_o = 0;                           // S tiles and tasks so far
         Task task;
         for (int i = 0; read_task(i, task); ++i) {
             const bool two = task.len - task.off > tokens;
             const Span all(task, tokens, two ? 1 : 0), span(task, tokens, x);
-            const uint32_t it0 = it;
-            it += 2 * all.tiles;
-            if (x == 1 && !two) continue;
+            if (x == 1 && !two) {
+                kv.advance(2 * all.tiles);
+                continue;
+            }
             // rows past the tile's tokens or the prompt hold anything; they are not written
             const int bound = span.first + token;
             float m_run = -INFINITY, l_run = 0.f;
@@ -264,103 +315,136 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait(LY::kSFull + x, n_s & 1, pa::ERR_WAIT_FULL);
                 if (!ok) break;
                 pa::tc::fence_after_sync();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) pa::tc::ld_32cols_nowait(s_tm + 32 * c, s[c]);
-                pa::tc::wait_ld();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) pa::tc::loaded(s[c]);
-                auto sv = [&](int j) -> float& { return reinterpret_cast<float&>(s[j >> 5][j & 31]); };
                 const int key0 = t * kKeys;
-                if (key0 + kKeys - 1 > span.first) {         // a tile that some row must not see all of
-#pragma unroll
-                    for (int j = 0; j < kKeys; ++j)
-                        if (key0 + j > bound) sv(j) = -INFINITY;
-                }
-                float m4[4] = {sv(0), sv(1), sv(2), sv(3)};
-#pragma unroll
-                for (int j = 4; j < kKeys - 4; j += 8)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], sv(j + 2 * q), sv(j + 2 * q + 1));
-                m4[0] = max3(m4[0], sv(kKeys - 4), sv(kKeys - 3));
-                m4[1] = max3(m4[1], sv(kKeys - 2), sv(kKeys - 1));
-                float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-                mx = mx == -INFINITY ? mx : mx * sl2;        // the scale is not negative
+                const int in_tile = span.keys - key0;        // visible keys of this tile
+                const bool cut = key0 + kKeys - 1 > span.first;   // some row must not see all
+                // Weights of the first 64 keys against the maximum so far, while the maximum of
+                // all 128 is found beside them; in the rare case that it has moved, once more. P
+                // goes over the columns of the last 64 keys' S, which are in registers by then.
                 float alpha = 1.f;
-                const bool moved = mx > m_run + kLazyMax;
-                if (moved) {
-                    alpha = pa::ex2(m_run - mx);             // 0 while m_run is -inf
-                    m_run = mx;
-                }
-                // O may be scaled now: S of this tile was issued behind the last P V, and the
-                // barrier says that both are done; the next P V waits for this P
-                if (t > 0 && __any_sync(0xffffffffu, moved)) {
-#pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {
-                        uint32_t ov[16];
-                        pa::tc::ld_16cols(o_tm + 16 * q, ov);
+                uint64_t l4[2], nm;
+                uint32_t hi[2][32];
+                auto weights = [&](uint32_t (&c)[32], int at) {
+                    uint32_t pk[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                        pa::tc::st_16cols(o_tm + 16 * q, ov);
+                    for (int j = 0; j < 32; j += 4) {
+#pragma unroll
+                        for (int q = 0; q < 4; q += 2) {
+                            float a, b;
+                            fma2(a, b, c[j + q], c[j + q + 1], sl2, nm);
+                            a = pa::ex2(a);
+                            b = pa::ex2(b);
+                            pk[(j + q) / 2] = pack2<T>(a, b);
+                            add2(l4[q / 2], a, b);
+                        }
+                    }
+                    pa::tc::st_16cols_nowait(s_tm + 64 + 16 * at, pk);
+                };
+                auto mask = [&](uint32_t (&c)[32], int first) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (first + j > bound) c[j] = 0xff800000u;   // -inf
+                };
+                auto max32 = [&](uint32_t (&c)[32], float (&m)[4]) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            m[q] = max3(m[q], __uint_as_float(c[j + 2 * q]),
+                                        __uint_as_float(c[j + 2 * q + 1]));
+                };
+                auto publish = [&](int half) {
+                    pa::tc::wait_st();
+                    pa::tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) pa::mbar_arrive(bar(LY::kPFull + 2 * x + half));
+                };
+                pa::tc::ld_32cols_nowait(s_tm + 64, hi[0]);
+                pa::tc::ld_32cols_nowait(s_tm + 96, hi[1]);
+                for (bool again = true; again;) {
+                    uint32_t lo[2][32];
+                    pa::tc::ld_32cols_nowait(s_tm, lo[0]);
+                    pa::tc::ld_32cols_nowait(s_tm + 32, lo[1]);
+                    pa::tc::wait_ld();
+                    pa::tc::loaded(lo[0]);
+                    pa::tc::loaded(lo[1]);
+                    pa::tc::loaded(hi[0]);
+                    pa::tc::loaded(hi[1]);
+                    if (cut) {
+                        mask(lo[0], key0);
+                        mask(lo[1], key0 + 32);
+                        mask(hi[0], key0 + 64);
+                        mask(hi[1], key0 + 96);
+                    }
+                    const float m = m_run == -INFINITY ? 0.f : -m_run;
+                    nm = pair(m, m);
+                    l4[0] = l4[1] = 0;
+                    weights(lo[0], 0);
+                    weights(lo[1], 1);
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    max32(lo[0], m4);
+                    max32(lo[1], m4);
+                    max32(hi[0], m4);
+                    max32(hi[1], m4);
+                    float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+                    mx = mx == -INFINITY ? mx : mx * p.scale_log2;   // the scale is positive
+                    const bool moved = mx > m_run + kLazyMax;
+                    again = __any_sync(0xffffffffu, moved);
+                    if (again) {
+                        if (moved) {
+                            alpha = pa::ex2(m_run - mx);         // 0 while m_run is -inf
+                            m_run = mx;
+                        }
+                        // O may be scaled now: S of this tile was issued behind the last P V, and
+                        // the barrier says that both are done; the next P V waits for this P
+                        if (t > 0) {
+#pragma unroll 1
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t ov[16];
+                                pa::tc::ld_16cols(o_tm + 16 * q, ov);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                pa::tc::st_16cols(o_tm + 16 * q, ov);
+                            }
+                        }
                     }
                 }
-                const float nm = m_run == -INFINITY ? 0.f : -m_run;
                 // V rows behind the prompt that a product reaches may hold anything: zeroed, so
                 // that a weight of 0 never meets a NaN. The first Q tile to reach them does it.
-                const int in_tile = span.keys - key0;        // visible keys of this tile
                 if (t == span.tiles - 1) {
-                    const int end = (span.keys + 15) & ~15;
-                    const bool first_has = x == 1 && [&] {
-                        const Span f(task, tokens, 0);
-                        return f.tiles == span.tiles && ((f.keys + 15) & ~15) > task.len;
-                    }();
-                    if (end > task.len && !first_has) {
-                        const uint32_t v = it0 + 2 * t + 1;
-                        ok = wait(LY::kKVFull + v % kStages, (v / kStages) & 1, pa::ERR_WAIT_FULL);
+                    const bool reaches = ((span.keys + 15) & ~15) > task.len;
+                    if (reaches && !(x == 1 && first_cleans(task))) {
+                        Ring<kStages> v = kv;
+                        v.advance(2 * t + 1);
+                        ok = wait(LY::kKVFull + v.slot, v.phase, pa::ERR_WAIT_FULL);
                         if (!ok) break;
-                        const int z0 = task.len - key0, n = (end - task.len) * (D / 8);
+                        const int z0 = task.len - key0;
+                        const int n = (((span.keys + 15) & ~15) - task.len) * (D / 8);
                         for (int e = row; e < n; e += kRows) {
                             const int r = z0 + e / (D / 8), ch = e % (D / 8);
-                            const uint32_t dst = base + LY::kKVOff + (v % kStages) * LY::kTile +
+                            const uint32_t dst = base + LY::kKVOff + v.slot * LY::kTile +
                                                  (ch >> 3) * LY::kHalf + r * 128 + ((ch & 7) << 4);
                             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0u)
                                          : "memory");
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    }
-                }
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (32 * c < in_tile) {                  // else no product reads it
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            float e[4];
-#pragma unroll
-                            for (int q = 0; q < 4; q += 2) {
-                                fma2(e[q], e[q + 1], sv(32 * c + j + q), sv(32 * c + j + q + 1), sl2,
-                                     nm);
-                                e[q] = pa::ex2(e[q]);
-                                e[q + 1] = pa::ex2(e[q + 1]);
-                                pk[(j + q) / 2] = pack2<T>(e[q], e[q + 1]);
-                            }
-                            add2(l4[0], l4[1], e[0], e[1]);
-                            add2(l4[2], l4[3], e[2], e[3]);
+                        if (x == 0 && first_cleans(task)) {
+                            __syncwarp();
+                            if (lane == 0) pa::mbar_arrive(bar(LY::kClean + v.slot));
                         }
-                        pa::tc::st_16cols_nowait(s_tm + 16 * c, pk);
-                    }
-                    if (c & 1) {
-                        pa::tc::wait_st();
-                        pa::tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) pa::mbar_arrive(bar(LY::kPFull + 2 * x + (c >> 1)));
                     }
                 }
-                l_run = l_run * alpha + ((l4[0] + l4[1]) + (l4[2] + l4[3]));
+                publish(0);
+                if (in_tile > 64) {                          // else no product reads it
+                    weights(hi[0], 2);
+                    weights(hi[1], 3);
+                }
+                publish(1);
+                l_run = l_run * alpha + (sum_of(l4[0]) + sum_of(l4[1]));
             }
             if (!ok) break;
+            kv.advance(2 * all.tiles);
             // the sums of the last task have been read
             if (n_o > 0 && !wait(LY::kOFree + x, (n_o - 1) & 1, pa::ERR_WAIT_EMPTY)) break;
             ++n_o;
@@ -370,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < 12) {
         // ---------------- epilogue: O / l of each Q tile ----------------
-        fewer_registers<96>();
+        fewer_registers<80>();
         const int row = 32 * (warp & 3) + lane;
         const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
         const int token = row / G, head = row % G;
@@ -423,130 +507,151 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
         }
     } else {
-        fewer_registers<64>();
-        if (warp == 12) {
-            // ---------------- all products, issued by one elected lane ----------------
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t sb = __shfl_sync(0xffffffffu, base, 0);
-            constexpr uint32_t idesc_qk = pa::tc::idesc_f16(kBF16, false, false, kRows, kKeys);
-            constexpr uint32_t idesc_pv = pa::tc::idesc_f16(kBF16, false, true, kRows, D);
-            // the descriptor of address a + o is the one of a plus o >> 4
-            const uint64_t dq = pa::tc::smem_desc_sw128(sb, 16, 1024);
-            const uint64_t dk = pa::tc::smem_desc_sw128(sb + LY::kKVOff, 16, 1024);
-            const uint64_t dv = pa::tc::smem_desc_sw128(sb + LY::kKVOff, LY::kHalf, 1024);
-            uint32_t it = 0, n_s[2] = {0, 0}, n_q[2] = {0, 0};
-            auto kv_ready = [&](uint32_t i) {
-                return wait(LY::kKVFull + i % kStages, (i / kStages) & 1, pa::ERR_WAIT_FULL);
-            };
-            auto kv_done = [&](uint32_t i) {
-                pa::tc::commit_warp(bar(LY::kKVEmpty + i % kStages));
-            };
-            auto issue_qk = [&](int x, uint32_t i) {         // S_x = Q_x K^T
-                pa::tc::fence_after_sync();
-                const uint64_t a = dq + (uint64_t)((x * LY::kTile) >> 4);
-                const uint64_t b = dk + (uint64_t)(((i % kStages) * LY::kTile) >> 4);
+        fewer_registers<80>();
+        if (warp == 12 || warp == 15) {
+            // ---------------- the products of Q tile x, issued by one elected lane ----------------
+            // One branch around everything: a product then issues in fewer cycles than it runs
+            // (64 at N = 128; with an election around each it took 140 to 160). A warp a Q tile:
+            // the waits of one overlap the products of the other. Both read every K and V tile
+            // (or pass it on), and P V and Q K'^T of a Q tile run in the order of their issue, so
+            // that P is read before the next S takes its columns.
+            if (elect_one()) {
+                const int x = warp == 12 ? 0 : 1;
+                constexpr uint32_t idesc_qk = pa::tc::idesc_f16(kBF16, false, false, kRows, kKeys);
+                constexpr uint32_t idesc_pv = pa::tc::idesc_f16(kBF16, false, true, kRows, D);
+                // the descriptor of address a + o is the one of a plus o >> 4
+                const uint64_t dq = pa::tc::smem_desc_sw128(base + x * LY::kTile, 16, 1024);
+                const uint64_t dk = pa::tc::smem_desc_sw128(base + LY::kKVOff, 16, 1024);
+                const uint64_t dv = pa::tc::smem_desc_sw128(base + LY::kKVOff, LY::kHalf, 1024);
+                const uint32_t s_tm = tmem + 128 * x, o_tm = tmem + kOCol + D * x;
+                Ring<kStages> kv;
+                uint32_t n_s = 0, n_q = 0;
+                uint32_t cleaned = 0;                        // parities of the ring's kClean
+                // With two Q tiles their products take turns: P V and Q K'^T of one, then of the
+                // other, or both softmaxes would come to run at once and then both products.
+                // The turn goes over before the last products are issued, so that the pipe does
+                // not wait for the other warp to wake up.
+                uint32_t turns = 0;
+                auto my_turn = [&](bool two) -> bool {
+                    return !two || wait_one(LY::kTurn + x, (turns++ & 1) ^ (x ^ 1), pa::ERR_WAIT_FULL);
+                };
+                auto pass_turn = [&](bool two) {
+                    if (two) pa::mbar_arrive(bar(LY::kTurn + (x ^ 1)));
+                };
+                auto issue_qk = [&](bool two) {              // S = Q K^T
+                    pa::tc::fence_after_sync();
+                    const uint64_t b = dk + (uint64_t)((kv.slot * LY::kTile) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t o = ((kk >> 2) * LY::kHalf + (kk & 3) * 32) >> 4;
-                    pa::tc::mma_f16_ss_warp(tm + 128 * x, a + o, b + o, idesc_qk, kk > 0 ? 1u : 0u);
-                }
-                pa::tc::commit_warp(bar(LY::kSFull + x));
-            };
-            auto issue_pv = [&](int x, uint32_t i, int half, int steps, bool more) {   // O_x += P_x V
-                pa::tc::fence_after_sync();
-                const uint64_t b = dv + (uint64_t)(((i % kStages) * LY::kTile) >> 4);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int kb = 4 * half + k;
-                    if (kb < steps)
-                        pa::tc::mma_f16_ts_warp(tm + kOCol + D * x, tm + 128 * x + 8 * kb,
-                                                b + (uint64_t)((kb * 16 * 128) >> 4), idesc_pv,
-                                                more || kb > 0 ? 1u : 0u);
-                }
-            };
-            Task task;
-            for (int i = 0; read_task(i, task); ++i) {
-                const int nq = task.len - task.off > tokens ? 2 : 1;
-                const Span s0(task, tokens, 0), s1(task, tokens, nq - 1);
-                const int tiles = s1.tiles;
-                bool ok = kv_ready(it);
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (ok && x < nq) {
-                        ok = wait(LY::kQFull + x, n_q[x] & 1, pa::ERR_WAIT_FULL);
-                        if (!ok) break;
-                        issue_qk(x, it);
-                        if ((x ? s1 : s0).tiles == 1) pa::tc::commit_warp(bar(LY::kQEmpty + x));
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t o = ((kk >> 2) * LY::kHalf + (kk & 3) * 32) >> 4;
+                        pa::tc::mma_f16_ss(s_tm, dq + o, b + o, idesc_qk, kk > 0 ? 1u : 0u);
+                        if (kk == D / 16 - 3) pass_turn(two);
                     }
-                if (ok) kv_done(it);
-                for (int t = 0; ok && t < tiles; ++t) {
-                    const uint32_t iv = it + 2 * t + 1, ik = iv + 1;
-                    ok = kv_ready(iv);
+                    pa::tc::commit(bar(LY::kSFull + x));
+                    pa::tc::commit(bar(LY::kKVEmpty + kv.slot));
+                    kv = kv.next();
+                };
+                auto issue_pv = [&](int half, int steps, bool more) {   // O += P V
+                    pa::tc::fence_after_sync();
+                    const uint64_t b = dv + (uint64_t)((kv.slot * LY::kTile) >> 4);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        if (!ok || x >= nq) continue;
-                        const Span& s = x ? s1 : s0;
-                        if (t < s.tiles) {
-                            // O of the last task has been read
-                            if (t == 0 && n_q[x] > 0)
-                                ok = wait(LY::kOFree + x, (n_q[x] - 1) & 1, pa::ERR_WAIT_EMPTY);
-                            const int steps = min(8, (s.keys - t * kKeys + 15) >> 4);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                ok = ok && wait(LY::kPFull + 2 * x + h, n_s[x] & 1, pa::ERR_WAIT_FULL);
-                                if (ok) issue_pv(x, iv, h, steps, t > 0);
-                            }
-                            if (!ok) continue;
-                            ++n_s[x];
-                            if (t == s.tiles - 1) pa::tc::commit_warp(bar(LY::kOFull + x));
-                        }
-                        if (x == nq - 1) kv_done(iv);
-                        if (t + 1 < s.tiles) {
-                            // the products run in the order of their issue: P V of this tile has
-                            // read P before S takes its columns
-                            ok = kv_ready(ik);
-                            if (!ok) continue;
-                            issue_qk(x, ik);
-                            if (t + 2 == s.tiles) pa::tc::commit_warp(bar(LY::kQEmpty + x));
-                            if (x == nq - 1) kv_done(ik);
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        const int kb = 4 * half + k;
+                        if (kb < steps)
+                            pa::tc::mma_f16_ts(o_tm, s_tm + 64 + 8 * kb,
+                                               b + (uint64_t)((kb * 16 * 128) >> 4), idesc_pv,
+                                               more || kb > 0 ? 1u : 0u);
                     }
-                }
-                if (!ok) break;
-                it += 2 * tiles;
-                ++n_q[0];
-                if (nq == 2) ++n_q[1];
-            }
-            // every product and commit of this warp is done before TMEM and the CTA go
-            pa::tc::commit_warp(bar(LY::kFin));
-            if (!__all_sync(0xffffffffu, pa::mbar_wait(bar(LY::kFin), 0, nullptr, 0)) && lane == 0 &&
-                p.err)
-                atomicOr(p.err, pa::ERR_WAIT_DRAIN);
-        } else if (warp == 13) {
-            // ---------------- TMA: Q tiles, then K and V tiles in turn ----------------
-            uint32_t it = 0, n_q[2] = {0, 0};
-            const uint32_t q_bytes = tokens * G * 128;
-            Task task;
-            for (int i = 0; read_task(i, task); ++i) {
+                };
+                auto pass_on = [&](int n) -> bool {          // tiles that only the other one reads
+                    for (int k = 0; k < n; ++k) {
+                        if (!wait_one(LY::kKVFull + kv.slot, kv.phase, pa::ERR_WAIT_FULL)) return false;
+                        pa::mbar_arrive(bar(LY::kKVEmpty + kv.slot));
+                        kv = kv.next();
+                    }
+                    return true;
+                };
+                Task task;
                 bool ok = true;
-                if (lane == 0) {
+                for (int i = 0; ok && read_task_one(i, task); ++i) {
+                    const bool two = task.len - task.off > tokens;
+                    const int tiles = Span(task, tokens, two ? 1 : 0).tiles;
+                    if (x == 1 && !two) {
+                        ok = pass_on(2 * tiles);
+                        continue;
+                    }
+                    const Span s(task, tokens, x);
+                    const int both = two ? Span(task, tokens, 0).tiles : 0;   // tiles of either
+                    ok = wait_one(LY::kKVFull + kv.slot, kv.phase, pa::ERR_WAIT_FULL) &&
+                         wait_one(LY::kQFull + x, n_q & 1, pa::ERR_WAIT_FULL) && my_turn(two);
+                    if (!ok) break;
+                    issue_qk(two);
+                    for (int t = 0; t < s.tiles; ++t, ++n_s) {
+                        const Ring<kStages> next = kv.next();
+                        const bool more = t + 1 < s.tiles, turn = t < both;
+                        // this V tile, the next K tile, and O of the last task read
+                        ok = wait_one(LY::kKVFull + kv.slot, kv.phase, pa::ERR_WAIT_FULL);
+                        if (more)
+                            ok = ok && wait_one(LY::kKVFull + next.slot, next.phase, pa::ERR_WAIT_FULL);
+                        if (t == 0 && n_q > 0)
+                            ok = ok && wait_one(LY::kOFree + x, (n_q - 1) & 1, pa::ERR_WAIT_EMPTY);
+                        if (!more) {
+                            pa::tc::commit(bar(LY::kQEmpty + x));
+                            if (x == 1 && first_cleans(task)) {
+                                ok = ok && wait_one(LY::kClean + kv.slot, (cleaned >> kv.slot) & 1,
+                                                    pa::ERR_WAIT_FULL);
+                                cleaned ^= 1u << kv.slot;
+                            }
+                        }
+                        const int steps = (s.keys - t * kKeys + 15) >> 4;
+                        ok = ok && my_turn(turn) &&
+                             wait_one(LY::kPFull + 2 * x, n_s & 1, pa::ERR_WAIT_FULL);
+                        if (!ok) break;
+                        issue_pv(0, steps, t > 0);
+                        ok = wait_one(LY::kPFull + 2 * x + 1, n_s & 1, pa::ERR_WAIT_FULL);
+                        if (!ok) break;
+                        issue_pv(1, steps, true);
+                        if (!more) {
+                            pass_turn(turn);
+                            pa::tc::commit(bar(LY::kOFull + x));
+                        }
+                        pa::tc::commit(bar(LY::kKVEmpty + kv.slot));
+                        kv = next;
+                        if (more) issue_qk(turn);
+                    }
+                    ok = ok && pass_on(2 * (tiles - s.tiles));
+                    ++n_q;
+                }
+                // every product and commit is done before TMEM and the CTA go
+                pa::tc::commit(bar(LY::kFin + x));
+                if (!pa::mbar_wait(bar(LY::kFin + x), 0, nullptr, 0) && p.err)
+                    atomicOr(p.err, pa::ERR_WAIT_DRAIN);
+            }
+            __syncwarp();
+        } else if (warp == 13) {
+            // ---------------- TMA: Q tiles, K and V tiles in turn ----------------
+            if (elect_one()) {
+                Ring<kStages> kv;
+                uint32_t loaded = 0, n_q[2] = {0, 0};
+                const uint32_t q_bytes = tokens * G * 128;
+                Task task;
+                for (int i = 0; read_task_one(i, task); ++i) {
                     const int nq = task.len - task.off > tokens ? 2 : 1;
                     const int tiles = Span(task, tokens, nq - 1).tiles;
                     auto load = [&](int k) -> bool {         // the task's k-th K (even) or V tile
-                        const uint32_t at = it + k;
-                        if (at >= kStages && !wait_one(LY::kKVEmpty + at % kStages,
-                                                       ((at / kStages) - 1) & 1, pa::ERR_WAIT_EMPTY))
+                        if (loaded >= kStages &&
+                            !wait_one(LY::kKVEmpty + kv.slot, kv.phase ^ 1, pa::ERR_WAIT_EMPTY))
                             return false;
-                        const uint32_t b = bar(LY::kKVFull + at % kStages);
+                        const uint32_t b = bar(LY::kKVFull + kv.slot);
                         pa::mbar_arrive_expect_tx(b, LY::kTile);
-                        tma_load_4d(base + LY::kKVOff + (at % kStages) * LY::kTile,
+                        tma_load_4d(base + LY::kKVOff + kv.slot * LY::kTile,
                                     k & 1 ? &map_v : &map_k, 0, task.start + (k >> 1) * kKeys, 0,
                                     task.head, b);
+                        kv = kv.next();
+                        ++loaded;
                         return true;
                     };
-                    int done = 0;
-                    ok = load(0);
-                    if (ok) done = 1;
+                    bool ok = load(0);
                     for (int x = 0; ok && x < nq; ++x) {
                         // Q of the last task has been read
                         if (n_q[x] > 0)
@@ -559,25 +664,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         task.head * G, task.start + task.off + x * tokens, b);
                         ++n_q[x];
                     }
-                    for (int k = 1; ok && k < 2 * tiles; ++k) {
-                        ok = load(k);
-                        if (ok) done = k + 1;
-                    }
-                    it += done;
+                    for (int k = 1; ok && k < 2 * tiles; ++k) ok = load(k);
+                    if (!ok) break;
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-            }
-            // no copy may be in flight when the CTA ends (those whose tiles were consumed are
-            // not; after a wait gave up, the last of the ring and of Q may be)
-            if (lane == 0 && *abort_flag) {
-                bool ok = true;
-                for (uint32_t u = it > kStages ? it - kStages : 0; u < it; ++u)
-                    ok &= pa::mbar_wait(bar(LY::kKVFull + u % kStages), (u / kStages) & 1, nullptr, 0);
-                for (int x = 0; x < 2; ++x)
-                    if (n_q[x] > 0)
-                        ok &= pa::mbar_wait(bar(LY::kQFull + x), (n_q[x] - 1) & 1, nullptr, 0);
-                if (!ok && p.err) atomicOr(p.err, pa::ERR_WAIT_DRAIN);
+                // no copy may be in flight when the CTA ends (those whose tiles were consumed are
+                // not; after a wait gave up, the last of the ring and of Q may be)
+                if (*abort_flag) {
+                    bool ok = true;
+                    for (uint32_t u = loaded > kStages ? loaded - kStages : 0; u < loaded; ++u)
+                        ok &= pa::mbar_wait(bar(LY::kKVFull + u % kStages), (u / kStages) & 1,
+                                            nullptr, 0);
+                    for (int x = 0; x < 2; ++x)
+                        if (n_q[x] > 0)
+                            ok &= pa::mbar_wait(bar(LY::kQFull + x), (n_q[x] - 1) & 1, nullptr, 0);
+                    if (!ok && p.err) atomicOr(p.err, pa::ERR_WAIT_DRAIN);
+                }
             }
             __syncwarp();
         } else if (warp == 14) {
