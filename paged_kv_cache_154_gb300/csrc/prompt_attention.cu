@@ -44,7 +44,7 @@ namespace {
 constexpr int kRows = 128;               // rows of a Q tile
 constexpr int kKeys = 128;               // keys of a K or V tile
 constexpr int kThreads = 512;
-constexpr int kLaunchSeqs = 512;         // prompts a launch: their chunk counts stay in registers
+constexpr int kLaunchSeqs = 256;         // prompts a launch: their chunk counts stay in registers
 constexpr int kMaxLen = 1 << 22;         // a task's products end well before a wait gives up
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyMax = 8.f;
@@ -193,6 +193,30 @@ struct Ring {
     }
 };
 
+// The rest of a wait whose first look failed, in few instructions (the roles' code takes turns
+// in the instruction caches): false once it has lasted kWaitNs, counted in cycles of 2 GHz, or
+// another one has. The flag holds the error that ends the kernel.
+constexpr uint32_t kWaitClocks = pa::kWaitNs < 1000000000ull ? (uint32_t)(2 * pa::kWaitNs) : 2000000000u;
+
+__device__ __forceinline__ uint32_t cycles() {
+    uint32_t c;
+    asm volatile("mov.u32 %0, %%clock;" : "=r"(c));
+    return c;
+}
+__device__ __forceinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t code,
+                                            volatile uint32_t* abort_flag) {
+    const uint32_t began = cycles();
+#pragma unroll 1
+    while (!pa::mbar_try_wait(bar, parity)) {
+        if (*abort_flag != 0) return false;
+        if (cycles() - began > kWaitClocks) {
+            *abort_flag = code;
+            return false;
+        }
+    }
+    return true;
+}
+
 // Length of prompt s, cut to what the tensors hold.
 __device__ __forceinline__ int length_of(const PromptParams& p, int s, int& start) {
     start = min(max(__ldg(p.start + s), 0), p.num_tokens);
@@ -218,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* const sums = reinterpret_cast<float*>(smem + LY::kSumOff);
     volatile Task* const tasks = reinterpret_cast<volatile Task*>(smem + LY::kTaskOff);
     uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(smem + LY::kFlagOff);
-    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + LY::kFlagOff + 8);
+    volatile uint32_t* const abort_flag =
+        reinterpret_cast<volatile uint32_t*>(smem + LY::kFlagOff + 8);
     auto bar = [&](int i) { return bars + 8u * i; };
 
     pa::grid_dependents_launch();
@@ -249,19 +274,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_holder;
     pa::grid_dependency_wait();
 
-    // a wait by the whole warp, or by one lane; false ends the role
-    auto wait = [&](int b, uint32_t parity, unsigned int code) -> bool {
-        if (__all_sync(0xffffffffu, pa::mbar_try_wait(bar(b), parity))) return true;
-        const bool ok = __all_sync(0xffffffffu, pa::mbar_wait(bar(b), parity, p.err, code)) &&
-                        __shfl_sync(0xffffffffu, *abort_flag, 0) == 0;
-        if (!ok && lane == 0) *abort_flag = 1;
-        return ok;
-    };
-    auto wait_one = [&](int b, uint32_t parity, unsigned int code) -> bool {
+    // a wait by one lane, or by the whole warp; false ends the role
+    auto wait_one = [&](int b, uint32_t parity, uint32_t code) -> bool {
         if (pa::mbar_try_wait(bar(b), parity)) return true;
-        const bool ok = pa::mbar_wait(bar(b), parity, p.err, code) && !*abort_flag;
-        if (!ok) *abort_flag = 1;
-        return ok;
+        return wait_longer(bar(b), parity, code, abort_flag);
+    };
+    auto wait = [&](int b, uint32_t parity, uint32_t code) -> bool {
+        return __all_sync(0xffffffffu, wait_one(b, parity, code));
+    };
+    // what has to have ended before the CTA goes, also after a wait gave up
+    auto drain = [&](int b, uint32_t parity) {
+        if (!pa::mbar_wait(bar(b), parity, nullptr, 0) && p.err) atomicOr(p.err, pa::ERR_WAIT_DRAIN);
     };
     // the i-th task of this CTA
     auto read_task = [&](int i, Task& t) -> bool {
@@ -317,41 +340,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pa::tc::fence_after_sync();
                 const int key0 = t * kKeys;
                 const int in_tile = span.keys - key0;        // visible keys of this tile
-                const bool cut = key0 + kKeys - 1 > span.first;   // some row must not see all
                 // Weights of the first 64 keys against the maximum so far, while the maximum of
                 // all 128 is found beside them; in the rare case that it has moved, once more. P
                 // goes over the columns of the last 64 keys' S, which are in registers by then.
                 float alpha = 1.f;
                 uint64_t l4[2], nm;
-                uint32_t hi[2][32];
-                auto weights = [&](uint32_t (&c)[32], int at) {
+                uint32_t c[4][32];
+                auto weights = [&](int i) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
 #pragma unroll
                         for (int q = 0; q < 4; q += 2) {
                             float a, b;
-                            fma2(a, b, c[j + q], c[j + q + 1], sl2, nm);
+                            fma2(a, b, c[i][j + q], c[i][j + q + 1], sl2, nm);
                             a = pa::ex2(a);
                             b = pa::ex2(b);
                             pk[(j + q) / 2] = pack2<T>(a, b);
                             add2(l4[q / 2], a, b);
                         }
                     }
-                    pa::tc::st_16cols_nowait(s_tm + 64 + 16 * at, pk);
+                    pa::tc::st_16cols_nowait(s_tm + 64 + 16 * i, pk);
                 };
-                auto mask = [&](uint32_t (&c)[32], int first) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (first + j > bound) c[j] = 0xff800000u;   // -inf
-                };
-                auto max32 = [&](uint32_t (&c)[32], float (&m)[4]) {
+                auto max32 = [&](int i, float (&m)[4]) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 8)
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            m[q] = max3(m[q], __uint_as_float(c[j + 2 * q]),
-                                        __uint_as_float(c[j + 2 * q + 1]));
+                            m[q] = max3(m[q], __uint_as_float(c[i][j + 2 * q]),
+                                        __uint_as_float(c[i][j + 2 * q + 1]));
+                };
+                auto scaled_max = [&](float (&m)[4]) {
+                    const float mx = fmaxf(max3(m[0], m[1], m[2]), m[3]);
+                    return mx == -INFINITY ? mx : mx * p.scale_log2;   // the scale is positive
                 };
                 auto publish = [&](int half) {
                     pa::tc::wait_st();
@@ -359,35 +380,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) pa::mbar_arrive(bar(LY::kPFull + 2 * x + half));
                 };
-                pa::tc::ld_32cols_nowait(s_tm + 64, hi[0]);
-                pa::tc::ld_32cols_nowait(s_tm + 96, hi[1]);
-                for (bool again = true; again;) {
-                    uint32_t lo[2][32];
-                    pa::tc::ld_32cols_nowait(s_tm, lo[0]);
-                    pa::tc::ld_32cols_nowait(s_tm + 32, lo[1]);
-                    pa::tc::wait_ld();
-                    pa::tc::loaded(lo[0]);
-                    pa::tc::loaded(lo[1]);
-                    pa::tc::loaded(hi[0]);
-                    pa::tc::loaded(hi[1]);
-                    if (cut) {
-                        mask(lo[0], key0);
-                        mask(lo[1], key0 + 32);
-                        mask(hi[0], key0 + 64);
-                        mask(hi[1], key0 + 96);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pa::tc::ld_32cols_nowait(s_tm + 32 * i, c[i]);
+                pa::tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pa::tc::loaded(c[i]);
+                if (key0 + kKeys - 1 > span.first) {         // some row must not see all
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int last = bound - key0 - 32 * i;   // visible keys of these, less 1
+                        if (key0 + 32 * i + 31 > span.first) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j > last) c[i][j] = 0xff800000u;   // -inf
+                        }
                     }
+                }
+                if (t == 0) {                                // a first guess, not above the maximum
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    max32(0, m4);
+                    m_run = scaled_max(m4);
+                }
+                for (bool again = true; again;) {
                     const float m = m_run == -INFINITY ? 0.f : -m_run;
                     nm = pair(m, m);
                     l4[0] = l4[1] = 0;
-                    weights(lo[0], 0);
-                    weights(lo[1], 1);
+                    weights(0);
+                    weights(1);
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    max32(lo[0], m4);
-                    max32(lo[1], m4);
-                    max32(hi[0], m4);
-                    max32(hi[1], m4);
-                    float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-                    mx = mx == -INFINITY ? mx : mx * p.scale_log2;   // the scale is positive
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) max32(i, m4);
+                    const float mx = scaled_max(m4);
                     const bool moved = mx > m_run + kLazyMax;
                     again = __any_sync(0xffffffffu, moved);
                     if (again) {
@@ -399,13 +422,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // the barrier says that both are done; the next P V waits for this P
                         if (t > 0) {
 #pragma unroll 1
-                            for (int q = 0; q < D / 16; ++q) {
-                                uint32_t ov[16];
-                                pa::tc::ld_16cols(o_tm + 16 * q, ov);
+                            for (int q = 0; q < D / 8; ++q) {
+                                uint32_t ov[8];
+                                pa::tc::ld_8cols(o_tm + 8 * q, ov);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
+                                for (int e = 0; e < 8; ++e)
                                     ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                                pa::tc::st_16cols(o_tm + 16 * q, ov);
+                                pa::tc::st_8cols(o_tm + 8 * q, ov);
                             }
                         }
                     }
@@ -437,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 publish(0);
                 if (in_tile > 64) {                          // else no product reads it
-                    weights(hi[0], 2);
-                    weights(hi[1], 3);
+                    weights(2);
+                    weights(3);
                 }
                 publish(1);
                 l_run = l_run * alpha + (sum_of(l4[0]) + sum_of(l4[1]));
@@ -624,8 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // every product and commit is done before TMEM and the CTA go
                 pa::tc::commit(bar(LY::kFin + x));
-                if (!pa::mbar_wait(bar(LY::kFin + x), 0, nullptr, 0) && p.err)
-                    atomicOr(p.err, pa::ERR_WAIT_DRAIN);
+                drain(LY::kFin + x, 0);
             }
             __syncwarp();
         } else if (warp == 13) {
@@ -670,14 +692,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // no copy may be in flight when the CTA ends (those whose tiles were consumed are
                 // not; after a wait gave up, the last of the ring and of Q may be)
                 if (*abort_flag) {
-                    bool ok = true;
                     for (uint32_t u = loaded > kStages ? loaded - kStages : 0; u < loaded; ++u)
-                        ok &= pa::mbar_wait(bar(LY::kKVFull + u % kStages), (u / kStages) & 1,
-                                            nullptr, 0);
+                        drain(LY::kKVFull + u % kStages, (u / kStages) & 1);
                     for (int x = 0; x < 2; ++x)
-                        if (n_q[x] > 0)
-                            ok &= pa::mbar_wait(bar(LY::kQFull + x), (n_q[x] - 1) & 1, nullptr, 0);
-                    if (!ok && p.err) atomicOr(p.err, pa::ERR_WAIT_DRAIN);
+                        if (n_q[x] > 0) drain(LY::kQFull + x, (n_q[x] - 1) & 1);
                 }
             }
             __syncwarp();
@@ -698,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto at_least = [&](int c) -> unsigned {
                 unsigned sum = 0;
 #pragma unroll
-                for (int j = 0; j < kLaunchSeqs / 32; ++j) sum += (unsigned)max(0, n[j] - c);
+                for (int j = 0; j < kLaunchSeqs / 32; ++j)
+                    if (32 * j < p.num_seqs) sum += (unsigned)max(0, n[j] - c);
                 return __reduce_add_sync(0xffffffffu, sum);
             };
             const unsigned all = at_least(0);
@@ -716,21 +735,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else hi = mid;
                     }
                     unsigned left = chunk - at_least(lo + 1);
-                    int s = 0;
-                    bool found = false;
+                    int s = -1;
 #pragma unroll
-                    for (int j = 0; j < kLaunchSeqs / 32; ++j) {
-                        const unsigned has = __ballot_sync(0xffffffffu, n[j] > lo);
-                        const unsigned cnt = __popc(has);
-                        if (!found) {
+                    for (int j = 0; j < kLaunchSeqs / 32; ++j)
+                        if (s < 0 && 32 * j < p.num_seqs) {
+                            const unsigned has = __ballot_sync(0xffffffffu, n[j] > lo);
+                            const unsigned cnt = __popc(has);
                             if (left < cnt) {
-                                s = 32 * j + __fns(has, 0, left + 1);
-                                found = true;
+                                const bool here = n[j] > lo &&
+                                                  __popc(has & ((1u << lane) - 1)) == left;
+                                s = 32 * j + __ffs(__ballot_sync(0xffffffffu, here)) - 1;
                             } else {
                                 left -= cnt;
                             }
                         }
-                    }
                     t.len = length_of(p, s, t.start);
                     t.off = lo * per_task;
                     t.head = (int)(v % (unsigned)p.num_kv_heads);
@@ -752,6 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     pa::tc::fence_after_sync();
     if (warp == 12) pa::tc::tmem_dealloc(tmem, kTmemCols);
+    if (threadIdx.x == 0 && *abort_flag && p.err) atomicOr(p.err, *abort_flag);
 }
 
 template <typename T, int D>
