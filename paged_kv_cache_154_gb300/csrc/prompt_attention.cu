@@ -44,7 +44,7 @@ namespace {
 constexpr int kRows = 128;               // rows of a Q tile
 constexpr int kKeys = 128;               // keys of a K or V tile
 constexpr int kThreads = 512;
-constexpr int kLaunchSeqs = 256;         // prompts a launch: their chunk counts stay in registers
+constexpr int kLaunchSeqs = 256;         // prompts a launch: finding a task reads their lengths
 constexpr int kMaxLen = 1 << 22;         // a task's products end well before a wait gives up
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyMax = 8.f;
@@ -481,31 +481,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = 32 * (warp & 3) + lane;
         const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
         const int token = row / G, head = row % G;
-        uint32_t n_o[2] = {0, 0};
+        uint32_t parity = 0;                                 // of Q tile x in bit x
         Task task;
-        for (int i = 0; read_task(i, task); ++i) {
-            bool ok = true;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (!ok || (x == 1 && task.len - task.off <= tokens)) continue;
+        bool ok = true;
+        for (int i = 0; ok && read_task(i, task); ++i) {
+            const int nq = task.len - task.off > tokens ? 2 : 1;
+#pragma unroll 1
+            for (int x = 0; x < nq; ++x) {
                 const int at = task.off + x * tokens + token;
                 const bool valid = token < tokens && at < task.len;
                 T* const dst = static_cast<T*>(p.out) + (int64_t)(task.start + at) * p.out_stride +
                                (int64_t)(task.head * G + head) * D;
-                ok = wait(LY::kLFull + x, n_o[x] & 1, pa::ERR_WAIT_FULL) &&
-                     wait(LY::kOFull + x, n_o[x] & 1, pa::ERR_WAIT_FULL);
-                if (!ok) continue;
+                ok = wait(LY::kLFull + x, (parity >> x) & 1, pa::ERR_WAIT_FULL) &&
+                     wait(LY::kOFull + x, (parity >> x) & 1, pa::ERR_WAIT_FULL);
+                if (!ok) break;
+                parity ^= 1u << x;
                 pa::tc::fence_after_sync();
                 const float l = sums[x * kRows + row];
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const uint32_t o_tm = tmem + lane_at + kOCol + D * x;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
-                    pa::tc::ld_32cols_nowait(o_tm + 32 * c, o);
+                    pa::tc::ld_32cols_nowait(o_tm + c, o);
                     pa::tc::wait_ld();
                     pa::tc::loaded(o);
-                    if (c == D / 32 - 1) {                   // all of O and l has been read
+                    if (c == D - 32) {                       // all of O and l has been read
                         pa::tc::fence_before_sync();
                         __syncwarp();
                         if (lane == 0) pa::mbar_arrive(bar(LY::kOFree + x));
@@ -521,13 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            __uint_as_float(o[e + 5]) * inv);
                             w.w = pack2<T>(__uint_as_float(o[e + 6]) * inv,
                                            __uint_as_float(o[e + 7]) * inv);
-                            *reinterpret_cast<uint4*>(dst + 32 * c + e) = w;
+                            *reinterpret_cast<uint4*>(dst + c + e) = w;
                         }
                     }
                 }
-                ++n_o[x];
             }
-            if (!ok) break;
         }
     } else {
         fewer_registers<80>();
@@ -705,19 +704,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             // equals by prompt, then by KV head. With n_s chunks of prompt s, F(c) = sum of
             // max(0, n_s - c) of them have a place of c or more: the chunk of task v is the
             // c with F(c + 1) <= v < F(c), its prompt the (v - F(c + 1))-th with n_s > c.
-            int n[kLaunchSeqs / 32];
             const int per_task = 2 * tokens;
-#pragma unroll
-            for (int j = 0; j < kLaunchSeqs / 32; ++j) {
-                const int s = 32 * j + lane;
+            auto chunks_of = [&](int s) -> int {
                 int start;
-                n[j] = s < p.num_seqs ? (length_of(p, s, start) + per_task - 1) / per_task : 0;
-            }
+                return s < p.num_seqs ? (length_of(p, s, start) + per_task - 1) / per_task : 0;
+            };
+            const int n = chunks_of(lane);                   // further prompts' are read as needed
             auto at_least = [&](int c) -> unsigned {
-                unsigned sum = 0;
-#pragma unroll
-                for (int j = 0; j < kLaunchSeqs / 32; ++j)
-                    if (32 * j < p.num_seqs) sum += (unsigned)max(0, n[j] - c);
+                unsigned sum = (unsigned)max(0, n - c);
+#pragma unroll 1
+                for (int s = 32; s < p.num_seqs; s += 32)
+                    sum += (unsigned)max(0, chunks_of(s + lane) - c);
                 return __reduce_add_sync(0xffffffffu, sum);
             };
             const unsigned all = at_least(0);
@@ -729,26 +726,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t.start = t.len = t.off = 0, t.head = -1;
                 if (chunk < all) {
                     int lo = 0, hi = p.max_chunks;           // F(lo) > chunk >= F(hi)
+                    unsigned above = 0;                      // F(hi)
                     while (hi - lo > 1) {
                         const int mid = (lo + hi) >> 1;
-                        if (at_least(mid) > chunk) lo = mid;
-                        else hi = mid;
+                        const unsigned f = at_least(mid);
+                        if (f > chunk) lo = mid;
+                        else hi = mid, above = f;
                     }
-                    unsigned left = chunk - at_least(lo + 1);
-                    int s = -1;
-#pragma unroll
-                    for (int j = 0; j < kLaunchSeqs / 32; ++j)
-                        if (s < 0 && 32 * j < p.num_seqs) {
-                            const unsigned has = __ballot_sync(0xffffffffu, n[j] > lo);
-                            const unsigned cnt = __popc(has);
-                            if (left < cnt) {
-                                const bool here = n[j] > lo &&
-                                                  __popc(has & ((1u << lane) - 1)) == left;
-                                s = 32 * j + __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-                            } else {
-                                left -= cnt;
-                            }
+                    unsigned left = chunk - above;
+                    int s = 0;
+#pragma unroll 1
+                    for (;; s += 32) {
+                        const bool in = (s == 0 ? n : chunks_of(s + lane)) > lo;
+                        const unsigned has = __ballot_sync(0xffffffffu, in);
+                        const unsigned cnt = __popc(has);
+                        if (left < cnt || s + 32 >= p.num_seqs) {
+                            const bool here = in && __popc(has & ((1u << lane) - 1)) == left;
+                            s += max(0, __ffs(__ballot_sync(0xffffffffu, here)) - 1);
+                            break;
                         }
+                        left -= cnt;
+                    }
                     t.len = length_of(p, s, t.start);
                     t.off = lo * per_task;
                     t.head = (int)(v % (unsigned)p.num_kv_heads);
