@@ -312,7 +312,7 @@ pa_status pa_append_kv(const void* key, const void* value, pa_dtype src_dtype,
  *   inverse        not 0: turned the other way (sin negated), which takes a rotation
  *                  back and is its gradient
  * Strides are multiples of 8 of at least a token's rows; rows and cos_sin are 16-byte
- * aligned. head_dim 64 or 128. */
+ * aligned, freq_axis 8-byte. head_dim 64 or 128. */
 pa_status pa_rope(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
                   int32_t num_heads, void* k_out, int64_t k_out_stride, const void* k,
                   int64_t k_stride, int32_t num_kv_heads, pa_dtype dtype, const float* cos_sin,

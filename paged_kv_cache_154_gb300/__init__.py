@@ -432,34 +432,47 @@ def _heads(name, t, T: int, d: int, dtype) -> Tuple[int, int]:
     s = t.shape
     if len(s) != 3 or s[0] != T or s[2] != d or t.dtype is not dtype:
         raise ValueError(f"{name} is {tuple(s)} {t.dtype}, not ({T}, heads, {d}) {dtype}")
-    if T == 0 or s[1] == 0:
-        return s[1], s[1] * d
     a, b, c = t.stride()
-    if c != 1 or (b != d and s[1] > 1):
-        raise ValueError(f"{name} has strides {(a, b, c)}: a token's heads must be contiguous")
-    return s[1], (a if T > 1 else s[1] * d)
+    heads = s[1]
+    if c != 1 or b != d or T < 2 or heads < 2:
+        if T == 0 or heads == 0:
+            return heads, heads * d
+        if c != 1 or (b != d and heads > 1):
+            raise ValueError(f"{name} has strides {(a, b, c)}: a token's heads must be contiguous")
+        if T == 1:
+            return heads, heads * d
+    return heads, a
 
 
-def _on_current_device(*named) -> None:
-    """Every (name, tensor) is on the current CUDA device, whose stream the call goes to."""
-    torch = sys.modules["torch"]
-    here = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for name, t in named:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"{name} is on {t.device}, not on the current device")
+_current_device = None
+
+
+def _device() -> int:
+    """The current CUDA device, whose stream a call goes to."""
+    global _current_device
+    if _current_device is None:
+        _current_device = sys.modules["torch"].cuda.current_device
+    return _current_device()
+
+
+def _elsewhere(names: str, *tensors) -> None:
+    """Raises for the tensors that are not on the current CUDA device."""
+    here = _device() if max(t.get_device() for t in tensors if t is not None) >= 0 else None
+    bad = [n for n, t in zip(names.split(), tensors) if t is not None and t.get_device() != here]
+    if bad:
+        raise ValueError(f"{', '.join(bad)} not on the current device")
 
 
 def _rotation(cos_sin, positions, freq_axis, T: int) -> Tuple[int, int, int]:
     """(positions of the table, rotary_dim, axes) of a rotation of T tokens."""
     torch = sys.modules["torch"]
-    shape = cos_sin.shape
+    shape, at = cos_sin.shape, positions.shape
     if len(shape) != 2 or cos_sin.dtype is not torch.float32:
         raise ValueError(f"cos_sin is {tuple(shape)} {cos_sin.dtype}, not (positions, rotary_dim) "
                          "torch.float32")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.numel() != axes * T or positions.shape[-1] != T or (
-            positions.dtype is not torch.int32):
-        raise ValueError(f"positions is {tuple(positions.shape)} {positions.dtype}, not "
+    axes = 1 if len(at) == 1 else at[0]
+    if len(at) not in (1, 2) or at[-1] != T or positions.dtype is not torch.int32:
+        raise ValueError(f"positions is {tuple(at)} {positions.dtype}, not "
                          f"({T},) or (axes, {T}) torch.int32")
     if freq_axis is not None and axes > 1:
         _sized(("freq_axis", freq_axis, shape[1] // 2, torch.uint8))
@@ -482,8 +495,13 @@ def rope(q_out, q, k_out, k, cos_sin, positions, interleaved: bool = False, freq
         Go, kos = _heads("k_out", k_out, T, d, q.dtype)
     if H != Ho or G != Go:
         raise ValueError(f"{H} and {G} heads of q and k, {Ho} and {Go} of q_out and k_out")
-    _on_current_device(("q", q), ("q_out", q_out), ("k", k), ("k_out", k_out),
-                       ("cos_sin", cos_sin), ("positions", positions), ("freq_axis", freq_axis))
+    dev = q.get_device()
+    if (dev < 0 or dev != _device() or q_out.get_device() != dev or cos_sin.get_device() != dev
+            or positions.get_device() != dev or (k is not None and (k.get_device() != dev or
+                                                                    k_out.get_device() != dev))
+            or (freq_axis is not None and freq_axis.get_device() != dev)):
+        _elsewhere("q q_out k k_out cos_sin positions freq_axis", q, q_out, k, k_out, cos_sin,
+                   positions, freq_axis)
     _check(lib().pa_rope(q_out.data_ptr(), qos, q.data_ptr(), qs, H,
                          k_out.data_ptr() if G else None, kos, k.data_ptr() if G else None, ks, G,
                          _dtype_code(q), _ptr(cos_sin), most, rd, int(interleaved),
@@ -517,11 +535,18 @@ def rope_append_kv(q_out, q, key, value, k_cache, v_cache, slot_mapping, cos_sin
         raise ValueError(f"key is {tuple(key.shape)}, the cache {tuple(shape)}")
     _cache_sized(code, nb, shape, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp)
     _sized(("slot_mapping", slot_mapping, T, sys.modules["torch"].int64))
-    _on_current_device(("q", q), ("q_out", q_out), ("key", key), ("value", value),
-                       ("k_cache", k_cache), ("v_cache", v_cache), ("slot_mapping", slot_mapping),
-                       ("cos_sin", cos_sin), ("positions", positions), ("k_scale", k_scale),
-                       ("v_scale", v_scale), ("k_zp", k_zp), ("v_zp", v_zp), ("key_out", key_out),
-                       ("freq_axis", freq_axis))
+    dev = key.get_device()
+    away = (dev < 0 or dev != _device() or value.get_device() != dev or k_cache.get_device() != dev
+            or v_cache.get_device() != dev or slot_mapping.get_device() != dev
+            or cos_sin.get_device() != dev or positions.get_device() != dev)
+    for t in (q, q_out, k_scale, v_scale, k_zp, v_zp, key_out, freq_axis):
+        if t is not None and t.get_device() != dev:
+            away = True
+    if away:
+        _elsewhere("q q_out key value k_cache v_cache slot_mapping cos_sin positions k_scale "
+                   "v_scale k_zp v_zp key_out freq_axis", q, q_out, key, value, k_cache, v_cache,
+                   slot_mapping, cos_sin, positions, k_scale, v_scale, k_zp, v_zp, key_out,
+                   freq_axis)
     _check(lib().pa_rope_append_kv(
         q_out.data_ptr() if H else None, qos, q.data_ptr() if H else None, qs, H,
         None if key_out is None else key_out.data_ptr(), kos, key.data_ptr(), ks,
@@ -545,8 +570,10 @@ def prompt_attention(out, q, key, value, seq_start, max_seq_len: int, scale: flo
     if seq_start.dim() != 1 or seq_start.dtype is not sys.modules["torch"].int32:
         raise ValueError(f"seq_start is {tuple(seq_start.shape)} {seq_start.dtype}, not "
                          "(num_seqs + 1,) torch.int32")
-    _on_current_device(("q", q), ("out", out), ("key", key), ("value", value),
-                       ("seq_start", seq_start))
+    dev = q.get_device()
+    if (dev < 0 or dev != _device() or out.get_device() != dev or key.get_device() != dev
+            or value.get_device() != dev or seq_start.get_device() != dev):
+        _elsewhere("q out key value seq_start", q, out, key, value, seq_start)
     _check(lib().pa_prompt_attention(
         out.data_ptr(), os_, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs,
         _dtype_code(q), _ptr(seq_start), seq_start.shape[0] - 1, T, int(max_seq_len), H, G, d,

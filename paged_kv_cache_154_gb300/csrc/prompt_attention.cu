@@ -54,23 +54,28 @@ struct Layout {
     static constexpr int kHalves = D / 64;                     // 128-byte wide parts of a row
     static constexpr int kTile = kKeys * D * 2;                // bytes of a K, V or Q tile
     static constexpr int kHalf = kKeys * 128;                  // bytes of one part
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr int kKVOff = 2 * kTile;
     static constexpr int kSumOff = kKVOff + kStages * kTile;   // l of both Q tiles' rows
     static constexpr int kBarOff = kSumOff + 2 * kRows * 4;
     // barriers
-    static constexpr int kKVFull = 0, kKVEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + 2,
-                         kSFull = kQEmpty + 2, kPFull = kSFull + 2 /* [tile][half] */,
-                         kOFull = kPFull + 4, kOFree = kOFull + 2, kLFull = kOFree + 2,
-                         kClean = kLFull + 2, kTaskFull = kClean + kStages, kTaskEmpty = kTaskFull + 2,
-                         kFin = kTaskEmpty + 2, kTurn = kFin + 2, kNumBars = kTurn + 2;
+    static constexpr int kKVFull = 0, kKVEmpty = kStages, kClean = 2 * kStages,
+                         kQFull = 3 * kStages, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2,
+                         kPFull = kSFull + 2 /* [tile][half] */, kSFree = kPFull + 4,
+                         kOFree = kSFree + 2, kLFull = kOFree + 2, kOFull = kLFull + 2,
+                         kODone = kOFull + 2, kTurn = kODone + 2, kTaskFull = kTurn + 2,
+                         kTaskEmpty = kTaskFull + 2, kFin = kTaskEmpty + 2, kNumBars = kFin + 2;
     static constexpr int kTaskOff = (kBarOff + 8 * kNumBars + 15) / 16 * 16;   // two task records
-    static constexpr int kFlagOff = kTaskOff + 2 * 32;            // TMEM address, abort flag
+    static constexpr int kFlagOff = kTaskOff + 2 * 16;            // TMEM address, abort flag
     static constexpr int kSmem = kFlagOff + 16 + 1024;            // + alignment slack
-    static_assert(kTaskOff % 16 == 0 && kSmem <= 227 * 1024, "shared memory per CTA");
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+    // TMEM columns: S of Q tile x at 128 x, O at 256 + D x. P goes over the last 64 columns of S
+    // where O leaves no others; else it has its own, and the next S is there before this P is.
+    static constexpr bool kApart = D == 64;
+    static constexpr uint32_t kOCol = 256;
+    __device__ static constexpr uint32_t p_col(int x) { return kApart ? 384 + 64 * x : 128 * x + 64; }
 };
-// TMEM columns: S of Q tile x at 128 x (P over its last 64), O at 256 + D x
-constexpr uint32_t kTmemCols = 512, kOCol = 256;
+constexpr uint32_t kTmemCols = 512;
 
 struct PromptParams {
     void* out;
@@ -159,6 +164,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// an arrival without a branch
+__device__ __forceinline__ void arrive_if(uint32_t bar, bool p) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"((uint32_t)p)
+        : "memory");
+}
 template <int kRegs>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -249,11 +262,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     pa::grid_dependents_launch();
     if (threadIdx.x == 0) {
         for (int i = 0; i < LY::kNumBars; ++i) {
-            // arrivals: P, l, zeroed V rows and a free O from the four warps of a group; a free
-            // K or V tile from both issuing warps; a task record from every warp that reads it
-            const int n = (i >= LY::kPFull && i < LY::kOFull) || (i >= LY::kOFree && i < LY::kTaskFull)
+            // arrivals: P, S read, l, zeroed V rows and a free O from the four warps of a group; a
+            // free K or V tile from both issuing warps; a task record from every warp that reads it
+            const int n = (i >= LY::kPFull && i < LY::kOFull) || (i >= LY::kClean && i < LY::kQFull)
                               ? 4
-                          : i >= LY::kKVEmpty && i < LY::kQFull ? 2
+                          : i >= LY::kKVEmpty && i < LY::kClean ? 2
                           : i >= LY::kTaskEmpty && i < LY::kFin ? 15
                                                                : 1;
             pa::mbar_init(bar(i), n);
@@ -317,7 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = warp >> 2;
         const int row = 32 * (warp & 3) + lane;
         const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t s_tm = tmem + lane_at + 128 * x, o_tm = tmem + lane_at + kOCol + D * x;
+        const uint32_t s_tm = tmem + lane_at + 128 * x, p_tm = tmem + lane_at + LY::p_col(x);
+        const uint32_t o_tm = tmem + lane_at + LY::kOCol + D * x;
         const int token = row / G;                           // of the tile
         const uint64_t sl2 = pair(p.scale_log2, p.scale_log2);
         Ring<kStages> kv;                                    // the task's first K tile
@@ -334,134 +348,151 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int bound = span.first + token;
             float m_run = -INFINITY, l_run = 0.f;
             bool ok = true;
+            uint64_t l4[2], nm;
+            // 32 keys' weights, from their scores to P
+            auto weights = [&](uint32_t (&c)[32], uint32_t p_at) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+#pragma unroll
+                    for (int q = 0; q < 4; q += 2) {
+                        float a, b;
+                        fma2(a, b, c[j + q], c[j + q + 1], sl2, nm);
+                        a = pa::ex2(a);
+                        b = pa::ex2(b);
+                        pk[(j + q) / 2] = pack2<T>(a, b);
+                        add2(l4[q / 2], a, b);
+                    }
+                }
+                pa::tc::st_16cols_nowait(p_at, pk);
+            };
+            auto max32 = [&](uint32_t (&c)[32], float (&m)[4]) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        m[q] = max3(m[q], __uint_as_float(c[j + 2 * q]),
+                                    __uint_as_float(c[j + 2 * q + 1]));
+            };
+            auto scaled_max = [&](float (&m)[4]) {
+                const float mx = fmaxf(max3(m[0], m[1], m[2]), m[3]);
+                return mx == -INFINITY ? mx : mx * p.scale_log2;   // the scale is positive
+            };
+            auto mask = [&](uint32_t (&c)[32], int key0) {   // keys that a row must not see
+                if (key0 + 31 > span.first) {
+                    const int last = bound - key0;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j > last) c[j] = 0xff800000u;    // -inf
+                }
+            };
+            auto reference = [&]() {
+                const float m = m_run == -INFINITY ? 0.f : -m_run;
+                nm = pair(m, m);
+            };
+            auto scale_o = [&](float alpha) {
+#pragma unroll 1
+                for (int q = 0; q < D / 8; ++q) {
+                    uint32_t ov[8];
+                    pa::tc::ld_8cols(o_tm + 8 * q, ov);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                    pa::tc::st_8cols(o_tm + 8 * q, ov);
+                }
+            };
+            auto publish = [&](int half) {
+                pa::tc::wait_st();
+                pa::tc::fence_before_sync();
+                __syncwarp();
+                arrive_if(bar(LY::kPFull + 2 * x + half), lane == 0);
+            };
+            // V rows behind the prompt that the last tile's product reaches may hold anything:
+            // zeroed, so that a weight of 0 never meets a NaN. The first Q tile to reach them
+            // does it.
+            auto zero_behind = [&]() -> bool {
+                if (((span.keys + 15) & ~15) <= task.len || (x == 1 && first_cleans(task))) return true;
+                Ring<kStages> v = kv;
+                v.advance(2 * span.tiles - 1);
+                if (!wait(LY::kKVFull + v.slot, v.phase, pa::ERR_WAIT_FULL)) return false;
+                const int z0 = task.len - (span.tiles - 1) * kKeys;
+                const int n = (((span.keys + 15) & ~15) - task.len) * (D / 8);
+                for (int e = row; e < n; e += kRows) {
+                    const int r = z0 + e / (D / 8), ch = e % (D / 8);
+                    const uint32_t dst = base + LY::kKVOff + v.slot * LY::kTile +
+                                         (ch >> 3) * LY::kHalf + r * 128 + ((ch & 7) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0u)
+                                 : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (x == 0 && first_cleans(task)) {
+                    __syncwarp();
+                    if (lane == 0) pa::mbar_arrive(bar(LY::kClean + v.slot));
+                }
+                return true;
+            };
+
             for (int t = 0; t < span.tiles; ++t, ++n_s) {
                 ok = wait(LY::kSFull + x, n_s & 1, pa::ERR_WAIT_FULL);
                 if (!ok) break;
                 pa::tc::fence_after_sync();
                 const int key0 = t * kKeys;
-                const int in_tile = span.keys - key0;        // visible keys of this tile
-                // Weights of the first 64 keys against the maximum so far, while the maximum of
-                // all 128 is found beside them; in the rare case that it has moved, once more. P
-                // goes over the columns of the last 64 keys' S, which are in registers by then.
+                const int in_tile = span.keys - key0;    // visible keys of this tile
                 float alpha = 1.f;
-                uint64_t l4[2], nm;
                 uint32_t c[4][32];
-                auto weights = [&](int i) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-#pragma unroll
-                        for (int q = 0; q < 4; q += 2) {
-                            float a, b;
-                            fma2(a, b, c[i][j + q], c[i][j + q + 1], sl2, nm);
-                            a = pa::ex2(a);
-                            b = pa::ex2(b);
-                            pk[(j + q) / 2] = pack2<T>(a, b);
-                            add2(l4[q / 2], a, b);
-                        }
-                    }
-                    pa::tc::st_16cols_nowait(s_tm + 64 + 16 * i, pk);
-                };
-                auto max32 = [&](int i, float (&m)[4]) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            m[q] = max3(m[q], __uint_as_float(c[i][j + 2 * q]),
-                                        __uint_as_float(c[i][j + 2 * q + 1]));
-                };
-                auto scaled_max = [&](float (&m)[4]) {
-                    const float mx = fmaxf(max3(m[0], m[1], m[2]), m[3]);
-                    return mx == -INFINITY ? mx : mx * p.scale_log2;   // the scale is positive
-                };
-                auto publish = [&](int half) {
-                    pa::tc::wait_st();
-                    pa::tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) pa::mbar_arrive(bar(LY::kPFull + 2 * x + half));
-                };
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pa::tc::ld_32cols_nowait(s_tm + 32 * i, c[i]);
                 pa::tc::wait_ld();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pa::tc::loaded(c[i]);
-                if (key0 + kKeys - 1 > span.first) {         // some row must not see all
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int last = bound - key0 - 32 * i;   // visible keys of these, less 1
-                        if (key0 + 32 * i + 31 > span.first) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j > last) c[i][j] = 0xff800000u;   // -inf
-                        }
-                    }
+                if (LY::kApart) {
+                    // the next S may come; P of the last tile has been read
+                    pa::tc::fence_before_sync();
+                    __syncwarp();
+                    arrive_if(bar(LY::kSFree + x), lane == 0);
+                    if (n_s > 0) ok = wait(LY::kODone + x, (n_s - 1) & 1, pa::ERR_WAIT_FULL);
+                    if (!ok) break;
+                    pa::tc::fence_after_sync();
                 }
-                if (t == 0) {                                // a first guess, not above the maximum
+                if (key0 + kKeys - 1 > span.first) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mask(c[i], key0 + 32 * i);
+                }
+                if (t == 0) {                            // a first guess, not above the maximum
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    max32(0, m4);
+                    max32(c[0], m4);
                     m_run = scaled_max(m4);
                 }
+                // Weights of the first 64 keys against the maximum so far, while the maximum of
+                // all 128 is found beside them; in the rare case that it has moved, once more. P
+                // goes over the columns of the last 64 keys' S, which are in registers by then.
                 for (bool again = true; again;) {
-                    const float m = m_run == -INFINITY ? 0.f : -m_run;
-                    nm = pair(m, m);
+                    reference();
                     l4[0] = l4[1] = 0;
-                    weights(0);
-                    weights(1);
+                    weights(c[0], p_tm);
+                    weights(c[1], p_tm + 16);
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) max32(i, m4);
+                    for (int i = 0; i < 4; ++i) max32(c[i], m4);
                     const float mx = scaled_max(m4);
                     const bool moved = mx > m_run + kLazyMax;
                     again = __any_sync(0xffffffffu, moved);
                     if (again) {
                         if (moved) {
-                            alpha = pa::ex2(m_run - mx);         // 0 while m_run is -inf
+                            alpha = pa::ex2(m_run - mx);     // 0 while m_run is -inf
                             m_run = mx;
                         }
-                        // O may be scaled now: S of this tile was issued behind the last P V, and
-                        // the barrier says that both are done; the next P V waits for this P
-                        if (t > 0) {
-#pragma unroll 1
-                            for (int q = 0; q < D / 8; ++q) {
-                                uint32_t ov[8];
-                                pa::tc::ld_8cols(o_tm + 8 * q, ov);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                                pa::tc::st_8cols(o_tm + 8 * q, ov);
-                            }
-                        }
+                        // O may be scaled now: S of this tile was issued behind the last P V,
+                        // and the barrier says that both are done; the next P V waits for this P
+                        if (t > 0) scale_o(alpha);
                     }
                 }
-                // V rows behind the prompt that a product reaches may hold anything: zeroed, so
-                // that a weight of 0 never meets a NaN. The first Q tile to reach them does it.
-                if (t == span.tiles - 1) {
-                    const bool reaches = ((span.keys + 15) & ~15) > task.len;
-                    if (reaches && !(x == 1 && first_cleans(task))) {
-                        Ring<kStages> v = kv;
-                        v.advance(2 * t + 1);
-                        ok = wait(LY::kKVFull + v.slot, v.phase, pa::ERR_WAIT_FULL);
-                        if (!ok) break;
-                        const int z0 = task.len - key0;
-                        const int n = (((span.keys + 15) & ~15) - task.len) * (D / 8);
-                        for (int e = row; e < n; e += kRows) {
-                            const int r = z0 + e / (D / 8), ch = e % (D / 8);
-                            const uint32_t dst = base + LY::kKVOff + v.slot * LY::kTile +
-                                                 (ch >> 3) * LY::kHalf + r * 128 + ((ch & 7) << 4);
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0u)
-                                         : "memory");
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        if (x == 0 && first_cleans(task)) {
-                            __syncwarp();
-                            if (lane == 0) pa::mbar_arrive(bar(LY::kClean + v.slot));
-                        }
-                    }
-                }
+                if (t == span.tiles - 1) ok = zero_behind();
+                if (!ok) break;
                 publish(0);
-                if (in_tile > 64) {                          // else no product reads it
-                    weights(2);
-                    weights(3);
+                if (in_tile > 64) {                      // else no product reads it
+                    weights(c[2], p_tm + 32);
+                    weights(c[3], p_tm + 48);
                 }
                 publish(1);
                 l_run = l_run * alpha + (sum_of(l4[0]) + sum_of(l4[1]));
@@ -499,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pa::tc::fence_after_sync();
                 const float l = sums[x * kRows + row];
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                const uint32_t o_tm = tmem + lane_at + kOCol + D * x;
+                const uint32_t o_tm = tmem + lane_at + LY::kOCol + D * x;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -545,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t dq = pa::tc::smem_desc_sw128(base + x * LY::kTile, 16, 1024);
                 const uint64_t dk = pa::tc::smem_desc_sw128(base + LY::kKVOff, 16, 1024);
                 const uint64_t dv = pa::tc::smem_desc_sw128(base + LY::kKVOff, LY::kHalf, 1024);
-                const uint32_t s_tm = tmem + 128 * x, o_tm = tmem + kOCol + D * x;
+                const uint32_t s_tm = tmem + 128 * x, o_tm = tmem + LY::kOCol + D * x;
                 Ring<kStages> kv;
                 uint32_t n_s = 0, n_q = 0;
                 uint32_t cleaned = 0;                        // parities of the ring's kClean
@@ -555,10 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // not wait for the other warp to wake up.
                 uint32_t turns = 0;
                 auto my_turn = [&](bool two) -> bool {
-                    return !two || wait_one(LY::kTurn + x, (turns++ & 1) ^ (x ^ 1), pa::ERR_WAIT_FULL);
+                    return LY::kApart || !two || wait_one(LY::kTurn + x, (turns++ & 1) ^ (x ^ 1), pa::ERR_WAIT_FULL);
                 };
                 auto pass_turn = [&](bool two) {
-                    if (two) pa::mbar_arrive(bar(LY::kTurn + (x ^ 1)));
+                    if (!LY::kApart && two) pa::mbar_arrive(bar(LY::kTurn + (x ^ 1)));
                 };
                 auto issue_qk = [&](bool two) {              // S = Q K^T
                     pa::tc::fence_after_sync();
@@ -573,14 +604,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pa::tc::commit(bar(LY::kKVEmpty + kv.slot));
                     kv = kv.next();
                 };
-                auto issue_pv = [&](int half, int steps, bool more) {   // O += P V
+                auto issue_pv = [&](const Ring<kStages>& v, int half, int steps, bool more) {   // O += P V
                     pa::tc::fence_after_sync();
-                    const uint64_t b = dv + (uint64_t)((kv.slot * LY::kTile) >> 4);
+                    const uint64_t b = dv + (uint64_t)((v.slot * LY::kTile) >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int kb = 4 * half + k;
                         if (kb < steps)
-                            pa::tc::mma_f16_ts(o_tm, s_tm + 64 + 8 * kb,
+                            pa::tc::mma_f16_ts(o_tm, tmem + LY::p_col(x) + 8 * kb,
                                                b + (uint64_t)((kb * 16 * 128) >> 4), idesc_pv,
                                                more || kb > 0 ? 1u : 0u);
                     }
@@ -609,37 +640,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     issue_qk(two);
                     for (int t = 0; t < s.tiles; ++t, ++n_s) {
-                        const Ring<kStages> next = kv.next();
+                        const Ring<kStages> v = kv, next = kv.next();
                         const bool more = t + 1 < s.tiles, turn = t < both;
+                        if (LY::kApart && more) {
+                            // the next S, once this one has been read
+                            ok = wait_one(LY::kKVFull + next.slot, next.phase, pa::ERR_WAIT_FULL) &&
+                                 wait_one(LY::kSFree + x, n_s & 1, pa::ERR_WAIT_FULL);
+                            if (!ok) break;
+                            kv = next;
+                            issue_qk(false);
+                        }
+                        if (!more) pa::tc::commit(bar(LY::kQEmpty + x));
                         // this V tile, the next K tile, and O of the last task read
-                        ok = wait_one(LY::kKVFull + kv.slot, kv.phase, pa::ERR_WAIT_FULL);
-                        if (more)
+                        ok = wait_one(LY::kKVFull + v.slot, v.phase, pa::ERR_WAIT_FULL);
+                        if (!LY::kApart && more)
                             ok = ok && wait_one(LY::kKVFull + next.slot, next.phase, pa::ERR_WAIT_FULL);
                         if (t == 0 && n_q > 0)
                             ok = ok && wait_one(LY::kOFree + x, (n_q - 1) & 1, pa::ERR_WAIT_EMPTY);
-                        if (!more) {
-                            pa::tc::commit(bar(LY::kQEmpty + x));
-                            if (x == 1 && first_cleans(task)) {
-                                ok = ok && wait_one(LY::kClean + kv.slot, (cleaned >> kv.slot) & 1,
-                                                    pa::ERR_WAIT_FULL);
-                                cleaned ^= 1u << kv.slot;
-                            }
+                        if (!more && x == 1 && first_cleans(task)) {
+                            ok = ok && wait_one(LY::kClean + v.slot, (cleaned >> v.slot) & 1,
+                                                pa::ERR_WAIT_FULL);
+                            cleaned ^= 1u << v.slot;
                         }
                         const int steps = (s.keys - t * kKeys + 15) >> 4;
                         ok = ok && my_turn(turn) &&
                              wait_one(LY::kPFull + 2 * x, n_s & 1, pa::ERR_WAIT_FULL);
                         if (!ok) break;
-                        issue_pv(0, steps, t > 0);
+                        issue_pv(v, 0, steps, t > 0);
                         ok = wait_one(LY::kPFull + 2 * x + 1, n_s & 1, pa::ERR_WAIT_FULL);
                         if (!ok) break;
-                        issue_pv(1, steps, true);
+                        issue_pv(v, 1, steps, true);
+                        if (LY::kApart) pa::tc::commit(bar(LY::kODone + x));
                         if (!more) {
                             pass_turn(turn);
                             pa::tc::commit(bar(LY::kOFull + x));
                         }
-                        pa::tc::commit(bar(LY::kKVEmpty + kv.slot));
-                        kv = next;
-                        if (more) issue_qk(turn);
+                        pa::tc::commit(bar(LY::kKVEmpty + v.slot));
+                        if (!LY::kApart || !more) kv = next;
+                        if (!LY::kApart && more) issue_qk(turn);
                     }
                     ok = ok && pass_on(2 * (tiles - s.tiles));
                     ++n_q;

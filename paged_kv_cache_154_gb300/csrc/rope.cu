@@ -22,7 +22,7 @@
 namespace {
 
 constexpr int kBlock = 16;
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 constexpr int kMaxAxes = 4;
 
 // what happens to the rotated keys and the values
@@ -102,7 +102,10 @@ __device__ __forceinline__ void rotate(float (&x)[8], float (&y)[8], const float
 // 16 elements a thread of a row (chunks of 8: a and b), head_dim / 16 threads a row; a
 // warp takes kUnroll times 32 / (head_dim / 16) rows of one token, so that a thread's
 // cosines and sines, read once, turn kUnroll rows and all its rows are on their way at
-// once. Which 8 frequencies a thread has does not depend on how pairs lie: chunks f / 8
+// once (8191 tokens of 32 heads of 128 cold: 29.8 us, 34.9 with one row a thread). CTAs of
+// two warps, for those that quantise are slower than those that rotate (6001 tokens of 64 + 8
+// + 8 heads into a 4-bit cache and read back: 58.5 us, 79 us with 8 warps, 60.5 with 4). Which 8
+// frequencies a thread has does not depend on how pairs lie: chunks f / 8
 // and (f + rotary_dim / 2) / 8 hold them, or chunks f / 4 and f / 4 + 1.
 template <int kSink, int D, typename T, bool kInterleaved, int kUnroll>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
@@ -142,19 +145,20 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     // cosines and sines of frequencies 8 c .. 8 c + 7
     float cs[8], sn[8];
     bool bad = false;
+    auto load8 = [&](int pos) {
+        const float4* row =
+            reinterpret_cast<const float4*>(p.cos_sin + (int64_t)pos * p.rotary_dim) + 2 * c;
+        const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(row + half / 4),
+                     s1 = __ldg(row + half / 4 + 1);
+        cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
+        cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
+        sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
+        sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
+    };
     if (p.num_axes == 1) {
         const int pos = __ldg(p.positions + t);
         bad = (uint32_t)pos >= (uint32_t)p.max_positions;
-        if (turned && !bad) {
-            const float4* row =
-                reinterpret_cast<const float4*>(p.cos_sin + (int64_t)pos * p.rotary_dim) + 2 * c;
-            const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(row + half / 4),
-                         s1 = __ldg(row + half / 4 + 1);
-            cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
-            cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-            sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
-            sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
-        }
+        if (turned && !bad) load8(pos);
     } else {
         int pos[kMaxAxes];
 #pragma unroll
@@ -163,15 +167,22 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             bad |= (uint32_t)pos[i] >= (uint32_t)p.max_positions;
         }
         if (turned) {
+            const uint2 axes = __ldg(reinterpret_cast<const uint2*>(p.freq_axis) + c);
+            const uint32_t x0 = axes.x & 255u;
+            if (axes.x == axes.y && axes.x == x0 * 0x01010101u) {   // 8 frequencies of one axis
+                bad |= x0 >= (uint32_t)p.num_axes;
+                if (!bad) load8(x0 == 0 ? pos[0] : x0 == 1 ? pos[1] : x0 == 2 ? pos[2] : pos[3]);
+            } else {
 #pragma unroll
-            for (int f = 0; f < 8; ++f) {
-                const int x = __ldg(p.freq_axis + 8 * c + f);
-                bad |= x >= p.num_axes;
-                const int at = x == 0 ? pos[0] : x == 1 ? pos[1] : x == 2 ? pos[2] : pos[3];
-                if (!bad) {
-                    const float* row = p.cos_sin + (int64_t)at * p.rotary_dim + 8 * c + f;
-                    cs[f] = __ldg(row);
-                    sn[f] = __ldg(row + half);
+                for (int f = 0; f < 8; ++f) {
+                    const uint32_t x = (f < 4 ? axes.x : axes.y) >> (8 * (f & 3)) & 255u;
+                    bad |= x >= (uint32_t)p.num_axes;
+                    const int at = x == 0 ? pos[0] : x == 1 ? pos[1] : x == 2 ? pos[2] : pos[3];
+                    if (!bad) {
+                        const float* row = p.cos_sin + (int64_t)at * p.rotary_dim + 8 * c + f;
+                        cs[f] = __ldg(row);
+                        sn[f] = __ldg(row + half);
+                    }
                 }
             }
         }
@@ -272,24 +283,37 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                     }
                 }
                 if (put) {
-                    float* const scales = is_k ? p.k_scale : p.v_scale;
-                    int8_t* const zps = is_k ? p.k_zp : p.v_zp;
-#pragma unroll
-                    for (int j = 0; j < kGroups; ++j) {
-                        const pa::Quantiser<kSink == kInt4 ? 15 : 255, kSink == kInt4 ? 0 : -128>
-                            quant(mn[j], mx[j]);
+                    using Quant = pa::Quantiser<kSink == kInt4 ? 15 : 255, kSink == kInt4 ? 0 : -128>;
+                    float* const scales = (is_k ? p.k_scale : p.v_scale) + row * kGroups;
+                    int8_t* const zps = (is_k ? p.k_zp : p.v_zp) + row * kGroups;
+                    const Quant qa(ga ? mn[kGroups - 1] : mn[0], ga ? mx[kGroups - 1] : mx[0]);
+                    if constexpr (kGroups == 1) {
                         if constexpr (kSink == kInt4) {
                             uint32_t* dst = static_cast<uint32_t*>(cache) + row * (D / 8);
-                            if (ga == j) dst[a] = quant.pack4(x);
-                            if (gb == j) dst[b] = quant.pack4(y);
+                            dst[a] = qa.pack4(x);
+                            dst[b] = qa.pack4(y);
                         } else {
                             uint2* dst = static_cast<uint2*>(cache) + row * (D / 8);
-                            dst[a] = quant.pack8(x);
-                            dst[b] = quant.pack8(y);
+                            dst[a] = qa.pack8(x);
+                            dst[b] = qa.pack8(y);
                         }
-                        if (c == j) {
-                            scales[row * kGroups + j] = quant.scale;
-                            zps[row * kGroups + j] = (int8_t)quant.zp;
+                        if (c == 0) {
+                            scales[0] = qa.scale;
+                            zps[0] = (int8_t)qa.zp;
+                        }
+                    } else {
+                        const Quant qb(gb ? mn[1] : mn[0], gb ? mx[1] : mx[0]);
+                        uint32_t* dst = static_cast<uint32_t*>(cache) + row * (D / 8);
+                        dst[a] = qa.pack4(x);
+                        dst[b] = qb.pack4(y);
+                        // chunk 0 is the first thread's; chunk 8 starts the second group
+                        if (a == 0 || a == 8) {
+                            scales[ga] = qa.scale;
+                            zps[ga] = (int8_t)qa.zp;
+                        }
+                        if (b == 8) {
+                            scales[1] = qb.scale;
+                            zps[1] = (int8_t)qb.zp;
                         }
                     }
                 }
@@ -360,6 +384,8 @@ pa_status check_rope(const void* q_out, int64_t q_out_stride, const void* q, int
         return fail(PA_ERR_UNSUPPORTED, "num_axes %d (1 to %d)", num_axes, kMaxAxes);
     if (num_axes > 1 && !freq_axis)
         return fail(PA_ERR_INVALID_ARG, "%d axes need freq_axis", num_axes);
+    if (num_axes > 1 && (uintptr_t)freq_axis % 8)
+        return fail(PA_ERR_INVALID_ARG, "freq_axis must be 8-byte aligned");
     if ((uintptr_t)cos_sin % 16) return fail(PA_ERR_INVALID_ARG, "cos_sin must be 16-byte aligned");
     if (num_heads > 0) {
         if (!q || !q_out) return fail(PA_ERR_INVALID_ARG, "NULL pointer");

@@ -28,7 +28,7 @@ BOTH = [
     (dict(qs=1023), 1), (dict(qs=1016), 1), (dict(qos=1016), 1), (dict(ks=248), 1),
     (dict(ks=260), 1), (dict(qs=-1024), 1), (dict(d=96), 2), (dict(d=256), 2), (dict(rd=0), 2),
     (dict(rd=24), 2), (dict(rd=144), 2), (dict(d=64, rd=80), 2), (dict(most=0), 1),
-    (dict(axes=0), 2), (dict(axes=5), 2), (dict(axes=2), 1), (dict(dt=pa.PA_F32), 2),
+    (dict(axes=0), 2), (dict(axes=5), 2), (dict(axes=2), 1), (dict(axes=2, axis=ODD), 1), (dict(dt=pa.PA_F32), 2),
     (dict(H=-1), 1), (dict(qos=2048), 1),
 ]
 
