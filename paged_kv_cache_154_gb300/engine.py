@@ -22,10 +22,33 @@ import torch
 from . import (BLOCK_SIZE, INT4_GROUP, Pool, accumulate_weights,
                accumulate_weights_workspace_size, append_kv, copy_blocks, decode,
                decode_shared_prefix, decode_shared_prefix_workspace_size, decode_workspace_size,
-               evict_select, move_tokens, zeroed_workspace)
+               evict_select, move_tokens, prompt_attention, rope_append_kv, zeroed_workspace)
 
 KV_TORCH = {"f16": torch.float16, "bf16": torch.bfloat16, "int8": torch.int8,
             "fp8": torch.float8_e4m3fn, "int4": torch.uint8}
+
+
+def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, inv_freq=None,
+               factor: float = 1.0, device="cuda") -> torch.Tensor:
+    """cos_sin for rope() and rope_append_kv(), fp32 [positions, rotary_dim]: angles of
+    position * inv_freq in 64 bits (far positions lose nothing), their cosines and sines
+    times `factor` (of scaled rotations) rounded once. inv_freq: rotary_dim / 2 frequencies,
+    base ** (-2 f / rotary_dim) without it."""
+    if inv_freq is None:
+        inv_freq = base ** (-np.arange(0, rotary_dim, 2, dtype=np.float64) / rotary_dim)
+    f = torch.as_tensor(np.asarray(inv_freq, np.float64), device=device)
+    if f.shape != (rotary_dim // 2,) or rotary_dim % 2:
+        raise ValueError(f"inv_freq is {tuple(f.shape)}, rotary_dim {rotary_dim}")
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * f
+    return (torch.cat((angle.cos(), angle.sin()), 1) * factor).float()
+
+
+@dataclass
+class Rotary:
+    """How a step's queries and keys are rotated on their way into the cache."""
+    cos_sin: torch.Tensor             # fp32 [positions, rotary_dim], as rope_table() makes it
+    interleaved: bool = False
+    freq_axis: Optional[torch.Tensor] = None   # uint8 [rotary_dim / 2], with several position axes
 
 
 @dataclass
@@ -47,6 +70,17 @@ class StepInputs:
     weights_workspace: Optional[torch.Tensor] = None   # accumulate_step's, from its first call on
     q_lens: Optional[Sequence[int]] = None   # query run of every sequence
     seqs: Optional[Sequence] = None          # their names
+    rotary: Optional[Rotary] = None          # then write_step rotates q and key into these:
+    positions: Optional[torch.Tensor] = None       # int32 [axes, T]
+    q_rotated: Optional[torch.Tensor] = None
+    key_rotated: Optional[torch.Tensor] = None
+    prompt_start: Optional[torch.Tensor] = None    # int32 [S + 1]: whole prompts, attended as rows
+
+
+def _queries(si) -> torch.Tensor:
+    """The queries of a step that attention takes: rotated, where its write rotates them."""
+    rotated = getattr(si, "q_rotated", None)
+    return si.q if rotated is None else rotated
 
 
 @dataclass
@@ -154,13 +188,34 @@ class PagedKVCache:
         return slots, pairs
 
     # -- decode step -------------------------------------------------------------
-    def prepare_step(self, step_ops, names: Dict, q: torch.Tensor, out_dtype=torch.float32,
+    def prepare_step(self, step_ops, names: Dict, q: torch.Tensor, out_dtype=None,
                      partition_size: int = 0, reserve: bool = True,
-                     shared_prefix: bool = False) -> StepInputs:
+                     shared_prefix: bool = False, rotary: Optional[Rotary] = None,
+                     positions=None, prompt: bool = False) -> StepInputs:
         """Reserve the step's slots (host) and build its device inputs. With
         shared_prefix, also the fork groups (adjacent sequences of the step
         holding the same prompt blocks), so that attend_step reads each
-        group's shared blocks once."""
+        group's shared blocks once.
+
+        rotary: q and the keys of the operations are rotated by write_step on their way
+        into the cache. positions: int [T] or [axes, T] of the step's tokens; without it a
+        token's place in its sequence, evicted tokens counted.
+
+        prompt: the operations are whole prompts, each all the tokens of its sequence;
+        attend_step then attends them from the rows themselves (the cache's type does not
+        matter to it), and the output has the type of q. Other steps' is fp32 unless
+        out_dtype says otherwise."""
+        if prompt:
+            if len({op.seq for op in step_ops}) < len(step_ops):
+                raise ValueError("a sequence appears twice among the prompts")
+            for op in step_ops:
+                held = self.pool.seq_len(names[op.seq]) - (0 if reserve else int(op.k.shape[0]))
+                if held:
+                    raise ValueError(f"sequence {op.seq!r} holds {held} tokens before this prompt")
+            if out_dtype not in (None, q.dtype) or partition_size or shared_prefix:
+                raise ValueError("a prompt's output has the type of q; it has no partitions and "
+                                 "no shared prefix")
+        out_dtype = out_dtype or (q.dtype if prompt else torch.float32)
         slots, pairs, ks, vs = self.reserve(step_ops, names) if reserve else (None, [], [], [])
         seqs = [names[op.seq] for op in step_ops]
         q_lens = [int(op.k.shape[0]) for op in step_ops]
@@ -171,8 +226,15 @@ class PagedKVCache:
         multi = max(q_lens) > 1
         qsl = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
         nq = int(qsl[-1])
-        ws_bytes = decode_workspace_size(len(seqs), nq, q.shape[1], self.num_kv_heads, q.shape[2],
-                                         max(q_lens), max(lens), partition_size)
+        if rotary is not None:
+            if positions is None:
+                positions = np.concatenate(
+                    [L - r + self.pool.evicted.get(s, 0) + np.arange(r)
+                     for s, L, r in zip(seqs, lens, q_lens)])
+            positions = torch.as_tensor(positions, dtype=torch.int32).to(dev).contiguous()
+        ws_bytes = 0 if prompt else decode_workspace_size(
+            len(seqs), nq, q.shape[1], self.num_kv_heads, q.shape[2], max(q_lens), max(lens),
+            partition_size)
         shared = None
         if shared_prefix:
             gs, pl = self.pool.prefix_groups(seqs, q_lens)
@@ -185,37 +247,53 @@ class PagedKVCache:
                 group_start_host=gs, prefix_len_host=pl, max_group_q_len=max(gq),
                 max_prefix_len=int(pl.max()),
                 workspace=zeroed_workspace(sp_bytes, dev))
+        key, q = torch.cat(ks).to(dev), q.to(dev).contiguous()
         return StepInputs(
-            key=torch.cat(ks).to(dev), value=torch.cat(vs).to(dev),
+            key=key, value=torch.cat(vs).to(dev),
             slots=torch.from_numpy(np.ascontiguousarray(slots)).to(dev),
             pairs=(torch.tensor(pairs, dtype=torch.int32, device=dev) if pairs else None),
-            q=q.to(dev).contiguous(),
+            q=q,
             block_tables=torch.from_numpy(bt).to(dev),
             context_lens=torch.from_numpy(cl).to(dev),
             query_start_loc=torch.from_numpy(qsl).to(dev) if multi else None,
             max_q_len=max(q_lens), max_context_len=max(lens),
             out=torch.empty((nq, q.shape[1], q.shape[2]), dtype=out_dtype, device=dev),
             workspace=zeroed_workspace(ws_bytes, dev),
-            shared=shared, q_lens=q_lens, seqs=[op.seq for op in step_ops])
+            shared=shared, q_lens=q_lens, seqs=[op.seq for op in step_ops],
+            rotary=rotary, positions=None if rotary is None else positions,
+            q_rotated=None if rotary is None else torch.empty_like(q),
+            key_rotated=None if rotary is None else torch.empty_like(key),
+            prompt_start=torch.from_numpy(qsl).to(dev) if prompt else None)
 
     def write_step(self, si: StepInputs) -> None:
         """The step's cache writes: copy-on-write block copies, then the append."""
         if si.pairs is not None:
             copy_blocks(self.k, self.v, si.pairs, self.num_blocks, self.k_scale,
                         self.v_scale, self.k_zp, self.v_zp)
+        if si.rotary is not None:
+            rope_append_kv(si.q_rotated, si.q, si.key, si.value, self.k, self.v, si.slots,
+                           si.rotary.cos_sin, si.positions, self.num_blocks, self.k_scale,
+                           self.v_scale, self.k_zp, self.v_zp, si.key_rotated,
+                           si.rotary.interleaved, si.rotary.freq_axis)
+            return
         append_kv(si.key, si.value, self.k, self.v, si.slots, self.num_blocks,
                   self.k_scale, self.v_scale, self.k_zp, self.v_zp)
 
     def attend_step(self, si: StepInputs, scale: float, partition_size: int = 0) -> torch.Tensor:
-        """The step's attention over the cache (decode kernel + partial merge)."""
+        """The step's attention over the cache (decode kernel + partial merge), or of whole
+        prompts over their own rows. Rotated queries are those that write_step left."""
+        if si.prompt_start is not None:
+            key = si.key if si.key_rotated is None else si.key_rotated
+            prompt_attention(si.out, _queries(si), key, si.value, si.prompt_start, si.max_q_len, scale)
+            return si.out
         if si.shared is not None:
             sp = si.shared
-            decode_shared_prefix(si.out, si.q, self.k, self.v, si.block_tables, si.context_lens,
+            decode_shared_prefix(si.out, _queries(si), self.k, self.v, si.block_tables, si.context_lens,
                                  si.max_context_len, scale, sp.group_start, sp.prefix_len,
                                  sp.max_group_q_len, sp.max_prefix_len, si.query_start_loc,
                                  si.max_q_len, self.num_blocks, sp.workspace)
             return si.out
-        decode(si.out, si.q, self.k, self.v, si.block_tables, si.context_lens,
+        decode(si.out, _queries(si), self.k, self.v, si.block_tables, si.context_lens,
                si.max_context_len, scale, si.query_start_loc, si.max_q_len, self.num_blocks,
                self.k_scale, self.v_scale, self.k_zp, self.v_zp, partition_size,
                si.workspace)
@@ -276,7 +354,7 @@ class PagedKVCache:
         every query counts, and what rejected ones gave stays in the sums."""
         if si.seqs is not None and list(si.seqs) != tw.seqs:
             raise ValueError(f"the step is of {list(si.seqs)}, the weights of {tw.seqs}")
-        q, lens, start = si.q, si.context_lens, si.query_start_loc
+        q, lens, start = _queries(si), si.context_lens, si.query_start_loc
         if accepted is not None:
             runs = np.asarray(si.q_lens, np.int64)
             acc = np.asarray(accepted, np.int64)

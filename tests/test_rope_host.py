@@ -166,3 +166,45 @@ def test_plain_int8_is_the_oracles():
     for i in range(len(x)):
         c, s, z = oracle.quantize_row(x[i])
         assert np.array_equal(c, code[i]) and s == scale[i] and z == zp[i]
+
+
+def test_table_of_angles():
+    from paged_kv_cache_154_gb300.engine import rope_table
+    tab = rope_table(50, 16, device="cpu").numpy()
+    assert tab.shape == (50, 16) and np.abs(tab - ref.table(50, 16)).max() < 1e-7
+    # far positions: angles in 64 bits
+    tab = rope_table(1 << 17, 8, device="cpu").numpy()
+    p = (1 << 17) - 1
+    want = np.cos(np.float64(p) * 10000.0 ** (-2 * np.arange(4) / 8))
+    assert np.abs(tab[p, :4] - want).max() < 2.0 ** -24
+    tab = rope_table(5, 4, inv_freq=[1.0, 0.5], factor=2.0, device="cpu").numpy()
+    assert np.allclose(tab[3], [2 * np.cos(3), 2 * np.cos(1.5), 2 * np.sin(3), 2 * np.sin(1.5)])
+    with pytest.raises(ValueError, match="inv_freq"):
+        rope_table(5, 4, inv_freq=[1.0], device="cpu")
+
+
+def test_engine_refuses_what_is_no_whole_prompt():
+    from types import SimpleNamespace as Op
+    from paged_kv_cache_154_gb300.engine import PagedKVCache
+    cache = PagedKVCache(8, 1, 64, "f16", device="cpu")
+    names = {}
+    cache.reserve([Op(seq="a"), Op(seq="b")], names)
+    cache.pool.seq_append_slots(names["b"], 3)
+    x = torch.zeros((2, 1, 64), dtype=torch.float16)
+    q = torch.zeros((4, 2, 64), dtype=torch.float16)
+
+    def op(s):
+        return Op(seq=s, k=x, v=x)
+
+    with pytest.raises(ValueError, match="'b' holds 3 tokens"):
+        cache.prepare_step([op("a"), op("b")], names, q, prompt=True)
+    with pytest.raises(ValueError, match="twice"):
+        cache.prepare_step([op("a"), op("a")], names, q, prompt=True)
+    for bad in (dict(out_dtype=torch.float32), dict(partition_size=64), dict(shared_prefix=True)):
+        with pytest.raises(ValueError, match="type of q"):
+            cache.prepare_step([op("a")], names, q[:2], prompt=True, **bad)
+    assert cache.pool.seq_len(names["a"]) == 0          # refused before anything is reserved
+    si = cache.prepare_step([op("a")], names, q[:2], prompt=True)
+    assert si.out.dtype == torch.float16 and si.workspace is None
+    si = cache.prepare_step([op("b")], names, q[:2])
+    assert si.out.dtype == torch.float32 and si.prompt_start is None
