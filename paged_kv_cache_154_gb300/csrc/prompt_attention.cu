@@ -57,7 +57,8 @@ struct Layout {
     static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr int kKVOff = 2 * kTile;
     static constexpr int kSumOff = kKVOff + kStages * kTile;   // l of both Q tiles' rows
-    static constexpr int kBarOff = kSumOff + 2 * kRows * 4;
+    static constexpr int kOutOff = kSumOff + 2 * kRows * 4;    // an output tile on its way out
+    static constexpr int kBarOff = kOutOff + kTile;
     // barriers
     static constexpr int kKVFull = 0, kKVEmpty = kStages, kClean = 2 * kStages,
                          kQFull = 3 * kStages, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2,
@@ -92,10 +93,14 @@ struct PromptParams {
     float scale_log2;
 };
 
+// Tokens off .. len - 1 of the prompt that starts at token `start`: what is behind them does
+// not matter to the task. Chunks are counted back from the prompt's end, so that the one that
+// may leave Q tile 1 empty is the one with the fewest keys.
 struct alignas(16) Task {
-    int start, len;             // of the prompt
-    int off;                    // first token of the task, in the prompt
-    int head;                   // KV head, or -1: no more tasks
+    int start, len, off;
+    int head_last;              // 2 x KV head + whether the prompt ends here; -1: no more tasks
+    __device__ __forceinline__ int head() const { return head_last >> 1; }
+    __device__ __forceinline__ bool last() const { return head_last & 1; }
 };
 
 // What a task's Q tile x sees: the prompt's tokens [0, keys), in `tiles` tiles.
@@ -303,24 +308,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto read_task = [&](int i, Task& t) -> bool {
         if (!wait(LY::kTaskFull + (i & 1), (i >> 1) & 1, pa::ERR_WAIT_FULL)) return false;
         volatile Task& r = tasks[i & 1];
-        t.start = r.start, t.len = r.len, t.off = r.off, t.head = r.head;
+        t.start = r.start, t.len = r.len, t.off = r.off, t.head_last = r.head_last;
         __syncwarp();
         if (lane == 0) pa::mbar_arrive(bar(LY::kTaskEmpty + (i & 1)));
-        return t.head >= 0;
+        return t.head_last >= 0;
     };
     auto read_task_one = [&](int i, Task& t) -> bool {
         if (!wait_one(LY::kTaskFull + (i & 1), (i >> 1) & 1, pa::ERR_WAIT_FULL)) return false;
         volatile Task& r = tasks[i & 1];
-        t.start = r.start, t.len = r.len, t.off = r.off, t.head = r.head;
+        t.start = r.start, t.len = r.len, t.off = r.off, t.head_last = r.head_last;
         pa::mbar_arrive(bar(LY::kTaskEmpty + (i & 1)));
-        return t.head >= 0;
+        return t.head_last >= 0;
     };
     const int G = p.group, tokens = p.tokens;
     // whether the last products of both Q tiles reach V rows behind the prompt, in one tile:
     // then Q tile 0's softmax zeroes them, and Q tile 1's products wait for that
     auto first_cleans = [&](const Task& t) {
         const Span a(t, tokens, 0), b(t, tokens, 1);
-        return b.keys > a.keys && a.tiles == b.tiles && ((a.keys + 15) & ~15) > t.len;
+        return t.last() && b.keys > a.keys && a.tiles == b.tiles && ((a.keys + 15) & ~15) > t.len;
     };
 
     if (warp < 8) {
@@ -411,7 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // zeroed, so that a weight of 0 never meets a NaN. The first Q tile to reach them
             // does it.
             auto zero_behind = [&]() -> bool {
-                if (((span.keys + 15) & ~15) <= task.len || (x == 1 && first_cleans(task))) return true;
+                if (!task.last() || ((span.keys + 15) & ~15) <= task.len ||
+                    (x == 1 && first_cleans(task)))
+                    return true;
                 Ring<kStages> v = kv;
                 v.advance(2 * span.tiles - 1);
                 if (!wait(LY::kKVFull + v.slot, v.phase, pa::ERR_WAIT_FULL)) return false;
@@ -512,6 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = 32 * (warp & 3) + lane;
         const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
         const int token = row / G, head = row % G;
+        constexpr int kChunks = D / 8;                       // 16-byte parts of a row
+        uint4* const out = reinterpret_cast<uint4*>(smem + LY::kOutOff) + 32 * (warp & 3) * kChunks;
         uint32_t parity = 0;                                 // of Q tile x in bit x
         Task task;
         bool ok = true;
@@ -520,9 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int x = 0; x < nq; ++x) {
                 const int at = task.off + x * tokens + token;
-                const bool valid = token < tokens && at < task.len;
-                T* const dst = static_cast<T*>(p.out) + (int64_t)(task.start + at) * p.out_stride +
-                               (int64_t)(task.head * G + head) * D;
+                // where this lane's row goes, in units of 8 elements; -1: nowhere
+                const int64_t mine =
+                    token < tokens && at < task.len
+                        ? ((int64_t)(task.start + at) * p.out_stride + (task.head() * G + head) * D) / 8
+                        : -1;
                 ok = wait(LY::kLFull + x, (parity >> x) & 1, pa::ERR_WAIT_FULL) &&
                      wait(LY::kOFull + x, (parity >> x) & 1, pa::ERR_WAIT_FULL);
                 if (!ok) break;
@@ -537,26 +548,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pa::tc::ld_32cols_nowait(o_tm + c, o);
                     pa::tc::wait_ld();
                     pa::tc::loaded(o);
-                    if (c == D - 32) {                       // all of O and l has been read
-                        pa::tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) pa::mbar_arrive(bar(LY::kOFree + x));
-                    }
-                    if (valid) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 w;
-                            w.x = pack2<T>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                            w.y = pack2<T>(__uint_as_float(o[e + 2]) * inv,
-                                           __uint_as_float(o[e + 3]) * inv);
-                            w.z = pack2<T>(__uint_as_float(o[e + 4]) * inv,
-                                           __uint_as_float(o[e + 5]) * inv);
-                            w.w = pack2<T>(__uint_as_float(o[e + 6]) * inv,
-                                           __uint_as_float(o[e + 7]) * inv);
-                            *reinterpret_cast<uint4*>(dst + c + e) = w;
-                        }
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 w;
+                        w.x = pack2<T>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                        w.y = pack2<T>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                        w.z = pack2<T>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                        w.w = pack2<T>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                        out[lane * kChunks + (((c + e) / 8) ^ (lane % kChunks))] = w;
                     }
                 }
+                // all of O and l has been read
+                pa::tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) pa::mbar_arrive(bar(LY::kOFree + x));
+                // whole rows side by side (a lane a row of its own took 2700 cycles a tile, most
+                // of them for 32 places a store)
+#pragma unroll 4
+                for (int r0 = 0; r0 < 32; r0 += 32 / kChunks) {
+                    const int r = r0 + lane / kChunks, ch = lane % kChunks;
+                    const int64_t to = __shfl_sync(0xffffffffu, mine, r);
+                    if (to >= 0)
+                        reinterpret_cast<uint4*>(p.out)[to + ch] = out[r * kChunks + (ch ^ (r % kChunks))];
+                }
+                __syncwarp();
             }
         }
     } else {
@@ -663,18 +678,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             cleaned ^= 1u << v.slot;
                         }
                         const int steps = (s.keys - t * kKeys + 15) >> 4;
-                        ok = ok && my_turn(turn) &&
-                             wait_one(LY::kPFull + 2 * x, n_s & 1, pa::ERR_WAIT_FULL);
+                        ok = ok && my_turn(turn);
+                        // the other one's next products need not wait for this task's last P
+                        if (ok && !more) pass_turn(turn);
+                        ok = ok && wait_one(LY::kPFull + 2 * x, n_s & 1, pa::ERR_WAIT_FULL);
                         if (!ok) break;
                         issue_pv(v, 0, steps, t > 0);
                         ok = wait_one(LY::kPFull + 2 * x + 1, n_s & 1, pa::ERR_WAIT_FULL);
                         if (!ok) break;
                         issue_pv(v, 1, steps, true);
                         if (LY::kApart) pa::tc::commit(bar(LY::kODone + x));
-                        if (!more) {
-                            pass_turn(turn);
-                            pa::tc::commit(bar(LY::kOFull + x));
-                        }
+                        if (!more) pa::tc::commit(bar(LY::kOFull + x));
                         pa::tc::commit(bar(LY::kKVEmpty + v.slot));
                         if (!LY::kApart || !more) kv = next;
                         if (!LY::kApart && more) issue_qk(turn);
@@ -705,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pa::mbar_arrive_expect_tx(b, LY::kTile);
                         tma_load_4d(base + LY::kKVOff + kv.slot * LY::kTile,
                                     k & 1 ? &map_v : &map_k, 0, task.start + (k >> 1) * kKeys, 0,
-                                    task.head, b);
+                                    task.head(), b);
                         kv = kv.next();
                         ++loaded;
                         return true;
@@ -720,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pa::mbar_arrive_expect_tx(b, q_bytes * LY::kHalves);
                         for (int h = 0; h < LY::kHalves; ++h)
                             tma_load_3d(base + x * LY::kTile + h * LY::kHalf, &map_q, 64 * h,
-                                        task.head * G, task.start + task.off + x * tokens, b);
+                                        task.head() * G, task.start + task.off + x * tokens, b);
                         ++n_q[x];
                     }
                     for (int k = 1; ok && k < 2 * tiles; ++k) ok = load(k);
@@ -761,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const unsigned v = i * P + (i & 1 ? P - 1 - blockIdx.x : blockIdx.x);
                 const unsigned chunk = v / (unsigned)p.num_kv_heads;
                 Task t;
-                t.start = t.len = t.off = 0, t.head = -1;
+                t.start = t.len = t.off = 0, t.head_last = -1;
                 if (chunk < all) {
                     int lo = 0, hi = p.max_chunks;           // F(lo) > chunk >= F(hi)
                     unsigned above = 0;                      // F(hi)
@@ -785,20 +799,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         left -= cnt;
                     }
-                    t.len = length_of(p, s, t.start);
-                    t.off = lo * per_task;
-                    t.head = (int)(v % (unsigned)p.num_kv_heads);
+                    const int len = length_of(p, s, t.start);
+                    // chunks behind this one (none, if the lengths changed under the kernel)
+                    const int behind = max(0, (len + per_task - 1) / per_task - 1 - lo);
+                    t.len = len - behind * per_task;
+                    t.off = max(0, t.len - per_task);
+                    t.head_last = 2 * (int)(v % (unsigned)p.num_kv_heads) + (behind == 0);
                 }
                 if (i >= 2 &&
                     !wait(LY::kTaskEmpty + (i & 1), ((i >> 1) - 1) & 1, pa::ERR_WAIT_EMPTY))
                     break;
                 if (lane == 0) {
                     volatile Task& r = tasks[i & 1];
-                    r.start = t.start, r.len = t.len, r.off = t.off, r.head = t.head;
+                    r.start = t.start, r.len = t.len, r.off = t.off, r.head_last = t.head_last;
                     pa::mbar_arrive(bar(LY::kTaskFull + (i & 1)));
                 }
                 __syncwarp();
-                if (t.head < 0) break;
+                if (t.head_last < 0) break;
             }
         }
     }
