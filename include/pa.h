@@ -572,9 +572,9 @@ pa_status pa_decode_shared_prefix(
  *   scale          softmax scale, 0 or more, finite
  * Needs no workspace. Scores, softmax and sums are fp32, softmax weights are rounded
  * once to dtype for the product with the values. Nothing of one prompt reaches
- * another's rows, whatever values it holds; within a prompt a value that is not finite
- * may reach queries up to 15 tokens before its own. At most 128 query heads per KV
- * head, head_dim 64 or 128. */
+ * another's rows, whatever values it holds; within a prompt, a value that is not finite
+ * may also reach queries of up to 142 tokens before its own (a masked weight is 0, and
+ * 0 times it is NaN). At most 128 query heads per KV head, head_dim 64 or 128. */
 pa_status pa_prompt_attention(void* out, int64_t out_stride, const void* q, int64_t q_stride,
                               const void* key, int64_t key_stride, const void* value,
                               int64_t value_stride, pa_dtype dtype, const int32_t* seq_start,

@@ -39,6 +39,15 @@
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 
+#ifdef PA_TEST_HOOKS
+// Test builds only (-DPA_TEST_HOOKS): the first CTA does not start the copy of its k-th K or V
+// tile when k == g_test_skip_tile, so that the waits for that tile run out.
+__device__ int g_test_skip_tile = -1;
+extern "C" pa_status pa_test_skip_tile(int k) {
+    return pa::cuda_status(cudaMemcpyToSymbol(g_test_skip_tile, &k, sizeof k), "test hook");
+}
+#endif
+
 namespace {
 
 constexpr int kRows = 128;               // rows of a Q tile
@@ -717,6 +726,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             return false;
                         const uint32_t b = bar(LY::kKVFull + kv.slot);
                         pa::mbar_arrive_expect_tx(b, LY::kTile);
+#ifdef PA_TEST_HOOKS
+                        if (blockIdx.x == 0 && (int)loaded == g_test_skip_tile) {
+                            kv = kv.next();
+                            ++loaded;
+                            return true;
+                        }
+#endif
                         tma_load_4d(base + LY::kKVOff + kv.slot * LY::kTile,
                                     k & 1 ? &map_v : &map_k, 0, task.start + (k >> 1) * kKeys, 0,
                                     task.head(), b);

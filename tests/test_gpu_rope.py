@@ -401,3 +401,22 @@ def test_streams_and_graphs():
         call(caches[0], outs[0])
         call(caches[1], outs[1])
         torch.cuda.synchronize()
+
+
+def test_slots_far_into_a_cache():
+    """Cache offsets past 2^32 bytes and 2^31 elements, in the first and the last blocks."""
+    nb, G, d, T = 140000, 8, 128, 40
+    gen = torch.Generator().manual_seed(21)
+    k, v = (torch.randn((T, G, d), generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    tab = on_gpu(ref.table(64, d))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = torch.cat([torch.arange(20), nb * 16 - 20 + torch.arange(20)]).cuda()
+    kc, vc = (torch.zeros((nb, G, 16, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pa.rope_append_kv(None, None, k, v, kc, vc, slots, tab, pos)
+    rows_ = torch.empty_like(k), torch.empty_like(v)
+    pa.gather_kv(*rows_, kc, vc, slots)
+    assert pa.device_error() == 0
+    want = torch.empty_like(k)
+    pa.rope(want, k, None, None, tab, pos)
+    assert torch.equal(rows_[0], want) and torch.equal(rows_[1], v)
+    assert int(kc[2:-2].count_nonzero()) == 0 and int(vc[2:-2].count_nonzero()) == 0
