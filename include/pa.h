@@ -582,6 +582,14 @@ pa_status pa_prompt_attention(void* out, int64_t out_stride, const void* q, int6
                               int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
                               float scale, void* stream);
 
+/* The three calls above with their arguments in one array of 64-bit words, in the order
+ * of their declarations: pointers and integers as they are, the scale as the bits of a
+ * double. Results and refusals are the same. For bindings whose calls cost by the
+ * argument: 22 converted one by one take 1.9 us on the host, packed 0.7. */
+pa_status pa_rope_packed(const int64_t* args);               /* 22 words */
+pa_status pa_rope_append_kv_packed(const int64_t* args);     /* 33 words */
+pa_status pa_prompt_attention_packed(const int64_t* args);   /* 18 words */
+
 /* ---- Eviction by accumulated attention weight. A cache of bounded size keeps
  * the tokens that attention has looked at most. Per decode step (or once, from
  * a prompt's last queries) pa_accumulate_weights adds up what every cached token

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import sys
 from typing import Optional, Sequence, Tuple
 
@@ -63,6 +64,9 @@ _SIGS = {
                            _I32, _P, _I32, _I32, _I32, _I32, _I32, _P], ctypes.c_int),
     "pa_prompt_attention": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, ctypes.c_int, _P, _I32, _I32,
                              _I32, _I32, _I32, _I32, ctypes.c_float, _P], ctypes.c_int),
+    "pa_rope_packed": ([ctypes.c_char_p], ctypes.c_int),
+    "pa_rope_append_kv_packed": ([ctypes.c_char_p], ctypes.c_int),
+    "pa_prompt_attention_packed": ([ctypes.c_char_p], ctypes.c_int),
     "pa_decode_workspace_size": ([_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32], _SZ),
     "pa_decode": ([_P, ctypes.c_int, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _P,
                    _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
@@ -426,6 +430,10 @@ def gather_kv(key, value, k_cache, v_cache, slot_mapping, num_blocks: Optional[i
 # rows of a projection: rotary positions, prompts
 # ---------------------------------------------------------------------------
 
+# arguments of the packed calls
+_ROPE, _ROPE_APPEND, _PROMPT = struct.Struct("22q"), struct.Struct("33q"), struct.Struct("16qdq")
+
+
 def _heads(name, t, T: int, d: int, dtype) -> Tuple[int, int]:
     """Rows [T, heads, d] of this type, heads one after another (tokens may lie further
     apart: parts of a fused projection): their number and the elements from token to token."""
@@ -434,14 +442,27 @@ def _heads(name, t, T: int, d: int, dtype) -> Tuple[int, int]:
         raise ValueError(f"{name} is {tuple(s)} {t.dtype}, not ({T}, heads, {d}) {dtype}")
     a, b, c = t.stride()
     heads = s[1]
-    if c != 1 or b != d or T < 2 or heads < 2:
-        if T == 0 or heads == 0:
-            return heads, heads * d
-        if c != 1 or (b != d and heads > 1):
-            raise ValueError(f"{name} has strides {(a, b, c)}: a token's heads must be contiguous")
-        if T == 1:
-            return heads, heads * d
-    return heads, a
+    if T == 0 or heads == 0:
+        return heads, heads * d
+    if c != 1 or (b != d and heads > 1):
+        raise ValueError(f"{name} has strides {(a, b, c)}: a token's heads must be contiguous")
+    return heads, (a if T > 1 else heads * d)
+
+
+def _two(name, x, y_name, y, T: int, d: int, dtype) -> Tuple[int, int, int]:
+    """Rows x and rows y of as many heads: their number, and both strides."""
+    s = x.shape
+    if s == y.shape and x.dtype is dtype and y.dtype is dtype and len(s) == 3:
+        t, h, e = s
+        a, b, c = x.stride()
+        u, v, w = y.stride()
+        if t == T and e == d and b == d and v == d and c == 1 and w == 1 and t > 1 and h > 0:
+            return h, a, u
+    h, a = _heads(name, x, T, d, dtype)
+    n, u = _heads(y_name, y, T, d, dtype)
+    if n != h:
+        raise ValueError(f"{name} has {h} heads, {y_name} {n} heads")
+    return h, a, u
 
 
 _current_device = None
@@ -485,28 +506,28 @@ def rope(q_out, q, k_out, k, cos_sin, positions, interleaved: bool = False, freq
     tokens may lie further apart than their rows (parts of a fused projection); cos_sin
     fp32 [positions, rotary_dim]; positions int32 [T] or [axes, T]; freq_axis uint8
     [rotary_dim / 2] with several axes."""
-    T, d = q.shape[0], q.shape[-1]
+    at, dt = q.shape, q.dtype
+    T, d = at[0], at[-1]
     most, rd, axes = _rotation(cos_sin, positions, freq_axis, T)
-    H, qs = _heads("q", q, T, d, q.dtype)
-    Ho, qos = _heads("q_out", q_out, T, d, q.dtype)
-    G = ks = kos = Go = 0
-    if k is not None or k_out is not None:
-        G, ks = _heads("k", k, T, d, q.dtype)
-        Go, kos = _heads("k_out", k_out, T, d, q.dtype)
-    if H != Ho or G != Go:
-        raise ValueError(f"{H} and {G} heads of q and k, {Ho} and {Go} of q_out and k_out")
+    H, qs, qos = _two("q", q, "q_out", q_out, T, d, dt)
     dev = q.get_device()
-    if (dev < 0 or dev != _device() or q_out.get_device() != dev or cos_sin.get_device() != dev
-            or positions.get_device() != dev or (k is not None and (k.get_device() != dev or
-                                                                    k_out.get_device() != dev))
-            or (freq_axis is not None and freq_axis.get_device() != dev)):
+    away = (dev < 0 or dev != _device() or q_out.get_device() != dev
+            or cos_sin.get_device() != dev or positions.get_device() != dev)
+    G = ks = kos = kp = kop = 0
+    if k is not None or k_out is not None:
+        if k is None or k_out is None:
+            raise ValueError("k and k_out: both or neither")
+        G, ks, kos = _two("k", k, "k_out", k_out, T, d, dt)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+        away = away or k.get_device() != dev or k_out.get_device() != dev
+    if away or (freq_axis is not None and freq_axis.get_device() != dev):
         _elsewhere("q q_out k k_out cos_sin positions freq_axis", q, q_out, k, k_out, cos_sin,
                    positions, freq_axis)
-    _check(lib().pa_rope(q_out.data_ptr(), qos, q.data_ptr(), qs, H,
-                         k_out.data_ptr() if G else None, kos, k.data_ptr() if G else None, ks, G,
-                         _dtype_code(q), _ptr(cos_sin), most, rd, int(interleaved),
-                         _ptr(positions), axes, _ptr(freq_axis), int(inverse), T, d,
-                         _stream(stream)))
+    _check(lib().pa_rope_packed(_ROPE.pack(
+        q_out.data_ptr(), qos, q.data_ptr(), qs, H, kop, kos, kp, ks, G, _dtype_code(q),
+        _ptr(cos_sin), most, rd, 1 if interleaved else 0, _ptr(positions), axes,
+        _ptr(freq_axis) or 0, 1 if inverse else 0,
+        T, d, _stream(stream))))
 
 
 def rope_append_kv(q_out, q, key, value, k_cache, v_cache, slot_mapping, cos_sin, positions,
@@ -515,31 +536,33 @@ def rope_append_kv(q_out, q, key, value, k_cache, v_cache, slot_mapping, cos_sin
                    stream=None) -> None:
     """pa_rope_append_kv; rows and rotation as rope() takes them (q and q_out may be None
     both; key_out, the rotated keys, may be key), cache and slots as append_kv()."""
-    T, d = key.shape[0], key.shape[-1]
+    at, dt = key.shape, key.dtype
+    T, d = at[0], at[-1]
     shape, code = k_cache.shape, _dtype_code(k_cache)
     nb = shape[0] if num_blocks is None else num_blocks
     most, rd, axes = _rotation(cos_sin, positions, freq_axis, T)
-    G, ks = _heads("key", key, T, d, key.dtype)
-    Gv, vs = _heads("value", value, T, d, key.dtype)
-    kos, Go = 0, G
-    if key_out is not None:
-        Go, kos = _heads("key_out", key_out, T, d, key.dtype)
-    H = qs = Ho = qos = 0
-    if q is not None or q_out is not None:
-        H, qs = _heads("q", q, T, d, key.dtype)
-        Ho, qos = _heads("q_out", q_out, T, d, key.dtype)
-    if H != Ho or Gv != G or Go != G:
-        raise ValueError(f"{H} heads of q, {Ho} of q_out; {G} of key, {Gv} of value, {Go} of "
-                         "key_out")
+    G, ks, vs = _two("key", key, "value", value, T, d, dt)
     if G != shape[1] or d != (shape[3] * 2 if code == PA_INT4 else shape[3]):
-        raise ValueError(f"key is {tuple(key.shape)}, the cache {tuple(shape)}")
-    _cache_sized(code, nb, shape, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp)
-    _sized(("slot_mapping", slot_mapping, T, sys.modules["torch"].int64))
+        raise ValueError(f"key is {tuple(at)}, the cache {tuple(shape)}")
     dev = key.get_device()
     away = (dev < 0 or dev != _device() or value.get_device() != dev or k_cache.get_device() != dev
             or v_cache.get_device() != dev or slot_mapping.get_device() != dev
             or cos_sin.get_device() != dev or positions.get_device() != dev)
-    for t in (q, q_out, k_scale, v_scale, k_zp, v_zp, key_out, freq_axis):
+    H = qs = qos = qp = qop = kos = kop = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out: both or neither")
+        H, qs, qos = _two("q", q, "q_out", q_out, T, d, dt)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+        away = away or q.get_device() != dev or q_out.get_device() != dev
+    if key_out is not None:
+        _, _, kos = _two("key", key, "key_out", key_out, T, d, dt)
+        kop = key_out.data_ptr()
+        away = away or key_out.get_device() != dev
+    _cache_sized(code, nb, shape, k_cache, v_cache, k_scale, v_scale, k_zp, v_zp)
+    if slot_mapping.nbytes != 8 * T or slot_mapping.dtype is not sys.modules["torch"].int64:
+        _sized(("slot_mapping", slot_mapping, T, sys.modules["torch"].int64))
+    for t in (k_scale, v_scale, k_zp, v_zp, freq_axis):
         if t is not None and t.get_device() != dev:
             away = True
     if away:
@@ -547,37 +570,32 @@ def rope_append_kv(q_out, q, key, value, k_cache, v_cache, slot_mapping, cos_sin
                    "v_scale k_zp v_zp key_out freq_axis", q, q_out, key, value, k_cache, v_cache,
                    slot_mapping, cos_sin, positions, k_scale, v_scale, k_zp, v_zp, key_out,
                    freq_axis)
-    _check(lib().pa_rope_append_kv(
-        q_out.data_ptr() if H else None, qos, q.data_ptr() if H else None, qs, H,
-        None if key_out is None else key_out.data_ptr(), kos, key.data_ptr(), ks,
-        value.data_ptr(), vs, _dtype_code(key), _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale),
-        _ptr(v_scale), _ptr(k_zp), _ptr(v_zp), _ptr(slot_mapping), _ptr(cos_sin), most, rd,
-        int(interleaved), _ptr(positions), axes, _ptr(freq_axis), T, nb, G, d, shape[2],
-        _stream(stream)))
+    _check(lib().pa_rope_append_kv_packed(_ROPE_APPEND.pack(
+        qop, qos, qp, qs, H, kop, kos, key.data_ptr(), ks, value.data_ptr(), vs, _dtype_code(key),
+        _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale) or 0, _ptr(v_scale) or 0, _ptr(k_zp) or 0,
+        _ptr(v_zp) or 0, _ptr(slot_mapping), _ptr(cos_sin), most, rd, 1 if interleaved else 0, _ptr(positions),
+        axes, _ptr(freq_axis) or 0, T, nb, G, d, shape[2], _stream(stream))))
 
 
 def prompt_attention(out, q, key, value, seq_start, max_seq_len: int, scale: float,
                      stream=None) -> None:
     """pa_prompt_attention; q and out [T, H, d], key and value [T, H_kv, d], of which tokens
     may lie further apart than their rows; seq_start int32 [num_seqs + 1] on the device."""
-    T, d = q.shape[0], q.shape[-1]
-    H, qs = _heads("q", q, T, d, q.dtype)
-    Ho, os_ = _heads("out", out, T, d, q.dtype)
-    G, ks = _heads("key", key, T, d, q.dtype)
-    Gv, vs = _heads("value", value, T, d, q.dtype)
-    if H != Ho or G != Gv:
-        raise ValueError(f"{H} heads of q, {Ho} of out; {G} of key, {Gv} of value")
-    if seq_start.dim() != 1 or seq_start.dtype is not sys.modules["torch"].int32:
-        raise ValueError(f"seq_start is {tuple(seq_start.shape)} {seq_start.dtype}, not "
-                         "(num_seqs + 1,) torch.int32")
+    at, dt = q.shape, q.dtype
+    T, d = at[0], at[-1]
+    H, qs, os_ = _two("q", q, "out", out, T, d, dt)
+    G, ks, vs = _two("key", key, "value", value, T, d, dt)
+    n = seq_start.shape
+    if len(n) != 1 or seq_start.dtype is not sys.modules["torch"].int32:
+        raise ValueError(f"seq_start is {tuple(n)} {seq_start.dtype}, not (num_seqs + 1,) torch.int32")
     dev = q.get_device()
     if (dev < 0 or dev != _device() or out.get_device() != dev or key.get_device() != dev
             or value.get_device() != dev or seq_start.get_device() != dev):
         _elsewhere("q out key value seq_start", q, out, key, value, seq_start)
-    _check(lib().pa_prompt_attention(
+    _check(lib().pa_prompt_attention_packed(_PROMPT.pack(
         out.data_ptr(), os_, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs,
-        _dtype_code(q), _ptr(seq_start), seq_start.shape[0] - 1, T, int(max_seq_len), H, G, d,
-        float(scale), _stream(stream)))
+        _dtype_code(q), _ptr(seq_start), n[0] - 1, T, max_seq_len, H, G, d, scale,
+        _stream(stream))))
 
 
 def decode_workspace_size(num_seqs: int, num_q_tokens: int, num_heads: int, num_kv_heads: int,

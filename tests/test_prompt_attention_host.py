@@ -1,5 +1,7 @@
 """Attention over prompts without a GPU: refusals of pa_prompt_attention and of its binding,
 and the plain form against torch's."""
+import struct
+
 import numpy as np
 import pytest
 import torch
@@ -20,7 +22,12 @@ CALL = dict(out=A, os=1024, q=A, qs=1024, k=A, ks=256, v=A, vs=256, dt=pa.PA_BF1
 
 
 def status(**change):
-    return pa.lib().pa_prompt_attention(*[change.get(n, CALL[n]) for n in CALL])
+    """The call's status, which the packed form of it shares."""
+    values = [change.get(n, CALL[n]) for n in CALL]
+    got = pa.lib().pa_prompt_attention(*values)
+    words = struct.pack("16qdq", *[v or 0 for v in values])
+    assert pa.lib().pa_prompt_attention_packed(words) == got
+    return got
 
 
 @pytest.mark.parametrize("change,want", [

@@ -1,5 +1,7 @@
 """Rotary positions without a GPU: the refusals of pa_rope and pa_rope_append_kv, made
 before anything is launched, the binding's own, and the plain forms against closed ones."""
+import struct
+
 import numpy as np
 import pytest
 import torch
@@ -34,7 +36,14 @@ BOTH = [
 
 
 def status(fn, args, change):
-    return getattr(pa.lib(), fn)(*[change.get(n, args[n]) for n in args])
+    """The call's status, which the packed form of it shares."""
+    values = [change.get(n, args[n]) for n in args]
+    got = getattr(pa.lib(), fn)(*values)
+    message = pa.lib().pa_last_error()
+    words = struct.pack(f"{len(values)}q", *[v or 0 for v in values])
+    assert getattr(pa.lib(), fn + "_packed")(words) == got
+    assert pa.lib().pa_last_error() == message
+    return got
 
 
 @pytest.mark.parametrize("change,want", BOTH + [
@@ -52,6 +61,11 @@ def test_rope_refusals(change, want):
     (dict(ko=A, kos=512), 1), (dict(ko=A + 4096, kos=128), 1)])
 def test_rope_append_refusals(change, want):
     assert status("pa_rope_append_kv", APPEND, change) == want
+
+
+def test_packed_calls_need_their_array():
+    for fn in ("pa_rope", "pa_rope_append_kv", "pa_prompt_attention"):
+        assert getattr(pa.lib(), fn + "_packed")(None) == 1
 
 
 def test_empty_calls_are_accepted():
@@ -102,6 +116,8 @@ def test_binding_of_rope():
         refuses("positions", pa.rope, rope_args(), positions=p)
     refuses("freq_axis", pa.rope, rope_args(), positions=torch.zeros((2, T), dtype=torch.int32),
             freq_axis=torch.zeros(D, dtype=torch.uint8))
+    refuses("both or neither", pa.rope, rope_args(), k=None)
+    refuses("both or neither", pa.rope, rope_args(), k_out=None)
     refuses("current device", pa.rope, rope_args())     # host tensors
 
 
@@ -115,6 +131,7 @@ def test_binding_of_rope_append():
             key_out=torch.zeros((T, G, D), dtype=torch.float16))
     refuses("slot_mapping", pa.rope_append_kv, append_args(),
             slot_mapping=torch.zeros(T, dtype=torch.int32))
+    refuses("both or neither", pa.rope_append_kv, append_args(), q=None)
     refuses("v_cache", pa.rope_append_kv, append_args(),
             v_cache=torch.zeros((NB - 1, G, 16, D), dtype=b))
     refuses("num_blocks", pa.rope_append_kv, append_args(), num_blocks=NB + 1)
