@@ -570,11 +570,12 @@ pa_status pa_decode_shared_prefix(
  *                  [0, num_tokens] and lengths past max_seq_len are cut to them.
  *   max_seq_len    the longest prompt (host value), at most 2^22
  *   scale          softmax scale, 0 or more, finite
- * Needs no workspace. Scores, softmax and sums are fp32, softmax weights are rounded
+ * Needs no workspace. A query whose scores are all -infinity gives 0. Scores, softmax and sums are fp32, softmax weights are rounded
  * once to dtype for the product with the values. Nothing of one prompt reaches
  * another's rows, whatever values it holds; within a prompt, a value that is not finite
  * may also reach queries of up to 142 tokens before its own (a masked weight is 0, and
- * 0 times it is NaN). At most 128 query heads per KV head, head_dim 64 or 128. */
+ * 0 times it is NaN). At most 128 query heads per KV head and 65535 in all, head_dim 64
+ * or 128. */
 pa_status pa_prompt_attention(void* out, int64_t out_stride, const void* q, int64_t q_stride,
                               const void* key, int64_t key_stride, const void* value,
                               int64_t value_stride, pa_dtype dtype, const int32_t* seq_start,

@@ -5,16 +5,17 @@
 // in contiguous groups per KV head ("cs336 lecture 10", GQA).
 //
 // A task is a run of a prompt's tokens and one KV head: two Q tiles of 128 rows,
-// a row a (token, head of the group) pair, tokens_per_tile = 128 / group tokens a
-// tile, against the prompt's keys up to its last token in tiles of 128. Per tile:
+// a row a (token, head of the group) pair, 128 / group tokens a tile, against the
+// prompt's keys up to its last token in tiles of 128. Per tile:
 //   S = Q K^T      M128 N128, both K-major in shared memory, S in TMEM
-//   P = 2^(S - m)  one thread a row, P as 16 bits over the columns of S
+//   P = 2^(S - m)  one thread a row, P as 16 bits into TMEM
 //   O += P V       M128 N = head_dim, P from TMEM, V MN-major in shared memory
 // The running maximum m moves only when a tile raises it by more than 2^8 (the
 // weights then stay below 2^8, and O is scaled in TMEM, which is rare); sums and O
-// are fp32. P is rounded to the 16-bit type once (half a step: 2^-9 bf16, 2^-12
-// fp16 of a weight), as the tensor cores take it: the same size as the rounding
-// of the output.
+// are fp32. P is rounded to the 16-bit type once, at most half a step (2^-8 bf16,
+// 2^-11 fp16 of a weight), as the tensor cores take it: the size of the rounding of
+// the output. (Two 16-bit parts, as the paged prefill has them, would be a third
+// product.)
 //
 // A CTA a SM stays and works off its tasks: the longest first (a task's keys grow
 // with its place in the prompt), dealt out to and fro over the CTAs. Its roles:
@@ -25,6 +26,19 @@
 //   warp 13          TMA: Q tiles, K and V tiles into a ring
 //   warp 14          finds the tasks
 // Every wait is bounded; one that gives up ends every role's loop.
+//
+// What bounds it. head_dim 128: the tensor cores, 2048 of about 2250 cycles of a
+// step (two Q tiles against 128 keys). One prompt of 8192 tokens, 32 heads over 8:
+// 323 us, 1700 TFLOP/s; of 32768: 5.5 ms, 1600 TFLOP/s, at the power limit.
+// head_dim 64: the softmax, 2200 cycles a step of which the products need 1024; the
+// two warps of a quarter need 1100 for arithmetic alone (exponentials 1024), the
+// rest are loads from TMEM and barriers. 16384 tokens, 32 heads over 8: 1.05 ms,
+// 1045 TFLOP/s. Measured beside it, per step of head_dim 64: products waiting for P as
+// at 128 (1.08 ms), four softmax warpgroups of half a tile's keys each (1.23 ms),
+// halves of a tile one after another with the next one's maximum beside them (1.20
+// ms), turns at the exponentials (1.18 ms).
+// Short prompts: a task costs about 7000 cycles besides its steps (its first tile
+// finds both softmaxes idle). 16 of 200 to 2000 tokens: 137 us, 1140 TFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -481,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // Weights of the first 64 keys against the maximum so far, while the maximum of
                 // all 128 is found beside them; in the rare case that it has moved, once more. P
-                // goes over the columns of the last 64 keys' S, which are in registers by then.
+                // may go over the columns of the last 64 keys' S: they are in registers by now.
                 for (bool again = true; again;) {
                     reference();
                     l4[0] = l4[1] = 0;
@@ -590,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // One branch around everything: a product then issues in fewer cycles than it runs
             // (64 at N = 128; with an election around each it took 140 to 160). A warp a Q tile:
             // the waits of one overlap the products of the other. Both read every K and V tile
-            // (or pass it on), and P V and Q K'^T of a Q tile run in the order of their issue, so
-            // that P is read before the next S takes its columns.
+            // (or pass it on). The tensor cores run a thread's products in the order of their
+            // issue, so that P V has read P before the next Q K^T takes its columns.
             if (elect_one()) {
                 const int x = warp == 12 ? 0 : 1;
                 constexpr uint32_t idesc_qk = pa::tc::idesc_f16(kBF16, false, false, kRows, kKeys);
@@ -607,10 +621,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // With two Q tiles their products take turns: P V and Q K'^T of one, then of the
                 // other, or both softmaxes would come to run at once and then both products.
                 // The turn goes over before the last products are issued, so that the pipe does
-                // not wait for the other warp to wake up.
+                // not wait for the other warp to wake up. (8192 tokens: 357 us, 410 without
+                // turns.) Where P has columns of its own, softmaxes do not wait for products.
                 uint32_t turns = 0;
                 auto my_turn = [&](bool two) -> bool {
-                    return LY::kApart || !two || wait_one(LY::kTurn + x, (turns++ & 1) ^ (x ^ 1), pa::ERR_WAIT_FULL);
+                    return LY::kApart || !two ||
+                           wait_one(LY::kTurn + x, (turns++ & 1) ^ (x ^ 1), pa::ERR_WAIT_FULL);
                 };
                 auto pass_turn = [&](bool two) {
                     if (!LY::kApart && two) pa::mbar_arrive(bar(LY::kTurn + (x ^ 1)));
@@ -892,7 +908,8 @@ extern "C" pa_status pa_prompt_attention(void* out, int64_t out_stride, const vo
     if (max_seq_len < 1) return fail(PA_ERR_INVALID_ARG, "max_seq_len %d", max_seq_len);
     if (max_seq_len > kMaxLen)
         return fail(PA_ERR_UNSUPPORTED, "prompts of more than %d tokens", kMaxLen);
-    if (!(scale >= 0.f) || isinf(scale)) return fail(PA_ERR_INVALID_ARG, "scale %g", (double)scale);
+    if (num_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_heads %d (at most 65535)", num_heads);
+    if (!(scale >= 0.f) || isinf(scale * kLog2e)) return fail(PA_ERR_INVALID_ARG, "scale %g", (double)scale);
     if (pa_status s = check_rows("q", q, q_stride, num_heads, head_dim)) return s;
     if (pa_status s = check_rows("key", key, key_stride, num_kv_heads, head_dim)) return s;
     if (pa_status s = check_rows("value", value, value_stride, num_kv_heads, head_dim)) return s;

@@ -35,7 +35,8 @@ def status(**change):
     (dict(v=None), 1), (dict(start=None), 1), (dict(dt=pa.PA_F32), 2), (dict(d=96), 2),
     (dict(H=7), 1), (dict(G=0), 1), (dict(H=0), 1), (dict(H=129, G=1, qs=1 << 20, os=1 << 20), 2),
     (dict(ml=0), 1), (dict(ml=(1 << 22) + 1), 2), (dict(scale=-1.0), 1),
-    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(out=ODD), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=3e38), 1),
+    (dict(H=65536, G=65536, qs=1 << 30, os=1 << 30, ks=1 << 30, vs=1 << 30), 2), (dict(scale=float("inf")), 1), (dict(out=ODD), 1),
     (dict(q=ODD), 1), (dict(k=ODD), 1), (dict(v=ODD), 1), (dict(qs=1016), 1), (dict(os=1028), 1),
     (dict(ks=248), 1), (dict(vs=-256), 1), (dict(ks=1 << 38), 2)])
 def test_refusals(change, want):
