@@ -555,6 +555,11 @@ pa_status pa_decode_shared_prefix(
     int32_t max_prefix_len, void* workspace, size_t workspace_bytes,
     void* stream);
 
+/* Bytes of workspace with which pa_prompt_attention sums prompts of this length best (0
+ * for up to 8192 tokens, and for invalid sizes); 16-byte aligned, needs no
+ * initialisation, may be shared by calls of one stream. Host-only: needs no GPU. */
+size_t pa_prompt_attention_workspace_size(int32_t head_dim, int32_t max_seq_len);
+
 /* Causal attention over whole prompts, packed one after another, straight from the
  * rows of a projection ([p3] §二 softmax(Q K^T / sqrt(d)) V; [p4] GQA): what a fresh
  * prompt needs besides its append, whatever type its cache has. Query i of a prompt
@@ -570,8 +575,15 @@ pa_status pa_decode_shared_prefix(
  *                  [0, num_tokens] and lengths past max_seq_len are cut to them.
  *   max_seq_len    the longest prompt (host value), at most 2^22
  *   scale          softmax scale, 0 or more, finite
- * Needs no workspace. A query whose scores are all -infinity gives 0. Scores, softmax and sums are fp32, softmax weights are rounded
- * once to dtype for the product with the values. Nothing of one prompt reaches
+ *   workspace      pa_prompt_attention_workspace_size() bytes, or NULL. With it the
+ *                  weighted sums of values, which the tensor cores cut off to 24 bits as
+ *                  they grow, are added up (to nearest) every 8192 keys. Without it a sum
+ *                  of one sign over n keys comes out short by up to about 5e-9 n of
+ *                  itself: 1.6e-4 for 32768. Where that would pass half a step of the
+ *                  output, max_seq_len above 2^16 (F16) or 2^19 (BF16), it is required. A
+ *                  smaller one is served by as many CTAs as it has parts for.
+ * Scores, softmax and sums are fp32, softmax weights are rounded once to dtype for the
+ * product with the values. A query whose scores are all -infinity gives 0. Nothing of one prompt reaches
  * another's rows, whatever values it holds; within a prompt, a value that is not finite
  * may also reach queries of up to 142 tokens before its own (a masked weight is 0, and
  * 0 times it is NaN). At most 128 query heads per KV head and 65535 in all, head_dim 64
@@ -581,7 +593,8 @@ pa_status pa_prompt_attention(void* out, int64_t out_stride, const void* q, int6
                               int64_t value_stride, pa_dtype dtype, const int32_t* seq_start,
                               int32_t num_seqs, int32_t num_tokens, int32_t max_seq_len,
                               int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
-                              float scale, void* stream);
+                              float scale, void* workspace, size_t workspace_bytes,
+                              void* stream);
 
 /* The three calls above with their arguments in one array of 64-bit words, in the order
  * of their declarations: pointers and integers as they are, the scale as the bits of a
@@ -589,7 +602,7 @@ pa_status pa_prompt_attention(void* out, int64_t out_stride, const void* q, int6
  * argument: 22 converted one by one take 1.9 us on the host, packed 0.7. */
 pa_status pa_rope_packed(const int64_t* args);               /* 22 words */
 pa_status pa_rope_append_kv_packed(const int64_t* args);     /* 33 words */
-pa_status pa_prompt_attention_packed(const int64_t* args);   /* 18 words */
+pa_status pa_prompt_attention_packed(const int64_t* args);   /* 20 words */
 
 /* ---- Eviction by accumulated attention weight. A cache of bounded size keeps
  * the tokens that attention has looked at most. Per decode step (or once, from

@@ -62,8 +62,9 @@ _SIGS = {
     "pa_rope_append_kv": ([_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, ctypes.c_int,
                            _P, _P, ctypes.c_int, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _P,
                            _I32, _P, _I32, _I32, _I32, _I32, _I32, _P], ctypes.c_int),
+    "pa_prompt_attention_workspace_size": ([_I32, _I32], _SZ),
     "pa_prompt_attention": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, ctypes.c_int, _P, _I32, _I32,
-                             _I32, _I32, _I32, _I32, ctypes.c_float, _P], ctypes.c_int),
+                             _I32, _I32, _I32, _I32, ctypes.c_float, _P, _SZ, _P], ctypes.c_int),
     "pa_rope_packed": ([ctypes.c_char_p], ctypes.c_int),
     "pa_rope_append_kv_packed": ([ctypes.c_char_p], ctypes.c_int),
     "pa_prompt_attention_packed": ([ctypes.c_char_p], ctypes.c_int),
@@ -431,7 +432,7 @@ def gather_kv(key, value, k_cache, v_cache, slot_mapping, num_blocks: Optional[i
 # ---------------------------------------------------------------------------
 
 # arguments of the packed calls
-_ROPE, _ROPE_APPEND, _PROMPT = struct.Struct("22q"), struct.Struct("33q"), struct.Struct("16qdq")
+_ROPE, _ROPE_APPEND, _PROMPT = struct.Struct("22q"), struct.Struct("33q"), struct.Struct("16qd3q")
 
 
 def _heads(name, t, T: int, d: int, dtype) -> Tuple[int, int]:
@@ -577,10 +578,16 @@ def rope_append_kv(q_out, q, key, value, k_cache, v_cache, slot_mapping, cos_sin
         axes, _ptr(freq_axis) or 0, T, nb, G, d, shape[2], _stream(stream))))
 
 
+def prompt_attention_workspace_size(head_dim: int, max_seq_len: int) -> int:
+    return int(lib().pa_prompt_attention_workspace_size(head_dim, max_seq_len))
+
+
 def prompt_attention(out, q, key, value, seq_start, max_seq_len: int, scale: float,
-                     stream=None) -> None:
+                     workspace=None, stream=None) -> None:
     """pa_prompt_attention; q and out [T, H, d], key and value [T, H_kv, d], of which tokens
-    may lie further apart than their rows; seq_start int32 [num_seqs + 1] on the device."""
+    may lie further apart than their rows; seq_start int32 [num_seqs + 1] on the device;
+    workspace: contiguous, prompt_attention_workspace_size() bytes, for the sums of long
+    prompts (required for the longest, without effect up to 8192 tokens)."""
     at, dt = q.shape, q.dtype
     T, d = at[0], at[-1]
     H, qs, os_ = _two("q", q, "out", out, T, d, dt)
@@ -590,11 +597,13 @@ def prompt_attention(out, q, key, value, seq_start, max_seq_len: int, scale: flo
         raise ValueError(f"seq_start is {tuple(n)} {seq_start.dtype}, not (num_seqs + 1,) torch.int32")
     dev = q.get_device()
     if (dev < 0 or dev != _device() or out.get_device() != dev or key.get_device() != dev
-            or value.get_device() != dev or seq_start.get_device() != dev):
-        _elsewhere("q out key value seq_start", q, out, key, value, seq_start)
+            or value.get_device() != dev or seq_start.get_device() != dev
+            or (workspace is not None and workspace.get_device() != dev)):
+        _elsewhere("q out key value seq_start workspace", q, out, key, value, seq_start, workspace)
     _check(lib().pa_prompt_attention_packed(_PROMPT.pack(
         out.data_ptr(), os_, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs,
         _dtype_code(q), _ptr(seq_start), n[0] - 1, T, max_seq_len, H, G, d, scale,
+        *((0, 0) if workspace is None else (_ptr(workspace), workspace.nbytes)),
         _stream(stream))))
 
 

@@ -43,5 +43,5 @@ extern "C" pa_status pa_prompt_attention_packed(const int64_t* a) {
                                at<const void>(a[4]), a[5], at<const void>(a[6]), a[7], type(a[8]),
                                at<const int32_t>(a[9]), i32(a[10]), i32(a[11]), i32(a[12]),
                                i32(a[13]), i32(a[14]), i32(a[15]), static_cast<float>(scale),
-                               at<void>(a[17]));
+                               at<void>(a[17]), static_cast<size_t>(a[18]), at<void>(a[19]));
 }

@@ -71,6 +71,8 @@ constexpr int kLaunchSeqs = 256;         // prompts a launch: finding a task rea
 constexpr int kMaxLen = 1 << 22;         // a task's products end well before a wait gives up
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyMax = 8.f;
+constexpr int kSpan = 64;                // key tiles whose products are summed in TMEM, with a workspace
+constexpr int kCtas = 152;               // that a workspace is sized for
 
 template <int D>
 struct Layout {
@@ -114,7 +116,17 @@ struct PromptParams {
     int tokens;                 // of a Q tile
     int max_chunks;             // tasks of the longest prompt and one KV head
     float scale_log2;
+    float* carry;               // sums of earlier spans, kept_floats() a CTA, or null: one span
 };
+
+// A CTA's part of the workspace: for either Q tile O as [column / 4][row][4], and the scale of
+// each row of it.
+constexpr int kept_floats(int head_dim) { return 2 * kRows * (head_dim + 1); }
+
+template <int D>
+__device__ __forceinline__ float* kept_sums(const PromptParams& p, int x) {
+    return p.carry + (int64_t)blockIdx.x * kept_floats(D) + x * (kept_floats(D) / 2);
+}
 
 // Tokens off .. len - 1 of the prompt that starts at token `start`: what is behind them does
 // not matter to the task. Chunks are counted back from the prompt's end, so that the one that
@@ -265,7 +277,9 @@ __device__ __forceinline__ int length_of(const PromptParams& p, int s, int& star
     return min(max(len, 0), min(p.max_len, p.num_tokens - start));
 }
 
-template <typename T, int D>
+// kCarry is its own variant: 64 wide, the registers it takes cost prompts too short for it 8 %
+// (16384 tokens: 1138 us against 1053); 128 wide, nothing.
+template <typename T, int D, bool kCarry>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q,
                             const __grid_constant__ CUtensorMap map_k,
@@ -375,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // rows past the tile's tokens or the prompt hold anything; they are not written
             const int bound = span.first + token;
             float m_run = -INFINITY, l_run = 0.f;
+            float kept_scale = 0.f;                          // of the sums of earlier spans
             bool ok = true;
             uint64_t l4[2], nm;
             // 32 keys' weights, from their scores to P
@@ -428,6 +443,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
                     pa::tc::st_8cols(o_tm + 8 * q, ov);
                 }
+            };
+            // The tensor cores cut off what does not fit when they add to O: 2.5e-3 of a sum of one
+            // sign over 524288 keys, 1.6e-4 over 32768. With a workspace O is added to the sums of
+            // earlier spans after every 64 tiles (in fp32, to nearest), and the products start anew.
+            auto keep = [&]() {
+                float4* const at = reinterpret_cast<float4*>(kept_sums<D>(p, x)) + row;
+#pragma unroll 1
+                for (int q = 0; q < D / 8; ++q) {
+                    uint32_t ov[8];
+                    pa::tc::ld_8cols(o_tm + 8 * q, ov);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float4 v = make_float4(
+                            __uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                            __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
+                        float4& sum = at[(2 * q + e) * kRows];
+                        if (kept_scale != 0.f) {
+                            const float4 old = sum;
+                            v.x = fmaf(old.x, kept_scale, v.x), v.y = fmaf(old.y, kept_scale, v.y);
+                            v.z = fmaf(old.z, kept_scale, v.z), v.w = fmaf(old.w, kept_scale, v.w);
+                        }
+                        sum = v;
+                    }
+                }
+                kept_scale = 1.f;
             };
             auto publish = [&](int half) {
                 pa::tc::wait_st();
@@ -484,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     pa::tc::fence_after_sync();
                 }
+                if (kCarry && t > 0 && t % kSpan == 0) keep();
                 if (key0 + kKeys - 1 > span.first) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mask(c[i], key0 + 32 * i);
@@ -511,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (moved) {
                             alpha = pa::ex2(m_run - mx);     // 0 while m_run is -inf
                             m_run = mx;
+                            kept_scale *= alpha;
                         }
                         // O may be scaled now: S of this tile was issued behind the last P V,
                         // and the barrier says that both are done; the next P V waits for this P
@@ -533,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n_o > 0 && !wait(LY::kOFree + x, (n_o - 1) & 1, pa::ERR_WAIT_EMPTY)) break;
             ++n_o;
             sums[x * kRows + row] = l_run;
+            if (kCarry) kept_sums<D>(p, x)[kRows * D + row] = kept_scale;
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(bar(LY::kLFull + x));
         }
@@ -564,6 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pa::tc::fence_after_sync();
                 const float l = sums[x * kRows + row];
                 const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float* const kept = kCarry ? kept_sums<D>(p, x) : nullptr;
+                const float kept_scale = kCarry ? kept[kRows * D + row] : 0.f;
                 const uint32_t o_tm = tmem + lane_at + LY::kOCol + D * x;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -571,6 +616,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pa::tc::ld_32cols_nowait(o_tm + c, o);
                     pa::tc::wait_ld();
                     pa::tc::loaded(o);
+                    if (kCarry && kept_scale != 0.f) {       // sums of earlier spans
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 v =
+                                reinterpret_cast<const float4*>(kept)[(c + e) / 4 * kRows + row];
+                            o[e] = __float_as_uint(fmaf(v.x, kept_scale, __uint_as_float(o[e])));
+                            o[e + 1] = __float_as_uint(fmaf(v.y, kept_scale, __uint_as_float(o[e + 1])));
+                            o[e + 2] = __float_as_uint(fmaf(v.z, kept_scale, __uint_as_float(o[e + 2])));
+                            o[e + 3] = __float_as_uint(fmaf(v.w, kept_scale, __uint_as_float(o[e + 3])));
+                        }
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint4 w;
@@ -708,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (ok && !more) pass_turn(turn);
                         ok = ok && wait_one(LY::kPFull + 2 * x, n_s & 1, pa::ERR_WAIT_FULL);
                         if (!ok) break;
-                        issue_pv(v, 0, steps, t > 0);
+                        issue_pv(v, 0, steps, t > 0 && !(kCarry && t % kSpan == 0));
                         ok = wait_one(LY::kPFull + 2 * x + 1, n_s & 1, pa::ERR_WAIT_FULL);
                         if (!ok) break;
                         issue_pv(v, 1, steps, true);
@@ -858,15 +914,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *abort_flag && p.err) atomicOr(p.err, *abort_flag);
 }
 
-template <typename T, int D>
-pa_status launch(const CUtensorMap* maps, PromptParams p, int64_t grid, cudaStream_t st) {
-    auto kern = prompt_attention_kernel<T, D>;
+template <typename T, int D, bool kCarry>
+pa_status launch_as(const CUtensorMap* maps, const PromptParams& p, int64_t grid, cudaStream_t st) {
+    auto kern = prompt_attention_kernel<T, D, kCarry>;
     static std::atomic<uint64_t> done{0};
     if (pa_status s = pa::allow_smem(kern, Layout<D>::kSmem, done, "prompt: shared memory size"))
         return s;
     return pa::cuda_status(pa::launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads),
                                           Layout<D>::kSmem, st, maps[0], maps[1], maps[2], p),
                            "prompt attention launch");
+}
+
+template <typename T, int D>
+pa_status launch(const CUtensorMap* maps, const PromptParams& p, int64_t grid, cudaStream_t st) {
+    return p.carry ? launch_as<T, D, true>(maps, p, grid, st)
+                   : launch_as<T, D, false>(maps, p, grid, st);
 }
 
 pa_status check_rows(const char* name, const void* rows, int64_t stride, int32_t heads,
@@ -883,13 +945,20 @@ pa_status check_rows(const char* name, const void* rows, int64_t stride, int32_t
 
 }  // namespace
 
+extern "C" size_t pa_prompt_attention_workspace_size(int32_t head_dim, int32_t max_seq_len) {
+    if ((head_dim != 64 && head_dim != 128) || max_seq_len <= kSpan * kKeys || max_seq_len > kMaxLen)
+        return 0;
+    return sizeof(float) * kept_floats(head_dim) * kCtas;
+}
+
 extern "C" pa_status pa_prompt_attention(void* out, int64_t out_stride, const void* q,
                                          int64_t q_stride, const void* key, int64_t key_stride,
                                          const void* value, int64_t value_stride, pa_dtype dtype,
                                          const int32_t* seq_start, int32_t num_seqs,
                                          int32_t num_tokens, int32_t max_seq_len,
                                          int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
-                                         float scale, void* stream) {
+                                         float scale, void* workspace, size_t workspace_bytes,
+                                         void* stream) {
     using pa::fail;
     if (num_seqs < 0 || num_tokens < 0)
         return fail(PA_ERR_INVALID_ARG, "num_seqs %d, num_tokens %d", num_seqs, num_tokens);
@@ -914,6 +983,15 @@ extern "C" pa_status pa_prompt_attention(void* out, int64_t out_stride, const vo
     if (pa_status s = check_rows("key", key, key_stride, num_kv_heads, head_dim)) return s;
     if (pa_status s = check_rows("value", value, value_stride, num_kv_heads, head_dim)) return s;
     if (pa_status s = check_rows("out", out, out_stride, num_heads, head_dim)) return s;
+    if (workspace && (uintptr_t)workspace % 16)
+        return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    const int64_t own = sizeof(float) * kept_floats(head_dim);   // a CTA's part of it
+    const bool carry = max_seq_len > kSpan * kKeys && workspace;
+    if (carry && (int64_t)workspace_bytes < own)
+        return fail(PA_ERR_INVALID_ARG, "workspace of %zu bytes (%zu serve every SM)", workspace_bytes,
+                    pa_prompt_attention_workspace_size(head_dim, max_seq_len));
+    if (!workspace && max_seq_len > (dtype == PA_F16 ? 1 << 16 : 1 << 19))
+        return fail(PA_ERR_INVALID_ARG, "prompts of up to %d tokens need a workspace", max_seq_len);
     cudaStream_t st = (cudaStream_t)stream;
     if (pa::validate_enabled())
         if (pa_status s = pa::validate_starts(seq_start, num_seqs, num_tokens, max_seq_len, st))
@@ -934,6 +1012,7 @@ extern "C" pa_status pa_prompt_attention(void* out, int64_t out_stride, const vo
     p.tokens = kRows / group;
     const int per_task = 2 * p.tokens;
     p.max_chunks = (max_seq_len + per_task - 1) / per_task;
+    p.carry = carry ? static_cast<float*>(workspace) : nullptr;
     // not 0: a masked score of -inf stays one (a score of 2^100 still has a weight of 1)
     p.scale_log2 = fmaxf(scale * kLog2e, FLT_MIN);
     CUtensorMap maps[3];
@@ -954,7 +1033,8 @@ extern "C" pa_status pa_prompt_attention(void* out, int64_t out_stride, const vo
                                         (int64_t)num_tokens / per_task + p.num_seqs);
         if (chunks * num_kv_heads > 0x7fffffff)
             return fail(PA_ERR_UNSUPPORTED, "too many rows for one launch");
-        const int64_t grid = std::min<int64_t>(sms, chunks * num_kv_heads);
+        int64_t grid = std::min<int64_t>(sms, chunks * num_kv_heads);
+        if (carry) grid = std::min(grid, (int64_t)workspace_bytes / own);
         pa_status s;
         if (dtype == PA_BF16)
             s = head_dim == 128 ? launch<__nv_bfloat16, 128>(maps, p, grid, st)

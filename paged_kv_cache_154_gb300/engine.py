@@ -22,7 +22,8 @@ import torch
 from . import (BLOCK_SIZE, INT4_GROUP, Pool, accumulate_weights,
                accumulate_weights_workspace_size, append_kv, copy_blocks, decode,
                decode_shared_prefix, decode_shared_prefix_workspace_size, decode_workspace_size,
-               evict_select, move_tokens, prompt_attention, rope_append_kv, zeroed_workspace)
+               evict_select, move_tokens, prompt_attention, prompt_attention_workspace_size,
+               rope_append_kv, zeroed_workspace)
 
 KV_TORCH = {"f16": torch.float16, "bf16": torch.bfloat16, "int8": torch.int8,
             "fp8": torch.float8_e4m3fn, "int4": torch.uint8}
@@ -232,9 +233,9 @@ class PagedKVCache:
                     [L - r + self.pool.evicted.get(s, 0) + np.arange(r)
                      for s, L, r in zip(seqs, lens, q_lens)])
             positions = torch.as_tensor(positions, dtype=torch.int32).to(dev).contiguous()
-        ws_bytes = 0 if prompt else decode_workspace_size(
-            len(seqs), nq, q.shape[1], self.num_kv_heads, q.shape[2], max(q_lens), max(lens),
-            partition_size)
+        ws_bytes = (prompt_attention_workspace_size(q.shape[2], max(q_lens)) if prompt else
+                    decode_workspace_size(len(seqs), nq, q.shape[1], self.num_kv_heads, q.shape[2],
+                                          max(q_lens), max(lens), partition_size))
         shared = None
         if shared_prefix:
             gs, pl = self.pool.prefix_groups(seqs, q_lens)
@@ -284,7 +285,8 @@ class PagedKVCache:
         prompts over their own rows. Rotated queries are those that write_step left."""
         if si.prompt_start is not None:
             key = si.key if si.key_rotated is None else si.key_rotated
-            prompt_attention(si.out, _queries(si), key, si.value, si.prompt_start, si.max_q_len, scale)
+            prompt_attention(si.out, _queries(si), key, si.value, si.prompt_start, si.max_q_len,
+                             scale, si.workspace)
             return si.out
         if si.shared is not None:
             sp = si.shared

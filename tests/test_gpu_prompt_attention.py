@@ -239,3 +239,64 @@ def test_validation_names_the_prompt(monkeypatch):
                                 torch.tensor(s, dtype=torch.int32, device="cuda"), 8, 0.1)
     pa.prompt_attention(torch.empty_like(q), q, k, v, starts([4, 6]), 8, 0.1)
     assert pa.device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_of_long_prompts(d):
+    """With a workspace the weighted sums of values of one sign stay as near to the 64-bit
+    ones over 131072 keys as over a few; the workspace holds NaN before, serves calls of other
+    lengths, and a part for 7 CTAs serves too. Tolerance: a span of 8192 keys is 512 sums of
+    16, each cut off by a step of 24 bits at most, 2^-23 of what is there so far: 512 * 2^-23 =
+    6.1e-5 of a span's sum. The mean over d columns also holds the rounding of the outputs,
+    which lie around 1: 2^-10 / sqrt(12 * 64) a standard deviation of it, 4 of them 1.4e-4."""
+    T, H = 131072, 2
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    q, k = ((torch.randn((T, n, d), device="cuda", generator=gen) * 0.3).half() for n in (H, 1))
+    v = (torch.rand((T, 1, d), device="cuda", generator=gen) + 0.5).half()
+    n = pa.prompt_attention_workspace_size(d, T)
+    start = torch.tensor([0, 5000, T], dtype=torch.int32, device="cuda")
+    outs = []
+    for size in (n, 7 * n // 152):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(q)
+        for _ in range(2):
+            pa.prompt_attention(out, q, k, v, start, T, d ** -0.5, ws)
+        outs.append(out)
+    assert pa.device_error() == 0
+    assert torch.equal(*outs)
+    short = torch.empty_like(q[:5000])
+    pa.prompt_attention(short, q[:5000], k[:5000], v[:5000], start[:2], 5000, d ** -0.5)
+    assert torch.equal(outs[0][:5000], short)
+    for row in (5000 + 8191, 5000 + 8192, 90000, T - 1):
+        s = (q[row].double() @ k[5000:row + 1, 0].double().t()) * d ** -0.5
+        want = torch.softmax(s, -1) @ v[5000:row + 1, 0].double()
+        off = (outs[0][row].double() - want) / want
+        # an output: its rounding, and at most as much of every weight's
+        assert off.abs().max() < 2.0 ** -10 + 6.1e-5
+        assert abs(off.mean().item()) < 6.1e-5 + 1.4e-4
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_kept_sums_follow_the_maximum(d):
+    """Scores that rise over several spans, so that the sums of earlier ones are scaled, and
+    that fall, so that they outweigh the later ones."""
+    T = 20000
+    q, k, v = make(15, T, 2, 1, d, torch.bfloat16, False)
+    ws = torch.full((pa.prompt_attention_workspace_size(d, T),), 255, dtype=torch.uint8,
+                    device="cuda")
+    for sign in (1.0, -1.0):
+        k2, q2 = k.clone() * 0.2, q.clone() * 0.2
+        k2[..., :1] = (torch.linspace(0, 40, T, device="cuda")[:, None, None] * sign).to(k.dtype)
+        q2[..., :1] = 0.6 * d ** 0.5
+        out = torch.empty_like(q)
+        pa.prompt_attention(out, q2, k2, v, starts([T]), T, d ** -0.5, ws)
+        assert pa.device_error() == 0
+        eps = torch.finfo(torch.bfloat16).eps / 2
+        for row in (8191, 8192, 8193, 13000, 16384, T - 1):
+            s = (q2[row].double() @ k2[:row + 1, 0].double().t()) * d ** -0.5
+            w, x = torch.softmax(s, -1), v[:row + 1, 0].double()
+            want, size = w @ x, w @ x.abs()
+            # scores up to 24, sums of d terms and the power: 24 * 132 * 2^-24 = 1.9e-4 of a
+            # weight; the sums of products 6.1e-5
+            tol = (eps + 2.6e-4 + 2.0 ** -21) * size * (1 + eps) + eps * want.abs() + 2.0 ** -24
+            assert ((out[row].double() - want).abs() <= tol).all()

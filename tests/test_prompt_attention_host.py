@@ -18,14 +18,14 @@ def built():
 
 A, ODD = 0x10000, 0x10004
 CALL = dict(out=A, os=1024, q=A, qs=1024, k=A, ks=256, v=A, vs=256, dt=pa.PA_BF16, start=A, S=2,
-            T=9, ml=8, H=8, G=2, d=128, scale=0.1, st=None)
+            T=9, ml=8, H=8, G=2, d=128, scale=0.1, ws=None, wb=0, st=None)
 
 
 def status(**change):
     """The call's status, which the packed form of it shares."""
     values = [change.get(n, CALL[n]) for n in CALL]
     got = pa.lib().pa_prompt_attention(*values)
-    words = struct.pack("16qdq", *[v or 0 for v in values])
+    words = struct.pack("16qd3q", *[v or 0 for v in values])
     assert pa.lib().pa_prompt_attention_packed(words) == got
     return got
 
@@ -36,9 +36,11 @@ def status(**change):
     (dict(H=7), 1), (dict(G=0), 1), (dict(H=0), 1), (dict(H=129, G=1, qs=1 << 20, os=1 << 20), 2),
     (dict(ml=0), 1), (dict(ml=(1 << 22) + 1), 2), (dict(scale=-1.0), 1),
     (dict(scale=float("nan")), 1), (dict(scale=3e38), 1),
-    (dict(H=65536, G=65536, qs=1 << 30, os=1 << 30, ks=1 << 30, vs=1 << 30), 2), (dict(scale=float("inf")), 1), (dict(out=ODD), 1),
-    (dict(q=ODD), 1), (dict(k=ODD), 1), (dict(v=ODD), 1), (dict(qs=1016), 1), (dict(os=1028), 1),
-    (dict(ks=248), 1), (dict(vs=-256), 1), (dict(ks=1 << 38), 2)])
+    (dict(H=65536, G=65536, qs=1 << 30, os=1 << 30, ks=1 << 30, vs=1 << 30), 2),
+    (dict(scale=float("inf")), 1), (dict(out=ODD), 1), (dict(q=ODD), 1), (dict(k=ODD), 1), (dict(v=ODD), 1), (dict(qs=1016), 1), (dict(os=1028), 1),
+    (dict(ks=248), 1), (dict(vs=-256), 1), (dict(ks=1 << 38), 2), (dict(ws=ODD, wb=1 << 30), 1),
+    (dict(ws=A, wb=1024, ml=8193), 1), (dict(ml=(1 << 19) + 1), 1),
+    (dict(dt=pa.PA_F16, ml=(1 << 16) + 1), 1)])
 def test_refusals(change, want):
     assert status(**change) == want
     assert pa.lib().pa_last_error()
@@ -47,6 +49,14 @@ def test_refusals(change, want):
 def test_empty_calls_are_accepted():
     assert status(S=0, q=None) == 0
     assert status(T=0, q=None) == 0
+
+
+def test_workspace_size():
+    assert pa.prompt_attention_workspace_size(128, 8192) == 0
+    assert pa.prompt_attention_workspace_size(96, 9000) == 0
+    assert pa.prompt_attention_workspace_size(64, (1 << 22) + 1) == 0
+    for d in (64, 128):
+        assert pa.prompt_attention_workspace_size(d, 8193) == 152 * 2 * 128 * (d + 1) * 4
 
 
 def test_binding():
