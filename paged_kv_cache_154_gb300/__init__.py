@@ -574,8 +574,8 @@ def rope_append_kv(q_out, q, key, value, k_cache, v_cache, slot_mapping, cos_sin
     _check(lib().pa_rope_append_kv_packed(_ROPE_APPEND.pack(
         qop, qos, qp, qs, H, kop, kos, key.data_ptr(), ks, value.data_ptr(), vs, _dtype_code(key),
         _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale) or 0, _ptr(v_scale) or 0, _ptr(k_zp) or 0,
-        _ptr(v_zp) or 0, _ptr(slot_mapping), _ptr(cos_sin), most, rd, 1 if interleaved else 0, _ptr(positions),
-        axes, _ptr(freq_axis) or 0, T, nb, G, d, shape[2], _stream(stream))))
+        _ptr(v_zp) or 0, _ptr(slot_mapping), _ptr(cos_sin), most, rd, 1 if interleaved else 0,
+        _ptr(positions), axes, _ptr(freq_axis) or 0, T, nb, G, d, shape[2], _stream(stream))))
 
 
 def prompt_attention_workspace_size(head_dim: int, max_seq_len: int) -> int:

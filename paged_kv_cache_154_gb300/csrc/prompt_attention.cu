@@ -29,7 +29,7 @@
 //
 // What bounds it. head_dim 128: the tensor cores, 2048 of about 2250 cycles of a
 // step (two Q tiles against 128 keys). One prompt of 8192 tokens, 32 heads over 8:
-// 323 us, 1700 TFLOP/s; of 32768: 5.5 ms, 1600 TFLOP/s, at the power limit.
+// 325 us, 1690 TFLOP/s; of 32768: 5.3 ms, 1670 TFLOP/s, at the power limit.
 // head_dim 64: the softmax, 2200 cycles a step of which the products need 1024; the
 // two warps of a quarter need 1100 for arithmetic alone (exponentials 1024), the
 // rest are loads from TMEM and barriers. 16384 tokens, 32 heads over 8: 1.05 ms,
@@ -273,8 +273,8 @@ __device__ __forceinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint3
 // Length of prompt s, cut to what the tensors hold.
 __device__ __forceinline__ int length_of(const PromptParams& p, int s, int& start) {
     start = min(max(__ldg(p.start + s), 0), p.num_tokens);
-    const int len = __ldg(p.start + s + 1) - start;
-    return min(max(len, 0), min(p.max_len, p.num_tokens - start));
+    const int end = min(max(__ldg(p.start + s + 1), 0), p.num_tokens);
+    return min(max(end - start, 0), p.max_len);
 }
 
 // kCarry is its own variant: 64 wide, the registers it takes cost prompts too short for it 8 %

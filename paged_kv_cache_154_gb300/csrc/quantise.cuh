@@ -18,7 +18,8 @@ __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) {
 }
 
 // Two fp32 numbers and the two-wide arithmetic on them (each operation rounds
-// as its scalar form does).
+// as its scalar form does, but a product that is only added to may be fused
+// with the sum).
 struct F2 {
     uint64_t v;
     __device__ __forceinline__ F2() {}
