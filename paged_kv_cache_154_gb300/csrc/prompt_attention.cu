@@ -423,10 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto mask = [&](uint32_t (&c)[32], int key0) {   // keys that a row must not see
                 if (key0 + 31 > span.first) {
-                    const int last = bound - key0;
+                    const int last = bound - key0;           // bits 0 .. last stay
+                    const uint32_t seen = last < 0 ? 0u : 0xffffffffu >> (31 - min(last, 31));
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (j > last) c[j] = 0xff800000u;    // -inf
+                        if (!(seen >> j & 1)) c[j] = 0xff800000u;    // -inf
                 }
             };
             auto reference = [&]() {
@@ -720,58 +721,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return true;
                 };
-                Task task;
-                bool ok = true;
-                for (int i = 0; ok && read_task_one(i, task); ++i) {
+                Task task, after;
+                bool ok = true, go = read_task_one(0, task);
+                // One place for each product, and the next task read while this one's last P is
+                // waited for: code that runs once a task has left the instruction caches.
+                for (int i = 0; ok && go; ++i, task = after) {
                     const bool two = task.len - task.off > tokens;
                     const int tiles = Span(task, tokens, two ? 1 : 0).tiles;
                     if (x == 1 && !two) {
                         ok = pass_on(2 * tiles);
+                        go = read_task_one(i + 1, after);
                         continue;
                     }
                     const Span s(task, tokens, x);
-                    const int both = two ? Span(task, tokens, 0).tiles : 0;   // tiles of either
-                    ok = wait_one(LY::kKVFull + kv.slot, kv.phase, pa::ERR_WAIT_FULL) &&
-                         wait_one(LY::kQFull + x, n_q & 1, pa::ERR_WAIT_FULL) && my_turn(two);
-                    if (!ok) break;
-                    issue_qk(two);
-                    for (int t = 0; t < s.tiles; ++t, ++n_s) {
-                        const Ring<kStages> v = kv, next = kv.next();
+                    const int both = two ? Span(task, tokens, 0).tiles : -1;  // tiles of either
+#pragma unroll 1
+                    for (int t = -1; t < s.tiles; ++t) {     // S of tile t + 1, O of tile t
+                        const Ring<kStages> v = kv, next = t < 0 ? kv : kv.next();
                         const bool more = t + 1 < s.tiles, turn = t < both;
                         if (LY::kApart && more) {
                             // the next S, once this one has been read
                             ok = wait_one(LY::kKVFull + next.slot, next.phase, pa::ERR_WAIT_FULL) &&
-                                 wait_one(LY::kSFree + x, n_s & 1, pa::ERR_WAIT_FULL);
+                                 wait_one(t < 0 ? LY::kQFull + x : LY::kSFree + x,
+                                          (t < 0 ? n_q : n_s) & 1, pa::ERR_WAIT_FULL);
                             if (!ok) break;
                             kv = next;
                             issue_qk(false);
                         }
+                        if (LY::kApart && t < 0) continue;
                         if (!more) pa::tc::commit(bar(LY::kQEmpty + x));
-                        // this V tile, the next K tile, and O of the last task read
+                        // this V tile and the next K tile, or the first K tile and Q
                         ok = wait_one(LY::kKVFull + v.slot, v.phase, pa::ERR_WAIT_FULL);
                         if (!LY::kApart && more)
-                            ok = ok && wait_one(LY::kKVFull + next.slot, next.phase, pa::ERR_WAIT_FULL);
-                        if (t == 0 && n_q > 0)
+                            ok = ok && (t < 0 ? wait_one(LY::kQFull + x, n_q & 1, pa::ERR_WAIT_FULL)
+                                              : wait_one(LY::kKVFull + next.slot, next.phase,
+                                                         pa::ERR_WAIT_FULL));
+                        if (t == 0 && n_q > 0)               // O of the last task read
                             ok = ok && wait_one(LY::kOFree + x, (n_q - 1) & 1, pa::ERR_WAIT_EMPTY);
                         if (!more && x == 1 && first_cleans(task)) {
                             ok = ok && wait_one(LY::kClean + v.slot, (cleaned >> v.slot) & 1,
                                                 pa::ERR_WAIT_FULL);
                             cleaned ^= 1u << v.slot;
                         }
-                        const int steps = (s.keys - t * kKeys + 15) >> 4;
                         ok = ok && my_turn(turn);
-                        // the other one's next products need not wait for this task's last P
-                        if (ok && !more) pass_turn(turn);
-                        ok = ok && wait_one(LY::kPFull + 2 * x, n_s & 1, pa::ERR_WAIT_FULL);
                         if (!ok) break;
-                        issue_pv(v, 0, steps, t > 0 && !(kCarry && t % kSpan == 0));
-                        ok = wait_one(LY::kPFull + 2 * x + 1, n_s & 1, pa::ERR_WAIT_FULL);
-                        if (!ok) break;
-                        issue_pv(v, 1, steps, true);
-                        if (LY::kApart) pa::tc::commit(bar(LY::kODone + x));
-                        if (!more) pa::tc::commit(bar(LY::kOFull + x));
-                        pa::tc::commit(bar(LY::kKVEmpty + v.slot));
-                        if (!LY::kApart || !more) kv = next;
+                        if (!more) {
+                            // the other one's next products need not wait for this task's last P
+                            pass_turn(turn);
+                            go = read_task_one(i + 1, after);
+                        }
+                        if (t >= 0) {
+                            const int steps = (s.keys - t * kKeys + 15) >> 4;
+                            ok = wait_one(LY::kPFull + 2 * x, n_s & 1, pa::ERR_WAIT_FULL);
+                            if (!ok) break;
+                            issue_pv(v, 0, steps, t > 0 && !(kCarry && t % kSpan == 0));
+                            ok = wait_one(LY::kPFull + 2 * x + 1, n_s & 1, pa::ERR_WAIT_FULL);
+                            if (!ok) break;
+                            issue_pv(v, 1, steps, true);
+                            if (LY::kApart) pa::tc::commit(bar(LY::kODone + x));
+                            if (!more) pa::tc::commit(bar(LY::kOFull + x));
+                            pa::tc::commit(bar(LY::kKVEmpty + v.slot));
+                            if (!LY::kApart || !more) kv = next;
+                            ++n_s;
+                        }
                         if (!LY::kApart && more) issue_qk(turn);
                     }
                     ok = ok && pass_on(2 * (tiles - s.tiles));
