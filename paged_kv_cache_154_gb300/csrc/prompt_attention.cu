@@ -25,11 +25,11 @@
 //                    has the other's products to run in
 //   warp 13          TMA: Q tiles, K and V tiles into a ring
 //   warp 14          finds the tasks
-// Every wait is bounded; one that gives up ends every role's loop.
+// Every wait is bounded: when the tasks stop being read, warp 14 ends every role's loop.
 //
 // What bounds it. head_dim 128: the tensor cores, 2048 of about 2250 cycles of a
 // step (two Q tiles against 128 keys). One prompt of 8192 tokens, 32 heads over 8:
-// 325 us, 1690 TFLOP/s; of 32768: 5.3 ms, 1670 TFLOP/s, at the power limit.
+// 318 us, 1730 TFLOP/s; of 32768: 5.2 ms, 1690 TFLOP/s, at the power limit.
 // head_dim 64: the softmax, 2200 cycles a step of which the products need 1024; the
 // two warps of a quarter need 1100 for arithmetic alone (exponentials 1024), the
 // rest are loads from TMEM and barriers. 16384 tokens, 32 heads over 8: 1.05 ms,
@@ -37,8 +37,10 @@
 // at 128 (1.08 ms), four softmax warpgroups of half a tile's keys each (1.23 ms),
 // halves of a tile one after another with the next one's maximum beside them (1.20
 // ms), turns at the exponentials (1.18 ms).
-// Short prompts: a task costs about 7000 cycles besides its steps (its first tile
-// finds both softmaxes idle). 16 of 200 to 2000 tokens: 137 us, 1140 TFLOP/s.
+// Short prompts: a task costs about 6000 cycles besides its steps: its first tile
+// finds both softmaxes idle, its last is masked, and code that runs once a task comes
+// from beyond the instruction caches (53 KB of code in all: 138 us, 46 KB: 128). 16
+// prompts of 200 to 2000 tokens: 128 us, 1220 TFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -114,6 +116,7 @@ struct PromptParams {
     int num_kv_heads;
     int group;
     int tokens;                 // of a Q tile
+    unsigned per_task_inv;      // 2^32 / (2 tokens) + 1
     int max_chunks;             // tasks of the longest prompt and one KV head
     float scale_log2;
     float* carry;               // sums of earlier spans, kept_floats() a CTA, or null: one span
@@ -247,8 +250,18 @@ struct Ring {
 };
 
 // The rest of a wait whose first look failed, in few instructions (the roles' code takes turns
-// in the instruction caches): false once it has lasted kWaitNs, counted in cycles of 2 GHz, or
-// another one has. The flag holds the error that ends the kernel.
+// in the instruction caches): false once the abort flag is set, which holds the error that ends
+// the kernel. The scheduler's warp sets it, whose waits alone are timed: no role goes without
+// reading the record that ends the tasks, and the scheduler waits for that.
+__device__ __forceinline__ bool wait_longer(uint32_t bar, uint32_t parity,
+                                            volatile uint32_t* abort_flag) {
+#pragma unroll 1
+    while (!pa::mbar_try_wait(bar, parity))
+        if (*abort_flag != 0) return false;
+    return true;
+}
+
+// A timed one: sets the flag after kWaitNs, counted in cycles of 2 GHz.
 constexpr uint32_t kWaitClocks = pa::kWaitNs < 1000000000ull ? (uint32_t)(2 * pa::kWaitNs) : 2000000000u;
 
 __device__ __forceinline__ uint32_t cycles() {
@@ -256,17 +269,15 @@ __device__ __forceinline__ uint32_t cycles() {
     asm volatile("mov.u32 %0, %%clock;" : "=r"(c));
     return c;
 }
-__device__ __forceinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t code,
-                                            volatile uint32_t* abort_flag) {
+__device__ __forceinline__ bool wait_timed(uint32_t bar, uint32_t parity,
+                                           volatile uint32_t* abort_flag) {
     const uint32_t began = cycles();
 #pragma unroll 1
-    while (!pa::mbar_try_wait(bar, parity)) {
-        if (*abort_flag != 0) return false;
+    while (!pa::mbar_try_wait(bar, parity))
         if (cycles() - began > kWaitClocks) {
-            *abort_flag = code;
+            *abort_flag = pa::ERR_WAIT_FULL;
             return false;
         }
-    }
     return true;
 }
 
@@ -330,12 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     pa::grid_dependency_wait();
 
     // a wait by one lane, or by the whole warp; false ends the role
-    auto wait_one = [&](int b, uint32_t parity, uint32_t code) -> bool {
+    auto wait_one = [&](int b, uint32_t parity) -> bool {
         if (pa::mbar_try_wait(bar(b), parity)) return true;
-        return wait_longer(bar(b), parity, code, abort_flag);
+        return wait_longer(bar(b), parity, abort_flag);
     };
-    auto wait = [&](int b, uint32_t parity, uint32_t code) -> bool {
-        return __all_sync(0xffffffffu, wait_one(b, parity, code));
+    auto wait = [&](int b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait_one(b, parity));
     };
     // what has to have ended before the CTA goes, also after a wait gave up
     auto drain = [&](int b, uint32_t parity) {
@@ -343,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // the i-th task of this CTA
     auto read_task = [&](int i, Task& t) -> bool {
-        if (!wait(LY::kTaskFull + (i & 1), (i >> 1) & 1, pa::ERR_WAIT_FULL)) return false;
+        if (!wait(LY::kTaskFull + (i & 1), (i >> 1) & 1)) return false;
         volatile Task& r = tasks[i & 1];
         t.start = r.start, t.len = r.len, t.off = r.off, t.head_last = r.head_last;
         __syncwarp();
@@ -351,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return t.head_last >= 0;
     };
     auto read_task_one = [&](int i, Task& t) -> bool {
-        if (!wait_one(LY::kTaskFull + (i & 1), (i >> 1) & 1, pa::ERR_WAIT_FULL)) return false;
+        if (!wait_one(LY::kTaskFull + (i & 1), (i >> 1) & 1)) return false;
         volatile Task& r = tasks[i & 1];
         t.start = r.start, t.len = r.len, t.off = r.off, t.head_last = r.head_last;
         pa::mbar_arrive(bar(LY::kTaskEmpty + (i & 1)));
@@ -485,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return true;
                 Ring<kStages> v = kv;
                 v.advance(2 * span.tiles - 1);
-                if (!wait(LY::kKVFull + v.slot, v.phase, pa::ERR_WAIT_FULL)) return false;
+                if (!wait(LY::kKVFull + v.slot, v.phase)) return false;
                 const int z0 = task.len - (span.tiles - 1) * kKeys;
                 const int n = (((span.keys + 15) & ~15) - task.len) * (D / 8);
                 for (int e = row; e < n; e += kRows) {
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
 
             for (int t = 0; t < span.tiles; ++t, ++n_s) {
-                ok = wait(LY::kSFull + x, n_s & 1, pa::ERR_WAIT_FULL);
+                ok = wait(LY::kSFull + x, n_s & 1);
                 if (!ok) break;
                 pa::tc::fence_after_sync();
                 const int key0 = t * kKeys;
@@ -521,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pa::tc::fence_before_sync();
                     __syncwarp();
                     arrive_if(bar(LY::kSFree + x), lane == 0);
-                    if (n_s > 0) ok = wait(LY::kODone + x, (n_s - 1) & 1, pa::ERR_WAIT_FULL);
+                    if (n_s > 0) ok = wait(LY::kODone + x, (n_s - 1) & 1);
                     if (!ok) break;
                     pa::tc::fence_after_sync();
                 }
@@ -573,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             kv.advance(2 * all.tiles);
             // the sums of the last task have been read
-            if (n_o > 0 && !wait(LY::kOFree + x, (n_o - 1) & 1, pa::ERR_WAIT_EMPTY)) break;
+            if (n_o > 0 && !wait(LY::kOFree + x, (n_o - 1) & 1)) break;
             ++n_o;
             sums[x * kRows + row] = l_run;
             if (kCarry) kept_sums<D>(p, x)[kRows * D + row] = kept_scale;
@@ -601,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     token < tokens && at < task.len
                         ? ((int64_t)(task.start + at) * p.out_stride + (task.head() * G + head) * D) / 8
                         : -1;
-                ok = wait(LY::kLFull + x, (parity >> x) & 1, pa::ERR_WAIT_FULL) &&
-                     wait(LY::kOFull + x, (parity >> x) & 1, pa::ERR_WAIT_FULL);
+                ok = wait(LY::kLFull + x, (parity >> x) & 1) &&
+                     wait(LY::kOFull + x, (parity >> x) & 1);
                 if (!ok) break;
                 parity ^= 1u << x;
                 pa::tc::fence_after_sync();
@@ -683,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t turns = 0;
                 auto my_turn = [&](bool two) -> bool {
                     return LY::kApart || !two ||
-                           wait_one(LY::kTurn + x, (turns++ & 1) ^ (x ^ 1), pa::ERR_WAIT_FULL);
+                           wait_one(LY::kTurn + x, (turns++ & 1) ^ (x ^ 1));
                 };
                 auto pass_turn = [&](bool two) {
                     if (!LY::kApart && two) pa::mbar_arrive(bar(LY::kTurn + (x ^ 1)));
@@ -715,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 auto pass_on = [&](int n) -> bool {          // tiles that only the other one reads
                     for (int k = 0; k < n; ++k) {
-                        if (!wait_one(LY::kKVFull + kv.slot, kv.phase, pa::ERR_WAIT_FULL)) return false;
+                        if (!wait_one(LY::kKVFull + kv.slot, kv.phase)) return false;
                         pa::mbar_arrive(bar(LY::kKVEmpty + kv.slot));
                         kv = kv.next();
                     }
@@ -741,9 +752,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool more = t + 1 < s.tiles, turn = t < both;
                         if (LY::kApart && more) {
                             // the next S, once this one has been read
-                            ok = wait_one(LY::kKVFull + next.slot, next.phase, pa::ERR_WAIT_FULL) &&
+                            ok = wait_one(LY::kKVFull + next.slot, next.phase) &&
                                  wait_one(t < 0 ? LY::kQFull + x : LY::kSFree + x,
-                                          (t < 0 ? n_q : n_s) & 1, pa::ERR_WAIT_FULL);
+                                          (t < 0 ? n_q : n_s) & 1);
                             if (!ok) break;
                             kv = next;
                             issue_qk(false);
@@ -751,16 +762,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (LY::kApart && t < 0) continue;
                         if (!more) pa::tc::commit(bar(LY::kQEmpty + x));
                         // this V tile and the next K tile, or the first K tile and Q
-                        ok = wait_one(LY::kKVFull + v.slot, v.phase, pa::ERR_WAIT_FULL);
+                        ok = wait_one(LY::kKVFull + v.slot, v.phase);
                         if (!LY::kApart && more)
-                            ok = ok && (t < 0 ? wait_one(LY::kQFull + x, n_q & 1, pa::ERR_WAIT_FULL)
-                                              : wait_one(LY::kKVFull + next.slot, next.phase,
-                                                         pa::ERR_WAIT_FULL));
+                            ok = ok && (t < 0 ? wait_one(LY::kQFull + x, n_q & 1)
+                                              : wait_one(LY::kKVFull + next.slot, next.phase));
                         if (t == 0 && n_q > 0)               // O of the last task read
-                            ok = ok && wait_one(LY::kOFree + x, (n_q - 1) & 1, pa::ERR_WAIT_EMPTY);
+                            ok = ok && wait_one(LY::kOFree + x, (n_q - 1) & 1);
                         if (!more && x == 1 && first_cleans(task)) {
-                            ok = ok && wait_one(LY::kClean + v.slot, (cleaned >> v.slot) & 1,
-                                                pa::ERR_WAIT_FULL);
+                            ok = ok && wait_one(LY::kClean + v.slot, (cleaned >> v.slot) & 1);
                             cleaned ^= 1u << v.slot;
                         }
                         ok = ok && my_turn(turn);
@@ -772,10 +781,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (t >= 0) {
                             const int steps = (s.keys - t * kKeys + 15) >> 4;
-                            ok = wait_one(LY::kPFull + 2 * x, n_s & 1, pa::ERR_WAIT_FULL);
+                            ok = wait_one(LY::kPFull + 2 * x, n_s & 1);
                             if (!ok) break;
                             issue_pv(v, 0, steps, t > 0 && !(kCarry && t % kSpan == 0));
-                            ok = wait_one(LY::kPFull + 2 * x + 1, n_s & 1, pa::ERR_WAIT_FULL);
+                            ok = wait_one(LY::kPFull + 2 * x + 1, n_s & 1);
                             if (!ok) break;
                             issue_pv(v, 1, steps, true);
                             if (LY::kApart) pa::tc::commit(bar(LY::kODone + x));
@@ -806,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int tiles = Span(task, tokens, nq - 1).tiles;
                     auto load = [&](int k) -> bool {         // the task's k-th K (even) or V tile
                         if (loaded >= kStages &&
-                            !wait_one(LY::kKVEmpty + kv.slot, kv.phase ^ 1, pa::ERR_WAIT_EMPTY))
+                            !wait_one(LY::kKVEmpty + kv.slot, kv.phase ^ 1))
                             return false;
                         const uint32_t b = bar(LY::kKVFull + kv.slot);
                         pa::mbar_arrive_expect_tx(b, LY::kTile);
@@ -828,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; ok && x < nq; ++x) {
                         // Q of the last task has been read
                         if (n_q[x] > 0)
-                            ok = wait_one(LY::kQEmpty + x, (n_q[x] - 1) & 1, pa::ERR_WAIT_EMPTY);
+                            ok = wait_one(LY::kQEmpty + x, (n_q[x] - 1) & 1);
                         if (!ok) break;
                         const uint32_t b = bar(LY::kQFull + x);
                         pa::mbar_arrive_expect_tx(b, q_bytes * LY::kHalves);
@@ -857,9 +866,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // max(0, n_s - c) of them have a place of c or more: the chunk of task v is the
             // c with F(c + 1) <= v < F(c), its prompt the (v - F(c + 1))-th with n_s > c.
             const int per_task = 2 * tokens;
+            auto chunks = [&](int len) -> int {              // ceil(len / per_task), len < 2^23
+                return (int)__umulhi((unsigned)(len + per_task - 1), p.per_task_inv);
+            };
             auto chunks_of = [&](int s) -> int {
                 int start;
-                return s < p.num_seqs ? (length_of(p, s, start) + per_task - 1) / per_task : 0;
+                return s < p.num_seqs ? chunks(length_of(p, s, start)) : 0;
             };
             const int n = chunks_of(lane);                   // further prompts' are read as needed
             auto at_least = [&](int c) -> unsigned {
@@ -869,22 +881,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum += (unsigned)max(0, chunks_of(s + lane) - c);
                 return __reduce_add_sync(0xffffffffu, sum);
             };
-            const unsigned all = at_least(0);
             const unsigned P = gridDim.x;
+            // every role has read record i, or the flag is set
+            auto all_read = [&](unsigned i) -> bool {
+                return __all_sync(0xffffffffu, wait_timed(bar(LY::kTaskEmpty + (i & 1)), (i >> 1) & 1,
+                                                          abort_flag));
+            };
             for (unsigned i = 0;; ++i) {
                 const unsigned v = i * P + (i & 1 ? P - 1 - blockIdx.x : blockIdx.x);
                 const unsigned chunk = v / (unsigned)p.num_kv_heads;
                 Task t;
                 t.start = t.len = t.off = 0, t.head_last = -1;
-                if (chunk < all) {
-                    int lo = 0, hi = p.max_chunks;           // F(lo) > chunk >= F(hi)
-                    unsigned above = 0;                      // F(hi)
-                    while (hi - lo > 1) {
-                        const int mid = (lo + hi) >> 1;
-                        const unsigned f = at_least(mid);
-                        if (f > chunk) lo = mid;
-                        else hi = mid, above = f;
-                    }
+                int lo = -1, hi = p.max_chunks;              // F(lo) > chunk >= F(hi)
+                unsigned above = 0;                          // F(hi)
+#pragma unroll 1
+                while (hi - lo > 1) {
+                    const int mid = lo < 0 ? 0 : (lo + hi) >> 1;
+                    const unsigned f = at_least(mid);
+                    if (f > chunk) lo = mid;
+                    else hi = mid, above = f;
+                }
+                if (lo >= 0) {                               // else there are no more
                     unsigned left = chunk - above;
                     int s = 0;
 #pragma unroll 1
@@ -901,21 +918,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int len = length_of(p, s, t.start);
                     // chunks behind this one (none, if the lengths changed under the kernel)
-                    const int behind = max(0, (len + per_task - 1) / per_task - 1 - lo);
+                    const int behind = max(0, chunks(len) - 1 - lo);
                     t.len = len - behind * per_task;
                     t.off = max(0, t.len - per_task);
-                    t.head_last = 2 * (int)(v % (unsigned)p.num_kv_heads) + (behind == 0);
+                    t.head_last = 2 * (int)(v - chunk * (unsigned)p.num_kv_heads) + (behind == 0);
                 }
-                if (i >= 2 &&
-                    !wait(LY::kTaskEmpty + (i & 1), ((i >> 1) - 1) & 1, pa::ERR_WAIT_EMPTY))
-                    break;
+                if (i >= 2 && !all_read(i - 2)) break;
                 if (lane == 0) {
                     volatile Task& r = tasks[i & 1];
                     r.start = t.start, r.len = t.len, r.off = t.off, r.head_last = t.head_last;
                     pa::mbar_arrive(bar(LY::kTaskFull + (i & 1)));
                 }
                 __syncwarp();
-                if (t.head_last < 0) break;
+                if (t.head_last < 0) {
+                    all_read(i);
+                    break;
+                }
             }
         }
     }
@@ -1023,6 +1041,7 @@ extern "C" pa_status pa_prompt_attention(void* out, int64_t out_stride, const vo
     p.group = group;
     p.tokens = kRows / group;
     const int per_task = 2 * p.tokens;
+    p.per_task_inv = (unsigned)((1ull << 32) / per_task) + 1;
     p.max_chunks = (max_seq_len + per_task - 1) / per_task;
     p.carry = carry ? static_cast<float*>(workspace) : nullptr;
     // not 0: a masked score of -inf stays one (a score of 2^100 still has a weight of 1)
