@@ -330,6 +330,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         pa::prefetch_tensormap(&map_k);
         pa::prefetch_tensormap(&map_v);
     }
+    // Rows that no copy of Q writes (groups that do not divide 128): zeros, whose scores never move
+    // a maximum. What an earlier kernel left there moved it in tile after tile (2 prompts of 4219
+    // and 4271, groups of 7: 189 us, 164 with zeros).
+    for (int e = p.tokens * p.group * 8 + threadIdx.x; e < kRows * 8; e += kThreads)
+        for (int h = 0; h < 2 * LY::kHalves; ++h)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(base + h * LY::kHalf + 16 * e),
+                         "r"(0u)
+                         : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (warp == 12) {
         pa::tc::tmem_alloc(pa::smem_addr(tmem_holder), kTmemCols);
         pa::tc::tmem_relinquish();
