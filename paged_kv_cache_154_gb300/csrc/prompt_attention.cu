@@ -38,7 +38,7 @@
 // at 128 (1.08 ms), four softmax warpgroups of half a tile's keys each (1.23 ms),
 // halves of a tile one after another with the next one's maximum beside them (1.20
 // ms), turns at the exponentials (1.18 ms).
-// Short prompts: a task costs about 6000 cycles besides its steps: its first tile
+// Short prompts: a task costs about 4000 cycles besides its steps: its first tile
 // finds both softmaxes idle, its last is masked, and code that runs once a task comes
 // from beyond the instruction caches (53 KB of code in all: 138 us, 46 KB: 128). 16
 // prompts of 200 to 2000 tokens: 128 us, 1220 TFLOP/s.

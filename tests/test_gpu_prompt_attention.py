@@ -300,3 +300,19 @@ def test_kept_sums_follow_the_maximum(d):
             # weight; the sums of products 6.1e-5
             tol = (eps + 2.6e-4 + 2.0 ** -21) * size * (1 + eps) + eps * want.abs() + 2.0 ** -24
             assert ((out[row].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_weights_far_above_the_reference(d, dt):
+    """Keys from 40 on score 14.7 binary orders above the first ones, by which the reference of
+    the weights is taken: it does not move, and all weights are near 2^14.7 (fp16 ends at 2^16)."""
+    T = 600
+    q, k, v = make(17, T, 2, 1, d, DT[dt], False)
+    k2, q2 = k * 0.2, q * 0.2
+    k2[:40, :, 0], k2[40:, :, 0] = 0, 2
+    q2[..., 0] = 5.1 * d ** 0.5
+    out = torch.empty_like(q)
+    pa.prompt_attention(out, q2, k2, v, starts([T]), T, d ** -0.5)
+    assert pa.device_error() == 0
+    check(out, q2, k2, v, [T], d ** -0.5, DT[dt])
