@@ -174,3 +174,42 @@ def test_positions_count_evicted_tokens():
             want[:21 + j] += w / w.sum()
     got = (tw.scores - before)[0, 0, :22].cpu().numpy()
     assert np.abs(got - want).max() < 1e-4
+
+
+def test_long_prompts_take_a_workspace():
+    """A prompt of more than 8192 tokens beside a short one, each the same as alone through the
+    call itself; captured, it runs again on other rows."""
+    H, G, d, lens = 2, 1, 64, [9000, 20]
+    cache = PagedKVCache(600, G, d, "int8")
+    names = {}
+    cache.reserve([Op(seq=0), Op(seq=1)], names)
+    gen = torch.Generator().manual_seed(10)
+
+    def rows(n, heads):
+        return torch.randn((n, heads, d), generator=gen).half()
+
+    ops = [Op(seq=i, k=rows(n, G), v=rows(n, G)) for i, n in enumerate(lens)]
+    si = cache.prepare_step(ops, names, rows(sum(lens), H).cuda(), prompt=True)
+    assert si.workspace.nbytes == pa.prompt_attention_workspace_size(d, max(lens)) > 0
+    si.workspace.fill_(255)
+
+    def alone():
+        parts = []
+        for a, b in ((0, lens[0]), (lens[0], sum(lens))):
+            out = torch.empty_like(si.q[a:b])
+            start = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
+            ws = torch.full_like(si.workspace, 255)
+            pa.prompt_attention(out, si.q[a:b], si.key[a:b], si.value[a:b], start, b - a,
+                                d ** -0.5, ws)
+            parts.append(out)
+        return torch.cat(parts)
+
+    assert torch.equal(cache.step(si, d ** -0.5), alone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend_step(si, d ** -0.5)
+    si.q.copy_(rows(sum(lens), H))
+    si.out.fill_(float("nan"))
+    graph.replay()
+    assert torch.equal(si.out, alone())
+    assert pa.device_error() == 0
