@@ -73,7 +73,7 @@ constexpr int kThreads = 512;
 constexpr int kLaunchSeqs = 256;         // prompts a launch: finding a task reads their lengths
 constexpr int kMaxLen = 1 << 22;         // a task's products end well before a wait gives up
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLazyMax = 15.f;         // fp16 weights end at 2^16
+constexpr float kLazyMax = 15.f, kLazySum = 32768.f;   // fp16 weights end at 2^16
 constexpr int kSpan = 64;                // key tiles whose products are summed in TMEM, with a workspace
 constexpr int kCtas = 152;               // that a workspace is sized for
 
@@ -556,30 +556,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     max32(c[0], m4);
                     m_run = scaled_max(m4);
                 }
-                // Weights of the first 64 keys against the maximum so far, while the maximum of
-                // all 128 is found beside them; in the rare case that it has moved, once more. P
-                // may go over the columns of the last 64 keys' S: they are in registers by now.
-                for (bool again = true; again;) {
+                // Weights of the first 64 keys against the maximum so far: a sum of them up to 2^15
+                // says that none is above it. The last 64 keys' maximum is found beside them. In
+                // the rare case that either passes 2^15, the maximum of all and once more. P may go
+                // over the columns of the last 64 keys' S: they are in registers by now.
+                for (;;) {
                     reference();
                     l4[0] = l4[1] = 0;
                     weights(c[0], p_tm);
                     weights(c[1], p_tm + 16);
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) max32(c[i], m4);
+                    max32(c[2], m4);
+                    max32(c[3], m4);
+                    const bool look = sum_of(l4[0]) + sum_of(l4[1]) > kLazySum || m_run == -INFINITY ||
+                                      scaled_max(m4) > m_run + kLazyMax;
+                    if (!__any_sync(0xffffffffu, look)) break;
+                    max32(c[0], m4);
+                    max32(c[1], m4);
                     const float mx = scaled_max(m4);
-                    const bool moved = mx > m_run + kLazyMax;
-                    again = __any_sync(0xffffffffu, moved);
-                    if (again) {
-                        if (moved) {
-                            alpha = pa::ex2(m_run - mx);     // 0 while m_run is -inf
-                            m_run = mx;
-                            kept_scale *= alpha;
-                        }
-                        // O may be scaled now: S of this tile was issued behind the last P V,
-                        // and the barrier says that both are done; the next P V waits for this P
-                        if (t > 0) scale_o(alpha);
+                    const bool moved = look && mx > m_run;
+                    if (!__any_sync(0xffffffffu, moved)) break;
+                    if (moved) {
+                        alpha = pa::ex2(m_run - mx);         // 0 while m_run is -inf
+                        m_run = mx;
+                        kept_scale *= alpha;
                     }
+                    // O may be scaled now: S of this tile was issued behind the last P V, and the
+                    // barrier says that both are done; the next P V waits for this P
+                    if (t > 0) scale_o(alpha);
                 }
                 if (t == span.tiles - 1) ok = zero_behind();
                 if (!ok) break;

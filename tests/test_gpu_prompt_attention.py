@@ -316,3 +316,19 @@ def test_weights_far_above_the_reference(d, dt):
     pa.prompt_attention(out, q2, k2, v, starts([T]), T, d ** -0.5)
     assert pa.device_error() == 0
     check(out, q2, k2, v, [T], d ** -0.5, DT[dt])
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("first", [70, 127, 128, 190])
+def test_weights_far_above_the_reference_from_any_key(first, dt):
+    """As above from other keys on: of a tile's second half, where the reference stays, of the
+    next tile, where the sum of many moves it, and with a last tile of few keys."""
+    T, d = 385, 64
+    q, k, v = make(18, T, 3, 1, d, DT[dt], False)
+    k2, q2 = k * 0.2, q * 0.2
+    k2[:first, :, 0], k2[first:, :, 0] = 0, 2
+    q2[..., 0] = 5.1 * d ** 0.5
+    out = torch.empty_like(q)
+    pa.prompt_attention(out, q2, k2, v, starts([T]), T, d ** -0.5)
+    assert pa.device_error() == 0
+    check(out, q2, k2, v, [T], d ** -0.5, DT[dt])
