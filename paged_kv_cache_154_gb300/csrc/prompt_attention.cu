@@ -208,6 +208,22 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// 32 consecutive columns without a wait; wait_ld() then waits for all loads before it, and
+// loaded() puts a use of these registers behind that wait.
+__device__ __forceinline__ void ld_32cols_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void wait_ld() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
 // an arrival without a branch
 __device__ __forceinline__ void arrive_if(uint32_t bar, bool p) {
     asm volatile(
@@ -533,10 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float alpha = 1.f;
                 uint32_t c[4][32];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) pa::tc::ld_32cols_nowait(s_tm + 32 * i, c[i]);
-                pa::tc::wait_ld();
+                for (int i = 0; i < 4; ++i) ld_32cols_nowait(s_tm + 32 * i, c[i]);
+                wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) pa::tc::loaded(c[i]);
+                for (int i = 0; i < 4; ++i) loaded(c[i]);
                 if (LY::kApart) {
                     // the next S may come; P of the last tile has been read
                     pa::tc::fence_before_sync();
@@ -639,9 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
-                    pa::tc::ld_32cols_nowait(o_tm + c, o);
-                    pa::tc::wait_ld();
-                    pa::tc::loaded(o);
+                    ld_32cols_nowait(o_tm + c, o);
+                    wait_ld();
+                    loaded(o);
                     if (kCarry && kept_scale != 0.f) {       // sums of earlier spans
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
