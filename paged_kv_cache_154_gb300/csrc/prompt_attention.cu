@@ -135,11 +135,14 @@ __device__ __forceinline__ float* kept_sums(const PromptParams& p, int x) {
 // Tokens off .. len - 1 of the prompt that starts at token `start`: what is behind them does
 // not matter to the task. Chunks are counted back from the prompt's end, so that the one that
 // may leave Q tile 1 empty is the one with the fewest keys.
+// A product takes 16 keys at a time and may pass the prompt's end, from its last chunk and, with
+// chunks of fewer tokens than that, from the ones before: the task says where the end is.
 struct alignas(16) Task {
     int start, len, off;
-    int head_last;              // 2 x KV head + whether the prompt ends here; -1: no more tasks
-    __device__ __forceinline__ int head() const { return head_last >> 1; }
-    __device__ __forceinline__ bool last() const { return head_last & 1; }
+    int head_rest;              // 16 x KV head + tokens of the prompt from len on, at most 15; -1: no more tasks
+    __device__ __forceinline__ int head() const { return head_rest >> 4; }
+    // the prompt's end, or a place that no product of the task reaches
+    __device__ __forceinline__ int end() const { return len + (head_rest & 15); }
 };
 
 // What a task's Q tile x sees: the prompt's tokens [0, keys), in `tiles` tiles.
@@ -382,24 +385,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto read_task = [&](int i, Task& t) -> bool {
         if (!wait(LY::kTaskFull + (i & 1), (i >> 1) & 1)) return false;
         volatile Task& r = tasks[i & 1];
-        t.start = r.start, t.len = r.len, t.off = r.off, t.head_last = r.head_last;
+        t.start = r.start, t.len = r.len, t.off = r.off, t.head_rest = r.head_rest;
         __syncwarp();
         if (lane == 0) pa::mbar_arrive(bar(LY::kTaskEmpty + (i & 1)));
-        return t.head_last >= 0;
+        return t.head_rest >= 0;
     };
     auto read_task_one = [&](int i, Task& t) -> bool {
         if (!wait_one(LY::kTaskFull + (i & 1), (i >> 1) & 1)) return false;
         volatile Task& r = tasks[i & 1];
-        t.start = r.start, t.len = r.len, t.off = r.off, t.head_last = r.head_last;
+        t.start = r.start, t.len = r.len, t.off = r.off, t.head_rest = r.head_rest;
         pa::mbar_arrive(bar(LY::kTaskEmpty + (i & 1)));
-        return t.head_last >= 0;
+        return t.head_rest >= 0;
     };
     const int G = p.group, tokens = p.tokens;
     // whether the last products of both Q tiles reach V rows behind the prompt, in one tile:
     // then Q tile 0's softmax zeroes them, and Q tile 1's products wait for that
     auto first_cleans = [&](const Task& t) {
         const Span a(t, tokens, 0), b(t, tokens, 1);
-        return t.last() && b.keys > a.keys && a.tiles == b.tiles && ((a.keys + 15) & ~15) > t.len;
+        return b.keys > a.keys && a.tiles == b.tiles && ((a.keys + 15) & ~15) > t.end();
     };
 
     if (warp < 8) {
@@ -517,14 +520,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // zeroed, so that a weight of 0 never meets a NaN. The first Q tile to reach them
             // does it.
             auto zero_behind = [&]() -> bool {
-                if (!task.last() || ((span.keys + 15) & ~15) <= task.len ||
-                    (x == 1 && first_cleans(task)))
-                    return true;
+                const int end = task.end();
+                if (((span.keys + 15) & ~15) <= end || (x == 1 && first_cleans(task))) return true;
                 Ring<kStages> v = kv;
                 v.advance(2 * span.tiles - 1);
                 if (!wait(LY::kKVFull + v.slot, v.phase)) return false;
-                const int z0 = task.len - (span.tiles - 1) * kKeys;
-                const int n = (((span.keys + 15) & ~15) - task.len) * (D / 8);
+                const int z0 = end - (span.tiles - 1) * kKeys;
+                const int n = (((span.keys + 15) & ~15) - end) * (D / 8);
                 for (int e = row; e < n; e += kRows) {
                     const int r = z0 + e / (D / 8), ch = e % (D / 8);
                     const uint32_t dst = base + LY::kKVOff + v.slot * LY::kTile +
@@ -921,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const unsigned v = i * P + (i & 1 ? P - 1 - blockIdx.x : blockIdx.x);
                 const unsigned chunk = v / (unsigned)p.num_kv_heads;
                 Task t;
-                t.start = t.len = t.off = 0, t.head_last = -1;
+                t.start = t.len = t.off = 0, t.head_rest = -1;
                 int lo = -1, hi = p.max_chunks;              // F(lo) > chunk >= F(hi)
                 unsigned above = 0;                          // F(hi)
 #pragma unroll 1
@@ -951,16 +953,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int behind = max(0, chunks(len) - 1 - lo);
                     t.len = len - behind * per_task;
                     t.off = max(0, t.len - per_task);
-                    t.head_last = 2 * (int)(v - chunk * (unsigned)p.num_kv_heads) + (behind == 0);
+                    t.head_rest = 16 * (int)(v - chunk * (unsigned)p.num_kv_heads) + min(15, len - t.len);
                 }
                 if (i >= 2 && !all_read(i - 2)) break;
                 if (lane == 0) {
                     volatile Task& r = tasks[i & 1];
-                    r.start = t.start, r.len = t.len, r.off = t.off, r.head_last = t.head_last;
+                    r.start = t.start, r.len = t.len, r.off = t.off, r.head_rest = t.head_rest;
                     pa::mbar_arrive(bar(LY::kTaskFull + (i & 1)));
                 }
                 __syncwarp();
-                if (t.head_last < 0) {
+                if (t.head_rest < 0) {
                     all_read(i);
                     break;
                 }
