@@ -577,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Weights of the first 64 keys against the maximum so far: a sum of them up to 2^15
                 // says that none is above it. The last 64 keys' maximum is found beside them. In
                 // the rare case that either passes 2^15, the maximum of all and once more. P may go
-                // over the columns of the last 64 keys' S: they are in registers by now.
+                // over the columns of the last 64 keys' S: they are in registers by now. (A
+                // difference, not m_run + kLazyMax, which large scores would round up.)
                 for (;;) {
                     reference();
                     l4[0] = l4[1] = 0;
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     max32(c[2], m4);
                     max32(c[3], m4);
                     const bool look = sum_of(l4[0]) + sum_of(l4[1]) > kLazySum || m_run == -INFINITY ||
-                                      scaled_max(m4) > m_run + kLazyMax;
+                                      scaled_max(m4) - m_run > kLazyMax;
                     if (!__any_sync(0xffffffffu, look)) break;
                     max32(c[0], m4);
                     max32(c[1], m4);
