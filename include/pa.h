@@ -583,13 +583,15 @@ size_t pa_prompt_attention_workspace_size(int32_t head_dim, int32_t max_seq_len)
  *                  output, max_seq_len above 2^16 (F16) or 2^19 (BF16), it is required. A
  *                  smaller one is served by as many CTAs as it has parts for.
  * Scores, softmax and sums are fp32, softmax weights are rounded once to dtype for the
- * product with the values; before the division by their sum the weights reach 2^15, so
- * that BF16 values from 2^90 on may overflow in the sums of the longest prompts. Scores
+ * product with the values (by half a step; F16 weights below 2^-22 of a query's largest by
+ * up to 2^-33 of that one); before the division by their sum BF16 weights reach 2^15, so
+ * that values from 2^90 on may overflow in the sums of the longest prompts. Scores
  * (scale q.k) are up to 2^27 (F16) or 2^30 (BF16) in magnitude; rows of larger ones may come
- * out as NaN or 0. A query whose scores are all -infinity gives 0. Nothing of one prompt reaches another's rows,
- * whatever values it holds; within a prompt, a value that is not finite may also reach
- * queries of up to 142 tokens before its own (a masked weight is 0, and 0 times it is
- * NaN). At most 128 query heads per KV head and 65535 in all, head_dim 64 or 128. */
+ * out as NaN or 0. A query whose scores are all -infinity gives 0. Nothing of one prompt
+ * reaches another's rows, whatever values it holds; within a prompt, a value that is not
+ * finite may also reach queries of up to 142 tokens before its own (a masked weight is 0, and
+ * 0 times it is NaN). At most 128 query heads per KV head and 65535 in all, head_dim 64 or
+ * 128. */
 pa_status pa_prompt_attention(void* out, int64_t out_stride, const void* q, int64_t q_stride,
                               const void* key, int64_t key_stride, const void* value,
                               int64_t value_stride, pa_dtype dtype, const int32_t* seq_start,

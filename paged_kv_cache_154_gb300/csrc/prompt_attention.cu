@@ -10,13 +10,19 @@
 //   S = Q K^T      M128 N128, both K-major in shared memory, S in TMEM
 //   P = 2^(S - m)  one thread a row, P as 16 bits into TMEM
 //   O += P V       M128 N = head_dim, P from TMEM, V MN-major in shared memory
-// The running maximum m moves only when a tile raises it by more than 2^15 (the
-// weights then stay below 2^15, and O is scaled in TMEM, which is rare: a bound of 2^8
-// was passed by ordinary scores of standard deviation 2 often enough to cost 8 %); sums
-// and O are fp32. P is rounded to the 16-bit type once, at most half a step (2^-8 bf16,
-// 2^-11 fp16 of a weight), as the tensor cores take it: the size of the rounding of
-// the output. (Two 16-bit parts, as the paged prefill has them, would be a third
-// product.)
+// The reference m of a row is its maximum of some tiles ago. It moves, and O is scaled in
+// TMEM, only when the weights of a tile's first 64 keys sum to more than 2^15 (a rise of 2^9
+// to 2^15, by how many keys share it) or one of its last 64 keys' passes 2^15, which is rare (a
+// bound of 2^8 was passed by ordinary scores of standard deviation 2 often enough to cost 8 %).
+// Sums and O are fp32. P is rounded to the 16-bit type once, as the tensor cores take it, by at
+// most half a step of a weight, 2^-8 bf16 and 2^-11 fp16: the size of the rounding of the
+// output. (Two 16-bit parts, as the paged prefill has them, would be a third product.)
+// fp16 has little room below 1: there weights are 2^8 times as large, so that those from 2^-22 of
+// the largest on keep all their bits and the others are off by at most 2^-33 of it. (With the
+// reference at 1 they were off by 2^-25: in a prompt whose first token takes e^18 of each other
+// one, what the others give came out 75 % short.) The reference then moves from a rise of 2^7.75
+// on. To keep that rare it starts from the maximum of the first 128 keys, not 32: 6 prompts of
+// 16 heads of 64 take 132 us, 138 from 32 keys, 127 without the factor.
 //
 // A CTA a SM stays and works off its tasks: the longest first (a task's keys grow
 // with its place in the prompt), dealt out to and fro over the CTAs. Its roles:
@@ -73,7 +79,6 @@ constexpr int kThreads = 512;
 constexpr int kLaunchSeqs = 256;         // prompts a launch: finding a task reads their lengths
 constexpr int kMaxLen = 1 << 22;         // a task's products end well before a wait gives up
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLazyMax = 15.f, kLazySum = 32768.f;   // fp16 weights end at 2^16
 constexpr int kSpan = 64;                // key tiles whose products are summed in TMEM, with a workspace
 constexpr int kCtas = 152;               // that a workspace is sized for
 
@@ -319,6 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     using LY = Layout<D>;
     constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr int kStages = LY::kStages;
+    // Weights are 2^kLift times as large; the reference moves when a key is kLazyMax orders above it
+    // or the first 64 keys' weights sum to more than kLazySum: fp16 ends at 65504.
+    constexpr float kLift = kBF16 ? 0.f : 8.f;
+    constexpr float kLazyMax = kBF16 ? 15.f : 7.75f, kLazySum = kBF16 ? 32768.f : 60000.f;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = pa::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -471,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             auto reference = [&]() {
-                const float m = m_run == -INFINITY ? 0.f : -m_run;
+                // rounded down: never more than the lift, also where scores are so large that it
+                // is less than their fp32 step
+                const float m = m_run == -INFINITY ? 0.f : __fadd_rd(kLift, -m_run);
                 nm = pair(m, m);
             };
             auto scale_o = [&](float alpha) {
@@ -569,14 +580,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mask(c[i], key0 + 32 * i);
                 }
-                if (t == 0) {                            // a first guess, not above the maximum
+                if (t == 0) {                            // a first reference, not above the maximum
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     max32(c[0], m4);
+                    if (!kBF16) max32(c[1], m4), max32(c[2], m4), max32(c[3], m4);
                     m_run = scaled_max(m4);
                 }
-                // Weights of the first 64 keys against the maximum so far: a sum of them up to 2^15
-                // says that none is above it. The last 64 keys' maximum is found beside them. In
-                // the rare case that either passes 2^15, the maximum of all and once more. P may go
+                // Weights of the first 64 keys against the reference so far: a sum of them up to
+                // kLazySum says that none is too large. The last 64 keys' maximum is found beside
+                // them. In the rare case that either is, the maximum of all and once more. P may go
                 // over the columns of the last 64 keys' S: they are in registers by now. (A
                 // difference, not m_run + kLazyMax, which large scores would round up.)
                 for (;;) {

@@ -56,3 +56,31 @@ def test_neighbours_that_are_not_finite(group, d, dt):
     assert torch.isfinite(outs[0]).all()
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
+
+
+@pytest.mark.parametrize("group", [1, 3, 5, 40])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_neighbours_with_other_scores(group, d, dt):
+    """Rows of another prompt stand in the same tiles as a prompt's own (and are not written from
+    there): their scores, small or large, do not decide how the prompt's are computed."""
+    lens = [70, 40, 300, 9, 513, 150, 33, 77]
+    at = np.concatenate([[0], np.cumsum(lens)])
+    T = int(at[-1])
+    q, k, v = rows(group + d, T, group, 1, d, DT[dt])
+    q *= 3                                     # references move
+    start = torch.from_numpy(at.astype(np.int32)).cuda()
+    for bad in (1, 3, 5, 7):
+        outs = []
+        for factor in (1.0, 0.0, 8.0, -60.0):
+            q2, k2, v2 = q.clone(), k.clone(), v.clone()
+            part = slice(int(at[bad]), int(at[bad + 1]))
+            q2[part] *= factor
+            k2[part] *= factor
+            v2[part] *= factor
+            out = torch.zeros_like(q)
+            pa.prompt_attention(out, q2, k2, v2, start, max(lens), d ** -0.5)
+            outs.append(torch.cat((out[:part.start], out[part.stop:])))
+        assert pa.device_error() == 0 and torch.isfinite(outs[0]).all()
+        for o in outs[1:]:
+            assert torch.equal(o, outs[0])
