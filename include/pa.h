@@ -602,8 +602,9 @@ pa_status pa_prompt_attention(void* out, int64_t out_stride, const void* q, int6
 
 /* The three calls above with their arguments in one array of 64-bit words, in the order
  * of their declarations: pointers and integers as they are, the scale as the bits of a
- * double. Results and refusals are the same. For bindings whose calls cost by the
- * argument: 22 converted one by one take 1.9 us on the host, packed 0.7. */
+ * double. Results and refusals are the same, and a word that does not fit its argument's 32
+ * bits is refused. For bindings whose calls cost by the argument: 22 converted one by one take
+ * 1.9 us on the host, packed 0.7. */
 pa_status pa_rope_packed(const int64_t* args);               /* 22 words */
 pa_status pa_rope_append_kv_packed(const int64_t* args);     /* 33 words */
 pa_status pa_prompt_attention_packed(const int64_t* args);   /* 20 words */

@@ -2,6 +2,8 @@
 // arguments one by one.
 #include <string.h>
 
+#include <initializer_list>
+
 #include "pa_internal.h"
 
 namespace {
@@ -12,12 +14,20 @@ T* at(int64_t word) {
 }
 int32_t i32(int64_t word) { return static_cast<int32_t>(word); }
 pa_dtype type(int64_t word) { return static_cast<pa_dtype>(word); }
-pa_status none() { return pa::fail(PA_ERR_INVALID_ARG, "args is NULL"); }
+// The array is there, and what the call takes as 32 bits (words whose places are given) fits them.
+pa_status check(const int64_t* a, std::initializer_list<int> small) {
+    if (!a) return pa::fail(PA_ERR_INVALID_ARG, "args is NULL");
+    for (int i : small)
+        if (a[i] != static_cast<int32_t>(a[i]))
+            return pa::fail(PA_ERR_INVALID_ARG, "argument %d, %lld, is no 32-bit number", i,
+                            (long long)a[i]);
+    return PA_OK;
+}
 
 }  // namespace
 
 extern "C" pa_status pa_rope_packed(const int64_t* a) {
-    if (!a) return none();
+    if (pa_status s = check(a, {4, 9, 10, 12, 13, 14, 16, 18, 19, 20})) return s;
     return pa_rope(at<void>(a[0]), a[1], at<const void>(a[2]), a[3], i32(a[4]), at<void>(a[5]), a[6],
                    at<const void>(a[7]), a[8], i32(a[9]), type(a[10]), at<const float>(a[11]),
                    i32(a[12]), i32(a[13]), i32(a[14]), at<const int32_t>(a[15]), i32(a[16]),
@@ -25,7 +35,7 @@ extern "C" pa_status pa_rope_packed(const int64_t* a) {
 }
 
 extern "C" pa_status pa_rope_append_kv_packed(const int64_t* a) {
-    if (!a) return none();
+    if (pa_status s = check(a, {4, 11, 14, 21, 22, 23, 25, 27, 28, 29, 30, 31})) return s;
     return pa_rope_append_kv(
         at<void>(a[0]), a[1], at<const void>(a[2]), a[3], i32(a[4]), at<void>(a[5]), a[6],
         at<const void>(a[7]), a[8], at<const void>(a[9]), a[10], type(a[11]), at<void>(a[12]),
@@ -36,7 +46,7 @@ extern "C" pa_status pa_rope_append_kv_packed(const int64_t* a) {
 }
 
 extern "C" pa_status pa_prompt_attention_packed(const int64_t* a) {
-    if (!a) return none();
+    if (pa_status s = check(a, {8, 10, 11, 12, 13, 14, 15})) return s;
     double scale;
     memcpy(&scale, a + 16, sizeof scale);
     return pa_prompt_attention(at<void>(a[0]), a[1], at<const void>(a[2]), a[3],
