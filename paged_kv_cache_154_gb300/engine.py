@@ -189,6 +189,29 @@ class PagedKVCache:
         return slots, pairs
 
     # -- decode step -------------------------------------------------------------
+    def _check_positions(self, step_ops, names: Dict, rotary: Rotary, positions, reserve) -> None:
+        """A step's positions lie within its table of angles: the cache would keep what its
+        slots held before, and attention take rows that nothing was written to."""
+        most, runs = rotary.cos_sin.shape[0], [int(op.k.shape[0]) for op in step_ops]
+        if positions is None:
+            end: Dict = {}
+            for op, r in zip(step_ops, runs):
+                s = names[op.seq]
+                if s not in end:
+                    end[s] = self.pool.seq_len(s) + self.pool.evicted.get(s, 0)
+                end[s] += r if reserve else 0
+                if end[s] > most:
+                    raise ValueError(f"sequence {op.seq!r} reaches position {end[s] - 1}, the table "
+                                     f"of angles has {most}")
+            return
+        at = tuple(np.shape(positions))
+        if len(at) not in (1, 2) or at[-1] != sum(runs):
+            raise ValueError(f"positions are {at}, the step has {sum(runs)} tokens")
+        if not (torch.is_tensor(positions) and positions.is_cuda):
+            p = np.asarray(positions)
+            if p.size and (p.min() < 0 or p.max() >= most):
+                raise ValueError(f"positions of {p.min()} to {p.max()}, the table of angles has {most}")
+
     def prepare_step(self, step_ops, names: Dict, q: torch.Tensor, out_dtype=None,
                      partition_size: int = 0, reserve: bool = True,
                      shared_prefix: bool = False, rotary: Optional[Rotary] = None,
@@ -200,7 +223,9 @@ class PagedKVCache:
 
         rotary: q and the keys of the operations are rotated by write_step on their way
         into the cache. positions: int [T] or [axes, T] of the step's tokens; without it a
-        token's place in its sequence, evicted tokens counted.
+        token's place in its sequence, evicted tokens counted. A position past the table is
+        refused before anything is reserved (those of a device tensor are not looked at here:
+        pa_rope_append_kv leaves their tokens out).
 
         prompt: the operations are whole prompts, each all the tokens of its sequence;
         attend_step then attends them from the rows themselves (the cache's type does not
@@ -217,6 +242,8 @@ class PagedKVCache:
                 raise ValueError("a prompt's output has the type of q; it has no partitions and "
                                  "no shared prefix")
         out_dtype = out_dtype or (q.dtype if prompt else torch.float32)
+        if rotary is not None:
+            self._check_positions(step_ops, names, rotary, positions, reserve)
         slots, pairs, ks, vs = self.reserve(step_ops, names) if reserve else (None, [], [], [])
         seqs = [names[op.seq] for op in step_ops]
         q_lens = [int(op.k.shape[0]) for op in step_ops]
