@@ -213,3 +213,60 @@ def test_long_prompts_take_a_workspace():
     graph.replay()
     assert torch.equal(si.out, alone())
     assert pa.device_error() == 0
+
+
+def test_prompts_then_steps_fp8():
+    """As above over an FP8 cache: codes of the rotated keys by per-head scales, and decode steps
+    over them, whose products take bf16 queries and the codes exactly (as fp16) and weights
+    rounded to fp16 once, by 2^-11 of themselves for the product and as much for their sum at
+    most; scores as above, 2.6e-4 of a weight. Both act on at most max |v|."""
+    H, G, d, dtype = 8, 2, 128, torch.bfloat16
+    gen = torch.Generator().manual_seed(6)
+    lens = {"a": 37, "b": 130}
+    scales = np.array([0.011, 0.02], np.float32), np.array([0.013, 0.009], np.float32)
+    cache = PagedKVCache(64, G, d, "fp8", head_scales=scales)
+    rotary = Rotary(rope_table(400, d), interleaved=True)
+    tab, names, scale = rotary.cos_sin.cpu().numpy(), {}, d ** -0.5
+    cache.reserve([Op(seq=s) for s in lens], names)
+
+    def rows(n, heads):
+        return (torch.randn((n, heads, d), generator=gen) * 0.8).to(dtype)
+
+    def step(runs, prompt):
+        at = {s: cache.pool.seq_len(names[s]) for s in runs}
+        ops = [Op(seq=s, k=rows(r, G), v=rows(r, G)) for s, r in runs.items()]
+        si = cache.prepare_step(ops, names, rows(sum(runs.values()), H).cuda(), rotary=rotary,
+                                prompt=prompt)
+        out = host(cache.step(si, scale))
+        assert pa.device_error() == 0
+        pos = np.concatenate([at[s] + np.arange(r) for s, r in runs.items()])[None]
+        c, s = ref.angles(tab, pos)
+        q, k = (ref.rotate(host(x), c, s, True, np.float32) for x in (si.q, si.key))
+        slots = si.slots.cpu().numpy()
+        for got, x, z in ((cache.k, k, scales[0]), (cache.v, host(si.value), scales[1])):
+            code = torch.from_numpy(x / z[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+            got = got.view(torch.uint8).cpu().numpy()[slots // 16, :, slots % 16]
+            assert np.array_equal(got, code.view(torch.uint8).numpy())
+        q, k = (host(torch.from_numpy(x).to(dtype)) for x in (q, k))
+        return out, q.astype(np.float64), k, host(si.value), at
+
+    out, q, k, v, _ = step(lens, True)
+    eps = torch.finfo(dtype).eps / 2
+    want = ref.prompt_attention(q, k, v, list(lens.values()), scale)
+    size = ref.prompt_attention(q, k, np.abs(v), list(lens.values()), scale)
+    assert (np.abs(out - want) <= (eps + 2.6e-4) * size * (1 + eps) + eps * np.abs(want) + 1e-7).all()
+    for i in range(2):
+        runs = {"a": 1 + 2 * i, "b": 2}
+        out, q, _, _, first = step(runs, False)
+        at = 0
+        for s, r in runs.items():
+            n = cache.pool.seq_len(names[s])
+            bt, _ = cache.pool.block_tables([names[s]], -(-n // 16))
+            t = np.arange(n)
+            keys, values = (x.float().cpu().numpy().astype(np.float64)[bt[0][t // 16], :, t % 16]
+                            * z[:, None] for x, z in ((cache.k, scales[0]), (cache.v, scales[1])))
+            for j in range(r):
+                e = first[s] + j + 1
+                want = attend(q[at + j], keys[:e], values[:e], scale)
+                assert np.abs(out[at + j] - want).max() <= (2.0 ** -10 + 2.6e-4) * np.abs(values).max()
+            at += r
