@@ -35,8 +35,9 @@
 // Every wait is bounded: when the tasks stop being read, warp 14 ends every role's loop.
 //
 // What bounds it. head_dim 128: the tensor cores, 2048 of about 2250 cycles of a
-// step (two Q tiles against 128 keys). One prompt of 8192 tokens, 32 heads over 8:
-// 318 us, 1730 TFLOP/s; of 32768: 5.2 ms, 1690 TFLOP/s, at the power limit.
+// step (two Q tiles against 128 keys). One prompt of 8192 tokens, 32 heads over 8, bf16:
+// 310 us, 1770 TFLOP/s; of 32768: 5.05 ms, 1740 TFLOP/s, at the power limit (5.3 ms where the
+// scores' standard deviation is 2, not 1; every figure here without a workspace).
 // head_dim 64: the softmax, 2200 cycles a step of which the products need 1024; the
 // two warps of a quarter need 1100 for arithmetic alone (exponentials 1024), the
 // rest are loads from TMEM and barriers. 16384 tokens, 32 heads over 8: 1.05 ms,
@@ -47,7 +48,7 @@
 // Short prompts: a task costs about 4000 cycles besides its steps: its first tile
 // finds both softmaxes idle, its last is masked, and code that runs once a task comes
 // from beyond the instruction caches (53 KB of code in all: 138 us, 46 KB: 128). 16
-// prompts of 200 to 2000 tokens: 128 us, 1220 TFLOP/s.
+// prompts of 200 to 2000 tokens: 126 us, 1250 TFLOP/s (137 us at a standard deviation of 2).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -313,8 +314,9 @@ __device__ __forceinline__ int length_of(const PromptParams& p, int s, int& star
     return min(max(end - start, 0), p.max_len);
 }
 
-// kCarry is its own variant: 64 wide, the registers it takes cost prompts too short for it 8 %
-// (16384 tokens: 1138 us against 1053); 128 wide, nothing.
+// kCarry is its own variant: 128 wide, what it adds to the softmax costs 6 to 8 % (16384 tokens, 32
+// heads over 8, bf16: 1392 us with a workspace, 1300 without; 32768: 5.5 ms, 5.05); 64 wide,
+// nothing (1040 us either way).
 template <typename T, int D, bool kCarry>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -482,7 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto reference = [&]() {
                 // rounded down: never more than the lift, also where scores are so large that it
                 // is less than their fp32 step
-                const float m = m_run == -INFINITY ? 0.f : __fadd_rd(kLift, -m_run);
+                const float m = m_run == -INFINITY ? 0.f
+                                : kLift == 0.f     ? -m_run
+                                                   : __fadd_rd(kLift, -m_run);
                 nm = pair(m, m);
             };
             auto scale_o = [&](float alpha) {
