@@ -200,7 +200,7 @@ class PagedKVCache:
                 if s not in end:
                     end[s] = self.pool.seq_len(s) + self.pool.evicted.get(s, 0)
                 end[s] += r if reserve else 0
-                if end[s] > most:
+                if r and end[s] > most:
                     raise ValueError(f"sequence {op.seq!r} reaches position {end[s] - 1}, the table "
                                      f"of angles has {most}")
             return

@@ -48,6 +48,12 @@ def test_positions_past_the_table(cache):
     assert si.positions.tolist() == [*range(40), 39]
 
 
+def test_a_sequence_without_new_tokens_may_be_longer(cache):
+    cache.pool.seq_append_slots(cache.names["b"], 50)
+    si = cache.prepare_step([op("a", 2), op("b", 0)], cache.names, rows(2, 2), rotary=ROTARY)
+    assert si.positions.tolist() == [0, 1]
+
+
 def test_evicted_tokens_count(cache):
     cache.pool.seq_append_slots(cache.names["a"], 10)
     cache.pool.evicted[cache.names["a"]] = 30
