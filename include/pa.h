@@ -572,7 +572,8 @@ size_t pa_prompt_attention_workspace_size(int32_t head_dim, int32_t max_seq_len)
  *   seq_start      int32 [num_seqs + 1]: prompt s is tokens seq_start[s] ..
  *                  seq_start[s + 1] - 1 (none, where they are equal). Rows of out of
  *                  tokens of no prompt are left as they were; starts outside
- *                  [0, num_tokens] and lengths past max_seq_len are cut to them.
+ *                  [0, num_tokens] and lengths past max_seq_len are cut to them, which
+ *                  PA_VALIDATE=1 alone reports: what is cut off gets no rows of out.
  *   max_seq_len    the longest prompt (host value), at most 2^22
  *   scale          softmax scale, 0 or more, finite
  *   workspace      pa_prompt_attention_workspace_size() bytes, or NULL. With it the
